@@ -132,7 +132,7 @@ def _normal(g, shape, std, dtype=torch.bfloat16):
 
 def _e4m3(g, shape, std):
     """E4M3 bytes of normal values, as a quantiser with power-of-two scales leaves them (largest of a block near 448 * 2^-1)."""
-    return _normal(g, shape, 96.0 * std).to(torch.float8_e4m3fn).view(torch.uint8)
+    return _normal(g, shape, 96.0 * std).clamp_(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
 
 
 def prepare(case, seed):
