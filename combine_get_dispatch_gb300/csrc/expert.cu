@@ -1,0 +1,465 @@
+// expert.cu -- the experts' products over a receive layout: entry points, the
+// elementwise half of the gradients and a plain product kernel.
+
+#include "expert.cuh"
+
+namespace ep {
+
+constexpr int kTM = 64, kTN = 128, kTK = 16;
+constexpr int kThreads = 256;
+
+enum Form { kGlu, kLinear, kDx, kDw };
+
+struct ProductParams {
+  Segments seg;
+  const void* a;             // rows operand
+  const uint8_t* a_scales;
+  const void* b;             // weights, or the second rows operand (kDw)
+  const uint8_t* b_scales;
+  int N, K;                  // output columns, inner extent (kDw: output rows K)
+  const __nv_bfloat16* bias;
+  const __nv_bfloat16* residual;
+  void* out;
+  uint8_t* out_scales;
+  __nv_bfloat16* keep;       // gu / pre
+};
+
+__device__ __forceinline__ float bf(const void* p, int64_t at) {
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+}
+__device__ __forceinline__ float e4m3(const void* p, int64_t at) {
+  __nv_fp8_e4m3 q;
+  q.__x = static_cast<const uint8_t*>(p)[at];
+  return (float)q;
+}
+__device__ __forceinline__ float pow2_scale(uint8_t b) {
+  return b == 0 ? 5.877472e-39f : __uint_as_float((uint32_t)b << 23);
+}
+
+// out tile [64 x 128] = A [64 x K] B [128 x K]^T in fp32, one CTA per tile,
+// tiles of all experts walked by a persistent grid.
+template <int kForm, int kAct, bool kFp8>
+__global__ void __launch_bounds__(kThreads) k_product(ProductParams p) {
+  __shared__ float sa[kTK][kTM + 4];
+  __shared__ float sb[kForm == kGlu ? 2 : 1][kTK][kTN + 4];
+  constexpr int kAcc = kForm == kGlu ? 2 : 1;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tiles_n = (p.N + kTN - 1) / kTN;
+  int64_t first = 0;   // tiles of the experts before this one
+  for (int e = 0; e < p.seg.E; ++e) {
+    const Segment s = segment_of(p.seg, e);
+    const int M = kForm == kDw ? p.K : s.count;
+    const int inner = kForm == kDw ? s.count : p.K;
+    const int64_t tiles = (int64_t)((M + kTM - 1) / kTM) * tiles_n;
+    // the tiles of this expert that fall on this CTA
+    int64_t t = (int64_t)blockIdx.x - first % gridDim.x;
+    if (t < 0) t += gridDim.x;
+    for (; t < tiles; t += gridDim.x) {
+      const int m0 = (int)(t / tiles_n) * kTM, n0 = (int)(t % tiles_n) * kTN;
+      float acc[kAcc][4][8] = {};
+      for (int k0 = 0; k0 < inner; k0 += kTK) {
+        for (int i = threadIdx.x; i < kTM * kTK; i += kThreads) {
+          const int m = kForm == kDw ? i % kTM : i / kTK, k = kForm == kDw ? i / kTM : i % kTK;
+          float v = 0.0f;
+          if (m0 + m < M && k0 + k < inner) {
+            if (kForm == kDw) {
+              v = bf(p.a, (s.start + k0 + k) * (int64_t)p.K + m0 + m);
+            } else {
+              const int64_t row = s.start + m0 + m;
+              if (kFp8) {
+                const int64_t blk = row / p.seg.cap * (p.K / kFp8Block) + (k0 + k) / kFp8Block;
+                v = e4m3(p.a, row * p.K + k0 + k) * pow2_scale(p.a_scales[blk * p.seg.cap + row % p.seg.cap]);
+              } else {
+                v = bf(p.a, row * p.K + k0 + k);
+              }
+            }
+          }
+          sa[k][m] = v;
+        }
+#pragma unroll
+        for (int c = 0; c < kAcc; ++c)
+          for (int i = threadIdx.x; i < kTN * kTK; i += kThreads) {
+            const bool n_fast = kForm == kDw || kForm == kDx;
+            const int n = n_fast ? i % kTN : i / kTK, k = n_fast ? i / kTN : i % kTK;
+            float v = 0.0f;
+            if (n0 + n < p.N && k0 + k < inner) {
+              if (kForm == kDw) {
+                v = bf(p.b, (s.start + k0 + k) * (int64_t)p.N + n0 + n);
+              } else if (kForm == kDx) {
+                v = bf(p.b, ((int64_t)e * p.K + k0 + k) * p.N + n0 + n);
+              } else {
+                const int64_t row = ((int64_t)e * kAcc + c) * p.N + n0 + n;
+                if (kFp8) {
+                  const int64_t blk = (((int64_t)e * kAcc + c) * (p.N / kFp8Block) + (n0 + n) / kFp8Block) *
+                                          (p.K / kFp8Block) + (k0 + k) / kFp8Block;
+                  v = e4m3(p.b, row * p.K + k0 + k) * pow2_scale(p.b_scales[blk]);
+                } else {
+                  v = bf(p.b, row * p.K + k0 + k);
+                }
+              }
+            }
+            sb[c][k][n] = v;
+          }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kTK; ++k) {
+          float a[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = sa[k][ty * 4 + i];
+#pragma unroll
+          for (int c = 0; c < kAcc; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float b = sb[c][k][tx + 16 * j];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[c][i][j] = fmaf(a[i], b, acc[c][i][j]);
+            }
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = m0 + ty * 4 + i;
+        const bool row_in = m < M;
+        const int64_t row = s.start + m;
+        float v[8], amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int n = n0 + tx + 16 * j;
+          const bool in = row_in && n < p.N;
+          float z = acc[0][i][j];
+          if (kForm == kGlu) {
+            const float u = acc[kAcc - 1][i][j];
+            if (in && p.keep != nullptr) {
+              p.keep[row * 2 * p.N + n] = __float2bfloat16_rn(z);
+              p.keep[(row * 2 + 1) * p.N + n] = __float2bfloat16_rn(u);
+            }
+            z = act_value<kAct>(z) * u;
+          } else if (kForm == kLinear) {
+            if (in && p.bias != nullptr) z += __bfloat162float(p.bias[(int64_t)e * p.N + n]);
+            if (in && p.keep != nullptr) p.keep[row * p.N + n] = __float2bfloat16_rn(z);
+            z = act_value<kAct>(z);
+            if (in && p.residual != nullptr) z += __bfloat162float(p.residual[row * p.N + n]);
+          }
+          v[j] = z;
+          amax = fmaxf(amax, fabsf(z));
+          if (in && p.out_scales == nullptr) {
+            const int64_t at = kForm == kDw ? ((int64_t)e * p.K + m) * p.N + n : row * p.N + n;
+            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(z);
+          }
+        }
+        if (kForm == kGlu && p.out_scales != nullptr) {   // 16 lanes hold the row's 128 columns
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const uint32_t byte = ue8m0_of(amax);
+          const float mul = __uint_as_float((254u - byte) << 23);
+          if (row_in) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              static_cast<uint8_t*>(p.out)[row * p.N + n0 + tx + 16 * j] =
+                  (uint8_t)(cvt_e4m3x2(v[j] * mul, 0.0f) & 0xffu);
+            if (tx == 0)
+              p.out_scales[(row / p.seg.cap * (p.N / kFp8Block) + n0 / kFp8Block) * p.seg.cap + row % p.seg.cap] =
+                  (uint8_t)byte;
+          }
+        }
+      }
+    }
+    first += tiles;
+  }
+}
+
+struct SlopeParams {
+  Segments seg;
+  const __nv_bfloat16* dy;    // dh [rows, N], or dy [rows, N]
+  const __nv_bfloat16* pre;   // gu [rows, 2, N], or pre [rows, N]
+  __nv_bfloat16* out;         // dgu, dpre; may be nullptr (sum only)
+  __nv_bfloat16* dbias;       // [E, N] or nullptr
+  int N;
+};
+
+// dgu = (dh * up * act'(gate), dh * act(gate)) over the rows of every segment,
+// 8 columns a thread.
+template <int kAct>
+__global__ void __launch_bounds__(kThreads) k_glu_slope(SlopeParams p) {
+  const int vec = p.N / 8;
+  for (int e = blockIdx.y; e < p.seg.E; e += gridDim.y) {
+    const Segment s = segment_of(p.seg, e);
+    const int64_t items = (int64_t)s.count * vec;
+    for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < items; it += (int64_t)gridDim.x * kThreads) {
+      const int64_t row = s.start + it / vec;
+      const int64_t c = (it % vec) * 8;
+      const uint4 d = *reinterpret_cast<const uint4*>(p.dy + row * p.N + c);
+      const uint4 g = *reinterpret_cast<const uint4*>(p.pre + row * 2 * p.N + c);
+      const uint4 u = *reinterpret_cast<const uint4*>(p.pre + (row * 2 + 1) * p.N + c);
+      const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+      uint32_t og[4], ou[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v0, s0, v1, s1;
+        act_both<kAct>(bf16_lo(gw[i]), v0, s0);
+        act_both<kAct>(bf16_hi(gw[i]), v1, s1);
+        const float d0 = bf16_lo(dw[i]), d1 = bf16_hi(dw[i]);
+        og[i] = pack_bf16x2(d0 * bf16_lo(uw[i]) * s0, d1 * bf16_hi(uw[i]) * s1);
+        ou[i] = pack_bf16x2(d0 * v0, d1 * v1);
+      }
+      st_v4(p.out + row * 2 * p.N + c, make_uint4(og[0], og[1], og[2], og[3]));
+      st_v4(p.out + (row * 2 + 1) * p.N + c, make_uint4(ou[0], ou[1], ou[2], ou[3]));
+    }
+  }
+}
+
+// dpre = dy * act'(pre) and dbias = its sum over the expert's rows.  A CTA owns
+// 64 columns of one expert: 8 threads a row, the row sums in 32 bits (before
+// dpre is rounded), added over the CTA's row groups in a fixed order.
+template <int kAct>
+__global__ void __launch_bounds__(1024) k_linear_slope(SlopeParams p) {
+  __shared__ float part[128][65];
+  const int c8 = threadIdx.x & 7, rg = threadIdx.x >> 3;
+  const int c = blockIdx.x * 64 + c8 * 8;
+  for (int e = blockIdx.y; e < p.seg.E; e += gridDim.y) {
+    const Segment s = segment_of(p.seg, e);
+    float sum[8] = {};
+    if (c < p.N) {
+      for (int i = rg; i < s.count; i += 128) {
+        const int64_t at = (s.start + i) * p.N + c;
+        const uint4 d = *reinterpret_cast<const uint4*>(p.dy + at);
+        uint4 z = make_uint4(0, 0, 0, 0);
+        if (kAct != EP_ACT_NONE) z = *reinterpret_cast<const uint4*>(p.pre + at);
+        const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, zw[4] = {z.x, z.y, z.z, z.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v, s0, s1;
+          act_both<kAct>(bf16_lo(zw[q]), v, s0);
+          act_both<kAct>(bf16_hi(zw[q]), v, s1);
+          const float d0 = bf16_lo(dw[q]) * s0, d1 = bf16_hi(dw[q]) * s1;
+          sum[2 * q] += d0;
+          sum[2 * q + 1] += d1;
+          o[q] = pack_bf16x2(d0, d1);
+        }
+        if (kAct != EP_ACT_NONE) st_v4(p.out + at, make_uint4(o[0], o[1], o[2], o[3]));
+      }
+    }
+    if (p.dbias != nullptr) {
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) part[rg][c8 * 8 + q] = sum[q];
+      __syncthreads();
+      for (int half = 64; half > 0; half >>= 1) {
+        for (int i = threadIdx.x; i < half * 64; i += 1024)
+          part[i / 64][i % 64] += part[i / 64 + half][i % 64];
+        __syncthreads();
+      }
+      if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < p.N)
+        p.dbias[(int64_t)e * p.N + blockIdx.x * 64 + threadIdx.x] = __float2bfloat16_rn(part[0][threadIdx.x]);
+    }
+  }
+}
+
+template <int kForm, int kAct, bool kFp8>
+static int launch_product_t(const ProductParams& p, cudaStream_t s) {
+  k_product<kForm, kAct, kFp8><<<ep_host::grid_cap(4), kThreads, 0, s>>>(p);
+  ep_host::count_launch();
+  return ep_host::check_launch();
+}
+
+template <int kForm, bool kFp8>
+static int launch_product(const ProductParams& p, int act, cudaStream_t s) {
+  switch (act) {
+    case EP_ACT_RELU: return launch_product_t<kForm, EP_ACT_RELU, kFp8>(p, s);
+    case EP_ACT_SILU: return launch_product_t<kForm, EP_ACT_SILU, kFp8>(p, s);
+    case EP_ACT_GELU: return launch_product_t<kForm, EP_ACT_GELU, kFp8>(p, s);
+    default: return launch_product_t<kForm, EP_ACT_NONE, kFp8>(p, s);
+  }
+}
+
+template <int kAct>
+static int launch_glu_slope(const SlopeParams& p, cudaStream_t s) {
+  const dim3 grid(std::max(1, ep_host::grid_cap(8) / p.seg.E), p.seg.E);
+  k_glu_slope<kAct><<<grid, kThreads, 0, s>>>(p);
+  ep_host::count_launch();
+  return ep_host::check_launch();
+}
+
+template <int kAct>
+static int launch_linear_slope(const SlopeParams& p, cudaStream_t s) {
+  const dim3 grid((p.N + 63) / 64, p.seg.E);
+  k_linear_slope<kAct><<<grid, 1024, 0, s>>>(p);
+  ep_host::count_launch();
+  return ep_host::check_launch();
+}
+
+// dx = d W and dw = d^T x, over d [rows, N].
+static int launch_gradients(const Segments& seg, const void* d, const void* x, const void* w, int K, int N,
+                            void* dx, void* dw, cudaStream_t s) {
+  if (dx != nullptr) {
+    ProductParams p{};
+    p.seg = seg;
+    p.a = d;
+    p.b = w;
+    p.K = N;
+    p.N = K;
+    p.out = dx;
+    const int rc = launch_product_t<kDx, EP_ACT_NONE, false>(p, s);
+    if (rc != EP_OK) return rc;
+  }
+  if (dw != nullptr) {
+    ProductParams p{};
+    p.seg = seg;
+    p.a = d;
+    p.b = x;
+    p.K = N;
+    p.N = K;
+    p.out = dw;
+    const int rc = launch_product_t<kDw, EP_ACT_NONE, false>(p, s);
+    if (rc != EP_OK) return rc;
+  }
+  return EP_OK;
+}
+
+static int check_expert(const int32_t* counts, const int64_t* psum, int R, int E, int K, int N, int64_t cap_rows,
+                        int unit) {
+  if (R <= 0 || R > kMaxR || E <= 0 || E > kMaxE || E % R != 0 || cap_rows < 0) return EP_ERR_INVALID_ARG;
+  if (K <= 0 || N <= 0 || K % unit != 0 || N % unit != 0 || K > (1 << 24) || N > (1 << 24)) return EP_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t)1 << 31;
+  const int64_t owners = psum != nullptr ? R : E;
+  if (cap_rows >= lim / owners || (int64_t)E * K >= lim || (int64_t)E * N >= lim / 2) return EP_ERR_INVALID_ARG;
+  if (counts == nullptr) return EP_ERR_INVALID_ARG;
+  return EP_OK;
+}
+
+static bool good(const void* p) { return p != nullptr && ep_host::aligned16(p); }
+
+static Segments segments(const int32_t* counts, const int64_t* psum, int R, int E, int64_t cap_rows, int32_t* status) {
+  Segments s;
+  s.counts = counts;
+  s.psum = psum;
+  s.E = E;
+  s.E_l = E / R;
+  s.cap = cap_rows;
+  s.status = status;
+  return s;
+}
+
+}  // namespace ep
+
+extern "C" int ep_expert_glu(const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
+                             int fp8_mode, const int32_t* counts, const int64_t* psum, int R, int E, int H,
+                             int I, int64_t cap_rows, int act, void* h, uint8_t* h_scales, void* gu,
+                             int32_t* status, void* stream) {
+  using namespace ep;
+  if (fp8_mode != EP_FP8_NONE && fp8_mode != EP_FP8_E4M3_UE8M0) return EP_ERR_INVALID_ARG;
+  const bool fp8 = fp8_mode != EP_FP8_NONE;
+  const int rc = check_expert(counts, psum, R, E, H, I, cap_rows, fp8 ? kFp8Block : 8);
+  if (rc != EP_OK) return rc;
+  if (act <= EP_ACT_NONE || act > EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+  if (fp8 ? (x_scales == nullptr || w_scales == nullptr || gu != nullptr) : h_scales != nullptr)
+    return EP_ERR_INVALID_ARG;
+  if (cap_rows == 0) return EP_OK;
+  if (!good(x) || !good(w) || !good(h) || !ep_host::aligned16(gu)) return EP_ERR_INVALID_ARG;
+  ProductParams p{};
+  p.seg = segments(counts, psum, R, E, cap_rows, status);
+  p.a = x;
+  p.a_scales = x_scales;
+  p.b = w;
+  p.b_scales = w_scales;
+  p.K = H;
+  p.N = I;
+  p.out = h;
+  p.out_scales = h_scales;
+  p.keep = static_cast<__nv_bfloat16*>(gu);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return fp8 ? launch_product<kGlu, true>(p, act, s) : launch_product<kGlu, false>(p, act, s);
+}
+
+extern "C" int ep_expert_glu_backward(const void* dh, const void* gu, const void* x, const void* w,
+                                      const int32_t* counts, const int64_t* psum, int R, int E, int H, int I,
+                                      int64_t cap_rows, int act, void* dgu, void* dx, void* dw,
+                                      int32_t* status, void* stream) {
+  using namespace ep;
+  int rc = check_expert(counts, psum, R, E, H, I, cap_rows, 8);
+  if (rc != EP_OK) return rc;
+  if (act <= EP_ACT_NONE || act > EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+  if (cap_rows > 0 && (!good(dh) || !good(gu) || !good(dgu) || (dw != nullptr && !good(x)))) return EP_ERR_INVALID_ARG;
+  if ((dx != nullptr && cap_rows > 0 && !good(w)) || !ep_host::aligned16(dx) || !ep_host::aligned16(dw))
+    return EP_ERR_INVALID_ARG;
+  SlopeParams p{};
+  p.seg = segments(counts, psum, R, E, cap_rows, status);
+  p.dy = static_cast<const __nv_bfloat16*>(dh);
+  p.pre = static_cast<const __nv_bfloat16*>(gu);
+  p.out = static_cast<__nv_bfloat16*>(dgu);
+  p.N = I;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cap_rows > 0) {
+    rc = act == EP_ACT_RELU ? launch_glu_slope<EP_ACT_RELU>(p, s)
+       : act == EP_ACT_SILU ? launch_glu_slope<EP_ACT_SILU>(p, s) : launch_glu_slope<EP_ACT_GELU>(p, s);
+    if (rc != EP_OK) return rc;
+  } else {
+    dx = nullptr;
+  }
+  return launch_gradients(p.seg, dgu, x, w, H, 2 * I, dx, dw, s);
+}
+
+extern "C" int ep_expert_linear(const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
+                                int fp8_mode, const void* bias, const void* residual, const int32_t* counts,
+                                const int64_t* psum, int R, int E, int K, int N, int64_t cap_rows, int act,
+                                void* y, void* pre, int32_t* status, void* stream) {
+  using namespace ep;
+  if (fp8_mode != EP_FP8_NONE && fp8_mode != EP_FP8_E4M3_UE8M0) return EP_ERR_INVALID_ARG;
+  const bool fp8 = fp8_mode != EP_FP8_NONE;
+  const int rc = check_expert(counts, psum, R, E, K, N, cap_rows, fp8 ? kFp8Block : 8);
+  if (rc != EP_OK) return rc;
+  if (act < EP_ACT_NONE || act > EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+  if (fp8 && (x_scales == nullptr || w_scales == nullptr)) return EP_ERR_INVALID_ARG;
+  if (cap_rows == 0) return EP_OK;
+  if (!good(x) || !good(w) || !good(y) || !ep_host::aligned16(pre) || !ep_host::aligned16(residual) ||
+      !ep_host::aligned16(bias))
+    return EP_ERR_INVALID_ARG;
+  ProductParams p{};
+  p.seg = segments(counts, psum, R, E, cap_rows, status);
+  p.a = x;
+  p.a_scales = x_scales;
+  p.b = w;
+  p.b_scales = w_scales;
+  p.K = K;
+  p.N = N;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.out = y;
+  p.keep = static_cast<__nv_bfloat16*>(pre);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return fp8 ? launch_product<kLinear, true>(p, act, s) : launch_product<kLinear, false>(p, act, s);
+}
+
+extern "C" int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, const void* w,
+                                         const int32_t* counts, const int64_t* psum, int R, int E, int K,
+                                         int N, int64_t cap_rows, int act, void* dpre, void* dx, void* dw,
+                                         void* dbias, int32_t* status, void* stream) {
+  using namespace ep;
+  int rc = check_expert(counts, psum, R, E, K, N, cap_rows, 8);
+  if (rc != EP_OK) return rc;
+  if (act < EP_ACT_NONE || act > EP_ACT_GELU) return EP_ERR_INVALID_ARG;
+  const bool curved = act != EP_ACT_NONE;
+  if (cap_rows > 0 && (!good(dy) || (curved && (!good(pre) || !good(dpre))) || (dw != nullptr && !good(x)) ||
+                       (dx != nullptr && !good(w))))
+    return EP_ERR_INVALID_ARG;
+  if (!ep_host::aligned16(dx) || !ep_host::aligned16(dw) || !ep_host::aligned16(dbias)) return EP_ERR_INVALID_ARG;
+  SlopeParams p{};
+  p.seg = segments(counts, psum, R, E, cap_rows, status);
+  p.dy = static_cast<const __nv_bfloat16*>(dy);
+  p.pre = static_cast<const __nv_bfloat16*>(pre);
+  p.out = static_cast<__nv_bfloat16*>(dpre);
+  p.dbias = static_cast<__nv_bfloat16*>(dbias);
+  p.N = N;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dbias != nullptr || (curved && cap_rows > 0)) {
+    rc = act == EP_ACT_RELU   ? launch_linear_slope<EP_ACT_RELU>(p, s)
+         : act == EP_ACT_SILU ? launch_linear_slope<EP_ACT_SILU>(p, s)
+         : act == EP_ACT_GELU ? launch_linear_slope<EP_ACT_GELU>(p, s)
+                              : launch_linear_slope<EP_ACT_NONE>(p, s);
+    if (rc != EP_OK) return rc;
+  }
+  if (cap_rows == 0) dx = nullptr;
+  return launch_gradients(p.seg, curved ? dpre : dy, x, w, K, N, dx, dw, s);
+}

@@ -37,7 +37,22 @@ EXPORTS = (
     "ep_host_wait_counters", "ep_launch_count", "ep_error_string", "ep_rank_ids",
     "ep_rank_recv_topk", "ep_rank_combine", "ep_set_num_sms", "ep_get_num_sms",
     "ep_format_e4m3", "ep_format_bf16", "ep_layout_notify", "ep_layout_notify_dispatch",
+    "ep_gate_topk", "ep_gate_topk_backward", "ep_expert_glu", "ep_expert_glu_backward",
+    "ep_expert_linear", "ep_expert_linear_backward",
 )
+
+EP_DTYPE_F32 = 0
+EP_DTYPE_BF16 = 1
+
+EP_GATE_SOFTMAX = 0
+EP_GATE_SOFTMAX_TOPK = 1
+GATE_SCORES = {"softmax": EP_GATE_SOFTMAX, "softmax_topk": EP_GATE_SOFTMAX_TOPK}
+
+EP_ACT_NONE = 0
+EP_ACT_RELU = 1
+EP_ACT_SILU = 2
+EP_ACT_GELU = 3
+ACTS = {"none": EP_ACT_NONE, "relu": EP_ACT_RELU, "silu": EP_ACT_SILU, "gelu": EP_ACT_GELU}
 
 
 class EPError(RuntimeError):
@@ -91,6 +106,16 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     L.ep_format_e4m3.restype = _I
     L.ep_format_bf16.argtypes = [_P, _P, _I64, _P]
     L.ep_format_bf16.restype = _I
+    L.ep_gate_topk.argtypes = [_P, _I, _I, _I, _I, _I, _I, _P, _P, _P]
+    L.ep_gate_topk_backward.argtypes = [_P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]
+    L.ep_expert_glu.argtypes = [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I64, _I, _P, _P, _P,
+                                _P, _P]
+    L.ep_expert_glu_backward.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _I, _P, _P,
+                                         _P, _P, _P]
+    L.ep_expert_linear.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _I,
+                                   _P, _P, _P, _P]
+    L.ep_expert_linear_backward.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _I, _P,
+                                            _P, _P, _P, _P, _P]
     L.ep_set_num_sms.argtypes = [_I]
     L.ep_set_num_sms.restype = _I
     L.ep_get_num_sms.argtypes = []
@@ -101,7 +126,9 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     L.ep_error_string.restype = ctypes.c_char_p
     for name in ("ep_get_dispatch_layout", "ep_notify_dispatch", "ep_dispatch", "ep_combine",
                  "ep_ll_dispatch", "ep_ll_combine", "ep_clean_ll_buffer", "ep_read_status",
-                 "ep_host_wait_counters", "ep_rank_ids", "ep_rank_recv_topk", "ep_rank_combine"):
+                 "ep_host_wait_counters", "ep_rank_ids", "ep_rank_recv_topk", "ep_rank_combine",
+                 "ep_gate_topk", "ep_gate_topk_backward", "ep_expert_glu",
+                 "ep_expert_glu_backward", "ep_expert_linear", "ep_expert_linear_backward"):
         getattr(L, name).restype = _I
     _lib = L
     return L
@@ -410,6 +437,165 @@ def ep_rank_combine(y, combine_idx, cap_rows, out, status=None, stream=None):
     rc = load().ep_rank_combine(_ptr(y), _ptr(combine_idx), R, T_r, H, k, cap_rows, _ptr(out),
                                 _ptr(status), _stream(stream))
     _check(rc, "ep_rank_combine")
+
+
+def _gate_dtype(logits):
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits: dtype {logits.dtype}, expected float32 or bfloat16")
+    return EP_DTYPE_F32 if logits.dtype == torch.float32 else EP_DTYPE_BF16
+
+
+def ep_gate_topk(logits, score, topk_idx, topk_weights, stream=None):
+    """Router top-k: logits [R, T_r, E] -> topk_idx, topk_weights [R, T_r, k]."""
+    R, T_r, E = logits.shape
+    k = topk_idx.shape[2]
+    dtype = _gate_dtype(logits)
+    _need(logits, None, name="logits")
+    _need(topk_idx, torch.int64, (R, T_r, k), "topk_idx")
+    _need(topk_weights, torch.float32, (R, T_r, k), "topk_weights")
+    rc = load().ep_gate_topk(_ptr(logits), dtype, R, T_r, E, k, score, _ptr(topk_idx),
+                             _ptr(topk_weights), _stream(stream))
+    _check(rc, "ep_gate_topk")
+
+
+def ep_gate_topk_backward(logits, score, topk_idx, grad_topk_weights, grad_logits, status=None,
+                          stream=None):
+    R, T_r, E = logits.shape
+    k = topk_idx.shape[2]
+    dtype = _gate_dtype(logits)
+    _need(logits, None, name="logits")
+    _need(topk_idx, torch.int64, (R, T_r, k), "topk_idx")
+    _need(grad_topk_weights, torch.float32, (R, T_r, k), "grad_topk_weights")
+    _need(grad_logits, logits.dtype, (R, T_r, E), "grad_logits")
+    _need(status, torch.int32, (1,), "status", optional=True)
+    rc = load().ep_gate_topk_backward(_ptr(logits), dtype, _ptr(topk_idx), _ptr(grad_topk_weights),
+                                      R, T_r, E, k, score, _ptr(grad_logits), _ptr(status),
+                                      _stream(stream))
+    _check(rc, "ep_gate_topk_backward")
+
+
+def _expert_rows(lead, E, counts, psum, status):
+    """Checks the tables of a receive layout with leading dimensions `lead`
+    ((R, cap_rows) with psum, (R, E_l, cap_rows) without); R and cap_rows."""
+    R, cap = lead[0], lead[-1]
+    if R == 0 or E % R != 0:
+        raise ValueError(f"{E} experts on {R} ranks")
+    if tuple(lead) != ((R, cap) if psum is not None else (R, E // R, cap)):
+        raise ValueError(f"rows: leading shape {tuple(lead)}, expected (R, cap_rows) with psum, "
+                         "(R, E_l, cap_rows) without")
+    _need(counts, torch.int32, name="counts")
+    if tuple(counts.shape) not in ((E,), (R, E // R)):
+        raise ValueError(f"counts: shape {tuple(counts.shape)}, expected {(E,)} or {(R, E // R)}")
+    _need(psum, torch.int64, (R, E // R + 1), "psum", optional=True)
+    _need(status, torch.int32, (1,), "status", optional=True)
+    return R, cap
+
+
+def _expert_inputs(x, x_scales, w, w_scales, lead):
+    """dtype and scale checks of the rows and weights; the FP8 mode."""
+    if x_scales is None:
+        _need(x, torch.bfloat16, name="x")
+        _need(w, torch.bfloat16, name="w")
+        if w_scales is not None:
+            raise ValueError("w_scales without x_scales")
+        return EP_FP8_NONE
+    K = x.shape[-1]
+    _need(x, torch.uint8, name="x")
+    _need(w, torch.uint8, name="w")
+    if x_scales.dtype == torch.float32:
+        _need(x_scales, torch.float32, (*lead[:-1], K // 128, lead[-1]), "x_scales")
+        _need(w_scales, None, name="w_scales")
+        return EP_FP8_E4M3_F32_SCALE
+    _need(x_scales, torch.uint8, (*lead[:-1], K // 128, lead[-1]), "x_scales")
+    _need(w_scales, torch.uint8, (*w.shape[:-2], w.shape[-2] // 128, K // 128), "w_scales")
+    return EP_FP8_E4M3_UE8M0
+
+
+def ep_expert_glu(x, x_scales, w, w_scales, counts, psum, act, h, h_scales=None, gu=None,
+                  status=None, stream=None):
+    """h = act(x Wg^T) * (x Wu^T) over a receive layout; w [E, 2, I, H].
+
+    x [R, cap_rows, H] with psum (normal layout), [R, E_l, cap_rows, H] without
+    (packed).  bf16 (scales None), or E4M3 bytes with ue8m0 scales; with
+    h_scales h is written as E4M3, with gu gate and up are kept in bf16."""
+    lead, H = x.shape[:-1], x.shape[-1]
+    E, two, I, Hw = w.shape
+    if two != 2 or Hw != H:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected (E, 2, I, {H})")
+    R, cap = _expert_rows(lead, E, counts, psum, status)
+    mode = _expert_inputs(x, x_scales, w, w_scales, lead)
+    _need(h, torch.bfloat16 if h_scales is None else torch.uint8, (*lead, I), "h")
+    _need(h_scales, torch.uint8, (*lead[:-1], I // 128, cap), "h_scales", optional=True)
+    _need(gu, torch.bfloat16, (*lead, 2, I), "gu", optional=True)
+    rc = load().ep_expert_glu(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), mode, _ptr(counts),
+                              _ptr(psum), R, E, H, I, cap, act, _ptr(h), _ptr(h_scales), _ptr(gu),
+                              _ptr(status), _stream(stream))
+    _check(rc, "ep_expert_glu")
+
+
+def ep_expert_glu_backward(dh, gu, x, w, counts, psum, act, dgu, dx, dw, status=None, stream=None):
+    """Gradient of ep_expert_glu: dgu (gate and up), dx and dw (either may be
+    None, and then w or x may be too)."""
+    lead, I = dh.shape[:-1], dh.shape[-1]
+    some = w if w is not None else dw
+    if some is None:
+        raise ValueError("w or dw is required")
+    E, H = some.shape[0], some.shape[-1]
+    R, cap = _expert_rows(lead, E, counts, psum, status)
+    _need(dh, torch.bfloat16, name="dh")
+    _need(gu, torch.bfloat16, (*lead, 2, I), "gu")
+    _need(dgu, torch.bfloat16, (*lead, 2, I), "dgu")
+    _need(x, torch.bfloat16, (*lead, H), "x", optional=dw is None)
+    _need(w, torch.bfloat16, (E, 2, I, H), "w", optional=dx is None)
+    _need(dx, torch.bfloat16, (*lead, H), "dx", optional=True)
+    _need(dw, torch.bfloat16, (E, 2, I, H), "dw", optional=True)
+    rc = load().ep_expert_glu_backward(_ptr(dh), _ptr(gu), _ptr(x), _ptr(w), _ptr(counts),
+                                       _ptr(psum), R, E, H, I, cap, act, _ptr(dgu), _ptr(dx),
+                                       _ptr(dw), _ptr(status), _stream(stream))
+    _check(rc, "ep_expert_glu_backward")
+
+
+def ep_expert_linear(x, x_scales, w, w_scales, bias, residual, counts, psum, act, y, pre=None,
+                     status=None, stream=None):
+    """y = act(x W^T + bias) + residual over a receive layout; w [E, N, K]."""
+    lead, K = x.shape[:-1], x.shape[-1]
+    E, N, Kw = w.shape
+    if Kw != K:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected (E, N, {K})")
+    R, cap = _expert_rows(lead, E, counts, psum, status)
+    mode = _expert_inputs(x, x_scales, w, w_scales, lead)
+    _need(bias, torch.bfloat16, (E, N), "bias", optional=True)
+    _need(residual, torch.bfloat16, (*lead, N), "residual", optional=True)
+    _need(y, torch.bfloat16, (*lead, N), "y")
+    _need(pre, torch.bfloat16, (*lead, N), "pre", optional=True)
+    rc = load().ep_expert_linear(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), mode, _ptr(bias),
+                                 _ptr(residual), _ptr(counts), _ptr(psum), R, E, K, N, cap, act,
+                                 _ptr(y), _ptr(pre), _ptr(status), _stream(stream))
+    _check(rc, "ep_expert_linear")
+
+
+def ep_expert_linear_backward(dy, pre, x, w, counts, psum, act, dpre, dx, dw, dbias=None,
+                              status=None, stream=None):
+    """Gradient of ep_expert_linear; pre and dpre are None without activation,
+    dx, dw and dbias may each be None."""
+    lead, N = dy.shape[:-1], dy.shape[-1]
+    some = w if w is not None else dw
+    if some is None:
+        raise ValueError("w or dw is required")
+    E, K = some.shape[0], some.shape[-1]
+    R, cap = _expert_rows(lead, E, counts, psum, status)
+    _need(dy, torch.bfloat16, name="dy")
+    _need(pre, torch.bfloat16, (*lead, N), "pre", optional=act == EP_ACT_NONE)
+    _need(dpre, torch.bfloat16, (*lead, N), "dpre", optional=act == EP_ACT_NONE)
+    _need(x, torch.bfloat16, (*lead, K), "x", optional=dw is None)
+    _need(w, torch.bfloat16, (E, N, K), "w", optional=dx is None)
+    _need(dx, torch.bfloat16, (*lead, K), "dx", optional=True)
+    _need(dw, torch.bfloat16, (E, N, K), "dw", optional=True)
+    _need(dbias, torch.bfloat16, (E, N), "dbias", optional=True)
+    rc = load().ep_expert_linear_backward(_ptr(dy), _ptr(pre), _ptr(x), _ptr(w), _ptr(counts),
+                                          _ptr(psum), R, E, K, N, cap, act, _ptr(dpre), _ptr(dx),
+                                          _ptr(dw), _ptr(dbias), _ptr(status), _stream(stream))
+    _check(rc, "ep_expert_linear_backward")
 
 
 def ep_read_status(status, stream=None) -> int:

@@ -24,7 +24,9 @@
  *    ep_layout_notify_dispatch) and combine (ep_combine), low-latency
  *    dispatch / combine (ep_ll_dispatch, ep_ll_combine, ep_clean_ll_buffer),
  *    the once-per-rank layout (ep_rank_ids, ep_rank_recv_topk,
- *    ep_rank_combine), the SM budget (ep_set_num_sms, ep_get_num_sms), the
+ *    ep_rank_combine), the router (ep_gate_topk, ep_gate_topk_backward) and
+ *    the experts' products (ep_expert_glu, ep_expert_linear and their
+ *    .._backward), the SM budget (ep_set_num_sms, ep_get_num_sms), the
  *    kernels' number formats (ep_format_e4m3, ep_format_bf16) and plumbing
  *    (ep_workspace_size, ep_read_status, ep_host_wait_counters,
  *    ep_launch_count, ep_error_string).
@@ -334,6 +336,102 @@ int ep_format_bf16(const float* in, uint16_t* out, int64_t n, void* stream);
  * the current device, or the budget). */
 int ep_set_num_sms(int num_sms);
 int ep_get_num_sms(void);
+
+/* ---- the layer around the exchange: router and experts -------------------
+ * What a mixture-of-experts layer computes before dispatch (which experts a
+ * token goes to) and between dispatch and combine (what the experts do with
+ * the rows dispatch laid out).  The article takes both as given; these calls
+ * read and write its layouts as they are. */
+#define EP_DTYPE_F32 0
+#define EP_DTYPE_BF16 1
+
+#define EP_GATE_SOFTMAX 0      /* probabilities over all E experts */
+#define EP_GATE_SOFTMAX_TOPK 1 /* softmax over the chosen experts */
+
+/* Activations of the expert calls (GELU is the erf form). */
+#define EP_ACT_NONE 0
+#define EP_ACT_RELU 1
+#define EP_ACT_SILU 2
+#define EP_ACT_GELU 3
+
+/* Router top-k.  logits [R, T_r, E] (dtype EP_DTYPE_F32 or EP_DTYPE_BF16).
+ *   topk_idx     [R, T_r, k] int64: the k largest logits in falling order,
+ *                ties to the lower expert id
+ *   topk_weights [R, T_r, k] fp32: exp(l - max) over its sum, the sum over all
+ *                experts (EP_GATE_SOFTMAX) or the chosen ones (.._TOPK),
+ *                in 32 bits
+ * An expert at -inf (switched off) or NaN is never chosen and adds nothing;
+ * with fewer than k experts left the remaining slots hold id -1 and weight 0.
+ * +inf logits share the whole weight equally.  k <= E. */
+int ep_gate_topk(const void* logits, int dtype, int R, int T_r, int E, int k, int score,
+                 int64_t* topk_idx, float* topk_weights, void* stream);
+
+/* Gradient of the weights with respect to the logits: grad_logits [R, T_r, E]
+ * in the logits' type, every element written, from grad_topk_weights
+ * [R, T_r, k] fp32 and the topk_idx of the forward call (the choice itself has
+ * no gradient).  Statistics are recomputed from the logits in 32 bits.  Ids
+ * outside [-1, E) set EP_ERR_INVALID_ARG in *status and count as unused. */
+int ep_gate_topk_backward(const void* logits, int dtype, const int64_t* topk_idx,
+                          const float* grad_topk_weights, int R, int T_r, int E, int k, int score,
+                          void* grad_logits, int32_t* status, void* stream);
+
+/* Expert calls: products over the receive layouts, one weight matrix per
+ * expert.  Expert e = r*E_l + l owns one segment of rows:
+ *   normal layout (psum [R, E_l + 1] as from notify): rows psum[r][l] ..
+ *     psum[r][l] + counts[e] of rank r's cap_rows rows; counts = the totals
+ *     row expert_prefix[R] (unaligned)
+ *   packed layout (psum NULL): rows 0 .. counts[e] of the expert's own
+ *     cap_rows (= R*max_tokens_per_rank) rows; counts = recv_count
+ * counts [E] int32.  Rows outside every segment are neither used nor written.
+ * A segment that leaves the buffer is cut at cap_rows (EP_ERR_CAPACITY in
+ * *status).  Sums run in 32 bits; each bf16 output is rounded once.
+ * Limits: widths are multiples of 8 (128 with FP8), the total of rows and
+ * E * width below 2^31, x / w / outputs 16-byte aligned, E <= 1024.
+ * With EP_FP8_E4M3_UE8M0, x is E4M3 with the scales dispatch writes
+ * ([R, K/128, cap_rows], packed [R, E_l, K/128, cap_rows]) and w is E4M3 with
+ * one ue8m0 byte per 128 x 128 block ([E, N/128, K/128]; glu
+ * [E, 2, I/128, H/128]); EP_FP8_E4M3_F32_SCALE is refused: the tensor cores
+ * scale by powers of two only. */
+
+/* Gated projection: h = act(x Wg^T) * (x Wu^T).
+ *   x [rows, H], w [E, 2, I, H] (gate, then up), h [rows, I] bf16
+ *   h_scales  FP8 only, may be NULL: h is then E4M3 with ue8m0 scales in the
+ *             layout of x_scales (K = I), quantised as dispatch quantises
+ *   gu        bf16 only, may be NULL: [rows, 2, I] bf16, gate and up before
+ *             the activation, for the backward */
+int ep_expert_glu(const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
+                  int fp8_mode, const int32_t* counts, const int64_t* psum, int R, int E, int H,
+                  int I, int64_t cap_rows, int act, void* h, uint8_t* h_scales, void* gu,
+                  int32_t* status, void* stream);
+
+/* Its gradient (bf16): dgu [rows, 2, I] = (dh * up * act'(gate), dh * act(gate))
+ * rounded to bf16 (the tensor cores' operand type), dx = dgu W [rows, H],
+ * dw[e] = dgu^T x [E, 2, I, H] (zeros for an expert without rows).  dx or dw
+ * may be NULL (and then w, x too).  dgu may be gu itself. */
+int ep_expert_glu_backward(const void* dh, const void* gu, const void* x, const void* w,
+                           const int32_t* counts, const int64_t* psum, int R, int E, int H, int I,
+                           int64_t cap_rows, int act, void* dgu, void* dx, void* dw,
+                           int32_t* status, void* stream);
+
+/* Product with an epilogue: y = act(x W^T + bias) + residual.
+ *   x [rows, K], w [E, N, K], bias [E, N] bf16 or NULL, residual [rows, N] bf16
+ *   or NULL (may be y itself), y [rows, N] bf16; pre (may be NULL) [rows, N]
+ *   bf16: x W^T + bias, for the backward.  One expert with one segment is an
+ *   ordinary dense layer. */
+int ep_expert_linear(const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
+                     int fp8_mode, const void* bias, const void* residual, const int32_t* counts,
+                     const int64_t* psum, int R, int E, int K, int N, int64_t cap_rows, int act,
+                     void* y, void* pre, int32_t* status, void* stream);
+
+/* Its gradient (bf16): dpre = dy * act'(pre) [rows, N] rounded to bf16 (pre and
+ * dpre NULL with EP_ACT_NONE: dpre is dy), dx = dpre W [rows, K], dw[e] =
+ * dpre^T x [E, N, K], dbias[e] = sum of dpre over the expert's rows [E, N]
+ * (zeros for an expert without rows).  dx, dw, dbias may each be NULL; the
+ * residual's gradient is dy.  dpre may be dy or pre itself. */
+int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, const void* w,
+                              const int32_t* counts, const int64_t* psum, int R, int E, int K,
+                              int N, int64_t cap_rows, int act, void* dpre, void* dx, void* dw,
+                              void* dbias, int32_t* status, void* stream);
 
 /* Number of kernels this library has launched in the process. */
 uint64_t ep_launch_count(void);
