@@ -1,28 +1,12 @@
 // expert.cu -- the experts' products over a receive layout: entry points, the
 // elementwise half of the gradients and a plain product kernel.
 
-#include "expert.cuh"
+#include "expert_gemm.cuh"
 
 namespace ep {
 
 constexpr int kTM = 64, kTN = 128, kTK = 16;
 constexpr int kThreads = 256;
-
-enum Form { kGlu, kLinear, kDx, kDw };
-
-struct ProductParams {
-  Segments seg;
-  const void* a;             // rows operand
-  const uint8_t* a_scales;
-  const void* b;             // weights, or the second rows operand (kDw)
-  const uint8_t* b_scales;
-  int N, K;                  // output columns, inner extent (kDw: output rows K)
-  const __nv_bfloat16* bias;
-  const __nv_bfloat16* residual;
-  void* out;
-  uint8_t* out_scales;
-  __nv_bfloat16* keep;       // gu / pre
-};
 
 __device__ __forceinline__ float bf(const void* p, int64_t at) {
   return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
@@ -290,29 +274,40 @@ static int launch_linear_slope(const SlopeParams& p, cudaStream_t s) {
   return ep_host::check_launch();
 }
 
+static int64_t rows_of(const Segments& s) { return s.cap * (s.psum != nullptr ? s.E / s.E_l : s.E); }
+
 // dx = d W and dw = d^T x, over d [rows, N].
 static int launch_gradients(const Segments& seg, const void* d, const void* x, const void* w, int K, int N,
                             void* dx, void* dw, cudaStream_t s) {
+  if (dw != nullptr && rows_of(seg) == 0) {   // no rows: zero weights' gradients
+    if (cudaMemsetAsync(dw, 0, (size_t)seg.E * N * K * 2, s) != cudaSuccess) {
+      cudaGetLastError();
+      return EP_ERR_CUDA;
+    }
+    dw = nullptr;
+  }
   if (dx != nullptr) {
     ProductParams p{};
     p.seg = seg;
+    p.rows = rows_of(seg);
     p.a = d;
     p.b = w;
     p.K = N;
     p.N = K;
     p.out = dx;
-    const int rc = launch_product_t<kDx, EP_ACT_NONE, false>(p, s);
+    const int rc = launch_gemm_bf16(kDx, p, EP_ACT_NONE, s);
     if (rc != EP_OK) return rc;
   }
   if (dw != nullptr) {
     ProductParams p{};
     p.seg = seg;
+    p.rows = rows_of(seg);
     p.a = d;
     p.b = x;
     p.K = N;
     p.N = K;
     p.out = dw;
-    const int rc = launch_product_t<kDw, EP_ACT_NONE, false>(p, s);
+    const int rc = launch_gemm_bf16(kDw, p, EP_ACT_NONE, s);
     if (rc != EP_OK) return rc;
   }
   return EP_OK;
@@ -360,6 +355,7 @@ extern "C" int ep_expert_glu(const void* x, const uint8_t* x_scales, const void*
   if (!good(x) || !good(w) || !good(h) || !ep_host::aligned16(gu)) return EP_ERR_INVALID_ARG;
   ProductParams p{};
   p.seg = segments(counts, psum, R, E, cap_rows, status);
+  p.rows = rows_of(p.seg);
   p.a = x;
   p.a_scales = x_scales;
   p.b = w;
@@ -370,7 +366,7 @@ extern "C" int ep_expert_glu(const void* x, const uint8_t* x_scales, const void*
   p.out_scales = h_scales;
   p.keep = static_cast<__nv_bfloat16*>(gu);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return fp8 ? launch_product<kGlu, true>(p, act, s) : launch_product<kGlu, false>(p, act, s);
+  return fp8 ? launch_product<kGlu, true>(p, act, s) : launch_gemm_bf16(kGlu, p, act, s);
 }
 
 extern "C" int ep_expert_glu_backward(const void* dh, const void* gu, const void* x, const void* w,
@@ -418,6 +414,7 @@ extern "C" int ep_expert_linear(const void* x, const uint8_t* x_scales, const vo
     return EP_ERR_INVALID_ARG;
   ProductParams p{};
   p.seg = segments(counts, psum, R, E, cap_rows, status);
+  p.rows = rows_of(p.seg);
   p.a = x;
   p.a_scales = x_scales;
   p.b = w;
@@ -429,7 +426,7 @@ extern "C" int ep_expert_linear(const void* x, const uint8_t* x_scales, const vo
   p.out = y;
   p.keep = static_cast<__nv_bfloat16*>(pre);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return fp8 ? launch_product<kLinear, true>(p, act, s) : launch_product<kLinear, false>(p, act, s);
+  return fp8 ? launch_product<kLinear, true>(p, act, s) : launch_gemm_bf16(kLinear, p, act, s);
 }
 
 extern "C" int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, const void* w,
