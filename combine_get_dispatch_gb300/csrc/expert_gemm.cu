@@ -43,7 +43,8 @@ struct GemmParams {
 };
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages], landed[kStages];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t landed[kStages], cleared[kStages];   // kDw: a segment's last block
   uint64_t sums_full[2], sums_empty[2];
   uint32_t tmem;
   int32_t warp_total[kGemmThreads / 32];
@@ -190,9 +191,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     prefetch_map(&g.a);
     prefetch_map(&g.b);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh.full[s], 2);     // one arrival of each CTA
-      mbar_init(&sh.empty[s], 1);    // the products' commit
+      mbar_init(&sh.full[s], 1);      // the first CTA's, with the bytes of both
+      mbar_init(&sh.empty[s], 1);     // the products' commit
       mbar_init(&sh.landed[s], 1);
+      mbar_init(&sh.cleared[s], 1);   // the second CTA's
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sums_full[i], 1);
@@ -224,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const int mine = boxes[rank];
       const uint32_t bytes = 2 * kOperandBytes + (uint32_t)(boxes[0] + boxes[1]) * (kOperandBytes / 4);
       for (int kb = 0; kb < blocks; ++kb) {
-        if (!mbar_wait_cluster(&sh.empty[s], phase ^ 1)) {
+        if (!mbar_wait_bounded(&sh.empty[s], phase ^ 1)) {
           ok = false;
           break;
         }
@@ -237,8 +239,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           mbar_arrive_expect_tx(&sh.landed[s], kStageBytes);
         } else if (rank == 0) {
           mbar_arrive_expect_tx(&sh.full[s], bytes);
-        } else {
-          mbar_arrive_cluster(bar);
         }
         const int k0 = kb * kTileK, am = t.m0 + (int)rank * kHalf;
         if (kAMn) {
@@ -286,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       }
       tmem_fence_after();
       for (int kb = 0; kb < blocks; ++kb) {
-        if (!mbar_wait_cluster(&sh.full[s], phase)) {
+        if (!mbar_wait_bounded(&sh.full[s], phase)) {
           ok = false;
           break;
         }
@@ -321,7 +321,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.landed[st], (parity >> st) & 1,
                                                        kWaitNs + (uint64_t)blocks * 2000));
         if (ok) {
-          parity ^= 1u << st;
           uint8_t* base = stages + st * kStageBytes;
           for (int i = lane; i < 4 * (kTileK - left) * 8; i += 32) {   // 4 boxes, rows, 16-byte pieces
             const int box = i / ((kTileK - left) * 8), r = i % ((kTileK - left) * 8);
@@ -329,7 +328,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&sh.full[st]), 0));
+          if (rank == 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.cleared[st], (parity >> st) & 1));
+            if (ok && lane == 0) mbar_arrive(&sh.full[st]);
+          } else if (lane == 0) {
+            mbar_arrive_cluster(map_to_rank(smem_addr(&sh.cleared[st]), 0));
+          }
+          parity ^= 1u << st;
         }
       }
       s = (s + blocks) % kStages;
