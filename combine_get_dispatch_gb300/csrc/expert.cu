@@ -1,157 +1,11 @@
-// expert.cu -- the experts' products over a receive layout: entry points, the
-// elementwise half of the gradients and a plain product kernel.
+// expert.cu -- the experts' products over a receive layout: entry points and the
+// elementwise half of the gradients.
 
 #include "expert_gemm.cuh"
 
 namespace ep {
 
-constexpr int kTM = 64, kTN = 128, kTK = 16;
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float bf(const void* p, int64_t at) {
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-}
-__device__ __forceinline__ float e4m3(const void* p, int64_t at) {
-  __nv_fp8_e4m3 q;
-  q.__x = static_cast<const uint8_t*>(p)[at];
-  return (float)q;
-}
-__device__ __forceinline__ float pow2_scale(uint8_t b) {
-  return b == 0 ? 5.877472e-39f : __uint_as_float((uint32_t)b << 23);
-}
-
-// out tile [64 x 128] = A [64 x K] B [128 x K]^T in fp32, one CTA per tile,
-// tiles of all experts walked by a persistent grid.
-template <int kForm, int kAct, bool kFp8>
-__global__ void __launch_bounds__(kThreads) k_product(ProductParams p) {
-  __shared__ float sa[kTK][kTM + 4];
-  __shared__ float sb[kForm == kGlu ? 2 : 1][kTK][kTN + 4];
-  constexpr int kAcc = kForm == kGlu ? 2 : 1;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int tiles_n = (p.N + kTN - 1) / kTN;
-  int64_t first = 0;   // tiles of the experts before this one
-  for (int e = 0; e < p.seg.E; ++e) {
-    const Segment s = segment_of(p.seg, e);
-    const int M = kForm == kDw ? p.K : s.count;
-    const int inner = kForm == kDw ? s.count : p.K;
-    const int64_t tiles = (int64_t)((M + kTM - 1) / kTM) * tiles_n;
-    // the tiles of this expert that fall on this CTA
-    int64_t t = (int64_t)blockIdx.x - first % gridDim.x;
-    if (t < 0) t += gridDim.x;
-    for (; t < tiles; t += gridDim.x) {
-      const int m0 = (int)(t / tiles_n) * kTM, n0 = (int)(t % tiles_n) * kTN;
-      float acc[kAcc][4][8] = {};
-      for (int k0 = 0; k0 < inner; k0 += kTK) {
-        for (int i = threadIdx.x; i < kTM * kTK; i += kThreads) {
-          const int m = kForm == kDw ? i % kTM : i / kTK, k = kForm == kDw ? i / kTM : i % kTK;
-          float v = 0.0f;
-          if (m0 + m < M && k0 + k < inner) {
-            if (kForm == kDw) {
-              v = bf(p.a, (s.start + k0 + k) * (int64_t)p.K + m0 + m);
-            } else {
-              const int64_t row = s.start + m0 + m;
-              if (kFp8) {
-                const int64_t blk = row / p.seg.cap * (p.K / kFp8Block) + (k0 + k) / kFp8Block;
-                v = e4m3(p.a, row * p.K + k0 + k) * pow2_scale(p.a_scales[blk * p.seg.cap + row % p.seg.cap]);
-              } else {
-                v = bf(p.a, row * p.K + k0 + k);
-              }
-            }
-          }
-          sa[k][m] = v;
-        }
-#pragma unroll
-        for (int c = 0; c < kAcc; ++c)
-          for (int i = threadIdx.x; i < kTN * kTK; i += kThreads) {
-            const bool n_fast = kForm == kDw || kForm == kDx;
-            const int n = n_fast ? i % kTN : i / kTK, k = n_fast ? i / kTN : i % kTK;
-            float v = 0.0f;
-            if (n0 + n < p.N && k0 + k < inner) {
-              if (kForm == kDw) {
-                v = bf(p.b, (s.start + k0 + k) * (int64_t)p.N + n0 + n);
-              } else if (kForm == kDx) {
-                v = bf(p.b, ((int64_t)e * p.K + k0 + k) * p.N + n0 + n);
-              } else {
-                const int64_t row = ((int64_t)e * kAcc + c) * p.N + n0 + n;
-                if (kFp8) {
-                  const int64_t blk = (((int64_t)e * kAcc + c) * (p.N / kFp8Block) + (n0 + n) / kFp8Block) *
-                                          (p.K / kFp8Block) + (k0 + k) / kFp8Block;
-                  v = e4m3(p.b, row * p.K + k0 + k) * pow2_scale(p.b_scales[blk]);
-                } else {
-                  v = bf(p.b, row * p.K + k0 + k);
-                }
-              }
-            }
-            sb[c][k][n] = v;
-          }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kTK; ++k) {
-          float a[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = sa[k][ty * 4 + i];
-#pragma unroll
-          for (int c = 0; c < kAcc; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float b = sb[c][k][tx + 16 * j];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[c][i][j] = fmaf(a[i], b, acc[c][i][j]);
-            }
-        }
-        __syncthreads();
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int m = m0 + ty * 4 + i;
-        const bool row_in = m < M;
-        const int64_t row = s.start + m;
-        float v[8], amax = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int n = n0 + tx + 16 * j;
-          const bool in = row_in && n < p.N;
-          float z = acc[0][i][j];
-          if (kForm == kGlu) {
-            const float u = acc[kAcc - 1][i][j];
-            if (in && p.keep != nullptr) {
-              p.keep[row * 2 * p.N + n] = __float2bfloat16_rn(z);
-              p.keep[(row * 2 + 1) * p.N + n] = __float2bfloat16_rn(u);
-            }
-            z = act_value<kAct>(z) * u;
-          } else if (kForm == kLinear) {
-            if (in && p.bias != nullptr) z += __bfloat162float(p.bias[(int64_t)e * p.N + n]);
-            if (in && p.keep != nullptr) p.keep[row * p.N + n] = __float2bfloat16_rn(z);
-            z = act_value<kAct>(z);
-            if (in && p.residual != nullptr) z += __bfloat162float(p.residual[row * p.N + n]);
-          }
-          v[j] = z;
-          amax = fmaxf(amax, fabsf(z));
-          if (in && p.out_scales == nullptr) {
-            const int64_t at = kForm == kDw ? ((int64_t)e * p.K + m) * p.N + n : row * p.N + n;
-            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(z);
-          }
-        }
-        if (kForm == kGlu && p.out_scales != nullptr) {   // 16 lanes hold the row's 128 columns
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const uint32_t byte = ue8m0_of(amax);
-          const float mul = __uint_as_float((254u - byte) << 23);
-          if (row_in) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              static_cast<uint8_t*>(p.out)[row * p.N + n0 + tx + 16 * j] =
-                  (uint8_t)(cvt_e4m3x2(v[j] * mul, 0.0f) & 0xffu);
-            if (tx == 0)
-              p.out_scales[(row / p.seg.cap * (p.N / kFp8Block) + n0 / kFp8Block) * p.seg.cap + row % p.seg.cap] =
-                  (uint8_t)byte;
-          }
-        }
-      }
-    }
-    first += tiles;
-  }
-}
 
 struct SlopeParams {
   Segments seg;
@@ -238,23 +92,6 @@ __global__ void __launch_bounds__(1024) k_linear_slope(SlopeParams p) {
       if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < p.N)
         p.dbias[(int64_t)e * p.N + blockIdx.x * 64 + threadIdx.x] = __float2bfloat16_rn(part[0][threadIdx.x]);
     }
-  }
-}
-
-template <int kForm, int kAct, bool kFp8>
-static int launch_product_t(const ProductParams& p, cudaStream_t s) {
-  k_product<kForm, kAct, kFp8><<<ep_host::grid_cap(4), kThreads, 0, s>>>(p);
-  ep_host::count_launch();
-  return ep_host::check_launch();
-}
-
-template <int kForm, bool kFp8>
-static int launch_product(const ProductParams& p, int act, cudaStream_t s) {
-  switch (act) {
-    case EP_ACT_RELU: return launch_product_t<kForm, EP_ACT_RELU, kFp8>(p, s);
-    case EP_ACT_SILU: return launch_product_t<kForm, EP_ACT_SILU, kFp8>(p, s);
-    case EP_ACT_GELU: return launch_product_t<kForm, EP_ACT_GELU, kFp8>(p, s);
-    default: return launch_product_t<kForm, EP_ACT_NONE, kFp8>(p, s);
   }
 }
 
@@ -366,7 +203,7 @@ extern "C" int ep_expert_glu(const void* x, const uint8_t* x_scales, const void*
   p.out_scales = h_scales;
   p.keep = static_cast<__nv_bfloat16*>(gu);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return fp8 ? launch_product<kGlu, true>(p, act, s) : launch_gemm_bf16(kGlu, p, act, s);
+  return fp8 ? launch_gemm_e4m3(kGlu, p, act, s) : launch_gemm_bf16(kGlu, p, act, s);
 }
 
 extern "C" int ep_expert_glu_backward(const void* dh, const void* gu, const void* x, const void* w,
@@ -426,7 +263,7 @@ extern "C" int ep_expert_linear(const void* x, const uint8_t* x_scales, const vo
   p.out = y;
   p.keep = static_cast<__nv_bfloat16*>(pre);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return fp8 ? launch_product<kLinear, true>(p, act, s) : launch_gemm_bf16(kLinear, p, act, s);
+  return fp8 ? launch_gemm_e4m3(kLinear, p, act, s) : launch_gemm_bf16(kLinear, p, act, s);
 }
 
 extern "C" int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, const void* w,

@@ -33,7 +33,6 @@ constexpr int kTileK = 64;                       // bf16 elements of one 128-byt
 constexpr int kOperandBytes = kHalf * kTileK * 2;   // 16 KB: one CTA's half of an operand
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBox = 32;                         // rows of a small A copy
-constexpr int kGroupM = 8;
 constexpr int kEpilogueWarps = 4;
 
 struct GemmParams {
@@ -47,130 +46,8 @@ struct Shared {
   uint64_t landed[kStages], cleared[kStages];   // kDw: a segment's last block
   uint64_t sums_full[2], sums_empty[2];
   uint32_t tmem;
-  int32_t warp_total[kGemmThreads / 32];
-  int32_t first_tile[kMaxE + 1];   // row tiles of the experts before e
-  int32_t start[kMaxE], count[kMaxE];
+  TileTable table;
 };
-
-struct Tile {
-  int e, m0, n0;       // expert, first row / column of the pair's tile (kGlu: column of the gate)
-  int start, count;    // segment
-};
-
-// Row tiles before each expert, and the segments, in shared memory.
-template <int kForm>
-__device__ __forceinline__ void build_table(Shared& sh, const ProductParams& p, bool report) {
-  const int E = p.seg.E, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int base = 0;
-  for (int e0 = 0; e0 < E; e0 += kGemmThreads) {
-    const int e = e0 + tid;
-    int tiles = 0;
-    if (e < E) {
-      Segments seg = p.seg;
-      if (!report) seg.status = nullptr;
-      const Segment s = segment_of(seg, e);
-      sh.start[e] = (int)s.start;
-      sh.count[e] = s.count;
-      tiles = ((kForm == kDw ? p.K : s.count) + kTileM - 1) / kTileM;
-    }
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) sh.warp_total[warp] = incl;
-    __syncthreads();
-    int before = base, all = base;
-    for (int w = 0; w < kGemmThreads / 32; ++w) {
-      if (w < warp) before += sh.warp_total[w];
-      all += sh.warp_total[w];
-    }
-    if (e < E) sh.first_tile[e] = before + incl - tiles;
-    base = all;
-    __syncthreads();
-  }
-  if (tid == 0) sh.first_tile[E] = base;
-  __syncthreads();
-}
-
-// Tile number t of the list, false past its end.
-__device__ __forceinline__ bool tile_at(const Shared& sh, int E, int tiles_n, int cols, int64_t t, Tile& out) {
-  const int64_t total = (int64_t)sh.first_tile[E] * tiles_n;
-  if (t >= total) return false;
-  int lo = 0, hi = E;   // last expert whose first tile is at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((int64_t)sh.first_tile[mid] * tiles_n <= t)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  // experts without tiles share a first tile with the next: lo is the last of them, the one that has it
-  const int tiles_m = sh.first_tile[lo + 1] - sh.first_tile[lo];
-  const int64_t in = t - (int64_t)sh.first_tile[lo] * tiles_n;
-  const int64_t group = in / ((int64_t)kGroupM * tiles_n);
-  const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
-  const int64_t r = in - group * kGroupM * tiles_n;
-  out.e = lo;
-  out.m0 = ((int)group * kGroupM + (int)(r % gm)) * kTileM;
-  out.n0 = (int)(r / gm) * cols;
-  out.start = sh.start[lo];
-  out.count = sh.count[lo];
-  return true;
-}
-
-// Eight fp32 sums -> 16 bytes of bf16.
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
-
-// The epilogue of 32 columns of one output row: v the sums (kGlu: of the gate),
-// u those of the up projection.
-template <int kForm, int kAct>
-__device__ __forceinline__ void store_row(const ProductParams& p, const Tile& t, int m, int c0, float (&v)[32],
-                                          float (&u)[32]) {
-  const int64_t row = kForm == kDw ? (int64_t)t.e * p.K + m : (int64_t)t.start + m;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.N;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int n = t.n0 + c0 + q * 8;
-    if (n >= p.N) break;
-    float* z = v + q * 8;
-    if (kForm == kGlu) {
-      if (p.keep != nullptr) {
-        st_v4(p.keep + row * 2 * p.N + n, pack8(z));
-        st_v4(p.keep + (row * 2 + 1) * p.N + n, pack8(u + q * 8));
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]) * u[q * 8 + i];
-    } else if (kForm == kLinear) {
-      if (p.bias != nullptr) {
-        const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)t.e * p.N + n));
-        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[2 * i] += bf16_lo(w[i]);
-          z[2 * i + 1] += bf16_hi(w[i]);
-        }
-      }
-      if (p.keep != nullptr) st_v4(p.keep + row * p.N + n, pack8(z));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]);
-      if (p.residual != nullptr) {   // may be the output itself: a plain load
-        const uint4 r = ld_v4(p.residual + row * p.N + n);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[2 * i] += bf16_lo(w[i]);
-          z[2 * i + 1] += bf16_hi(w[i]);
-        }
-      }
-    }
-    st_v4(out + n, pack8(z));
-  }
-}
 
 template <int kForm, int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
@@ -203,7 +80,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     fence_barrier_init();
   }
   if (warp == 2) tmem_alloc<2>(&sh.tmem, 512);
-  build_table<kForm>(sh, p, blockIdx.x == 0);
+  build_table<kTileM, kGemmThreads>(sh.table, p.seg, kForm == kDw ? p.K : -1, blockIdx.x == 0);
   tmem_fence_before();
   cluster_sync();
   tmem_fence_after();
@@ -216,7 +93,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     int s = 0;
     uint32_t phase = 0;
     Tile t;
-    for (int64_t at = pair; ok && tile_at(sh, E, g.tiles_n, kCols, at, t); at += pairs) {
+    for (int64_t at = pair; ok && tile_at<kTileM>(sh.table, E, g.tiles_n, kCols, at, t); at += pairs) {
       const int inner = kForm == kDw ? t.count : p.K;
       const int blocks = (inner + kTileK - 1) / kTileK;
       // rows of A that each CTA has to read: all 128 of them in one copy, or 32 at a time
@@ -276,7 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     int s = 0;
     uint32_t phase = 0, n = 0;
     Tile t;
-    for (int64_t at = pair; ok && tile_at(sh, E, g.tiles_n, kCols, at, t); at += pairs) {
+    for (int64_t at = pair; ok && tile_at<kTileM>(sh.table, E, g.tiles_n, kCols, at, t); at += pairs) {
       const int blocks = ((kForm == kDw ? t.count : p.K) + kTileK - 1) / kTileK;
       if (blocks == 0) continue;
       const uint32_t half = n & 1, d = tmem + half * kTileN;
@@ -312,7 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     int s = 0;
     uint32_t parity = 0;   // bit per stage
     Tile t;
-    for (int64_t at = pair; ok && tile_at(sh, E, g.tiles_n, kCols, at, t); at += pairs) {
+    for (int64_t at = pair; ok && tile_at<kTileM>(sh.table, E, g.tiles_n, kCols, at, t); at += pairs) {
       const int blocks = (t.count + kTileK - 1) / kTileK;
       const int left = t.count % kTileK;
       if (left != 0) {
@@ -344,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int q = warp & 3;   // this warp's 32 lanes of the tensor memory
     uint32_t n = 0;
     Tile t;
-    for (int64_t at = pair; ok && tile_at(sh, E, g.tiles_n, kCols, at, t); at += pairs) {
+    for (int64_t at = pair; ok && tile_at<kTileM>(sh.table, E, g.tiles_n, kCols, at, t); at += pairs) {
       const int blocks = ((kForm == kDw ? t.count : p.K) + kTileK - 1) / kTileK;
       const int m = t.m0 + (int)rank * kHalf + q * 32 + lane;
       const bool in = m < (kForm == kDw ? p.K : t.count);

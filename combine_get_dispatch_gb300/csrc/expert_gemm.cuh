@@ -1,4 +1,5 @@
-// expert_gemm.cuh -- what expert.cu asks of the product kernels.
+// expert_gemm.cuh -- what the product kernels share: arguments, the list of
+// tiles over the experts' segments, the epilogue of a row.
 #pragma once
 
 #include "expert.cuh"
@@ -22,6 +23,136 @@ struct ProductParams {
   __nv_bfloat16* keep;       // gu / pre
 };
 
+struct Tile {
+  int e, m0, n0;       // expert, first row / column of the pair's tile (kGlu: column of the gate)
+  int start, count;    // segment
+};
+
+constexpr int kGroupM = 8;   // row tiles taken together
+
+struct TileTable {
+  int32_t warp_total[32];
+  int32_t first_tile[kMaxE + 1];   // row tiles of the experts before e
+  int32_t start[kMaxE], count[kMaxE];
+};
+
+// Row tiles before each expert, and the segments, in shared memory.
+// fixed_rows: the output's rows where they are not the segment's (kDw), else -1.
+template <int kTileM, int kThreads>
+__device__ __forceinline__ void build_table(TileTable& sh, Segments seg, int fixed_rows, bool report) {
+  const int E = seg.E, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int base = 0;
+  if (!report) seg.status = nullptr;   // one CTA reports a segment that was cut
+  for (int e0 = 0; e0 < E; e0 += kThreads) {
+    const int e = e0 + tid;
+    int tiles = 0;
+    if (e < E) {
+      const Segment s = segment_of(seg, e);
+      sh.start[e] = (int)s.start;
+      sh.count[e] = s.count;
+      tiles = ((fixed_rows >= 0 ? fixed_rows : s.count) + kTileM - 1) / kTileM;
+    }
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh.warp_total[warp] = incl;
+    __syncthreads();
+    int before = base, all = base;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sh.warp_total[w];
+      all += sh.warp_total[w];
+    }
+    if (e < E) sh.first_tile[e] = before + incl - tiles;
+    base = all;
+    __syncthreads();
+  }
+  if (tid == 0) sh.first_tile[E] = base;
+  __syncthreads();
+}
+
+// Tile number t of the list, false past its end.
+template <int kTileM>
+__device__ __forceinline__ bool tile_at(const TileTable& sh, int E, int tiles_n, int cols, int64_t t, Tile& out) {
+  const int64_t total = (int64_t)sh.first_tile[E] * tiles_n;
+  if (t >= total) return false;
+  int lo = 0, hi = E;   // last expert whose first tile is at or before t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)sh.first_tile[mid] * tiles_n <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  // experts without tiles share a first tile with the next: lo is the last of them, the one that has it
+  const int tiles_m = sh.first_tile[lo + 1] - sh.first_tile[lo];
+  const int64_t in = t - (int64_t)sh.first_tile[lo] * tiles_n;
+  const int64_t group = in / ((int64_t)kGroupM * tiles_n);
+  const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
+  const int64_t r = in - group * kGroupM * tiles_n;
+  out.e = lo;
+  out.m0 = ((int)group * kGroupM + (int)(r % gm)) * kTileM;
+  out.n0 = (int)(r / gm) * cols;
+  out.start = sh.start[lo];
+  out.count = sh.count[lo];
+  return true;
+}
+
+// Eight fp32 sums -> 16 bytes of bf16.
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// The epilogue of 32 columns of one output row: v the sums (kGlu: of the gate),
+// u those of the up projection.
+template <int kForm, int kAct>
+__device__ __forceinline__ void store_row(const ProductParams& p, const Tile& t, int m, int c0, float (&v)[32],
+                                          float (&u)[32]) {
+  const int64_t row = kForm == kDw ? (int64_t)t.e * p.K + m : (int64_t)t.start + m;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.N;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int n = t.n0 + c0 + q * 8;
+    if (n >= p.N) break;
+    float* z = v + q * 8;
+    if (kForm == kGlu) {
+      if (p.keep != nullptr) {
+        st_v4(p.keep + row * 2 * p.N + n, pack8(z));
+        st_v4(p.keep + (row * 2 + 1) * p.N + n, pack8(u + q * 8));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]) * u[q * 8 + i];
+    } else if (kForm == kLinear) {
+      if (p.bias != nullptr) {
+        const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)t.e * p.N + n));
+        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[2 * i] += bf16_lo(w[i]);
+          z[2 * i + 1] += bf16_hi(w[i]);
+        }
+      }
+      if (p.keep != nullptr) st_v4(p.keep + row * p.N + n, pack8(z));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]);
+      if (p.residual != nullptr) {   // may be the output itself: a plain load
+        const uint4 r = ld_v4(p.residual + row * p.N + n);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[2 * i] += bf16_lo(w[i]);
+          z[2 * i + 1] += bf16_hi(w[i]);
+        }
+      }
+    }
+    st_v4(out + n, pack8(z));
+  }
+}
+
 int launch_gemm_bf16(Form form, const ProductParams& p, int act, cudaStream_t stream);
+int launch_gemm_e4m3(Form form, const ProductParams& p, int act, cudaStream_t stream);
 
 }  // namespace ep
