@@ -23,9 +23,11 @@ struct ProductParams {
   __nv_bfloat16* keep;       // gu / pre
 };
 
+// One tile of the list: output rows m0 .. m0 + rows of expert e (numbered inside
+// its segment; kDw: inside its weights) and output columns from n0 on.
 struct Tile {
-  int e, m0, n0;       // expert, first row / column of the pair's tile (kGlu: column of the gate)
-  int start, count;    // segment
+  int e, m0, rows, n0;
+  int start, count;   // segment
 };
 
 constexpr int kGroupM = 8;   // row tiles taken together
@@ -74,8 +76,9 @@ __device__ __forceinline__ void build_table(TileTable& sh, Segments seg, int fix
 }
 
 // Tile number t of the list, false past its end.
-template <int kTileM>
-__device__ __forceinline__ bool tile_at(const TileTable& sh, int E, int tiles_n, int cols, int64_t t, Tile& out) {
+template <int kTileM, bool kEven>
+__device__ __forceinline__ bool tile_at(const TileTable& sh, int E, int fixed_rows, int tiles_n, int cols, int64_t t,
+                                        Tile& out) {
   const int64_t total = (int64_t)sh.first_tile[E] * tiles_n;
   if (t >= total) return false;
   int lo = 0, hi = E;   // last expert whose first tile is at or before t
@@ -93,10 +96,19 @@ __device__ __forceinline__ bool tile_at(const TileTable& sh, int E, int tiles_n,
   const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
   const int64_t r = in - group * kGroupM * tiles_n;
   out.e = lo;
-  out.m0 = ((int)group * kGroupM + (int)(r % gm)) * kTileM;
-  out.n0 = (int)(r / gm) * cols;
   out.start = sh.start[lo];
   out.count = sh.count[lo];
+  out.n0 = (int)(r / gm) * cols;
+  const int of = fixed_rows >= 0 ? fixed_rows : out.count;
+  const int i = (int)group * kGroupM + (int)(r % gm);
+  if (kEven) {   // an expert's rows are spread over its row tiles in units of 16
+    const int64_t units = (of + 15) / 16;
+    out.m0 = (int)(units * i / tiles_m) * 16;
+    out.rows = min(of, (int)(units * (i + 1) / tiles_m) * 16) - out.m0;
+  } else {
+    out.m0 = i * kTileM;
+    out.rows = min(kTileM, of - out.m0);
+  }
   return true;
 }
 
@@ -106,49 +118,55 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
                     pack_bf16x2(v[6], v[7]));
 }
 
-// The epilogue of 32 columns of one output row: v the sums (kGlu: of the gate),
-// u those of the up projection.
+// The epilogue of 8 columns from n on of output row `row` of expert e: z the sums
+// (kGlu: of the gate), u those of the up projection.
 template <int kForm, int kAct>
-__device__ __forceinline__ void store_row(const ProductParams& p, const Tile& t, int m, int c0, float (&v)[32],
-                                          float (&u)[32]) {
-  const int64_t row = kForm == kDw ? (int64_t)t.e * p.K + m : (int64_t)t.start + m;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.N;
+__device__ __forceinline__ void store8(const ProductParams& p, int e, int64_t row, int n, float (&z)[8],
+                                       const float* u) {
+  if (kForm == kGlu) {
+    if (p.keep != nullptr) {
+      st_v4(p.keep + row * 2 * p.N + n, pack8(z));
+      st_v4(p.keep + (row * 2 + 1) * p.N + n, pack8(u));
+    }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int n = t.n0 + c0 + q * 8;
-    if (n >= p.N) break;
-    float* z = v + q * 8;
-    if (kForm == kGlu) {
-      if (p.keep != nullptr) {
-        st_v4(p.keep + row * 2 * p.N + n, pack8(z));
-        st_v4(p.keep + (row * 2 + 1) * p.N + n, pack8(u + q * 8));
-      }
+    for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]) * u[i];
+  } else if (kForm == kLinear) {
+    if (p.bias != nullptr) {
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)e * p.N + n));
+      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]) * u[q * 8 + i];
-    } else if (kForm == kLinear) {
-      if (p.bias != nullptr) {
-        const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)t.e * p.N + n));
-        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[2 * i] += bf16_lo(w[i]);
-          z[2 * i + 1] += bf16_hi(w[i]);
-        }
-      }
-      if (p.keep != nullptr) st_v4(p.keep + row * p.N + n, pack8(z));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]);
-      if (p.residual != nullptr) {   // may be the output itself: a plain load
-        const uint4 r = ld_v4(p.residual + row * p.N + n);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[2 * i] += bf16_lo(w[i]);
-          z[2 * i + 1] += bf16_hi(w[i]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        z[2 * i] += bf16_lo(w[i]);
+        z[2 * i + 1] += bf16_hi(w[i]);
       }
     }
-    st_v4(out + n, pack8(z));
+    if (p.keep != nullptr) st_v4(p.keep + row * p.N + n, pack8(z));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]);
+    if (p.residual != nullptr) {   // may be the output itself: a plain load
+      const uint4 r = ld_v4(p.residual + row * p.N + n);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[2 * i] += bf16_lo(w[i]);
+        z[2 * i + 1] += bf16_hi(w[i]);
+      }
+    }
+  }
+  st_v4(static_cast<__nv_bfloat16*>(p.out) + row * p.N + n, pack8(z));
+}
+
+// As store8 for 32 columns that one thread holds, up to the output's last.
+template <int kForm, int kAct>
+__device__ __forceinline__ void store32(const ProductParams& p, int e, int64_t row, int n0, float (&v)[32],
+                                        const float* u) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (n0 + q * 8 >= p.N) break;
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = v[q * 8 + i];
+    store8<kForm, kAct>(p, e, row, n0 + q * 8, z, u + q * 8);
   }
 }
 

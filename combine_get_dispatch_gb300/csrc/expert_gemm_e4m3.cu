@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
   if (warp == 0 && lane == 0) {
     int s = 0;
     uint32_t phase = 0;
-    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM>(sh.table, E, g.tiles_n, kCols, at, t); at += gridDim.x) {
+    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM, false>(sh.table, E, -1, g.tiles_n, kCols, at, t); at += gridDim.x) {
       const int boxes = min(4, (t.count - t.m0 + kMxBox - 1) / kMxBox);
       for (int kb = 0; kb < blocks; ++kb) {
         if (!mbar_wait_bounded(&sh.empty[s], phase ^ 1)) {
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
   } else if (warp == 1 && lane == 0) {
     int s = 0;
     uint32_t phase = 0, n = 0;
-    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM>(sh.table, E, g.tiles_n, kCols, at, t); at += gridDim.x) {
+    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM, false>(sh.table, E, -1, g.tiles_n, kCols, at, t); at += gridDim.x) {
       if (!mbar_wait_bounded(&sh.sums_empty, (n & 1) ^ 1)) {
         ok = false;
         break;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     int s = 0;
     uint32_t phase = 0;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM>(sh.table, E, g.tiles_n, kCols, at, t); at += gridDim.x) {
+    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM, false>(sh.table, E, -1, g.tiles_n, kCols, at, t); at += gridDim.x) {
       const int64_t owner = t.start / p.seg.cap;
       const uint8_t* xs = p.a_scales + owner * blocks * p.seg.cap + (t.start - owner * p.seg.cap) + t.m0 + lane;
       const uint8_t* ws[2];
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     const int q = warp & 3;
     uint32_t n = 0;
     const uint32_t d = tmem + ((uint32_t)(q * 32) << 16);
-    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM>(sh.table, E, g.tiles_n, kCols, at, t); at += gridDim.x) {
+    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM, false>(sh.table, E, -1, g.tiles_n, kCols, at, t); at += gridDim.x) {
       const int m = t.m0 + q * 32 + lane;
       const bool in = m < t.count;
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_full, n & 1, kWaitNs + (uint64_t)blocks * 2000));
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
             st_v4(out, make_uint4(w[0], w[1], w[2], w[3]));
             st_v4(out + 16, make_uint4(w[4], w[5], w[6], w[7]));
           } else {
-            store_row<kForm, kAct>(p, t, m, c0, v, u);
+            store32<kForm, kAct>(p, t.e, (int64_t)t.start + m, t.n0 + c0, v, u);
           }
         }
         __syncwarp();
@@ -299,9 +299,9 @@ int launch_gemm_e4m3(Form form, const ProductParams& p, int act, cudaStream_t st
   const uint64_t ad[3] = {K, rows, 1}, bd[3] = {K, N, (uint64_t)p.seg.E * (form == kGlu ? 2 : 1)};
   const uint64_t as[2] = {K, K * rows}, bs[2] = {K, K * N};
   const uint32_t big[3] = {kFp8Block, kMxTileM, 1}, small[3] = {kFp8Block, kMxBox, 1};
-  int rc = ep_host::make_map(&g.a, true, p.a, ad, as, big);
-  if (rc == EP_OK) rc = ep_host::make_map(&g.a_small, true, p.a, ad, as, small);
-  if (rc == EP_OK) rc = ep_host::make_map(&g.b, true, p.b, bd, bs, big);
+  int rc = ep_host::make_map(&g.a, true, 3, p.a, ad, as, big);
+  if (rc == EP_OK) rc = ep_host::make_map(&g.a_small, true, 3, p.a, ad, as, small);
+  if (rc == EP_OK) rc = ep_host::make_map(&g.b, true, 3, p.b, bd, bs, big);
   if (rc != EP_OK) return rc;
   const int cols = form == kGlu ? 128 : 256;
   g.tiles_n = (p.N + cols - 1) / cols;

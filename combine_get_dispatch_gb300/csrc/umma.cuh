@@ -73,6 +73,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
+// As tma_load_3d<true> with five coordinates.
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- tensor memory
 
 template <int kGroup>
@@ -111,6 +121,20 @@ __device__ __forceinline__ void tmem_st4(uint32_t addr, uint32_t a, uint32_t b, 
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
                : "memory");
+}
+
+// 16 consecutive columns of this thread's lane (one warp, converged).
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 32 consecutive columns of this thread's lane (one warp, converged).
@@ -193,8 +217,8 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 }  // namespace ep
 
 namespace ep_host {
-// A 3-d tensor map (dims[0] contiguous; strides in bytes of dims 1 and 2),
-// 128-byte swizzle, elements outside read as zero.
-int make_map(CUtensorMap* m, bool bytes, const void* base, const uint64_t dims[3], const uint64_t strides[2],
-             const uint32_t box[3]);
+// A tensor map of `rank` dimensions (dims[0] contiguous; strides in bytes of the
+// others), 128-byte swizzle, elements outside read as zero.
+int make_map(CUtensorMap* m, bool bytes, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+             const uint32_t* box);
 }  // namespace ep_host
