@@ -126,16 +126,6 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 __device__ __forceinline__ void named_barrier_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
-// As named_barrier_sync; true if `v` is true in every thread.
-__device__ __forceinline__ bool named_barrier_and(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n barrier.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(n), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
 // Arrive at barrier `id` without waiting: this thread's earlier memory
 // accesses are performed for the threads that wait there (bar.sync id, n).
 __device__ __forceinline__ void named_barrier_arrive(int id, int n) {

@@ -5,29 +5,28 @@
 //   kDx      dx = d W
 //   kDw      dw = d^T x                        contraction over the segment's rows
 //
-// A pair of CTAs (one cluster, two SMs) computes a tile of 256 x up to 256 with
-// tcgen05.mma.cta_group::2: each CTA stages 128 rows of the first operand and half
-// of the second and holds its 128 rows of the sums in tensor memory.  Per 64 inner
-// elements a CTA reads 32 KB for 512 clocks of products, where a single CTA with
-// the same tile would read 48 KB: the L2 is what a 1-CTA form waits for.
+// A pair of CTAs (one cluster, two SMs) computes a tile of 256 output columns by
+// up to 256 output rows with tcgen05.mma.cta_group::2: each CTA stages 128
+// columns of the first operand (the weights; kDw: x) and half the rows of the
+// second (the segment's; kDw: d) and holds its 128 columns of the sums in tensor
+// memory.  Per 64 inner elements a CTA reads 32 KB for 512 clocks of products,
+// where a single CTA with the same tile would read 48 KB: the L2 is what a 1-CTA
+// form waits for.
 //
-// In kGlu, kLinear and kDx the weights are the first operand and the segment's
-// rows the second: the product's second extent is any multiple of 16, so that an
-// expert with 40 rows, or the last rows of one with 2088, cost what they are and
-// not a tile of 256 (65536 rows over 32 experts of about 2048 rows: 2737 us with
-// the rows as the first operand, 2248 us where every segment was a multiple of
-// 256).  Sums then lie column by column; the epilogue turns 32 rows at a time
-// around in shared memory.  kGlu's first operand alternates 8 rows of Wg with the
-// same 8 of Wu (one copy through a 5-d tensor map), which puts both halves of an
-// output next to each other.
+// The output's rows are the product's second extent because that is any multiple
+// of 16: an expert with 40 rows, or the last rows of one with 2088, cost what they
+// are and not a tile of 256 (65536 rows over 32 experts of about 2048: 2737 us
+// with the rows as the first operand).  A thread then holds one column of many
+// rows; eight lanes turn 8 x 8 of them around with shuffles, so that rows leave
+// in 16-byte pieces and no shared memory is taken from the copies' stages.
+// kGlu's first operand alternates 8 rows of Wg with the same 8 of Wu (one copy
+// through a 5-d tensor map), which brings both halves of an output into one warp.
 //
-// Roles: warp 0 copies (TMA, 6 stages), warp 1 of the first CTA issues products,
-// warp 2 owns the tensor memory and looks the tiles up, warp 3 clears the rows past a segment's end
-// (kDw, whose inner index is the row), warps 4-11 read the sums back and run the
-// epilogue while the products of the next tile fill the other half of the tensor
-// memory.  Tiles of all experts form one list that the pairs walk with a fixed
-// stride; inside an expert 8 row tiles are taken together, so that the tiles in
-// flight share operands in L2.
+// Roles: warp 0 copies (TMA, 7 stages), warp 1 of the first CTA issues products,
+// warp 2 owns the tensor memory and walks the list of tiles, warp 3 clears the
+// rows past a segment's end (kDw, whose inner index is the row), warps 4-11 read
+// the sums back and run the epilogue while the products of the next tile fill the
+// other half of the tensor memory.
 
 #include "expert_gemm.cuh"
 #include "umma.cuh"
@@ -35,40 +34,86 @@
 namespace ep {
 
 constexpr int kGemmThreads = 384;
-constexpr int kStages = 6;
-constexpr int kTileM = 256, kTileN = 256, kHalf = 128;
+constexpr int kStages = 7;
+constexpr int kTileM = 256, kTileN = 256, kHalf = 128;   // columns, rows of the output; a CTA's columns
 constexpr int kTileK = 64;                       // bf16 elements of one 128-byte row
 constexpr int kOperandBytes = kHalf * kTileK * 2;   // 16 KB: one CTA's part of an operand
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBox = 32;                         // rows of a small copy
 constexpr int kEpilogueWarps = 8;
-constexpr int kTiles = 4;                        // tiles looked up ahead
-constexpr int kChunk = 32;                       // rows turned around at a time
-constexpr int kTurnBytes = kChunk * kHalf * 4;
 
 struct GemmParams {
   CUtensorMap a, b, b_small;
   ProductParams p;
   int tiles_n;
+  bool a_whole, b_whole;   // an MN-major operand's 128 columns in one copy (4-d map)
 };
 
 struct Shared {
   uint64_t full[kStages], empty[kStages];
   uint64_t landed[kStages], cleared[kStages];   // kDw: the block that a segment ends in
   uint64_t sums_full[2], sums_empty[2];
-  uint64_t tile_full[kTiles], tile_empty[kTiles];
-  Tile tiles[kTiles];
+  TileRing ring;
   uint32_t tmem;
-  TileTable table;
 };
+
+// Eight fp32 values -> 16 bytes of bf16, and back.
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void unpack8(uint4 b, float (&v)[8]) {
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+// Sums come column by column: a lane holds 16 rows of one column.  Eight lanes
+// turn eight of their rows around, after which lane j of them holds the eight
+// columns of row j.
+__device__ __forceinline__ void turn8(float (&v)[8], int lane) {
+#pragma unroll
+  for (int s = 4; s > 0; s >>= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & s) == 0) {
+        const float theirs = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i | s], s);
+        if (up)
+          v[i] = theirs;
+        else
+          v[i | s] = theirs;
+      }
+    }
+  }
+}
+
+// The epilogue of 8 columns from `col` on of output row `row` (kGlu aside).
+template <int kForm, int kAct>
+__device__ __forceinline__ void store8(const ProductParams& p, int64_t row, int col, const float (&bias)[8],
+                                       float (&z)[8]) {
+  const int64_t at = row * p.N + col;
+  if (kForm == kLinear) {
+    float r[8] = {};
+    if (p.residual != nullptr) unpack8(ld_v4(p.residual + at), r);   // may be the output itself: a plain load
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += bias[i];
+    if (p.keep != nullptr) st_v4(p.keep + at, pack8(z));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]) + r[i];
+  }
+  st_v4(static_cast<__nv_bfloat16*>(p.out) + at, pack8(z));
+}
 
 template <int kForm, int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_expert_gemm(const __grid_constant__ GemmParams g) {
   extern __shared__ uint8_t raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  float* turn = reinterpret_cast<float*>(stages + kStages * kStageBytes);   // [kChunk][kHalf]
-  Shared& sh = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes + (kForm == kDw ? 0 : kTurnBytes));
+  Shared& sh = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
   constexpr bool kAMn = kForm == kDw || kForm == kDx, kBMn = kForm == kDw;
   constexpr int kCols = kForm == kGlu ? kHalf : 256;   // output columns of a tile
 
@@ -76,12 +121,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int E = p.seg.E, fixed_rows = kForm == kDw ? p.K : -1;
 
   if (threadIdx.x == 0) {
     prefetch_map(&g.a);
     prefetch_map(&g.b);
-    if (kForm != kDw) prefetch_map(&g.b_small);
+    prefetch_map(&g.b_small);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh.full[s], 1);      // the first CTA's, with the bytes of both
       mbar_init(&sh.empty[s], 1);     // the products' commit
@@ -93,51 +137,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       mbar_init(&sh.sums_empty[i], 2 * kEpilogueWarps);
     }
     for (int i = 0; i < kTiles; ++i) {
-      mbar_init(&sh.tile_full[i], 1);
-      mbar_init(&sh.tile_empty[i], 1 + (rank == 0 ? 1 : 0) + (kForm == kDw ? 1 : 0) + kEpilogueWarps);
+      mbar_init(&sh.ring.full[i], 1);
+      mbar_init(&sh.ring.empty[i], 1 + (rank == 0 ? 1 : 0) + (kForm == kDw ? 1 : 0) + kEpilogueWarps);
     }
     fence_barrier_init();
   }
-  if (warp == 2) tmem_alloc<2>(&sh.tmem, 512);
-  build_table<kTileM, kGemmThreads>(sh.table, p.seg, fixed_rows, blockIdx.x == 0);
+  TileWalk walk;
+  if (warp == 2) {
+    tmem_alloc<2>(&sh.tmem, 512);
+    walk.begin(p.seg, kForm == kDw ? p.K : -1, kTileN, g.tiles_n, kCols, blockIdx.x == 0, lane);
+  }
   tmem_fence_before();
   cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = sh.tmem;
 
   bool ok = true;
-  Tile t;
   uint32_t taken = 0;
-  // the pair's next tile, as warp 2 looked it up; e < 0 past the last.  One
-  // arrival a consumer frees its place: `first` in a single thread, or in lane 0
-  // of a converged warp.
-  auto next_tile = [&](bool first) {
-    if (!ok) return false;
-    const uint32_t i = taken % kTiles;
-    ok = mbar_wait_bounded(&sh.tile_full[i], (taken / kTiles) & 1, 30 * kWaitNs);
-    if (!ok) return false;
-    t = sh.tiles[i];
-    ++taken;
-    if (first) mbar_arrive(&sh.tile_empty[i]);
-    return t.e >= 0;
-  };
-  auto next_tile_warp = [&]() {
-    const bool more = next_tile(false);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok && lane == 0) mbar_arrive(&sh.tile_empty[(taken - 1) % kTiles]);
-    return ok && more;
-  };
+  Tile t;
   auto inner_blocks = [&]() { return ((kForm == kDw ? t.count : p.K) + kTileK - 1) / kTileK; };
 
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- copies
     int s = 0;
     uint32_t phase = 0;
-    while (next_tile(true)) {
+    while (next_tile(sh.ring, taken, t, ok)) {
       const int blocks = inner_blocks();
-      const int half = kForm == kDw ? kHalf : (t.rows + 15) / 16 * 8;   // rows of the second operand in a CTA
-      const int boxes = (half + kBox - 1) / kBox;
-      const uint32_t bytes = 2 * kOperandBytes + 2 * (kForm == kDw ? kOperandBytes : boxes * (kOperandBytes / 4));
+      const int half = (t.rows + 15) / 16 * 8;   // rows of the second operand in a CTA
+      // copied 32 at a time, or all 128; kDw: 64 columns of d at a time
+      const int boxes = kForm == kDw ? (half + 63) / 64 : (half + kBox - 1) / kBox;
+      const uint32_t mine = kOperandBytes + boxes * (kForm == kDw ? kOperandBytes / 2 : kOperandBytes / 4);
       for (int kb = 0; kb < blocks; ++kb) {
         if (!mbar_wait_bounded(&sh.empty[s], phase ^ 1)) {
           ok = false;
@@ -149,22 +178,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         uint32_t bar = map_to_rank(smem_addr(&sh.full[s]), 0);
         if (tail) {
           bar = smem_addr(&sh.landed[s]);
-          mbar_arrive_expect_tx(&sh.landed[s], kStageBytes);
+          mbar_arrive_expect_tx(&sh.landed[s], mine);
         } else if (rank == 0) {
-          mbar_arrive_expect_tx(&sh.full[s], bytes);
+          mbar_arrive_expect_tx(&sh.full[s], 2 * mine);
         }
         const int k0 = (kForm == kDw ? blocks - 1 - kb : kb) * kTileK;
         if (kForm == kDw) {
-          for (int i = 0; i < 2; ++i) {
-            const int at_box = (int)rank * kHalf + i * 64;
-            tma_load_3d<true>(sa + i * (kOperandBytes / 2), &g.a, bar, t.m0 + at_box, t.start + k0, 0);
-            tma_load_3d<true>(sb + i * (kOperandBytes / 2), &g.b, bar, t.n0 + at_box, t.start + k0, 0);
-          }
+          const int n0 = t.n0 + (int)rank * kHalf, m0 = t.m0 + (int)rank * half;
+          if (g.a_whole)
+            tma_load_4d_pair(sa, &g.a, bar, 0, t.start + k0, n0 / 64, 0);
+          else
+            for (int i = 0; i < 2; ++i)
+              tma_load_3d<true>(sa + i * (kOperandBytes / 2), &g.a, bar, n0 + i * 64, t.start + k0, 0);
+          if (g.b_whole && half == kHalf && m0 % 64 == 0)
+            tma_load_4d_pair(sb, &g.b, bar, 0, t.start + k0, m0 / 64, 0);
+          else
+            for (int i = 0; i < boxes; ++i)
+              tma_load_3d<true>(sb + i * (kOperandBytes / 2), &g.b_small, bar, m0 + i * 64, t.start + k0, 0);
         } else {
           if (kForm == kGlu)
             tma_load_5d_pair(sa, &g.a, bar, k0, 0, 0, t.n0 / 8 + (int)rank * 8, t.e);
           else if (kForm == kLinear)
             tma_load_3d<true>(sa, &g.a, bar, k0, t.n0 + (int)rank * kHalf, t.e);
+          else if (g.a_whole)
+            tma_load_4d_pair(sa, &g.a, bar, 0, k0, (t.n0 + (int)rank * kHalf) / 64, t.e);
           else
             for (int i = 0; i < 2; ++i)
               tma_load_3d<true>(sa + i * (kOperandBytes / 2), &g.a, bar, t.n0 + (int)rank * kHalf + i * 64, k0, t.e);
@@ -186,66 +223,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       while (globaltimer_ns() - t0 < 2000000ull) {
       }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- products
-    int s = 0;
-    uint32_t n = 0, full = 0, cleared = 0;   // parities, a bit per stage
-    while (next_tile(true)) {
+    // the whole warp walks along, so that addresses stay uniform; one lane issues
+    const bool issue = elect_one();
+    // MN-major: 64-element columns 8 KB apart, 16 inner rows of 128 bytes a product
+    const uint32_t a0 = umma_desc_lo(smem_addr(stages), kAMn ? kOperandBytes / 2 : 16);
+    const uint32_t b0 = umma_desc_lo(smem_addr(stages) + kOperandBytes, kBMn ? kOperandBytes / 2 : 16);
+    constexpr uint32_t kStepA = (kAMn ? 2048 : 32) >> 4, kStepB = (kBMn ? 2048 : 32) >> 4;
+    uint32_t s = 0, n = 0, full = 0, cleared = 0;   // parities: a bit per stage
+    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       if (blocks == 0) continue;
-      const uint32_t idesc = umma_idesc_bf16(kTileM, kForm == kDw ? kTileN : (t.rows + 15) / 16 * 16, kAMn, kBMn);
+      const uint32_t idesc = umma_idesc_bf16(kTileM, (t.rows + 15) / 16 * 16, kAMn, kBMn);
       const uint32_t half = n & 1, d = tmem + half * kTileN;
-      if (!mbar_wait_cluster(&sh.sums_empty[half], ((n >> 1) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
+      ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.sums_empty[half], ((n >> 1) & 1) ^ 1));
+      if (!ok) break;
       tmem_fence_after();
-      for (int kb = 0; kb < blocks; ++kb) {
-        const bool tail = kForm == kDw && kb == 0 && t.count % 16 != 0;
-        if (tail) {
-          ok = mbar_wait_cluster(&sh.cleared[s], (cleared >> s) & 1);
+      int kb = 0;
+      if (kForm == kDw) {   // the segment's end first: as many products of 16 inner rows as it leaves
+        if (t.count % 16 != 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.cleared[s], (cleared >> s) & 1));
           cleared ^= 1u << s;
         } else {
-          ok = mbar_wait_bounded(&sh.full[s], (full >> s) & 1);
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], (full >> s) & 1));
           full ^= 1u << s;
         }
         if (!ok) break;
         tmem_fence_after();
-        // products of 16 inner rows: as many as the segment's end leaves
-        const int steps = kForm == kDw && kb == 0 ? (t.count - (blocks - 1) * kTileK + 15) / 16 : kTileK / 16;
-        const uint32_t sa = smem_addr(stages + s * kStageBytes), sb = sa + kOperandBytes;
-        // MN-major: 64-element columns 8 KB apart, 16 inner rows of 128 bytes a product
-        const uint64_t da = umma_desc(sa, kAMn ? kOperandBytes / 2 : 16), db = umma_desc(sb, kBMn ? kOperandBytes / 2 : 16);
+        if (issue) {
+          const int steps = (t.count - (blocks - 1) * kTileK + 15) / 16;
+          for (int i = 0; i < steps; ++i)
+            umma_bf16_pair(d, a0 + s * (kStageBytes >> 4) + i * kStepA, b0 + s * (kStageBytes >> 4) + i * kStepB, idesc, i > 0);
+          umma_commit_pair(&sh.empty[s]);
+        }
+        if (++s == kStages) s = 0;
+        kb = 1;
+      }
+      for (; kb < blocks; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], (full >> s) & 1));
+        if (!ok) break;
+        full ^= 1u << s;
+        tmem_fence_after();
+        if (issue) {
+          const uint32_t a = a0 + s * (kStageBytes >> 4), b = b0 + s * (kStageBytes >> 4);
+          umma_bf16_pair(d, a, b, idesc, kForm == kDw || kb > 0);
 #pragma unroll
-        for (int i = 0; i < kTileK / 16; ++i)
-          if (i < steps)
-            umma_bf16_pair(d, da + i * (kAMn ? 2048 >> 4 : 32 >> 4), db + i * (kBMn ? 2048 >> 4 : 32 >> 4), idesc,
-                           kb > 0 || i > 0);
-        umma_commit_pair(&sh.empty[s]);
+          for (uint32_t i = 1; i < kTileK / 16; ++i) umma_bf16_pair(d, a + i * kStepA, b + i * kStepB, idesc, true);
+          umma_commit_pair(&sh.empty[s]);
+        }
         if (++s == kStages) s = 0;
       }
-      umma_commit_pair(&sh.sums_full[half]);
+      if (!ok) break;
+      if (issue) umma_commit_pair(&sh.sums_full[half]);
       ++n;
     }
-  } else if (warp == 2 && lane == 0) {
-    // ---------------------------------------------------------------- tiles
-    int64_t at = pair;
-    for (uint32_t n = 0; ok; ++n, at += pairs) {
-      const uint32_t i = n % kTiles;
-      const bool more = tile_at<kTileM, kForm != kDw>(sh.table, E, fixed_rows, g.tiles_n, kCols, at, t);
-      // a place is free when the slowest reader is done with a tile: as long as the epilogue's wait
-      ok = mbar_wait_bounded(&sh.tile_empty[i], ((n / kTiles) & 1) ^ 1, 30 * kWaitNs);
-      if (!ok) break;
-      if (!more) t.e = -1;
-      sh.tiles[i] = t;
-      mbar_arrive(&sh.tile_full[i]);
-      if (!more) break;
-    }
+  } else if (warp == 2) {
+    ok = feed_tiles(sh.ring, walk, pair, pairs, lane);
   } else if (kForm == kDw && warp == 3) {
     // ---------------------------------------------------------------- rows past a segment's end
     int s = 0;
     uint32_t parity = 0;   // bit per stage
-    while (next_tile_warp()) {
+    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       if (t.count % 16 != 0) {
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.landed[s], (parity >> s) & 1, 2 * kWaitNs));
@@ -265,70 +304,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3, side = (warp - 4) >> 2;   // 32 lanes of the tensor memory; which columns of them
-    const int tid = threadIdx.x - 128;
+    const int q = warp & 3, side = (warp - 4) >> 2;   // 32 lanes of the tensor memory; which 16 of 32 rows
+    // the 8 columns of this lane's group; kGlu: 8 lanes of gate, 8 of up sums, of the same columns
+    const int h = (lane >> 3) & 1, j = lane & 7;
+    const int in_cta = kForm == kGlu ? q * 16 + (lane >> 4) * 8 : q * 32 + (lane & ~7);
     uint32_t n = 0;
-    while (next_tile_warp()) {
+    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       const uint32_t half = n & 1;
       if (blocks > 0) {
-        ok = mbar_wait_cluster(&sh.sums_full[half], (n >> 1) & 1, kWaitNs + (uint64_t)blocks * 2000);
-        // a thread that gives up takes its group along: the barriers below are for all of them
-        ok = __all_sync(0xffffffffu, ok);
-        if (kForm != kDw) ok = named_barrier_and(1, 32 * kEpilogueWarps, ok);
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.sums_full[half], (n >> 1) & 1,
+                                                       kWaitNs + (uint64_t)blocks * 2000));
         if (!ok) break;
         tmem_fence_after();
         ++n;
       }
       const uint32_t d = tmem + half * kTileN + ((uint32_t)(q * 32) << 16);
-      auto sums_read = [&]() {   // the next tile's products may have this half
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
-      };
-      if (kForm == kDw) {
-        const int m = t.m0 + (int)rank * kHalf + q * 32 + lane;
+      const int col = t.n0 + (int)rank * (kCols / 2) + in_cta;
+      const bool in = col < p.N;
+      const int64_t row0 = kForm == kDw ? (int64_t)t.e * p.K + t.m0 : (int64_t)t.start + t.m0;
+      float bias[8] = {};
+      if (kForm == kLinear && p.bias != nullptr && in)
+        unpack8(__ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)t.e * p.N + col)), bias);
 #pragma unroll 1
-        for (int c0 = side * kHalf; c0 < side * kHalf + kHalf; c0 += 32) {
-          float v[32];
-          if (blocks > 0) {
-            tmem_ld32(d + c0, v);
-            tmem_wait_ld();
-            if (c0 + 32 == side * kHalf + kHalf) sums_read();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-          }
-          if (m < p.K) store32<kForm, kAct>(p, t.e, (int64_t)t.e * p.K + m, t.n0 + c0, v, v);
-          __syncwarp();
-        }
-      } else {
-        constexpr int kGroups = kForm == kGlu ? 8 : 16;   // of 8 output columns in this CTA
-#pragma unroll 1
-        for (int r0 = 0; r0 < t.rows; r0 += kChunk) {
-          float v[16];
+      for (int r0 = 0; r0 < t.rows; r0 += 32) {
+        float v[16];
+        if (blocks > 0) {
           tmem_ld16(d + r0 + side * 16, v);
           tmem_wait_ld();
-          if (r0 + kChunk >= t.rows) sums_read();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) turn[(side * 16 + i) * kHalf + q * 32 + lane] = v[i];
-          named_barrier_sync(1, 32 * kEpilogueWarps);
-#pragma unroll
-          for (int i = tid; i < kChunk * kGroups; i += 32 * kEpilogueWarps) {
-            const int r = r0 + i / kGroups, c = i % kGroups;
-            const int col = t.n0 + (int)rank * (kGroups * 8) + c * 8;
-            if (r < t.rows && col < p.N) {
-              float z[8], u[8];
-              const float* src = turn + (i / kGroups) * kHalf + c * (kForm == kGlu ? 16 : 8);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) z[j] = src[j];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) u[j] = kForm == kGlu ? src[8 + j] : 0.0f;
-              store8<kForm, kAct>(p, t.e, (int64_t)t.start + t.m0 + r, col, z, u);
-            }
+          if (r0 + 32 >= t.rows) {   // the sums are read: the next tile's products may have this half
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
           }
-          named_barrier_sync(1, 32 * kEpilogueWarps);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
         }
+        float lo[8], hi[8];   // rows j and j + 8 of the 16
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          lo[i] = v[i];
+          hi[i] = v[8 + i];
+        }
+        turn8(lo, lane);
+        turn8(hi, lane);
+        const int r = r0 + side * 16 + j;
+        if (kForm == kGlu) {
+          if (p.keep != nullptr && in) {
+            __nv_bfloat16* keep = p.keep + ((row0 + r) * 2 + h) * p.N + col;
+            if (r < t.rows) st_v4(keep, pack8(lo));
+            if (r + 8 < t.rows) st_v4(keep + (int64_t)16 * p.N, pack8(hi));
+          }
+          // gate lanes take row j, up lanes row j + 8
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float theirs = __shfl_xor_sync(0xffffffffu, h ? lo[i] : hi[i], 8);
+            lo[i] = act_value<kAct>(h ? theirs : lo[i]) * (h ? hi[i] : theirs);
+          }
+          if (in && r + 8 * h < t.rows)
+            st_v4(static_cast<__nv_bfloat16*>(p.out) + (row0 + r + 8 * h) * p.N + col, pack8(lo));
+        } else if (in) {
+          if (r < t.rows) store8<kForm, kAct>(p, row0 + r, col, bias, lo);
+          if (r + 8 < t.rows) store8<kForm, kAct>(p, row0 + r + 8, col, bias, hi);
+        }
+        __syncwarp();
       }
     }
   }
@@ -342,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
 template <int kForm, int kAct>
 static int launch_gemm_t(const GemmParams& g, int64_t tiles, cudaStream_t stream) {
-  const int smem = kStages * kStageBytes + (kForm == kDw ? 0 : kTurnBytes) + (int)sizeof(Shared) + 1024;
+  const int smem = kStages * kStageBytes + (int)sizeof(Shared) + 1024;
   const void* fn = reinterpret_cast<const void*>(k_expert_gemm<kForm, kAct>);
   if (ep_host::ensure_max_smem(fn, smem) != EP_OK) return EP_ERR_CUDA;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, ep_host::grid_cap(1) / 2));
@@ -370,10 +410,25 @@ int launch_gemm_bf16(Form form, const ProductParams& p, int act, cudaStream_t st
     const uint32_t box[3] = {b0, b1, 1};
     if (rc == EP_OK) rc = ep_host::make_map(m, false, 3, base, dims, strides, box);
   };
+  // An MN-major operand of `wide` columns whose 64-column pieces end with the row: both pieces of a
+  // CTA's 128 columns in one copy.
+  auto map_whole = [&](CUtensorMap* m, const void* base, uint64_t wide, uint64_t deep, uint64_t count) {
+    const uint64_t dims[4] = {64, deep, wide / 64, count}, strides[3] = {wide * 2, 128, wide * deep * 2};
+    const uint32_t box[4] = {64, kTileK, 2, 1};
+    if (rc == EP_OK) rc = ep_host::make_map(m, false, 4, base, dims, strides, box);
+  };
+  g.a_whole = (form == kDw || form == kDx) && p.N % 64 == 0;
+  g.b_whole = form == kDw && p.K % 64 == 0;
   if (form == kDw) {
-    map(&g.a, p.a, K, rows, 1, 64, kTileK);
-    map(&g.b, p.b, N, rows, 1, 64, kTileK);
-    g.b_small = g.b;
+    if (g.a_whole)
+      map_whole(&g.a, p.b, N, rows, 1);
+    else
+      map(&g.a, p.b, N, rows, 1, 64, kTileK);
+    map(&g.b_small, p.a, K, rows, 1, 64, kTileK);
+    if (g.b_whole)
+      map_whole(&g.b, p.a, K, rows, 1);
+    else
+      g.b = g.b_small;
   } else {
     if (form == kGlu) {   // (inner, row of 8, gate / up, 8-row group, expert)
       const uint64_t dims[5] = {K, 8, 2, N / 8, E}, strides[4] = {K * 2, N * K * 2, 8 * K * 2, 2 * N * K * 2};
@@ -381,6 +436,8 @@ int launch_gemm_bf16(Form form, const ProductParams& p, int act, cudaStream_t st
       rc = ep_host::make_map(&g.a, false, 5, p.b, dims, strides, box);
     } else if (form == kLinear) {
       map(&g.a, p.b, K, N, E, kTileK, kHalf);
+    } else if (g.a_whole) {
+      map_whole(&g.a, p.b, N, K, E);
     } else {
       map(&g.a, p.b, N, K, E, 64, kTileK);
     }
@@ -391,7 +448,7 @@ int launch_gemm_bf16(Form form, const ProductParams& p, int act, cudaStream_t st
   const int cols = form == kGlu ? kHalf : kTileN;
   g.tiles_n = (p.N + cols - 1) / cols;
   // at most one ragged row tile an expert
-  const int64_t tiles_m = form == kDw ? (int64_t)p.seg.E * ((p.K + kTileM - 1) / kTileM) : p.rows / kTileM + p.seg.E;
+  const int64_t tiles_m = form == kDw ? (int64_t)p.seg.E * ((p.K + kTileN - 1) / kTileN) : p.rows / kTileN + p.seg.E;
   if (tiles_m >= (int64_t)1 << 31) return EP_ERR_INVALID_ARG;
   const int64_t tiles = tiles_m * g.tiles_n;
   switch (form) {

@@ -24,7 +24,8 @@ struct ProductParams {
 };
 
 // One tile of the list: output rows m0 .. m0 + rows of expert e (numbered inside
-// its segment; kDw: inside its weights) and output columns from n0 on.
+// its segment; kDw: inside its weights) and output columns from n0 on.  e < 0:
+// past the last.
 struct Tile {
   int e, m0, rows, n0;
   int start, count;   // segment
@@ -32,141 +33,125 @@ struct Tile {
 
 constexpr int kGroupM = 8;   // row tiles taken together
 
-struct TileTable {
-  int32_t warp_total[32];
-  int32_t first_tile[kMaxE + 1];   // row tiles of the experts before e
-  int32_t start[kMaxE], count[kMaxE];
-};
+// Walks the list of all experts' tiles; one warp, converged.  An expert has
+// ceil(rows / tile_rows) row tiles, its rows spread over them in units of 16, and
+// tiles_n column tiles of `cols`; 8 row tiles are taken together, column after
+// column.  Looks at 32 experts at a time, so that nothing has to be kept for
+// all of them.
+struct TileWalk {
+  Segments seg;
+  int fixed_rows;   // output rows where they are not the segment's (kDw), else -1
+  int tile_rows, tiles_n, cols;
+  int e0;           // first of the 32 experts looked at
+  int64_t before;   // tiles of the experts below e0
+  Segment s;        // this lane's expert
+  int rows, upto;   // its output rows; row tiles of the lanes up to it
 
-// Row tiles before each expert, and the segments, in shared memory.
-// fixed_rows: the output's rows where they are not the segment's (kDw), else -1.
-template <int kTileM, int kThreads>
-__device__ __forceinline__ void build_table(TileTable& sh, Segments seg, int fixed_rows, bool report) {
-  const int E = seg.E, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int base = 0;
-  if (!report) seg.status = nullptr;   // one CTA reports a segment that was cut
-  for (int e0 = 0; e0 < E; e0 += kThreads) {
-    const int e = e0 + tid;
-    int tiles = 0;
-    if (e < E) {
-      const Segment s = segment_of(seg, e);
-      sh.start[e] = (int)s.start;
-      sh.count[e] = s.count;
-      tiles = ((fixed_rows >= 0 ? fixed_rows : s.count) + kTileM - 1) / kTileM;
+  __device__ __forceinline__ void look(int at, int lane) {
+    e0 = at;
+    s = {0, 0};
+    rows = 0;
+    if (e0 + lane < seg.E) {
+      s = segment_of(seg, e0 + lane);
+      rows = fixed_rows >= 0 ? fixed_rows : s.count;
     }
-    int incl = tiles;
+    upto = (rows + tile_rows - 1) / tile_rows;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    if (lane == 31) sh.warp_total[warp] = incl;
-    __syncthreads();
-    int before = base, all = base;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += sh.warp_total[w];
-      all += sh.warp_total[w];
-    }
-    if (e < E) sh.first_tile[e] = before + incl - tiles;
-    base = all;
-    __syncthreads();
   }
-  if (tid == 0) sh.first_tile[E] = base;
-  __syncthreads();
-}
 
-// Tile number t of the list, false past its end.
-template <int kTileM, bool kEven>
-__device__ __forceinline__ bool tile_at(const TileTable& sh, int E, int fixed_rows, int tiles_n, int cols, int64_t t,
-                                        Tile& out) {
-  const int64_t total = (int64_t)sh.first_tile[E] * tiles_n;
-  if (t >= total) return false;
-  int lo = 0, hi = E;   // last expert whose first tile is at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((int64_t)sh.first_tile[mid] * tiles_n <= t)
-      lo = mid;
-    else
-      hi = mid;
+  // report: this warp records a segment that was cut.
+  __device__ __forceinline__ void begin(const Segments& segments, int fixed, int tile, int n, int c, bool report, int lane) {
+    seg = segments;
+    if (!report) seg.status = nullptr;
+    fixed_rows = fixed;
+    tile_rows = tile;
+    tiles_n = n;
+    cols = c;
+    before = 0;
+    look(0, lane);
   }
-  // experts without tiles share a first tile with the next: lo is the last of them, the one that has it
-  const int tiles_m = sh.first_tile[lo + 1] - sh.first_tile[lo];
-  const int64_t in = t - (int64_t)sh.first_tile[lo] * tiles_n;
-  const int64_t group = in / ((int64_t)kGroupM * tiles_n);
-  const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
-  const int64_t r = in - group * kGroupM * tiles_n;
-  out.e = lo;
-  out.start = sh.start[lo];
-  out.count = sh.count[lo];
-  out.n0 = (int)(r / gm) * cols;
-  const int of = fixed_rows >= 0 ? fixed_rows : out.count;
-  const int i = (int)group * kGroupM + (int)(r % gm);
-  if (kEven) {   // an expert's rows are spread over its row tiles in units of 16
+
+  // Tile number t (not below the last one asked for).
+  __device__ __forceinline__ Tile at(int64_t t, int lane) {
+    Tile out = {-1, 0, 0, 0, 0, 0};
+    for (;;) {
+      const int64_t all = (int64_t)__shfl_sync(0xffffffffu, upto, 31) * tiles_n;
+      if (t < before + all) break;
+      if (e0 + 32 >= seg.E) return out;
+      before += all;
+      look(e0 + 32, lane);
+    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, t < before + (int64_t)upto * tiles_n)) - 1;
+    const int tiles_m = __shfl_sync(0xffffffffu, (rows + tile_rows - 1) / tile_rows, who);
+    const int64_t in = t - before - (int64_t)(__shfl_sync(0xffffffffu, upto, who) - tiles_m) * tiles_n;
+    const int of = __shfl_sync(0xffffffffu, rows, who);
+    out.e = e0 + who;
+    out.start = __shfl_sync(0xffffffffu, (int)s.start, who);
+    out.count = __shfl_sync(0xffffffffu, s.count, who);
+    const int64_t group = in / ((int64_t)kGroupM * tiles_n);
+    const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
+    const int64_t r = in - group * kGroupM * tiles_n;
+    const int i = (int)group * kGroupM + (int)(r % gm);
     const int64_t units = (of + 15) / 16;
+    out.n0 = (int)(r / gm) * cols;
     out.m0 = (int)(units * i / tiles_m) * 16;
     out.rows = min(of, (int)(units * (i + 1) / tiles_m) * 16) - out.m0;
-  } else {
-    out.m0 = i * kTileM;
-    out.rows = min(kTileM, of - out.m0);
+    return out;
   }
-  return true;
-}
+};
 
-// Eight fp32 sums -> 16 bytes of bf16.
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
+// The looked-up tiles on their way from the warp that walks the list to the
+// other warps of the CTA.
+constexpr int kTiles = 4;
+constexpr uint64_t kTileWaitNs = 30 * kWaitNs;   // a reader may be as far behind as a tile takes
+struct TileRing {
+  uint64_t full[kTiles], empty[kTiles];
+  Tile tiles[kTiles];
+};
 
-// The epilogue of 8 columns from n on of output row `row` of expert e: z the sums
-// (kGlu: of the gate), u those of the up projection.
-template <int kForm, int kAct>
-__device__ __forceinline__ void store8(const ProductParams& p, int e, int64_t row, int n, float (&z)[8],
-                                       const float* u) {
-  if (kForm == kGlu) {
-    if (p.keep != nullptr) {
-      st_v4(p.keep + row * 2 * p.N + n, pack8(z));
-      st_v4(p.keep + (row * 2 + 1) * p.N + n, pack8(u));
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]) * u[i];
-  } else if (kForm == kLinear) {
-    if (p.bias != nullptr) {
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)e * p.N + n));
-      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[2 * i] += bf16_lo(w[i]);
-        z[2 * i + 1] += bf16_hi(w[i]);
-      }
-    }
-    if (p.keep != nullptr) st_v4(p.keep + row * p.N + n, pack8(z));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]);
-    if (p.residual != nullptr) {   // may be the output itself: a plain load
-      const uint4 r = ld_v4(p.residual + row * p.N + n);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[2 * i] += bf16_lo(w[i]);
-        z[2 * i + 1] += bf16_hi(w[i]);
-      }
-    }
-  }
-  st_v4(static_cast<__nv_bfloat16*>(p.out) + row * p.N + n, pack8(z));
+// Takes the next tile; false past the last one, or (ok false) when the wait ran
+// out.  The caller frees the place with one arrival on *free.
+__device__ __forceinline__ bool take_tile(TileRing& ring, uint32_t& taken, Tile& t, bool& ok, uint64_t*& free) {
+  const uint32_t i = taken % kTiles;
+  ok = mbar_wait_bounded(&ring.full[i], (taken / kTiles) & 1, kTileWaitNs);
+  if (!ok) return false;
+  t = ring.tiles[i];
+  free = &ring.empty[i];
+  ++taken;
+  return t.e >= 0;
 }
-
-// As store8 for 32 columns that one thread holds, up to the output's last.
-template <int kForm, int kAct>
-__device__ __forceinline__ void store32(const ProductParams& p, int e, int64_t row, int n0, float (&v)[32],
-                                        const float* u) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (n0 + q * 8 >= p.N) break;
-    float z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = v[q * 8 + i];
-    store8<kForm, kAct>(p, e, row, n0 + q * 8, z, u + q * 8);
+// One thread alone.
+__device__ __forceinline__ bool next_tile(TileRing& ring, uint32_t& taken, Tile& t, bool& ok) {
+  uint64_t* free;
+  if (!ok) return false;
+  const bool more = take_tile(ring, taken, t, ok, free);
+  if (ok) mbar_arrive(free);
+  return more;
+}
+// A converged warp.
+__device__ __forceinline__ bool next_tile_warp(TileRing& ring, uint32_t& taken, Tile& t, bool& ok, int lane) {
+  uint64_t* free = nullptr;
+  if (!ok) return false;
+  const bool more = take_tile(ring, taken, t, ok, free);
+  ok = __all_sync(0xffffffffu, ok);
+  if (ok && lane == 0) mbar_arrive(free);
+  return ok && more;
+}
+// The walking warp: tiles first, first + step, ... until the list ends.
+__device__ __forceinline__ bool feed_tiles(TileRing& ring, TileWalk& walk, int64_t first, int64_t step, int lane) {
+  for (uint32_t n = 0;; ++n, first += step) {
+    const uint32_t i = n % kTiles;
+    const Tile t = walk.at(first, lane);
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ring.empty[i], ((n / kTiles) & 1) ^ 1, kTileWaitNs))) return false;
+    if (lane == 0) {
+      ring.tiles[i] = t;
+      mbar_arrive(&ring.full[i]);
+    }
+    if (t.e < 0) return true;
   }
 }
 

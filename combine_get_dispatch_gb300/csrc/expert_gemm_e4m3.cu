@@ -39,8 +39,8 @@ struct MxParams {
 struct MxShared {
   uint64_t full[kMxStages], scaled[kMxStages], empty[kMxStages];
   uint64_t sums_full, sums_empty;
+  TileRing ring;
   uint32_t tmem;
-  TileTable table;
 };
 
 // One block's scale bytes as a lane of a scale warp reads them: rows lane + 32 j
@@ -48,6 +48,45 @@ struct MxShared {
 struct MxScales {
   uint8_t a[4], b[2];
 };
+
+// Eight fp32 sums -> 16 bytes of bf16.
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void add8(float* z, uint4 b) {
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    z[2 * i] += bf16_lo(w[i]);
+    z[2 * i + 1] += bf16_hi(w[i]);
+  }
+}
+
+// The epilogue of 32 columns from n0 on of output row `row` of expert e: v the
+// sums (kGlu: of the gate), u those of the up projection.
+template <int kForm, int kAct>
+__device__ __forceinline__ void store32(const ProductParams& p, int e, int64_t row, int n0, float (&v)[32],
+                                        const float (&u)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int n = n0 + q * 8;
+    if (n >= p.N) break;
+    float* z = v + q * 8;
+    if (kForm == kGlu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]) * u[q * 8 + i];
+    } else {
+      if (p.bias != nullptr) add8(z, __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)e * p.N + n)));
+      if (p.keep != nullptr) st_v4(p.keep + row * p.N + n, pack8(z));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]);
+      if (p.residual != nullptr) add8(z, ld_v4(p.residual + row * p.N + n));   // may be the output itself
+    }
+    st_v4(static_cast<__nv_bfloat16*>(p.out) + row * p.N + n, pack8(z));
+  }
+}
 
 template <int kForm, int kAct>
 __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid_constant__ MxParams g) {
@@ -59,7 +98,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
 
   const ProductParams& p = g.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = p.seg.E, blocks = p.K / kFp8Block;
+  const int blocks = p.K / kFp8Block;
 
   if (threadIdx.x == 0) {
     prefetch_map(&g.a);
@@ -72,22 +111,30 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     }
     mbar_init(&sh.sums_full, 1);
     mbar_init(&sh.sums_empty, 4);
+    for (int i = 0; i < kTiles; ++i) {
+      mbar_init(&sh.ring.full[i], 1);
+      mbar_init(&sh.ring.empty[i], 2 + 4 + 4);   // copies, products, scale warps, epilogue warps
+    }
     fence_barrier_init();
   }
-  if (warp == 2) tmem_alloc<1>(&sh.tmem, 512);
-  build_table<kMxTileM, kMxThreads>(sh.table, p.seg, -1, blockIdx.x == 0);
+  TileWalk walk;
+  if (warp == 2) {
+    tmem_alloc<1>(&sh.tmem, 512);
+    walk.begin(p.seg, -1, kMxTileM, g.tiles_n, kCols, blockIdx.x == 0, lane);
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = sh.tmem;
 
   bool ok = true;
+  uint32_t taken = 0;
   Tile t;
   if (warp == 0 && lane == 0) {
     int s = 0;
     uint32_t phase = 0;
-    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM, false>(sh.table, E, -1, g.tiles_n, kCols, at, t); at += gridDim.x) {
-      const int boxes = min(4, (t.count - t.m0 + kMxBox - 1) / kMxBox);
+    while (next_tile(sh.ring, taken, t, ok)) {
+      const int boxes = (t.rows + kMxBox - 1) / kMxBox;
       for (int kb = 0; kb < blocks; ++kb) {
         if (!mbar_wait_bounded(&sh.empty[s], phase ^ 1)) {
           ok = false;
@@ -115,42 +162,44 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
       while (globaltimer_ns() - t0 < 2000000ull) {
       }
     }
-  } else if (warp == 1 && lane == 0) {
-    int s = 0;
-    uint32_t phase = 0, n = 0;
-    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM, false>(sh.table, E, -1, g.tiles_n, kCols, at, t); at += gridDim.x) {
-      if (!mbar_wait_bounded(&sh.sums_empty, (n & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
+  } else if (warp == 1) {
+    // the whole warp walks along, so that addresses stay uniform; one lane issues
+    const bool issue = elect_one();
+    const uint32_t a0 = umma_desc_lo(smem_addr(stages), 16), b0 = umma_desc_lo(smem_addr(stages) + kMxABytes, 16);
+    uint32_t s = 0, phase = 0, n = 0;
+    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_empty, (n & 1) ^ 1));
+      if (!ok) break;
       ++n;
       tmem_fence_after();
       for (int kb = 0; kb < blocks; ++kb) {
-        if (!mbar_wait_bounded(&sh.full[s], phase) || !mbar_wait_bounded(&sh.scaled[s], phase)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], phase) && mbar_wait_bounded(&sh.scaled[s], phase));
+        if (!ok) break;
         tmem_fence_after();
-        const uint32_t sa = smem_addr(stages + s * kMxStageBytes);
-        const uint64_t da = umma_desc(sa, 16), db = umma_desc(sa + kMxABytes, 16);
-        const uint32_t sc = tmem + kMxScaleCol + s * kMxScaleCols;
+        if (issue) {
+          const uint32_t a = a0 + s * (kMxStageBytes >> 4), b = b0 + s * (kMxStageBytes >> 4);
+          const uint32_t sc = tmem + kMxScaleCol + s * kMxScaleCols;
 #pragma unroll
-        for (int i = 0; i < kFp8Block / 32; ++i)
-          umma_mx8(tmem, da + i * (32 >> 4), db + i * (32 >> 4), kIdesc, sc, sc + kMxScaleB, kb > 0 || i > 0);
-        umma_commit(&sh.empty[s]);
+          for (uint32_t i = 0; i < kFp8Block / 32; ++i)
+            umma_mx8(tmem, a + i * (32 >> 4), b + i * (32 >> 4), kIdesc, sc, sc + kMxScaleB, kb > 0 || i > 0);
+          umma_commit(&sh.empty[s]);
+        }
         if (++s == kMxStages) {
           s = 0;
           phase ^= 1;
         }
       }
-      umma_commit(&sh.sums_full);
+      if (!ok) break;
+      if (issue) umma_commit(&sh.sums_full);
     }
+  } else if (warp == 2) {
+    ok = feed_tiles(sh.ring, walk, blockIdx.x, gridDim.x, lane);
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- scales
     int s = 0;
     uint32_t phase = 0;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM, false>(sh.table, E, -1, g.tiles_n, kCols, at, t); at += gridDim.x) {
+    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
       const int64_t owner = t.start / p.seg.cap;
       const uint8_t* xs = p.a_scales + owner * blocks * p.seg.cap + (t.start - owner * p.seg.cap) + t.m0 + lane;
       const uint8_t* ws[2];
@@ -165,7 +214,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
         MxScales v;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          v.a[j] = kb < blocks && t.m0 + 32 * j + lane < t.count ? __ldg(xs + (int64_t)kb * p.seg.cap + 32 * j) : (uint8_t)0;
+          v.a[j] = kb < blocks && 32 * j + lane < t.rows ? __ldg(xs + (int64_t)kb * p.seg.cap + 32 * j) : (uint8_t)0;
         v.b[0] = kb < blocks ? __ldg(ws[0] + kb) : (uint8_t)0;
         v.b[1] = kb < blocks && second ? __ldg(ws[1] + kb) : (uint8_t)0;
         return v;
@@ -207,9 +256,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     const int q = warp & 3;
     uint32_t n = 0;
     const uint32_t d = tmem + ((uint32_t)(q * 32) << 16);
-    for (int64_t at = blockIdx.x; ok && tile_at<kMxTileM, false>(sh.table, E, -1, g.tiles_n, kCols, at, t); at += gridDim.x) {
+    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
       const int m = t.m0 + q * 32 + lane;
-      const bool in = m < t.count;
+      const bool in = q * 32 + lane < t.rows;
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_full, n & 1, kWaitNs + (uint64_t)blocks * 2000));
       if (!ok) break;
       ++n;

@@ -73,7 +73,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
-// As tma_load_3d<true> with five coordinates.
+// As tma_load_3d<true> with four and five coordinates.
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
                                                  int c2, int c3, int c4) {
   asm volatile(
@@ -158,14 +167,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
 
 // Shared-memory operand in the 128-byte swizzle: rows of 128 bytes, 8-row
 // groups 1024 bytes apart (SBO).  K-major operands are one 128-byte row wide;
-// MN-major ones continue every LBO bytes.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo_bytes) {
-  uint64_t d = (uint64_t)((addr & 0x3ffffu) >> 4);
-  d |= (uint64_t)(lbo_bytes >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;   // descriptor version of sm_100
-  d |= (uint64_t)2 << 61;   // 128-byte swizzle
-  return d;
+// MN-major ones continue every LBO bytes.  The low word holds the address (in
+// 16-byte units, so that it advances by additions) and the LBO, the high word is
+// the same for all.
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t addr, uint32_t lbo_bytes) {
+  return ((addr & 0x3ffffu) >> 4) | ((lbo_bytes >> 4) << 16);
+}
+// SBO, descriptor version of sm_100, 128-byte swizzle
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
 }
 
 // Instruction descriptor, bf16 operands and fp32 sums.
@@ -174,11 +189,12 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool a_mn, 
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void umma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "r"(kDescHi)
       : "memory");
 }
 
@@ -188,12 +204,13 @@ __host__ __device__ constexpr uint32_t umma_idesc_mx8(int m, int n) {
   return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void umma_mx8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t scale_a,
+__device__ __forceinline__ void umma_mx8(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t scale_a,
                                          uint32_t scale_b, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"((uint32_t)add)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 a, {%1, %7};\n mov.b64 b, {%2, %7};\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"((uint32_t)add), "r"(kDescHi)
       : "memory");
 }
 
