@@ -31,11 +31,11 @@ struct Tile {
   int start, count;   // segment
 };
 
-constexpr int kGroupM = 8;   // row tiles taken together
+constexpr int kGroupM = 16;   // row tiles taken together
 
 // Walks the list of all experts' tiles; one warp, converged.  An expert has
 // ceil(rows / tile_rows) row tiles, its rows spread over them in units of 16, and
-// tiles_n column tiles of `cols`; 8 row tiles are taken together, column after
+// tiles_n column tiles of `cols`; 16 row tiles are taken together, column after
 // column.  Looks at 32 experts at a time, so that nothing has to be kept for
 // all of them.
 struct TileWalk {
