@@ -139,15 +139,20 @@ def error_string(code: int) -> str:
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    # the raw handle of torch.cuda.current_stream(), without the object (2.8 us of a call's host time)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t: torch.Tensor | None, dtype, shape=None, name="tensor", optional=False):
+    if (t is not None and t.is_cuda and (dtype is None or t.dtype == dtype) and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if t is None:
         if optional:
             return
