@@ -7,7 +7,7 @@
 namespace ep {
 
 constexpr int kThreads = 256;
-constexpr int kSlopeRows = 16;   // rows a CTA of k_glu_slope takes at a time
+constexpr int kSlopeRows = 32;   // rows a CTA of k_glu_slope takes at a time
 
 struct SlopeParams {
   Segments seg;
@@ -19,7 +19,7 @@ struct SlopeParams {
 };
 
 // dgu = (dh * up * act'(gate), dh * act(gate)) over the rows of every segment,
-// 8 columns a thread.  A CTA takes 16 rows of an expert at a time from the list
+// 8 columns a thread.  A CTA takes 32 rows of an expert at a time from the list
 // of all of them, whatever the experts' shares are (one grid row an expert took
 // 97 us where one of 32 experts had a quarter of 12288 rows; read and written
 // once, 174 MB, 26 us at the copy rate).

@@ -16,13 +16,15 @@
 // The output's rows are the product's second extent because that is any multiple
 // of 16: an expert with 40 rows, or the last rows of one with 2088, cost what they
 // are and not a tile of 256 (65536 rows over 32 experts of about 2048: 2737 us
-// with the rows as the first operand).  A thread then holds one column of many
-// rows; eight lanes turn 8 x 8 of them around with shuffles, so that rows leave
-// in 16-byte pieces and no shared memory is taken from the copies' stages.
-// kGlu's first operand alternates 8 rows of Wg with the same 8 of Wu (one copy
-// through a 5-d tensor map), which brings both halves of an output into one warp.
+// with the rows as the first operand).  Sums then come out column by column;
+// stmatrix turns them around on their way to a 32-row buffer from which one TMA
+// store writes whole lines (turned by shuffles and stored by every thread, the
+// weights' gradient of 32 experts with 12288 rows took 440 us, 278 us of them
+// without any epilogue).  kGlu's first operand alternates 8 rows of Wg with the
+// same 8 of Wu (one copy through a 5-d tensor map), which brings both halves of
+// an output into one thread.
 //
-// Roles: warp 0 copies (TMA, 7 stages), warp 1 of the first CTA issues products,
+// Roles: warp 0 copies (TMA, 6 stages; 5 to 7 measure the same), warp 1 of the first CTA issues products,
 // warp 2 owns the tensor memory and walks the list of tiles, warp 3 clears the
 // rows past a segment's end (kDw, whose inner index is the row), warps 4-11 read
 // the sums back and run the epilogue while the products of the next tile fill the
@@ -34,16 +36,20 @@
 namespace ep {
 
 constexpr int kGemmThreads = 384;
-constexpr int kStages = 7;
+constexpr int kStages = 6;
 constexpr int kTileM = 256, kTileN = 256, kHalf = 128;   // columns, rows of the output; a CTA's columns
 constexpr int kTileK = 64;                       // bf16 elements of one 128-byte row
 constexpr int kOperandBytes = kHalf * kTileK * 2;   // 16 KB: one CTA's part of an operand
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBox = 32;                         // rows of a small copy
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueWarps = 8;                // two groups of four
+constexpr int kChunk = 32;                       // rows a group takes at a time
+constexpr int kPieceBytes = kChunk * 128;        // 32 rows of 64 columns
+constexpr int kBufferBytes = 2 * kPieceBytes;    // two buffers a group
+constexpr int kOutBytes = 4 * kBufferBytes;
 
 struct GemmParams {
-  CUtensorMap a, b, b_small;
+  CUtensorMap a, b, b_small, out, keep;
   ProductParams p;
   int tiles_n;
   bool a_whole, b_whole;   // an MN-major operand's 128 columns in one copy (4-d map)
@@ -57,55 +63,32 @@ struct Shared {
   uint32_t tmem;
 };
 
-// Eight fp32 values -> 16 bytes of bf16, and back.
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void unpack8(uint4 b, float (&v)[8]) {
-  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
+// A group's way out: four warps fill a buffer (32 rows x 128 columns of bf16, two
+// pieces of 64 columns in the 128-byte swizzle), one thread copies it out while
+// the other buffer is filled.
+struct OutBuffer {
+  uint8_t* base;
+  int barrier;      // named barrier of the group's 128 threads
+  bool leader;
+  uint32_t used;
 
-// Sums come column by column: a lane holds 16 rows of one column.  Eight lanes
-// turn eight of their rows around, after which lane j of them holds the eight
-// columns of row j.
-__device__ __forceinline__ void turn8(float (&v)[8], int lane) {
-#pragma unroll
-  for (int s = 4; s > 0; s >>= 1) {
-    const bool up = (lane & s) != 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if ((i & s) == 0) {
-        const float theirs = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i | s], s);
-        if (up)
-          v[i] = theirs;
-        else
-          v[i | s] = theirs;
-      }
-    }
+  // The next buffer, free for all of the group.
+  __device__ __forceinline__ uint8_t* take() {
+    if (leader) tma_wait_read<1>();
+    named_barrier_sync(barrier, 128);
+    return base + (used++ & 1) * kBufferBytes;
   }
-}
+  // The group's writes to the buffer are done; true in the thread that copies.
+  __device__ __forceinline__ bool filled() {
+    fence_proxy_async_smem();
+    named_barrier_sync(barrier, 128);
+    return leader;
+  }
+};
 
-// The epilogue of 8 columns from `col` on of output row `row` (kGlu aside).
-template <int kForm, int kAct>
-__device__ __forceinline__ void store8(const ProductParams& p, int64_t row, int col, const float (&bias)[8],
-                                       float (&z)[8]) {
-  const int64_t at = row * p.N + col;
-  if (kForm == kLinear) {
-    float r[8] = {};
-    if (p.residual != nullptr) unpack8(ld_v4(p.residual + at), r);   // may be the output itself: a plain load
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += bias[i];
-    if (p.keep != nullptr) st_v4(p.keep + at, pack8(z));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_value<kAct>(z[i]) + r[i];
-  }
-  st_v4(static_cast<__nv_bfloat16*>(p.out) + at, pack8(z));
+// Address of 8 columns (16 bytes) of a row in a buffer: piece number 0-15.
+__device__ __forceinline__ uint32_t out_address(const uint8_t* buffer, int row, int piece) {
+  return smem_addr(buffer) + (piece >> 3) * kPieceBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
 template <int kForm, int kAct>
@@ -113,7 +96,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_expert_gemm(const __grid_constant__ GemmParams g) {
   extern __shared__ uint8_t raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  Shared& sh = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
+  uint8_t* out_buffers = stages + kStages * kStageBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(out_buffers + kOutBytes);
   constexpr bool kAMn = kForm == kDw || kForm == kDx, kBMn = kForm == kDw;
   constexpr int kCols = kForm == kGlu ? kHalf : 256;   // output columns of a tile
 
@@ -304,73 +288,152 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3, side = (warp - 4) >> 2;   // 32 lanes of the tensor memory; which 16 of 32 rows
-    // the 8 columns of this lane's group; kGlu: 8 lanes of gate, 8 of up sums, of the same columns
-    const int h = (lane >> 3) & 1, j = lane & 7;
-    const int in_cta = kForm == kGlu ? q * 16 + (lane >> 4) * 8 : q * 32 + (lane & ~7);
+    const int q = warp & 3, side = (warp - 4) >> 2;   // 32 lanes of the tensor memory; even or odd chunks of rows
+    OutBuffer buffers = {out_buffers + side * 2 * kBufferBytes, 1 + side, q == 0 && lane == 0, 0};
+    const int mrow = lane & 7, mat = lane >> 3;   // this lane's address in the four 8 x 8 matrices of a store
+    // columns of this thread's sums: 16 hh + lane / 4 (+ 8); kGlu: gate and up of column 8 hh + lane / 4
     uint32_t n = 0;
     while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       const uint32_t half = n & 1;
       if (blocks > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.sums_full[half], (n >> 1) & 1,
-                                                       kWaitNs + (uint64_t)blocks * 2000));
+        // a group's threads wait for one another below, so they give up together
+        ok = named_barrier_and(1 + side, 128, mbar_wait_cluster(&sh.sums_full[half], (n >> 1) & 1,
+                                                                kWaitNs + (uint64_t)blocks * 2000));
         if (!ok) break;
         tmem_fence_after();
         ++n;
       }
       const uint32_t d = tmem + half * kTileN + ((uint32_t)(q * 32) << 16);
-      const int col = t.n0 + (int)rank * (kCols / 2) + in_cta;
-      const bool in = col < p.N;
+      const int col0 = t.n0 + (int)rank * (kCols / 2);   // first output column of this CTA
       const int64_t row0 = kForm == kDw ? (int64_t)t.e * p.K + t.m0 : (int64_t)t.start + t.m0;
-      float bias[8] = {};
-      if (kForm == kLinear && p.bias != nullptr && in)
-        unpack8(__ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)t.e * p.N + col)), bias);
+      const int y0 = kForm == kDw ? t.m0 : t.start + t.m0, z0 = kForm == kDw ? t.e : 0;
+      float bias[4] = {};
+      if (kForm == kLinear && p.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = col0 + q * 32 + i * 8 + (lane >> 2);
+          if (col < p.N) bias[i] = __bfloat162float(p.bias[(int64_t)t.e * p.N + col]);
+        }
+      }
+      auto sums_read = [&]() {   // the next tile's products may have this half
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
+      };
+      if (blocks > 0 && side * kChunk >= t.rows) sums_read();
 #pragma unroll 1
-      for (int r0 = 0; r0 < t.rows; r0 += 32) {
-        float v[16];
+      for (int r0 = side * kChunk; r0 < t.rows; r0 += 2 * kChunk) {
+        const int rows = min(kChunk, t.rows - r0);
+        float v[2][16];
         if (blocks > 0) {
-          tmem_ld16(d + r0 + side * 16, v);
+          tmem_ld_16x32(d + r0, v[0]);
+          tmem_ld_16x32(d + (16u << 16) + r0, v[1]);
           tmem_wait_ld();
-          if (r0 + 32 >= t.rows) {   // the sums are read: the next tile's products may have this half
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
-          }
+          if (r0 + 2 * kChunk >= t.rows) sums_read();
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+          for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.0f;
         }
-        float lo[8], hi[8];   // rows j and j + 8 of the 16
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          lo[i] = v[i];
-          hi[i] = v[8 + i];
-        }
-        turn8(lo, lane);
-        turn8(hi, lane);
-        const int r = r0 + side * 16 + j;
+        // a filled buffer's pieces of 64 columns, at column x of `dst` (kept gate and up: both at x)
+        auto copy_out = [&](const uint8_t* buf, const CUtensorMap* map, __nv_bfloat16* dst, int pieces, bool gate_up) {
+          const bool copies = buffers.filled();
+          if (rows == kChunk) {
+            if (copies) {
+              for (int i = 0; i < pieces; ++i) {
+                const int col = col0 + (gate_up ? 0 : i * 64);
+                if (col < p.N)
+                  tma_store_3d(map, smem_addr(buf) + i * kPieceBytes, col, gate_up ? i : y0 + r0, gate_up ? y0 + r0 : z0);
+              }
+            }
+          } else {   // the segment ends inside the chunk
+            for (int i = q * 32 + lane; i < rows * pieces * 8; i += 128) {
+              const int r = i / (pieces * 8), c = i % (pieces * 8);
+              const int col = col0 + (gate_up ? (c & 7) * 8 : c * 8);
+              const int64_t row = gate_up ? (row0 + r0 + r) * 2 + (c >> 3) : row0 + r0 + r;
+              if (col < p.N) st_v4(dst + row * p.N + col, ld_shared_v4_at(out_address(buf, r, c)));
+            }
+          }
+          if (copies) tma_commit();   // one group a buffer, empty or not: take() counts them
+        };
         if (kForm == kGlu) {
-          if (p.keep != nullptr && in) {
-            __nv_bfloat16* keep = p.keep + ((row0 + r) * 2 + h) * p.N + col;
-            if (r < t.rows) st_v4(keep, pack8(lo));
-            if (r + 8 < t.rows) st_v4(keep + (int64_t)16 * p.N, pack8(hi));
-          }
-          // gate lanes take row j, up lanes row j + 8
+          if (p.keep != nullptr) {
+            uint8_t* buf = buffers.take();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float theirs = __shfl_xor_sync(0xffffffffu, h ? lo[i] : hi[i], 8);
-            lo[i] = act_value<kAct>(h ? theirs : lo[i]) * (h ? hi[i] : theirs);
+            for (int i = 0; i < 4; ++i)   // gate of both column groups, then up
+              stmatrix4_trans(out_address(buf, 8 * i + mrow, (mat >> 1) * 8 + q * 2 + (mat & 1)),
+                              pack_bf16x2(v[0][4 * i], v[0][4 * i + 1]), pack_bf16x2(v[1][4 * i], v[1][4 * i + 1]),
+                              pack_bf16x2(v[0][4 * i + 2], v[0][4 * i + 3]), pack_bf16x2(v[1][4 * i + 2], v[1][4 * i + 3]));
+            copy_out(buf, &g.keep, p.keep, 2, true);
           }
-          if (in && r + 8 * h < t.rows)
-            st_v4(static_cast<__nv_bfloat16*>(p.out) + (row0 + r + 8 * h) * p.N + col, pack8(lo));
-        } else if (in) {
-          if (r < t.rows) store8<kForm, kAct>(p, row0 + r, col, bias, lo);
-          if (r + 8 < t.rows) store8<kForm, kAct>(p, row0 + r + 8, col, bias, hi);
+          uint32_t w[2][4];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[hh][i] = pack_bf16x2(act_value<kAct>(v[hh][4 * i]) * v[hh][4 * i + 2],
+                                     act_value<kAct>(v[hh][4 * i + 1]) * v[hh][4 * i + 3]);
+          uint8_t* buf = buffers.take();
+#pragma unroll
+          for (int i = 0; i < 4; i += 2)   // both column groups of 8 rows, then of the next 8
+            stmatrix4_trans(out_address(buf, 8 * i + 8 * (mat >> 1) + mrow, q * 2 + (mat & 1)), w[0][i], w[1][i],
+                            w[0][i + 1], w[1][i + 1]);
+          copy_out(buf, &g.out, static_cast<__nv_bfloat16*>(p.out), 1, false);
+        } else {
+          const int piece = q * 4 + mat;   // 8 columns a matrix
+          uint8_t* buf;
+          if (kForm == kLinear) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[hh][i] += bias[2 * hh + ((i >> 1) & 1)];
+            if (p.keep != nullptr) {
+              buf = buffers.take();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                stmatrix4_trans(out_address(buf, 8 * i + mrow, piece), pack_bf16x2(v[0][4 * i], v[0][4 * i + 1]),
+                                pack_bf16x2(v[0][4 * i + 2], v[0][4 * i + 3]), pack_bf16x2(v[1][4 * i], v[1][4 * i + 1]),
+                                pack_bf16x2(v[1][4 * i + 2], v[1][4 * i + 3]));
+              copy_out(buf, &g.keep, p.keep, 2, false);
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[hh][i] = act_value<kAct>(v[hh][i]);
+          }
+          buf = buffers.take();
+          if (kForm == kLinear && p.residual != nullptr) {
+            // this warp's 32 rows x 32 columns through its own part of the buffer
+#pragma unroll
+            for (int i = lane; i < kChunk * 4; i += 32) {
+              const int r = i >> 2, c = q * 4 + (i & 3);
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (r < rows && col0 + c * 8 < p.N) x = ld_v4(p.residual + (row0 + r0 + r) * p.N + col0 + c * 8);
+              st_shared_v4_at(out_address(buf, r, c), x);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x[4];
+              ldmatrix4_trans(out_address(buf, 8 * i + mrow, piece), x);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                v[m >> 1][4 * i + 2 * (m & 1)] += bf16_lo(x[m]);
+                v[m >> 1][4 * i + 2 * (m & 1) + 1] += bf16_hi(x[m]);
+              }
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            stmatrix4_trans(out_address(buf, 8 * i + mrow, piece), pack_bf16x2(v[0][4 * i], v[0][4 * i + 1]),
+                            pack_bf16x2(v[0][4 * i + 2], v[0][4 * i + 3]), pack_bf16x2(v[1][4 * i], v[1][4 * i + 1]),
+                            pack_bf16x2(v[1][4 * i + 2], v[1][4 * i + 3]));
+          copy_out(buf, &g.out, static_cast<__nv_bfloat16*>(p.out), 2, false);
         }
-        __syncwarp();
       }
     }
+    if (buffers.leader) tma_wait_all();
   }
   if (!ok) set_status(p.seg.status, EP_ERR_TIMEOUT);
   __syncwarp();
@@ -382,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
 template <int kForm, int kAct>
 static int launch_gemm_t(const GemmParams& g, int64_t tiles, cudaStream_t stream) {
-  const int smem = kStages * kStageBytes + (int)sizeof(Shared) + 1024;
+  const int smem = kStages * kStageBytes + kOutBytes + (int)sizeof(Shared) + 1024;
   const void* fn = reinterpret_cast<const void*>(k_expert_gemm<kForm, kAct>);
   if (ep_host::ensure_max_smem(fn, smem) != EP_OK) return EP_ERR_CUDA;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, ep_host::grid_cap(1) / 2));
@@ -443,6 +506,22 @@ int launch_gemm_bf16(Form form, const ProductParams& p, int act, cudaStream_t st
     }
     map(&g.b, p.a, K, rows, 1, kTileK, kHalf);
     map(&g.b_small, p.a, K, rows, 1, kTileK, kBox);
+  }
+  auto map_out = [&](CUtensorMap* m, const void* base, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
+    const uint64_t dims[3] = {N, d1, d2}, strides[2] = {N * 2, N * d1 * 2};
+    const uint32_t box[3] = {64, b1, b2};
+    if (rc == EP_OK) rc = ep_host::make_map(m, false, 3, base, dims, strides, box);
+  };
+  if (form == kDw)
+    map_out(&g.out, p.out, K, E, kChunk, 1);
+  else
+    map_out(&g.out, p.out, rows, 1, kChunk, 1);
+  g.keep = g.out;
+  if (p.keep != nullptr) {
+    if (form == kGlu)
+      map_out(&g.keep, p.keep, 2, rows, 1, kChunk);
+    else
+      map_out(&g.keep, p.keep, rows, 1, kChunk, 1);
   }
   if (rc != EP_OK) return rc;
   const int cols = form == kGlu ? kHalf : kTileN;

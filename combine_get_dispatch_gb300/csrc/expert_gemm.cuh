@@ -34,7 +34,7 @@ struct Tile {
 constexpr int kGroupM = 16;   // row tiles taken together
 
 // Walks the list of all experts' tiles; one warp, converged.  An expert has
-// ceil(rows / tile_rows) row tiles, its rows spread over them in units of 16, and
+// ceil(rows / tile_rows) row tiles, its rows spread over them in units of 32, and
 // tiles_n column tiles of `cols`; 16 row tiles are taken together, column after
 // column.  Looks at 32 experts at a time, so that nothing has to be kept for
 // all of them.
@@ -96,10 +96,10 @@ struct TileWalk {
     const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
     const int64_t r = in - group * kGroupM * tiles_n;
     const int i = (int)group * kGroupM + (int)(r % gm);
-    const int64_t units = (of + 15) / 16;
+    const int64_t units = (of + 31) / 32;
     out.n0 = (int)(r / gm) * cols;
-    out.m0 = (int)(units * i / tiles_m) * 16;
-    out.rows = min(of, (int)(units * (i + 1) / tiles_m) * 16) - out.m0;
+    out.m0 = (int)(units * i / tiles_m) * 32;
+    out.rows = min(of, (int)(units * (i + 1) / tiles_m) * 32) - out.m0;
     return out;
   }
 };

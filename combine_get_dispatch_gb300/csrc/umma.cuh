@@ -97,6 +97,29 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// Tile of a 3-d tensor from this CTA's shared memory, in the calling thread's
+// current bulk group; what lies outside the tensor is not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m), "r"(src),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed: lane l holds elements
+// (l / 4, 2 (l % 4)) and the next of each; lane 8 m + j gives the address of
+// column j of matrix m.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- tensor memory
 
 template <int kGroup>
@@ -137,11 +160,13 @@ __device__ __forceinline__ void tmem_st4(uint32_t addr, uint32_t a, uint32_t b, 
                : "memory");
 }
 
-// 16 consecutive columns of this thread's lane (one warp, converged).
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+// 16 lanes x 32 columns (one warp, converged): v[4 i], v[4 i + 1] are columns
+// 8 i + 2 (l % 4) and the next of lane l / 4, v[4 i + 2], v[4 i + 3] the same
+// columns of lane l / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t addr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
