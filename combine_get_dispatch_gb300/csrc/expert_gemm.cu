@@ -36,7 +36,7 @@
 namespace ep {
 
 constexpr int kGemmThreads = 384;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kTileM = 256, kTileN = 256, kHalf = 128;   // columns, rows of the output; a CTA's columns
 constexpr int kTileK = 64;                       // bf16 elements of one 128-byte row
 constexpr int kOperandBytes = kHalf * kTileK * 2;   // 16 KB: one CTA's part of an operand
@@ -45,8 +45,9 @@ constexpr int kBox = 32;                         // rows of a small copy
 constexpr int kEpilogueWarps = 8;                // two groups of four
 constexpr int kChunk = 32;                       // rows a group takes at a time
 constexpr int kPieceBytes = kChunk * 128;        // 32 rows of 64 columns
-constexpr int kBufferBytes = 2 * kPieceBytes;    // two buffers a group
-constexpr int kOutBytes = 4 * kBufferBytes;
+constexpr int kBufferBytes = 2 * kPieceBytes;
+constexpr int kBuffers = 4;                      // of a group
+constexpr int kOutBytes = 2 * kBuffers * kBufferBytes;
 
 struct GemmParams {
   CUtensorMap a, b, b_small, out, keep;
@@ -65,7 +66,7 @@ struct Shared {
 
 // A group's way out: four warps fill a buffer (32 rows x 128 columns of bf16, two
 // pieces of 64 columns in the 128-byte swizzle), one thread copies it out while
-// the other buffer is filled.
+// the next ones are filled.
 struct OutBuffer {
   uint8_t* base;
   int barrier;      // named barrier of the group's 128 threads
@@ -74,9 +75,9 @@ struct OutBuffer {
 
   // The next buffer, free for all of the group.
   __device__ __forceinline__ uint8_t* take() {
-    if (leader) tma_wait_read<1>();
+    if (leader) tma_wait_read<kBuffers - 1>();
     named_barrier_sync(barrier, 128);
-    return base + (used++ & 1) * kBufferBytes;
+    return base + (used++ % kBuffers) * kBufferBytes;
   }
   // The group's writes to the buffer are done; true in the thread that copies.
   __device__ __forceinline__ bool filled() {
@@ -221,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (blocks == 0) continue;
       const uint32_t idesc = umma_idesc_bf16(kTileM, (t.rows + 15) / 16 * 16, kAMn, kBMn);
       const uint32_t half = n & 1, d = tmem + half * kTileN;
-      ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.sums_empty[half], ((n >> 1) & 1) ^ 1));
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_empty[half], ((n >> 1) & 1) ^ 1));
       if (!ok) break;
       tmem_fence_after();
       int kb = 0;
@@ -289,7 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, side = (warp - 4) >> 2;   // 32 lanes of the tensor memory; even or odd chunks of rows
-    OutBuffer buffers = {out_buffers + side * 2 * kBufferBytes, 1 + side, q == 0 && lane == 0, 0};
+    OutBuffer buffers = {out_buffers + side * kBuffers * kBufferBytes, 1 + side, q == 0 && lane == 0, 0};
     const int mrow = lane & 7, mat = lane >> 3;   // this lane's address in the four 8 x 8 matrices of a store
     // columns of this thread's sums: 16 hh + lane / 4 (+ 8); kGlu: gate and up of column 8 hh + lane / 4
     uint32_t n = 0;
@@ -298,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const uint32_t half = n & 1;
       if (blocks > 0) {
         // a group's threads wait for one another below, so they give up together
-        ok = named_barrier_and(1 + side, 128, mbar_wait_cluster(&sh.sums_full[half], (n >> 1) & 1,
+        ok = named_barrier_and(1 + side, 128, mbar_wait_bounded(&sh.sums_full[half], (n >> 1) & 1,
                                                                 kWaitNs + (uint64_t)blocks * 2000));
         if (!ok) break;
         tmem_fence_after();
@@ -319,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       auto sums_read = [&]() {   // the next tile's products may have this half
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
+        if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
       };
       if (blocks > 0 && side * kChunk >= t.rows) sums_read();
 #pragma unroll 1

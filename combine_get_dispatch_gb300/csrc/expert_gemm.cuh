@@ -87,19 +87,22 @@ struct TileWalk {
     }
     const int who = __ffs(__ballot_sync(0xffffffffu, t < before + (int64_t)upto * tiles_n)) - 1;
     const int tiles_m = __shfl_sync(0xffffffffu, (rows + tile_rows - 1) / tile_rows, who);
-    const int64_t in = t - before - (int64_t)(__shfl_sync(0xffffffffu, upto, who) - tiles_m) * tiles_n;
+    // 32-bit divisions: the tiles of one expert's output are far below 2^31 (each is 64 KB or more of it)
+    const uint32_t in = (uint32_t)(t - before - (int64_t)(__shfl_sync(0xffffffffu, upto, who) - tiles_m) * tiles_n);
     const int of = __shfl_sync(0xffffffffu, rows, who);
     out.e = e0 + who;
     out.start = __shfl_sync(0xffffffffu, (int)s.start, who);
     out.count = __shfl_sync(0xffffffffu, s.count, who);
-    const int64_t group = in / ((int64_t)kGroupM * tiles_n);
-    const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
-    const int64_t r = in - group * kGroupM * tiles_n;
-    const int i = (int)group * kGroupM + (int)(r % gm);
-    const int64_t units = (of + 31) / 32;
-    out.n0 = (int)(r / gm) * cols;
-    out.m0 = (int)(units * i / tiles_m) * 32;
-    out.rows = min(of, (int)(units * (i + 1) / tiles_m) * 32) - out.m0;
+    const uint32_t group = in / (uint32_t)(kGroupM * tiles_n);
+    const uint32_t r = in - group * (uint32_t)(kGroupM * tiles_n);
+    const uint32_t gm = (uint32_t)min(kGroupM, tiles_m - (int)group * kGroupM);
+    const uint32_t column = r / gm;
+    const int i = (int)(group * kGroupM + r - column * gm);
+    const int units = (int)((uint32_t)(of + 31) / 32u);
+    const int each = (int)((uint32_t)units / (uint32_t)tiles_m), more = units - each * tiles_m;
+    out.n0 = (int)column * cols;
+    out.m0 = (i * each + min(i, more)) * 32;
+    out.rows = min(of, out.m0 + (each + (i < more ? 1 : 0)) * 32) - out.m0;
     return out;
   }
 };
