@@ -46,7 +46,7 @@ constexpr int kEpilogueWarps = 8;                // two groups of four
 constexpr int kChunk = 32;                       // rows a group takes at a time
 constexpr int kPieceBytes = kChunk * 128;        // 32 rows of 64 columns
 constexpr int kBufferBytes = 2 * kPieceBytes;
-constexpr int kBuffers = 4;                      // of a group
+constexpr int kBuffers = 4;                      // of a group, one a warp
 constexpr int kOutBytes = 2 * kBuffers * kBufferBytes;
 
 struct GemmParams {
@@ -65,25 +65,23 @@ struct Shared {
 };
 
 // A group's way out: four warps fill a buffer (32 rows x 128 columns of bf16, two
-// pieces of 64 columns in the 128-byte swizzle), one thread copies it out while
-// the next ones are filled.
-struct OutBuffer {
+// pieces of 64 columns in the 128-byte swizzle), lane 0 of the buffer's own warp
+// copies it out while the next ones are filled.  One barrier a buffer: before it,
+// the next buffer's warp has seen that buffer's last copy read.
+struct OutBuffers {
   uint8_t* base;
-  int barrier;      // named barrier of the group's 128 threads
-  bool leader;
+  int barrier;       // named barrier of the group's 128 threads
+  int q, lane;
   uint32_t used;
 
-  // The next buffer, free for all of the group.
-  __device__ __forceinline__ uint8_t* take() {
-    if (leader) tma_wait_read<kBuffers - 1>();
-    named_barrier_sync(barrier, 128);
-    return base + (used++ % kBuffers) * kBufferBytes;
-  }
-  // The group's writes to the buffer are done; true in the thread that copies.
+  __device__ __forceinline__ uint8_t* next() { return base + (used % kBuffers) * kBufferBytes; }
+  // The group's writes to next() are done; true in the thread that copies.
   __device__ __forceinline__ bool filled() {
+    const int mine = used++ % kBuffers;
     fence_proxy_async_smem();
+    if (lane == 0 && q == (int)(used % kBuffers)) tma_wait_read<0>();
     named_barrier_sync(barrier, 128);
-    return leader;
+    return lane == 0 && q == mine;
   }
 };
 
@@ -290,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, side = (warp - 4) >> 2;   // 32 lanes of the tensor memory; even or odd chunks of rows
-    OutBuffer buffers = {out_buffers + side * kBuffers * kBufferBytes, 1 + side, q == 0 && lane == 0, 0};
+    OutBuffers buffers = {out_buffers + side * kBuffers * kBufferBytes, 1 + side, q, lane, 0};
     const int mrow = lane & 7, mat = lane >> 3;   // this lane's address in the four 8 x 8 matrices of a store
     // columns of this thread's sums: 16 hh + lane / 4 (+ 8); kGlu: gate and up of column 8 hh + lane / 4
     uint32_t n = 0;
@@ -355,11 +353,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
               if (col < p.N) st_v4(dst + row * p.N + col, ld_shared_v4_at(out_address(buf, r, c)));
             }
           }
-          if (copies) tma_commit();   // one group a buffer, empty or not: take() counts them
+          if (copies) tma_commit();
         };
         if (kForm == kGlu) {
           if (p.keep != nullptr) {
-            uint8_t* buf = buffers.take();
+            uint8_t* buf = buffers.next();
 #pragma unroll
             for (int i = 0; i < 4; ++i)   // gate of both column groups, then up
               stmatrix4_trans(out_address(buf, 8 * i + mrow, (mat >> 1) * 8 + q * 2 + (mat & 1)),
@@ -374,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             for (int i = 0; i < 4; ++i)
               w[hh][i] = pack_bf16x2(act_value<kAct>(v[hh][4 * i]) * v[hh][4 * i + 2],
                                      act_value<kAct>(v[hh][4 * i + 1]) * v[hh][4 * i + 3]);
-          uint8_t* buf = buffers.take();
+          uint8_t* buf = buffers.next();
 #pragma unroll
           for (int i = 0; i < 4; i += 2)   // both column groups of 8 rows, then of the next 8
             stmatrix4_trans(out_address(buf, 8 * i + 8 * (mat >> 1) + mrow, q * 2 + (mat & 1)), w[0][i], w[1][i],
@@ -389,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[hh][i] += bias[2 * hh + ((i >> 1) & 1)];
             if (p.keep != nullptr) {
-              buf = buffers.take();
+              buf = buffers.next();
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 stmatrix4_trans(out_address(buf, 8 * i + mrow, piece), pack_bf16x2(v[0][4 * i], v[0][4 * i + 1]),
@@ -402,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[hh][i] = act_value<kAct>(v[hh][i]);
           }
-          buf = buffers.take();
+          buf = buffers.next();
           if (kForm == kLinear && p.residual != nullptr) {
             // this warp's 32 rows x 32 columns through its own part of the buffer
 #pragma unroll
@@ -434,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
       }
     }
-    if (buffers.leader) tma_wait_all();
+    if (lane == 0) tma_wait_all();
   }
   if (!ok) set_status(p.seg.status, EP_ERR_TIMEOUT);
   __syncwarp();
