@@ -332,5 +332,26 @@ int check_launch();   // EP_OK or EP_ERR_CUDA after a launch
 // device (the attribute is per device; it is set again only when a call asks
 // for more than the largest limit set so far for that kernel and device).
 int ensure_max_smem(const void* func, int bytes);
+// Launch as a programmatic dependent of the kernel before it in the stream: the
+// grid may come up while that one drains; the kernel waits (pdl_wait) before it
+// touches global memory.
+template <typename P>
+inline int launch_dependent(void (*kernel)(P), int grid, int threads, int smem, cudaStream_t stream, const P& params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, params) != cudaSuccess) {
+    cudaGetLastError();
+    return EP_ERR_CUDA;
+  }
+  return EP_OK;
+}
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 }  // namespace ep_host

@@ -27,6 +27,7 @@ template <int kAct>
 __global__ void __launch_bounds__(kThreads) k_glu_slope(SlopeParams p) {
   __shared__ Tile next[2];
   const int vec = p.N / 8, lane = threadIdx.x & 31;
+  pdl_wait();
   TileWalk walk;
   if (threadIdx.x < 32) walk.begin(p.seg, -1, kSlopeRows, 1, 0, blockIdx.x == 0, lane);
   for (int64_t at = blockIdx.x, n = 0;; at += gridDim.x, ++n) {
@@ -117,7 +118,8 @@ __global__ void __launch_bounds__(1024) k_linear_slope(SlopeParams p) {
 template <int kAct>
 static int launch_glu_slope(const SlopeParams& p, int64_t rows, cudaStream_t s) {
   const int64_t tiles = rows / kSlopeRows + p.seg.E;
-  k_glu_slope<kAct><<<(int)std::min<int64_t>(tiles, ep_host::grid_cap(8)), kThreads, 0, s>>>(p);
+  const int grid = (int)std::min<int64_t>(tiles, ep_host::grid_cap(8));
+  if (ep_host::launch_dependent(k_glu_slope<kAct>, grid, kThreads, 0, s, p) != EP_OK) return EP_ERR_CUDA;
   ep_host::count_launch();
   return ep_host::check_launch();
 }

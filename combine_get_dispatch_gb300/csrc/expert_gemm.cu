@@ -24,7 +24,7 @@
 // same 8 of Wu (one copy through a 5-d tensor map), which brings both halves of
 // an output into one thread.
 //
-// Roles: warp 0 copies (TMA, 6 stages; 5 to 7 measure the same), warp 1 of the first CTA issues products,
+// Roles: warp 0 copies (TMA, 5 or 6 stages), warp 1 of the first CTA issues products,
 // warp 2 owns the tensor memory and walks the list of tiles, warp 3 clears the
 // rows past a segment's end (kDw, whose inner index is the row), warps 4-11 read
 // the sums back and run the epilogue while the products of the next tile fill the
@@ -36,7 +36,7 @@
 namespace ep {
 
 constexpr int kGemmThreads = 384;
-constexpr int kStages = 5;
+constexpr int kMaxStages = 6;
 constexpr int kTileM = 256, kTileN = 256, kHalf = 128;   // columns, rows of the output; a CTA's columns
 constexpr int kTileK = 64;                       // bf16 elements of one 128-byte row
 constexpr int kOperandBytes = kHalf * kTileK * 2;   // 16 KB: one CTA's part of an operand
@@ -46,19 +46,24 @@ constexpr int kEpilogueWarps = 8;                // two groups of four
 constexpr int kChunk = 32;                       // rows a group takes at a time
 constexpr int kPieceBytes = kChunk * 128;        // 32 rows of 64 columns
 constexpr int kBufferBytes = 2 * kPieceBytes;
-constexpr int kBuffers = 4;                      // of a group, one a warp
-constexpr int kOutBytes = 2 * kBuffers * kBufferBytes;
+
+// Stages of copies and output buffers of a group (one a warp) share 224 KB.  kGlu,
+// in calls that the power limit bounds, does better with fewer stages (65536 x
+// 7168 x 4096: 2326 us against 2413), the others with more (4096 x 8192 x 4864:
+// 172 us against 176; zeros, which the power limit leaves alone, 148 against 158).
+__host__ __device__ constexpr int stages_of(int form) { return form == kGlu ? 5 : 6; }
+__host__ __device__ constexpr int buffers_of(int form) { return form == kGlu ? 4 : 2; }
 
 struct GemmParams {
   CUtensorMap a, b, b_small, out, keep;
   ProductParams p;
-  int tiles_n;
+  int tile_rows, tiles_n;
   bool a_whole, b_whole;   // an MN-major operand's 128 columns in one copy (4-d map)
 };
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t landed[kStages], cleared[kStages];   // kDw: the block that a segment ends in
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t landed[kMaxStages], cleared[kMaxStages];   // kDw: the block that a segment ends in
   uint64_t sums_full[2], sums_empty[2];
   TileRing ring;
   uint32_t tmem;
@@ -68,6 +73,7 @@ struct Shared {
 // pieces of 64 columns in the 128-byte swizzle), lane 0 of the buffer's own warp
 // copies it out while the next ones are filled.  One barrier a buffer: before it,
 // the next buffer's warp has seen that buffer's last copy read.
+template <int kBuffers>
 struct OutBuffers {
   uint8_t* base;
   int barrier;       // named barrier of the group's 128 threads
@@ -95,8 +101,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_expert_gemm(const __grid_constant__ GemmParams g) {
   extern __shared__ uint8_t raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  constexpr int kStages = stages_of(kForm), kBuffers = buffers_of(kForm);
   uint8_t* out_buffers = stages + kStages * kStageBytes;
-  Shared& sh = *reinterpret_cast<Shared*>(out_buffers + kOutBytes);
+  Shared& sh = *reinterpret_cast<Shared*>(out_buffers + 2 * kBuffers * kBufferBytes);
   constexpr bool kAMn = kForm == kDw || kForm == kDx, kBMn = kForm == kDw;
   constexpr int kCols = kForm == kGlu ? kHalf : 256;   // output columns of a tile
 
@@ -128,8 +135,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   TileWalk walk;
   if (warp == 2) {
     tmem_alloc<2>(&sh.tmem, 512);
-    walk.begin(p.seg, kForm == kDw ? p.K : -1, kTileN, g.tiles_n, kCols, blockIdx.x == 0, lane);
+    pdl_wait();   // all that follows reads what kernels before this one may have written
+    walk.begin(p.seg, kForm == kDw ? p.K : -1, g.tile_rows, g.tiles_n, kCols, blockIdx.x == 0, lane);
   }
+  pdl_wait();
   tmem_fence_before();
   cluster_sync();
   tmem_fence_after();
@@ -137,7 +146,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   bool ok = true;
   uint32_t taken = 0;
-  Tile t;
+  Tile t = {};
   auto inner_blocks = [&]() { return ((kForm == kDw ? t.count : p.K) + kTileK - 1) / kTileK; };
 
   if (warp == 0 && lane == 0) {
@@ -288,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, side = (warp - 4) >> 2;   // 32 lanes of the tensor memory; even or odd chunks of rows
-    OutBuffers buffers = {out_buffers + side * kBuffers * kBufferBytes, 1 + side, q, lane, 0};
+    OutBuffers<kBuffers> buffers = {out_buffers + side * kBuffers * kBufferBytes, 1 + side, q, lane, 0};
     const int mrow = lane & 7, mat = lane >> 3;   // this lane's address in the four 8 x 8 matrices of a store
     // columns of this thread's sums: 16 hh + lane / 4 (+ 8); kGlu: gate and up of column 8 hh + lane / 4
     uint32_t n = 0;
@@ -444,11 +453,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
 template <int kForm, int kAct>
 static int launch_gemm_t(const GemmParams& g, int64_t tiles, cudaStream_t stream) {
-  const int smem = kStages * kStageBytes + kOutBytes + (int)sizeof(Shared) + 1024;
+  const int smem = stages_of(kForm) * kStageBytes + 2 * buffers_of(kForm) * kBufferBytes + (int)sizeof(Shared) + 1024;
   const void* fn = reinterpret_cast<const void*>(k_expert_gemm<kForm, kAct>);
   if (ep_host::ensure_max_smem(fn, smem) != EP_OK) return EP_ERR_CUDA;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, ep_host::grid_cap(1) / 2));
-  k_expert_gemm<kForm, kAct><<<(int)pairs * 2, kGemmThreads, smem, stream>>>(g);
+  if (ep_host::launch_dependent(k_expert_gemm<kForm, kAct>, (int)pairs * 2, kGemmThreads, smem, stream, g) != EP_OK)
+    return EP_ERR_CUDA;
   ep_host::count_launch();
   return ep_host::check_launch();
 }
@@ -525,10 +535,18 @@ int launch_gemm_bf16(Form form, const ProductParams& p, int act, cudaStream_t st
   if (rc != EP_OK) return rc;
   const int cols = form == kGlu ? kHalf : kTileN;
   g.tiles_n = (p.N + cols - 1) / cols;
-  // at most one ragged row tile an expert
-  const int64_t tiles_m = form == kDw ? (int64_t)p.seg.E * ((p.K + kTileN - 1) / kTileN) : p.rows / kTileN + p.seg.E;
-  if (tiles_m >= (int64_t)1 << 31) return EP_ERR_INVALID_ARG;
-  const int64_t tiles = tiles_m * g.tiles_n;
+  // Row tiles: whole ones and at most one ragged one an expert.  Where that leaves pairs without a tile they
+  // are made smaller (777 x 2048 x 1000, dx: 21.7 us with 16 tiles of 256 rows).
+  auto tiles_of = [&](int64_t tile) {
+    const int64_t each = (p.K + tile - 1) / tile;
+    const int64_t m = form == kDw ? p.seg.E * each : p.seg.E == 1 ? (p.rows + tile - 1) / tile : p.rows / tile + p.seg.E;
+    return m * g.tiles_n;
+  };
+  const int64_t pairs = std::max(1, ep_host::grid_cap(1) / 2);
+  g.tile_rows = kTileN;
+  while (g.tile_rows > 32 && tiles_of(g.tile_rows / 2) <= pairs) g.tile_rows /= 2;
+  const int64_t tiles = tiles_of(g.tile_rows);
+  if (tiles / g.tiles_n >= (int64_t)1 << 31) return EP_ERR_INVALID_ARG;
   switch (form) {
     case kGlu: return launch_gemm_act<kGlu>(g, tiles, act, stream);
     case kLinear:

@@ -120,8 +120,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
   TileWalk walk;
   if (warp == 2) {
     tmem_alloc<1>(&sh.tmem, 512);
+    pdl_wait();   // all that follows reads what kernels before this one may have written
     walk.begin(p.seg, -1, kMxTileM, g.tiles_n, kCols, blockIdx.x == 0, lane);
   }
+  pdl_wait();
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
 
   bool ok = true;
   uint32_t taken = 0;
-  Tile t;
+  Tile t = {};
   if (warp == 0 && lane == 0) {
     int s = 0;
     uint32_t phase = 0;
@@ -327,7 +329,8 @@ static int launch_mx_t(const MxParams& g, int64_t tiles, cudaStream_t stream) {
   const void* fn = reinterpret_cast<const void*>(k_expert_gemm_e4m3<kForm, kAct>);
   if (ep_host::ensure_max_smem(fn, smem) != EP_OK) return EP_ERR_CUDA;
   const int grid = (int)std::min<int64_t>(tiles, ep_host::grid_cap(1));
-  k_expert_gemm_e4m3<kForm, kAct><<<grid, kMxThreads, smem, stream>>>(g);
+  if (ep_host::launch_dependent(k_expert_gemm_e4m3<kForm, kAct>, grid, kMxThreads, smem, stream, g) != EP_OK)
+    return EP_ERR_CUDA;
   ep_host::count_launch();
   return ep_host::check_launch();
 }
