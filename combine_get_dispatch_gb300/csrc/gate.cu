@@ -8,14 +8,15 @@
 //   gradient      SOFTMAX: dl_e = [e chosen] w_e g_e - p_e sum_j w_j g_j
 //                 TOPK:    dl_e = [e chosen] w_e (g_e - sum_j w_j g_j)
 //
-// One warp per token.  NaN becomes -inf on the way in; -inf is never chosen.
+// Issue slots bound the choice, memory nearly bounds the gradient.  NaN becomes
+// -inf on the way in; -inf is never chosen.
 
 #include "ep_common.cuh"
 
 namespace ep {
 
-constexpr int kGateThreads = 256;
-constexpr int kGateCtas = 6;   // CTAs an SM holds
+constexpr int kForwardThreads = 256, kBackwardThreads = 128;
+constexpr int kForwardCtas = 6, kBackwardCtas = 8;   // of an SM
 
 struct GateParams {
   const void* logits;
@@ -26,7 +27,7 @@ struct GateParams {
   float* w;
   void* grad_logits;
   int32_t* status;
-  bool vec;   // rows start on 16 bytes, a lane's experts are all there or all not
+  bool vec;   // rows are whole 16-byte pieces (forward: and a lane's logits all inside or all past the row)
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -46,10 +47,15 @@ __device__ __forceinline__ float warp_min(float v) {
 }
 
 constexpr float kNone = -INFINITY;   // an expert that is never chosen
+constexpr float kLowest = -3.40282346638528859812e+38f;
 
 // exp(l - m): the difference rounds once and its product with log2(e) once, so
-// it is off by |l - m| 2^-23 of itself.  m is finite.
-__device__ __forceinline__ float gate_exp(float l, float m) { return __expf(l - m); }
+// it is off by |l - m| 2^-23 of itself; below 2^-126 it is 0.  m is finite.
+__device__ __forceinline__ float gate_exp(float l, float m) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((l - m) * 1.44269504f));
+  return r;
+}
 
 // A logit as the kernels see it: NaN is an expert that is never chosen.
 __device__ __forceinline__ float gate_clean(float l) { return fmaxf(l, kNone); }
@@ -106,6 +112,8 @@ __device__ __forceinline__ float gate_base(float most) { return most == kNone ? 
 // As gate_exp in a row whose largest logit is +inf.
 __device__ __forceinline__ float gate_share(float l) { return l == INFINITY ? 1.0f : 0.0f; }
 
+__device__ __forceinline__ float gate_weight(float l, float m) { return m < INFINITY ? gate_exp(l, m) : gate_share(l); }
+
 // The k largest of the warp's logits, one round a choice: the largest, the
 // lowest lane that holds it, that lane's lowest expert.  Lane j of the result
 // holds choice j (-inf: none).
@@ -136,15 +144,44 @@ __device__ __forceinline__ void gate_choose(float (&l)[kV], int k, int lane, flo
   }
 }
 
-// A round of choosing costs a warp about as many instructions as it holds
-// logits, so most logits are thrown out first: 8 groups (16 for k > 8) of lanes
-// have a largest logit each, the least of those is at most the k-th largest
-// logit, and only logits at or above it can be chosen (some 15 of 256).  They
-// are packed, in expert order, one to a lane, and a choice is then one reduction
-// and one ballot.  Rows where more than 32 remain take the plain rounds.
+// A lower bound of a row's 8th largest logit, from the lanes' largest: eight
+// disjoint groups of four lanes have a largest logit each, and the least of those
+// is no larger; the better of two such groupings.
+__device__ __forceinline__ float gate_bound8(float best) {
+  float near = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1)), far = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 16));
+  near = fmaxf(near, __shfl_xor_sync(0xffffffffu, near, 2));
+  far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, 8));
+  return fmaxf(warp_min(near), warp_min(far));
+}
+
+// The same of the k-th largest: the k-th of the 32 lanes' largest, sorted across
+// the warp.  Dearer and closer; with groups as above, rows of 512 experts mostly
+// kept more than 32 candidates for k = 16 (178 us for 65536 of them).
+__device__ __forceinline__ float gate_bound(float best, int k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= kWarp; size <<= 1) {
+#pragma unroll
+    for (int o = size / 2; o > 0; o >>= 1) {
+      const float theirs = __shfl_xor_sync(0xffffffffu, best, o);
+      const bool larger = ((lane & o) == 0) == ((lane & size) == 0);   // falling order within lower halves
+      best = larger ? fmaxf(best, theirs) : fminf(best, theirs);
+    }
+  }
+  return __shfl_sync(0xffffffffu, best, k - 1);
+}
+
+// One warp per token.  A round of choosing costs a warp about as many instructions
+// as it holds logits, so most logits are thrown out first: only those at or above
+// a bound of the k-th largest can be chosen (some 15 of 256).  They are packed, in
+// expert order, one to a lane, and a choice is then one reduction and one ballot.
+// Rows where more than 32 remain take the plain rounds.  Issue
+// slots bound it: about 420 instructions a token of 256 experts, 63.5 us for 131072
+// tokens (21.7 us to read and write them).  As slow or slower: places counted
+// against the packed list (68 us); 8 lanes a token with 32 logits each (99 us: as
+// many instructions a token, and registers for half the warps).
 template <int kV, bool kBf16, bool kTopk>
-__global__ void __launch_bounds__(kGateThreads, kV <= 8 ? kGateCtas : 1) k_gate(GateParams p) {
-  __shared__ uint2 packed[kGateThreads / kWarp][2 * kWarp];   // the upper half takes what is not packed
+__global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k_gate(GateParams p) {
+  __shared__ uint2 packed[kForwardThreads / kWarp][2 * kWarp];   // the upper half takes what is not packed
   const int lane = threadIdx.x & 31;
   uint2* mine = packed[threadIdx.x >> 5];
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -156,13 +193,8 @@ __global__ void __launch_bounds__(kGateThreads, kV <= 8 ? kGateCtas : 1) k_gate(
 #pragma unroll
     for (int i = 1; i < kV; ++i) best = fmaxf(best, l[i]);
     const float m = gate_base(warp_max(best));
-    float near = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1)), far = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 16));
-    if (p.k <= 8) {
-      near = fmaxf(near, __shfl_xor_sync(0xffffffffu, near, 2));
-      far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, 8));
-    }
     // at least the type's lowest value, so that -inf is no candidate
-    const float least = fmaxf(-3.40282346638528859812e+38f, fmaxf(warp_min(near), warp_min(far)));
+    const float least = fmaxf(kLowest, p.k <= 8 ? gate_bound8(best) : gate_bound(best, p.k, lane));
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kV; ++i) n += l[i] >= least ? 1 : 0;
@@ -215,7 +247,7 @@ __global__ void __launch_bounds__(kGateThreads, kV <= 8 ? kGateCtas : 1) k_gate(
       found = __popc(__ballot_sync(0xffffffffu, my_idx >= 0));
       slot = my_idx >= 0 ? lane : p.k;
     }
-    const float ex = m < INFINITY ? gate_exp(my_l, m) : gate_share(my_l);
+    const float ex = gate_weight(my_l, m);
     if (kTopk) total = warp_sum(ex);
     if (slot < p.k) {
       p.idx[t * p.k + slot] = my_idx;
@@ -228,117 +260,202 @@ __global__ void __launch_bounds__(kGateThreads, kV <= 8 ? kGateCtas : 1) k_gate(
   }
 }
 
-// The row of the gradient is laid out in shared memory (-p inner of the lane's
-// own experts, or zeros), the k chosen experts add their own term to it in slot
-// order, and the row is stored as it was read.
-template <int kV, bool kBf16, bool kTopk>
-__global__ void __launch_bounds__(kGateThreads) k_gate_backward(GateParams p) {
-  extern __shared__ float rows[];
-  const int lane = threadIdx.x & 31;
-  float* mine = rows + (threadIdx.x >> 5) * (kV * kWarp);
+// Over the kG lanes of a token; every lane has the result.
+template <int kG, typename Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
+#pragma unroll
+  for (int o = kG / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Sum {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// In the gradient value v of lane g is expert (v / kP * kG + g) * kP + v % kP:
+// 16-byte pieces in turn, so that the lanes of a token read whole lines.
+template <bool kBf16>
+struct Piece {
+  static constexpr int kP = kBf16 ? 8 : 4;
+};
+// A lane's logits of the row at `row`, -inf past its end (or for no row at all).
+// p.vec: rows are whole 16-byte pieces.
+template <int kG, int kV, bool kBf16>
+__device__ __forceinline__ void gate_pieces(const GateParams& p, bool in, const uint8_t* row, int g, float (&l)[kV]) {
+  constexpr int kP = Piece<kBf16>::kP;
+#pragma unroll
+  for (int i = 0; i < kV / kP; ++i) {
+    const int e0 = (i * kG + g) * kP;
+    if (p.vec) {
+      const uint32_t none = kBf16 ? 0xff80ff80u : 0xff800000u;
+      uint4 x = make_uint4(none, none, none, none);
+      if (in && e0 < p.E) x = __ldg(reinterpret_cast<const uint4*>(row + g * 16 + i * kG * 16));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int c = 0; c < kP; ++c)
+        l[i * kP + c] = gate_clean(kBf16 ? ((c & 1) ? bf16_hi(w[c / 2]) : bf16_lo(w[c / 2])) : __uint_as_float(w[c % 4]));
+    } else {
+#pragma unroll
+      for (int c = 0; c < kP; ++c) l[i * kP + c] = in && e0 + c < p.E ? gate_load<kBf16>(row, e0 + c) : kNone;
+    }
+  }
+}
+
+// kG lanes (8, 16 or 32) hold a token's logits, up to 32 each, so that a warp works
+// on several tokens at once (one warp a token: 22 us for 32768 x 256).  Every lane stores the gradient of its own logits (-p inner, or zero); then the
+// lanes of the chosen experts store those whole.
+template <int kG, int kV, bool kBf16, bool kTopk>
+__global__ void __launch_bounds__(kBackwardThreads, kBackwardCtas) k_gate_backward(GateParams p) {
+  constexpr int kTokens = kWarp / kG, kP = Piece<kBf16>::kP;
+  const int lane = threadIdx.x & 31, g = lane % kG, token = lane / kG;
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t t = warp0; t < p.T; t += nwarps) {
-    int my_idx = -1;
-    float g = 0.0f, chosen = kNone;
-    if (lane < p.k) {
-      const int64_t id = p.idx[t * p.k + lane];
+  for (int64_t t0 = warp0 * kTokens; t0 < p.T; t0 += nwarps * kTokens) {
+    const int64_t t = t0 + token;
+    const bool in = t < p.T;
+    int my_idx = -1;   // of slot g (k <= kG)
+    float grad = 0.0f, chosen = kNone;
+    if (in && g < p.k) {
+      const int64_t id = p.idx[t * p.k + g];
       if (id < -1 || id >= p.E)
         set_status(p.status, EP_ERR_INVALID_ARG);
       else
         my_idx = (int)id;
       if (my_idx >= 0) {
-        g = p.grad[t * p.k + lane];
+        grad = p.grad[t * p.k + g];
         chosen = gate_load<kBf16>(p.logits, t * p.E + my_idx);
       }
     }
-    if (chosen == kNone) g = 0.0f;
+    if (chosen == kNone) grad = 0.0f;
     float l[kV];
     float best = chosen;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) l[i] = kNone;
     if (!kTopk) {
-      gate_row<kV, kBf16>(p, t * p.E, lane, l);
+      gate_pieces<kG, kV, kBf16>(p, in, static_cast<const uint8_t*>(p.logits) + t * p.E * (kBf16 ? 2 : 4), g, l);
 #pragma unroll
       for (int i = 0; i < kV; ++i) best = fmaxf(best, l[i]);
     }
-    const float m = gate_base(warp_max(best));
-    const float ex = m < INFINITY ? gate_exp(chosen, m) : gate_share(chosen);
+    const float most = group_reduce<kG>(best, Max());
+    const float m = most == kNone ? 0.0f : most;
+    const float ex = gate_weight(chosen, m);
     float total = ex;
     if (!kTopk) {
       total = 0.0f;
+      if (__all_sync(0xffffffffu, m < INFINITY)) {
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        l[i] = m < INFINITY ? gate_exp(l[i], m) : gate_share(l[i]);
-        total += l[i];
+        for (int i = 0; i < kV; ++i) l[i] = gate_exp(l[i], m);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) l[i] = gate_weight(l[i], m);
       }
+#pragma unroll
+      for (int i = 0; i < kV; ++i) total += l[i];
     }
-    total = warp_sum(total);
+    total = group_reduce<kG>(total, Sum());
     const float inv = total > 0.0f ? 1.0f / total : 0.0f;
     const float w = ex * inv;
-    const float inner = warp_sum(w * g);
-    const float add = kTopk ? w * (g - inner) : w * g;
-    __syncwarp();
+    const float inner = group_reduce<kG>(w * grad, Sum());
+    const float add = kTopk ? w * (grad - inner) : w * grad;
+    const float scale = -inv * inner;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) mine[lane * kV + i] = kTopk ? 0.0f : -l[i] * inv * inner;
-    __syncwarp();
-    for (int j = 0; j < p.k; ++j) {   // in slot order, should a token name an expert twice
-      if (lane == j && my_idx >= 0) mine[my_idx] += add;
-      __syncwarp();
+    for (int i = 0; i < kV / kP; ++i) {
+      const int e0 = (i * kG + g) * kP;
+      float d[kP];
+#pragma unroll
+      for (int c = 0; c < kP; ++c) d[c] = kTopk ? 0.0f : l[i * kP + c] * scale;
+      if (p.vec) {
+        if (in && e0 < p.E) {
+          uint4 x;
+          if (kBf16)
+            x = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[kP - 4], d[kP - 3]),
+                           pack_bf16x2(d[kP - 2], d[kP - 1]));
+          else
+            x = make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]), __float_as_uint(d[3]));
+          st_v4(static_cast<uint8_t*>(p.grad_logits) + (t * p.E + e0) * (kBf16 ? 2 : 4), x);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kP; ++c) {
+          if (in && e0 + c < p.E) {
+            if (kBf16)
+              static_cast<__nv_bfloat16*>(p.grad_logits)[t * p.E + e0 + c] = __float2bfloat16_rn(d[c]);
+            else
+              static_cast<float*>(p.grad_logits)[t * p.E + e0 + c] = d[c];
+          }
+        }
+      }
     }
-    if (p.vec) {
-      const int unit = kBf16 ? 8 : 4;   // 16 bytes
-      for (int e = lane * unit; e < p.E; e += kWarp * unit) {
-        uint4 v;
-        if (kBf16)
-          v = make_uint4(pack_bf16x2(mine[e], mine[e + 1]), pack_bf16x2(mine[e + 2], mine[e + 3]),
-                         pack_bf16x2(mine[e + 4], mine[e + 5]), pack_bf16x2(mine[e + 6], mine[e + 7]));
-        else
-          v = ld_shared_v4(mine + e);
-        st_v4(static_cast<uint8_t*>(p.grad_logits) + (t * p.E + e) * (kBf16 ? 2 : 4), v);
-      }
-    } else {
-      for (int e = lane; e < p.E; e += kWarp) {
-        if (kBf16)
-          static_cast<__nv_bfloat16*>(p.grad_logits)[t * p.E + e] = __float2bfloat16_rn(mine[e]);
-        else
-          static_cast<float*>(p.grad_logits)[t * p.E + e] = mine[e];
-      }
+    // a token that names an expert twice: the terms in slot order, the same sum from every slot
+    float own = kTopk ? 0.0f : ex * scale;
+    for (int j = 0; j < p.k; ++j) {
+      const int ej = __shfl_sync(0xffffffffu, my_idx, j, kG);
+      const float aj = __shfl_sync(0xffffffffu, add, j, kG);
+      if (ej == my_idx) own += aj;
+    }
+    __syncwarp();   // the row's stores come first
+    if (my_idx >= 0) {
+      if (kBf16)
+        static_cast<__nv_bfloat16*>(p.grad_logits)[t * p.E + my_idx] = __float2bfloat16_rn(own);
+      else
+        static_cast<float*>(p.grad_logits)[t * p.E + my_idx] = own;
     }
   }
 }
 
+template <int kG, int kV, bool kBf16, bool kTopk>
+static int launch_backward_t(const GateParams& p, cudaStream_t stream) {
+  constexpr int kTokens = kBackwardThreads / kG;   // of a CTA
+  const int64_t want = (p.T + kTokens - 1) / kTokens;
+  const int grid = (int)std::min<int64_t>(want, (int64_t)ep_host::num_sms() * kBackwardCtas);
+  k_gate_backward<kG, kV, kBf16, kTopk><<<grid, kBackwardThreads, 0, stream>>>(p);
+  ep_host::count_launch();
+  return ep_host::check_launch();
+}
 template <int kV, bool kBf16, bool kTopk>
-static int launch_gate_t(const GateParams& p, bool backward, cudaStream_t stream) {
-  const int64_t warps = kGateThreads / kWarp;
-  const int64_t want = (p.T + warps - 1) / warps;
-  const int grid = (int)std::min<int64_t>(want, (int64_t)ep_host::num_sms() * kGateCtas);
-  if (backward)
-    k_gate_backward<kV, kBf16, kTopk><<<grid, kGateThreads, kV * kGateThreads * sizeof(float), stream>>>(p);
-  else
-    k_gate<kV, kBf16, kTopk><<<grid, kGateThreads, 0, stream>>>(p);
+static int launch_forward_t(const GateParams& p, cudaStream_t stream) {
+  constexpr int kTokens = kForwardThreads / kWarp;
+  const int64_t want = (p.T + kTokens - 1) / kTokens;
+  const int grid = (int)std::min<int64_t>(want, (int64_t)ep_host::num_sms() * kForwardCtas);
+  k_gate<kV, kBf16, kTopk><<<grid, kForwardThreads, 0, stream>>>(p);
   ep_host::count_launch();
   return ep_host::check_launch();
 }
 
+template <int kG, int kV>
+static int launch_backward(const GateParams& p, bool bf16, bool topk, cudaStream_t s) {
+  if (bf16) return topk ? launch_backward_t<kG, kV, true, true>(p, s) : launch_backward_t<kG, kV, true, false>(p, s);
+  return topk ? launch_backward_t<kG, kV, false, true>(p, s) : launch_backward_t<kG, kV, false, false>(p, s);
+}
 template <int kV>
-static int launch_gate_v(const GateParams& p, bool bf16, bool topk, bool backward, cudaStream_t s) {
-  if (bf16)
-    return topk ? launch_gate_t<kV, true, true>(p, backward, s) : launch_gate_t<kV, true, false>(p, backward, s);
-  return topk ? launch_gate_t<kV, false, true>(p, backward, s) : launch_gate_t<kV, false, false>(p, backward, s);
+static int launch_forward(const GateParams& p, bool bf16, bool topk, cudaStream_t s) {
+  if (bf16) return topk ? launch_forward_t<kV, true, true>(p, s) : launch_forward_t<kV, true, false>(p, s);
+  return topk ? launch_forward_t<kV, false, true>(p, s) : launch_forward_t<kV, false, false>(p, s);
 }
 
-static int launch_gate(const GateParams& p, int dtype, int score, bool backward, cudaStream_t s) {
-  if (p.T == 0) return EP_OK;
+static int launch_gate(const GateParams& params, int dtype, int score, bool backward, cudaStream_t s) {
+  if (params.T == 0) return EP_OK;
   const bool bf16 = dtype == EP_DTYPE_BF16, topk = score == EP_GATE_SOFTMAX_TOPK;
-  GateParams q = p;
-  const int kv = p.E <= 64 ? 2 : p.E <= 128 ? 4 : p.E <= 256 ? 8 : p.E <= 512 ? 16 : 32;
-  q.vec = p.E % std::max(kv, 8) == 0 && ep_host::aligned16(p.logits) && ep_host::aligned16(p.grad_logits);
-  if (p.E <= 64) return launch_gate_v<2>(q, bf16, topk, backward, s);
-  if (p.E <= 128) return launch_gate_v<4>(q, bf16, topk, backward, s);
-  if (p.E <= 256) return launch_gate_v<8>(q, bf16, topk, backward, s);
-  if (p.E <= 512) return launch_gate_v<16>(q, bf16, topk, backward, s);
-  return launch_gate_v<32>(q, bf16, topk, backward, s);
+  GateParams p = params;
+  if (!backward) {
+    const int kv = p.E <= 64 ? 2 : p.E <= 128 ? 4 : p.E <= 256 ? 8 : p.E <= 512 ? 16 : 32;
+    p.vec = p.E % std::max(kv, 8) == 0 && ep_host::aligned16(p.logits);
+    if (p.E <= 64) return launch_forward<2>(p, bf16, topk, s);
+    if (p.E <= 128) return launch_forward<4>(p, bf16, topk, s);
+    if (p.E <= 256) return launch_forward<8>(p, bf16, topk, s);
+    if (p.E <= 512) return launch_forward<16>(p, bf16, topk, s);
+    return launch_forward<32>(p, bf16, topk, s);
+  }
+  p.vec = p.E % (bf16 ? 8 : 4) == 0 && ep_host::aligned16(p.logits) && ep_host::aligned16(p.grad_logits);
+  // as few lanes a token as hold its logits in 32 registers each and its k slots in one each
+  if (p.k <= 8) {
+    if (p.E <= 64) return launch_backward<8, 8>(p, bf16, topk, s);
+    if (p.E <= 128) return launch_backward<8, 16>(p, bf16, topk, s);
+    if (p.E <= 256) return launch_backward<8, 32>(p, bf16, topk, s);
+  }
+  if (p.E <= 128) return launch_backward<16, 8>(p, bf16, topk, s);
+  if (p.E <= 512) return launch_backward<16, 32>(p, bf16, topk, s);
+  return launch_backward<32, 32>(p, bf16, topk, s);
 }
 
 static int check_gate(const void* logits, int dtype, int R, int T_r, int E, int k, int score) {
