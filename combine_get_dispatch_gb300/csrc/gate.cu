@@ -144,6 +144,16 @@ __device__ __forceinline__ void gate_choose(float (&l)[kV], int k, int lane, flo
   }
 }
 
+// One choice among the lanes' candidates: the largest, and of those the one in the
+// lowest lane, gets place j and is out.
+__device__ __forceinline__ void gate_round(float& left, int j, uint32_t lane_bit, int& slot) {
+  const uint32_t who = __ballot_sync(0xffffffffu, left == warp_max(left));
+  if ((who & (0u - who)) == lane_bit) {
+    slot = j;
+    left = kNone;
+  }
+}
+
 // A lower bound of a row's 8th largest logit, from the lanes' largest: eight
 // disjoint groups of four lanes have a largest logit each, and the least of those
 // is no larger; the better of two such groupings.
@@ -183,6 +193,7 @@ template <int kV, bool kBf16, bool kTopk>
 __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k_gate(GateParams p) {
   __shared__ uint2 packed[kForwardThreads / kWarp][2 * kWarp];   // the upper half takes what is not packed
   const int lane = threadIdx.x & 31;
+  const uint32_t lane_bit = 1u << lane;
   uint2* mine = packed[threadIdx.x >> 5];
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
@@ -198,13 +209,13 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kV; ++i) n += l[i] >= least ? 1 : 0;
-    int before = 0, all = 0;   // candidates of lower lanes, of all: a bit of n at a time
+    int upto = n;   // candidates of this lane and those before it
 #pragma unroll
-    for (int b = 0; (1 << b) <= kV; ++b) {
-      const uint32_t has = __ballot_sync(0xffffffffu, (n >> b) & 1);
-      before += __popc(has & lanemask_lt()) << b;
-      all += __popc(has) << b;
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
+    const int all = __shfl_sync(0xffffffffu, upto, 31);
     float total = 0.0f;
     if (!kTopk) {
       if (m < INFINITY) {
@@ -219,6 +230,7 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
     float my_l = kNone;
     int my_idx = -1, slot = p.k, found = 0;
     if (all <= kWarp) {
+      int before = upto - n;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
@@ -234,13 +246,12 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
       }
       float left = my_l;
       const int rounds = min(p.k, all);
-      for (; found < rounds; ++found) {
-        const uint32_t who = __ballot_sync(0xffffffffu, left == warp_max(left));
-        if (((who & (0u - who)) >> lane) == 1u) {   // the lowest lane of them
-          slot = found;
-          left = kNone;
-        }
+#pragma unroll 1
+      for (; found + 4 <= rounds; found += 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gate_round(left, found + j, lane_bit, slot);
       }
+      for (; found < rounds; ++found) gate_round(left, found, lane_bit, slot);
       if (slot == p.k) my_l = kNone;
     } else {
       gate_choose<kV>(l, p.k, lane, my_l, my_idx);
@@ -251,7 +262,7 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
     if (kTopk) total = warp_sum(ex);
     if (slot < p.k) {
       p.idx[t * p.k + slot] = my_idx;
-      p.w[t * p.k + slot] = ex / total;
+      p.w[t * p.k + slot] = __fdividef(ex, total);   // 1 <= total <= E: within 2 ulp
     }
     if (lane >= found && lane < p.k) {
       p.idx[t * p.k + lane] = -1;
