@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t ue8m0_of(float amax) {
 template <int kAct>
 __device__ __forceinline__ float act_value(float z) {
   if (kAct == EP_ACT_RELU) return z < 0.0f ? 0.0f : z;   // a NaN stays one
-  if (kAct == EP_ACT_SILU) return z / (1.0f + __expf(-z));
+  if (kAct == EP_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));   // 2 ulp; 0 where the divisor passes 2^126
   if (kAct == EP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
   return z;
 }
@@ -70,7 +70,7 @@ __device__ __forceinline__ void act_both(float z, float& value, float& slope) {
     value = z < 0.0f ? 0.0f : z;
     slope = z > 0.0f ? 1.0f : 0.0f;
   } else if (kAct == EP_ACT_SILU) {
-    const float q = 1.0f / (1.0f + __expf(-z));
+    const float q = __fdividef(1.0f, 1.0f + __expf(-z));
     value = z * q;
     slope = q * (1.0f + z * (1.0f - q));
   } else if (kAct == EP_ACT_GELU) {

@@ -36,11 +36,11 @@
 namespace ep {
 
 constexpr int kGemmThreads = 384;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 10;
 constexpr int kTileM = 256, kTileN = 256, kHalf = 128;   // columns, rows of the output; a CTA's columns
 constexpr int kTileK = 64;                       // bf16 elements of one 128-byte row
 constexpr int kOperandBytes = kHalf * kTileK * 2;   // 16 KB: one CTA's part of an operand
-constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kStageBytes = 2 * kOperandBytes;      // of a whole tile
 constexpr int kBox = 32;                         // rows of a small copy
 constexpr int kEpilogueWarps = 8;                // two groups of four
 constexpr int kChunk = 32;                       // rows a group takes at a time
@@ -58,6 +58,7 @@ struct GemmParams {
   CUtensorMap a, b, b_small, out, keep;
   ProductParams p;
   int tile_rows, tiles_n;
+  int stages, stage_bytes;   // small tiles' stages hold fewer rows, and there are more of them
   bool a_whole, b_whole;   // an MN-major operand's 128 columns in one copy (4-d map)
 };
 
@@ -101,8 +102,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_expert_gemm(const __grid_constant__ GemmParams g) {
   extern __shared__ uint8_t raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  constexpr int kStages = stages_of(kForm), kBuffers = buffers_of(kForm);
-  uint8_t* out_buffers = stages + kStages * kStageBytes;
+  constexpr int kBuffers = buffers_of(kForm);
+  const int n_stages = g.stages, stage_bytes = g.stage_bytes;
+  uint8_t* out_buffers = stages + stages_of(kForm) * kStageBytes;
   Shared& sh = *reinterpret_cast<Shared*>(out_buffers + 2 * kBuffers * kBufferBytes);
   constexpr bool kAMn = kForm == kDw || kForm == kDx, kBMn = kForm == kDw;
   constexpr int kCols = kForm == kGlu ? kHalf : 256;   // output columns of a tile
@@ -116,7 +118,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     prefetch_map(&g.a);
     prefetch_map(&g.b);
     prefetch_map(&g.b_small);
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sh.full[s], 1);      // the first CTA's, with the bytes of both
       mbar_init(&sh.empty[s], 1);     // the products' commit
       mbar_init(&sh.landed[s], 1);
@@ -132,15 +134,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     fence_barrier_init();
   }
-  TileWalk walk;
-  if (warp == 2) {
-    tmem_alloc<2>(&sh.tmem, 512);
-    pdl_wait();   // all that follows reads what kernels before this one may have written
-    walk.begin(p.seg, kForm == kDw ? p.K : -1, g.tile_rows, g.tiles_n, kCols, blockIdx.x == 0, lane);
-  }
-  pdl_wait();
+  if (warp == 2) tmem_alloc<2>(&sh.tmem, 512);
   tmem_fence_before();
-  cluster_sync();
+  __syncwarp();
+  cluster_arrive();
+  pdl_wait();   // all that follows reads what kernels before this one may have written
+  TileWalk walk;
+  Tile first = {};
+  if (warp == 2) {
+    walk.begin(p.seg, kForm == kDw ? p.K : -1, g.tile_rows, g.tiles_n, kCols, blockIdx.x == 0, lane);
+    first = walk.at(pair, lane);
+  }
+  __syncwarp();
+  cluster_wait();
   tmem_fence_after();
   const uint32_t tmem = sh.tmem;
 
@@ -164,7 +170,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t sa = smem_addr(stages + s * kStageBytes), sb = sa + kOperandBytes;
+        const uint32_t sa = smem_addr(stages + s * stage_bytes), sb = sa + kOperandBytes;
         // kDw takes the segment's last rows first; where they end inside a product's 16, warp 3 clears the others
         const bool tail = kForm == kDw && kb == 0 && t.count % 16 != 0;
         uint32_t bar = map_to_rank(smem_addr(&sh.full[s]), 0);
@@ -204,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             for (int i = 0; i < boxes; ++i)
               tma_load_3d<true>(sb + i * (kOperandBytes / 4), &g.b_small, bar, k0, row + i * kBox, 0);
         }
-        if (++s == kStages) {
+        if (++s == n_stages) {
           s = 0;
           phase ^= 1;
         }
@@ -246,10 +252,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (issue) {
           const int steps = (t.count - (blocks - 1) * kTileK + 15) / 16;
           for (int i = 0; i < steps; ++i)
-            umma_bf16_pair(d, a0 + s * (kStageBytes >> 4) + i * kStepA, b0 + s * (kStageBytes >> 4) + i * kStepB, idesc, i > 0);
+            umma_bf16_pair(d, a0 + s * (stage_bytes >> 4) + i * kStepA, b0 + s * (stage_bytes >> 4) + i * kStepB, idesc, i > 0);
           umma_commit_pair(&sh.empty[s]);
         }
-        if (++s == kStages) s = 0;
+        if (++s == n_stages) s = 0;
         kb = 1;
       }
       for (; kb < blocks; ++kb) {
@@ -258,20 +264,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         full ^= 1u << s;
         tmem_fence_after();
         if (issue) {
-          const uint32_t a = a0 + s * (kStageBytes >> 4), b = b0 + s * (kStageBytes >> 4);
+          const uint32_t a = a0 + s * (stage_bytes >> 4), b = b0 + s * (stage_bytes >> 4);
           umma_bf16_pair(d, a, b, idesc, kForm == kDw || kb > 0);
 #pragma unroll
           for (uint32_t i = 1; i < kTileK / 16; ++i) umma_bf16_pair(d, a + i * kStepA, b + i * kStepB, idesc, true);
           umma_commit_pair(&sh.empty[s]);
         }
-        if (++s == kStages) s = 0;
+        if (++s == n_stages) s = 0;
       }
       if (!ok) break;
       if (issue) umma_commit_pair(&sh.sums_full[half]);
       ++n;
     }
   } else if (warp == 2) {
-    ok = feed_tiles(sh.ring, walk, pair, pairs, lane);
+    ok = feed_tiles(sh.ring, walk, first, pair, pairs, lane);
   } else if (kForm == kDw && warp == 3) {
     // ---------------------------------------------------------------- rows past a segment's end
     int s = 0;
@@ -281,9 +287,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (t.count % 16 != 0) {
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.landed[s], (parity >> s) & 1, 2 * kWaitNs));
         if (ok) {
-          uint8_t* base = stages + s * kStageBytes;
+          uint8_t* base = stages + s * stage_bytes;
           const int last = t.count - (blocks - 1) * kTileK, rows = 16 - last % 16;
-          for (int i = lane; i < 4 * 8 * rows; i += 32)   // 4 boxes of 64 x 64, rows of 8 16-byte pieces
+          const int boxes = 2 + ((t.rows + 15) / 16 * 8 + 63) / 64;   // of 64 x 64: two of x, one or two of d
+          for (int i = lane; i < boxes * 8 * rows; i += 32)           // rows of 8 16-byte pieces
             st_shared_v4(base + (i / (8 * rows)) * (kOperandBytes / 2) + (last + i / 8 % rows) * 128 + (i % 8) * 16,
                          make_uint4(0, 0, 0, 0));
           fence_proxy_async_smem();
@@ -292,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           parity ^= 1u << s;
         }
       }
-      s = (s + blocks) % kStages;
+      s = (s + blocks) % n_stages;
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
@@ -546,6 +553,9 @@ int launch_gemm_bf16(Form form, const ProductParams& p, int act, cudaStream_t st
   g.tile_rows = kTileN;
   while (g.tile_rows > 32 && tiles_of(g.tile_rows / 2) <= pairs) g.tile_rows /= 2;
   const int64_t tiles = tiles_of(g.tile_rows);
+  const int b_bytes = form == kDw ? (g.tile_rows / 2 + 63) / 64 * (kOperandBytes / 2) : (g.tile_rows / 2 + kBox - 1) / kBox * (kOperandBytes / 4);
+  g.stage_bytes = kOperandBytes + b_bytes;
+  g.stages = std::min(kMaxStages, stages_of(form) * kStageBytes / g.stage_bytes);
   if (tiles / g.tiles_n >= (int64_t)1 << 31) return EP_ERR_INVALID_ARG;
   switch (form) {
     case kGlu: return launch_gemm_act<kGlu>(g, tiles, act, stream);

@@ -144,17 +144,19 @@ __device__ __forceinline__ bool next_tile_warp(TileRing& ring, uint32_t& taken, 
   if (ok && lane == 0) mbar_arrive(free);
   return ok && more;
 }
-// The walking warp: tiles first, first + step, ... until the list ends.
-__device__ __forceinline__ bool feed_tiles(TileRing& ring, TileWalk& walk, int64_t first, int64_t step, int lane) {
-  for (uint32_t n = 0;; ++n, first += step) {
+// The walking warp: tiles first (which is t), first + step, ... until the list
+// ends.
+__device__ __forceinline__ bool feed_tiles(TileRing& ring, TileWalk& walk, Tile t, int64_t first, int64_t step, int lane) {
+  for (uint32_t n = 0;; ++n) {
     const uint32_t i = n % kTiles;
-    const Tile t = walk.at(first, lane);
     if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ring.empty[i], ((n / kTiles) & 1) ^ 1, kTileWaitNs))) return false;
     if (lane == 0) {
       ring.tiles[i] = t;
       mbar_arrive(&ring.full[i]);
     }
     if (t.e < 0) return true;
+    first += step;
+    t = walk.at(first, lane);
   }
 }
 

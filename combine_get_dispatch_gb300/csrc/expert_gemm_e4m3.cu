@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks = p.K / kFp8Block;
 
+  if (warp == 2) tmem_alloc<1>(&sh.tmem, 512);
   if (threadIdx.x == 0) {
     prefetch_map(&g.a);
     prefetch_map(&g.a_small);
@@ -117,16 +118,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     }
     fence_barrier_init();
   }
-  TileWalk walk;
-  if (warp == 2) {
-    tmem_alloc<1>(&sh.tmem, 512);
-    pdl_wait();   // all that follows reads what kernels before this one may have written
-    walk.begin(p.seg, -1, kMxTileM, g.tiles_n, kCols, blockIdx.x == 0, lane);
-  }
-  pdl_wait();
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  pdl_wait();   // all that follows reads what kernels before this one may have written
   const uint32_t tmem = sh.tmem;
 
   bool ok = true;
@@ -195,7 +190,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
       if (issue) umma_commit(&sh.sums_full);
     }
   } else if (warp == 2) {
-    ok = feed_tiles(sh.ring, walk, blockIdx.x, gridDim.x, lane);
+    TileWalk walk;
+    walk.begin(p.seg, -1, kMxTileM, g.tiles_n, kCols, blockIdx.x == 0, lane);
+    ok = feed_tiles(sh.ring, walk, walk.at(blockIdx.x, lane), blockIdx.x, gridDim.x, lane);
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- scales
     int s = 0;
