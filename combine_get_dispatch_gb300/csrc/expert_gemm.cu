@@ -288,11 +288,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.landed[s], (parity >> s) & 1, 2 * kWaitNs));
         if (ok) {
           uint8_t* base = stages + s * stage_bytes;
-          const int last = t.count - (blocks - 1) * kTileK, rows = 16 - last % 16;
-          const int boxes = 2 + ((t.rows + 15) / 16 * 8 + 63) / 64;   // of 64 x 64: two of x, one or two of d
-          for (int i = lane; i < boxes * 8 * rows; i += 32)           // rows of 8 16-byte pieces
-            st_shared_v4(base + (i / (8 * rows)) * (kOperandBytes / 2) + (last + i / 8 % rows) * 128 + (i % 8) * 16,
-                         make_uint4(0, 0, 0, 0));
+          // boxes of 64 x 64 (two of x, one or two of d), rows of 8 16-byte pieces: a lane a piece of one box
+          const int boxes = 2 + ((t.rows + 15) / 16 * 8 + 63) / 64;
+          if (lane >> 3 < boxes)
+            for (int r = t.count - (blocks - 1) * kTileK; r % 16 != 0; ++r)
+              st_shared_v4(base + (lane >> 3) * (kOperandBytes / 2) + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&sh.cleared[s]), 0));

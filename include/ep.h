@@ -324,12 +324,15 @@ int ep_format_bf16(const float* in, uint16_t* out, int64_t n, void* stream);
 
 /* SM budget (Buffer.num_sms, §2.2; the per-SM bandwidth model of §4.6):
  * caps the SMs that the data kernels of ep_dispatch, ep_ll_dispatch,
- * ep_combine, ep_ll_combine and ep_rank_combine occupy, so the rest of the
+ * ep_combine, ep_ll_combine, ep_rank_combine and the expert calls' products
+ * (ep_expert_*) occupy, so the rest of the
  * GPU stays free for work that overlaps them.  num_sms = 0 lifts the cap
  * (every SM; the default); num_sms > 0 launches those kernels with at most
  * min(num_sms, SM count) CTAs of one per SM.  The single-launch low-latency
  * path then runs on that many SMs if the batch still fits them, else the
- * multi-kernel path is taken.  The layout and notify kernels (a few
+ * multi-kernel path is taken.  The bf16 expert products (and the gradients')
+ * run on pairs of SMs: on the largest even number within the cap, but two at
+ * least.  The layout and notify kernels (a few
  * microseconds, one CTA per id chunk / one CTA) are not capped.  Process-
  * wide, read at every launch; returns EP_ERR_INVALID_ARG for num_sms < 0.
  * ep_get_num_sms: the CTA count one-per-SM kernels get now (the SM count of
