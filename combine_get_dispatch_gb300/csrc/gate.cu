@@ -114,6 +114,42 @@ __device__ __forceinline__ float gate_share(float l) { return l == INFINITY ? 1.
 
 __device__ __forceinline__ float gate_weight(float l, float m) { return m < INFINITY ? gate_exp(l, m) : gate_share(l); }
 
+// A candidate's place in the falling order of the list: the number of larger
+// logits, and (exact) of equal ones of a lower expert.  The list is padded with
+// -inf to a multiple of 8.
+__device__ __forceinline__ int gate_place(const float* logits, int all, float mine) {
+  int place = 0;
+  for (int j = 0; j < all; j += 8) {
+    const float4 x = *reinterpret_cast<const float4*>(logits + j), y = *reinterpret_cast<const float4*>(logits + j + 4);
+    place += (x.x > mine ? 1 : 0) + (x.y > mine ? 1 : 0) + (x.z > mine ? 1 : 0) + (x.w > mine ? 1 : 0);
+    place += (y.x > mine ? 1 : 0) + (y.y > mine ? 1 : 0) + (y.z > mine ? 1 : 0) + (y.w > mine ? 1 : 0);
+  }
+  return place;
+}
+__device__ __forceinline__ int gate_place_exact(const float* logits, const int* experts, int all, float mine, int expert) {
+  int place = 0;
+  for (int j = 0; j < all; ++j) {
+    const float x = logits[j];
+    place += x > mine || (x == mine && experts[j] < expert) ? 1 : 0;
+  }
+  return place;
+}
+
+// Writes a logit and its expert (32 words on) where the logit is a candidate.
+__device__ __forceinline__ void gate_put(uint32_t at, float l, float least, int expert) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ge.f32 p, %1, %2;\n @p st.shared.f32 [%0], %1;\n @p st.shared.u32 [%0 + 128], %3;\n}\n" ::"r"(at),
+      "f"(l), "f"(least), "r"(expert)
+      : "memory");
+}
+
+// A finite bf16 logit with its expert in the 16 bits below it: equal logits (and
+// zeros of both signs) then fall in the order of their experts.
+__device__ __forceinline__ float gate_unique(float l, int expert) {
+  const uint32_t u = __float_as_uint(l + 0.0f);
+  return __uint_as_float(u | (uint32_t)((u & 0x80000000u) ? expert : 0xffff - expert));
+}
+
 // The k largest of the warp's logits, one round a choice: the largest, the
 // lowest lane that holds it, that lane's lowest expert.  Lane j of the result
 // holds choice j (-inf: none).
@@ -144,16 +180,6 @@ __device__ __forceinline__ void gate_choose(float (&l)[kV], int k, int lane, flo
   }
 }
 
-// One choice among the lanes' candidates: the largest, and of those the one in the
-// lowest lane, gets place j and is out.
-__device__ __forceinline__ void gate_round(float& left, int j, uint32_t lane_bit, int& slot) {
-  const uint32_t who = __ballot_sync(0xffffffffu, left == warp_max(left));
-  if ((who & (0u - who)) == lane_bit) {
-    slot = j;
-    left = kNone;
-  }
-}
-
 // A lower bound of a row's 8th largest logit, from the lanes' largest: eight
 // disjoint groups of four lanes have a largest logit each, and the least of those
 // is no larger; the better of two such groupings.
@@ -180,21 +206,22 @@ __device__ __forceinline__ float gate_bound(float best, int k, int lane) {
   return __shfl_sync(0xffffffffu, best, k - 1);
 }
 
-// One warp per token.  A round of choosing costs a warp about as many instructions
-// as it holds logits, so most logits are thrown out first: only those at or above
-// a bound of the k-th largest can be chosen (some 15 of 256).  They are packed, in
-// expert order, one to a lane, and a choice is then one reduction and one ballot.
-// Rows where more than 32 remain take the plain rounds.  Issue
-// slots bound it: about 420 instructions a token of 256 experts, 63.5 us for 131072
-// tokens (21.7 us to read and write them).  As slow or slower: places counted
-// against the packed list (68 us); 8 lanes a token with 32 logits each (99 us: as
-// many instructions a token, and registers for half the warps).
+// One warp per token.  Most logits are thrown out first: only those at or above a
+// bound of the k-th largest can be chosen (17 of 256 on average).  The others go to
+// a list, one to a lane, and each counts the larger ones.  Equal logits, in the
+// order of their experts, are looked at only where they have left a gap in the
+// places; bf16 logits, often equal, are made unique.  Rows where more than 32
+// remain take their choices one round at a time.  Issue slots bound it: about 380
+// instructions a token, 59.5 us for 131072 x 256 (21.7 us to read and write them).
+// Slower: k rounds of a reduction and a ballot over the list (63.5 us); 8 lanes a
+// token with 32 logits each (99 us: registers for half the warps).
 template <int kV, bool kBf16, bool kTopk>
 __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k_gate(GateParams p) {
-  __shared__ uint2 packed[kForwardThreads / kWarp][2 * kWarp];   // the upper half takes what is not packed
+  __shared__ float4 lists[kForwardThreads / kWarp][2 * kWarp / 4];   // 32 logits, their 32 experts
   const int lane = threadIdx.x & 31;
-  const uint32_t lane_bit = 1u << lane;
-  uint2* mine = packed[threadIdx.x >> 5];
+  float* list = reinterpret_cast<float*>(lists[threadIdx.x >> 5]);
+  const int* experts = reinterpret_cast<const int*>(list + kWarp);
+  const uint32_t list_at = smem_addr(list), lower = lanemask_lt();
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   for (int64_t t = warp0; t < p.T; t += nwarps) {
@@ -206,16 +233,13 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
     const float m = gate_base(warp_max(best));
     // at least the type's lowest value, so that -inf is no candidate
     const float least = fmaxf(kLowest, p.k <= 8 ? gate_bound8(best) : gate_bound(best, p.k, lane));
-    int n = 0;
+    uint32_t who[kV];
+    int all = 0;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) n += l[i] >= least ? 1 : 0;
-    int upto = n;   // candidates of this lane and those before it
-#pragma unroll
-    for (int o = 1; o < kWarp; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
+    for (int i = 0; i < kV; ++i) {
+      who[i] = __ballot_sync(0xffffffffu, l[i] >= least);
+      all += __popc(who[i]);
     }
-    const int all = __shfl_sync(0xffffffffu, upto, 31);
     float total = 0.0f;
     if (!kTopk) {
       if (m < INFINITY) {
@@ -228,41 +252,44 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
       total = warp_sum(total);
     }
     float my_l = kNone;
-    int my_idx = -1, slot = p.k, found = 0;
+    int my_idx = -1, place = p.k, found;
     if (all <= kWarp) {
-      int before = upto - n;
+      found = min(p.k, all);
       __syncwarp();
+      list[lane] = kNone;
+      __syncwarp();
+      uint32_t at = list_at;
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
-        const bool take = l[i] >= least;
-        mine[take ? before : kWarp + lane] = make_uint2(__float_as_uint(l[i]), (uint32_t)(lane * kV + i));
-        before += take ? 1 : 0;
+        gate_put(at + 4 * __popc(who[i] & lower), l[i], least, lane * kV + i);
+        at += 4 * __popc(who[i]);
       }
       __syncwarp();
-      if (lane < all) {
-        const uint2 c = mine[lane];
-        my_l = __uint_as_float(c.x);
-        my_idx = (int)c.y;
+      my_l = list[lane];
+      my_idx = experts[lane];
+      float key = my_l;
+      if (kBf16 && m < INFINITY) {
+        key = gate_unique(my_l, my_idx);
+        __syncwarp();
+        if (lane < all) list[lane] = key;
+        __syncwarp();
       }
-      float left = my_l;
-      const int rounds = min(p.k, all);
-#pragma unroll 1
-      for (; found + 4 <= rounds; found += 4) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) gate_round(left, found + j, lane_bit, slot);
-      }
-      for (; found < rounds; ++found) gate_round(left, found, lane_bit, slot);
-      if (slot == p.k) my_l = kNone;
+      place = gate_place(list, all, key);
+      // the places below k are as many as there are choices, each once, unless equal logits share one
+      const bool taken = lane < all && place < p.k;
+      if (__reduce_add_sync(0xffffffffu, taken ? (1 << 16) + place : 0) != (found << 16) + found * (found - 1) / 2)
+        place = gate_place_exact(list, experts, all, key, my_idx);
+      if (lane >= all) place = p.k;
     } else {
       gate_choose<kV>(l, p.k, lane, my_l, my_idx);
       found = __popc(__ballot_sync(0xffffffffu, my_idx >= 0));
-      slot = my_idx >= 0 ? lane : p.k;
+      place = my_idx >= 0 ? lane : p.k;
     }
-    const float ex = gate_weight(my_l, m);
+    const float ex = place < p.k ? gate_weight(my_l, m) : 0.0f;
     if (kTopk) total = warp_sum(ex);
-    if (slot < p.k) {
-      p.idx[t * p.k + slot] = my_idx;
-      p.w[t * p.k + slot] = __fdividef(ex, total);   // 1 <= total <= E: within 2 ulp
+    if (place < p.k) {
+      p.idx[t * p.k + place] = my_idx;
+      p.w[t * p.k + place] = __fdividef(ex, total);   // 1 <= total <= E: within 2 ulp
     }
     if (lane >= found && lane < p.k) {
       p.idx[t * p.k + lane] = -1;
