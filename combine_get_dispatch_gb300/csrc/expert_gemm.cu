@@ -24,9 +24,10 @@
 // same 8 of Wu (one copy through a 5-d tensor map), which brings both halves of
 // an output into one thread.
 //
-// Roles: warp 0 copies (TMA, 5 or 6 stages), warp 1 of the first CTA issues products,
-// warp 2 owns the tensor memory and walks the list of tiles, warp 3 clears the
-// rows past a segment's end (kDw, whose inner index is the row), warps 4-11 read
+// Roles: warps 0 and 3 copy (TMA, 5 or 6 stages), warp 1 of the first CTA issues
+// products, warp 2 owns the tensor memory and walks the list of tiles, in kDw,
+// whose inner index is the row, warp 3 clears the rows past a segment's end
+// instead and warp 0 copies both operands, warps 4-11 read
 // the sums back and run the epilogue while the products of the next tile fill the
 // other half of the tensor memory.
 
@@ -130,7 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&sh.ring.full[i], 1);
-      mbar_init(&sh.ring.empty[i], 1 + (rank == 0 ? 1 : 0) + (kForm == kDw ? 1 : 0) + kEpilogueWarps);
+      mbar_init(&sh.ring.empty[i], 2 + (rank == 0 ? 1 : 0) + kEpilogueWarps);   // warps 0, 3, 1 and the epilogue's
     }
     fence_barrier_init();
   }
@@ -155,62 +156,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   Tile t = {};
   auto inner_blocks = [&]() { return ((kForm == kDw ? t.count : p.K) + kTileK - 1) / kTileK; };
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 || (kForm != kDw && warp == 3)) {
     // ---------------------------------------------------------------- copies
-    int s = 0;
-    uint32_t phase = 0;
-    while (next_tile(sh.ring, taken, t, ok)) {
+    // warp 0 the first operand and kDw's second, else warp 3 the second: one warp issues a stage's copies in
+    // about 300 ns, as long as the products of a whole tile's stage take.  Converged, one lane issues.
+    const bool issue = elect_one();
+    const uint32_t stage0 = smem_addr(stages), full0 = map_to_rank(smem_addr(&sh.full[0]), 0);
+    uint32_t s = 0, phase = 0;
+    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       const int half = (t.rows + 15) / 16 * 8;   // rows of the second operand in a CTA
       // copied 32 at a time, or all 128; kDw: 64 columns of d at a time
       const int boxes = kForm == kDw ? (half + 63) / 64 : (half + kBox - 1) / kBox;
       const uint32_t mine = kOperandBytes + boxes * (kForm == kDw ? kOperandBytes / 2 : kOperandBytes / 4);
+      const int n0 = t.n0 + (int)rank * (kForm == kGlu ? 64 : kHalf);                        // of the first operand
+      const int m0 = t.m0 + (int)rank * half + (kForm == kDw ? 0 : t.start);                 // of the second
       for (int kb = 0; kb < blocks; ++kb) {
-        if (!mbar_wait_bounded(&sh.empty[s], phase ^ 1)) {
-          ok = false;
-          break;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
+        if (!ok) break;
+        if (issue) {
+          const uint32_t sa = stage0 + s * stage_bytes, sb = sa + kOperandBytes;
+          uint32_t bar = full0 + s * (uint32_t)sizeof(uint64_t);
+          if (kForm == kDw) {
+            // the segment's last rows first; where they end inside a product's 16, warp 3 clears the others
+            if (kb == 0 && t.count % 16 != 0) {
+              bar = smem_addr(&sh.landed[s]);
+              mbar_arrive_expect_tx(&sh.landed[s], mine);
+            } else if (rank == 0) {
+              mbar_arrive_expect_tx(&sh.full[s], 2 * mine);
+            }
+            const int row = t.start + (blocks - 1 - kb) * kTileK;
+            if (g.a_whole)
+              tma_load_4d_pair(sa, &g.a, bar, 0, row, n0 / 64, 0);
+            else
+              for (int i = 0; i < 2; ++i)
+                tma_load_3d<true>(sa + i * (kOperandBytes / 2), &g.a, bar, n0 + i * 64, row, 0);
+            if (g.b_whole && half == kHalf && m0 % 64 == 0)
+              tma_load_4d_pair(sb, &g.b, bar, 0, row, m0 / 64, 0);
+            else
+              for (int i = 0; i < boxes; ++i)
+                tma_load_3d<true>(sb + i * (kOperandBytes / 2), &g.b_small, bar, m0 + i * 64, row, 0);
+          } else if (warp == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * mine);
+            const int k0 = kb * kTileK;
+            if (kForm == kGlu)
+              tma_load_5d_pair(sa, &g.a, bar, k0, 0, 0, n0 / 8, t.e);
+            else if (kForm == kLinear)
+              tma_load_3d<true>(sa, &g.a, bar, k0, n0, t.e);
+            else if (g.a_whole)
+              tma_load_4d_pair(sa, &g.a, bar, 0, k0, n0 / 64, t.e);
+            else
+              for (int i = 0; i < 2; ++i)
+                tma_load_3d<true>(sa + i * (kOperandBytes / 2), &g.a, bar, n0 + i * 64, k0, t.e);
+          } else {
+            const int k0 = kb * kTileK;
+            if (boxes == 4)
+              tma_load_3d<true>(sb, &g.b, bar, k0, m0, 0);
+            else
+              for (int i = 0; i < boxes; ++i)
+                tma_load_3d<true>(sb + i * (kOperandBytes / 4), &g.b_small, bar, k0, m0 + i * kBox, 0);
+          }
         }
-        const uint32_t sa = smem_addr(stages + s * stage_bytes), sb = sa + kOperandBytes;
-        // kDw takes the segment's last rows first; where they end inside a product's 16, warp 3 clears the others
-        const bool tail = kForm == kDw && kb == 0 && t.count % 16 != 0;
-        uint32_t bar = map_to_rank(smem_addr(&sh.full[s]), 0);
-        if (tail) {
-          bar = smem_addr(&sh.landed[s]);
-          mbar_arrive_expect_tx(&sh.landed[s], mine);
-        } else if (rank == 0) {
-          mbar_arrive_expect_tx(&sh.full[s], 2 * mine);
-        }
-        const int k0 = (kForm == kDw ? blocks - 1 - kb : kb) * kTileK;
-        if (kForm == kDw) {
-          const int n0 = t.n0 + (int)rank * kHalf, m0 = t.m0 + (int)rank * half;
-          if (g.a_whole)
-            tma_load_4d_pair(sa, &g.a, bar, 0, t.start + k0, n0 / 64, 0);
-          else
-            for (int i = 0; i < 2; ++i)
-              tma_load_3d<true>(sa + i * (kOperandBytes / 2), &g.a, bar, n0 + i * 64, t.start + k0, 0);
-          if (g.b_whole && half == kHalf && m0 % 64 == 0)
-            tma_load_4d_pair(sb, &g.b, bar, 0, t.start + k0, m0 / 64, 0);
-          else
-            for (int i = 0; i < boxes; ++i)
-              tma_load_3d<true>(sb + i * (kOperandBytes / 2), &g.b_small, bar, m0 + i * 64, t.start + k0, 0);
-        } else {
-          if (kForm == kGlu)
-            tma_load_5d_pair(sa, &g.a, bar, k0, 0, 0, t.n0 / 8 + (int)rank * 8, t.e);
-          else if (kForm == kLinear)
-            tma_load_3d<true>(sa, &g.a, bar, k0, t.n0 + (int)rank * kHalf, t.e);
-          else if (g.a_whole)
-            tma_load_4d_pair(sa, &g.a, bar, 0, k0, (t.n0 + (int)rank * kHalf) / 64, t.e);
-          else
-            for (int i = 0; i < 2; ++i)
-              tma_load_3d<true>(sa + i * (kOperandBytes / 2), &g.a, bar, t.n0 + (int)rank * kHalf + i * 64, k0, t.e);
-          const int row = t.start + t.m0 + (int)rank * half;
-          if (boxes == 4)
-            tma_load_3d<true>(sb, &g.b, bar, k0, row, 0);
-          else
-            for (int i = 0; i < boxes; ++i)
-              tma_load_3d<true>(sb + i * (kOperandBytes / 4), &g.b_small, bar, k0, row + i * kBox, 0);
-        }
-        if (++s == n_stages) {
+        if (++s == (uint32_t)n_stages) {
           s = 0;
           phase ^= 1;
         }
