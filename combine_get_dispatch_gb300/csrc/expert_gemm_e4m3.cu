@@ -16,7 +16,7 @@
 // 361 and 193 us on the two decode products, whose few rows leave most of a
 // 256-row tile empty.
 //
-// Roles: warp 0 copies, warp 1 issues products, warp 2 owns the tensor memory,
+// Roles: warps 0 and 3 copy, warp 1 issues products, warp 2 owns the tensor memory,
 // warps 4-7 run the epilogue, warps 8-11 move the scales of a stage from global
 // memory (read a few blocks ahead) to tensor memory, each to its own 32 lanes.
 
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     mbar_init(&sh.sums_empty, 4);
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&sh.ring.full[i], 1);
-      mbar_init(&sh.ring.empty[i], 2 + 4 + 4);   // copies, products, scale warps, epilogue warps
+      mbar_init(&sh.ring.empty[i], 3 + 4 + 4);   // copies (two), products, scale warps, epilogue warps
     }
     fence_barrier_init();
   }
@@ -132,27 +132,31 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
   bool ok = true;
   uint32_t taken = 0;
   Tile t = {};
-  if (warp == 0 && lane == 0) {
-    int s = 0;
-    uint32_t phase = 0;
-    while (next_tile(sh.ring, taken, t, ok)) {
-      const int boxes = (t.rows + kMxBox - 1) / kMxBox;
+  if (warp == 0 || warp == 3) {   // the weights; the rows: converged warps, one lane issues
+    const bool issue = elect_one();
+    const uint32_t stage0 = smem_addr(stages);
+    uint32_t s = 0, phase = 0;
+    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+      const int boxes = (t.rows + kMxBox - 1) / kMxBox, row = t.start + t.m0;
       for (int kb = 0; kb < blocks; ++kb) {
-        if (!mbar_wait_bounded(&sh.empty[s], phase ^ 1)) {
-          ok = false;
-          break;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
+        if (!ok) break;
+        if (issue) {
+          const uint32_t sa = stage0 + s * kMxStageBytes, sb = sa + kMxABytes, bar = smem_addr(&sh.full[s]);
+          const int k0 = kb * kFp8Block;
+          if (warp == 0) {
+            mbar_arrive_expect_tx(&sh.full[s], kMxBBytes + boxes * (kMxABytes / 4));
+            if (kForm == kGlu)
+              tma_load_4d(sb, &g.b, bar, k0, t.n0, 0, t.e);
+            else
+              tma_load_3d<false>(sb, &g.b, bar, k0, t.n0, t.e);
+          } else if (boxes == 4) {
+            tma_load_3d<false>(sa, &g.a, bar, k0, row, 0);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_3d<false>(sa + i * (kMxABytes / 4), &g.a_small, bar, k0, row + i * kMxBox, 0);
+          }
         }
-        const uint32_t sa = smem_addr(stages + s * kMxStageBytes), sb = sa + kMxABytes, bar = smem_addr(&sh.full[s]);
-        mbar_arrive_expect_tx(&sh.full[s], kMxBBytes + boxes * (kMxABytes / 4));
-        const int k0 = kb * kFp8Block;
-        for (int i = 0; i < 2; ++i)
-          tma_load_3d<false>(sb + i * (kMxBBytes / 2), &g.b, bar, k0, t.n0 + (kForm == kGlu ? 0 : i * 128),
-                             kForm == kGlu ? 2 * t.e + i : t.e);
-        if (boxes == 4)
-          tma_load_3d<false>(sa, &g.a, bar, k0, t.start + t.m0, 0);
-        else
-          for (int i = 0; i < boxes; ++i)
-            tma_load_3d<false>(sa + i * (kMxABytes / 4), &g.a_small, bar, k0, t.start + t.m0 + i * kMxBox, 0);
         if (++s == kMxStages) {
           s = 0;
           phase ^= 1;
@@ -349,13 +353,20 @@ static int launch_mx_act(const MxParams& g, int64_t tiles, int act, cudaStream_t
 int launch_gemm_e4m3(Form form, const ProductParams& p, int act, cudaStream_t stream) {
   MxParams g;
   g.p = p;
-  const uint64_t K = (uint64_t)p.K, N = (uint64_t)p.N, rows = (uint64_t)p.rows;
-  const uint64_t ad[3] = {K, rows, 1}, bd[3] = {K, N, (uint64_t)p.seg.E * (form == kGlu ? 2 : 1)};
-  const uint64_t as[2] = {K, K * rows}, bs[2] = {K, K * N};
+  const uint64_t K = (uint64_t)p.K, N = (uint64_t)p.N, rows = (uint64_t)p.rows, E = (uint64_t)p.seg.E;
+  const uint64_t ad[3] = {K, rows, 1}, as[2] = {K, K * rows};
   const uint32_t big[3] = {kFp8Block, kMxTileM, 1}, small[3] = {kFp8Block, kMxBox, 1};
   int rc = ep_host::make_map(&g.a, true, 3, p.a, ad, as, big);
   if (rc == EP_OK) rc = ep_host::make_map(&g.a_small, true, 3, p.a, ad, as, small);
-  if (rc == EP_OK) rc = ep_host::make_map(&g.b, true, 3, p.b, bd, bs, big);
+  if (form == kGlu) {   // 128 columns of gate and the same of up
+    const uint64_t bd[4] = {K, N, 2, E}, bs[3] = {K, K * N, 2 * K * N};
+    const uint32_t box[4] = {kFp8Block, kMxTileN / 2, 2, 1};
+    if (rc == EP_OK) rc = ep_host::make_map(&g.b, true, 4, p.b, bd, bs, box);
+  } else {
+    const uint64_t bd[3] = {K, N, E}, bs[2] = {K, K * N};
+    const uint32_t box[3] = {kFp8Block, kMxTileN, 1};
+    if (rc == EP_OK) rc = ep_host::make_map(&g.b, true, 3, p.b, bd, bs, box);
+  }
   if (rc != EP_OK) return rc;
   const int cols = form == kGlu ? 128 : 256;
   g.tiles_n = (p.N + cols - 1) / cols;
