@@ -10,14 +10,14 @@
 // some tens of rows and the time is that of reading its weights once: one CTA per
 // SM computes 128 x 256 tiles, so that two thirds of the bytes in flight (4 stages
 // of 48 KB, fewer rows of A where the segment has fewer) are weights: 64 experts
-// with 64 rows of 7168, gated, in 288 us (0.99 of the copy rate), 2048 -> 7168 in
-// 154 us (0.96).  Large batches wait for the L2 in this form (65536 rows over 32
-// experts: 1549 us, 2480 TFLOP/s); pairs of CTAs as for bf16 took 1343 us there, but
-// 361 and 193 us on the two decode products, whose few rows leave most of a
-// 256-row tile empty.
+// with 64 rows of 7168, gated, in 285-291 us (0.98-1.0 of the copy rate), 2048 ->
+// 7168 in 154-157 us (0.94-0.96).  65536 rows over 32 experts, gated, take 1303 us
+// (2950 TFLOP/s; 1549 us while one warp issued all copies); pairs of CTAs as for
+// bf16 took 1343 us there, and 361 and 193 us on the two decode products, whose
+// few rows leave most of a 256-row tile empty.
 //
 // Roles: warps 0 and 3 copy, warp 1 issues products, warp 2 owns the tensor memory,
-// warps 4-7 run the epilogue, warps 8-11 move the scales of a stage from global
+// warps 4-7 and 12-15 run the epilogue, warps 8-11 move the scales of a stage from global
 // memory (read a few blocks ahead) to tensor memory, each to its own 32 lanes.
 
 #include "expert_gemm.cuh"
@@ -25,7 +25,7 @@
 
 namespace ep {
 
-constexpr int kMxThreads = 384;
+constexpr int kMxThreads = 512;
 constexpr int kMxStages = 4;
 constexpr int kMxTileM = 128, kMxTileN = 256;
 constexpr int kMxABytes = kMxTileM * kFp8Block, kMxBBytes = kMxTileN * kFp8Block;
@@ -46,6 +46,7 @@ struct MxShared {
   uint64_t sums_full, sums_empty;
   TileRing ring;
   uint32_t tmem;
+  float amax[2][kMxTileM];   // of the halves of a row's outputs (E4M3 output)
 };
 
 // One block's scale bytes as a lane of a scale warp reads them: rows lane + 32 j
@@ -116,10 +117,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
       mbar_init(&sh.empty[s], 1);
     }
     mbar_init(&sh.sums_full, 1);
-    mbar_init(&sh.sums_empty, 4);
+    mbar_init(&sh.sums_empty, 8);
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&sh.ring.full[i], 1);
-      mbar_init(&sh.ring.empty[i], 3 + 4 + 4);   // copies (two), products, scale warps, epilogue warps
+      mbar_init(&sh.ring.empty[i], 3 + 4 + 8);   // copies (two), products, scale warps, epilogue warps
     }
     fence_barrier_init();
   }
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     TileWalk walk;
     walk.begin(p.seg, -1, kMxTileM, g.tiles_n, kCols, blockIdx.x == 0, lane);
     ok = feed_tiles(sh.ring, walk, walk.at(blockIdx.x, lane), blockIdx.x, gridDim.x, lane);
-  } else if (warp >= 8) {
+  } else if (warp >= 8 && warp < 12) {
     // ---------------------------------------------------------------- scales
     int s = 0;
     uint32_t phase = 0;
@@ -261,44 +262,59 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;
+    const int q = warp & 3, side = warp >= 12 ? 1 : 0;   // 32 rows; which half of the columns
+    const int first = side * (kCols / 2);
     uint32_t n = 0;
     const uint32_t d = tmem + ((uint32_t)(q * 32) << 16);
     while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
-      const int m = t.m0 + q * 32 + lane;
-      const bool in = q * 32 + lane < t.rows;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_full, n & 1, kWaitNs + (uint64_t)blocks * 2000));
+      const int r = q * 32 + lane;
+      const bool in = r < t.rows, quantised = kForm == kGlu && p.out_scales != nullptr;
+      // with scales the two warps of a row meet below, so they give up together
+      ok = mbar_wait_bounded(&sh.sums_full, n & 1, kWaitNs + (uint64_t)blocks * 2000);
+      ok = quantised ? named_barrier_and(1 + q, 64, ok) : __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ++n;
       tmem_fence_after();
+      auto sums_read = [&]() {   // the next tile's products may have them
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.sums_empty);
+      };
+      if (q * 32 >= t.rows) {   // none of this warp's rows
+        sums_read();
+        continue;
+      }
+      const int64_t row = (int64_t)t.start + t.m0 + r;
       float v[32], u[32];
-      float amax = 0.0f;
-      const bool quantised = kForm == kGlu && p.out_scales != nullptr;
+      float mul = 1.0f;
       if (quantised) {   // the row's largest output first: its 128 columns are one scale block
+        float amax = 0.0f;
 #pragma unroll 1
-        for (int c0 = 0; c0 < kCols; c0 += 32) {
+        for (int c0 = first; c0 < first + kCols / 2; c0 += 32) {
           tmem_ld32(d + c0, v);
           tmem_ld32(d + 128 + c0, u);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(act_value<kAct>(v[i]) * u[i]));
         }
+        sh.amax[side][r] = amax;
+        named_barrier_sync(1 + q, 64);
+        const uint32_t byte = ue8m0_of(fmaxf(amax, sh.amax[side ^ 1][r]));
+        mul = __uint_as_float((254u - byte) << 23);
+        if (in && side == 0) {
+          const int64_t owner = row / p.seg.cap;
+          p.out_scales[(owner * (p.N / kFp8Block) + t.n0 / kFp8Block) * p.seg.cap + (row - owner * p.seg.cap)] = (uint8_t)byte;
+        }
       }
-      const uint32_t byte = ue8m0_of(amax);
-      const float mul = __uint_as_float((254u - byte) << 23);
 #pragma unroll 1
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
+      for (int c0 = first; c0 < first + kCols / 2; c0 += 32) {
         tmem_ld32(d + c0, v);
         if (kForm == kGlu) tmem_ld32(d + 128 + c0, u);
         tmem_wait_ld();
-        if (c0 + 32 == kCols) {   // the sums are read: the next tile's products may have them
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.sums_empty);
-        }
+        if (c0 + 32 == first + kCols / 2) sums_read();
         if (in) {
           if (quantised) {
-            uint8_t* out = static_cast<uint8_t*>(p.out) + ((int64_t)t.start + m) * p.N + t.n0 + c0;
+            uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.N + t.n0 + c0;
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -310,14 +326,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
             st_v4(out, make_uint4(w[0], w[1], w[2], w[3]));
             st_v4(out + 16, make_uint4(w[4], w[5], w[6], w[7]));
           } else {
-            store32<kForm, kAct>(p, t.e, (int64_t)t.start + m, t.n0 + c0, v, u);
+            store32<kForm, kAct>(p, t.e, row, t.n0 + c0, v, u);
           }
         }
         __syncwarp();
-      }
-      if (quantised && in) {
-        const int64_t row = (int64_t)t.start + m, owner = row / p.seg.cap;
-        p.out_scales[(owner * (p.N / kFp8Block) + t.n0 / kFp8Block) * p.seg.cap + (row - owner * p.seg.cap)] = (uint8_t)byte;
       }
     }
   }
