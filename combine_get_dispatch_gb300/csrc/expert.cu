@@ -62,13 +62,15 @@ __global__ void __launch_bounds__(kThreads) k_glu_slope(SlopeParams p) {
 }
 
 // dpre = dy * act'(pre) and dbias = its sum over the expert's rows.  A cluster of
-// kSplit CTAs owns 64 columns of one expert: 8 threads a row, every kSplit-th
-// group of 128 rows a CTA, the row sums in 32 bits (before dpre is rounded), added
-// over the CTA's threads and then over the cluster in a fixed order.
+// kSplit CTAs owns 64 columns of one expert: 8 threads a row, 32 rows a CTA and
+// step, four steps' loads at a time, the sums in 32 bits (before dpre is
+// rounded), added over the CTA's rows and then over the cluster in a fixed order.
+// Memory bounds it (50288 x 4072, sum only: read once, 410 MB).
 template <int kAct, int kSplit>
-__global__ void __launch_bounds__(1024) k_linear_slope(SlopeParams p) {
-  __shared__ float part[128][65];
-  const int c8 = threadIdx.x & 7, rg = threadIdx.x >> 3;
+__global__ void __launch_bounds__(kThreads) k_linear_slope(SlopeParams p) {
+  constexpr int kRows = kThreads / 8, kSteps = 4;
+  __shared__ float part[kThreads / kWarp][64];
+  const int c8 = threadIdx.x & 7, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = blockIdx.x % kSplit;
   const int c = blockIdx.x / kSplit * 64 + c8 * 8;
   const int e = blockIdx.y;
@@ -77,42 +79,61 @@ __global__ void __launch_bounds__(1024) k_linear_slope(SlopeParams p) {
   const Segment s = segment_of(seg, e);
   float sum[8] = {};
   if (c < p.N) {
-    for (int i = share * 128 + rg; i < s.count; i += kSplit * 128) {
-      const int64_t at = (s.start + i) * p.N + c;
-      const uint4 d = *reinterpret_cast<const uint4*>(p.dy + at);
-      uint4 z = make_uint4(0, 0, 0, 0);
-      if (kAct != EP_ACT_NONE) z = *reinterpret_cast<const uint4*>(p.pre + at);
-      const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, zw[4] = {z.x, z.y, z.z, z.w};
-      uint32_t o[4];
+    for (int64_t i0 = share * kRows + (threadIdx.x >> 3); i0 < s.count; i0 += kSplit * kRows * kSteps) {
+      uint4 d[kSteps], z[kSteps];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v, s0, s1;
-        act_both<kAct>(bf16_lo(zw[q]), v, s0);
-        act_both<kAct>(bf16_hi(zw[q]), v, s1);
-        const float d0 = bf16_lo(dw[q]) * s0, d1 = bf16_hi(dw[q]) * s1;
-        sum[2 * q] += d0;
-        sum[2 * q + 1] += d1;
-        o[q] = pack_bf16x2(d0, d1);
+      for (int k = 0; k < kSteps; ++k) {
+        const int64_t i = i0 + k * kSplit * kRows;
+        d[k] = z[k] = make_uint4(0, 0, 0, 0);
+        if (i < s.count) {
+          const int64_t at = (s.start + i) * p.N + c;
+          d[k] = *reinterpret_cast<const uint4*>(p.dy + at);
+          if (kAct != EP_ACT_NONE) z[k] = *reinterpret_cast<const uint4*>(p.pre + at);
+        }
       }
-      if (kAct != EP_ACT_NONE) st_v4(p.out + at, make_uint4(o[0], o[1], o[2], o[3]));
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int64_t i = i0 + k * kSplit * kRows;
+        const uint32_t dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w}, zw[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v, s0, s1;
+          act_both<kAct>(bf16_lo(zw[q]), v, s0);
+          act_both<kAct>(bf16_hi(zw[q]), v, s1);
+          const float d0 = bf16_lo(dw[q]) * s0, d1 = bf16_hi(dw[q]) * s1;
+          sum[2 * q] += d0;
+          sum[2 * q + 1] += d1;
+          o[q] = pack_bf16x2(d0, d1);
+        }
+        if (kAct != EP_ACT_NONE && i < s.count) st_v4(p.out + (s.start + i) * p.N + c, make_uint4(o[0], o[1], o[2], o[3]));
+      }
     }
   }
   if (p.dbias == nullptr) return;   // the same for every CTA of the cluster
 #pragma unroll
-  for (int q = 0; q < 8; ++q) part[rg][c8 * 8 + q] = sum[q];
+  for (int q = 0; q < 8; ++q) {
+    sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 8);
+    sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 16);
+    if (lane < 8) part[warp][c8 * 8 + q] = sum[q];
+  }
   __syncthreads();
-  for (int half = 64; half > 0; half >>= 1) {
-    for (int i = threadIdx.x; i < half * 64; i += 1024) part[i / 64][i % 64] += part[i / 64 + half][i % 64];
-    __syncthreads();
+  float all = 0.0f;
+  if (threadIdx.x < 64) {
+#pragma unroll
+    for (int w = 0; w < kThreads / kWarp; ++w) all += part[w][threadIdx.x];
   }
-  if (kSplit > 1) cluster_sync();
   const int col = blockIdx.x / kSplit * 64 + threadIdx.x;
-  if (share == 0 && threadIdx.x < 64 && col < p.N) {
-    float all = part[0][threadIdx.x];
-    for (int r = 1; r < kSplit; ++r) all += ld_cluster_f32(map_to_rank(smem_addr(&part[0][threadIdx.x]), r));
-    p.dbias[(int64_t)e * p.N + col] = __float2bfloat16_rn(all);
+  if (kSplit > 1) {
+    __syncthreads();
+    if (threadIdx.x < 64) part[0][threadIdx.x] = all;
+    cluster_sync();
+    if (share == 0 && threadIdx.x < 64) {
+      for (int r = 1; r < kSplit; ++r) all += ld_cluster_f32(map_to_rank(smem_addr(&part[0][threadIdx.x]), r));
+    }
+    cluster_sync();   // no CTA leaves while its sums are read
   }
-  if (kSplit > 1) cluster_sync();   // no CTA leaves while its sums are read
+  if (share == 0 && threadIdx.x < 64 && col < p.N) p.dbias[(int64_t)e * p.N + col] = __float2bfloat16_rn(all);
 }
 
 template <int kAct>
@@ -128,7 +149,7 @@ template <int kAct, int kSplit>
 static int launch_linear_slope_t(const SlopeParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.N + 63) / 64 * kSplit, p.seg.E);
-  cfg.blockDim = dim3(1024);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -144,12 +165,17 @@ static int launch_linear_slope_t(const SlopeParams& p, cudaStream_t s) {
   return ep_host::check_launch();
 }
 
-// The rows are split over 8 CTAs where the columns alone leave SMs without one
-// (777 x 2048, one expert: 13.2 us by 32 CTAs).
+// One CTA for 64 columns of an expert where those fill the SMs' 8 places several
+// times; with fewer the rows are split over 2, so that one expert's many rows are
+// not the kernel's time (11088 rows x 272, 224 experts of uneven sizes: 31 us
+// whole, 17 by 2, 24 by 8; 37140 x 1400, 32 even experts: 52, 58-60, 78); with
+// fewer than two an SM over 8 (777 x 2048, one expert: 13.2 us by 32 CTAs, 7.4).
 template <int kAct>
 static int launch_linear_slope(const SlopeParams& p, cudaStream_t s) {
-  const bool split = (int64_t)((p.N + 63) / 64) * p.seg.E < ep_host::num_sms();
-  return split ? launch_linear_slope_t<kAct, 8>(p, s) : launch_linear_slope_t<kAct, 1>(p, s);
+  const int64_t groups = (int64_t)((p.N + 63) / 64) * p.seg.E;
+  const int sms = ep_host::num_sms();
+  if (groups < 2 * sms) return launch_linear_slope_t<kAct, 8>(p, s);
+  return groups < 16 * sms ? launch_linear_slope_t<kAct, 2>(p, s) : launch_linear_slope_t<kAct, 1>(p, s);
 }
 
 static int64_t rows_of(const Segments& s) { return s.cap * (s.psum != nullptr ? s.E / s.E_l : s.E); }

@@ -163,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const bool issue = elect_one();
     const uint32_t stage0 = smem_addr(stages), full0 = map_to_rank(smem_addr(&sh.full[0]), 0);
     uint32_t s = 0, phase = 0;
-    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+    while (next_tile(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       const int half = (t.rows + 15) / 16 * 8;   // rows of the second operand in a CTA
       // copied 32 at a time, or all 128; kDw: 64 columns of d at a time
@@ -237,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const uint32_t b0 = umma_desc_lo(smem_addr(stages) + kOperandBytes, kBMn ? kOperandBytes / 2 : 16);
     constexpr uint32_t kStepA = (kAMn ? 2048 : 32) >> 4, kStepB = (kBMn ? 2048 : 32) >> 4;
     uint32_t s = 0, n = 0, full = 0, cleared = 0;   // parities: a bit per stage
-    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+    while (next_tile(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       if (blocks == 0) continue;
       const uint32_t idesc = umma_idesc_bf16(kTileM, (t.rows + 15) / 16 * 16, kAMn, kBMn);
@@ -289,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // ---------------------------------------------------------------- rows past a segment's end
     int s = 0;
     uint32_t parity = 0;   // bit per stage
-    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+    while (next_tile(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       if (t.count % 16 != 0) {
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sh.landed[s], (parity >> s) & 1, 2 * kWaitNs));
@@ -315,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int mrow = lane & 7, mat = lane >> 3;   // this lane's address in the four 8 x 8 matrices of a store
     // columns of this thread's sums: 16 hh + lane / 4 (+ 8); kGlu: gate and up of column 8 hh + lane / 4
     uint32_t n = 0;
-    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+    while (next_tile(sh.ring, taken, t, ok, lane)) {
       const int blocks = inner_blocks();
       const uint32_t half = n & 1;
       if (blocks > 0) {

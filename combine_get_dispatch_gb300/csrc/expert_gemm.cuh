@@ -116,33 +116,18 @@ struct TileRing {
   Tile tiles[kTiles];
 };
 
-// Takes the next tile; false past the last one, or (ok false) when the wait ran
-// out.  The caller frees the place with one arrival on *free.
-__device__ __forceinline__ bool take_tile(TileRing& ring, uint32_t& taken, Tile& t, bool& ok, uint64_t*& free) {
+// The next tile for a converged warp; false past the last one, or (ok false) when
+// the wait ran out.
+__device__ __forceinline__ bool next_tile(TileRing& ring, uint32_t& taken, Tile& t, bool& ok, int lane) {
+  if (!ok) return false;
   const uint32_t i = taken % kTiles;
-  ok = mbar_wait_bounded(&ring.full[i], (taken / kTiles) & 1, kTileWaitNs);
+  ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ring.full[i], (taken / kTiles) & 1, kTileWaitNs));
   if (!ok) return false;
   t = ring.tiles[i];
-  free = &ring.empty[i];
   ++taken;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ring.empty[i]);
   return t.e >= 0;
-}
-// One thread alone.
-__device__ __forceinline__ bool next_tile(TileRing& ring, uint32_t& taken, Tile& t, bool& ok) {
-  uint64_t* free;
-  if (!ok) return false;
-  const bool more = take_tile(ring, taken, t, ok, free);
-  if (ok) mbar_arrive(free);
-  return more;
-}
-// A converged warp.
-__device__ __forceinline__ bool next_tile_warp(TileRing& ring, uint32_t& taken, Tile& t, bool& ok, int lane) {
-  uint64_t* free = nullptr;
-  if (!ok) return false;
-  const bool more = take_tile(ring, taken, t, ok, free);
-  ok = __all_sync(0xffffffffu, ok);
-  if (ok && lane == 0) mbar_arrive(free);
-  return ok && more;
 }
 // The walking warp: tiles first (which is t), first + step, ... until the list
 // ends.

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     const bool issue = elect_one();
     const uint32_t stage0 = smem_addr(stages);
     uint32_t s = 0, phase = 0;
-    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+    while (next_tile(sh.ring, taken, t, ok, lane)) {
       const int boxes = (t.rows + kMxBox - 1) / kMxBox, row = t.start + t.m0;
       for (int kb = 0; kb < blocks; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     const bool issue = elect_one();
     const uint32_t a0 = umma_desc_lo(smem_addr(stages), 16), b0 = umma_desc_lo(smem_addr(stages) + kMxABytes, 16);
     uint32_t s = 0, phase = 0, n = 0;
-    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+    while (next_tile(sh.ring, taken, t, ok, lane)) {
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_empty, (n & 1) ^ 1));
       if (!ok) break;
       ++n;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     int s = 0;
     uint32_t phase = 0;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+    while (next_tile(sh.ring, taken, t, ok, lane)) {
       const int64_t owner = t.start / p.seg.cap;
       const uint8_t* xs = p.a_scales + owner * blocks * p.seg.cap + (t.start - owner * p.seg.cap) + t.m0 + lane;
       const uint8_t* ws[2];
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
     const int first = side * (kCols / 2);
     uint32_t n = 0;
     const uint32_t d = tmem + ((uint32_t)(q * 32) << 16);
-    while (next_tile_warp(sh.ring, taken, t, ok, lane)) {
+    while (next_tile(sh.ring, taken, t, ok, lane)) {
       const int r = q * 32 + lane;
       const bool in = r < t.rows, quantised = kForm == kGlu && p.out_scales != nullptr;
       // with scales the two warps of a row meet below, so they give up together

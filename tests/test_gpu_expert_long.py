@@ -55,6 +55,35 @@ def test_many_tiles(counts, K, N, sms):
         at += n
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("E,N,most", [(3, 200, 2100), (24, 1096, 700), (56, 4104, 300)])
+def test_bias_gradient_split(E, N, most, act):
+    """An expert's rows summed by 8 CTAs, by 2 and by one; uneven segments, none and
+    one row among them.  The slope of SiLU and its product are within 2^-18."""
+    rng = np.random.default_rng(E)
+    counts = rng.integers(0, most, E).tolist()
+    counts[0], counts[1], counts[2] = 0, most, 1
+    dy = normal(counts, N, 1)
+    pre = normal(counts, N, 2) if act != "none" else None
+    dpre = torch.empty_like(dy) if act != "none" else None
+    c, ps = tables(counts)
+    db = torch.full((E, N), -77.0, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((E, N, 8), dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_linear_backward(dy, pre, None, w, c, ps, ep.ACTS[act], dpre, None, None, dbias=db)
+    at = 0
+    for e, n in enumerate(counts):
+        d, e_d = dy[0, at:at + n].double(), 0.0
+        if pre is not None:
+            z = pre[0, at:at + n].double()
+            q = torch.sigmoid(z)
+            e_d = 2.0 ** -18 * d.abs()
+            d = d * (q * (1 + z * (1 - q)))
+            near(dpre[0, at:at + n], d, 2.0 ** -8 * d.abs() + e_d)
+        s = d.sum(0)
+        near(db[e], s, 2.0 ** -8 * s.abs() + (n * 2.0 ** -24 * d.abs() + e_d).sum(0) + 1e-30)
+        at += n
+
+
 def test_a_thousand_experts():
     """1024 experts of 0 to 40 rows on 4 ranks, gated, forward and weights' gradient."""
     rng = np.random.default_rng(4)
