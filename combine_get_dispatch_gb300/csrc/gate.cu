@@ -322,28 +322,37 @@ struct Piece {
 // p.vec: rows are whole 16-byte pieces.
 template <int kG, int kV, bool kBf16>
 __device__ __forceinline__ void gate_pieces(const GateParams& p, bool in, const uint8_t* row, int g, float (&l)[kV]) {
-  constexpr int kP = Piece<kBf16>::kP;
+  constexpr int kP = Piece<kBf16>::kP, kN = kV / kP;
+  if (p.vec) {
+    const uint32_t none = kBf16 ? 0xff80ff80u : 0xff800000u;
+    uint4 x[kN];
 #pragma unroll
-  for (int i = 0; i < kV / kP; ++i) {
-    const int e0 = (i * kG + g) * kP;
-    if (p.vec) {
-      const uint32_t none = kBf16 ? 0xff80ff80u : 0xff800000u;
-      uint4 x = make_uint4(none, none, none, none);
-      if (in && e0 < p.E) x = __ldg(reinterpret_cast<const uint4*>(row + g * 16 + i * kG * 16));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int i = 0; i < kN; ++i) {
+      x[i] = make_uint4(none, none, none, none);
+      if (in && (i * kG + g) * kP < p.E) x[i] = __ldg(reinterpret_cast<const uint4*>(row + g * 16 + i * kG * 16));
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
       for (int c = 0; c < kP; ++c)
         l[i * kP + c] = gate_clean(kBf16 ? ((c & 1) ? bf16_hi(w[c / 2]) : bf16_lo(w[c / 2])) : __uint_as_float(w[c % 4]));
-    } else {
+    }
+  } else {
 #pragma unroll
-      for (int c = 0; c < kP; ++c) l[i * kP + c] = in && e0 + c < p.E ? gate_load<kBf16>(row, e0 + c) : kNone;
+    for (int i = 0; i < kV; ++i) {
+      const int e = (i / kP * kG + g) * kP + i % kP;
+      l[i] = in && e < p.E ? gate_load<kBf16>(row, e) : kNone;
     }
   }
 }
 
 // kG lanes (8, 16 or 32) hold a token's logits, up to 32 each, so that a warp works
-// on several tokens at once (one warp a token: 22 us for 32768 x 256).  Every lane stores the gradient of its own logits (-p inner, or zero); then the
-// lanes of the chosen experts store those whole.
+// on several tokens at once (32768 x 256 fp32: 14.4 us, 4.9 TB/s; 16 lanes a
+// token 15.5, a warp 18; memory bounds it).  All loads are issued before the
+// first is used (one after another they took 22 us).  Every
+// lane stores the gradient of its own logits (-p inner, or zero); then the lanes
+// of the chosen experts store those whole.
 template <int kG, int kV, bool kBf16, bool kTopk>
 __global__ void __launch_bounds__(kBackwardThreads, kBackwardCtas) k_gate_backward(GateParams p) {
   constexpr int kTokens = kWarp / kG, kP = Piece<kBf16>::kP;
@@ -353,24 +362,27 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardCtas) k_gate_backwa
   for (int64_t t0 = warp0 * kTokens; t0 < p.T; t0 += nwarps * kTokens) {
     const int64_t t = t0 + token;
     const bool in = t < p.T;
-    int my_idx = -1;   // of slot g (k <= kG)
-    float grad = 0.0f, chosen = kNone;
+    // every load that waits for nothing first: the slot's id and gradient, the row
+    int64_t id = -1;   // of slot g (k <= kG)
+    float grad = 0.0f;
     if (in && g < p.k) {
-      const int64_t id = p.idx[t * p.k + g];
-      if (id < -1 || id >= p.E)
-        set_status(p.status, EP_ERR_INVALID_ARG);
-      else
-        my_idx = (int)id;
-      if (my_idx >= 0) {
-        grad = p.grad[t * p.k + g];
-        chosen = gate_load<kBf16>(p.logits, t * p.E + my_idx);
-      }
+      id = p.idx[t * p.k + g];
+      grad = p.grad[t * p.k + g];
+    }
+    float l[kV];
+    if (!kTopk)
+      gate_pieces<kG, kV, kBf16>(p, in, static_cast<const uint8_t*>(p.logits) + t * p.E * (kBf16 ? 2 : 4), g, l);
+    int my_idx = -1;
+    float chosen = kNone;
+    if (id < -1 || id >= p.E)
+      set_status(p.status, EP_ERR_INVALID_ARG);
+    else if (id >= 0) {
+      my_idx = (int)id;
+      chosen = gate_load<kBf16>(p.logits, t * p.E + my_idx);
     }
     if (chosen == kNone) grad = 0.0f;
-    float l[kV];
     float best = chosen;
     if (!kTopk) {
-      gate_pieces<kG, kV, kBf16>(p, in, static_cast<const uint8_t*>(p.logits) + t * p.E * (kBf16 ? 2 : 4), g, l);
 #pragma unroll
       for (int i = 0; i < kV; ++i) best = fmaxf(best, l[i]);
     }
