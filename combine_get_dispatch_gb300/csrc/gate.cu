@@ -135,12 +135,25 @@ __device__ __forceinline__ int gate_place_exact(const float* logits, const int* 
   return place;
 }
 
-// Writes a logit and its expert (32 words on) where the logit is a candidate.
-__device__ __forceinline__ void gate_put(uint32_t at, float l, float least, int expert) {
+// Writes a logit and its expert (32 words on) where the logit is a candidate, and
+// moves on.
+__device__ __forceinline__ void gate_put(uint32_t& at, float l, float least, int expert) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ge.f32 p, %1, %2;\n @p st.shared.f32 [%0], %1;\n @p st.shared.u32 [%0 + 128], %3;\n}\n" ::"r"(at),
-      "f"(l), "f"(least), "r"(expert)
+      "{\n .reg .pred p;\n setp.ge.f32 p, %1, %2;\n @p st.shared.f32 [%0], %1;\n @p st.shared.u32 [%0 + 128], %3;\n"
+      " @p add.u32 %0, %0, 4;\n}\n"
+      : "+r"(at)
+      : "f"(l), "f"(least), "r"(expert)
       : "memory");
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int warp_scan(int v) {
+#pragma unroll
+  for (int o = 1; o < kWarp; o <<= 1)
+    asm volatile("{\n .reg .u32 r;\n .reg .pred p;\n shfl.sync.up.b32 r|p, %0, %1, 0, 0xffffffff;\n @p add.u32 %0, %0, r;\n}\n"
+                 : "+r"(v)
+                 : "r"(o));
+  return v;
 }
 
 // A finite bf16 logit with its expert in the 16 bits below it: equal logits (and
@@ -211,8 +224,9 @@ __device__ __forceinline__ float gate_bound(float best, int k, int lane) {
 // a list, one to a lane, and each counts the larger ones.  Equal logits, in the
 // order of their experts, are looked at only where they have left a gap in the
 // places; bf16 logits, often equal, are made unique.  Rows where more than 32
-// remain take their choices one round at a time.  Issue slots bound it: about 380
-// instructions a token, 59.5 us for 131072 x 256 (21.7 us to read and write them).
+// remain take their choices one round at a time.  Issue slots bound it: about 345
+// instructions a token, 55.3 us for 131072 x 256 (21.7 us to read and write them;
+// places in the list from a ballot a logit: 380 instructions, 59.4 us).
 // Slower: k rounds of a reduction and a ballot over the list (63.5 us); 8 lanes a
 // token with 32 logits each (99 us: registers for half the warps).
 template <int kV, bool kBf16, bool kTopk>
@@ -221,7 +235,7 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
   const int lane = threadIdx.x & 31;
   float* list = reinterpret_cast<float*>(lists[threadIdx.x >> 5]);
   const int* experts = reinterpret_cast<const int*>(list + kWarp);
-  const uint32_t list_at = smem_addr(list), lower = lanemask_lt();
+  const uint32_t list_at = smem_addr(list);
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   for (int64_t t = warp0; t < p.T; t += nwarps) {
@@ -233,12 +247,21 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
     const float m = gate_base(warp_max(best));
     // at least the type's lowest value, so that -inf is no candidate
     const float least = fmaxf(kLowest, p.k <= 8 ? gate_bound8(best) : gate_bound(best, p.k, lane));
-    uint32_t who[kV];
-    int all = 0;
+    int before = 0, all = 0;   // candidates of the lanes below, of all
+    if (kV <= 2) {   // a ballot a logit: 65536 x 64, 21.5 us against 22.5 by a scan; from 4 logits on a scan
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      who[i] = __ballot_sync(0xffffffffu, l[i] >= least);
-      all += __popc(who[i]);
+      for (int i = 0; i < kV; ++i) {
+        const uint32_t who = __ballot_sync(0xffffffffu, l[i] >= least);
+        before += __popc(who & lanemask_lt());
+        all += __popc(who);
+      }
+    } else {
+      int own = 0;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) own += l[i] >= least ? 1 : 0;
+      const int upto = warp_scan(own);
+      before = upto - own;
+      all = __shfl_sync(0xffffffffu, upto, kWarp - 1);
     }
     float total = 0.0f;
     if (!kTopk) {
@@ -258,12 +281,9 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
       __syncwarp();
       list[lane] = kNone;
       __syncwarp();
-      uint32_t at = list_at;
+      uint32_t at = list_at + 4 * before;
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        gate_put(at + 4 * __popc(who[i] & lower), l[i], least, lane * kV + i);
-        at += 4 * __popc(who[i]);
-      }
+      for (int i = 0; i < kV; ++i) gate_put(at, l[i], least, lane * kV + i);
       __syncwarp();
       my_l = list[lane];
       my_idx = experts[lane];
