@@ -16,7 +16,11 @@
 namespace ep {
 
 constexpr int kForwardThreads = 256, kBackwardThreads = 128;
-constexpr int kForwardCtas = 6, kBackwardCtas = 8;   // of an SM
+constexpr int kBackwardCtas = 8;   // of an SM
+// Rows of up to 256 logits are loaded one ahead (131072 x 256 53.2 us, 55.3
+// without); longer ones take too many registers for it (65536 x 512 55.3, 57-63 with).
+__host__ __device__ constexpr bool row_ahead(int logits) { return logits <= 8; }   // of a lane
+__host__ __device__ constexpr int forward_ctas(int logits) { return row_ahead(logits) ? 5 : 6; }
 
 struct GateParams {
   const void* logits;
@@ -67,43 +71,57 @@ __device__ __forceinline__ float gate_load(const void* logits, int64_t at) {
 }
 
 // The logits of a lane's kV experts, lane * kV on, of the row that starts at
-// `row` (-inf past its end); vec: rows start on 16 bytes and E is a multiple of
-// kV.
+// `row` (-inf past its end), as they are stored; vec: rows start on 16 bytes and E
+// is a multiple of kV.
 template <int kV, bool kBf16>
-__device__ __forceinline__ void gate_row(const GateParams& p, int64_t row, int lane, float (&l)[kV]) {
-  constexpr int kWords = kV * (kBf16 ? 2 : 4) / 4;   // 32-bit words a lane reads
-  const int e0 = lane * kV;
-  if (p.vec) {
-    uint32_t w[kWords];
+struct Row {
+  static constexpr int kWords = kV * (kBf16 ? 2 : 4) / 4;   // 32-bit words a lane reads
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const GateParams& p, int64_t row, int lane) {
+    const int e0 = lane * kV;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = kBf16 ? 0xff80ff80u : 0xff800000u;   // -inf
-    if (e0 < p.E) {
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.logits) + (row + e0) * (kBf16 ? 2 : 4));
-      if (kWords >= 4) {
+    if (p.vec) {
+      if (e0 < p.E) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.logits) + (row + e0) * (kBf16 ? 2 : 4));
+        if (kWords >= 4) {
 #pragma unroll
-        for (int i = 0; i < kWords / 4; ++i) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-          w[4 * i] = v.x;
-          w[4 * i + 1] = v.y;
-          w[4 * i + 2] = v.z;
-          w[4 * i + 3] = v.w;
+          for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+          }
+        } else if (kWords == 2) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+          w[0] = v.x;
+          w[kWords - 1] = v.y;
+        } else {
+          w[0] = __ldg(src);
         }
-      } else if (kWords == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-        w[0] = v.x;
-        w[kWords - 1] = v.y;
-      } else {
-        w[0] = __ldg(src);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        if (e0 + i < p.E) {
+          if (kBf16) {
+            const uint32_t u = static_cast<const uint16_t*>(p.logits)[row + e0 + i];
+            w[i / 2] = (i & 1) ? (w[i / 2] & 0xffffu) | u << 16 : (w[i / 2] & 0xffff0000u) | u;
+          } else {
+            w[kBf16 ? 0 : i] = static_cast<const uint32_t*>(p.logits)[row + e0 + i];
+          }
+        }
       }
     }
+  }
+  __device__ __forceinline__ void get(float (&l)[kV]) const {
 #pragma unroll
     for (int i = 0; i < kV; ++i)
       l[i] = gate_clean(kBf16 ? ((i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) : __uint_as_float(w[kBf16 ? 0 : i]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < kV; ++i) l[i] = e0 + i < p.E ? gate_load<kBf16>(p.logits, row + e0 + i) : kNone;
   }
-}
+};
 
 // The value to subtract, from the row's largest logit: itself, or 0 where nothing
 // can be chosen.
@@ -225,12 +243,12 @@ __device__ __forceinline__ float gate_bound(float best, int k, int lane) {
 // order of their experts, are looked at only where they have left a gap in the
 // places; bf16 logits, often equal, are made unique.  Rows where more than 32
 // remain take their choices one round at a time.  Issue slots bound it: about 345
-// instructions a token, 55.3 us for 131072 x 256 (21.7 us to read and write them;
-// places in the list from a ballot a logit: 380 instructions, 59.4 us).
+// instructions a token, 53.2 us for 131072 x 256 (21.7 us to read and write them;
+// places in the list from a ballot a logit: 380 instructions, 4 us more).
 // Slower: k rounds of a reduction and a ballot over the list (63.5 us); 8 lanes a
 // token with 32 logits each (99 us: registers for half the warps).
 template <int kV, bool kBf16, bool kTopk>
-__global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k_gate(GateParams p) {
+__global__ void __launch_bounds__(kForwardThreads, row_ahead(kV) ? forward_ctas(kV) : 1) k_gate(GateParams p) {
   __shared__ float4 lists[kForwardThreads / kWarp][2 * kWarp / 4];   // 32 logits, their 32 experts
   const int lane = threadIdx.x & 31;
   float* list = reinterpret_cast<float*>(lists[threadIdx.x >> 5]);
@@ -238,9 +256,13 @@ __global__ void __launch_bounds__(kForwardThreads, kV <= 8 ? kForwardCtas : 1) k
   const uint32_t list_at = smem_addr(list);
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  Row<kV, kBf16> row;
+  if (row_ahead(kV) && warp0 < p.T) row.load(p, warp0 * p.E, lane);
   for (int64_t t = warp0; t < p.T; t += nwarps) {
     float l[kV];
-    gate_row<kV, kBf16>(p, t * p.E, lane, l);
+    if (!row_ahead(kV)) row.load(p, t * p.E, lane);
+    row.get(l);
+    if (row_ahead(kV) && t + nwarps < p.T) row.load(p, (t + nwarps) * p.E, lane);   // arrives while this one is worked on
     float best = l[0];
 #pragma unroll
     for (int i = 1; i < kV; ++i) best = fmaxf(best, l[i]);
@@ -486,7 +508,7 @@ template <int kV, bool kBf16, bool kTopk>
 static int launch_forward_t(const GateParams& p, cudaStream_t stream) {
   constexpr int kTokens = kForwardThreads / kWarp;
   const int64_t want = (p.T + kTokens - 1) / kTokens;
-  const int grid = (int)std::min<int64_t>(want, (int64_t)ep_host::num_sms() * kForwardCtas);
+  const int grid = (int)std::min<int64_t>(want, (int64_t)ep_host::num_sms() * forward_ctas(kV));
   k_gate<kV, kBf16, kTopk><<<grid, kForwardThreads, 0, stream>>>(p);
   ep_host::count_launch();
   return ep_host::check_launch();
