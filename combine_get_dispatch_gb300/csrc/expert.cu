@@ -7,7 +7,7 @@
 namespace ep {
 
 constexpr int kThreads = 256;
-constexpr int kSlopeRows = 32;   // rows a CTA of k_glu_slope takes at a time
+constexpr int kSlopeRows = 32, kSlopeCols = 512, kSlopeCtas = 4;   // a piece of k_glu_slope; CTAs of an SM
 
 struct SlopeParams {
   Segments seg;
@@ -19,17 +19,20 @@ struct SlopeParams {
 };
 
 // dgu = (dh * up * act'(gate), dh * act(gate)) over the rows of every segment,
-// 8 columns a thread.  A CTA takes 32 rows of an expert at a time from the list
-// of all of them, whatever the experts' shares are (one grid row an expert took
-// 97 us where one of 32 experts had a quarter of 12288 rows; read and written
-// once, 174 MB, 26 us at the copy rate).
+// 8 columns a thread, two rows' loads at a time.  A CTA takes 32 rows x 512
+// columns of an expert from the list of all of them, whatever the experts' shares
+// are (one grid row an expert took 97 us where one of 32 experts had a quarter of
+// 12288 rows x 1416; whole rows, one load at a time, 33, and 72 us for 96 rows x
+// 3984 of 16 experts; now 28 and 14).  Memory bounds it: 65536 x 2048 198 us, 6.8 TB/s.
 template <int kAct>
-__global__ void __launch_bounds__(kThreads) k_glu_slope(SlopeParams p) {
+__global__ void __launch_bounds__(kThreads, kSlopeCtas) k_glu_slope(SlopeParams p) {
+  constexpr int kWide = kSlopeCols / 8, kStep = kThreads / kWide, kLoads = 2;
   __shared__ Tile next[2];
-  const int vec = p.N / 8, lane = threadIdx.x & 31;
+  __shared__ TileWalk walks[kWarp];   // not in registers, which the rows need
+  const int lane = threadIdx.x & 31;
+  TileWalk& walk = walks[lane];
   pdl_wait();
-  TileWalk walk;
-  if (threadIdx.x < 32) walk.begin(p.seg, -1, kSlopeRows, 1, 0, blockIdx.x == 0, lane);
+  if (threadIdx.x < 32) walk.begin(p.seg, -1, kSlopeRows, (p.N + kSlopeCols - 1) / kSlopeCols, kSlopeCols, blockIdx.x == 0, lane);
   for (int64_t at = blockIdx.x, n = 0;; at += gridDim.x, ++n) {
     if (threadIdx.x < 32) {
       const Tile t = walk.at(at, lane);
@@ -38,25 +41,40 @@ __global__ void __launch_bounds__(kThreads) k_glu_slope(SlopeParams p) {
     __syncthreads();
     const Tile t = next[n & 1];
     if (t.e < 0) break;
-    for (int it = threadIdx.x; it < t.rows * vec; it += kThreads) {
-      const int64_t row = (int64_t)t.start + t.m0 + it / vec;
-      const int64_t c = (it % vec) * 8;
-      const uint4 d = *reinterpret_cast<const uint4*>(p.dy + row * p.N + c);
-      const uint4 g = *reinterpret_cast<const uint4*>(p.pre + row * 2 * p.N + c);
-      const uint4 u = *reinterpret_cast<const uint4*>(p.pre + (row * 2 + 1) * p.N + c);
-      const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-      uint32_t og[4], ou[4];
+    const int c = t.n0 + (int)(threadIdx.x % kWide) * 8;
+    if (c >= p.N) continue;
+    for (int r0 = threadIdx.x / kWide; r0 < t.rows; r0 += kLoads * kStep) {
+      uint4 d[kLoads], g[kLoads], u[kLoads];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v0, s0, v1, s1;
-        act_both<kAct>(bf16_lo(gw[i]), v0, s0);
-        act_both<kAct>(bf16_hi(gw[i]), v1, s1);
-        const float d0 = bf16_lo(dw[i]), d1 = bf16_hi(dw[i]);
-        og[i] = pack_bf16x2(d0 * bf16_lo(uw[i]) * s0, d1 * bf16_hi(uw[i]) * s1);
-        ou[i] = pack_bf16x2(d0 * v0, d1 * v1);
+      for (int k = 0; k < kLoads; ++k) {
+        d[k] = g[k] = u[k] = make_uint4(0, 0, 0, 0);
+        if (r0 + k * kStep < t.rows) {
+          const int64_t row = (int64_t)t.start + t.m0 + r0 + k * kStep;
+          d[k] = *reinterpret_cast<const uint4*>(p.dy + row * p.N + c);
+          g[k] = *reinterpret_cast<const uint4*>(p.pre + row * 2 * p.N + c);
+          u[k] = *reinterpret_cast<const uint4*>(p.pre + (row * 2 + 1) * p.N + c);
+        }
       }
-      st_v4(p.out + row * 2 * p.N + c, make_uint4(og[0], og[1], og[2], og[3]));
-      st_v4(p.out + (row * 2 + 1) * p.N + c, make_uint4(ou[0], ou[1], ou[2], ou[3]));
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int64_t row = (int64_t)t.start + t.m0 + r0 + k * kStep;
+        const uint32_t dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w}, gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+        const uint32_t uw[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        uint32_t og[4], ou[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v0, s0, v1, s1;
+          act_both<kAct>(bf16_lo(gw[i]), v0, s0);
+          act_both<kAct>(bf16_hi(gw[i]), v1, s1);
+          const float d0 = bf16_lo(dw[i]), d1 = bf16_hi(dw[i]);
+          og[i] = pack_bf16x2(d0 * bf16_lo(uw[i]) * s0, d1 * bf16_hi(uw[i]) * s1);
+          ou[i] = pack_bf16x2(d0 * v0, d1 * v1);
+        }
+        if (r0 + k * kStep < t.rows) {
+          st_v4(p.out + row * 2 * p.N + c, make_uint4(og[0], og[1], og[2], og[3]));
+          st_v4(p.out + (row * 2 + 1) * p.N + c, make_uint4(ou[0], ou[1], ou[2], ou[3]));
+        }
+      }
     }
   }
 }
@@ -138,8 +156,8 @@ __global__ void __launch_bounds__(kThreads) k_linear_slope(SlopeParams p) {
 
 template <int kAct>
 static int launch_glu_slope(const SlopeParams& p, int64_t rows, cudaStream_t s) {
-  const int64_t tiles = rows / kSlopeRows + p.seg.E;
-  const int grid = (int)std::min<int64_t>(tiles, ep_host::grid_cap(8));
+  const int64_t tiles = (rows / kSlopeRows + p.seg.E) * ((p.N + kSlopeCols - 1) / kSlopeCols);
+  const int grid = (int)std::min<int64_t>(tiles, ep_host::grid_cap(kSlopeCtas));
   if (ep_host::launch_dependent(k_glu_slope<kAct>, grid, kThreads, 0, s, p) != EP_OK) return EP_ERR_CUDA;
   ep_host::count_launch();
   return ep_host::check_launch();
@@ -169,12 +187,12 @@ static int launch_linear_slope_t(const SlopeParams& p, cudaStream_t s) {
 // times; with fewer the rows are split over 2, so that one expert's many rows are
 // not the kernel's time (11088 rows x 272, 224 experts of uneven sizes: 31 us
 // whole, 17 by 2, 24 by 8; 37140 x 1400, 32 even experts: 52, 58-60, 78); with
-// fewer than two an SM over 8 (777 x 2048, one expert: 13.2 us by 32 CTAs, 7.4).
+// at most one an SM over 8 (777 x 2048, one expert: 13.2 us by 32 CTAs, 7.4).
 template <int kAct>
 static int launch_linear_slope(const SlopeParams& p, cudaStream_t s) {
   const int64_t groups = (int64_t)((p.N + 63) / 64) * p.seg.E;
   const int sms = ep_host::num_sms();
-  if (groups < 2 * sms) return launch_linear_slope_t<kAct, 8>(p, s);
+  if (groups <= sms) return launch_linear_slope_t<kAct, 8>(p, s);
   return groups < 16 * sms ? launch_linear_slope_t<kAct, 2>(p, s) : launch_linear_slope_t<kAct, 1>(p, s);
 }
 
