@@ -242,9 +242,9 @@ __device__ __forceinline__ float gate_bound(float best, int k, int lane) {
 // a list, one to a lane, and each counts the larger ones.  Equal logits, in the
 // order of their experts, are looked at only where they have left a gap in the
 // places; bf16 logits, often equal, are made unique.  Rows where more than 32
-// remain take their choices one round at a time.  Issue slots bound it: about 345
+// remain take their choices one round at a time.  Issue slots bound it: about 355
 // instructions a token, 53.2 us for 131072 x 256 (21.7 us to read and write them;
-// places in the list from a ballot a logit: 380 instructions, 4 us more).
+// places in the list from a ballot a logit: 35 more, 4 us).
 // Slower: k rounds of a reduction and a ballot over the list (63.5 us); 8 lanes a
 // token with 32 logits each (99 us: registers for half the warps).
 template <int kV, bool kBf16, bool kTopk>
