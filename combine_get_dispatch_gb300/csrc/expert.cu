@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kThreads, kSlopeCtas) k_glu_slope(SlopeParams 
   __shared__ TileWalk walks[kWarp];   // not in registers, which the rows need
   const int lane = threadIdx.x & 31;
   TileWalk& walk = walks[lane];
+  pdl_launch_dependents();
   pdl_wait();
   if (threadIdx.x < 32) walk.begin(p.seg, -1, kSlopeRows, (p.N + kSlopeCols - 1) / kSlopeCols, kSlopeCols, blockIdx.x == 0, lane);
   for (int64_t at = blockIdx.x, n = 0;; at += gridDim.x, ++n) {
@@ -94,6 +95,8 @@ __global__ void __launch_bounds__(kThreads) k_linear_slope(SlopeParams p) {
   const int e = blockIdx.y;
   Segments seg = p.seg;
   if (blockIdx.x != 0) seg.status = nullptr;
+  pdl_launch_dependents();   // the products come up while this runs
+  pdl_wait();
   const Segment s = segment_of(seg, e);
   float sum[8] = {};
   if (c < p.N) {
@@ -169,12 +172,14 @@ static int launch_linear_slope_t(const SlopeParams& p, cudaStream_t s) {
   cfg.gridDim = dim3((p.N + 63) / 64 * kSplit, p.seg.E);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kSplit;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, k_linear_slope<kAct, kSplit>, p) != cudaSuccess) {
     cudaGetLastError();
     return EP_ERR_CUDA;
