@@ -246,7 +246,8 @@ static int check_expert(const int32_t* counts, const int64_t* psum, int R, int E
   if (K <= 0 || N <= 0 || K % unit != 0 || N % unit != 0 || K > (1 << 24) || N > (1 << 24)) return EP_ERR_INVALID_ARG;
   const int64_t lim = (int64_t)1 << 31;
   const int64_t owners = psum != nullptr ? R : E;
-  if (cap_rows >= lim / owners || (int64_t)E * K >= lim || (int64_t)E * N >= lim / 2) return EP_ERR_INVALID_ARG;
+  // coordinates run past a segment's end, by less than a tile, without leaving 31 bits
+  if (cap_rows > (lim - (1 << 16)) / owners || (int64_t)E * K >= lim || (int64_t)E * N >= lim / 2) return EP_ERR_INVALID_ARG;
   if (counts == nullptr) return EP_ERR_INVALID_ARG;
   return EP_OK;
 }

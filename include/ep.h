@@ -388,8 +388,8 @@ int ep_gate_topk_backward(const void* logits, int dtype, const int64_t* topk_idx
  * counts [E] int32.  Rows outside every segment are neither used nor written.
  * A segment that leaves the buffer is cut at cap_rows (EP_ERR_CAPACITY in
  * *status).  Sums run in 32 bits; each bf16 output is rounded once.
- * Limits: widths are multiples of 8 (128 with FP8), the total of rows and
- * E * width below 2^31, x / w / outputs 16-byte aligned, E <= 1024.
+ * Limits: widths are multiples of 8 (128 with FP8), all segments' rows
+ * together at most 2^31 - 2^16, E * width below 2^31, x / w / outputs 16-byte aligned, E <= 1024.
  * With EP_FP8_E4M3_UE8M0, x is E4M3 with the scales dispatch writes
  * ([R, K/128, cap_rows], packed [R, E_l, K/128, cap_rows]) and w is E4M3 with
  * one ue8m0 byte per 128 x 128 block ([E, N/128, K/128]; glu

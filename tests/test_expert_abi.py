@@ -24,6 +24,14 @@ def test_glu_refuses(bad):
     assert ep.ep_launch_count() == before
 
 
+@pytest.mark.parametrize("R,E,psum", [(1, 1, FAKE), (2, 4, FAKE), (2, 4, None), (1024, 1024, None)])
+def test_rows_stay_in_31_bits(R, E, psum):
+    """One row more than 2^31 - 2^16 over all segments' buffers is refused."""
+    cap = ((1 << 31) - (1 << 16)) // (E if psum is None else R) + 1
+    assert glu(R=R, E=E, psum=psum, cap=cap) == ep.EP_ERR_INVALID_ARG
+    assert glu(R=R, E=E, psum=psum, cap=0) == ep.EP_OK
+
+
 def linear(R=1, E=1, K=64, N=64, cap=8, act=0, x=FAKE, w=FAKE, y=FAKE, bias=None, residual=None, pre=None):
     return ep.load().ep_expert_linear(x, None, w, None, 0, bias, residual, FAKE, FAKE, R, E, K, N, cap, act, y, pre, None, None)
 
