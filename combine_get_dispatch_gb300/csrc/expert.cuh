@@ -1,5 +1,5 @@
-// expert.cuh -- what the expert kernels share: segments of a receive layout,
-// the tile table over them, activations.
+// expert.cuh -- what the expert kernels share: the segments of a receive layout
+// and the activations.
 #pragma once
 
 #include "ep_common.cuh"

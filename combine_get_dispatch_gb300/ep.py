@@ -485,14 +485,17 @@ def _expert_rows(lead, E, counts, psum, status):
     R, cap = lead[0], lead[-1]
     if R == 0 or E % R != 0:
         raise ValueError(f"{E} experts on {R} ranks")
-    if tuple(lead) != ((R, cap) if psum is not None else (R, E // R, cap)):
+    if lead != ((R, cap) if psum is not None else (R, E // R, cap)):
         raise ValueError(f"rows: leading shape {tuple(lead)}, expected (R, cap_rows) with psum, "
                          "(R, E_l, cap_rows) without")
     _need(counts, torch.int32, name="counts")
-    if tuple(counts.shape) not in ((E,), (R, E // R)):
-        raise ValueError(f"counts: shape {tuple(counts.shape)}, expected {(E,)} or {(R, E // R)}")
-    _need(psum, torch.int64, (R, E // R + 1), "psum", optional=True)
-    _need(status, torch.int32, (1,), "status", optional=True)
+    shape = counts.shape
+    if shape != (R, E // R) and shape != (E,):
+        raise ValueError(f"counts: shape {tuple(shape)}, expected {(E,)} or {(R, E // R)}")
+    if psum is not None:
+        _need(psum, torch.int64, (R, E // R + 1), "psum")
+    if status is not None:
+        _need(status, torch.int32, (1,), "status")
     return R, cap
 
 
@@ -523,15 +526,18 @@ def ep_expert_glu(x, x_scales, w, w_scales, counts, psum, act, h, h_scales=None,
     x [R, cap_rows, H] with psum (normal layout), [R, E_l, cap_rows, H] without
     (packed).  bf16 (scales None), or E4M3 bytes with ue8m0 scales; with
     h_scales h is written as E4M3, with gu gate and up are kept in bf16."""
-    lead, H = x.shape[:-1], x.shape[-1]
+    *lead, H = x.shape
+    lead = tuple(lead)
     E, two, I, Hw = w.shape
     if two != 2 or Hw != H:
         raise ValueError(f"w: shape {tuple(w.shape)}, expected (E, 2, I, {H})")
     R, cap = _expert_rows(lead, E, counts, psum, status)
     mode = _expert_inputs(x, x_scales, w, w_scales, lead)
     _need(h, torch.bfloat16 if h_scales is None else torch.uint8, (*lead, I), "h")
-    _need(h_scales, torch.uint8, (*lead[:-1], I // 128, cap), "h_scales", optional=True)
-    _need(gu, torch.bfloat16, (*lead, 2, I), "gu", optional=True)
+    if h_scales is not None:
+        _need(h_scales, torch.uint8, (*lead[:-1], I // 128, cap), "h_scales")
+    if gu is not None:
+        _need(gu, torch.bfloat16, (*lead, 2, I), "gu")
     rc = load().ep_expert_glu(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), mode, _ptr(counts),
                               _ptr(psum), R, E, H, I, cap, act, _ptr(h), _ptr(h_scales), _ptr(gu),
                               _ptr(status), _stream(stream))
@@ -563,16 +569,21 @@ def ep_expert_glu_backward(dh, gu, x, w, counts, psum, act, dgu, dx, dw, status=
 def ep_expert_linear(x, x_scales, w, w_scales, bias, residual, counts, psum, act, y, pre=None,
                      status=None, stream=None):
     """y = act(x W^T + bias) + residual over a receive layout; w [E, N, K]."""
-    lead, K = x.shape[:-1], x.shape[-1]
+    *lead, K = x.shape
+    lead = tuple(lead)
     E, N, Kw = w.shape
     if Kw != K:
         raise ValueError(f"w: shape {tuple(w.shape)}, expected (E, N, {K})")
     R, cap = _expert_rows(lead, E, counts, psum, status)
     mode = _expert_inputs(x, x_scales, w, w_scales, lead)
-    _need(bias, torch.bfloat16, (E, N), "bias", optional=True)
-    _need(residual, torch.bfloat16, (*lead, N), "residual", optional=True)
-    _need(y, torch.bfloat16, (*lead, N), "y")
-    _need(pre, torch.bfloat16, (*lead, N), "pre", optional=True)
+    rows = (*lead, N)
+    if bias is not None:
+        _need(bias, torch.bfloat16, (E, N), "bias")
+    if residual is not None:
+        _need(residual, torch.bfloat16, rows, "residual")
+    _need(y, torch.bfloat16, rows, "y")
+    if pre is not None:
+        _need(pre, torch.bfloat16, rows, "pre")
     rc = load().ep_expert_linear(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), mode, _ptr(bias),
                                  _ptr(residual), _ptr(counts), _ptr(psum), R, E, K, N, cap, act,
                                  _ptr(y), _ptr(pre), _ptr(status), _stream(stream))
