@@ -17,10 +17,10 @@ namespace ep {
 
 constexpr int kForwardThreads = 256, kBackwardThreads = 128;
 constexpr int kBackwardCtas = 8;   // of an SM
-// Rows of up to 256 logits are loaded one ahead (131072 x 256 53.2 us, 55.3
-// without); longer ones take too many registers for it (65536 x 512 55.3, 57-63 with).
-__host__ __device__ constexpr bool row_ahead(int logits) { return logits <= 8; }   // of a lane
-__host__ __device__ constexpr int forward_ctas(int logits) { return row_ahead(logits) ? 5 : 6; }
+// Up to 8 logits a lane are loaded one row ahead; more take too many registers
+// (131072 x 256, two tokens a warp: 47 us, 70 with the row ahead).
+__host__ __device__ constexpr bool row_ahead(int logits) { return logits <= 8; }
+__host__ __device__ constexpr int forward_ctas(int logits) { return row_ahead(logits) ? 5 : 4; }
 
 struct GateParams {
   const void* logits;
@@ -31,23 +31,57 @@ struct GateParams {
   float* w;
   void* grad_logits;
   int32_t* status;
-  bool vec;   // rows are whole 16-byte pieces (forward: and a lane's logits all inside or all past the row)
+  bool vec;   // rows are whole 16-byte pieces
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Over the kG lanes of a token; every lane has the result.
+template <int kG, typename Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = kG / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Min {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); }
+};
+struct Sum {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// The same, by one instruction where the lanes are the whole warp.
+template <int kG>
+__device__ __forceinline__ float group_max(float v) {
+  if (kG < kWarp) return group_reduce<kG>(v, Max());
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ float warp_min(float v) {
+template <int kG>
+__device__ __forceinline__ float group_min(float v) {
+  if (kG < kWarp) return group_reduce<kG>(v, Min());
   float r;
   asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
+}
+template <int kG>
+__device__ __forceinline__ int group_total(int v) {
+  if (kG == kWarp) return __reduce_add_sync(0xffffffffu, v);
+#pragma unroll
+  for (int o = kG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Sum over the lanes of a token up to this one.
+template <int kG>
+__device__ __forceinline__ int group_scan(int v) {
+#pragma unroll
+  for (int o = 1; o < kG; o <<= 1)
+    asm volatile("{\n .reg .u32 r;\n .reg .pred p;\n shfl.sync.up.b32 r|p, %0, %1, %2, 0xffffffff;\n @p add.u32 %0, %0, r;\n}\n"
+                 : "+r"(v)
+                 : "r"(o), "n"((kWarp - kG) << 8));
+  return v;
 }
 
 constexpr float kNone = -INFINITY;   // an expert that is never chosen
@@ -70,47 +104,50 @@ __device__ __forceinline__ float gate_load(const void* logits, int64_t at) {
   return gate_clean(static_cast<const float*>(logits)[at]);
 }
 
-// The logits of a lane's kV experts, lane * kV on, of the row that starts at
-// `row` (-inf past its end), as they are stored; vec: rows start on 16 bytes and E
-// is a multiple of kV.
-template <int kV, bool kBf16>
+// A lane's kV logits of a row, as they are stored (-inf past its end, or without
+// one): pieces of kP in turn over the kG lanes, so that those read whole lines.
+// vec: rows are whole 16-byte pieces.
+template <int kG, int kV, bool kBf16>
 struct Row {
-  static constexpr int kWords = kV * (kBf16 ? 2 : 4) / 4;   // 32-bit words a lane reads
+  static constexpr int kP = kV < (kBf16 ? 8 : 4) ? kV : (kBf16 ? 8 : 4);
+  static constexpr int kWords = kV * (kBf16 ? 2 : 4) / 4, kPieceWords = kP * (kBf16 ? 2 : 4) / 4;
+  static_assert(kPieceWords == 2 || kPieceWords == 4, "one load of 8 bytes, or of 16");
   uint32_t w[kWords];
 
-  __device__ __forceinline__ void load(const GateParams& p, int64_t row, int lane) {
-    const int e0 = lane * kV;
+  // The expert of lane g's value i.
+  static __device__ __forceinline__ int expert(int g, int i) { return (i / kP * kG + g) * kP + i % kP; }
+
+  __device__ __forceinline__ void load(const GateParams& p, bool in, int64_t row, int g) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = kBf16 ? 0xff80ff80u : 0xff800000u;   // -inf
+    if (!in) return;
     if (p.vec) {
-      if (e0 < p.E) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.logits) + (row + e0) * (kBf16 ? 2 : 4));
-        if (kWords >= 4) {
+      const uint8_t* src = static_cast<const uint8_t*>(p.logits) + (row + g * kP) * (kBf16 ? 2 : 4);
 #pragma unroll
-          for (int i = 0; i < kWords / 4; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      for (int i = 0; i < kV / kP; ++i) {
+        if (expert(g, i * kP) < p.E) {
+          if (kPieceWords == 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i * kG);
             w[4 * i] = v.x;
             w[4 * i + 1] = v.y;
-            w[4 * i + 2] = v.z;
-            w[4 * i + 3] = v.w;
+            w[kPieceWords * i + kPieceWords - 2] = v.z;
+            w[kPieceWords * i + kPieceWords - 1] = v.w;
+          } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + i * kG);
+            w[2 * i] = v.x;
+            w[2 * i + 1] = v.y;
           }
-        } else if (kWords == 2) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-          w[0] = v.x;
-          w[kWords - 1] = v.y;
-        } else {
-          w[0] = __ldg(src);
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
-        if (e0 + i < p.E) {
+        if (expert(g, i) < p.E) {
           if (kBf16) {
-            const uint32_t u = static_cast<const uint16_t*>(p.logits)[row + e0 + i];
+            const uint32_t u = static_cast<const uint16_t*>(p.logits)[row + expert(g, i)];
             w[i / 2] = (i & 1) ? (w[i / 2] & 0xffffu) | u << 16 : (w[i / 2] & 0xffff0000u) | u;
           } else {
-            w[kBf16 ? 0 : i] = static_cast<const uint32_t*>(p.logits)[row + e0 + i];
+            w[kBf16 ? 0 : i] = static_cast<const uint32_t*>(p.logits)[row + expert(g, i)];
           }
         }
       }
@@ -132,17 +169,21 @@ __device__ __forceinline__ float gate_share(float l) { return l == INFINITY ? 1.
 
 __device__ __forceinline__ float gate_weight(float l, float m) { return m < INFINITY ? gate_exp(l, m) : gate_share(l); }
 
-// A candidate's place in the falling order of the list: the number of larger
-// logits, and (exact) of equal ones of a lower expert.  The list is padded with
-// -inf to a multiple of 8.
-__device__ __forceinline__ int gate_place(const float* logits, int all, float mine) {
-  int place = 0;
+// The places of a lane's candidates in the falling order of the list: the number
+// of larger logits, and (exact) of equal ones of a lower expert.  The list is
+// padded with -inf to a multiple of 8.
+template <int kOwn>
+__device__ __forceinline__ void gate_places(const float* logits, int all, const float (&mine)[kOwn], int (&place)[kOwn]) {
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) place[o] = 0;
   for (int j = 0; j < all; j += 8) {
     const float4 x = *reinterpret_cast<const float4*>(logits + j), y = *reinterpret_cast<const float4*>(logits + j + 4);
-    place += (x.x > mine ? 1 : 0) + (x.y > mine ? 1 : 0) + (x.z > mine ? 1 : 0) + (x.w > mine ? 1 : 0);
-    place += (y.x > mine ? 1 : 0) + (y.y > mine ? 1 : 0) + (y.z > mine ? 1 : 0) + (y.w > mine ? 1 : 0);
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+      place[o] += (x.x > mine[o] ? 1 : 0) + (x.y > mine[o] ? 1 : 0) + (x.z > mine[o] ? 1 : 0) + (x.w > mine[o] ? 1 : 0);
+      place[o] += (y.x > mine[o] ? 1 : 0) + (y.y > mine[o] ? 1 : 0) + (y.z > mine[o] ? 1 : 0) + (y.w > mine[o] ? 1 : 0);
+    }
   }
-  return place;
 }
 __device__ __forceinline__ int gate_place_exact(const float* logits, const int* experts, int all, float mine, int expert) {
   int place = 0;
@@ -164,16 +205,6 @@ __device__ __forceinline__ void gate_put(uint32_t& at, float l, float least, int
       : "memory");
 }
 
-// Sum over the lanes up to this one.
-__device__ __forceinline__ int warp_scan(int v) {
-#pragma unroll
-  for (int o = 1; o < kWarp; o <<= 1)
-    asm volatile("{\n .reg .u32 r;\n .reg .pred p;\n shfl.sync.up.b32 r|p, %0, %1, 0, 0xffffffff;\n @p add.u32 %0, %0, r;\n}\n"
-                 : "+r"(v)
-                 : "r"(o));
-  return v;
-}
-
 // A finite bf16 logit with its expert in the 16 bits below it: equal logits (and
 // zeros of both signs) then fall in the order of their experts.
 __device__ __forceinline__ float gate_unique(float l, int expert) {
@@ -181,110 +212,99 @@ __device__ __forceinline__ float gate_unique(float l, int expert) {
   return __uint_as_float(u | (uint32_t)((u & 0x80000000u) ? expert : 0xffff - expert));
 }
 
-// The k largest of the warp's logits, one round a choice: the largest, the
-// lowest lane that holds it, that lane's lowest expert.  Lane j of the result
-// holds choice j (-inf: none).
-template <int kV>
-__device__ __forceinline__ void gate_choose(float (&l)[kV], int k, int lane, float& my_l, int& my_idx) {
+// The k largest of a token's logits, one round a choice: the largest, and the
+// lowest expert that has it.  Lane j of the result holds choice j (-inf: none).
+template <int kG, int kV, bool kBf16>
+__device__ __forceinline__ void gate_choose(float (&l)[kV], int k, int g, float& my_l, int& my_idx) {
   my_l = kNone;
   my_idx = -1;
   for (int j = 0; j < k; ++j) {
     float b = kNone;
-    int at = 0;
+    int e = 0;
 #pragma unroll
     for (int i = 0; i < kV; ++i)
       if (l[i] > b) {
         b = l[i];
-        at = i;
+        e = Row<kG, kV, kBf16>::expert(g, i);
       }
-    const float top = warp_max(b);
-    if (top == kNone) break;   // nothing left to choose
-    const int win = __ffs(__ballot_sync(0xffffffffu, b == top)) - 1;
-    const int e = __shfl_sync(0xffffffffu, lane * kV + at, win);
-    if (lane == j) {
+    const float top = group_max<kG>(b);   // -inf: nothing left to choose
+    // below 2^24: whole numbers, larger is lower
+    e = -(int)group_max<kG>(b == top ? (float)-e : kNone);
+    if (g == j && top != kNone) {
       my_l = top;
       my_idx = e;
     }
 #pragma unroll
     for (int i = 0; i < kV; ++i)
-      if (e == lane * kV + i) l[i] = kNone;
+      if (e == Row<kG, kV, kBf16>::expert(g, i)) l[i] = kNone;
   }
 }
 
-// A lower bound of a row's 8th largest logit, from the lanes' largest: eight
-// disjoint groups of four lanes have a largest logit each, and the least of those
-// is no larger; the better of two such groupings.
+// A lower bound of a row's k-th largest logit: the k-th of the lanes' largest, by
+// their places.
+template <int kG>
+__device__ __forceinline__ float gate_bound(float* list, float best, int k, int g) {
+  __syncwarp();
+  list[g] = best;
+  __syncwarp();
+  int place[1];
+  gate_places<1>(list, kG, {best}, place);
+  return group_min<kG>(place[0] < k ? best : INFINITY);
+}
+
+// The same for 32 lanes and k <= 8, cheaper and not as close: eight disjoint groups
+// of four lanes have a largest logit each, and the least of those is no larger;
+// the better of two such groupings.  (For k = 16 groups of two lanes mostly kept
+// more than 32 candidates of 512: 178 us for 65536 tokens.)
 __device__ __forceinline__ float gate_bound8(float best) {
   float near = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1)), far = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 16));
   near = fmaxf(near, __shfl_xor_sync(0xffffffffu, near, 2));
   far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, 8));
-  return fmaxf(warp_min(near), warp_min(far));
+  return fmaxf(group_min<kWarp>(near), group_min<kWarp>(far));
 }
 
-// The same of the k-th largest: the k-th of the 32 lanes' largest, sorted across
-// the warp.  Dearer and closer; with groups as above, rows of 512 experts mostly
-// kept more than 32 candidates for k = 16 (178 us for 65536 of them).
-__device__ __forceinline__ float gate_bound(float best, int k, int lane) {
-#pragma unroll
-  for (int size = 2; size <= kWarp; size <<= 1) {
-#pragma unroll
-    for (int o = size / 2; o > 0; o >>= 1) {
-      const float theirs = __shfl_xor_sync(0xffffffffu, best, o);
-      const bool larger = ((lane & o) == 0) == ((lane & size) == 0);   // falling order within lower halves
-      best = larger ? fmaxf(best, theirs) : fminf(best, theirs);
-    }
-  }
-  return __shfl_sync(0xffffffffu, best, k - 1);
-}
-
-// One warp per token.  Most logits are thrown out first: only those at or above a
-// bound of the k-th largest can be chosen (17 of 256 on average).  The others go to
-// a list, one to a lane, and each counts the larger ones.  Equal logits, in the
+// kG lanes (16: two tokens a warp; 32) per token, kV logits each.  Most logits are
+// thrown out first: only those at or above a bound of the k-th largest can be
+// chosen (17 of 256 on average for k = 8).  The others go to a list of 32, one or
+// two to a lane, and the larger ones of each are counted.  Equal logits, in the
 // order of their experts, are looked at only where they have left a gap in the
 // places; bf16 logits, often equal, are made unique.  Rows where more than 32
-// remain take their choices one round at a time.  Issue slots bound it: about 355
-// instructions a token, 53.2 us for 131072 x 256 (21.7 us to read and write them;
-// places in the list from a ballot a logit: 35 more, 4 us).
-// Slower: k rounds of a reduction and a ballot over the list (63.5 us); 8 lanes a
-// token with 32 logits each (99 us: registers for half the warps).
-template <int kV, bool kBf16, bool kTopk>
-__global__ void __launch_bounds__(kForwardThreads, row_ahead(kV) ? forward_ctas(kV) : 1) k_gate(GateParams p) {
-  __shared__ float4 lists[kForwardThreads / kWarp][2 * kWarp / 4];   // 32 logits, their 32 experts
-  const int lane = threadIdx.x & 31;
-  float* list = reinterpret_cast<float*>(lists[threadIdx.x >> 5]);
+// remain take their choices one round at a time.  Issue slots bound it (0.78 taken):
+// about 300 instructions a token, 47 us for 131072 x 256, top-8 (21.7 us to read
+// and write them).  A warp a token took 53 us there, 24.6 against 20.5 for 65536 x
+// 128, top-6, and 21.5 against 17.5 for 65536 x 64, top-2; 64 bytes in a row a
+// lane instead of 16-byte pieces in turn 51, and 55 against 43 for 32768 x 1024.
+// Slower: k rounds of a reduction and a ballot over the list; 8 lanes a token (99
+// us: registers for half the warps).  With more than 8 choices two tokens' lists
+// outgrow a warp too often, with more than 256 experts its registers: a warp a token.
+template <int kG, int kV, bool kBf16, bool kTopk>
+__global__ void __launch_bounds__(kForwardThreads, kV <= 16 ? forward_ctas(kV) : 1) k_gate(GateParams p) {
+  constexpr int kOwn = kWarp / kG;   // tokens of a warp; places of the list a lane has
+  __shared__ float4 lists[kForwardThreads / kG][2 * kWarp / 4];   // 32 logits, their 32 experts
+  const int g = threadIdx.x % kG;
+  float* list = reinterpret_cast<float*>(lists[threadIdx.x / kG]);
   const int* experts = reinterpret_cast<const int*>(list + kWarp);
   const uint32_t list_at = smem_addr(list);
-  const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  Row<kV, kBf16> row;
-  if (row_ahead(kV) && warp0 < p.T) row.load(p, warp0 * p.E, lane);
-  for (int64_t t = warp0; t < p.T; t += nwarps) {
+  const int64_t step = (int64_t)gridDim.x * (kForwardThreads / kG);
+  // all lanes of a warp go round as long as its first token is one
+  int64_t t = (int64_t)blockIdx.x * (kForwardThreads / kG) + threadIdx.x / kG;
+  Row<kG, kV, kBf16> row;
+  if (row_ahead(kV)) row.load(p, t < p.T, t * p.E, g);
+  for (; t - (threadIdx.x & 31) / kG < p.T; t += step) {
     float l[kV];
-    if (!row_ahead(kV)) row.load(p, t * p.E, lane);
+    if (!row_ahead(kV)) row.load(p, t < p.T, t * p.E, g);
     row.get(l);
-    if (row_ahead(kV) && t + nwarps < p.T) row.load(p, (t + nwarps) * p.E, lane);   // arrives while this one is worked on
+    if (row_ahead(kV)) row.load(p, t + step < p.T, (t + step) * p.E, g);   // arrives while this one is worked on
     float best = l[0];
 #pragma unroll
     for (int i = 1; i < kV; ++i) best = fmaxf(best, l[i]);
-    const float m = gate_base(warp_max(best));
+    const float m = gate_base(group_max<kG>(best));
     // at least the type's lowest value, so that -inf is no candidate
-    const float least = fmaxf(kLowest, p.k <= 8 ? gate_bound8(best) : gate_bound(best, p.k, lane));
-    int before = 0, all = 0;   // candidates of the lanes below, of all
-    if (kV <= 2) {   // a ballot a logit: 65536 x 64, 21.5 us against 22.5 by a scan; from 4 logits on a scan
+    const float least = fmaxf(kLowest, kG == kWarp && p.k <= 8 ? gate_bound8(best) : gate_bound<kG>(list, best, p.k, g));
+    int own = 0;
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const uint32_t who = __ballot_sync(0xffffffffu, l[i] >= least);
-        before += __popc(who & lanemask_lt());
-        all += __popc(who);
-      }
-    } else {
-      int own = 0;
-#pragma unroll
-      for (int i = 0; i < kV; ++i) own += l[i] >= least ? 1 : 0;
-      const int upto = warp_scan(own);
-      before = upto - own;
-      all = __shfl_sync(0xffffffffu, upto, kWarp - 1);
-    }
+    for (int i = 0; i < kV; ++i) own += l[i] >= least ? 1 : 0;
+    const int upto = group_scan<kG>(own), all = __shfl_sync(0xffffffffu, upto, kG - 1, kG);
     float total = 0.0f;
     if (!kTopk) {
       if (m < INFINITY) {
@@ -294,65 +314,82 @@ __global__ void __launch_bounds__(kForwardThreads, row_ahead(kV) ? forward_ctas(
 #pragma unroll
         for (int i = 0; i < kV; ++i) total += gate_share(l[i]);
       }
-      total = warp_sum(total);
+      total = group_reduce<kG>(total, Sum());
     }
-    float my_l = kNone;
-    int my_idx = -1, place = p.k, found;
-    if (all <= kWarp) {
-      found = min(p.k, all);
-      __syncwarp();
-      list[lane] = kNone;
-      __syncwarp();
-      uint32_t at = list_at + 4 * before;
+    float my_l[kOwn];
+    int my_idx[kOwn], place[kOwn], found = min(p.k, all);
 #pragma unroll
-      for (int i = 0; i < kV; ++i) gate_put(at, l[i], least, lane * kV + i);
+    for (int j = 1; j < kOwn; ++j) {
+      my_l[j] = kNone;
+      my_idx[j] = -1;
+      place[j] = p.k;
+    }
+    if (__all_sync(0xffffffffu, all <= kWarp)) {
+      const bool more = kOwn > 1 && __any_sync(0xffffffffu, all > kG);   // a lane has a second candidate
       __syncwarp();
-      my_l = list[lane];
-      my_idx = experts[lane];
-      float key = my_l;
-      if (kBf16 && m < INFINITY) {
-        key = gate_unique(my_l, my_idx);
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) list[g + j * kG] = kNone;
+      __syncwarp();
+      uint32_t at = list_at + 4 * (upto - own);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) gate_put(at, l[i], least, row.expert(g, i));
+      __syncwarp();
+      auto fetch = [&](int j) {
+        my_l[j] = list[g + j * kG];
+        my_idx[j] = experts[g + j * kG];
+        return kBf16 && m < INFINITY ? gate_unique(my_l[j], my_idx[j]) : my_l[j];
+      };
+      float key[kOwn];
+      key[0] = fetch(0);
+      if (more) key[kOwn - 1] = fetch(kOwn - 1);
+      if (kBf16) {
         __syncwarp();
-        if (lane < all) list[lane] = key;
+        if (g < all) list[g] = key[0];
+        if (more && g + kG < all) list[g + kG] = key[kOwn - 1];
         __syncwarp();
       }
-      place = gate_place(list, all, key);
+      if (more)
+        gate_places<kOwn>(list, all, key, place);
+      else
+        gate_places<1>(list, all, {key[0]}, reinterpret_cast<int(&)[1]>(place[0]));
       // the places below k are as many as there are choices, each once, unless equal logits share one
-      const bool taken = lane < all && place < p.k;
-      if (__reduce_add_sync(0xffffffffu, taken ? (1 << 16) + place : 0) != (found << 16) + found * (found - 1) / 2)
-        place = gate_place_exact(list, experts, all, key, my_idx);
-      if (lane >= all) place = p.k;
+      int taken = 0;
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) taken += g + j * kG < all && place[j] < p.k ? (1 << 16) + place[j] : 0;
+      taken = group_total<kG>(taken);
+      if (taken != (found << 16) + found * (found - 1) / 2) {
+        place[0] = gate_place_exact(list, experts, all, key[0], my_idx[0]);
+        if (more) place[kOwn - 1] = gate_place_exact(list, experts, all, key[kOwn - 1], my_idx[kOwn - 1]);
+      }
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j)
+        if (g + j * kG >= all) place[j] = p.k;
     } else {
-      gate_choose<kV>(l, p.k, lane, my_l, my_idx);
-      found = __popc(__ballot_sync(0xffffffffu, my_idx >= 0));
-      place = my_idx >= 0 ? lane : p.k;
+      gate_choose<kG, kV, kBf16>(l, p.k, g, my_l[0], my_idx[0]);
+      place[0] = my_idx[0] >= 0 ? g : p.k;
     }
-    const float ex = place < p.k ? gate_weight(my_l, m) : 0.0f;
-    if (kTopk) total = warp_sum(ex);
-    if (place < p.k) {
-      p.idx[t * p.k + place] = my_idx;
-      p.w[t * p.k + place] = __fdividef(ex, total);   // 1 <= total <= E: within 2 ulp
+    float ex[kOwn], chosen = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      ex[j] = place[j] < p.k ? gate_weight(my_l[j], m) : 0.0f;
+      chosen += ex[j];
     }
-    if (lane >= found && lane < p.k) {
-      p.idx[t * p.k + lane] = -1;
-      p.w[t * p.k + lane] = 0.0f;
+    if (kTopk) total = group_reduce<kG>(chosen, Sum());
+    if (t < p.T) {
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) {
+        if (place[j] < p.k) {
+          p.idx[t * p.k + place[j]] = my_idx[j];
+          p.w[t * p.k + place[j]] = __fdividef(ex[j], total);   // 1 <= total <= E: within 2 ulp
+        }
+      }
+      if (g >= found && g < p.k) {
+        p.idx[t * p.k + g] = -1;
+        p.w[t * p.k + g] = 0.0f;
+      }
     }
   }
 }
-
-// Over the kG lanes of a token; every lane has the result.
-template <int kG, typename Op>
-__device__ __forceinline__ float group_reduce(float v, Op op) {
-#pragma unroll
-  for (int o = kG / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-struct Max {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-struct Sum {
-  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
 
 // In the gradient value v of lane g is expert (v / kP * kG + g) * kP + v % kP:
 // 16-byte pieces in turn, so that the lanes of a token read whole lines.
@@ -504,12 +541,12 @@ static int launch_backward_t(const GateParams& p, cudaStream_t stream) {
   ep_host::count_launch();
   return ep_host::check_launch();
 }
-template <int kV, bool kBf16, bool kTopk>
+template <int kG, int kV, bool kBf16, bool kTopk>
 static int launch_forward_t(const GateParams& p, cudaStream_t stream) {
-  constexpr int kTokens = kForwardThreads / kWarp;
+  constexpr int kTokens = kForwardThreads / kG;
   const int64_t want = (p.T + kTokens - 1) / kTokens;
   const int grid = (int)std::min<int64_t>(want, (int64_t)ep_host::num_sms() * forward_ctas(kV));
-  k_gate<kV, kBf16, kTopk><<<grid, kForwardThreads, 0, stream>>>(p);
+  k_gate<kG, kV, kBf16, kTopk><<<grid, kForwardThreads, 0, stream>>>(p);
   ep_host::count_launch();
   return ep_host::check_launch();
 }
@@ -519,26 +556,28 @@ static int launch_backward(const GateParams& p, bool bf16, bool topk, cudaStream
   if (bf16) return topk ? launch_backward_t<kG, kV, true, true>(p, s) : launch_backward_t<kG, kV, true, false>(p, s);
   return topk ? launch_backward_t<kG, kV, false, true>(p, s) : launch_backward_t<kG, kV, false, false>(p, s);
 }
-template <int kV>
+template <int kG, int kV>
 static int launch_forward(const GateParams& p, bool bf16, bool topk, cudaStream_t s) {
-  if (bf16) return topk ? launch_forward_t<kV, true, true>(p, s) : launch_forward_t<kV, true, false>(p, s);
-  return topk ? launch_forward_t<kV, false, true>(p, s) : launch_forward_t<kV, false, false>(p, s);
+  if (bf16) return topk ? launch_forward_t<kG, kV, true, true>(p, s) : launch_forward_t<kG, kV, true, false>(p, s);
+  return topk ? launch_forward_t<kG, kV, false, true>(p, s) : launch_forward_t<kG, kV, false, false>(p, s);
 }
 
 static int launch_gate(const GateParams& params, int dtype, int score, bool backward, cudaStream_t s) {
   if (params.T == 0) return EP_OK;
   const bool bf16 = dtype == EP_DTYPE_BF16, topk = score == EP_GATE_SOFTMAX_TOPK;
   GateParams p = params;
+  p.vec = p.E % (bf16 ? 8 : 4) == 0 && ep_host::aligned16(p.logits) && (!backward || ep_host::aligned16(p.grad_logits));
   if (!backward) {
-    const int kv = p.E <= 64 ? 2 : p.E <= 128 ? 4 : p.E <= 256 ? 8 : p.E <= 512 ? 16 : 32;
-    p.vec = p.E % std::max(kv, 8) == 0 && ep_host::aligned16(p.logits);
-    if (p.E <= 64) return launch_forward<2>(p, bf16, topk, s);
-    if (p.E <= 128) return launch_forward<4>(p, bf16, topk, s);
-    if (p.E <= 256) return launch_forward<8>(p, bf16, topk, s);
-    if (p.E <= 512) return launch_forward<16>(p, bf16, topk, s);
-    return launch_forward<32>(p, bf16, topk, s);
+    if (p.k <= 8) {
+      if (p.E <= 64) return launch_forward<16, 4>(p, bf16, topk, s);
+      if (p.E <= 128) return launch_forward<16, 8>(p, bf16, topk, s);
+      if (p.E <= 256) return launch_forward<16, 16>(p, bf16, topk, s);
+    }
+    if (p.E <= 128) return launch_forward<32, 4>(p, bf16, topk, s);
+    if (p.E <= 256) return launch_forward<32, 8>(p, bf16, topk, s);
+    if (p.E <= 512) return launch_forward<32, 16>(p, bf16, topk, s);
+    return launch_forward<32, 32>(p, bf16, topk, s);
   }
-  p.vec = p.E % (bf16 ? 8 : 4) == 0 && ep_host::aligned16(p.logits) && ep_host::aligned16(p.grad_logits);
   // as few lanes a token as hold its logits in 32 registers each and its k slots in one each
   if (p.k <= 8) {
     if (p.E <= 64) return launch_backward<8, 8>(p, bf16, topk, s);
