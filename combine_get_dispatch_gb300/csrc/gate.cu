@@ -68,10 +68,13 @@ __device__ __forceinline__ float group_min(float v) {
 }
 template <int kG>
 __device__ __forceinline__ int group_total(int v) {
-  if (kG == kWarp) return __reduce_add_sync(0xffffffffu, v);
+  if constexpr (kG == kWarp) {
+    return __reduce_add_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = kG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+    for (int o = kG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
 }
 // Sum over the lanes of a token up to this one.
 template <int kG>
@@ -111,7 +114,6 @@ template <int kG, int kV, bool kBf16>
 struct Row {
   static constexpr int kP = kV < (kBf16 ? 8 : 4) ? kV : (kBf16 ? 8 : 4);
   static constexpr int kWords = kV * (kBf16 ? 2 : 4) / 4, kPieceWords = kP * (kBf16 ? 2 : 4) / 4;
-  static_assert(kPieceWords == 2 || kPieceWords == 4, "one load of 8 bytes, or of 16");
   uint32_t w[kWords];
 
   // The expert of lane g's value i.
@@ -128,14 +130,16 @@ struct Row {
         if (expert(g, i * kP) < p.E) {
           if (kPieceWords == 4) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i * kG);
-            w[4 * i] = v.x;
-            w[4 * i + 1] = v.y;
-            w[kPieceWords * i + kPieceWords - 2] = v.z;
+            w[kPieceWords * i] = v.x;
+            w[kPieceWords * i + kPieceWords / 4] = v.y;
+            w[kPieceWords * i + kPieceWords / 2] = v.z;
             w[kPieceWords * i + kPieceWords - 1] = v.w;
-          } else {
+          } else if (kPieceWords == 2) {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + i * kG);
-            w[2 * i] = v.x;
-            w[2 * i + 1] = v.y;
+            w[kPieceWords * i] = v.x;
+            w[kPieceWords * i + kPieceWords - 1] = v.y;
+          } else {
+            w[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + i * kG);
           }
         }
       }
@@ -275,8 +279,7 @@ __device__ __forceinline__ float gate_bound8(float best) {
 // 128, top-6, and 21.5 against 17.5 for 65536 x 64, top-2; 64 bytes in a row a
 // lane instead of 16-byte pieces in turn 51, and 55 against 43 for 32768 x 1024.
 // Slower: k rounds of a reduction and a ballot over the list; 8 lanes a token (99
-// us: registers for half the warps).  With more than 8 choices two tokens' lists
-// outgrow a warp too often, with more than 256 experts its registers: a warp a token.
+// us: registers for half the warps).
 template <int kG, int kV, bool kBf16, bool kTopk>
 __global__ void __launch_bounds__(kForwardThreads, kV <= 16 ? forward_ctas(kV) : 1) k_gate(GateParams p) {
   constexpr int kOwn = kWarp / kG;   // tokens of a warp; places of the list a lane has
@@ -568,11 +571,15 @@ static int launch_gate(const GateParams& params, int dtype, int score, bool back
   GateParams p = params;
   p.vec = p.E % (bf16 ? 8 : 4) == 0 && ep_host::aligned16(p.logits) && (!backward || ep_host::aligned16(p.grad_logits));
   if (!backward) {
-    if (p.k <= 8) {
+    // Two tokens a warp while their lists mostly hold what is left of a row (131072 x 256: top-9 44 us against
+    // 61 by a warp a token, top-12 57 against 61, top-13 77 against 63; x 64, top-16 86 against 51) and their
+    // rows fit the registers (65536 x 512, top-8: 40 us either way).
+    if (p.k <= 12) {
       if (p.E <= 64) return launch_forward<16, 4>(p, bf16, topk, s);
       if (p.E <= 128) return launch_forward<16, 8>(p, bf16, topk, s);
       if (p.E <= 256) return launch_forward<16, 16>(p, bf16, topk, s);
     }
+    if (p.E <= 64) return launch_forward<32, 2>(p, bf16, topk, s);
     if (p.E <= 128) return launch_forward<32, 4>(p, bf16, topk, s);
     if (p.E <= 256) return launch_forward<32, 8>(p, bf16, topk, s);
     if (p.E <= 512) return launch_forward<32, 16>(p, bf16, topk, s);

@@ -205,3 +205,27 @@ def test_gate_empty_batch_and_refusals():
     with pytest.raises(ep.EPError):   # E not a multiple of R
         ep.ep_gate_topk(l[..., :7].contiguous(), 0, i, w)
     assert ep.ep_launch_count() == before
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(5, 3), (33, 1), (64, 8), (100, 4), (128, 8), (250, 7), (256, 8), (256, 12), (300, 8)])
+def test_gate_unlike_neighbours(E, k, dtype):
+    """Tokens side by side (an odd number of them) that take different ways: few and
+    many candidates, all equal, switched off, infinite."""
+    g = torch.Generator().manual_seed(E * 16 + k)
+    rows = torch.randn((61, E), generator=g)
+    rows[1::8] = 2.5                                  # every expert ties
+    rows[2::8] = -INF
+    rows[3::8, 1:] = -INF                             # one expert left
+    rows[4::8] = torch.linspace(-3, 3, E)             # the largest in the last lanes
+    rows[5::8] = torch.linspace(3, -3, E)
+    rows[6::8, :: max(1, E // 40)] = 5.0              # some forty equal largest
+    rows[7::16, E // 2] = INF
+    rows[15::16, :2] = math.nan
+    rows = rows.to(dtype)[None]
+    for score in ("softmax", "softmax_topk"):
+        idx, w = run_gate(rows.cuda(), k, score)
+        ref_idx, ref_w = reference(rows, k, score)
+        assert torch.equal(idx.cpu(), ref_idx)
+        assert torch.isfinite(w).all()
+        assert ((w.cpu().double() - ref_w).abs() <= 6e-6 * ref_w + 1e-37).all()
