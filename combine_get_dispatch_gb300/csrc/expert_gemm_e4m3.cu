@@ -10,8 +10,8 @@
 // some tens of rows and the time is that of reading its weights once: one CTA per
 // SM computes 128 x 256 tiles, so that two thirds of the bytes in flight (4 stages
 // of 48 KB, fewer rows of A where the segment has fewer) are weights: 64 experts
-// with 64 rows of 7168, gated, in 285-291 us (0.98-1.0 of the copy rate), 2048 ->
-// 7168 in 154-157 us (0.94-0.96).  65536 rows over 32 experts, gated, take 1303 us
+// with 64 rows of 7168, gated, in 278-285 us (1.0 of the copy rate), 2048 ->
+// 7168 in 148-151 us (0.98-1.0).  65536 rows over 32 experts, gated, take 1303 us
 // (2950 TFLOP/s; 1549 us while one warp issued all copies); pairs of CTAs as for
 // bf16 took 1343 us there, and 361 and 193 us on the two decode products, whose
 // few rows leave most of a 256-row tile empty.

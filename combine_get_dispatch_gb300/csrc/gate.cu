@@ -269,7 +269,7 @@ __device__ __forceinline__ float gate_bound8(float best) {
 
 // kG lanes (16: two tokens a warp; 32) per token, kV logits each.  Most logits are
 // thrown out first: only those at or above a bound of the k-th largest can be
-// chosen (17 of 256 on average for k = 8).  The others go to a list of 32, one or
+// chosen (11 to 17 of 256 on average for k = 8).  The others go to a list of 32, one or
 // two to a lane, and the larger ones of each are counted.  Equal logits, in the
 // order of their experts, are looked at only where they have left a gap in the
 // places; bf16 logits, often equal, are made unique.  Rows where more than 32
