@@ -352,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (blocks > 0) {
           tmem_ld_16x32(d + r0, v[0]);
           tmem_ld_16x32(d + (16u << 16) + r0, v[1]);
-          tmem_wait_ld();
+          tmem_wait_ld(v[0], v[1]);
           if (r0 + 2 * kChunk >= t.rows) sums_read();
         } else {
 #pragma unroll

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
         for (int c0 = first; c0 < first + kCols / 2; c0 += 32) {
           tmem_ld32(d + c0, v);
           tmem_ld32(d + 128 + c0, u);
-          tmem_wait_ld();
+          tmem_wait_ld(v, u);
 #pragma unroll
           for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(act_value<kAct>(v[i]) * u[i]));
         }
@@ -310,8 +310,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
 #pragma unroll 1
       for (int c0 = first; c0 < first + kCols / 2; c0 += 32) {
         tmem_ld32(d + c0, v);
-        if (kForm == kGlu) tmem_ld32(d + 128 + c0, u);
-        tmem_wait_ld();
+        if constexpr (kForm == kGlu) {
+          tmem_ld32(d + 128 + c0, u);
+          tmem_wait_ld(v, u);
+        } else {
+          tmem_wait_ld(v);
+        }
         if (c0 + 32 == first + kCols / 2) sums_read();
         if (in) {
           if (quantised) {

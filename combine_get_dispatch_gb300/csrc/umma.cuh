@@ -169,7 +169,17 @@ __device__ __forceinline__ void tmem_fence_before() {
 __device__ __forceinline__ void tmem_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads before it; the arrays they fill are named, so that nothing
+// made from them is moved above the wait.
+template <int... kN>
+__device__ __forceinline__ void tmem_wait_ld(float (&... v)[kN]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  auto after = [](float* x, int n) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm volatile("" : "+f"(x[i])::"memory");
+  };
+  (after(v, kN), ...);
+}
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
