@@ -55,11 +55,36 @@ __device__ __forceinline__ uint32_t ue8m0_of(float amax) {
 
 // ---------------------------------------------------------------- activations
 
+// g = exp(-z^2 / 2) and Phi(z), the normal distribution up to z.  Its tail is
+// Phi(-|z|) = g t Q(t), t = 1 / (1 + 0.36 |z|): the form of Hastings (Approximations
+// for Digital Computers, 1955), Q fitted to erfc by its relative error, 2^-19.8 in
+// 32 bits; with the exponential's argument 2^-17 at |z| = 12; 0 below 2^-126.
+// 1 + erf(z / sqrt 2) is a multiple of 2^-24, 4 % off at z = -5 and 57 % at -5.5;
+// erfcf is right but slow (8192 x 512 x 7168 with GELU: 130 us, 86 by erff, 71 so).
+__device__ __forceinline__ float normal_cdf(float z, float& g) {
+  const float u = fabsf(z);
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.36f, u, 1.0f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(z * z * -0.72134752f));
+  float q = 0.0473445728f;
+  q = fmaf(q, t, -0.180751652f);
+  q = fmaf(q, t, 0.182297572f);
+  q = fmaf(q, t, 0.0256238226f);
+  q = fmaf(q, t, 0.14005743f);
+  q = fmaf(q, t, 0.141710669f);
+  q = fmaf(q, t, 0.143717438f);
+  const float tail = q * t * g;
+  return z > 0.0f ? 1.0f - tail : tail;
+}
+
 template <int kAct>
 __device__ __forceinline__ float act_value(float z) {
   if (kAct == EP_ACT_RELU) return z < 0.0f ? 0.0f : z;   // a NaN stays one
   if (kAct == EP_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));   // 2 ulp; 0 where the divisor passes 2^126
-  if (kAct == EP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+  if (kAct == EP_ACT_GELU) {
+    float g;
+    return z * normal_cdf(z, g);
+  }
   return z;
 }
 
@@ -74,9 +99,10 @@ __device__ __forceinline__ void act_both(float z, float& value, float& slope) {
     value = z * q;
     slope = q * (1.0f + z * (1.0f - q));
   } else if (kAct == EP_ACT_GELU) {
-    const float c = 0.5f * (1.0f + erff(z * 0.70710678f));
+    float g;
+    const float c = normal_cdf(z, g);
     value = z * c;
-    slope = c + z * 0.39894228f * __expf(-0.5f * z * z);
+    slope = c + z * 0.39894228f * g;
   } else {
     value = z;
     slope = 1.0f;
