@@ -334,19 +334,23 @@ int check_launch();   // EP_OK or EP_ERR_CUDA after a launch
 int ensure_max_smem(const void* func, int bytes);
 // Launch as a programmatic dependent of the kernel before it in the stream: the
 // grid may come up while that one drains; the kernel waits (pdl_wait) before it
-// touches global memory.
+// touches global memory.  cluster: CTAs of a cluster, where the kernel does not say.
 template <typename P>
-inline int launch_dependent(void (*kernel)(P), int grid, int threads, int smem, cudaStream_t stream, const P& params) {
+inline int launch_dependent(void (*kernel)(P), dim3 grid, int threads, int smem, cudaStream_t stream, const P& params,
+                            int cluster = 0) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kernel, params) != cudaSuccess) {
     cudaGetLastError();
     return EP_ERR_CUDA;

@@ -84,77 +84,89 @@ __global__ void __launch_bounds__(kThreads, kSlopeCtas) k_glu_slope(SlopeParams 
 // kSplit CTAs owns 64 columns of one expert: 8 threads a row, 32 rows a CTA and
 // step, four steps' loads at a time, the sums in 32 bits (before dpre is
 // rounded), added over the CTA's rows and then over the cluster in a fixed order.
-// Memory bounds it (50288 x 4072, sum only: read once, 410 MB).
-template <int kAct, int kSplit>
+// kAlone (under an SM budget): a CTA takes the shares of a cluster one after
+// another, and as many column groups as its part of the grid is; the same sums in
+// the same order.  Memory bounds it (50288 x 4072, sum only: read once, 410 MB).
+template <int kAct, int kSplit, bool kAlone>
 __global__ void __launch_bounds__(kThreads) k_linear_slope(SlopeParams p) {
-  constexpr int kRows = kThreads / 8, kSteps = 4;
+  constexpr int kRows = kThreads / 8, kSteps = 4, kCluster = kAlone ? 1 : kSplit;
   __shared__ float part[kThreads / kWarp][64];
   const int c8 = threadIdx.x & 7, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int share = blockIdx.x % kSplit;
-  const int c = blockIdx.x / kSplit * 64 + c8 * 8;
-  const int e = blockIdx.y;
-  Segments seg = p.seg;
-  if (blockIdx.x != 0) seg.status = nullptr;
+  const int rank = blockIdx.x % kCluster, groups = (p.N + 63) / 64;
   pdl_launch_dependents();   // the products come up while this runs
   pdl_wait();
-  const Segment s = segment_of(seg, e);
-  float sum[8] = {};
-  if (c < p.N) {
-    for (int64_t i0 = share * kRows + (threadIdx.x >> 3); i0 < s.count; i0 += kSplit * kRows * kSteps) {
-      uint4 d[kSteps], z[kSteps];
+  for (int item = blockIdx.x / kCluster; !kAlone || item < groups * p.seg.E; item += gridDim.x) {
+    const int e = kAlone ? item / groups : blockIdx.y;
+    const int c0 = (kAlone ? item % groups : item) * 64, c = c0 + c8 * 8;
+    Segments seg = p.seg;
+    if (c0 != 0 || rank != 0) seg.status = nullptr;
+    const Segment s = segment_of(seg, e);
+    float all = 0.0f;
+    for (int share = rank;; ++share) {
+      float sum[8] = {};
+      if (c < p.N) {
+        for (int64_t i0 = share * kRows + (threadIdx.x >> 3); i0 < s.count; i0 += kSplit * kRows * kSteps) {
+          uint4 d[kSteps], z[kSteps];
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int64_t i = i0 + k * kSplit * kRows;
-        d[k] = z[k] = make_uint4(0, 0, 0, 0);
-        if (i < s.count) {
-          const int64_t at = (s.start + i) * p.N + c;
-          d[k] = *reinterpret_cast<const uint4*>(p.dy + at);
-          if (kAct != EP_ACT_NONE) z[k] = *reinterpret_cast<const uint4*>(p.pre + at);
+          for (int k = 0; k < kSteps; ++k) {
+            const int64_t i = i0 + k * kSplit * kRows;
+            d[k] = z[k] = make_uint4(0, 0, 0, 0);
+            if (i < s.count) {
+              const int64_t at = (s.start + i) * p.N + c;
+              d[k] = *reinterpret_cast<const uint4*>(p.dy + at);
+              if (kAct != EP_ACT_NONE) z[k] = *reinterpret_cast<const uint4*>(p.pre + at);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const int64_t i = i0 + k * kSplit * kRows;
+            const uint32_t dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w}, zw[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float v, s0, s1;
+              act_both<kAct>(bf16_lo(zw[q]), v, s0);
+              act_both<kAct>(bf16_hi(zw[q]), v, s1);
+              const float d0 = bf16_lo(dw[q]) * s0, d1 = bf16_hi(dw[q]) * s1;
+              sum[2 * q] += d0;
+              sum[2 * q + 1] += d1;
+              o[q] = pack_bf16x2(d0, d1);
+            }
+            if (kAct != EP_ACT_NONE && i < s.count) st_v4(p.out + (s.start + i) * p.N + c, make_uint4(o[0], o[1], o[2], o[3]));
+          }
         }
       }
+      if (p.dbias != nullptr) {   // the same for every CTA of the cluster
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int64_t i = i0 + k * kSplit * kRows;
-        const uint32_t dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w}, zw[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float v, s0, s1;
-          act_both<kAct>(bf16_lo(zw[q]), v, s0);
-          act_both<kAct>(bf16_hi(zw[q]), v, s1);
-          const float d0 = bf16_lo(dw[q]) * s0, d1 = bf16_hi(dw[q]) * s1;
-          sum[2 * q] += d0;
-          sum[2 * q + 1] += d1;
-          o[q] = pack_bf16x2(d0, d1);
+        for (int q = 0; q < 8; ++q) {
+          sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 8);
+          sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 16);
+          if (lane < 8) part[warp][c8 * 8 + q] = sum[q];
         }
-        if (kAct != EP_ACT_NONE && i < s.count) st_v4(p.out + (s.start + i) * p.N + c, make_uint4(o[0], o[1], o[2], o[3]));
+        __syncthreads();
+        float rows = 0.0f;
+        if (threadIdx.x < 64) {
+#pragma unroll
+          for (int w = 0; w < kThreads / kWarp; ++w) rows += part[w][threadIdx.x];
+        }
+        all = kAlone && share > 0 ? all + rows : rows;
+        if (kSplit > 1 || kAlone) __syncthreads();   // part is written again
       }
+      if (!kAlone || share + 1 == kSplit) break;
     }
-  }
-  if (p.dbias == nullptr) return;   // the same for every CTA of the cluster
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 8);
-    sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 16);
-    if (lane < 8) part[warp][c8 * 8 + q] = sum[q];
-  }
-  __syncthreads();
-  float all = 0.0f;
-  if (threadIdx.x < 64) {
-#pragma unroll
-    for (int w = 0; w < kThreads / kWarp; ++w) all += part[w][threadIdx.x];
-  }
-  const int col = blockIdx.x / kSplit * 64 + threadIdx.x;
-  if (kSplit > 1) {
-    __syncthreads();
-    if (threadIdx.x < 64) part[0][threadIdx.x] = all;
-    cluster_sync();
-    if (share == 0 && threadIdx.x < 64) {
-      for (int r = 1; r < kSplit; ++r) all += ld_cluster_f32(map_to_rank(smem_addr(&part[0][threadIdx.x]), r));
+    const int col = c0 + threadIdx.x;
+    const bool writes = p.dbias != nullptr && rank == 0 && threadIdx.x < 64 && col < p.N;
+    if (kCluster > 1 && p.dbias != nullptr) {
+      if (threadIdx.x < 64) part[0][threadIdx.x] = all;
+      cluster_sync();
+      if (writes) {
+        for (int r = 1; r < kCluster; ++r) all += ld_cluster_f32(map_to_rank(smem_addr(&part[0][threadIdx.x]), r));
+      }
+      cluster_sync();   // no CTA leaves while its sums are read
     }
-    cluster_sync();   // no CTA leaves while its sums are read
+    if (writes) p.dbias[(int64_t)e * p.N + col] = __float2bfloat16_rn(all);
+    if (!kAlone) break;
   }
-  if (share == 0 && threadIdx.x < 64 && col < p.N) p.dbias[(int64_t)e * p.N + col] = __float2bfloat16_rn(all);
 }
 
 template <int kAct>
@@ -168,22 +180,13 @@ static int launch_glu_slope(const SlopeParams& p, int64_t rows, cudaStream_t s) 
 
 template <int kAct, int kSplit>
 static int launch_linear_slope_t(const SlopeParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.N + 63) / 64 * kSplit, p.seg.E);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kSplit;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, k_linear_slope<kAct, kSplit>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return EP_ERR_CUDA;
-  }
+  const int groups = (p.N + 63) / 64;
+  const int rc =
+      ep_host::sm_budget_set()
+          ? ep_host::launch_dependent(k_linear_slope<kAct, kSplit, true>, std::min(groups * p.seg.E, ep_host::grid_cap(1)),
+                                      kThreads, 0, s, p)
+          : ep_host::launch_dependent(k_linear_slope<kAct, kSplit, false>, dim3(groups * kSplit, p.seg.E), kThreads, 0, s, p, kSplit);
+  if (rc != EP_OK) return rc;
   ep_host::count_launch();
   return ep_host::check_launch();
 }
@@ -193,6 +196,7 @@ static int launch_linear_slope_t(const SlopeParams& p, cudaStream_t s) {
 // not the kernel's time (11088 rows x 272, 224 experts of uneven sizes: 31 us
 // whole, 17 by 2, 24 by 8; 37140 x 1400, 32 even experts: 52, 58-60, 78); with
 // at most one an SM over 8 (777 x 2048, one expert: 13.2 us by 32 CTAs, 7.4).
+// The split does not look at the SM budget, so that the sums are the same under one.
 template <int kAct>
 static int launch_linear_slope(const SlopeParams& p, cudaStream_t s) {
   const int64_t groups = (int64_t)((p.N + 63) / 64) * p.seg.E;
