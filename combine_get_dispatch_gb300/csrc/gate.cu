@@ -539,7 +539,7 @@ template <int kG, int kV, bool kBf16, bool kTopk>
 static int launch_backward_t(const GateParams& p, cudaStream_t stream) {
   constexpr int kTokens = kBackwardThreads / kG;   // of a CTA
   const int64_t want = (p.T + kTokens - 1) / kTokens;
-  const int grid = (int)std::min<int64_t>(want, (int64_t)ep_host::num_sms() * kBackwardCtas);
+  const int grid = (int)std::min<int64_t>(want, ep_host::grid_cap(kBackwardCtas));
   k_gate_backward<kG, kV, kBf16, kTopk><<<grid, kBackwardThreads, 0, stream>>>(p);
   ep_host::count_launch();
   return ep_host::check_launch();
@@ -548,7 +548,7 @@ template <int kG, int kV, bool kBf16, bool kTopk>
 static int launch_forward_t(const GateParams& p, cudaStream_t stream) {
   constexpr int kTokens = kForwardThreads / kG;
   const int64_t want = (p.T + kTokens - 1) / kTokens;
-  const int grid = (int)std::min<int64_t>(want, (int64_t)ep_host::num_sms() * forward_ctas(kV));
+  const int grid = (int)std::min<int64_t>(want, ep_host::grid_cap(forward_ctas(kV)));
   k_gate<kG, kV, kBf16, kTopk><<<grid, kForwardThreads, 0, stream>>>(p);
   ep_host::count_launch();
   return ep_host::check_launch();

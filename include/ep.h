@@ -324,8 +324,9 @@ int ep_format_bf16(const float* in, uint16_t* out, int64_t n, void* stream);
 
 /* SM budget (Buffer.num_sms, §2.2; the per-SM bandwidth model of §4.6):
  * caps the SMs that the data kernels of ep_dispatch, ep_ll_dispatch,
- * ep_combine, ep_ll_combine, ep_rank_combine and the expert calls
- * (ep_expert_*: products and the gradients' elementwise half) occupy, so the
+ * ep_combine, ep_ll_combine, ep_rank_combine, the router
+ * (ep_gate_topk, ep_gate_topk_backward) and the expert calls (ep_expert_*:
+ * products and the gradients' elementwise half) occupy, so the
  * rest of the GPU stays free for work that overlaps them.  num_sms = 0 lifts the cap
  * (every SM; the default); num_sms > 0 launches those kernels with at most
  * min(num_sms, SM count) CTAs of one per SM.  The single-launch low-latency
