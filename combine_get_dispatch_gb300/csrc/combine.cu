@@ -11,7 +11,8 @@
 //
 // Launched with programmatic dependent launch: it waits (griddepcontrol)
 // for the kernel before it -- the dispatch that wrote combine_idx -- to
-// complete.  The library's kernels before it do not trigger it early: its
+// complete.  The library's kernels before it (the dispatch's; the expert
+// products whose rows it reads) do not trigger it early: its
 // CTAs would then be placed on whichever SMs free up first, several to an
 // SM, and the static split of the items over them would run unevenly.
 //

@@ -139,7 +139,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   tmem_fence_before();
   __syncwarp();
   cluster_arrive();
-  pdl_launch_dependents();
+  if (p.early) pdl_launch_dependents();
   pdl_wait();   // all that follows reads what kernels before this one may have written
   TileWalk walk;
   Tile first = {};

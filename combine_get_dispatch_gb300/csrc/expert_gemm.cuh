@@ -21,6 +21,7 @@ struct ProductParams {
   void* out;
   uint8_t* out_scales;
   __nv_bfloat16* keep;       // gu / pre
+  bool early;                // the next kernel of the stream may come up while this one runs
 };
 
 // One tile of the list: output rows m0 .. m0 + rows of expert e (numbered inside

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_expert_gemm_e4m3(const __grid
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  pdl_launch_dependents();
+  if (p.early) pdl_launch_dependents();
   pdl_wait();   // all that follows reads what kernels before this one may have written
   const uint32_t tmem = sh.tmem;
 
