@@ -18,7 +18,7 @@ namespace ep {
 constexpr int kForwardThreads = 256, kBackwardThreads = 128;
 constexpr int kBackwardCtas = 8;   // of an SM
 // Up to 8 logits a lane are loaded one row ahead; more take too many registers
-// (131072 x 256, two tokens a warp: 47 us, 70 with the row ahead).
+// (131072 x 256, two tokens a warp: 70 us with the row ahead, 47 without; 45 now).
 __host__ __device__ constexpr bool row_ahead(int logits) { return logits <= 8; }
 __host__ __device__ constexpr int forward_ctas(int logits) { return row_ahead(logits) ? 5 : 4; }
 
@@ -91,7 +91,8 @@ constexpr float kNone = -INFINITY;   // an expert that is never chosen
 constexpr float kLowest = -3.40282346638528859812e+38f;
 
 // exp(l - m): the difference rounds once and its product with log2(e) once, so
-// it is off by |l - m| 2^-23 of itself; below 2^-126 it is 0.  m is finite.
+// it is off by |l - m| 2^-23 of itself; below 2^-126 it is 0.  m is finite.  Logits of
+// a spread of 1.5: weights 6.4e-8 off (rms), 5.6e-8 by expf and a rounded quotient.
 __device__ __forceinline__ float gate_exp(float l, float m) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((l - m) * 1.44269504f));
@@ -273,9 +274,9 @@ __device__ __forceinline__ float gate_bound8(float best) {
 // two to a lane, and the larger ones of each are counted.  Equal logits, in the
 // order of their experts, are looked at only where they have left a gap in the
 // places; bf16 logits, often equal, are made unique.  Rows where more than 32
-// remain take their choices one round at a time.  Issue slots bound it (0.78 taken):
-// about 300 instructions a token, 47 us for 131072 x 256, top-8 (21.7 us to read
-// and write them).  A warp a token took 53 us there, 24.6 against 20.5 for 65536 x
+// remain take their choices one round at a time.  Issue slots bound it (0.77 taken):
+// about 300 instructions a token, 45 us for 131072 x 256, top-8 (21.7 us to read
+// and write them).  A warp a token took 53 us there against 47, 24.6 against 20.5 for 65536 x
 // 128, top-6, and 21.5 against 17.5 for 65536 x 64, top-2; 64 bytes in a row a
 // lane instead of 16-byte pieces in turn 51, and 55 against 43 for 32768 x 1024.
 // Slower: k rounds of a reduction and a ballot over the list; 8 lanes a token (99

@@ -465,6 +465,8 @@ def ep_gate_topk(logits, score, topk_idx, topk_weights, stream=None):
 
 def ep_gate_topk_backward(logits, score, topk_idx, grad_topk_weights, grad_logits, status=None,
                           stream=None):
+    """Gradient of ep_gate_topk's weights; ids outside [-1, E) count as unused,
+    which only the status word says."""
     R, T_r, E = logits.shape
     k = topk_idx.shape[2]
     dtype = _gate_dtype(logits)
@@ -525,7 +527,11 @@ def ep_expert_glu(x, x_scales, w, w_scales, counts, psum, act, h, h_scales=None,
 
     x [R, cap_rows, H] with psum (normal layout), [R, E_l, cap_rows, H] without
     (packed).  bf16 (scales None), or E4M3 bytes with ue8m0 scales; with
-    h_scales h is written as E4M3, with gu gate and up are kept in bf16."""
+    h_scales h is written as E4M3, with gu gate and up are kept in bf16.
+
+    As in all the expert calls, rows past cap_rows are left out and a wait that
+    ran out leaves outputs incomplete; only the status word says so
+    (ep_read_status), and without one there is no sign."""
     *lead, H = x.shape
     lead = tuple(lead)
     E, two, I, Hw = w.shape
@@ -546,7 +552,8 @@ def ep_expert_glu(x, x_scales, w, w_scales, counts, psum, act, h, h_scales=None,
 
 def ep_expert_glu_backward(dh, gu, x, w, counts, psum, act, dgu, dx, dw, status=None, stream=None):
     """Gradient of ep_expert_glu: dgu (gate and up), dx and dw (either may be
-    None, and then w or x may be too)."""
+    None, and then w or x may be too).  Rows left out are told by status alone
+    (see ep_expert_glu)."""
     lead, I = dh.shape[:-1], dh.shape[-1]
     some = w if w is not None else dw
     if some is None:
@@ -568,7 +575,8 @@ def ep_expert_glu_backward(dh, gu, x, w, counts, psum, act, dgu, dx, dw, status=
 
 def ep_expert_linear(x, x_scales, w, w_scales, bias, residual, counts, psum, act, y, pre=None,
                      status=None, stream=None):
-    """y = act(x W^T + bias) + residual over a receive layout; w [E, N, K]."""
+    """y = act(x W^T + bias) + residual over a receive layout; w [E, N, K].
+    Rows left out are told by status alone (see ep_expert_glu)."""
     *lead, K = x.shape
     lead = tuple(lead)
     E, N, Kw = w.shape
@@ -593,7 +601,8 @@ def ep_expert_linear(x, x_scales, w, w_scales, bias, residual, counts, psum, act
 def ep_expert_linear_backward(dy, pre, x, w, counts, psum, act, dpre, dx, dw, dbias=None,
                               status=None, stream=None):
     """Gradient of ep_expert_linear; pre and dpre are None without activation,
-    dx, dw and dbias may each be None."""
+    dx, dw and dbias may each be None.  Rows left out are told by status alone
+    (see ep_expert_glu)."""
     lead, N = dy.shape[:-1], dy.shape[-1]
     some = w if w is not None else dw
     if some is None:

@@ -388,7 +388,9 @@ int ep_gate_topk_backward(const void* logits, int dtype, const int64_t* topk_idx
  *     cap_rows (= R*max_tokens_per_rank) rows; counts = recv_count
  * counts [E] int32.  Rows outside every segment are neither used nor written.
  * A segment that leaves the buffer is cut at cap_rows (EP_ERR_CAPACITY in
- * *status).  Sums run in 32 bits; each bf16 output is rounded once.
+ * *status), and a wait that runs out ends the kernel (EP_ERR_TIMEOUT there): rows
+ * are then missing from the outputs, which nothing but *status tells; without
+ * status there is no sign.  Sums run in 32 bits; each bf16 output is rounded once.
  * Limits: widths are multiples of 8 (128 with FP8), all segments' rows
  * together at most 2^31 - 2^16, E * width below 2^31, x / w / outputs 16-byte aligned, E <= 1024.
  * With EP_FP8_E4M3_UE8M0, x is E4M3 with the scales dispatch writes
