@@ -13,6 +13,7 @@ The alloc_* helpers only create output tensors of the documented shapes
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -38,8 +39,11 @@ EXPORTS = (
     "ep_rank_recv_topk", "ep_rank_combine", "ep_set_num_sms", "ep_get_num_sms",
     "ep_format_e4m3", "ep_format_bf16", "ep_layout_notify", "ep_layout_notify_dispatch",
     "ep_gate_topk", "ep_gate_topk_backward", "ep_expert_glu", "ep_expert_glu_backward",
-    "ep_expert_linear", "ep_expert_linear_backward",
+    "ep_expert_linear", "ep_expert_linear_backward", "ep_moe_few_workspace_size", "ep_moe_few",
+    "ep_orthogonalize_workspace_size", "ep_orthogonalize", "ep_muon_update",
 )
+
+EP_MOE_FEW_TOKENS = 64
 
 EP_DTYPE_F32 = 0
 EP_DTYPE_BF16 = 1
@@ -63,6 +67,7 @@ class EPError(RuntimeError):
 
 _lib = None
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_F = ctypes.c_float
 
 
 def lib_path() -> str:
@@ -116,6 +121,15 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                    _P, _P, _P, _P]
     L.ep_expert_linear_backward.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _I, _P,
                                             _P, _P, _P, _P, _P]
+    L.ep_moe_few_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+    L.ep_moe_few_workspace_size.restype = _SZ
+    L.ep_moe_few.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P,
+                             _SZ, _P, _P]
+    L.ep_orthogonalize_workspace_size.argtypes = [_I, _I, _I]
+    L.ep_orthogonalize_workspace_size.restype = _SZ
+    L.ep_orthogonalize.argtypes = [_P, _I, _I, _I, _I, _I, _P, _F, _P, _P, _SZ, _P, _P]
+    L.ep_muon_update.argtypes = [_P, _I, _P, _P, _P, _I, _I, _I, _F, _F, _F, _I, _F, _I, _P, _F,
+                                 _P, _SZ, _P, _P]
     L.ep_set_num_sms.argtypes = [_I]
     L.ep_set_num_sms.restype = _I
     L.ep_get_num_sms.argtypes = []
@@ -128,7 +142,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                  "ep_ll_dispatch", "ep_ll_combine", "ep_clean_ll_buffer", "ep_read_status",
                  "ep_host_wait_counters", "ep_rank_ids", "ep_rank_recv_topk", "ep_rank_combine",
                  "ep_gate_topk", "ep_gate_topk_backward", "ep_expert_glu",
-                 "ep_expert_glu_backward", "ep_expert_linear", "ep_expert_linear_backward"):
+                 "ep_expert_glu_backward", "ep_expert_linear", "ep_expert_linear_backward",
+                 "ep_moe_few", "ep_orthogonalize", "ep_muon_update"):
         getattr(L, name).restype = _I
     _lib = L
     return L
@@ -165,6 +180,14 @@ def _need(t: torch.Tensor | None, dtype, shape=None, name="tensor", optional=Fal
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _here(*tensors):
+    """The tensors are on the current device, whose stream the call uses."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on device {t.get_device()}, the current one is {dev}")
 
 
 def _need_out(t: torch.Tensor, dtype, shape, name="out"):
@@ -623,6 +646,103 @@ def ep_expert_linear_backward(dy, pre, x, w, counts, psum, act, dpre, dx, dw, db
     _check(rc, "ep_expert_linear_backward")
 
 
+def ep_moe_few_workspace_size(R: int, T_r: int, k: int, E: int, I: int) -> int:
+    return int(load().ep_moe_few_workspace_size(R, T_r, k, E, I))
+
+
+def ep_moe_few(x, topk_idx, topk_weights, w_gu, w_gu_scales, w_down, w_down_scales, act, out,
+               workspace, status=None, stream=None):
+    """A whole layer for at most EP_MOE_FEW_TOKENS tokens: out = sum over a
+    token's slots of weight * W_down (act(W_gate x) * (W_up x)).
+
+    x, out [R, T_r, H] bf16 (out may be x), topk_idx / topk_weights [R, T_r, k],
+    w_gu [E, 2, I, H], w_down [E, H, I] in bf16 (scales None) or E4M3 bytes with
+    ue8m0 scales of 128 x 128 blocks.  Ids outside [-1, E) count as unused, which
+    only the status word says; workspace: alloc_moe_few_workspace."""
+    R, T_r, H = x.shape
+    k = topk_idx.shape[-1]
+    E, two, I, Hw = w_gu.shape
+    if two != 2 or Hw != H:
+        raise ValueError(f"w_gu: shape {tuple(w_gu.shape)}, expected (E, 2, I, {H})")
+    _need(x, torch.bfloat16, name="x")
+    _need(topk_idx, torch.int64, (R, T_r, k), "topk_idx")
+    _need(topk_weights, torch.float32, (R, T_r, k), "topk_weights")
+    if w_gu_scales is None:
+        mode, dtype = EP_FP8_NONE, torch.bfloat16
+        if w_down_scales is not None:
+            raise ValueError("w_down_scales without w_gu_scales")
+    else:
+        mode, dtype = EP_FP8_E4M3_UE8M0, torch.uint8
+        _need(w_gu_scales, torch.uint8, (E, 2, I // 128, H // 128), "w_gu_scales")
+        _need(w_down_scales, torch.uint8, (E, H // 128, I // 128), "w_down_scales")
+    _need(w_gu, dtype, name="w_gu")
+    _need(w_down, dtype, (E, H, I), "w_down")
+    _need(out, torch.bfloat16, (R, T_r, H), "out")
+    _need(workspace, torch.uint8, name="workspace")
+    if status is not None:
+        _need(status, torch.int32, (1,), "status")
+    _here(x, topk_idx, topk_weights, w_gu, w_gu_scales, w_down, w_down_scales, out, workspace, status)
+    rc = load().ep_moe_few(_ptr(x), _ptr(topk_idx), _ptr(topk_weights), _ptr(w_gu), _ptr(w_gu_scales),
+                           _ptr(w_down), _ptr(w_down_scales), mode, R, T_r, k, E, H, I, act,
+                           _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status),
+                           _stream(stream))
+    _check(rc, "ep_moe_few")
+
+
+def ep_orthogonalize_workspace_size(count: int, M: int, N: int) -> int:
+    return int(load().ep_orthogonalize_workspace_size(count, M, N))
+
+
+def _stack(g, steps):
+    """(count, M, N), dtype and coefficients of a stack of matrices [..., M, N]."""
+    if g.dim() < 2:
+        raise ValueError(f"g: shape {tuple(g.shape)}, expected (..., M, N)")
+    if g.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"g: dtype {g.dtype}, expected float32 or bfloat16")
+    _need(g, None, name="g")
+    M, N = g.shape[-2:]
+    abc = [float(v) for step in steps for v in step]
+    if len(abc) != 3 * len(steps):
+        raise ValueError("steps: expected (a, b, c) for every step")
+    return (math.prod(g.shape[:-2]), M, N, EP_DTYPE_F32 if g.dtype == torch.float32 else EP_DTYPE_BF16,
+            (ctypes.c_float * max(1, len(abc)))(*abc))
+
+
+def ep_orthogonalize(g, steps, out, workspace, eps=1e-7, status=None, stream=None):
+    """out = Newton-Schulz orthogonalisation of every matrix of g [..., M, N] (bf16
+    or fp32); steps: a sequence of (a, b, c), one a step.  out bf16, may be g;
+    workspace: alloc_orthogonalize_workspace.  A wait that ran out is told by
+    status alone."""
+    count, M, N, dtype, abc = _stack(g, steps)
+    _need(out, torch.bfloat16, g.shape, "out")
+    _need(workspace, torch.uint8, name="workspace")
+    if status is not None:
+        _need(status, torch.int32, (1,), "status")
+    _here(g, out, workspace, status)
+    rc = load().ep_orthogonalize(_ptr(g), dtype, count, M, N, len(steps), abc, eps, _ptr(out),
+                                 _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
+    _check(rc, "ep_orthogonalize")
+
+
+def ep_muon_update(g, m, w, w16, steps, workspace, lr, scale=1.0, momentum=0.95, nesterov=True,
+                   weight_decay=0.0, eps=1e-7, status=None, stream=None):
+    """One Muon step on a stack of weights [..., M, N], in place: momentum m and
+    weights w (fp32), their bf16 copy w16 (may be None), from the gradient g (bf16
+    or fp32).  steps and workspace as for ep_orthogonalize."""
+    count, M, N, dtype, abc = _stack(g, steps)
+    _need(m, torch.float32, g.shape, "m")
+    _need(w, torch.float32, g.shape, "w")
+    _need(w16, torch.bfloat16, g.shape, "w16", optional=True)
+    _need(workspace, torch.uint8, name="workspace")
+    if status is not None:
+        _need(status, torch.int32, (1,), "status")
+    _here(g, m, w, w16, workspace, status)
+    rc = load().ep_muon_update(_ptr(g), dtype, _ptr(m), _ptr(w), _ptr(w16), count, M, N, lr, scale,
+                               momentum, int(nesterov), weight_decay, len(steps), abc, eps,
+                               _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
+    _check(rc, "ep_muon_update")
+
+
 def ep_read_status(status, stream=None) -> int:
     _need(status, torch.int32, (1,), "status")
     v = ctypes.c_int32(0)
@@ -723,6 +843,18 @@ def alloc_workspace(R: int, T_r: int, k: int, E: int, H: int, device="cuda", str
     ws = torch.empty((ep_workspace_size(R, T_r, k, E, H),), dtype=torch.uint8, device=device)
     ep_clean_ll_buffer(None, R, E, ws, stream=stream)
     return ws
+
+
+def alloc_moe_few_workspace(R: int, T_r: int, k: int, E: int, I: int, device="cuda"):
+    """Workspace of ep_moe_few."""
+    return torch.empty((ep_moe_few_workspace_size(R, T_r, k, E, I),), dtype=torch.uint8,
+                       device=device)
+
+
+def alloc_orthogonalize_workspace(shape, device="cuda"):
+    """Workspace of ep_orthogonalize and ep_muon_update for a stack [..., M, N]."""
+    size = ep_orthogonalize_workspace_size(math.prod(shape[:-2]), shape[-2], shape[-1])
+    return torch.empty((size,), dtype=torch.uint8, device=device)
 
 
 class LowLatencyBuffers:

@@ -26,7 +26,9 @@
  *    the once-per-rank layout (ep_rank_ids, ep_rank_recv_topk,
  *    ep_rank_combine), the router (ep_gate_topk, ep_gate_topk_backward) and
  *    the experts' products (ep_expert_glu, ep_expert_linear and their
- *    .._backward), the SM budget (ep_set_num_sms, ep_get_num_sms), the
+ *    .._backward), the whole layer for a few tokens (ep_moe_few), the
+ *    optimiser's step on the experts' weights (ep_orthogonalize,
+ *    ep_muon_update), the SM budget (ep_set_num_sms, ep_get_num_sms), the
  *    kernels' number formats (ep_format_e4m3, ep_format_bf16) and plumbing
  *    (ep_workspace_size, ep_read_status, ep_host_wait_counters,
  *    ep_launch_count, ep_error_string).
@@ -325,13 +327,15 @@ int ep_format_bf16(const float* in, uint16_t* out, int64_t n, void* stream);
 /* SM budget (Buffer.num_sms, §2.2; the per-SM bandwidth model of §4.6):
  * caps the SMs that the data kernels of ep_dispatch, ep_ll_dispatch,
  * ep_combine, ep_ll_combine, ep_rank_combine, the router
- * (ep_gate_topk, ep_gate_topk_backward) and the expert calls (ep_expert_*:
- * products and the gradients' elementwise half) occupy, so the
+ * (ep_gate_topk, ep_gate_topk_backward), the expert calls (ep_expert_*:
+ * products and the gradients' elementwise half), ep_moe_few, ep_orthogonalize
+ * and ep_muon_update occupy, so the
  * rest of the GPU stays free for work that overlaps them.  num_sms = 0 lifts the cap
  * (every SM; the default); num_sms > 0 launches those kernels with at most
  * min(num_sms, SM count) CTAs of one per SM.  The single-launch low-latency
  * path then runs on that many SMs if the batch still fits them, else the
- * multi-kernel path is taken.  The bf16 expert products (and the gradients')
+ * multi-kernel path is taken.  The bf16 expert products (and the gradients', and those of
+ * ep_orthogonalize and ep_muon_update)
  * run on pairs of SMs: on the largest even number within the cap, but two at
  * least.  The layout and notify kernels (a few
  * microseconds, one CTA per id chunk / one CTA) are not capped.  Process-
@@ -438,6 +442,81 @@ int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, co
                               const int32_t* counts, const int64_t* psum, int R, int E, int K,
                               int N, int64_t cap_rows, int act, void* dpre, void* dx, void* dw,
                               void* dbias, int32_t* status, void* stream);
+
+/* ---- the whole layer for a few tokens ------------------------------------
+ * out[t] = sum over the used slots j of topk_weights[t][j] * (W_down[e] h),
+ * h = act(W_gate[e] x[t]) * (W_up[e] x[t]), e = topk_idx[t][j]: what layout,
+ * dispatch, ep_expert_glu, ep_expert_linear and combine compute, straight from
+ * the routed tokens in two kernels, for batches that are bound by reading each
+ * used expert's weights once.
+ *   x            [R, T_r, H] bf16, R * T_r <= EP_MOE_FEW_TOKENS
+ *   topk_idx / topk_weights [R, T_r, k] int64 / fp32; -1: unused slot, whose
+ *                weight is not read; a token without a used slot comes out as +0
+ *                and its x is not read.  An expert named twice counts twice.
+ *   w_gu         [E, 2, I, H] (gate, then up), w_down [E, H, I]: bf16
+ *                (EP_FP8_NONE, scales NULL), or E4M3 with one ue8m0 byte per
+ *                128 x 128 block (EP_FP8_E4M3_UE8M0; scales [E, 2, I/128, H/128]
+ *                and [E, H/128, I/128]; scale byte 255 is NaN).  x and h stay
+ *                bf16 either way: nothing is quantised here.
+ *   out          [R, T_r, H] bf16; may be x itself
+ *   workspace    ep_moe_few_workspace_size bytes, 16-byte aligned, no
+ *                initialisation; calls that share one must be ordered
+ * Sums run in 32 bits in an order that neither the SM budget nor the batch's
+ * other tokens change (over the slots: by expert, then by slot); h and out are
+ * rounded to bf16 once each.  Ids outside [-1, E) set EP_ERR_INVALID_ARG in
+ * *status and count as unused; a wait that runs out sets EP_ERR_TIMEOUT and
+ * leaves outputs incomplete.  Limits: H, I multiples of 8 (128 with E4M3),
+ * E * H and E * I below 2^31, act as for ep_expert_glu. */
+#define EP_MOE_FEW_TOKENS 64
+size_t ep_moe_few_workspace_size(int R, int T_r, int k, int E, int I);
+int ep_moe_few(const void* x, const int64_t* topk_idx, const float* topk_weights, const void* w_gu,
+               const uint8_t* w_gu_scales, const void* w_down, const uint8_t* w_down_scales,
+               int fp8_mode, int R, int T_r, int k, int E, int H, int I, int act, void* out,
+               void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ---- the experts' weights: orthogonalised update ------------------------
+ * Newton-Schulz orthogonalisation of every matrix of a stack (Muon: Jordan et
+ * al., 2024), with X [M, N], S = min(M, N):
+ *   X = G / (|G| + eps), |G| the Frobenius norm
+ *   `steps` times: X <- a X + (b A + c A^2) X,  A = X X^T      (M <= N)
+ *                  X <- a X + X (b A + c A^2),  A = X^T X      (M > N)
+ * coefficients: HOST array [steps][3] of a, b, c, read before the call returns.
+ * A step with c = 0 costs no A^2.  The weights' gradients that the experts'
+ * backward calls leave are such stacks: [E, 2, I, H] is 2 E matrices of I x H.
+ * The products take fp16 operands (11 significant bits; X and the polynomial
+ * are held 2^8 times as large) with sums in 32 bits; the term a X is carried in
+ * two fp16 words (22 bits), since its rounding is what small singular values
+ * are multiplied with.  So the matrices of a step must stay below 2^8 in size,
+ * which polynomials that map [0, 1] near it do; beyond it they turn infinite.
+ * A matrix with an infinity or NaN, or whose norm passes 2^60, comes out as NaN;
+ * the others are not touched by it.  Zeros come out as zeros.
+ *   g            [count, M, N] EP_DTYPE_BF16 or EP_DTYPE_F32
+ *   out          [count, M, N] bf16; may be g itself (bf16)
+ *   workspace    ep_orthogonalize_workspace_size bytes, 16-byte aligned, no
+ *                initialisation; calls that share one must be ordered
+ * Limits: M >= 1, N a multiple of 8, M and N at most 2^20, count at most 65535,
+ * count * M below 2^31, 1 <= steps <= 32, eps >= 1e-12, finite coefficients;
+ * pointers 16-byte aligned.  Results do not depend on the SM budget.  A wait that runs
+ * out sets EP_ERR_TIMEOUT in *status and leaves outputs incomplete. */
+size_t ep_orthogonalize_workspace_size(int count, int M, int N);
+int ep_orthogonalize(const void* g, int dtype, int count, int M, int N, int steps,
+                     const float* coefficients, float eps, void* out, void* workspace,
+                     size_t workspace_bytes, int32_t* status, void* stream);
+
+/* One optimiser step on a stack of weights:
+ *   m <- momentum m + g
+ *   u = g + momentum m (nesterov != 0, m already updated) or m
+ *   w <- (1 - lr weight_decay) w - lr scale O(u),  O as ep_orthogonalize
+ *   w16 = w rounded to bf16
+ * g [count, M, N] EP_DTYPE_BF16 or EP_DTYPE_F32 (read only), m and w [count, M, N]
+ * fp32, w16 [count, M, N] bf16 or NULL; m, w and w16 are updated in place.  The host's
+ * numbers are read before the call returns (a captured call keeps them).  The
+ * workspace, limits and errors are ep_orthogonalize's; momentum in [0, 1), lr, scale
+ * and weight_decay finite. */
+int ep_muon_update(const void* g, int dtype, float* m, float* w, void* w16, int count, int M, int N,
+                   float lr, float scale, float momentum, int nesterov, float weight_decay, int steps,
+                   const float* coefficients, float eps, void* workspace, size_t workspace_bytes,
+                   int32_t* status, void* stream);
 
 /* Number of kernels this library has launched in the process. */
 uint64_t ep_launch_count(void);
