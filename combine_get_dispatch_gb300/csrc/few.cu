@@ -1,103 +1,499 @@
 // few.cu -- a whole mixture-of-experts layer for a few tokens, in two kernels.
+//
+//   k_few<.., kIn>    h = act(Wg x) * (Wu x)   for every slot (a token and one of its experts)
+//   k_few<.., kOut>   out = sum over a token's slots of weight * (W_down h)
+//
+// Both are bound by reading each used expert's weights once.  The first deals
+// out (expert, h column) pairs evenly over the CTAs, the second output columns, so
+// that every CTA sums its own columns over all experts in a fixed order and
+// nothing is added up between CTAs.  A CTA walks its columns in units: 16 columns'
+// rows of gate and up, or 32 rows of W_down, whole in the inner index, for up to 32
+// tokens of the expert.  One warp copies 1 KB pieces of those rows and of the
+// tokens' rows into a ring of stages (cp.async.bulk); the others take the inner
+// index of a stage apart between them, multiply on the tensor cores with the
+// weights' rows as the first operand and 8 tokens as the second (m16n8k16, at
+// a few tokens an expert the widest form that is not mostly padding: tcgen05
+// wants 64 rows or more in tiles of their own, and an SM gets 13 to 110 columns),
+// and add their sums up in shared memory once a unit.
+//
+// The second kernel comes up as the first one's CTAs leave and fills its ring with
+// weights before it waits for h.
 
 #include "expert.cuh"
+#include "umma.cuh"
 
 namespace ep {
 
-constexpr int kFewThreads = 256;
+constexpr int kConsumers = 8;                       // warps that multiply
+constexpr int kFewThreads = (kConsumers + 1) * kWarp;
+constexpr int kPiece = 1024;                        // bytes of a weight row in a stage
+constexpr int kPitch = kPiece + 64;                 // 8 lanes' 16 bytes of two rows side by side: no bank twice
+constexpr int kUnitRows = 32;
+constexpr int kPass = 32;                           // tokens of an expert taken at a time
+constexpr int kRedPitch = 36;                       // floats: a quarter-warp's sums fall into distinct banks
+constexpr int kMaxSlots = EP_MOE_FEW_TOKENS * kMaxK;
+constexpr int kMaxFewStages = 8;
+constexpr int kFewSmem = 226 * 1024;
 
 struct FewParams {
-  const __nv_bfloat16* x;      // [T, H]
+  const uint8_t* w;            // bf16 or E4M3: [E, 2, I, H] or [E, H, I]
+  const uint8_t* scales;
+  const __nv_bfloat16* v;      // kIn: x [T, H]; kOut: h [T k, I]
   const int64_t* idx;          // [T, k]
   const float* weights;
-  const uint8_t* w_gu;         // bf16 or E4M3
-  const uint8_t* gu_scales;
-  const uint8_t* w_down;
-  const uint8_t* down_scales;
-  __nv_bfloat16* h;            // [T k, I], workspace
-  __nv_bfloat16* out;
+  __nv_bfloat16* out;          // kIn: h; kOut: out [T, H]
   int32_t* status;
-  int T, k, E, H, I;
+  int T, k, E, K, N;           // K: inner extent; N: columns of h or out
 };
 
-__device__ __forceinline__ float scale_of(uint32_t b) {
+// What every CTA works out first: the used experts in rising order, and their
+// slots in rising order.
+struct FewLists {
+  int16_t slot[kMaxSlots];
+  int16_t id[kMaxSlots];        // expert of a slot, -1: unused
+  int16_t rank[kMaxSlots];      // among its expert's slots
+  int16_t expert[kMaxE];
+  int16_t first[kMaxE + 1];     // of the used expert's slots in `slot`
+  int count[kMaxE];
+  int used, most;               // used experts; slots of the largest
+};
+
+struct FewShared {
+  uint64_t full[kMaxFewStages], empty[kMaxFewStages];
+  FewLists lists;
+  float sums[EP_MOE_FEW_TOKENS * kUnitRows];   // kOut: the columns in hand, [token][column]
+};
+
+__device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, bool report) {
+  const int n = p.T * p.k, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < p.E; e += kFewThreads) l.count[e] = 0;
+  for (int i = threadIdx.x; i < n; i += kFewThreads) {
+    const int64_t e = p.idx[i];
+    const bool fits = e >= 0 && e < p.E;
+    if (report && !fits && e != -1) set_status(p.status, EP_ERR_INVALID_ARG);
+    l.id[i] = fits ? (int16_t)e : (int16_t)-1;
+  }
+  __syncthreads();
+  if (threadIdx.x < kWarp) {
+    for (int i0 = 0; i0 < n; i0 += kWarp) {   // 32 slots at a time: their places among the expert's
+      const int e = i0 + lane < n ? l.id[i0 + lane] : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      const int before = e >= 0 ? l.count[e] : 0, at = __popc(same & lanemask_lt());
+      __syncwarp();
+      if (e >= 0) {
+        l.rank[i0 + lane] = (int16_t)(before + at);
+        if (at == 0) l.count[e] = before + __popc(same);
+      }
+      __syncwarp();
+    }
+    int used = 0, first = 0, most = 0;
+    for (int e0 = 0; e0 < p.E; e0 += kWarp) {
+      const int c = e0 + lane < p.E ? l.count[e0 + lane] : 0;
+      const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
+      if (some == 0) continue;
+      int upto = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (c > 0) {
+        const int d = used + __popc(some & lanemask_lt());
+        l.expert[d] = (int16_t)(e0 + lane);
+        l.first[d] = (int16_t)(first + upto - c);
+        l.count[e0 + lane] = first + upto - c;   // from here on: where the expert's slots start
+      }
+      used += __popc(some);
+      first += __shfl_sync(0xffffffffu, upto, 31);
+      most = max(most, __reduce_max_sync(0xffffffffu, c));
+    }
+    if (lane == 0) {
+      l.first[used] = (int16_t)first;
+      l.used = used;
+      l.most = most;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kFewThreads)
+    if (l.id[i] >= 0) l.slot[l.count[l.id[i]] + l.rank[i]] = (int16_t)i;
+  __syncthreads();
+}
+
+// A CTA's units, one after another: `cols` columns from `col` on of used expert d,
+// for the tokens s0 .. s0 + m of the lists.
+template <bool kIn>
+struct FewWalk {
+  const FewLists* l;
+  int N, at, end;        // kIn: (expert, column) pairs; kOut: columns
+  int d, col, cols, s0, m;
+  bool last;             // kOut: of these columns
+
+  __device__ __forceinline__ FewWalk(const FewLists& lists, int n) {
+    l = &lists;
+    N = n;
+    const int64_t all = kIn ? (int64_t)lists.used * n : n;
+    at = (int)(all * blockIdx.x / gridDim.x);
+    end = (int)(all * (blockIdx.x + 1) / gridDim.x);
+    d = -1;
+    cols = s0 = m = 0;
+  }
+  __device__ __forceinline__ bool next() {
+    if (d >= 0 && s0 + m < l->first[d + 1]) {   // more tokens of the expert
+      s0 += m;
+    } else {
+      if (kIn) {
+        at += cols;
+        if (at >= end) return false;
+        d = at / N;
+        col = at - d * N;
+        cols = min(min(kUnitRows / 2, N - col), end - at);
+      } else {
+        if (d < 0 || d + 1 == l->used) {
+          if (d >= 0) at += cols;
+          if (at >= end || l->used == 0) return false;
+          d = 0;
+          col = at;
+          cols = min(kUnitRows, end - at);
+        } else {
+          ++d;
+        }
+      }
+      s0 = l->first[d];
+    }
+    m = min(kPass, l->first[d + 1] - s0);
+    last = d + 1 == l->used && s0 + m == l->first[d + 1];
+    return true;
+  }
+  // Column of row r of the unit, -1 for a row that is none; kIn: up says which half.
+  __device__ __forceinline__ int column(int r, bool& up) const {
+    const int c = kIn ? (r >> 4) * 8 + (r & 7) : r;
+    up = kIn && (r & 8);
+    return c < cols ? col + c : -1;
+  }
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// E4M3 bytes 0 and 2 (1 and 3) of a word as bf16: the byte's exponent and fraction
+// fields set lowest in bf16's give 2^-120 of the value, subnormals too; one exact
+// product brings them up.  (The NaN code would read as 480: found apart.)
+__device__ __forceinline__ uint32_t times_2_120(uint32_t v) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7b807b80u));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_even(uint32_t w) { return times_2_120(((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u)); }
+__device__ __forceinline__ uint32_t e4m3_odd(uint32_t w) { return times_2_120(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u)); }
+// High bits set in the bytes that are NaN.
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+__device__ __forceinline__ float ue8m0_value(uint32_t b) {
   return b == 255 ? __uint_as_float(0x7fc00000u) : b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
 }
 
-// Sum over the row of 8 elements a lane and step.
-template <bool kFp8>
-__device__ __forceinline__ float dot(const uint8_t* w, int64_t row, const uint8_t* scales, int64_t scale_row, const __nv_bfloat16* v, int K, int lane) {
-  float sum = 0.0f;
-  for (int c = lane; c < K; c += 32) {
-    float a;
-    if (kFp8) {
-      __half_raw r = __nv_cvt_fp8_to_halfraw(w[row * K + c], __NV_E4M3);
-      a = __half2float(__half(r)) * scale_of(scales[scale_row * (K / kFp8Block) + c / kFp8Block]);
-    } else {
-      a = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[row * K + c]);
+template <bool kFp8, bool kIn, int kAct>
+__global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
+  constexpr int kOne = kFp8 ? 1 : 2;                 // bytes of a weight
+  constexpr int kChunk = kPiece / kOne;              // inner elements of a stage
+  constexpr int kTokenPitch = kFp8 ? 2 * kPiece + 16 : kPitch;
+  constexpr int kStep = kFp8 ? 64 : 32;              // inner elements a warp multiplies at a time: 16 bytes of weights a lane
+  extern __shared__ uint8_t raw[];
+  FewShared& sh = *reinterpret_cast<FewShared*>(raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxFewStages; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], kConsumers);
     }
-    sum = fmaf(a, __bfloat162float(v[c]), sum);
+    fence_barrier_init();
   }
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
-}
+  if (kIn) {
+    pdl_wait();   // ids and tokens may come from the kernel before
+    pdl_launch_dependents();
+  }
+  few_lists(p, sh.lists, kIn && blockIdx.x == 0);
+  const FewLists& l = sh.lists;
+  const int groups_most = (min(l.most, kPass) + 7) / 8;
+  const int red_bytes = kConsumers * groups_most * 8 * kRedPitch * 4;
+  const int stage_bytes = kUnitRows * kPitch + groups_most * 8 * kTokenPitch;
+  uint8_t* const red_base = raw + (sizeof(FewShared) + 127) / 128 * 128;
+  uint8_t* const ring = red_base + red_bytes;
+  const int stages = min(kMaxFewStages, (int)((kFewSmem - (int)(ring - raw)) / stage_bytes));
+  const int chunks = (p.K + kChunk - 1) / kChunk;
+  bool ok = true;
 
-// h of every slot: a warp an element.
-template <bool kFp8, int kAct>
-__global__ void __launch_bounds__(kFewThreads) k_few_in(FewParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kFewThreads / kWarp), n = (int64_t)p.T * p.k * p.I;
-  for (int64_t at = (int64_t)blockIdx.x * (kFewThreads / kWarp) + threadIdx.x / kWarp; at < n; at += warps) {
-    const int slot = (int)(at / p.I), i = (int)(at - (int64_t)slot * p.I);
-    const int64_t e = p.idx[slot];
-    if (e < 0 || e >= p.E) {
-      if (lane == 0 && e != -1) set_status(p.status, EP_ERR_INVALID_ARG);
-      continue;
+  if (warp == kConsumers) {
+    // ---------------------------------------------------------------- copies
+    // one row a lane; kOut: the weights of the first stages before h is there
+    const int64_t each = (int64_t)p.N * p.K;          // elements of an expert's matrix (kIn: of its gate)
+    auto weights_of = [&](const FewWalk<kIn>& w, int c, int s) {
+      bool up;
+      const int n = w.column(lane, up);
+      if (n < 0) return;
+      const int64_t e = l.expert[w.d];
+      const int64_t row = kIn ? (e * 2 + up) * each + (int64_t)n * p.K : e * each + (int64_t)n * p.K;
+      tma_load_1d(ring + s * stage_bytes + lane * kPitch, p.w + (row + (int64_t)c * kChunk) * kOne, min(kChunk, p.K - c * kChunk) * kOne, &sh.full[s]);
+    };
+    auto tokens_of = [&](const FewWalk<kIn>& w, int c, int s) {
+      if (lane >= w.m) return;
+      const int slot = l.slot[w.s0 + lane];
+      const int64_t row = (int64_t)(kIn ? slot / p.k : slot) * p.K;
+      tma_load_1d(ring + s * stage_bytes + kUnitRows * kPitch + lane * kTokenPitch, p.v + row + c * kChunk, min(kChunk, p.K - c * kChunk) * 2, &sh.full[s]);
+    };
+    auto expect = [&](const FewWalk<kIn>& w, int c, int s) {
+      const int k = min(kChunk, p.K - c * kChunk);
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], (kIn ? 2 : 1) * w.cols * k * kOne + w.m * k * 2);
+      __syncwarp();
+    };
+    FewWalk<kIn> w(l, p.N);
+    int c = 0, s = 0;
+    uint32_t phase = 0;
+    bool more = w.next();
+    if (!kIn) {
+      FewWalk<kIn> ahead = w;
+      int ca = 0, filled = 0;
+      for (bool go = more; go && filled < stages; ++filled) {
+        expect(ahead, ca, filled);
+        weights_of(ahead, ca, filled);
+        if (++ca == chunks) {
+          ca = 0;
+          go = ahead.next();
+        }
+      }
+      pdl_wait();
+      for (int i = 0; i < filled; ++i) {
+        tokens_of(w, c, i);
+        if (++c == chunks) {
+          c = 0;
+          more = w.next();
+        }
+      }
+      if (filled == stages) phase = 1;
+      s = filled == stages ? 0 : filled;
     }
-    const __nv_bfloat16* v = p.x + (int64_t)(slot / p.k) * p.H;
-    const int64_t row = e * 2 * p.I + i, block = e * 2 * (p.I / kFp8Block) + i / kFp8Block;
-    const float gate = dot<kFp8>(p.w_gu, row, p.gu_scales, block, v, p.H, lane);
-    const float up = dot<kFp8>(p.w_gu, row + p.I, p.gu_scales, block + p.I / kFp8Block, v, p.H, lane);
-    if (lane == 0) p.h[at] = __float2bfloat16_rn(act_value<kAct>(gate) * up);
-  }
-}
-
-// out: a warp an element, its token's slots in order of their experts.
-template <bool kFp8>
-__global__ void __launch_bounds__(kFewThreads) k_few_out(FewParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kFewThreads / kWarp), n = (int64_t)p.T * p.H;
-  for (int64_t at = (int64_t)blockIdx.x * (kFewThreads / kWarp) + threadIdx.x / kWarp; at < n; at += warps) {
-    const int t = (int)(at / p.H), c = (int)(at - (int64_t)t * p.H);
-    const int64_t* idx = p.idx + (int64_t)t * p.k;
-    float sum = 0.0f;
-    for (int64_t last = -1;;) {   // the next expert above the last one
-      int64_t e = p.E;
-      for (int j = 0; j < p.k; ++j)
-        if (idx[j] > last && idx[j] < e) e = idx[j];
-      if (e >= p.E) break;
-      last = e;
-      for (int j = 0; j < p.k; ++j) {
-        if (idx[j] != e) continue;
-        const int slot = t * p.k + j;
-        const float y = dot<kFp8>(p.w_down, e * p.H + c, p.down_scales, e * (p.H / kFp8Block) + c / kFp8Block, p.h + (int64_t)slot * p.I, p.I, lane);
-        sum = fmaf(p.weights[slot], y, sum);
+    while (more) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
+      if (!ok) break;
+      expect(w, c, s);
+      weights_of(w, c, s);
+      tokens_of(w, c, s);
+      if (++s == stages) {
+        s = 0;
+        phase ^= 1;
+      }
+      if (++c == chunks) {
+        c = 0;
+        more = w.next();
       }
     }
-    if (lane == 0) p.out[at] = __float2bfloat16_rn(sum);
+    if (!ok) {   // give the copies in flight time to land before the memory goes
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- products
+    const int g = lane >> 2, t = lane & 3;
+    float* const red = reinterpret_cast<float*>(red_base);
+    const int red_warp = groups_most * 8 * kRedPitch;
+    int s = 0;
+    uint32_t phase = 0;
+    if (!kIn)
+      for (int i = threadIdx.x; i < p.T * kUnitRows; i += kConsumers * kWarp) sh.sums[i] = 0.0f;
+    FewWalk<kIn> w(l, p.N);
+    while (w.next()) {
+      const int groups = (w.m + 7) / 8;
+      const bool second = w.cols > (kIn ? 8 : 16);     // the upper 16 rows hold some
+      float acc[2][4][4] = {};
+      int64_t scale_row[4];                              // kFp8: of rows g, g + 8, g + 16, g + 24
+      if (kFp8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bool up;
+          const int n = max(0, w.column(g + 8 * i, up));
+          const int64_t e = l.expert[w.d];
+          scale_row[i] = ((kIn ? e * 2 + up : e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
+        }
+      }
+      for (int c = 0; c < chunks; ++c) {
+        const int left = p.K - c * kChunk;               // inner elements from this stage on
+        uint32_t sc[4] = {};
+        const int block = c * (kChunk / kFp8Block) + warp;   // kFp8: this warp's 128 inner elements of the stage
+        if (kFp8 && block * kFp8Block < p.K) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[i] = __ldg(p.scales + scale_row[i] + block);
+        }
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], phase));
+        const uint32_t wa = smem_addr(ring + s * stage_bytes) + g * kPitch + t * 16;
+        const uint32_t va = smem_addr(ring + s * stage_bytes) + kUnitRows * kPitch + g * kTokenPitch + t * (kFp8 ? 32 : 16);
+        if (kFp8) {
+          if (block * kFp8Block < p.K) {
+            float part[2][4][4] = {};
+            uint32_t nan[4] = {};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int k0 = warp * kFp8Block + i * kStep;
+              uint4 r[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) r[q] = q < 2 || second ? ld_shared_v4_at(wa + q * 8 * kPitch + k0) : make_uint4(0, 0, 0, 0);
+              uint32_t b[4][8];   // tokens' elements 0, 2 and 1, 3 of every four
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (j < groups) {
+                  const uint4 lo = ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2), hi = ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2 + 16);
+                  const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                  for (int f = 0; f < 4; ++f) {
+                    b[j][2 * f] = __byte_perm(x[2 * f], x[2 * f + 1], 0x5410);
+                    b[j][2 * f + 1] = __byte_perm(x[2 * f], x[2 * f + 1], 0x7632);
+                  }
+                }
+              }
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                uint32_t wd[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  wd[q] = f == 0 ? r[q].x : f == 1 ? r[q].y : f == 2 ? r[q].z : r[q].w;
+                  nan[q] |= e4m3_nan(wd[q]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  if (h == 1 && !second) break;
+                  const uint32_t a0 = e4m3_even(wd[2 * h]), a1 = e4m3_even(wd[2 * h + 1]);
+                  const uint32_t a2 = e4m3_odd(wd[2 * h]), a3 = e4m3_odd(wd[2 * h + 1]);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    if (j < groups) mma_bf16(part[h][j], a0, a1, a2, a3, b[j][2 * f], b[j][2 * f + 1]);
+                }
+              }
+            }
+            float row_scale[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) row_scale[q] = ue8m0_value(sc[q]);
+            if (__any_sync(0xffffffffu, (nan[0] | nan[1] | nan[2] | nan[3]) != 0)) {   // a NaN makes its row's sums NaN
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t n = nan[q] | __shfl_xor_sync(0xffffffffu, nan[q], 1);
+                n |= __shfl_xor_sync(0xffffffffu, n, 2);
+                if (n != 0) row_scale[q] = __uint_as_float(0x7fc00000u);
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (j < groups) acc[h][j][i] = fmaf(part[h][j][i], row_scale[2 * h + (i >> 1)], acc[h][j][i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kChunk / kStep / kConsumers; ++i) {
+            const int k0 = (warp + i * kConsumers) * kStep;
+            if (k0 < left) {
+              const bool in = k0 + t * 8 < left;          // what lies behind a row is not multiplied
+              uint4 r[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) r[q] = in && (q < 2 || second) ? ld_shared_v4_at(wa + q * 8 * kPitch + k0 * 2) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (j < groups) {
+                  const uint4 b = in ? ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2) : make_uint4(0, 0, 0, 0);
+                  mma_bf16(acc[0][j], r[0].x, r[1].x, r[0].y, r[1].y, b.x, b.y);
+                  mma_bf16(acc[0][j], r[0].z, r[1].z, r[0].w, r[1].w, b.z, b.w);
+                  if (second) {
+                    mma_bf16(acc[1][j], r[2].x, r[3].x, r[2].y, r[3].y, b.x, b.y);
+                    mma_bf16(acc[1][j], r[2].z, r[3].z, r[2].w, r[3].w, b.z, b.w);
+                  }
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[s]);
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      // ---------------------------------------------------------------- the warps' sums
+      named_barrier_sync(1, kConsumers * kWarp);   // the last unit's have been read
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < groups && (h == 0 || second))
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              red[warp * red_warp + (j * 8 + 2 * t + (i & 1)) * kRedPitch + h * 16 + (i >> 1) * 8 + g] = acc[h][j][i];
+      named_barrier_sync(1, kConsumers * kWarp);
+      auto total = [&](int n, int row) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kConsumers; ++q) sum += red[q * red_warp + n * kRedPitch + row];
+        return sum;
+      };
+      if (kIn) {
+        for (int i = threadIdx.x; i < w.m * (kUnitRows / 2); i += kConsumers * kWarp) {
+          const int n = i / (kUnitRows / 2), c = i % (kUnitRows / 2), row = (c >> 3) * 16 + (c & 7);
+          if (c < w.cols)   // rounded to bf16: the second kernel's operand
+            p.out[(int64_t)l.slot[w.s0 + n] * p.N + w.col + c] = __float2bfloat16_rn(act_value<kAct>(total(n, row)) * total(n, row + 8));
+        }
+      } else {
+        for (int i = threadIdx.x; i < w.m * kUnitRows; i += kConsumers * kWarp) {
+          const int n = i / kUnitRows, c = i % kUnitRows, token = l.slot[w.s0 + n] / p.k;
+          if (c >= w.cols || (n > 0 && l.slot[w.s0 + n - 1] / p.k == token)) continue;
+          float sum = sh.sums[token * kUnitRows + c];
+          for (int q = n; q < w.m && l.slot[w.s0 + q] / p.k == token; ++q)   // one, but for an expert named twice
+            sum = fmaf(__ldg(p.weights + l.slot[w.s0 + q]), total(q, c), sum);
+          sh.sums[token * kUnitRows + c] = sum;
+        }
+        if (w.last) {
+          named_barrier_sync(1, kConsumers * kWarp);
+          for (int i = threadIdx.x; i < p.T * kUnitRows; i += kConsumers * kWarp) {
+            const int c = i % kUnitRows;
+            if (c < w.cols) p.out[(int64_t)(i / kUnitRows) * p.N + w.col + c] = __float2bfloat16_rn(sh.sums[i]);
+            sh.sums[i] = 0.0f;
+          }
+        }
+      }
+    }
+    if (!kIn) {
+      pdl_wait();   // (the copying warp has; this one writes where the first kernel may still read)
+      if (l.used == 0)
+        for (int64_t i = (int64_t)blockIdx.x * (kConsumers * kWarp) + threadIdx.x; i < (int64_t)p.T * p.N; i += (int64_t)gridDim.x * (kConsumers * kWarp))
+          p.out[i] = __float2bfloat16_rn(0.0f);
+    }
   }
+  if (!ok) set_status(p.status, EP_ERR_TIMEOUT);
 }
 
-template <bool kFp8, int kAct>
-static int launch_few(const FewParams& p, cudaStream_t s) {
-  const int grid = ep_host::grid_cap(4);
-  k_few_in<kFp8, kAct><<<grid, kFewThreads, 0, s>>>(p);
-  ep_host::count_launch();
-  int rc = ep_host::check_launch();
-  if (rc != EP_OK) return rc;
-  k_few_out<kFp8><<<grid, kFewThreads, 0, s>>>(p);
+template <bool kFp8, bool kIn, int kAct>
+static int launch_few_half(const FewParams& p, cudaStream_t s) {
+  auto* fn = k_few<kFp8, kIn, kAct>;
+  if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(fn), kFewSmem) != EP_OK) return EP_ERR_CUDA;
+  const int grid = ep_host::grid_cap(1);
+  if (!kIn && ep_host::sm_budget_set()) {   // the second kernel's CTAs do not come up beside the first's
+    fn<<<grid, kFewThreads, kFewSmem, s>>>(p);
+  } else if (ep_host::launch_dependent<FewParams>(fn, grid, kFewThreads, kFewSmem, s, p) != EP_OK) {
+    return EP_ERR_CUDA;
+  }
   ep_host::count_launch();
   return ep_host::check_launch();
+}
+
+template <bool kFp8>
+static int launch_few(const FewParams& in, const FewParams& out, int act, cudaStream_t s) {
+  const int rc = act == EP_ACT_RELU   ? launch_few_half<kFp8, true, EP_ACT_RELU>(in, s)
+                 : act == EP_ACT_SILU ? launch_few_half<kFp8, true, EP_ACT_SILU>(in, s)
+                                      : launch_few_half<kFp8, true, EP_ACT_GELU>(in, s);
+  return rc != EP_OK ? rc : launch_few_half<kFp8, false, EP_ACT_NONE>(out, s);
 }
 
 static bool few_sizes(int R, int T_r, int k, int E, int I) {
@@ -131,25 +527,25 @@ extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* t
   if (topk_idx == nullptr || topk_weights == nullptr || workspace_bytes < ep_moe_few_workspace_size(R, T_r, k, E, I))
     return EP_ERR_INVALID_ARG;
   FewParams p{};
-  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.w = static_cast<const uint8_t*>(w_gu);
+  p.scales = w_gu_scales;
+  p.v = static_cast<const __nv_bfloat16*>(x);
   p.idx = topk_idx;
   p.weights = topk_weights;
-  p.w_gu = static_cast<const uint8_t*>(w_gu);
-  p.gu_scales = w_gu_scales;
-  p.w_down = static_cast<const uint8_t*>(w_down);
-  p.down_scales = w_down_scales;
-  p.h = static_cast<__nv_bfloat16*>(workspace);
-  p.out = static_cast<__nv_bfloat16*>(out);
+  p.out = static_cast<__nv_bfloat16*>(workspace);
   p.status = status;
   p.T = R * T_r;
   p.k = k;
   p.E = E;
-  p.H = H;
-  p.I = I;
+  p.K = H;
+  p.N = I;
+  FewParams q = p;
+  q.w = static_cast<const uint8_t*>(w_down);
+  q.scales = w_down_scales;
+  q.v = p.out;
+  q.out = static_cast<__nv_bfloat16*>(out);
+  q.K = I;
+  q.N = H;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  switch (act) {
-    case EP_ACT_RELU: return fp8 ? launch_few<true, EP_ACT_RELU>(p, s) : launch_few<false, EP_ACT_RELU>(p, s);
-    case EP_ACT_SILU: return fp8 ? launch_few<true, EP_ACT_SILU>(p, s) : launch_few<false, EP_ACT_SILU>(p, s);
-    default: return fp8 ? launch_few<true, EP_ACT_GELU>(p, s) : launch_few<false, EP_ACT_GELU>(p, s);
-  }
+  return fp8 ? launch_few<true>(p, q, act, s) : launch_few<false>(p, q, act, s);
 }
