@@ -25,18 +25,18 @@
 namespace ep {
 
 constexpr int kConsumers = 8;                       // warps that multiply
-constexpr int kFewThreads = (kConsumers + 1) * kWarp;
+constexpr int kTokenWarps = 3;                      // warps that copy tokens' rows
+constexpr int kFewThreads = (kConsumers + 1 + kTokenWarps) * kWarp;
 constexpr int kPiece = 1024;                        // bytes of a weight row in a stage
-constexpr int kPitch = kPiece + 64;                 // 8 lanes' 16 bytes of two rows side by side: no bank twice
 constexpr int kUnitRows = 32;
-constexpr int kPass = 32;                           // tokens of an expert taken at a time
 constexpr int kRedPitch = 36;                       // floats: a quarter-warp's sums fall into distinct banks
 constexpr int kMaxSlots = EP_MOE_FEW_TOKENS * kMaxK;
 constexpr int kMaxFewStages = 8;
 constexpr int kFewSmem = 226 * 1024;
+__host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 32; }   // tokens of an expert taken at a time: two stages at least
 
 struct FewParams {
-  const uint8_t* w;            // bf16 or E4M3: [E, 2, I, H] or [E, H, I]
+  CUtensorMap whole, four, one;   // weights [2 E or E][N][K]: boxes of 1 KB of a unit's rows (kIn: of gate or up), 4 and 1
   const uint8_t* scales;
   const __nv_bfloat16* v;      // kIn: x [T, H]; kOut: h [T k, I]
   const int64_t* idx;          // [T, k]
@@ -121,7 +121,7 @@ __device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, bool 
 
 // A CTA's units, one after another: `cols` columns from `col` on of used expert d,
 // for the tokens s0 .. s0 + m of the lists.
-template <bool kIn>
+template <bool kIn, int kPass>
 struct FewWalk {
   const FewLists* l;
   int N, at, end;        // kIn: (expert, column) pairs; kOut: columns
@@ -164,12 +164,6 @@ struct FewWalk {
     last = d + 1 == l->used && s0 + m == l->first[d + 1];
     return true;
   }
-  // Column of row r of the unit, -1 for a row that is none; kIn: up says which half.
-  __device__ __forceinline__ int column(int r, bool& up) const {
-    const int c = kIn ? (r >> 4) * 8 + (r & 7) : r;
-    up = kIn && (r & 8);
-    return c < cols ? col + c : -1;
-  }
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -196,12 +190,13 @@ __device__ __forceinline__ float ue8m0_value(uint32_t b) {
 }
 
 template <bool kFp8, bool kIn, int kAct>
-__global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
+__global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ FewParams p) {
   constexpr int kOne = kFp8 ? 1 : 2;                 // bytes of a weight
   constexpr int kChunk = kPiece / kOne;              // inner elements of a stage
-  constexpr int kTokenPitch = kFp8 ? 2 * kPiece + 16 : kPitch;
+  constexpr int kTokenPitch = kFp8 ? 2 * kPiece + 16 : kPiece + 64;   // 8 lanes' 16 bytes fall into distinct banks
+  constexpr int kPass = pass_of(kFp8), kGroups = kPass / 8;
   constexpr int kStep = kFp8 ? 64 : 32;              // inner elements a warp multiplies at a time: 16 bytes of weights a lane
-  extern __shared__ uint8_t raw[];
+  extern __shared__ __align__(1024) uint8_t raw[];
   FewShared& sh = *reinterpret_cast<FewShared*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -219,75 +214,56 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
   const FewLists& l = sh.lists;
   const int groups_most = (min(l.most, kPass) + 7) / 8;
   const int red_bytes = kConsumers * groups_most * 8 * kRedPitch * 4;
-  const int stage_bytes = kUnitRows * kPitch + groups_most * 8 * kTokenPitch;
+  const int stage_bytes = kUnitRows * kPiece + groups_most * 8 * kTokenPitch;
   uint8_t* const red_base = raw + (sizeof(FewShared) + 127) / 128 * 128;
   uint8_t* const ring = red_base + red_bytes;
   const int stages = min(kMaxFewStages, (int)((kFewSmem - (int)(ring - raw)) / stage_bytes));
   const int chunks = (p.K + kChunk - 1) / kChunk;
+  FewWalk<kIn, kPass> w(l, p.N);
   bool ok = true;
+  int s = 0;
+  uint32_t phase = 0;
 
-  if (warp == kConsumers) {
+  if (warp >= kConsumers) {
     // ---------------------------------------------------------------- copies
-    // one row a lane; kOut: the weights of the first stages before h is there
-    const int64_t each = (int64_t)p.N * p.K;          // elements of an expert's matrix (kIn: of its gate)
-    auto weights_of = [&](const FewWalk<kIn>& w, int c, int s) {
-      bool up;
-      const int n = w.column(lane, up);
-      if (n < 0) return;
-      const int64_t e = l.expert[w.d];
-      const int64_t row = kIn ? (e * 2 + up) * each + (int64_t)n * p.K : e * each + (int64_t)n * p.K;
-      tma_load_1d(ring + s * stage_bytes + lane * kPitch, p.w + (row + (int64_t)c * kChunk) * kOne, min(kChunk, p.K - c * kChunk) * kOne, &sh.full[s]);
-    };
-    auto tokens_of = [&](const FewWalk<kIn>& w, int c, int s) {
-      if (lane >= w.m) return;
-      const int slot = l.slot[w.s0 + lane];
-      const int64_t row = (int64_t)(kIn ? slot / p.k : slot) * p.K;
-      tma_load_1d(ring + s * stage_bytes + kUnitRows * kPitch + lane * kTokenPitch, p.v + row + c * kChunk, min(kChunk, p.K - c * kChunk) * 2, &sh.full[s]);
-    };
-    auto expect = [&](const FewWalk<kIn>& w, int c, int s) {
-      const int k = min(kChunk, p.K - c * kChunk);
-      if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], (kIn ? 2 : 1) * w.cols * k * kOne + w.m * k * 2);
-      __syncwarp();
-    };
-    FewWalk<kIn> w(l, p.N);
-    int c = 0, s = 0;
-    uint32_t phase = 0;
-    bool more = w.next();
-    if (!kIn) {
-      FewWalk<kIn> ahead = w;
-      int ca = 0, filled = 0;
-      for (bool go = more; go && filled < stages; ++filled) {
-        expect(ahead, ca, filled);
-        weights_of(ahead, ca, filled);
-        if (++ca == chunks) {
-          ca = 0;
-          go = ahead.next();
+    // one warp the weights, a unit's rows in two copies (kIn) or one: by rows of 1 KB a warp got through 2.4 TB/s; the
+    // others tokens' rows, one a lane.  kOut: the weights of the first stages before h is there.
+    const bool weights = warp == kConsumers;
+    if (!kIn && !weights) pdl_wait();
+    while (ok && w.next()) {
+      const int e = l.expert[w.d], turn = warp - kConsumers - 1, mine = lane * kTokenWarps + turn;
+      const int slot = !weights && mine < w.m ? l.slot[w.s0 + mine] : -1;
+      const __nv_bfloat16* row = p.v + (int64_t)(kIn ? slot / p.k : slot) * p.K;
+      for (int c = 0; c < chunks; ++c) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
+        if (!ok) break;
+        uint8_t* stage = ring + s * stage_bytes;
+        const int k = min(kChunk, p.K - c * kChunk);
+        if (weights) {
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&sh.full[s], (kIn ? 2 : 1) * w.cols * kPiece + w.m * k * 2);
+            const uint32_t bar = smem_addr(&sh.full[s]);
+            constexpr int kWhole = kIn ? kUnitRows / 2 : kUnitRows;
+            for (int half = 0; half < (kIn ? 2 : 1); ++half) {
+              const uint32_t to = smem_addr(stage) + half * kWhole * kPiece;
+              const int z = kIn ? 2 * e + half : e;
+              if (w.cols == kWhole) {
+                tma_load_3d<false>(to, &p.whole, bar, c * (kPiece / 4), w.col, z);
+              } else {
+                int n = 0;
+                for (; n + 4 <= w.cols; n += 4) tma_load_3d<false>(to + n * kPiece, &p.four, bar, c * (kPiece / 4), w.col + n, z);
+                for (; n < w.cols; ++n) tma_load_3d<false>(to + n * kPiece, &p.one, bar, c * (kPiece / 4), w.col + n, z);
+              }
+            }
+          }
+        } else if (slot >= 0) {
+          tma_load_1d(stage + kUnitRows * kPiece + mine * kTokenPitch, row + c * kChunk, k * 2, &sh.full[s]);
         }
-      }
-      pdl_wait();
-      for (int i = 0; i < filled; ++i) {
-        tokens_of(w, c, i);
-        if (++c == chunks) {
-          c = 0;
-          more = w.next();
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1;
         }
-      }
-      if (filled == stages) phase = 1;
-      s = filled == stages ? 0 : filled;
-    }
-    while (more) {
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
-      if (!ok) break;
-      expect(w, c, s);
-      weights_of(w, c, s);
-      tokens_of(w, c, s);
-      if (++s == stages) {
-        s = 0;
-        phase ^= 1;
-      }
-      if (++c == chunks) {
-        c = 0;
-        more = w.next();
       }
     }
     if (!ok) {   // give the copies in flight time to land before the memory goes
@@ -300,23 +276,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
     const int g = lane >> 2, t = lane & 3;
     float* const red = reinterpret_cast<float*>(red_base);
     const int red_warp = groups_most * 8 * kRedPitch;
-    int s = 0;
-    uint32_t phase = 0;
     if (!kIn)
       for (int i = threadIdx.x; i < p.T * kUnitRows; i += kConsumers * kWarp) sh.sums[i] = 0.0f;
-    FewWalk<kIn> w(l, p.N);
+    // rows q = 0 .. 3 of this lane: kIn gate and up of column g, then of g + 8; kOut g, g + 8, g + 16, g + 24
+    auto row_of = [&](int q) { return kIn ? (q & 1) * 16 + (q >> 1) * 8 + g : q * 8 + g; };
     while (w.next()) {
       const int groups = (w.m + 7) / 8;
       const bool second = w.cols > (kIn ? 8 : 16);     // the upper 16 rows hold some
-      float acc[2][4][4] = {};
-      int64_t scale_row[4];                              // kFp8: of rows g, g + 8, g + 16, g + 24
+      float acc[2][kGroups][4] = {};
+      int64_t scale_row[4];                              // kFp8
       if (kFp8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          bool up;
-          const int n = max(0, w.column(g + 8 * i, up));
+          const int n = min(w.col + (kIn ? (i >> 1) * 8 + g : i * 8 + g), p.N - 1);
           const int64_t e = l.expert[w.d];
-          scale_row[i] = ((kIn ? e * 2 + up : e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
+          scale_row[i] = ((kIn ? e * 2 + (i & 1) : e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
         }
       }
       for (int c = 0; c < chunks; ++c) {
@@ -328,21 +302,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
           for (int i = 0; i < 4; ++i) sc[i] = __ldg(p.scales + scale_row[i] + block);
         }
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], phase));
-        const uint32_t wa = smem_addr(ring + s * stage_bytes) + g * kPitch + t * 16;
-        const uint32_t va = smem_addr(ring + s * stage_bytes) + kUnitRows * kPitch + g * kTokenPitch + t * (kFp8 ? 32 : 16);
+        const uint32_t wa = smem_addr(ring + s * stage_bytes) + t * 16;
+        const uint32_t va = smem_addr(ring + s * stage_bytes) + kUnitRows * kPiece + g * kTokenPitch + t * (kFp8 ? 32 : 16);
         if (kFp8) {
           if (block * kFp8Block < p.K) {
-            float part[2][4][4] = {};
+            float part[2][kGroups][4] = {};
             uint32_t nan[4] = {};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int k0 = warp * kFp8Block + i * kStep;
               uint4 r[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) r[q] = q < 2 || second ? ld_shared_v4_at(wa + q * 8 * kPitch + k0) : make_uint4(0, 0, 0, 0);
-              uint32_t b[4][8];   // tokens' elements 0, 2 and 1, 3 of every four
+              for (int q = 0; q < 4; ++q) r[q] = q < 2 || second ? ld_shared_v4_at(wa + row_of(q) * kPiece + k0) : make_uint4(0, 0, 0, 0);
+              uint32_t b[kGroups][8];   // tokens' elements 0, 2 and 1, 3 of every four
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < kGroups; ++j) {
                 if (j < groups) {
                   const uint4 lo = ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2), hi = ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2 + 16);
                   const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -367,7 +341,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
                   const uint32_t a0 = e4m3_even(wd[2 * h]), a1 = e4m3_even(wd[2 * h + 1]);
                   const uint32_t a2 = e4m3_odd(wd[2 * h]), a3 = e4m3_odd(wd[2 * h + 1]);
 #pragma unroll
-                  for (int j = 0; j < 4; ++j)
+                  for (int j = 0; j < kGroups; ++j)
                     if (j < groups) mma_bf16(part[h][j], a0, a1, a2, a3, b[j][2 * f], b[j][2 * f + 1]);
                 }
               }
@@ -386,7 +360,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
+              for (int j = 0; j < kGroups; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   if (j < groups) acc[h][j][i] = fmaf(part[h][j][i], row_scale[2 * h + (i >> 1)], acc[h][j][i]);
@@ -399,9 +373,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
               const bool in = k0 + t * 8 < left;          // what lies behind a row is not multiplied
               uint4 r[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) r[q] = in && (q < 2 || second) ? ld_shared_v4_at(wa + q * 8 * kPitch + k0 * 2) : make_uint4(0, 0, 0, 0);
+              for (int q = 0; q < 4; ++q) r[q] = in && (q < 2 || second) ? ld_shared_v4_at(wa + row_of(q) * kPiece + k0 * 2) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < kGroups; ++j) {
                 if (j < groups) {
                   const uint4 b = in ? ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2) : make_uint4(0, 0, 0, 0);
                   mma_bf16(acc[0][j], r[0].x, r[1].x, r[0].y, r[1].y, b.x, b.y);
@@ -427,7 +401,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const FewParams p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kGroups; ++j)
           if (j < groups && (h == 0 || second))
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -527,7 +501,6 @@ extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* t
   if (topk_idx == nullptr || topk_weights == nullptr || workspace_bytes < ep_moe_few_workspace_size(R, T_r, k, E, I))
     return EP_ERR_INVALID_ARG;
   FewParams p{};
-  p.w = static_cast<const uint8_t*>(w_gu);
   p.scales = w_gu_scales;
   p.v = static_cast<const __nv_bfloat16*>(x);
   p.idx = topk_idx;
@@ -540,12 +513,19 @@ extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* t
   p.K = H;
   p.N = I;
   FewParams q = p;
-  q.w = static_cast<const uint8_t*>(w_down);
   q.scales = w_down_scales;
   q.v = p.out;
   q.out = static_cast<__nv_bfloat16*>(out);
   q.K = I;
   q.N = H;
+  const int one = fp8 ? 1 : 2;
+  auto maps = [&](FewParams& f, const void* w, int count, int whole) {
+    const uint64_t words = (uint64_t)f.K * one / 4;
+    int rc = ep_host::make_row_map(&f.whole, w, words, f.N, count, whole);
+    if (rc == EP_OK) rc = ep_host::make_row_map(&f.four, w, words, f.N, count, 4);
+    return rc == EP_OK ? ep_host::make_row_map(&f.one, w, words, f.N, count, 1) : rc;
+  };
+  if (maps(p, w_gu, 2 * E, kUnitRows / 2) != EP_OK || maps(q, w_down, E, kUnitRows) != EP_OK) return EP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return fp8 ? launch_few<true>(p, q, act, s) : launch_few<false>(p, q, act, s);
 }
