@@ -24,7 +24,8 @@
 
 namespace ep {
 
-constexpr int kConsumers = 8;                       // warps that multiply
+constexpr int kSplit = 8;                           // parts of a stage's inner index
+constexpr int kConsumers = 2 * kSplit;              // warps that multiply: 16 of a unit's 32 rows each
 constexpr int kTokenWarps = 3;                      // warps that copy tokens' rows
 constexpr int kFewThreads = (kConsumers + 1 + kTokenWarps) * kWarp;
 constexpr int kPiece = 1024;                        // bytes of a weight row in a stage
@@ -33,7 +34,7 @@ constexpr int kRedPitch = 36;                       // floats: a quarter-warp's 
 constexpr int kMaxSlots = EP_MOE_FEW_TOKENS * kMaxK;
 constexpr int kMaxFewStages = 8;
 constexpr int kFewSmem = 226 * 1024;
-__host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 32; }   // tokens of an expert taken at a time: two stages at least
+__host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 24; }   // tokens of an expert taken at a time: two stages at least
 
 struct FewParams {
   CUtensorMap whole, four, one;   // weights [2 E or E][N][K]: boxes of 1 KB of a unit's rows (kIn: of gate or up), 4 and 1
@@ -52,6 +53,7 @@ struct FewLists {
   int16_t slot[kMaxSlots];
   int16_t id[kMaxSlots];        // expert of a slot, -1: unused
   int16_t rank[kMaxSlots];      // among its expert's slots
+  int16_t token[kMaxSlots];     // of slot[i]
   int16_t expert[kMaxE];
   int16_t first[kMaxE + 1];     // of the used expert's slots in `slot`
   int count[kMaxE];
@@ -115,7 +117,11 @@ __device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, bool 
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kFewThreads)
-    if (l.id[i] >= 0) l.slot[l.count[l.id[i]] + l.rank[i]] = (int16_t)i;
+    if (l.id[i] >= 0) {
+      const int at = l.count[l.id[i]] + l.rank[i];
+      l.slot[at] = (int16_t)i;
+      l.token[at] = (int16_t)(i / p.k);
+    }
   __syncthreads();
 }
 
@@ -213,10 +219,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
   few_lists(p, sh.lists, kIn && blockIdx.x == 0);
   const FewLists& l = sh.lists;
   const int groups_most = (min(l.most, kPass) + 7) / 8;
-  const int red_bytes = kConsumers * groups_most * 8 * kRedPitch * 4;
+  const int red_bytes = kSplit * groups_most * 8 * kRedPitch * 4;   // of one unit; the next one's go to a second part
   const int stage_bytes = kUnitRows * kPiece + groups_most * 8 * kTokenPitch;
   uint8_t* const red_base = raw + (sizeof(FewShared) + 127) / 128 * 128;
-  uint8_t* const ring = red_base + red_bytes;
+  uint8_t* const ring = red_base + 2 * red_bytes;
   const int stages = min(kMaxFewStages, (int)((kFewSmem - (int)(ring - raw)) / stage_bytes));
   const int chunks = (p.K + kChunk - 1) / kChunk;
   FewWalk<kIn, kPass> w(l, p.N);
@@ -232,8 +238,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     if (!kIn && !weights) pdl_wait();
     while (ok && w.next()) {
       const int e = l.expert[w.d], turn = warp - kConsumers - 1, mine = lane * kTokenWarps + turn;
-      const int slot = !weights && mine < w.m ? l.slot[w.s0 + mine] : -1;
-      const __nv_bfloat16* row = p.v + (int64_t)(kIn ? slot / p.k : slot) * p.K;
+      const int from = !weights && mine < w.m ? (kIn ? l.token[w.s0 + mine] : l.slot[w.s0 + mine]) : -1;
+      const __nv_bfloat16* row = p.v + (int64_t)from * p.K;
       for (int c = 0; c < chunks; ++c) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
         if (!ok) break;
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
               }
             }
           }
-        } else if (slot >= 0) {
+        } else if (from >= 0) {
           tma_load_1d(stage + kUnitRows * kPiece + mine * kTokenPitch, row + c * kChunk, k * 2, &sh.full[s]);
         }
         __syncwarp();
@@ -273,47 +279,46 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     }
   } else {
     // ---------------------------------------------------------------- products
-    const int g = lane >> 2, t = lane & 3;
-    float* const red = reinterpret_cast<float*>(red_base);
-    const int red_warp = groups_most * 8 * kRedPitch;
+    // 16 rows (h: the lower or the upper ones) by a part (part) of a stage's inner index
+    const int g = lane >> 2, t = lane & 3, part = warp % kSplit, h = warp / kSplit;
+    float* red = reinterpret_cast<float*>(red_base);
+    float* red_next = reinterpret_cast<float*>(red_base + red_bytes);
+    const int red_part = groups_most * 8 * kRedPitch;
+    // this lane's two rows in a stage: kIn gate and up of column 8 h + g; kOut 16 h + g, 16 h + g + 8
+    const int row0 = kIn ? 8 * h + g : 16 * h + g, row1 = row0 + (kIn ? 16 : 8);
     if (!kIn)
       for (int i = threadIdx.x; i < p.T * kUnitRows; i += kConsumers * kWarp) sh.sums[i] = 0.0f;
-    // rows q = 0 .. 3 of this lane: kIn gate and up of column g, then of g + 8; kOut g, g + 8, g + 16, g + 24
-    auto row_of = [&](int q) { return kIn ? (q & 1) * 16 + (q >> 1) * 8 + g : q * 8 + g; };
     while (w.next()) {
       const int groups = (w.m + 7) / 8;
-      const bool second = w.cols > (kIn ? 8 : 16);     // the upper 16 rows hold some
-      float acc[2][kGroups][4] = {};
-      int64_t scale_row[4];                              // kFp8
+      const bool some = w.cols > (kIn ? 8 : 16) * h;   // of these rows
+      float acc[kGroups][4] = {};
+      const uint8_t *scale0 = nullptr, *scale1 = nullptr;
+      uint32_t sc0 = 0, sc1 = 0;
       if (kFp8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = min(w.col + (kIn ? (i >> 1) * 8 + g : i * 8 + g), p.N - 1);
-          const int64_t e = l.expert[w.d];
-          scale_row[i] = ((kIn ? e * 2 + (i & 1) : e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
+        const int blocks_n = p.N / kFp8Block, blocks_k = p.K / kFp8Block;
+        const int64_t e = l.expert[w.d];
+        const int n0 = min(w.col + row0, p.N - 1), n1 = min(w.col + (kIn ? row0 : row1), p.N - 1);
+        scale0 = p.scales + ((kIn ? e * 2 : e) * blocks_n + n0 / kFp8Block) * blocks_k;
+        scale1 = p.scales + ((kIn ? e * 2 + 1 : e) * blocks_n + n1 / kFp8Block) * blocks_k;
+        if (part < blocks_k) {
+          sc0 = __ldg(scale0 + part);
+          sc1 = __ldg(scale1 + part);
         }
       }
       for (int c = 0; c < chunks; ++c) {
-        const int left = p.K - c * kChunk;               // inner elements from this stage on
-        uint32_t sc[4] = {};
-        const int block = c * (kChunk / kFp8Block) + warp;   // kFp8: this warp's 128 inner elements of the stage
-        if (kFp8 && block * kFp8Block < p.K) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[i] = __ldg(p.scales + scale_row[i] + block);
-        }
+        const int left = p.K - c * kChunk;   // inner elements from this stage on
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], phase));
-        const uint32_t wa = smem_addr(ring + s * stage_bytes) + t * 16;
-        const uint32_t va = smem_addr(ring + s * stage_bytes) + kUnitRows * kPiece + g * kTokenPitch + t * (kFp8 ? 32 : 16);
+        const uint32_t at = smem_addr(ring + s * stage_bytes);
+        const uint32_t wa = at + t * 16, va = at + kUnitRows * kPiece + g * kTokenPitch + t * (kFp8 ? 32 : 16);
         if (kFp8) {
-          if (block * kFp8Block < p.K) {
-            float part[2][kGroups][4] = {};
-            uint32_t nan[4] = {};
+          if (some && part * kFp8Block < left) {   // a block of 128 inner elements, whose scale is one a row
+            float sum[kGroups][4] = {};
+            uint32_t nan0 = 0, nan1 = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int k0 = warp * kFp8Block + i * kStep;
-              uint4 r[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) r[q] = q < 2 || second ? ld_shared_v4_at(wa + row_of(q) * kPiece + k0) : make_uint4(0, 0, 0, 0);
+              const int k0 = part * kFp8Block + i * kStep;
+              const uint4 r0 = ld_shared_v4_at(wa + row0 * kPiece + k0), r1 = ld_shared_v4_at(wa + row1 * kPiece + k0);
+              const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
               uint32_t b[kGroups][8];   // tokens' elements 0, 2 and 1, 3 of every four
 #pragma unroll
               for (int j = 0; j < kGroups; ++j) {
@@ -329,61 +334,47 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
               }
 #pragma unroll
               for (int f = 0; f < 4; ++f) {
-                uint32_t wd[4];
+                nan0 |= e4m3_nan(w0[f]);
+                nan1 |= e4m3_nan(w1[f]);
+                const uint32_t a0 = e4m3_even(w0[f]), a1 = e4m3_even(w1[f]), a2 = e4m3_odd(w0[f]), a3 = e4m3_odd(w1[f]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  wd[q] = f == 0 ? r[q].x : f == 1 ? r[q].y : f == 2 ? r[q].z : r[q].w;
-                  nan[q] |= e4m3_nan(wd[q]);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  if (h == 1 && !second) break;
-                  const uint32_t a0 = e4m3_even(wd[2 * h]), a1 = e4m3_even(wd[2 * h + 1]);
-                  const uint32_t a2 = e4m3_odd(wd[2 * h]), a3 = e4m3_odd(wd[2 * h + 1]);
-#pragma unroll
-                  for (int j = 0; j < kGroups; ++j)
-                    if (j < groups) mma_bf16(part[h][j], a0, a1, a2, a3, b[j][2 * f], b[j][2 * f + 1]);
-                }
+                for (int j = 0; j < kGroups; ++j)
+                  if (j < groups) mma_bf16(sum[j], a0, a1, a2, a3, b[j][2 * f], b[j][2 * f + 1]);
               }
             }
-            float row_scale[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) row_scale[q] = ue8m0_value(sc[q]);
-            if (__any_sync(0xffffffffu, (nan[0] | nan[1] | nan[2] | nan[3]) != 0)) {   // a NaN makes its row's sums NaN
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t n = nan[q] | __shfl_xor_sync(0xffffffffu, nan[q], 1);
-                n |= __shfl_xor_sync(0xffffffffu, n, 2);
-                if (n != 0) row_scale[q] = __uint_as_float(0x7fc00000u);
-              }
+            float f0 = ue8m0_value(sc0), f1 = ue8m0_value(sc1);
+            if (__any_sync(0xffffffffu, (nan0 | nan1) != 0)) {   // a NaN makes its row's sums NaN
+              nan0 |= __shfl_xor_sync(0xffffffffu, nan0, 1);
+              nan0 |= __shfl_xor_sync(0xffffffffu, nan0, 2);
+              nan1 |= __shfl_xor_sync(0xffffffffu, nan1, 1);
+              nan1 |= __shfl_xor_sync(0xffffffffu, nan1, 2);
+              if (nan0 != 0) f0 = __uint_as_float(0x7fc00000u);
+              if (nan1 != 0) f1 = __uint_as_float(0x7fc00000u);
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-              for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (j < groups) acc[h][j][i] = fmaf(part[h][j][i], row_scale[2 * h + (i >> 1)], acc[h][j][i]);
+              for (int i = 0; i < 4; ++i)
+                if (j < groups) acc[j][i] = fmaf(sum[j][i], i < 2 ? f0 : f1, acc[j][i]);
           }
-        } else {
+          const int next = (c + 1) * kSplit + part;   // the next stage's scales, while this one's products run
+          if (next * kFp8Block < p.K) {
+            sc0 = __ldg(scale0 + next);
+            sc1 = __ldg(scale1 + next);
+          }
+        } else if (some) {
 #pragma unroll
-          for (int i = 0; i < kChunk / kStep / kConsumers; ++i) {
-            const int k0 = (warp + i * kConsumers) * kStep;
+          for (int i = 0; i < kChunk / kStep / kSplit; ++i) {
+            const int k0 = (part + i * kSplit) * kStep;
             if (k0 < left) {
               const bool in = k0 + t * 8 < left;          // what lies behind a row is not multiplied
-              uint4 r[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) r[q] = in && (q < 2 || second) ? ld_shared_v4_at(wa + row_of(q) * kPiece + k0 * 2) : make_uint4(0, 0, 0, 0);
+              const uint4 r0 = ld_shared_v4_at(wa + row0 * kPiece + k0 * 2), r1 = ld_shared_v4_at(wa + row1 * kPiece + k0 * 2);
 #pragma unroll
               for (int j = 0; j < kGroups; ++j) {
                 if (j < groups) {
                   const uint4 b = in ? ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2) : make_uint4(0, 0, 0, 0);
-                  mma_bf16(acc[0][j], r[0].x, r[1].x, r[0].y, r[1].y, b.x, b.y);
-                  mma_bf16(acc[0][j], r[0].z, r[1].z, r[0].w, r[1].w, b.z, b.w);
-                  if (second) {
-                    mma_bf16(acc[1][j], r[2].x, r[3].x, r[2].y, r[3].y, b.x, b.y);
-                    mma_bf16(acc[1][j], r[2].z, r[3].z, r[2].w, r[3].w, b.z, b.w);
-                  }
+                  mma_bf16(acc[j], r0.x, r1.x, r0.y, r1.y, b.x, b.y);
+                  mma_bf16(acc[j], r0.z, r1.z, r0.w, r1.w, b.z, b.w);
                 }
               }
             }
@@ -397,20 +388,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         }
       }
       // ---------------------------------------------------------------- the warps' sums
-      named_barrier_sync(1, kConsumers * kWarp);   // the last unit's have been read
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
+      if (some) {
 #pragma unroll
         for (int j = 0; j < kGroups; ++j)
-          if (j < groups && (h == 0 || second))
+          if (j < groups)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              red[warp * red_warp + (j * 8 + 2 * t + (i & 1)) * kRedPitch + h * 16 + (i >> 1) * 8 + g] = acc[h][j][i];
+              red[part * red_part + (j * 8 + 2 * t + (i & 1)) * kRedPitch + h * 16 + (i >> 1) * 8 + g] = acc[j][i];
+      }
       named_barrier_sync(1, kConsumers * kWarp);
       auto total = [&](int n, int row) {
         float sum = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kConsumers; ++q) sum += red[q * red_warp + n * kRedPitch + row];
+        for (int q = 0; q < kSplit; ++q) sum += red[q * red_part + n * kRedPitch + row];
         return sum;
       };
       if (kIn) {
@@ -421,10 +411,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         }
       } else {
         for (int i = threadIdx.x; i < w.m * kUnitRows; i += kConsumers * kWarp) {
-          const int n = i / kUnitRows, c = i % kUnitRows, token = l.slot[w.s0 + n] / p.k;
-          if (c >= w.cols || (n > 0 && l.slot[w.s0 + n - 1] / p.k == token)) continue;
+          const int n = i / kUnitRows, c = i % kUnitRows, token = l.token[w.s0 + n];
+          if (c >= w.cols || (n > 0 && l.token[w.s0 + n - 1] == token)) continue;
           float sum = sh.sums[token * kUnitRows + c];
-          for (int q = n; q < w.m && l.slot[w.s0 + q] / p.k == token; ++q)   // one, but for an expert named twice
+          for (int q = n; q < w.m && l.token[w.s0 + q] == token; ++q)   // one, but for an expert named twice
             sum = fmaf(__ldg(p.weights + l.slot[w.s0 + q]), total(q, c), sum);
           sh.sums[token * kUnitRows + c] = sum;
         }
@@ -437,9 +427,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
           }
         }
       }
+      float* const was = red;   // the next unit's sums go elsewhere: these may still be read
+      red = red_next;
+      red_next = was;
     }
     if (!kIn) {
-      pdl_wait();   // (the copying warp has; this one writes where the first kernel may still read)
+      pdl_wait();   // (the copying warps have; this one writes where the first kernel may still read)
       if (l.used == 0)
         for (int64_t i = (int64_t)blockIdx.x * (kConsumers * kWarp) + threadIdx.x; i < (int64_t)p.T * p.N; i += (int64_t)gridDim.x * (kConsumers * kWarp))
           p.out[i] = __float2bfloat16_rn(0.0f);
