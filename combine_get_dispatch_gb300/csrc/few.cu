@@ -7,15 +7,14 @@
 // out (expert, h column) pairs evenly over the CTAs, the second output columns, so
 // that every CTA sums its own columns over all experts in a fixed order and
 // nothing is added up between CTAs.  A CTA walks its columns in units: 16 columns'
-// rows of gate and up, or 32 rows of W_down, whole in the inner index, for up to 32
-// tokens of the expert.  One warp copies 1 KB pieces of those rows and of the
-// tokens' rows into a ring of stages (cp.async.bulk); the others take the inner
-// index of a stage apart between them, multiply on the tensor cores with the
-// weights' rows as the first operand and 8 tokens as the second (m16n8k16, at
-// a few tokens an expert the widest form that is not mostly padding: tcgen05
-// wants 64 rows or more in tiles of their own, and an SM gets 13 to 110 columns),
-// and add their sums up in shared memory once a unit.
-//
+// rows of gate and up, or 32 rows of W_down, whole in the inner index, for the
+// tokens of one expert.  Its warps:
+//   8 multiply: each its eighth of a stage's inner index, 32 weight rows as the
+//     first operand and 8 tokens as the second (m16n8k16: at a few tokens an expert
+//     the widest form that is not mostly padding; tcgen05 wants 64 rows or more in
+//     tiles of their own, and an SM gets 13 to 110 columns)
+//   4 add the eight sums of a unit up and finish it while the next one's products run
+//   1 copies the weights (TMA, 1 KB of each row a stage), the rest tokens' rows
 // The second kernel comes up as the first one's CTAs leave and fills its ring with
 // weights before it waits for h.
 
@@ -24,17 +23,17 @@
 
 namespace ep {
 
-constexpr int kSplit = 8;                           // parts of a stage's inner index
-constexpr int kConsumers = 2 * kSplit;              // warps that multiply: 16 of a unit's 32 rows each
-constexpr int kTokenWarps = 3;                      // warps that copy tokens' rows
-constexpr int kFewThreads = (kConsumers + 1 + kTokenWarps) * kWarp;
-constexpr int kPiece = 1024;                        // bytes of a weight row in a stage
+constexpr int kParts = 8;             // warps that multiply
+constexpr int kAdders = 4;            // warps that add up
+constexpr int kPiece = 1024;          // bytes of a weight row in a stage
 constexpr int kUnitRows = 32;
-constexpr int kRedPitch = 36;                       // floats: a quarter-warp's sums fall into distinct banks
+constexpr int kRedPitch = 36;         // floats: a warp's sums fall into distinct banks
 constexpr int kMaxSlots = EP_MOE_FEW_TOKENS * kMaxK;
 constexpr int kMaxFewStages = 8;
 constexpr int kFewSmem = 226 * 1024;
-__host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 24; }   // tokens of an expert taken at a time: two stages at least
+__host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 24; }        // tokens of an expert taken at a time: two stages at least
+__host__ __device__ constexpr int token_warps_of(bool fp8) { return fp8 ? 3 : 2; }   // fp8: they also turn numbers into fp16
+__host__ __device__ constexpr int few_threads(bool fp8) { return (kParts + kAdders + 1 + token_warps_of(fp8)) * kWarp; }
 
 struct FewParams {
   CUtensorMap whole, four, one;   // weights [2 E or E][N][K]: boxes of 1 KB of a unit's rows (kIn: of gate or up), 4 and 1
@@ -49,125 +48,147 @@ struct FewParams {
 
 // What every CTA works out first: the used experts in rising order, and their
 // slots in rising order.
+struct FewUsed {
+  int16_t expert, first, count, pad;   // slots first .. first + count of the lists
+};
 struct FewLists {
-  int16_t slot[kMaxSlots];
-  int16_t id[kMaxSlots];        // expert of a slot, -1: unused
-  int16_t rank[kMaxSlots];      // among its expert's slots
-  int16_t token[kMaxSlots];     // of slot[i]
-  int16_t expert[kMaxE];
-  int16_t first[kMaxE + 1];     // of the used expert's slots in `slot`
-  int count[kMaxE];
-  int used, most;               // used experts; slots of the largest
+  FewUsed used[kMaxE];
+  int16_t slot[kMaxSlots], token[kMaxSlots];
+  float weight[kMaxSlots];
+  int16_t id[kMaxSlots];               // expert of a slot, -1: unused
+  int16_t start[kMaxE];
+  int group_slots[kMaxE / kWarp], group_used[kMaxE / kWarp], group_most[kMaxE / kWarp];   // of 32 experts
+  int n_used, most;                    // used experts; slots of the largest
 };
 
 struct FewShared {
   uint64_t full[kMaxFewStages], empty[kMaxFewStages];
+  uint64_t red_full[2], red_empty[2];
   FewLists lists;
   float sums[EP_MOE_FEW_TOKENS * kUnitRows];   // kOut: the columns in hand, [token][column]
 };
 
-__device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, bool report) {
-  const int n = p.T * p.k, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < p.E; e += kFewThreads) l.count[e] = 0;
-  for (int i = threadIdx.x; i < n; i += kFewThreads) {
+// masks: a bit a slot for every expert; memory that nothing else uses yet.
+template <int kThreads>
+__device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, uint32_t* masks, bool report) {
+  const int n = p.T * p.k, words = (n + 31) / 32, groups = (p.E + 31) / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < p.E * words; i += kThreads) masks[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     const int64_t e = p.idx[i];
     const bool fits = e >= 0 && e < p.E;
     if (report && !fits && e != -1) set_status(p.status, EP_ERR_INVALID_ARG);
+    if (fits) atomicOr(masks + (int)e * words + (i >> 5), 1u << (i & 31));
     l.id[i] = fits ? (int16_t)e : (int16_t)-1;
   }
   __syncthreads();
-  if (threadIdx.x < kWarp) {
-    for (int i0 = 0; i0 < n; i0 += kWarp) {   // 32 slots at a time: their places among the expert's
-      const int e = i0 + lane < n ? l.id[i0 + lane] : -1;
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      const int before = e >= 0 ? l.count[e] : 0, at = __popc(same & lanemask_lt());
-      __syncwarp();
-      if (e >= 0) {
-        l.rank[i0 + lane] = (int16_t)(before + at);
-        if (at == 0) l.count[e] = before + __popc(same);
-      }
-      __syncwarp();
-    }
-    int used = 0, first = 0, most = 0;
-    for (int e0 = 0; e0 < p.E; e0 += kWarp) {
-      const int c = e0 + lane < p.E ? l.count[e0 + lane] : 0;
-      const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
-      if (some == 0) continue;
-      int upto = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      if (c > 0) {
-        const int d = used + __popc(some & lanemask_lt());
-        l.expert[d] = (int16_t)(e0 + lane);
-        l.first[d] = (int16_t)(first + upto - c);
-        l.count[e0 + lane] = first + upto - c;   // from here on: where the expert's slots start
-      }
-      used += __popc(some);
-      first += __shfl_sync(0xffffffffu, upto, 31);
-      most = max(most, __reduce_max_sync(0xffffffffu, c));
-    }
+  auto count_of = [&](int e) {
+    int c = 0;
+    if (e < p.E)
+      for (int w = 0; w < words; ++w) c += __popc(masks[e * words + w]);
+    return c;
+  };
+  for (int q = warp; q < groups; q += kThreads / kWarp) {
+    const int c = count_of(q * 32 + lane);
+    const int all = __reduce_add_sync(0xffffffffu, c), most = __reduce_max_sync(0xffffffffu, c);
+    const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
     if (lane == 0) {
-      l.first[used] = (int16_t)first;
-      l.used = used;
-      l.most = most;
+      l.group_slots[q] = all;
+      l.group_used[q] = __popc(some);
+      l.group_most[q] = most;
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kFewThreads)
-    if (l.id[i] >= 0) {
-      const int at = l.count[l.id[i]] + l.rank[i];
-      l.slot[at] = (int16_t)i;
-      l.token[at] = (int16_t)(i / p.k);
+  for (int q = warp; q < groups; q += kThreads / kWarp) {
+    const bool before = lane < q;
+    const int slots = __reduce_add_sync(0xffffffffu, before ? l.group_slots[lane] : 0);
+    const int used = __reduce_add_sync(0xffffffffu, before ? l.group_used[lane] : 0);
+    const int c = count_of(q * 32 + lane);
+    int upto = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
+    const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
+    if (c > 0) {
+      const int first = slots + upto - c;
+      l.used[used + __popc(some & lanemask_lt())] = {(int16_t)(q * 32 + lane), (int16_t)first, (int16_t)c, 0};
+      l.start[q * 32 + lane] = (int16_t)first;
+    }
+    if (q == 0) {
+      const int all = __reduce_add_sync(0xffffffffu, lane < groups ? l.group_used[lane] : 0);
+      const int most = __reduce_max_sync(0xffffffffu, lane < groups ? l.group_most[lane] : 0);
+      if (lane == 0) {
+        l.n_used = all;
+        l.most = most;
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int e = l.id[i];
+    if (e < 0) continue;
+    int at = l.start[e] + __popc(masks[e * words + (i >> 5)] & ((1u << (i & 31)) - 1));
+    for (int w = 0; w < (i >> 5); ++w) at += __popc(masks[e * words + w]);
+    l.slot[at] = (int16_t)i;
+    l.token[at] = (int16_t)(i / p.k);
+    l.weight[at] = p.weights[i];
+  }
+  fence_proxy_async_smem();   // copies will land where the masks are
   __syncthreads();
 }
 
-// A CTA's units, one after another: `cols` columns from `col` on of used expert d,
-// for the tokens s0 .. s0 + m of the lists.
+// A CTA's units, one after another: `cols` columns from `col` on of an expert, for
+// the tokens s0 .. s0 + m of the lists.
 template <bool kIn, int kPass>
 struct FewWalk {
   const FewLists* l;
-  int N, at, end;        // kIn: (expert, column) pairs; kOut: columns
-  int d, col, cols, s0, m;
-  bool last;             // kOut: of these columns
+  int N, left;           // kIn: (expert, column) pairs to come, from `col` of expert d on; kOut: columns from `col` on
+  int d, e, col, cols, s0, m, behind;   // behind: the expert's tokens after these
+  bool last;             // kOut: unit of these columns
 
   __device__ __forceinline__ FewWalk(const FewLists& lists, int n) {
     l = &lists;
     N = n;
-    const int64_t all = kIn ? (int64_t)lists.used * n : n;
-    at = (int)(all * blockIdx.x / gridDim.x);
-    end = (int)(all * (blockIdx.x + 1) / gridDim.x);
-    d = -1;
-    cols = s0 = m = 0;
+    const int64_t all = kIn ? (int64_t)lists.n_used * n : lists.n_used > 0 ? n : 0;
+    const int at = (int)(all * blockIdx.x / gridDim.x);
+    left = (int)(all * (blockIdx.x + 1) / gridDim.x) - at;
+    d = kIn ? at / n : lists.n_used - 1;
+    col = kIn ? at - d * n : at;
+    cols = s0 = m = behind = 0;
   }
   __device__ __forceinline__ bool next() {
-    if (d >= 0 && s0 + m < l->first[d + 1]) {   // more tokens of the expert
+    if (behind > 0) {
       s0 += m;
     } else {
       if (kIn) {
-        at += cols;
-        if (at >= end) return false;
-        d = at / N;
-        col = at - d * N;
-        cols = min(min(kUnitRows / 2, N - col), end - at);
-      } else {
-        if (d < 0 || d + 1 == l->used) {
-          if (d >= 0) at += cols;
-          if (at >= end || l->used == 0) return false;
-          d = 0;
-          col = at;
-          cols = min(kUnitRows, end - at);
-        } else {
+        left -= cols;
+        col += cols;
+        if (col == N) {
+          col = 0;
           ++d;
         }
+        if (left <= 0) return false;
+        cols = min(min(kUnitRows / 2, N - col), left);
+      } else {
+        if (++d >= l->n_used) {
+          left -= cols;
+          col += cols;
+          if (left <= 0) return false;
+          cols = min(kUnitRows, left);
+          d = 0;
+        }
       }
-      s0 = l->first[d];
+      const FewUsed u = l->used[d];
+      e = u.expert;
+      s0 = u.first;
+      behind = u.count;
     }
-    m = min(kPass, l->first[d + 1] - s0);
-    last = d + 1 == l->used && s0 + m == l->first[d + 1];
+    m = min(kPass, behind);
+    behind -= m;
+    last = !kIn && behind == 0 && d + 1 == l->n_used;
     return true;
   }
 };
@@ -178,37 +199,229 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// E4M3 bytes 0 and 2 (1 and 3) of a word as bf16: the byte's exponent and fraction
-// fields set lowest in bf16's give 2^-120 of the value, subnormals too; one exact
-// product brings them up.  (The NaN code would read as 480: found apart.)
-__device__ __forceinline__ uint32_t times_2_120(uint32_t v) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7b807b80u));
-  return r;
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t e4m3_even(uint32_t w) { return times_2_120(((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u)); }
-__device__ __forceinline__ uint32_t e4m3_odd(uint32_t w) { return times_2_120(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u)); }
-// High bits set in the bytes that are NaN.
-__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// Four E4M3 numbers as fp16, exactly (one instruction a pair; a bf16 form of them
+// took 12 for the four and bounded the kernels at 3.5-4.0 TB/s of weights).
+__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// So tokens' bf16 numbers are multiplied as fp16: a block of 128 inner elements
+// whose largest is in [2^e, 2^(e+1)) as x 2^(14-e), which is x itself down to
+// 2^-31 of the largest and 2^-39 of the largest off below: far less than sums in 32
+// bits lose.  A block with an infinity or NaN gets the scale NaN.
+// 32 elements a lane, 128 over four lanes; the scale 2^(e-14) by the first of them.
+__device__ __forceinline__ void scaled_f16(const uint4 (&v)[4], uint8_t* to, float* scale, bool first) {
+  const uint32_t w[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
+                          v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+  uint32_t tops[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    tops[i] = w[i] & 0x7fff7fffu;
+#pragma unroll
+    for (int q = 4; q < 16; q += 4) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(tops[i]) : "r"(w[i + q] & 0x7fff7fffu));
+  }
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(tops[0]) : "r"(tops[1]));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(tops[2]) : "r"(tops[3]));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(tops[0]) : "r"(tops[2]));
+  uint32_t top = max(tops[0] >> 16, tops[0] & 0xffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint32_t e = top >> 7;   // biased; up = 2^(141 - e), no more than 2^127
+  const float up = __uint_as_float((e <= 14 ? 254u : 268u - min(e, 254u)) << 23);
+  if (first) *scale = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(e <= 14 ? 0x00400000u : (e - 14) << 23);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t f[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __half2 h = __floats2half2_rn(bf16_lo(w[4 * i + q]) * up, bf16_hi(w[4 * i + q]) * up);
+      f[q] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    st_shared_v4(to + 16 * i, make_uint4(f[0], f[1], f[2], f[3]));
+  }
+}
 
 __device__ __forceinline__ float ue8m0_value(uint32_t b) {
   return b == 255 ? __uint_as_float(0x7fc00000u) : b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
 }
 
+// Where a role is in the ring of stages.
+struct RingPosition {
+  int s;
+  uint32_t phase;
+  int stages, stage_bytes;
+
+  __device__ __forceinline__ void advance() {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ int offset() const { return s * stage_bytes; }
+};
+
+// A token's part of a stage: 8 lanes' 16 bytes (fp8: every second 16) fall into
+// distinct banks; fp8: the scales of its 8 blocks lie behind.
+__host__ __device__ constexpr int token_bytes(bool fp8) { return fp8 ? 2 * kPiece : kPiece; }
+__host__ __device__ constexpr int token_pitch(bool fp8) { return token_bytes(fp8) + (fp8 ? 48 : 64); }
+
+// A warp's eighth of a unit: 32 rows from column col of expert e on, 8 G tokens.
+// Nothing in here branches on what the unit holds (what lies where no row or token
+// does is multiplied and not used): with branches around its loads a stage took
+// 1500 clocks, most of them waiting for one load after the other.
+template <bool kFp8, bool kIn, int G>
+__device__ __forceinline__ void few_products(const FewParams& p, FewShared& sh, int e, int col, const uint8_t* ring, float* red, int chunks,
+                                             uint32_t unit, RingPosition& position, bool& ok) {
+  constexpr int kOne = kFp8 ? 1 : 2, kChunk = kPiece / kOne, kTokenPitch = token_pitch(kFp8);
+  constexpr int kStep = kFp8 ? 64 : 32;   // inner elements a warp multiplies at a time: 16 bytes of weights a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, odd = g & 1;
+  const int k0 = warp * 2 * kStep;        // this warp's first inner element of a stage
+  // this lane's rows of a stage: kIn gate and up of column g, then of g + 8; kOut g, g + 8, g + 16, g + 24
+  auto row_of = [&](int q) { return kIn ? (q & 1) * 16 + (q >> 1) * 8 + g : q * 8 + g; };
+  float acc[2][G][4] = {};
+  const uint8_t* scale[4] = {};
+  uint32_t sc[4] = {};
+  if (kFp8) {
+    const int blocks_n = p.N / kFp8Block, blocks_k = p.K / kFp8Block;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = min(col + (kIn ? (q >> 1) * 8 + g : q * 8 + g), p.N - 1);
+      scale[q] = p.scales + ((int64_t)(kIn ? e * 2 + (q & 1) : e) * blocks_n + n / kFp8Block) * blocks_k;
+      if (warp < blocks_k) sc[q] = __ldg(scale[q] + warp);
+    }
+  }
+  for (int c = 0; c < chunks; ++c) {
+    const int left = p.K - c * kChunk;   // inner elements from this stage on
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[position.s], position.phase));
+    if (k0 < left) {
+      const uint32_t at = smem_addr(ring + position.offset()), tokens = at + kUnitRows * kPiece;
+      const uint32_t wa = at + k0 * kOne + t * 16, va = tokens + g * kTokenPitch + k0 * 2 + t * (kFp8 ? 32 : 16);
+      // Rows lie 1 KB apart, in the same banks: lanes of odd rows read the two steps in the other order, so that
+      // a quarter-warp's two rows fall into different halves of the banks, and swap.
+      uint4 r[4][2];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) r[q][i] = ld_shared_v4_at(wa + row_of(q) * kPiece + (odd ^ i) * 64);
+      if constexpr (kFp8) {   // a block of 128 inner elements, whose scale is one a row and one a token
+        uint4 lo[2][G], hi[2][G];
+        float token[G][2];   // scales of tokens 2 t and 2 t + 1
+        auto tokens_of = [&](int i) {
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            lo[i][j] = ld_shared_v4_at(va + j * 8 * kTokenPitch + i * kStep * 2);
+            hi[i][j] = ld_shared_v4_at(va + j * 8 * kTokenPitch + i * kStep * 2 + 16);
+          }
+        };
+        tokens_of(0);
+        if (G == 1) tokens_of(1);
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            asm volatile("ld.shared.f32 %0, [%1];"
+                         : "=f"(token[j][i])
+                         : "r"(tokens + (j * 8 + 2 * t + i) * kTokenPitch + token_bytes(true) + warp * 4));
+        float sum[2][G][4] = {};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (G > 1 && i == 1) tokens_of(1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w0[4], w1[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              w0[f] = odd ? (&r[2 * h][i ^ 1].x)[f] : (&r[2 * h][i].x)[f];
+              w1[f] = odd ? (&r[2 * h + 1][i ^ 1].x)[f] : (&r[2 * h + 1][i].x)[f];
+            }
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              uint32_t a0, a1, a2, a3;
+              e4m3_to_f16(w0[f], a0, a2);
+              e4m3_to_f16(w1[f], a1, a3);
+#pragma unroll
+              for (int j = 0; j < G; ++j)
+                mma_f16(sum[h][j], a0, a1, a2, a3, f == 0 ? lo[i][j].x : f == 1 ? lo[i][j].z : f == 2 ? hi[i][j].x : hi[i][j].z,
+                        f == 0 ? lo[i][j].y : f == 1 ? lo[i][j].w : f == 2 ? hi[i][j].y : hi[i][j].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f0 = ue8m0_value(sc[2 * h]), f1 = ue8m0_value(sc[2 * h + 1]);
+#pragma unroll
+          for (int j = 0; j < G; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[h][j][i] = fmaf(sum[h][j][i] * token[j][i & 1], i < 2 ? f0 : f1, acc[h][j][i]);
+        }
+      } else {
+        uint4 b[2][G];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < G; ++j) b[i][j] = ld_shared_v4_at(va + j * 8 * kTokenPitch + i * kStep * 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool in = k0 + i * kStep + t * 8 < left;   // what lies behind a token's row is not multiplied (weights are zeros there)
+#pragma unroll
+          for (int j = 0; j < G; ++j)
+            if (!in) b[i][j] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 r0 = odd ? r[2 * h][i ^ 1] : r[2 * h][i], r1 = odd ? r[2 * h + 1][i ^ 1] : r[2 * h + 1][i];
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              mma_bf16(acc[h][j], r0.x, r1.x, r0.y, r1.y, b[i][j].x, b[i][j].y);
+              mma_bf16(acc[h][j], r0.z, r1.z, r0.w, r1.w, b[i][j].z, b[i][j].w);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[position.s]);
+    position.advance();
+    if (kFp8) {   // the next stage's scales
+      const int next = (c + 1) * kParts + warp;
+      if (next * kFp8Block < p.K) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sc[q] = __ldg(scale[q] + next);
+      }
+    }
+  }
+  if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.red_empty[unit & 1], ((unit >> 1) & 1) ^ 1));
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[(j * 8 + 2 * t + (i & 1)) * kRedPitch + h * 16 + (i >> 1) * 8 + g] = acc[h][j][i];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.red_full[unit & 1]);
+}
+
 template <bool kFp8, bool kIn, int kAct>
-__global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(few_threads(kFp8), 1) k_few(const __grid_constant__ FewParams p) {
   constexpr int kOne = kFp8 ? 1 : 2;                 // bytes of a weight
   constexpr int kChunk = kPiece / kOne;              // inner elements of a stage
-  constexpr int kTokenPitch = kFp8 ? 2 * kPiece + 16 : kPiece + 64;   // 8 lanes' 16 bytes fall into distinct banks
-  constexpr int kPass = pass_of(kFp8), kGroups = kPass / 8;
-  constexpr int kStep = kFp8 ? 64 : 32;              // inner elements a warp multiplies at a time: 16 bytes of weights a lane
+  constexpr int kPass = pass_of(kFp8), kTokenWarps = token_warps_of(kFp8), kTokenBytes = token_bytes(kFp8), kTokenPitch = token_pitch(kFp8);
   extern __shared__ __align__(1024) uint8_t raw[];
   FewShared& sh = *reinterpret_cast<FewShared*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxFewStages; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], kConsumers);
+      mbar_init(&sh.full[s], kFp8 ? 1 + kTokenWarps : 1);
+      mbar_init(&sh.empty[s], kParts);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.red_full[b], kParts);
+      mbar_init(&sh.red_empty[b], kAdders);
     }
     fence_barrier_init();
   }
@@ -216,229 +429,177 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     pdl_wait();   // ids and tokens may come from the kernel before
     pdl_launch_dependents();
   }
-  few_lists(p, sh.lists, kIn && blockIdx.x == 0);
-  const FewLists& l = sh.lists;
-  const int groups_most = (min(l.most, kPass) + 7) / 8;
-  const int red_bytes = kSplit * groups_most * 8 * kRedPitch * 4;   // of one unit; the next one's go to a second part
-  const int stage_bytes = kUnitRows * kPiece + groups_most * 8 * kTokenPitch;
   uint8_t* const red_base = raw + (sizeof(FewShared) + 127) / 128 * 128;
+  few_lists<few_threads(kFp8)>(p, sh.lists, reinterpret_cast<uint32_t*>(red_base), kIn && blockIdx.x == 0);
+  const FewLists& l = sh.lists;
+  const int tokens_most = min(l.most, kPass);
+  const int red_part = (tokens_most + 7) / 8 * 8 * kRedPitch;         // floats of one part's sums
+  const int red_bytes = kParts * red_part * 4;                        // of one unit; the next one's go to a second part
+  const int stage_bytes = kUnitRows * kPiece + (tokens_most * kTokenPitch + 127) / 128 * 128;
   uint8_t* const ring = red_base + 2 * red_bytes;
-  const int stages = min(kMaxFewStages, (int)((kFewSmem - (int)(ring - raw)) / stage_bytes));
+  // products read 8 tokens' rows, there or not: seven may lie behind the last stage
+  const int stages = min(kMaxFewStages, (int)((kFewSmem - (int)(ring - raw) - 7 * kTokenPitch) / stage_bytes));
   const int chunks = (p.K + kChunk - 1) / kChunk;
   FewWalk<kIn, kPass> w(l, p.N);
   bool ok = true;
-  int s = 0;
-  uint32_t phase = 0;
+  RingPosition position = {0, 0, stages, stage_bytes};
 
-  if (warp >= kConsumers) {
-    // ---------------------------------------------------------------- copies
-    // one warp the weights, a unit's rows in two copies (kIn) or one: by rows of 1 KB a warp got through 2.4 TB/s; the
-    // others tokens' rows, one a lane.  kOut: the weights of the first stages before h is there.
-    const bool weights = warp == kConsumers;
-    if (!kIn && !weights) pdl_wait();
-    while (ok && w.next()) {
-      const int e = l.expert[w.d], turn = warp - kConsumers - 1, mine = lane * kTokenWarps + turn;
-      const int from = !weights && mine < w.m ? (kIn ? l.token[w.s0 + mine] : l.slot[w.s0 + mine]) : -1;
-      const __nv_bfloat16* row = p.v + (int64_t)from * p.K;
-      for (int c = 0; c < chunks; ++c) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
-        if (!ok) break;
-        uint8_t* stage = ring + s * stage_bytes;
-        const int k = min(kChunk, p.K - c * kChunk);
-        if (weights) {
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&sh.full[s], (kIn ? 2 : 1) * w.cols * kPiece + w.m * k * 2);
-            const uint32_t bar = smem_addr(&sh.full[s]);
-            constexpr int kWhole = kIn ? kUnitRows / 2 : kUnitRows;
-            for (int half = 0; half < (kIn ? 2 : 1); ++half) {
-              const uint32_t to = smem_addr(stage) + half * kWhole * kPiece;
-              const int z = kIn ? 2 * e + half : e;
-              if (w.cols == kWhole) {
-                tma_load_3d<false>(to, &p.whole, bar, c * (kPiece / 4), w.col, z);
-              } else {
-                int n = 0;
-                for (; n + 4 <= w.cols; n += 4) tma_load_3d<false>(to + n * kPiece, &p.four, bar, c * (kPiece / 4), w.col + n, z);
-                for (; n < w.cols; ++n) tma_load_3d<false>(to + n * kPiece, &p.one, bar, c * (kPiece / 4), w.col + n, z);
-              }
-            }
+  if (warp < kParts) {
+    // ---------------------------------------------------------------- products
+    uint32_t unit = 0;
+    while (w.next()) {
+      float* const red = reinterpret_cast<float*>(red_base + (unit & 1) * red_bytes) + warp * red_part;
+      if (w.m <= 8)
+        few_products<kFp8, kIn, 1>(p, sh, w.e, w.col, ring, red, chunks, unit, position, ok);
+      else if (w.m <= 16)
+        few_products<kFp8, kIn, 2>(p, sh, w.e, w.col, ring, red, chunks, unit, position, ok);
+      else
+        few_products<kFp8, kIn, kPass / 8>(p, sh, w.e, w.col, ring, red, chunks, unit, position, ok);
+      ++unit;
+    }
+  } else if (warp < kParts + kAdders) {
+    // ---------------------------------------------------------------- sums
+    const int q = warp - kParts;
+    uint32_t unit = 0;
+    if (!kIn)
+      for (int n = q; n < p.T; n += kAdders) sh.sums[n * kUnitRows + lane] = 0.0f;
+    while (w.next()) {
+      const int b = unit & 1;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.red_full[b], (unit >> 1) & 1, 2 * kWaitNs));
+      const float* const red = reinterpret_cast<const float*>(red_base + b * red_bytes);
+      auto total = [&](int n, int row) {
+        float v[kParts];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) v[i] = red[i * red_part + n * kRedPitch + row];
+        return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      };
+      if (kIn) {
+        const int c = lane & 15, row = (c >> 3) * 16 + (c & 7);
+        for (int n = q * 2 + (lane >> 4); n < w.m; n += 2 * kAdders)
+          if (c < w.cols)   // rounded to bf16: the second kernel's operand
+            p.out[(int64_t)l.slot[w.s0 + n] * p.N + w.col + c] = __float2bfloat16_rn(act_value<kAct>(total(n, row)) * total(n, row + 8));
+      } else {
+        // a token is one warp's, so its slots are added in the lists' order
+        for (int n = 0; n < w.m; ++n) {
+          const int token = l.token[w.s0 + n];
+          if (token % kAdders == q) {
+            float* const sum = sh.sums + token * kUnitRows + lane;
+            *sum = fmaf(l.weight[w.s0 + n], total(n, lane), *sum);
           }
-        } else if (from >= 0) {
-          tma_load_1d(stage + kUnitRows * kPiece + mine * kTokenPitch, row + c * kChunk, k * 2, &sh.full[s]);
         }
-        __syncwarp();
-        if (++s == stages) {
-          s = 0;
-          phase ^= 1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.red_empty[b]);
+      ++unit;
+      if (!kIn && w.last) {
+        for (int n = q; n < p.T; n += kAdders) {
+          if (lane < w.cols) p.out[(int64_t)n * p.N + w.col + lane] = __float2bfloat16_rn(sh.sums[n * kUnitRows + lane]);
+          sh.sums[n * kUnitRows + lane] = 0.0f;
         }
       }
     }
-    if (!ok) {   // give the copies in flight time to land before the memory goes
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 2000000ull) {
+    if (!kIn && l.n_used == 0) {
+      pdl_wait();   // out may be x
+      for (int64_t i = (int64_t)blockIdx.x * (kAdders * kWarp) + q * kWarp + lane; i < (int64_t)p.T * p.N; i += (int64_t)gridDim.x * (kAdders * kWarp))
+        p.out[i] = __float2bfloat16_rn(0.0f);
+    }
+  } else if (warp == kParts + kAdders) {
+    // ---------------------------------------------------------------- weights
+    // a unit's rows in two copies (kIn) or one: by rows of 1 KB, a copy each, a warp got through 2.4 TB/s.  kOut: those of
+    // the first stages before h is there.
+    const bool issue = elect_one();
+    while (ok && w.next()) {
+      for (int c = 0; c < chunks; ++c) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[position.s], position.phase ^ 1));
+        if (!ok) break;
+        if (issue) {
+          const int k = min(kChunk, p.K - c * kChunk);
+          mbar_arrive_expect_tx(&sh.full[position.s], (kIn ? 2 : 1) * w.cols * kPiece + (kFp8 ? 0 : w.m * k * 2));
+          const uint32_t bar = smem_addr(&sh.full[position.s]);
+          constexpr int kWhole = kIn ? kUnitRows / 2 : kUnitRows;
+          for (int half = 0; half < (kIn ? 2 : 1); ++half) {
+            const uint32_t to = smem_addr(ring + position.offset()) + half * kWhole * kPiece;
+            const int z = kIn ? 2 * w.e + half : w.e;
+            if (w.cols == kWhole) {
+              tma_load_3d<false>(to, &p.whole, bar, c * (kPiece / 4), w.col, z);
+            } else {
+              int n = 0;
+              for (; n + 4 <= w.cols; n += 4) tma_load_3d<false>(to + n * kPiece, &p.four, bar, c * (kPiece / 4), w.col + n, z);
+              for (; n < w.cols; ++n) tma_load_3d<false>(to + n * kPiece, &p.one, bar, c * (kPiece / 4), w.col + n, z);
+            }
+          }
+        }
+        __syncwarp();
+        position.advance();
       }
     }
   } else {
-    // ---------------------------------------------------------------- products
-    // 16 rows (h: the lower or the upper ones) by a part (part) of a stage's inner index
-    const int g = lane >> 2, t = lane & 3, part = warp % kSplit, h = warp / kSplit;
-    float* red = reinterpret_cast<float*>(red_base);
-    float* red_next = reinterpret_cast<float*>(red_base + red_bytes);
-    const int red_part = groups_most * 8 * kRedPitch;
-    // this lane's two rows in a stage: kIn gate and up of column 8 h + g; kOut 16 h + g, 16 h + g + 8
-    const int row0 = kIn ? 8 * h + g : 16 * h + g, row1 = row0 + (kIn ? 16 : 8);
-    if (!kIn)
-      for (int i = threadIdx.x; i < p.T * kUnitRows; i += kConsumers * kWarp) sh.sums[i] = 0.0f;
-    while (w.next()) {
-      const int groups = (w.m + 7) / 8;
-      const bool some = w.cols > (kIn ? 8 : 16) * h;   // of these rows
-      float acc[kGroups][4] = {};
-      const uint8_t *scale0 = nullptr, *scale1 = nullptr;
-      uint32_t sc0 = 0, sc1 = 0;
-      if (kFp8) {
-        const int blocks_n = p.N / kFp8Block, blocks_k = p.K / kFp8Block;
-        const int64_t e = l.expert[w.d];
-        const int n0 = min(w.col + row0, p.N - 1), n1 = min(w.col + (kIn ? row0 : row1), p.N - 1);
-        scale0 = p.scales + ((kIn ? e * 2 : e) * blocks_n + n0 / kFp8Block) * blocks_k;
-        scale1 = p.scales + ((kIn ? e * 2 + 1 : e) * blocks_n + n1 / kFp8Block) * blocks_k;
-        if (part < blocks_k) {
-          sc0 = __ldg(scale0 + part);
-          sc1 = __ldg(scale1 + part);
-        }
-      }
-      for (int c = 0; c < chunks; ++c) {
-        const int left = p.K - c * kChunk;   // inner elements from this stage on
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], phase));
-        const uint32_t at = smem_addr(ring + s * stage_bytes);
-        const uint32_t wa = at + t * 16, va = at + kUnitRows * kPiece + g * kTokenPitch + t * (kFp8 ? 32 : 16);
-        if (kFp8) {
-          if (some && part * kFp8Block < left) {   // a block of 128 inner elements, whose scale is one a row
-            float sum[kGroups][4] = {};
-            uint32_t nan0 = 0, nan1 = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int k0 = part * kFp8Block + i * kStep;
-              const uint4 r0 = ld_shared_v4_at(wa + row0 * kPiece + k0), r1 = ld_shared_v4_at(wa + row1 * kPiece + k0);
-              const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-              uint32_t b[kGroups][8];   // tokens' elements 0, 2 and 1, 3 of every four
-#pragma unroll
-              for (int j = 0; j < kGroups; ++j) {
-                if (j < groups) {
-                  const uint4 lo = ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2), hi = ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2 + 16);
-                  const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                  for (int f = 0; f < 4; ++f) {
-                    b[j][2 * f] = __byte_perm(x[2 * f], x[2 * f + 1], 0x5410);
-                    b[j][2 * f + 1] = __byte_perm(x[2 * f], x[2 * f + 1], 0x7632);
-                  }
-                }
-              }
-#pragma unroll
-              for (int f = 0; f < 4; ++f) {
-                nan0 |= e4m3_nan(w0[f]);
-                nan1 |= e4m3_nan(w1[f]);
-                const uint32_t a0 = e4m3_even(w0[f]), a1 = e4m3_even(w1[f]), a2 = e4m3_odd(w0[f]), a3 = e4m3_odd(w1[f]);
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j)
-                  if (j < groups) mma_bf16(sum[j], a0, a1, a2, a3, b[j][2 * f], b[j][2 * f + 1]);
-              }
-            }
-            float f0 = ue8m0_value(sc0), f1 = ue8m0_value(sc1);
-            if (__any_sync(0xffffffffu, (nan0 | nan1) != 0)) {   // a NaN makes its row's sums NaN
-              nan0 |= __shfl_xor_sync(0xffffffffu, nan0, 1);
-              nan0 |= __shfl_xor_sync(0xffffffffu, nan0, 2);
-              nan1 |= __shfl_xor_sync(0xffffffffu, nan1, 1);
-              nan1 |= __shfl_xor_sync(0xffffffffu, nan1, 2);
-              if (nan0 != 0) f0 = __uint_as_float(0x7fc00000u);
-              if (nan1 != 0) f1 = __uint_as_float(0x7fc00000u);
-            }
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (j < groups) acc[j][i] = fmaf(sum[j][i], i < 2 ? f0 : f1, acc[j][i]);
-          }
-          const int next = (c + 1) * kSplit + part;   // the next stage's scales, while this one's products run
-          if (next * kFp8Block < p.K) {
-            sc0 = __ldg(scale0 + next);
-            sc1 = __ldg(scale1 + next);
-          }
-        } else if (some) {
-#pragma unroll
-          for (int i = 0; i < kChunk / kStep / kSplit; ++i) {
-            const int k0 = (part + i * kSplit) * kStep;
-            if (k0 < left) {
-              const bool in = k0 + t * 8 < left;          // what lies behind a row is not multiplied
-              const uint4 r0 = ld_shared_v4_at(wa + row0 * kPiece + k0 * 2), r1 = ld_shared_v4_at(wa + row1 * kPiece + k0 * 2);
-#pragma unroll
-              for (int j = 0; j < kGroups; ++j) {
-                if (j < groups) {
-                  const uint4 b = in ? ld_shared_v4_at(va + j * 8 * kTokenPitch + k0 * 2) : make_uint4(0, 0, 0, 0);
-                  mma_bf16(acc[j], r0.x, r1.x, r0.y, r1.y, b.x, b.y);
-                  mma_bf16(acc[j], r0.z, r1.z, r0.w, r1.w, b.z, b.w);
-                }
-              }
-            }
+    // ---------------------------------------------------------------- tokens
+    const int turn = warp - (kParts + kAdders + 1);
+    if (!kIn) pdl_wait();
+    if constexpr (kFp8) {
+      // a token a warp at a time, the next one's loads before this one is turned into fp16
+      FewWalk<kIn, kPass> ahead = w;
+      int ahead_c = 0, ahead_i = turn;
+      bool go = ahead.next();
+      uint4 next[4];
+      auto load = [&]() {   // the first token from here on that is this warp's
+        while (go && ahead_i >= ahead.m) {
+          ahead_i = turn;
+          if (++ahead_c == chunks) {
+            ahead_c = 0;
+            go = ahead.next();
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[s]);
-        if (++s == stages) {
-          s = 0;
-          phase ^= 1;
-        }
-      }
-      // ---------------------------------------------------------------- the warps' sums
-      if (some) {
+        if (!go || ahead_c * kChunk + lane * 32 >= p.K) return;
+        const int from = kIn ? l.token[ahead.s0 + ahead_i] : l.slot[ahead.s0 + ahead_i];
+        const __nv_bfloat16* row = p.v + (int64_t)from * p.K + ahead_c * kChunk + lane * 32;
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j)
-          if (j < groups)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              red[part * red_part + (j * 8 + 2 * t + (i & 1)) * kRedPitch + h * 16 + (i >> 1) * 8 + g] = acc[j][i];
-      }
-      named_barrier_sync(1, kConsumers * kWarp);
-      auto total = [&](int n, int row) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kSplit; ++q) sum += red[q * red_part + n * kRedPitch + row];
-        return sum;
+        for (int q = 0; q < 4; ++q) next[q] = ld_v4(row + 8 * q);
       };
-      if (kIn) {
-        for (int i = threadIdx.x; i < w.m * (kUnitRows / 2); i += kConsumers * kWarp) {
-          const int n = i / (kUnitRows / 2), c = i % (kUnitRows / 2), row = (c >> 3) * 16 + (c & 7);
-          if (c < w.cols)   // rounded to bf16: the second kernel's operand
-            p.out[(int64_t)l.slot[w.s0 + n] * p.N + w.col + c] = __float2bfloat16_rn(act_value<kAct>(total(n, row)) * total(n, row + 8));
-        }
-      } else {
-        for (int i = threadIdx.x; i < w.m * kUnitRows; i += kConsumers * kWarp) {
-          const int n = i / kUnitRows, c = i % kUnitRows, token = l.token[w.s0 + n];
-          if (c >= w.cols || (n > 0 && l.token[w.s0 + n - 1] == token)) continue;
-          float sum = sh.sums[token * kUnitRows + c];
-          for (int q = n; q < w.m && l.token[w.s0 + q] == token; ++q)   // one, but for an expert named twice
-            sum = fmaf(__ldg(p.weights + l.slot[w.s0 + q]), total(q, c), sum);
-          sh.sums[token * kUnitRows + c] = sum;
-        }
-        if (w.last) {
-          named_barrier_sync(1, kConsumers * kWarp);
-          for (int i = threadIdx.x; i < p.T * kUnitRows; i += kConsumers * kWarp) {
-            const int c = i % kUnitRows;
-            if (c < w.cols) p.out[(int64_t)(i / kUnitRows) * p.N + w.col + c] = __float2bfloat16_rn(sh.sums[i]);
-            sh.sums[i] = 0.0f;
+      load();
+      while (ok && w.next()) {
+        for (int c = 0; c < chunks; ++c) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[position.s], position.phase ^ 1));
+          if (!ok) break;
+          uint8_t* const tokens = ring + position.offset() + kUnitRows * kPiece;
+          for (int i = turn; i < w.m; i += kTokenWarps) {
+            const bool in = c * kChunk + lane * 32 < p.K;
+            uint4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = in ? next[q] : make_uint4(0, 0, 0, 0);
+            ahead_i += kTokenWarps;
+            load();
+            uint8_t* const to = tokens + i * kTokenPitch;
+            scaled_f16(v, to + lane * 64, reinterpret_cast<float*>(to + kTokenBytes) + (lane >> 2), (lane & 3) == 0);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[position.s]);
+          position.advance();
         }
       }
-      float* const was = red;   // the next unit's sums go elsewhere: these may still be read
-      red = red_next;
-      red_next = was;
-    }
-    if (!kIn) {
-      pdl_wait();   // (the copying warps have; this one writes where the first kernel may still read)
-      if (l.used == 0)
-        for (int64_t i = (int64_t)blockIdx.x * (kConsumers * kWarp) + threadIdx.x; i < (int64_t)p.T * p.N; i += (int64_t)gridDim.x * (kConsumers * kWarp))
-          p.out[i] = __float2bfloat16_rn(0.0f);
+    } else {
+      while (ok && w.next()) {   // a row a lane
+        const int mine = lane * kTokenWarps + turn;
+        const int from = mine < w.m ? (kIn ? l.token[w.s0 + mine] : l.slot[w.s0 + mine]) : -1;
+        const __nv_bfloat16* row = p.v + (int64_t)from * p.K;
+        for (int c = 0; c < chunks; ++c) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[position.s], position.phase ^ 1));
+          if (!ok) break;
+          if (from >= 0)
+            tma_load_1d(ring + position.offset() + kUnitRows * kPiece + mine * kTokenPitch, row + c * kChunk, min(kChunk, p.K - c * kChunk) * 2, &sh.full[position.s]);
+          __syncwarp();
+          position.advance();
+        }
+      }
     }
   }
-  if (!ok) set_status(p.status, EP_ERR_TIMEOUT);
+  if (!ok) {
+    set_status(p.status, EP_ERR_TIMEOUT);
+    const uint64_t t0 = globaltimer_ns();   // give the copies in flight time to land before the memory goes
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
 }
 
 template <bool kFp8, bool kIn, int kAct>
@@ -447,8 +608,8 @@ static int launch_few_half(const FewParams& p, cudaStream_t s) {
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(fn), kFewSmem) != EP_OK) return EP_ERR_CUDA;
   const int grid = ep_host::grid_cap(1);
   if (!kIn && ep_host::sm_budget_set()) {   // the second kernel's CTAs do not come up beside the first's
-    fn<<<grid, kFewThreads, kFewSmem, s>>>(p);
-  } else if (ep_host::launch_dependent<FewParams>(fn, grid, kFewThreads, kFewSmem, s, p) != EP_OK) {
+    fn<<<grid, few_threads(kFp8), kFewSmem, s>>>(p);
+  } else if (ep_host::launch_dependent<FewParams>(fn, grid, few_threads(kFp8), kFewSmem, s, p) != EP_OK) {
     return EP_ERR_CUDA;
   }
   ep_host::count_launch();
