@@ -1,127 +1,694 @@
 // newton.cu -- orthogonalised update of the experts' weights: momentum, norm,
 // Newton-Schulz products, weight update.
+//
+// Every matrix X [M, N] of a stack goes through steps X <- a X + (b A + c A^2) X
+// with A = X X^T (S x S, S the smaller side; X^T X and a product from the right
+// where M > N, so that nothing is transposed: an operand that lies the other way
+// is read MN-major).  A step is three launches over all matrices:
+//   kGram    A = X X^T                 symmetric: tiles on and below the diagonal,
+//   kSquare  P = b A + c A^2           the others mirrored (none where c = 0)
+//   kApply   X' = a X + P X
+// all bound by the tensor cores.  Pairs of SMs compute 256 x 256 tiles as the
+// experts' products do (tcgen05.mma.cta_group::2, TMA, sums in tensor memory, the
+// epilogue of one tile under the products of the next).
+//
+// Operands are fp16: X and P stay near 1 in size by construction, so fp16's range
+// is enough (they are held 2^8 times as large, which keeps what matters of them above its
+// subnormals) and its 11 bits are worth having: bf16's 8 would put the rounding of
+// the operands above that of a bf16 result.  a X is the term that lifts small singular values,
+// by 3.4 a step; rounding it would lift the rounding too, so X is carried as
+// hi + lo, two fp16 words, of which the products take hi alone.
+// The first X is the source times a power of two, exact for a bf16 gradient; the
+// rest of the norm, a factor f in (1/2, 1], goes into the first step's epilogues.
 
 #include <cmath>
 
 #include "ep_common.cuh"
+#include "umma.cuh"
 
 namespace ep {
 
-constexpr int kTile = 32;
+// ---------------------------------------------------------------- momentum and norm
 
-struct NewtonShape {
-  int count, M, N, S;
-};
+constexpr int kSourceThreads = 256;
+constexpr int kMostParts = 64;            // of a matrix's norm
+constexpr float kHeld = 256.0f;           // X, A and P are held this many times as large
 
-// u of element i: the gradient, or with momentum what the step goes along.
 struct Source {
   const void* g;
   bool f32;
-  float* m;
+  float* m;               // or nullptr: u is the gradient
   float momentum;
   bool nesterov;
+  int64_t each;           // elements of a matrix, a multiple of 8
+  int64_t part;           // elements of a part, a multiple of 8 kSourceThreads
+  int parts, count;
+  float eps;
+  float* sums;            // [count, parts]
+  float* factor;          // [count]
+  __half *hi, *lo;        // [count, each]; lo may be nullptr
 };
 
-// X = u, m updated; norms[matrix] = |u|: one CTA a matrix.
-__global__ void __launch_bounds__(1024) k_newton_begin(Source src, int64_t each, float eps, float* x) {
-  __shared__ float part[32];
-  const int64_t base = blockIdx.x * each;
-  float sum = 0.0f;
-  for (int64_t i = threadIdx.x; i < each; i += blockDim.x) {
-    float u = src.f32 ? static_cast<const float*>(src.g)[base + i] : __bfloat162float(static_cast<const __nv_bfloat16*>(src.g)[base + i]);
-    if (src.m != nullptr) {
-      const float g = u, m = fmaf(src.momentum, src.m[base + i], g);
-      src.m[base + i] = m;
-      u = src.nesterov ? fmaf(src.momentum, m, g) : m;
-    }
-    x[base + i] = u;
-    sum = fmaf(u, u, sum);
-  }
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  float all = 0.0f;
-  for (int w = 0; w < 32; ++w) all += part[w];
-  const float f = all <= 1.329228e36f ? 1.0f / (sqrtf(all) + eps) : __uint_as_float(0x7fc00000u);   // 2^120
-  __syncthreads();
-  for (int64_t i = threadIdx.x; i < each; i += blockDim.x) x[base + i] *= f;
-}
-
-// C = alpha P Q + beta D per matrix; element (i, j) of P at i p0 + j p1, of Q at i q0 + j q1.
-struct Product {
-  const float *P, *Q, *D;
-  float* C;
-  int64_t p0, p1, q0, q1, p_each, q_each, c_each;
-  int rows, cols, inner;
-  float alpha, beta;
-};
-
-__global__ void __launch_bounds__(1024) k_newton_product(Product a) {
-  __shared__ float P[kTile][kTile + 1], Q[kTile][kTile + 1];
-  const int tx = threadIdx.x % kTile, ty = threadIdx.x / kTile;
-  const int i = blockIdx.y * kTile + ty, j = blockIdx.x * kTile + tx;
-  for (int z = blockIdx.z;; z += gridDim.z) {
-    const float *p = a.P + z * a.p_each, *q = a.Q + z * a.q_each;
-    float sum = 0.0f;
-    for (int k0 = 0; k0 < a.inner; k0 += kTile) {
-      P[ty][tx] = i < a.rows && k0 + tx < a.inner ? p[i * a.p0 + (k0 + tx) * a.p1] : 0.0f;
-      Q[ty][tx] = j < a.cols && k0 + ty < a.inner ? q[(k0 + ty) * a.q0 + j * a.q1] : 0.0f;
-      __syncthreads();
-      for (int k = 0; k < kTile; ++k) sum = fmaf(P[ty][k], Q[k][tx], sum);
-      __syncthreads();
-    }
-    if (i < a.rows && j < a.cols) {
-      const int64_t at = z * a.c_each + (int64_t)i * a.cols + j;
-      a.C[at] = a.alpha * sum + (a.beta != 0.0f ? a.beta * a.D[at] : 0.0f);
-    }
-    break;
+__device__ __forceinline__ void load8(const Source& s, int64_t i, float (&v)[8]) {
+  if (s.f32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(s.g) + i);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(s.g) + i);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
   }
 }
 
-__global__ void __launch_bounds__(256) k_newton_end(const float* x, int64_t n, __nv_bfloat16* out, float* w, __nv_bfloat16* w16, float keep, float step) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    if (out != nullptr) out[i] = __float2bfloat16_rn(x[i]);
-    if (w != nullptr) {
-      const float v = fmaf(-step, x[i], keep * w[i]);
-      w[i] = v;
-      if (w16 != nullptr) w16[i] = __float2bfloat16_rn(v);
+// m <- momentum m + g and the squares' sums of u, a part of a matrix a CTA, in an
+// order that only the sizes give.  Memory bounds it.
+__global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
+  __shared__ float warps[kSourceThreads / kWarp];
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t item = blockIdx.x; item < (int64_t)s.count * s.parts; item += gridDim.x) {
+    const int64_t z = item / s.parts, begin = (item - z * s.parts) * s.part, end = min(begin + s.part, s.each), base = z * s.each;
+    float sum[2] = {};
+    for (int64_t i0 = begin + threadIdx.x * 8; i0 < end; i0 += 2 * kSourceThreads * 8) {
+      float g[2][8] = {}, m[2][8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t i = i0 + k * kSourceThreads * 8;
+        if (i >= end) continue;
+        load8(s, base + i, g[k]);
+        if (s.m != nullptr) {
+          const float4* p = reinterpret_cast<const float4*>(s.m + base + i);
+          const float4 a = p[0], b = p[1];
+          m[k][0] = a.x, m[k][1] = a.y, m[k][2] = a.z, m[k][3] = a.w, m[k][4] = b.x, m[k][5] = b.y, m[k][6] = b.z, m[k][7] = b.w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t i = i0 + k * kSourceThreads * 8;
+        if (i >= end) continue;
+        if (s.m != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            m[k][e] = fmaf(s.momentum, m[k][e], g[k][e]);
+            g[k][e] = s.nesterov ? fmaf(s.momentum, m[k][e], g[k][e]) : m[k][e];
+          }
+          float4* p = reinterpret_cast<float4*>(s.m + base + i);
+          p[0] = make_float4(m[k][0], m[k][1], m[k][2], m[k][3]);
+          p[1] = make_float4(m[k][4], m[k][5], m[k][6], m[k][7]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[k] = fmaf(g[k][e], g[k][e], sum[k]);
+      }
+    }
+    float all = sum[0] + sum[1];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = all;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      all = 0.0f;
+      for (int w = 0; w < kSourceThreads / kWarp; ++w) all += warps[w];
+      s.sums[item] = all;
+    }
+    __syncthreads();
+  }
+}
+
+// X = u 2^q, in hi and lo, and the factor that makes it 2^8 u / (|u| + eps).  The
+// parts in the other order, as the last ones of the kernel before are still in L2.
+__global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t items = (int64_t)s.count * s.parts;
+  for (int64_t at = blockIdx.x; at < items; at += gridDim.x) {
+    const int64_t item = items - 1 - at;
+    const int64_t z = item / s.parts, begin = (item - z * s.parts) * s.part, end = min(begin + s.part, s.each), base = z * s.each;
+    float square = 0.0f;
+    for (int k = 0; k < s.parts; ++k) square += __ldcg(s.sums + z * s.parts + k);
+    const float norm = sqrtf(square) + s.eps;   // at least 1e-12
+    // 2^q the least power of two that is not below 2^8 / norm
+    const int q = 8 - ilogbf(norm);
+    const float up = norm <= 1.152921505e18f ? __uint_as_float((uint32_t)(127 + q) << 23) : __uint_as_float(0x7fc00000u);   // 2^60; NaN beyond and for NaN
+    if (begin == 0 && threadIdx.x == 0) s.factor[z] = norm <= 1.152921505e18f ? kHeld / (norm * up) : __uint_as_float(0x7fc00000u);
+    for (int64_t i = begin + threadIdx.x * 8; i < end; i += kSourceThreads * 8) {
+      float u[8];
+      load8(s, base + i, u);
+      if (s.m != nullptr) {
+        const float4* p = reinterpret_cast<const float4*>(s.m + base + i);
+        const float4 a = __ldcg(p), b = __ldcg(p + 1);   // from L2: an SM may hold what m was
+        const float m[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = s.nesterov ? fmaf(s.momentum, m[e], u[e]) : m[e];
+      }
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = u[2 * k] * up, y = u[2 * k + 1] * up;
+        const __half2 v = __floats2half2_rn(x, y);
+        const float2 b = __half22float2(v);
+        const __half2 r = __floats2half2_rn(x - b.x, y - b.y);
+        h[k] = *reinterpret_cast<const uint32_t*>(&v);
+        l[k] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+      st_v4(s.hi + base + i, make_uint4(h[0], h[1], h[2], h[3]));
+      if (s.lo != nullptr) st_v4(s.lo + base + i, make_uint4(l[0], l[1], l[2], l[3]));
     }
   }
+}
+
+// ---------------------------------------------------------------- products
+
+constexpr int kNewtonThreads = 384;
+constexpr int kNewtonStages = 5;
+constexpr int kBlock = 256;                           // output rows of a pair's tile, and its columns at most
+constexpr int kInner = 64;                            // fp16 elements of one 128-byte row
+constexpr int kNewtonOperand = 128 * kInner * 2;      // 16 KB: one CTA's part of an operand
+constexpr int kNewtonStage = 2 * kNewtonOperand;
+constexpr int kSide = 128 * 64 * 2;                   // a buffer: 128 rows x 64 columns
+constexpr int kNewtonWarps = 8;                       // of the epilogue, two sides of four
+
+enum NewtonForm { kGram, kSquare, kApply, kApplyOut, kApplyWeights };
+__host__ __device__ constexpr bool reads_tile(int form) { return form != kGram; }
+__host__ __device__ constexpr bool symmetric(int form) { return form == kGram || form == kSquare; }
+
+struct NewtonParams {
+  CUtensorMap a, b;             // operands
+  CUtensorMap in, in_lo;        // what the epilogue adds: A, or X
+  CUtensorMap out, out_lo;      // or out's mirror image
+  int count, rows, cols, inner; // of a product
+  int wide;                     // columns of a tile: 256 or 128
+  int tiles_m, tiles_n;         // kSquare, kGram: tiles_m only
+  int64_t tiles;
+  bool rows_fast, has_lo;
+  bool a_mn, b_mn;
+  float scale, add;             // epilogue: scale * sums + add * in
+  const float* factor;          // [count] or nullptr
+  float *w, keep, step;         // kApplyWeights
+  __nv_bfloat16* w16;
+  int32_t* status;
+};
+
+struct NewtonShared {
+  uint64_t full[kNewtonStages], empty[kNewtonStages];
+  uint64_t sums_full[2], sums_empty[2];
+  uint64_t tile_full[2];        // what the epilogue adds, by side
+  uint32_t tmem;
+};
+
+struct NewtonTile {
+  int z, i0, j0;
+  bool mirror;
+};
+
+template <int kForm>
+__device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, int64_t t) {
+  NewtonTile out;
+  const int each = (int)(p.tiles / p.count);
+  out.z = (int)(t / each);
+  const int u = (int)(t - (int64_t)out.z * each);
+  if (symmetric(kForm)) {
+    const int f = kBlock / p.wide, b = u / f;
+    int r = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
+    while ((int64_t)(r + 1) * (r + 2) / 2 <= b) ++r;
+    while ((int64_t)r * (r + 1) / 2 > b) --r;
+    const int c = b - (int)((int64_t)r * (r + 1) / 2);
+    out.i0 = r * kBlock;
+    out.j0 = c * kBlock + (u - b * f) * p.wide;
+    out.mirror = c < r;
+  } else {
+    const int r = p.rows_fast ? u % p.tiles_m : u / p.tiles_n, c = p.rows_fast ? u / p.tiles_m : u % p.tiles_n;
+    out.i0 = r * kBlock;
+    out.j0 = c * p.wide;
+    out.mirror = false;
+  }
+  return out;
+}
+
+// Address of 8 columns (16 bytes) of a row in a buffer, 128-byte swizzle.
+__device__ __forceinline__ uint32_t side_address(uint32_t buffer, int row, int piece) { return buffer + row * 128 + ((piece ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
+// Instruction descriptor, fp16 operands and fp32 sums.
+__device__ __forceinline__ uint32_t umma_idesc_f16(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+template <int kForm>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k_newton(const __grid_constant__ NewtonParams p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* sides = stages + kNewtonStages * kNewtonStage;
+  NewtonShared& sh = *reinterpret_cast<NewtonShared*>(sides + 4 * kSide);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&p.a);
+    prefetch_map(&p.b);
+    for (int s = 0; s < kNewtonStages; ++s) {
+      mbar_init(&sh.full[s], 1);      // the first CTA's, with the bytes of both
+      mbar_init(&sh.empty[s], 1);     // the products' commit
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.sums_full[i], 1);
+      mbar_init(&sh.sums_empty[i], 2 * kNewtonWarps);
+      mbar_init(&sh.tile_full[i], 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 2) tmem_alloc<2>(&sh.tmem, 512);
+  tmem_fence_before();
+  __syncwarp();
+  cluster_sync();
+  tmem_fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  bool ok = true;
+  const int blocks = (p.inner + kInner - 1) / kInner;
+  // a symmetric form's last column tile may lie past the matrix
+  auto next = [&](int64_t& t, NewtonTile& tile) {
+    for (; t < p.tiles; t += pairs) {
+      tile = newton_tile<kForm>(p, t);
+      if (tile.j0 < p.cols) return true;
+    }
+    return false;
+  };
+  NewtonTile tile;
+  if (warp == 0 || warp == 3) {
+    // ---------------------------------------------------------------- copies, a warp an operand
+    const bool issue = elect_one(), first = warp == 0;
+    const bool mn = first ? p.a_mn : p.b_mn;
+    const int half = p.wide / 2;   // of the second operand in a CTA
+    const uint32_t both = 2 * (kNewtonOperand + half * kInner * 2);
+    const CUtensorMap* map = first ? &p.a : &p.b;
+    const uint32_t to0 = smem_addr(stages) + (first ? 0 : kNewtonOperand), full0 = map_to_rank(smem_addr(&sh.full[0]), 0);
+    uint32_t s = 0, phase = 0;
+    for (int64_t t = pair; ok && next(t, tile); t += pairs) {
+      const int m0 = first ? tile.i0 + (int)rank * 128 : tile.j0 + (int)rank * half;
+      for (int kb = 0; kb < blocks; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
+        if (!ok) break;
+        if (issue) {
+          const uint32_t to = to0 + s * kNewtonStage, bar = full0 + s * (uint32_t)sizeof(uint64_t);
+          if (first && rank == 0) mbar_arrive_expect_tx(&sh.full[s], both);
+          if (!mn) {
+            tma_load_3d<true>(to, map, bar, kb * kInner, m0, tile.z);
+          } else {
+            for (int i = 0; i < (first ? 2 : half / 64); ++i) tma_load_3d<true>(to + i * (kNewtonOperand / 2), map, bar, m0 + i * 64, kb * kInner, tile.z);
+          }
+        }
+        if (++s == kNewtonStages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) {   // give the copies in flight time to land before the memory goes
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------------- products
+    const bool issue = elect_one();
+    const uint32_t a0 = umma_desc_lo(smem_addr(stages), p.a_mn ? kNewtonOperand / 2 : 16);
+    const uint32_t b0 = umma_desc_lo(smem_addr(stages) + kNewtonOperand, p.b_mn ? kNewtonOperand / 2 : 16);
+    const uint32_t step_a = (p.a_mn ? 2048 : 32) >> 4, step_b = (p.b_mn ? 2048 : 32) >> 4;
+    const uint32_t idesc = umma_idesc_f16(kBlock, p.wide, p.a_mn, p.b_mn);
+    uint32_t s = 0, phase = 0, n = 0;
+    for (int64_t t = pair; ok && next(t, tile); t += pairs, ++n) {
+      const uint32_t half = n & 1, d = tmem + half * kBlock;
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_empty[half], ((n >> 1) & 1) ^ 1, 4 * kWaitNs));
+      if (!ok) break;
+      tmem_fence_after();
+      for (int kb = 0; kb < blocks; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], phase));
+        if (!ok) break;
+        tmem_fence_after();
+        if (issue) {
+          const uint32_t a = a0 + s * (kNewtonStage >> 4), b = b0 + s * (kNewtonStage >> 4);
+#pragma unroll
+          for (uint32_t i = 0; i < kInner / 16; ++i) umma_bf16_pair(d, a + i * step_a, b + i * step_b, idesc, kb > 0 || i > 0);
+          umma_commit_pair(&sh.empty[s]);
+        }
+        if (++s == kNewtonStages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (issue) umma_commit_pair(&sh.sums_full[half]);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- epilogue
+    // a side's four warps take 64 columns at a time, a row a thread: what is added is copied into the side's
+    // buffers, replaced by the result in place and copied out; the mirror image is turned around by ldmatrix
+    const int q = warp & 3, side = (warp - 4) >> 2, row = q * 32 + lane;
+    const bool lead = q == 0 && lane == 0;
+    const uint32_t buf0 = smem_addr(sides) + side * 2 * kSide, buf1 = buf0 + kSide;
+    const int chunks = p.wide / 64;
+    auto live = [&](const NewtonTile& x, int ch) { return x.j0 + ch * 64 < p.cols && x.i0 + (int)rank * 128 < p.rows; };
+    // the first chunk of this side from (t, ch) on
+    auto seek = [&](int64_t& t, NewtonTile& x, int& ch) {
+      for (; next(t, x); t += pairs, ch = side)
+        for (; ch < chunks; ch += 2)
+          if (live(x, ch)) return true;
+      return false;
+    };
+    int64_t t_ask = pair;
+    int ch_ask = side;
+    NewtonTile asked;
+    auto ask = [&]() {   // the lead: copy in what the next chunk adds
+      if (!seek(t_ask, asked, ch_ask)) return;
+      const int x = asked.j0 + ch_ask * 64, y = asked.i0 + (int)rank * 128;
+      mbar_arrive_expect_tx(&sh.tile_full[side], kForm != kSquare && p.has_lo ? 2 * kSide : kSide);
+      tma_load_3d<false>(buf0, &p.in, smem_addr(&sh.tile_full[side]), x, y, asked.z);
+      if (kForm != kSquare && p.has_lo) tma_load_3d<false>(buf1, &p.in_lo, smem_addr(&sh.tile_full[side]), x, y, asked.z);
+      ch_ask += 2;
+    };
+    if (reads_tile(kForm) && lead) ask();
+    uint32_t n = 0, tile_phase = 0;
+    for (int64_t t = pair; next(t, tile); t += pairs, ++n) {
+      const uint32_t half = n & 1;
+      ok = named_barrier_and(1 + side, 128, mbar_wait_bounded(&sh.sums_full[half], (n >> 1) & 1, kWaitNs + (uint64_t)blocks * 4000));
+      if (!ok) break;
+      tmem_fence_after();
+      const uint32_t d = tmem + half * kBlock + ((uint32_t)(q * 32) << 16);
+      auto sums_read = [&]() {   // the next tile's products may have this half
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
+      };
+      const float f = p.factor != nullptr ? __ldcg(p.factor + tile.z) : 1.0f;
+      const float scale = kForm == kGram ? p.scale * f * f : p.scale;
+      int last = -1;
+      for (int ch = side; ch < chunks; ch += 2)
+        if (live(tile, ch)) last = ch;
+      if (last < 0) sums_read();
+#pragma unroll 1
+      for (int ch = side; ch <= last; ch += 2) {
+        if (reads_tile(kForm)) {
+          ok = named_barrier_and(1 + side, 128, mbar_wait_bounded(&sh.tile_full[side], tile_phase));
+          if (!ok) break;
+          tile_phase ^= 1;
+        } else {
+          if (lead) tma_wait_read<0>();
+          named_barrier_sync(1 + side, 128);
+        }
+        const int col0 = tile.j0 + ch * 64;
+        const int64_t line = (int64_t)tile.z * p.rows + tile.i0 + (int)rank * 128 + row;
+        const bool there = tile.i0 + (int)rank * 128 + row < p.rows;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float v[32];
+          tmem_ld32(d + ch * 64 + hf * 32, v);
+          tmem_wait_ld(v);
+          if (hf == 1 && ch == last) sums_read();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {   // 8 columns
+            const int piece = hf * 4 + c;
+            const uint32_t at = side_address(buf0, row, piece), at_lo = side_address(buf1, row, piece);
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = v[c * 8 + e] * scale;
+            if (reads_tile(kForm)) {
+              const uint4 hi = ld_shared_v4_at(at);
+              uint4 lo = make_uint4(0, 0, 0, 0);
+              if (kForm != kSquare && p.has_lo) lo = ld_shared_v4_at(at_lo);
+              const uint32_t wh[4] = {hi.x, hi.y, hi.z, hi.w}, wl[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float2 y = __half22float2(*reinterpret_cast<const __half2*>(&wh[e]));
+                if (kForm != kSquare) {
+                  const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&wl[e]));
+                  y.x += l.x;
+                  y.y += l.y;
+                }
+                x[2 * e] = fmaf(p.add, y.x, x[2 * e]);
+                x[2 * e + 1] = fmaf(p.add, y.y, x[2 * e + 1]);
+                if (kForm != kSquare) {
+                  x[2 * e] *= f;
+                  x[2 * e + 1] *= f;
+                }
+              }
+            }
+            if (kForm == kApplyWeights) {
+              if (there && col0 + piece * 8 < p.cols) {
+                float4* w = reinterpret_cast<float4*>(p.w + line * p.cols + col0 + piece * 8);
+                float4 a = __ldcg(w), b = __ldcg(w + 1);
+                a.x = fmaf(-p.step, x[0], p.keep * a.x), a.y = fmaf(-p.step, x[1], p.keep * a.y);
+                a.z = fmaf(-p.step, x[2], p.keep * a.z), a.w = fmaf(-p.step, x[3], p.keep * a.w);
+                b.x = fmaf(-p.step, x[4], p.keep * b.x), b.y = fmaf(-p.step, x[5], p.keep * b.y);
+                b.z = fmaf(-p.step, x[6], p.keep * b.z), b.w = fmaf(-p.step, x[7], p.keep * b.w);
+                w[0] = a;
+                w[1] = b;
+                if (p.w16 != nullptr)
+                  st_v4(p.w16 + line * p.cols + col0 + piece * 8,
+                        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w)));
+              }
+              continue;
+            }
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (kForm == kApplyOut) {
+                h[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+              } else {
+                const __half2 r = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+                h[e] = *reinterpret_cast<const uint32_t*>(&r);
+                if (kForm == kApply) {
+                  const float2 y = __half22float2(r);
+                  const __half2 rest = __floats2half2_rn(x[2 * e] - y.x, x[2 * e + 1] - y.y);
+                  l[e] = *reinterpret_cast<const uint32_t*>(&rest);
+                }
+              }
+            }
+            st_shared_v4_at(at, make_uint4(h[0], h[1], h[2], h[3]));
+            if (kForm == kApply) st_shared_v4_at(at_lo, make_uint4(l[0], l[1], l[2], l[3]));
+          }
+        }
+        if (symmetric(kForm) && tile.mirror) {   // this warp's 32 rows x 64 columns: rows j, columns i of the image
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t x[4];
+            ldmatrix4_trans(side_address(buf0, row, j), x);
+            stmatrix4(side_address(buf1 + (q >> 1) * (kSide / 2), j * 8 + (lane & 7), (q & 1) * 4 + (lane >> 3)), x);
+          }
+        }
+        fence_proxy_async_smem();
+        named_barrier_sync(1 + side, 128);
+        if (lead) {
+          const int y = tile.i0 + (int)rank * 128;
+          if (kForm != kApplyWeights) {
+            tma_store_3d(&p.out, buf0, col0, y, tile.z);
+            if (kForm == kApply) tma_store_3d(&p.out_lo, buf1, col0, y, tile.z);
+            if (symmetric(kForm) && tile.mirror)
+              for (int i = 0; i < 2; ++i)
+                if (y + i * 64 < p.rows) tma_store_3d(&p.out_lo, buf1 + i * (kSide / 2), y + i * 64, col0, tile.z);
+            tma_commit();
+          }
+          if (reads_tile(kForm)) {
+            tma_wait_read<0>();
+            ask();
+          }
+        }
+      }
+      if (!ok) break;
+    }
+    if (lead) {
+      tma_wait_all();
+      if (!ok) {   // what was asked for may be on its way
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+  }
+  if (!ok) set_status(p.status, EP_ERR_TIMEOUT);
+  __syncwarp();
+  tmem_fence_before();
+  cluster_sync();
+  tmem_fence_after();
+  if (warp == 2) tmem_free<2>(tmem, 512);
+}
+
+// ---------------------------------------------------------------- host
+
+struct NewtonSpace {
+  float *sums, *factor;
+  __half *x[2], *lo[2], *A, *P;
+  size_t bytes;
+};
+
+static int64_t padded(int n) { return (int64_t)(n + 7) / 8 * 8; }
+
+static NewtonSpace newton_space(int count, int M, int N, void* base) {
+  NewtonSpace s;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* const p = static_cast<uint8_t*>(base) + at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  const size_t each = (size_t)M * N, S = std::min(M, N);
+  s.sums = reinterpret_cast<float*>(take((size_t)count * kMostParts * 4));
+  s.factor = reinterpret_cast<float*>(take((size_t)count * 4));
+  for (int i = 0; i < 2; ++i) {
+    s.x[i] = reinterpret_cast<__half*>(take(count * each * 2));
+    s.lo[i] = reinterpret_cast<__half*>(take(count * each * 2));
+  }
+  s.A = reinterpret_cast<__half*>(take(count * S * padded((int)S) * 2));
+  s.P = reinterpret_cast<__half*>(take(count * S * padded((int)S) * 2));
+  s.bytes = std::max<size_t>(16, at);
+  return s;
 }
 
 static bool newton_sizes(int count, int M, int N) {
   return count >= 0 && count <= 65535 && M > 0 && N > 0 && N % 8 == 0 && M <= (1 << 20) && N <= (1 << 20) && (int64_t)count * M < ((int64_t)1 << 31);
 }
 
-static int newton(const Source& src, int count, int M, int N, int steps, const float* abc, float eps, __nv_bfloat16* out, float* w,
-                  __nv_bfloat16* w16, float keep, float step, void* workspace, cudaStream_t s) {
-  const int S = std::min(M, N);
-  const int64_t each = (int64_t)M * N, square = (int64_t)S * S;
-  float* x = static_cast<float*>(workspace);
-  float *y = x + count * each, *A = y + count * each, *B = A + count * square;
-  k_newton_begin<<<count, 1024, 0, s>>>(src, each, eps, x);
-  ep_host::count_launch();
-  const bool tall = M > N;
-  auto product = [&](Product p) {
-    k_newton_product<<<dim3((p.cols + kTile - 1) / kTile, (p.rows + kTile - 1) / kTile, count), 1024, 0, s>>>(p);
-    ep_host::count_launch();
-  };
-  for (int t = 0; t < steps; ++t) {
-    const float a = abc[3 * t], b = abc[3 * t + 1], c = abc[3 * t + 2];
-    if (tall)
-      product({x, x, nullptr, A, 1, N, N, 1, each, each, square, S, S, M, 1.0f, 0.0f});
-    else
-      product({x, x, nullptr, A, N, 1, 1, N, each, each, square, S, S, N, 1.0f, 0.0f});
-    product({A, A, A, B, S, 1, S, 1, square, square, square, S, S, c != 0.0f ? S : 0, c, b});
-    if (tall)
-      product({x, B, x, y, N, 1, S, 1, each, square, each, M, N, S, 1.0f, a});
-    else
-      product({B, x, x, y, S, 1, N, 1, square, each, each, M, N, S, 1.0f, a});
-    std::swap(x, y);
-  }
-  k_newton_end<<<ep_host::grid_cap(4), 256, 0, s>>>(x, count * each, out, w, w16, keep, step);
+// Rows of `cols` 16-bit elements at `stride` elements; boxes of 64 columns.
+static int newton_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t stride, int box_rows) {
+  const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)count}, strides[2] = {(uint64_t)stride * 2, (uint64_t)(stride * rows) * 2};
+  const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+  return ep_host::make_map(m, false, 3, base, dims, strides, box);
+}
+
+template <int kForm>
+static int launch_newton(NewtonParams& p, cudaStream_t s) {
+  constexpr int kSmem = kNewtonStages * kNewtonStage + 4 * kSide + (int)sizeof(NewtonShared) + 1024;
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(p.tiles, ep_host::grid_cap(1) / 2));
+  if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(k_newton<kForm>), kSmem) != EP_OK) return EP_ERR_CUDA;
+  if (ep_host::launch_dependent(k_newton<kForm>, (int)pairs * 2, kNewtonThreads, kSmem, s, p) != EP_OK) return EP_ERR_CUDA;
   ep_host::count_launch();
   return ep_host::check_launch();
+}
+
+// What all steps share, and the launches.
+struct Newton {
+  int count, M, N, S;
+  NewtonSpace space;
+  int32_t* status;
+  cudaStream_t stream;
+
+  // Tiles of 256 columns, of 128 where those would leave pairs of SMs without one.
+  void tiles(NewtonParams& p, bool sym) const {
+    auto of = [&](int wide) {
+      p.wide = wide;
+      p.tiles_m = (p.rows + kBlock - 1) / kBlock;
+      p.tiles_n = (p.cols + wide - 1) / wide;
+      const int64_t each = sym ? (int64_t)p.tiles_m * (p.tiles_m + 1) / 2 * (kBlock / wide) : (int64_t)p.tiles_m * p.tiles_n;
+      p.tiles = each * count;
+    };
+    of(kBlock);
+    if (p.tiles < std::max(1, ep_host::grid_cap(1) / 2)) of(kBlock / 2);
+  }
+  NewtonParams start(int rows, int cols, int inner, bool sym) const {
+    NewtonParams p{};
+    p.count = count;
+    p.rows = rows;
+    p.cols = cols;
+    p.inner = inner;
+    p.status = status;
+    tiles(p, sym);
+    return p;
+  }
+  int square_map(CUtensorMap* m, const __half* base, int box_rows) const { return newton_map(m, base, S, S, count, padded(S), box_rows); }
+  int x_map(CUtensorMap* m, const void* base, int box_rows) const { return newton_map(m, base, N, M, count, N, box_rows); }
+
+  // A = X X^T (or b A where that is the whole polynomial) from x.
+  int gram(const __half* x, __half* to, float b, const float* factor) const {
+    NewtonParams p = start(S, S, std::max(M, N), true);
+    p.a_mn = p.b_mn = M > N;
+    p.scale = b / kHeld;
+    p.factor = factor;
+    int rc = x_map(&p.a, x, M > N ? 64 : 128);
+    if (rc == EP_OK) rc = x_map(&p.b, x, M > N ? 64 : p.wide / 2);
+    if (rc == EP_OK) rc = square_map(&p.out, to, 128);
+    if (rc == EP_OK) rc = square_map(&p.out_lo, to, 64);
+    return rc != EP_OK ? rc : launch_newton<kGram>(p, stream);
+  }
+  int square(float b, float c) const {
+    NewtonParams p = start(S, S, S, true);
+    p.scale = c / kHeld;
+    p.add = b;
+    int rc = square_map(&p.a, space.A, 128);
+    if (rc == EP_OK) rc = square_map(&p.b, space.A, p.wide / 2);
+    if (rc == EP_OK) rc = square_map(&p.in, space.A, 128);
+    if (rc == EP_OK) rc = square_map(&p.out, space.P, 128);
+    if (rc == EP_OK) rc = square_map(&p.out_lo, space.P, 64);
+    return rc != EP_OK ? rc : launch_newton<kSquare>(p, stream);
+  }
+  // X' = a X + P X, into buffer `to`; the last one into out or w.
+  int apply(int from, bool has_lo, float a, const float* factor, bool last, __nv_bfloat16* out, float* w, __nv_bfloat16* w16, float keep,
+            float step) const {
+    NewtonParams p = start(M, N, S, false);
+    const bool tall = M > N;
+    p.rows_fast = !tall;
+    p.b_mn = !tall;
+    p.has_lo = has_lo;
+    p.factor = factor;
+    p.scale = (last ? 1.0f / kHeld : 1.0f) / kHeld;
+    p.add = last ? a / kHeld : a;
+    int rc = tall ? x_map(&p.a, space.x[from], 128) : square_map(&p.a, space.P, 128);
+    if (rc == EP_OK) rc = tall ? square_map(&p.b, space.P, p.wide / 2) : x_map(&p.b, space.x[from], 64);
+    if (rc == EP_OK) rc = x_map(&p.in, space.x[from], 128);
+    if (rc == EP_OK) rc = x_map(&p.in_lo, has_lo ? space.lo[from] : space.x[from], 128);
+    if (rc != EP_OK) return rc;
+    if (!last) {
+      rc = x_map(&p.out, space.x[1 - from], 128);
+      if (rc == EP_OK) rc = x_map(&p.out_lo, space.lo[1 - from], 128);
+      return rc != EP_OK ? rc : launch_newton<kApply>(p, stream);
+    }
+    if (out != nullptr) {
+      rc = x_map(&p.out, out, 128);
+      return rc != EP_OK ? rc : launch_newton<kApplyOut>(p, stream);
+    }
+    p.w = w;
+    p.w16 = w16;
+    p.keep = keep;
+    p.step = step;
+    return launch_newton<kApplyWeights>(p, stream);
+  }
+};
+
+static int newton(Source src, int count, int M, int N, int steps, const float* abc, float eps, __nv_bfloat16* out, float* w,
+                  __nv_bfloat16* w16, float keep, float step, void* workspace, int32_t* status, cudaStream_t s) {
+  Newton n = {count, M, N, std::min(M, N), newton_space(count, M, N, workspace), status, s};
+  src.each = (int64_t)M * N;
+  const int64_t unit = 8 * kSourceThreads;
+  src.part = std::max<int64_t>(2 * unit, ((src.each + kMostParts - 1) / kMostParts + unit - 1) / unit * unit);
+  src.parts = (int)((src.each + src.part - 1) / src.part);
+  src.count = count;
+  src.eps = eps;
+  src.sums = n.space.sums;
+  src.factor = n.space.factor;
+  src.hi = n.space.x[0];
+  const bool exact = !src.f32 && src.m == nullptr;   // bf16 times a power of two is fp16, but for what is 2^-24 of the norm and smaller
+  src.lo = exact ? nullptr : n.space.lo[0];
+  const int grid = (int)std::min<int64_t>((int64_t)count * src.parts, ep_host::grid_cap(4));
+  for (auto* kernel : {k_newton_norm, k_newton_scale}) {
+    if (ep_host::launch_dependent(kernel, grid, kSourceThreads, 0, s, src) != EP_OK) return EP_ERR_CUDA;
+    ep_host::count_launch();
+  }
+  for (int t = 0; t < steps; ++t) {
+    const float a = abc[3 * t], b = abc[3 * t + 1], c = abc[3 * t + 2];
+    const float* factor = t == 0 ? n.space.factor : nullptr;
+    int rc = n.gram(n.space.x[t & 1], c != 0.0f ? n.space.A : n.space.P, c != 0.0f ? 1.0f : b, factor);
+    if (rc == EP_OK && c != 0.0f) rc = n.square(b, c);
+    if (rc == EP_OK) rc = n.apply(t & 1, t > 0 || !exact, a, factor, t + 1 == steps, out, w, w16, keep, step);
+    if (rc != EP_OK) return rc;
+  }
+  return EP_OK;
 }
 
 static int check_newton(const void* g, int dtype, int count, int M, int N, int steps, const float* abc, float eps, const void* workspace,
@@ -140,8 +707,7 @@ static int check_newton(const void* g, int dtype, int count, int M, int N, int s
 
 extern "C" size_t ep_orthogonalize_workspace_size(int count, int M, int N) {
   if (!ep::newton_sizes(count, M, N)) return 0;
-  const size_t S = std::min(M, N);
-  return std::max<size_t>(16, (size_t)count * ((size_t)M * N * 8 + S * S * 8));
+  return ep::newton_space(count, M, N, nullptr).bytes;
 }
 
 extern "C" int ep_orthogonalize(const void* g, int dtype, int count, int M, int N, int steps, const float* coefficients, float eps, void* out,
@@ -151,8 +717,10 @@ extern "C" int ep_orthogonalize(const void* g, int dtype, int count, int M, int 
   if (rc != EP_OK) return rc;
   if (count == 0) return EP_OK;
   if (out == nullptr || !ep_host::aligned16(out)) return EP_ERR_INVALID_ARG;
-  const Source src = {g, dtype == EP_DTYPE_F32, nullptr, 0.0f, false};
-  return newton(src, count, M, N, steps, coefficients, eps, static_cast<__nv_bfloat16*>(out), nullptr, nullptr, 0.0f, 0.0f, workspace,
+  Source src{};
+  src.g = g;
+  src.f32 = dtype == EP_DTYPE_F32;
+  return newton(src, count, M, N, steps, coefficients, eps, static_cast<__nv_bfloat16*>(out), nullptr, nullptr, 0.0f, 0.0f, workspace, status,
                 static_cast<cudaStream_t>(stream));
 }
 
@@ -166,7 +734,12 @@ extern "C" int ep_muon_update(const void* g, int dtype, float* m, float* w, void
     return EP_ERR_INVALID_ARG;
   if (count == 0) return EP_OK;
   if (m == nullptr || w == nullptr || !ep_host::aligned16(m) || !ep_host::aligned16(w) || !ep_host::aligned16(w16)) return EP_ERR_INVALID_ARG;
-  const Source src = {g, dtype == EP_DTYPE_F32, m, momentum, nesterov != 0};
+  Source src{};
+  src.g = g;
+  src.f32 = dtype == EP_DTYPE_F32;
+  src.m = m;
+  src.momentum = momentum;
+  src.nesterov = nesterov != 0;
   return newton(src, count, M, N, steps, coefficients, eps, nullptr, w, static_cast<__nv_bfloat16*>(w16),
-                (float)(1.0 - (double)lr * weight_decay), (float)((double)lr * scale), workspace, static_cast<cudaStream_t>(stream));
+                (float)(1.0 - (double)lr * weight_decay), (float)((double)lr * scale), workspace, status, static_cast<cudaStream_t>(stream));
 }
