@@ -18,6 +18,10 @@
 // the operands above that of a bf16 result.  a X is the term that lifts small singular values,
 // by 3.4 a step; rounding it would lift the rounding too, so X is carried as
 // hi + lo, two fp16 words, of which the products take hi alone.
+// P's diagonal is kept out of the product: in 32 bits it multiplies both words of X.
+// Where singular values are near 1, P is near -2.7 I and all but the diagonal is
+// small, and so is what rounding P and leaving out lo costs (256 x 512 normal numbers, five quintic
+// steps: 1.7e-3 of the result off without this, 0.8e-3 so).
 // The first X is the source times a power of two, exact for a bf16 gradient; the
 // rest of the norm, a factor f in (1/2, 1], goes into the first step's epilogues.
 
@@ -183,8 +187,10 @@ struct NewtonParams {
   int64_t tiles;
   bool rows_fast, has_lo;
   bool a_mn, b_mn;
-  float scale, add;             // epilogue: scale * sums + add * in
+  float scale, add;             // epilogue: scale * sums + (add + diagonal_scale * diagonal) * in
+  float diagonal_scale;
   const float* factor;          // [count] or nullptr
+  float* diagonal;              // [count, S]: P's
   float *w, keep, step;         // kApplyWeights
   __nv_bfloat16* w16;
   int32_t* status;
@@ -406,6 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
         const int col0 = tile.j0 + ch * 64;
         const int64_t line = (int64_t)tile.z * p.rows + tile.i0 + (int)rank * 128 + row;
         const bool there = tile.i0 + (int)rank * 128 + row < p.rows;
+        const float row_add = reads_tile(kForm) && kForm != kSquare && p.rows_fast && there ? __ldcg(p.diagonal + line) * p.diagonal_scale : 0.0f;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           float v[32];
@@ -424,6 +431,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
               uint4 lo = make_uint4(0, 0, 0, 0);
               if (kForm != kSquare && p.has_lo) lo = ld_shared_v4_at(at_lo);
               const uint32_t wh[4] = {hi.x, hi.y, hi.z, hi.w}, wl[4] = {lo.x, lo.y, lo.z, lo.w};
+              float add[8];   // a, and P's diagonal for the row, or for the column where P stands to the right
+#pragma unroll
+              for (int e = 0; e < 8; ++e) add[e] = p.add + row_add;
+              if (kForm != kSquare && !p.rows_fast && col0 + piece * 8 < p.cols) {
+                const float4* at_columns = reinterpret_cast<const float4*>(p.diagonal + (int64_t)tile.z * p.cols + col0 + piece * 8);
+                const float4 c0 = __ldcg(at_columns), c1 = __ldcg(at_columns + 1);
+                add[0] = fmaf(c0.x, p.diagonal_scale, add[0]), add[1] = fmaf(c0.y, p.diagonal_scale, add[1]);
+                add[2] = fmaf(c0.z, p.diagonal_scale, add[2]), add[3] = fmaf(c0.w, p.diagonal_scale, add[3]);
+                add[4] = fmaf(c1.x, p.diagonal_scale, add[4]), add[5] = fmaf(c1.y, p.diagonal_scale, add[5]);
+                add[6] = fmaf(c1.z, p.diagonal_scale, add[6]), add[7] = fmaf(c1.w, p.diagonal_scale, add[7]);
+              }
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 float2 y = __half22float2(*reinterpret_cast<const __half2*>(&wh[e]));
@@ -432,11 +450,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
                   y.x += l.x;
                   y.y += l.y;
                 }
-                x[2 * e] = fmaf(p.add, y.x, x[2 * e]);
-                x[2 * e + 1] = fmaf(p.add, y.y, x[2 * e + 1]);
+                x[2 * e] = fmaf(add[2 * e], y.x, x[2 * e]);
+                x[2 * e + 1] = fmaf(add[2 * e + 1], y.y, x[2 * e + 1]);
                 if (kForm != kSquare) {
                   x[2 * e] *= f;
                   x[2 * e + 1] *= f;
+                }
+              }
+            }
+            if (symmetric(kForm) && p.diagonal != nullptr && !tile.mirror) {
+              const int at_diagonal = tile.i0 + (int)rank * 128 + row - (col0 + piece * 8);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if (at_diagonal == e) {
+                  if (there) p.diagonal[line] = x[e] * (1.0f / kHeld);
+                  x[e] = 0.0f;
                 }
               }
             }
@@ -524,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
 // ---------------------------------------------------------------- host
 
 struct NewtonSpace {
-  float *sums, *factor;
+  float *sums, *factor, *diagonal;
   __half *x[2], *lo[2], *A, *P;
   size_t bytes;
 };
@@ -542,6 +570,7 @@ static NewtonSpace newton_space(int count, int M, int N, void* base) {
   const size_t each = (size_t)M * N, S = std::min(M, N);
   s.sums = reinterpret_cast<float*>(take((size_t)count * kMostParts * 4));
   s.factor = reinterpret_cast<float*>(take((size_t)count * 4));
+  s.diagonal = reinterpret_cast<float*>(take((size_t)count * S * 4));
   for (int i = 0; i < 2; ++i) {
     s.x[i] = reinterpret_cast<__half*>(take(count * each * 2));
     s.lo[i] = reinterpret_cast<__half*>(take(count * each * 2));
@@ -611,6 +640,7 @@ struct Newton {
     p.a_mn = p.b_mn = M > N;
     p.scale = b / kHeld;
     p.factor = factor;
+    p.diagonal = to == space.P ? space.diagonal : nullptr;
     int rc = x_map(&p.a, x, M > N ? 64 : 128);
     if (rc == EP_OK) rc = x_map(&p.b, x, M > N ? 64 : p.wide / 2);
     if (rc == EP_OK) rc = square_map(&p.out, to, 128);
@@ -621,6 +651,7 @@ struct Newton {
     NewtonParams p = start(S, S, S, true);
     p.scale = c / kHeld;
     p.add = b;
+    p.diagonal = space.diagonal;
     int rc = square_map(&p.a, space.A, 128);
     if (rc == EP_OK) rc = square_map(&p.b, space.A, p.wide / 2);
     if (rc == EP_OK) rc = square_map(&p.in, space.A, 128);
@@ -638,7 +669,9 @@ struct Newton {
     p.has_lo = has_lo;
     p.factor = factor;
     p.scale = (last ? 1.0f / kHeld : 1.0f) / kHeld;
-    p.add = last ? a / kHeld : a;
+    p.diagonal_scale = last ? 1.0f / kHeld : 1.0f;
+    p.add = a * p.diagonal_scale;
+    p.diagonal = space.diagonal;
     int rc = tall ? x_map(&p.a, space.x[from], 128) : square_map(&p.a, space.P, 128);
     if (rc == EP_OK) rc = tall ? square_map(&p.b, space.P, p.wide / 2) : x_map(&p.b, space.x[from], 64);
     if (rc == EP_OK) rc = x_map(&p.in, space.x[from], 128);
