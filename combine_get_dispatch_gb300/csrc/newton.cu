@@ -170,8 +170,10 @@ constexpr int kBlock = 256;                           // output rows of a pair's
 constexpr int kInner = 64;                            // fp16 elements of one 128-byte row
 constexpr int kNewtonOperand = 128 * kInner * 2;      // 16 KB: one CTA's part of an operand
 constexpr int kNewtonStage = 2 * kNewtonOperand;
-constexpr int kSide = 128 * 64 * 2;                   // a buffer: 128 rows x 64 columns
-constexpr int kNewtonWarps = 8;                       // of the epilogue, two sides of four
+constexpr int kNewtonWarps = 8;                       // of the epilogue: four for the rows, two sides of column chunks
+constexpr int kChunkCols = 32;                        // columns that a warp takes at a time, of its 32 rows
+constexpr int kPiece = 32 * kChunkCols * 2;           // 2 KB: such a block of 16-bit numbers
+constexpr int kWarpBytes = 4 * kPiece;                // a warp's buffers
 
 enum NewtonForm { kGram, kSquare, kApply, kApplyOut, kApplyWeights };
 __host__ __device__ constexpr bool reads_tile(int form) { return form != kGram; }
@@ -180,7 +182,8 @@ __host__ __device__ constexpr bool symmetric(int form) { return form == kGram ||
 struct NewtonParams {
   CUtensorMap a, b;             // operands
   CUtensorMap in, in_lo;        // what the epilogue adds: A, or X
-  CUtensorMap out, out_lo;      // or out's mirror image
+  CUtensorMap out, out_lo;
+  CUtensorMap weights;          // kApplyWeights: w as 16-bit halves, 64 at a time
   int count, rows, cols, inner; // of a product
   int wide;                     // columns of a tile: 256 or 128
   int tiles_m, tiles_n;         // kSquare, kGram: tiles_m only
@@ -191,15 +194,15 @@ struct NewtonParams {
   float diagonal_scale;
   const float* factor;          // [count] or nullptr
   float* diagonal;              // [count, S]: P's
-  float *w, keep, step;         // kApplyWeights
-  __nv_bfloat16* w16;
+  float keep, step;             // kApplyWeights
+  bool w16;                     // out is their bf16 copy
   int32_t* status;
 };
 
 struct NewtonShared {
   uint64_t full[kNewtonStages], empty[kNewtonStages];
   uint64_t sums_full[2], sums_empty[2];
-  uint64_t tile_full[2];        // what the epilogue adds, by side
+  uint64_t tile_full[kNewtonWarps][2];   // what a warp adds, by buffer
   uint32_t tmem;
 };
 
@@ -232,8 +235,8 @@ __device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, int64_t
   return out;
 }
 
-// Address of 8 columns (16 bytes) of a row in a buffer, 128-byte swizzle.
-__device__ __forceinline__ uint32_t side_address(uint32_t buffer, int row, int piece) { return buffer + row * 128 + ((piece ^ (row & 7)) << 4); }
+// Address of 8 columns (16 bytes) of a row in a piece, 64-byte swizzle.
+__device__ __forceinline__ uint32_t piece_address(uint32_t piece, int row, int c) { return piece + row * 64 + ((c ^ ((row >> 1) & 3)) << 4); }
 
 __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&v)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
@@ -248,8 +251,8 @@ template <int kForm>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k_newton(const __grid_constant__ NewtonParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* sides = stages + kNewtonStages * kNewtonStage;
-  NewtonShared& sh = *reinterpret_cast<NewtonShared*>(sides + 4 * kSide);
+  uint8_t* pieces = stages + kNewtonStages * kNewtonStage;
+  NewtonShared& sh = *reinterpret_cast<NewtonShared*>(pieces + kNewtonWarps * kWarpBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -264,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sums_full[i], 1);
       mbar_init(&sh.sums_empty[i], 2 * kNewtonWarps);
-      mbar_init(&sh.tile_full[i], 1);
+      for (int w = 0; w < kNewtonWarps; ++w) mbar_init(&sh.tile_full[w][i], 1);
     }
     fence_barrier_init();
   }
@@ -355,136 +358,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    // a side's four warps take 64 columns at a time, a row a thread: what is added is copied into the side's
-    // buffers, replaced by the result in place and copied out; the mirror image is turned around by ldmatrix
-    const int q = warp & 3, side = (warp - 4) >> 2, row = q * 32 + lane;
-    const bool lead = q == 0 && lane == 0;
-    const uint32_t buf0 = smem_addr(sides) + side * 2 * kSide, buf1 = buf0 + kSide;
-    const int chunks = p.wide / 64;
-    auto live = [&](const NewtonTile& x, int ch) { return x.j0 + ch * 64 < p.cols && x.i0 + (int)rank * 128 < p.rows; };
-    // the first chunk of this side from (t, ch) on
-    auto seek = [&](int64_t& t, NewtonTile& x, int& ch) {
-      for (; next(t, x); t += pairs, ch = side)
-        for (; ch < chunks; ch += 2)
-          if (live(x, ch)) return true;
-      return false;
-    };
+    // A warp takes its 32 rows, 32 columns at a time, on its own: what is added is copied into one of its buffers
+    // while the chunk before is worked on, replaced by the result in place and copied out.  (128 rows x 64 columns by
+    // four warps with barriers between them, one buffer: 25800 clocks a tile whose products take 16400.)
+    const int q = warp & 3, side = (warp - 4) >> 2;
+    constexpr int kBuffers = kForm == kApplyWeights ? 1 : 2;   // those hold w too
+    const uint32_t buffers = smem_addr(pieces) + (warp - 4) * kWarpBytes;
+    uint64_t* const tile_full = sh.tile_full[warp - 4];
+    const int chunks = p.wide / kChunkCols, row0 = (int)rank * 128 + q * 32;
+    auto live = [&](const NewtonTile& x, int ch) { return x.j0 + ch * kChunkCols < p.cols && x.i0 + row0 < p.rows; };
     int64_t t_ask = pair;
     int ch_ask = side;
-    NewtonTile asked;
-    auto ask = [&]() {   // the lead: copy in what the next chunk adds
-      if (!seek(t_ask, asked, ch_ask)) return;
-      const int x = asked.j0 + ch_ask * 64, y = asked.i0 + (int)rank * 128;
-      mbar_arrive_expect_tx(&sh.tile_full[side], kForm != kSquare && p.has_lo ? 2 * kSide : kSide);
-      tma_load_3d<false>(buf0, &p.in, smem_addr(&sh.tile_full[side]), x, y, asked.z);
-      if (kForm != kSquare && p.has_lo) tma_load_3d<false>(buf1, &p.in_lo, smem_addr(&sh.tile_full[side]), x, y, asked.z);
+    uint32_t n_ask = 0;
+    // copy in what the next chunk adds
+    auto ask = [&]() {
+      NewtonTile x;
+      for (; next(t_ask, x); t_ask += pairs, ch_ask = side)
+        if (ch_ask < chunks && live(x, ch_ask)) break;
+      if (t_ask >= p.tiles) return;
+      const int col = x.j0 + ch_ask * kChunkCols, i = n_ask % kBuffers;
+      const uint32_t to = buffers + i * (kWarpBytes / 2), bar = smem_addr(&tile_full[i]);
+      const bool lo = kForm != kSquare && p.has_lo;
+      mbar_arrive_expect_tx(&tile_full[i], (lo ? 2 : 1) * kPiece + (kForm == kApplyWeights ? 2 * kPiece : 0));
+      tma_load_3d<false>(to, &p.in, bar, col, x.i0 + row0, x.z);
+      if (lo) tma_load_3d<false>(to + kPiece, &p.in_lo, bar, col, x.i0 + row0, x.z);
+      if (kForm == kApplyWeights) tma_load_3d<false>(to + 2 * kPiece, &p.weights, bar, 2 * col, x.i0 + row0, x.z);
       ch_ask += 2;
+      ++n_ask;
     };
-    if (reads_tile(kForm) && lead) ask();
-    uint32_t n = 0, tile_phase = 0;
+    if (reads_tile(kForm) && lane == 0) ask();
+    uint32_t n = 0, k = 0;   // tiles, chunks
     for (int64_t t = pair; next(t, tile); t += pairs, ++n) {
       const uint32_t half = n & 1;
-      ok = named_barrier_and(1 + side, 128, mbar_wait_bounded(&sh.sums_full[half], (n >> 1) & 1, kWaitNs + (uint64_t)blocks * 4000));
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_full[half], (n >> 1) & 1, kWaitNs + (uint64_t)blocks * 4000));
       if (!ok) break;
       tmem_fence_after();
       const uint32_t d = tmem + half * kBlock + ((uint32_t)(q * 32) << 16);
-      auto sums_read = [&]() {   // the next tile's products may have this half
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
-      };
       const float f = p.factor != nullptr ? __ldcg(p.factor + tile.z) : 1.0f;
       const float scale = kForm == kGram ? p.scale * f * f : p.scale;
-      int last = -1;
-      for (int ch = side; ch < chunks; ch += 2)
-        if (live(tile, ch)) last = ch;
-      if (last < 0) sums_read();
-#pragma unroll 1
-      for (int ch = side; ch <= last; ch += 2) {
+      const int row = tile.i0 + row0 + lane;
+      const bool there = row < p.rows;
+      const int64_t line = (int64_t)tile.z * p.rows + row;
+      const float row_add =
+          reads_tile(kForm) && kForm != kSquare && p.rows_fast && there ? fmaf(__ldcg(p.diagonal + line), p.diagonal_scale, p.add) : p.add;
+      int ch = side;
+      for (; ch < chunks && live(tile, ch); ch += 2, ++k) {
+        const int i = k % kBuffers;
+        const uint32_t at = buffers + i * (kWarpBytes / 2), at_lo = at + kPiece, at_w = at + 2 * kPiece;
         if (reads_tile(kForm)) {
-          ok = named_barrier_and(1 + side, 128, mbar_wait_bounded(&sh.tile_full[side], tile_phase));
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tile_full[i], (k / kBuffers) & 1));
           if (!ok) break;
-          tile_phase ^= 1;
+          if (kBuffers == 2 && lane == 0) {   // the other buffer's last copy has been read by now
+            tma_wait_read<0>();
+            ask();
+          }
         } else {
-          if (lead) tma_wait_read<0>();
-          named_barrier_sync(1 + side, 128);
+          if (lane == 0) tma_wait_read<1>();
         }
-        const int col0 = tile.j0 + ch * 64;
-        const int64_t line = (int64_t)tile.z * p.rows + tile.i0 + (int)rank * 128 + row;
-        const bool there = tile.i0 + (int)rank * 128 + row < p.rows;
-        const float row_add = reads_tile(kForm) && kForm != kSquare && p.rows_fast && there ? __ldcg(p.diagonal + line) * p.diagonal_scale : 0.0f;
+        __syncwarp();
+        const int col0 = tile.j0 + ch * kChunkCols;
+        float v[32];
+        tmem_ld32(d + ch * kChunkCols, v);
+        tmem_wait_ld(v);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float v[32];
-          tmem_ld32(d + ch * 64 + hf * 32, v);
-          tmem_wait_ld(v);
-          if (hf == 1 && ch == last) sums_read();
+        for (int c = 0; c < 4; ++c) {   // 8 columns
+          float x[8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {   // 8 columns
-            const int piece = hf * 4 + c;
-            const uint32_t at = side_address(buf0, row, piece), at_lo = side_address(buf1, row, piece);
-            float x[8];
+          for (int e = 0; e < 8; ++e) x[e] = v[c * 8 + e] * scale;
+          if (reads_tile(kForm)) {
+            const uint4 hi = ld_shared_v4_at(piece_address(at, lane, c));
+            uint4 lo = make_uint4(0, 0, 0, 0);
+            if (kForm != kSquare && p.has_lo) lo = ld_shared_v4_at(piece_address(at_lo, lane, c));
+            const uint32_t wh[4] = {hi.x, hi.y, hi.z, hi.w}, wl[4] = {lo.x, lo.y, lo.z, lo.w};
+            float add[8];   // a, and P's diagonal for the row, or for the column where P stands to the right
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = v[c * 8 + e] * scale;
-            if (reads_tile(kForm)) {
-              const uint4 hi = ld_shared_v4_at(at);
-              uint4 lo = make_uint4(0, 0, 0, 0);
-              if (kForm != kSquare && p.has_lo) lo = ld_shared_v4_at(at_lo);
-              const uint32_t wh[4] = {hi.x, hi.y, hi.z, hi.w}, wl[4] = {lo.x, lo.y, lo.z, lo.w};
-              float add[8];   // a, and P's diagonal for the row, or for the column where P stands to the right
+            for (int e = 0; e < 8; ++e) add[e] = row_add;
+            if (kForm != kSquare && !p.rows_fast && col0 + c * 8 < p.cols) {
+              const float4* at_columns = reinterpret_cast<const float4*>(p.diagonal + (int64_t)tile.z * p.cols + col0 + c * 8);
+              const float4 c0 = __ldcg(at_columns), c1 = __ldcg(at_columns + 1);
+              add[0] = fmaf(c0.x, p.diagonal_scale, add[0]), add[1] = fmaf(c0.y, p.diagonal_scale, add[1]);
+              add[2] = fmaf(c0.z, p.diagonal_scale, add[2]), add[3] = fmaf(c0.w, p.diagonal_scale, add[3]);
+              add[4] = fmaf(c1.x, p.diagonal_scale, add[4]), add[5] = fmaf(c1.y, p.diagonal_scale, add[5]);
+              add[6] = fmaf(c1.z, p.diagonal_scale, add[6]), add[7] = fmaf(c1.w, p.diagonal_scale, add[7]);
+            }
 #pragma unroll
-              for (int e = 0; e < 8; ++e) add[e] = p.add + row_add;
-              if (kForm != kSquare && !p.rows_fast && col0 + piece * 8 < p.cols) {
-                const float4* at_columns = reinterpret_cast<const float4*>(p.diagonal + (int64_t)tile.z * p.cols + col0 + piece * 8);
-                const float4 c0 = __ldcg(at_columns), c1 = __ldcg(at_columns + 1);
-                add[0] = fmaf(c0.x, p.diagonal_scale, add[0]), add[1] = fmaf(c0.y, p.diagonal_scale, add[1]);
-                add[2] = fmaf(c0.z, p.diagonal_scale, add[2]), add[3] = fmaf(c0.w, p.diagonal_scale, add[3]);
-                add[4] = fmaf(c1.x, p.diagonal_scale, add[4]), add[5] = fmaf(c1.y, p.diagonal_scale, add[5]);
-                add[6] = fmaf(c1.z, p.diagonal_scale, add[6]), add[7] = fmaf(c1.w, p.diagonal_scale, add[7]);
+            for (int e = 0; e < 4; ++e) {
+              float2 y = __half22float2(*reinterpret_cast<const __half2*>(&wh[e]));
+              if (kForm != kSquare) {
+                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&wl[e]));
+                y.x += l.x;
+                y.y += l.y;
               }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float2 y = __half22float2(*reinterpret_cast<const __half2*>(&wh[e]));
-                if (kForm != kSquare) {
-                  const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&wl[e]));
-                  y.x += l.x;
-                  y.y += l.y;
-                }
-                x[2 * e] = fmaf(add[2 * e], y.x, x[2 * e]);
-                x[2 * e + 1] = fmaf(add[2 * e + 1], y.y, x[2 * e + 1]);
-                if (kForm != kSquare) {
-                  x[2 * e] *= f;
-                  x[2 * e + 1] *= f;
-                }
+              x[2 * e] = fmaf(add[2 * e], y.x, x[2 * e]);
+              x[2 * e + 1] = fmaf(add[2 * e + 1], y.y, x[2 * e + 1]);
+              if (kForm != kSquare) {
+                x[2 * e] *= f;
+                x[2 * e + 1] *= f;
               }
             }
-            if (symmetric(kForm) && p.diagonal != nullptr && !tile.mirror) {
-              const int at_diagonal = tile.i0 + (int)rank * 128 + row - (col0 + piece * 8);
+          }
+          if (symmetric(kForm) && p.diagonal != nullptr && !tile.mirror) {
+            const int at_diagonal = row - (col0 + c * 8);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if (at_diagonal == e) {
-                  if (there) p.diagonal[line] = x[e] * (1.0f / kHeld);
-                  x[e] = 0.0f;
-                }
+            for (int e = 0; e < 8; ++e) {
+              if (at_diagonal == e) {
+                if (there) p.diagonal[line] = x[e] * (1.0f / kHeld);
+                x[e] = 0.0f;
               }
             }
-            if (kForm == kApplyWeights) {
-              if (there && col0 + piece * 8 < p.cols) {
-                float4* w = reinterpret_cast<float4*>(p.w + line * p.cols + col0 + piece * 8);
-                float4 a = __ldcg(w), b = __ldcg(w + 1);
-                a.x = fmaf(-p.step, x[0], p.keep * a.x), a.y = fmaf(-p.step, x[1], p.keep * a.y);
-                a.z = fmaf(-p.step, x[2], p.keep * a.z), a.w = fmaf(-p.step, x[3], p.keep * a.w);
-                b.x = fmaf(-p.step, x[4], p.keep * b.x), b.y = fmaf(-p.step, x[5], p.keep * b.y);
-                b.z = fmaf(-p.step, x[6], p.keep * b.z), b.w = fmaf(-p.step, x[7], p.keep * b.w);
-                w[0] = a;
-                w[1] = b;
-                if (p.w16 != nullptr)
-                  st_v4(p.w16 + line * p.cols + col0 + piece * 8,
-                        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w)));
-              }
-              continue;
+          }
+          uint32_t h[4], l[4];
+          if (kForm == kApplyWeights) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {   // a row of w is 8 pieces of 4, 128-byte swizzle
+              const uint32_t to = at_w + lane * 128 + (((2 * c + e) ^ (lane & 7)) << 4);
+              const uint4 w = ld_shared_v4_at(to);
+              const float w0 = fmaf(-p.step, x[4 * e], p.keep * __uint_as_float(w.x)), w1 = fmaf(-p.step, x[4 * e + 1], p.keep * __uint_as_float(w.y));
+              const float w2 = fmaf(-p.step, x[4 * e + 2], p.keep * __uint_as_float(w.z)), w3 = fmaf(-p.step, x[4 * e + 3], p.keep * __uint_as_float(w.w));
+              st_shared_v4_at(to, make_uint4(__float_as_uint(w0), __float_as_uint(w1), __float_as_uint(w2), __float_as_uint(w3)));
+              h[2 * e] = pack_bf16x2(w0, w1);
+              h[2 * e + 1] = pack_bf16x2(w2, w3);
             }
-            uint32_t h[4], l[4];
+          } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (kForm == kApplyOut) {
@@ -499,40 +494,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
                 }
               }
             }
-            st_shared_v4_at(at, make_uint4(h[0], h[1], h[2], h[3]));
-            if (kForm == kApply) st_shared_v4_at(at_lo, make_uint4(l[0], l[1], l[2], l[3]));
           }
+          st_shared_v4_at(piece_address(at, lane, c), make_uint4(h[0], h[1], h[2], h[3]));
+          if (kForm == kApply) st_shared_v4_at(piece_address(at_lo, lane, c), make_uint4(l[0], l[1], l[2], l[3]));
         }
-        if (symmetric(kForm) && tile.mirror) {   // this warp's 32 rows x 64 columns: rows j, columns i of the image
+        if (symmetric(kForm) && tile.mirror) {   // the block turned around: rows j, columns i
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             uint32_t x[4];
-            ldmatrix4_trans(side_address(buf0, row, j), x);
-            stmatrix4(side_address(buf1 + (q >> 1) * (kSide / 2), j * 8 + (lane & 7), (q & 1) * 4 + (lane >> 3)), x);
+            ldmatrix4_trans(piece_address(at, lane, j), x);
+            stmatrix4(piece_address(at_lo, j * 8 + (lane & 7), lane >> 3), x);
           }
         }
         fence_proxy_async_smem();
-        named_barrier_sync(1 + side, 128);
-        if (lead) {
-          const int y = tile.i0 + (int)rank * 128;
-          if (kForm != kApplyWeights) {
-            tma_store_3d(&p.out, buf0, col0, y, tile.z);
-            if (kForm == kApply) tma_store_3d(&p.out_lo, buf1, col0, y, tile.z);
-            if (symmetric(kForm) && tile.mirror)
-              for (int i = 0; i < 2; ++i)
-                if (y + i * 64 < p.rows) tma_store_3d(&p.out_lo, buf1 + i * (kSide / 2), y + i * 64, col0, tile.z);
-            tma_commit();
-          }
-          if (reads_tile(kForm)) {
+        __syncwarp();
+        if (lane == 0) {
+          if (kForm != kApplyWeights || p.w16) tma_store_3d(&p.out, at, col0, tile.i0 + row0, tile.z);
+          if (kForm == kApplyWeights) tma_store_3d(&p.weights, at_w, 2 * col0, tile.i0 + row0, tile.z);
+          if (kForm == kApply) tma_store_3d(&p.out_lo, at_lo, col0, tile.i0 + row0, tile.z);
+          if (symmetric(kForm) && tile.mirror) tma_store_3d(&p.out, at_lo, tile.i0 + row0, col0, tile.z);
+          tma_commit();
+          if (kBuffers == 1) {
             tma_wait_read<0>();
             ask();
           }
         }
       }
       if (!ok) break;
+      tmem_fence_before();   // the next tile's products may have this half
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
     }
-    if (lead) {
+    if (lane == 0) {
       tma_wait_all();
       if (!ok) {   // what was asked for may be on its way
         const uint64_t t0 = globaltimer_ns();
@@ -585,16 +579,16 @@ static bool newton_sizes(int count, int M, int N) {
   return count >= 0 && count <= 65535 && M > 0 && N > 0 && N % 8 == 0 && M <= (1 << 20) && N <= (1 << 20) && (int64_t)count * M < ((int64_t)1 << 31);
 }
 
-// Rows of `cols` 16-bit elements at `stride` elements; boxes of 64 columns.
+// Rows of `cols` 16-bit elements at `stride` elements; boxes of 64 columns, or an epilogue's of 32 x 32 (box_rows 0).
 static int newton_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t stride, int box_rows) {
   const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)count}, strides[2] = {(uint64_t)stride * 2, (uint64_t)(stride * rows) * 2};
-  const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
-  return ep_host::make_map(m, false, 3, base, dims, strides, box);
+  const uint32_t box[3] = {box_rows > 0 ? 64u : (uint32_t)kChunkCols, box_rows > 0 ? (uint32_t)box_rows : 32u, 1};
+  return ep_host::make_map(m, false, 3, base, dims, strides, box, box_rows == 0);
 }
 
 template <int kForm>
 static int launch_newton(NewtonParams& p, cudaStream_t s) {
-  constexpr int kSmem = kNewtonStages * kNewtonStage + 4 * kSide + (int)sizeof(NewtonShared) + 1024;
+  constexpr int kSmem = kNewtonStages * kNewtonStage + kNewtonWarps * kWarpBytes + (int)sizeof(NewtonShared) + 1024;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(p.tiles, ep_host::grid_cap(1) / 2));
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(k_newton<kForm>), kSmem) != EP_OK) return EP_ERR_CUDA;
   if (ep_host::launch_dependent(k_newton<kForm>, (int)pairs * 2, kNewtonThreads, kSmem, s, p) != EP_OK) return EP_ERR_CUDA;
@@ -643,8 +637,7 @@ struct Newton {
     p.diagonal = to == space.P ? space.diagonal : nullptr;
     int rc = x_map(&p.a, x, M > N ? 64 : 128);
     if (rc == EP_OK) rc = x_map(&p.b, x, M > N ? 64 : p.wide / 2);
-    if (rc == EP_OK) rc = square_map(&p.out, to, 128);
-    if (rc == EP_OK) rc = square_map(&p.out_lo, to, 64);
+    if (rc == EP_OK) rc = square_map(&p.out, to, 0);
     return rc != EP_OK ? rc : launch_newton<kGram>(p, stream);
   }
   int square(float b, float c) const {
@@ -654,9 +647,8 @@ struct Newton {
     p.diagonal = space.diagonal;
     int rc = square_map(&p.a, space.A, 128);
     if (rc == EP_OK) rc = square_map(&p.b, space.A, p.wide / 2);
-    if (rc == EP_OK) rc = square_map(&p.in, space.A, 128);
-    if (rc == EP_OK) rc = square_map(&p.out, space.P, 128);
-    if (rc == EP_OK) rc = square_map(&p.out_lo, space.P, 64);
+    if (rc == EP_OK) rc = square_map(&p.in, space.A, 0);
+    if (rc == EP_OK) rc = square_map(&p.out, space.P, 0);
     return rc != EP_OK ? rc : launch_newton<kSquare>(p, stream);
   }
   // X' = a X + P X, into buffer `to`; the last one into out or w.
@@ -674,22 +666,24 @@ struct Newton {
     p.diagonal = space.diagonal;
     int rc = tall ? x_map(&p.a, space.x[from], 128) : square_map(&p.a, space.P, 128);
     if (rc == EP_OK) rc = tall ? square_map(&p.b, space.P, p.wide / 2) : x_map(&p.b, space.x[from], 64);
-    if (rc == EP_OK) rc = x_map(&p.in, space.x[from], 128);
-    if (rc == EP_OK) rc = x_map(&p.in_lo, has_lo ? space.lo[from] : space.x[from], 128);
+    if (rc == EP_OK) rc = x_map(&p.in, space.x[from], 0);
+    if (rc == EP_OK) rc = x_map(&p.in_lo, has_lo ? space.lo[from] : space.x[from], 0);
     if (rc != EP_OK) return rc;
     if (!last) {
-      rc = x_map(&p.out, space.x[1 - from], 128);
-      if (rc == EP_OK) rc = x_map(&p.out_lo, space.lo[1 - from], 128);
+      rc = x_map(&p.out, space.x[1 - from], 0);
+      if (rc == EP_OK) rc = x_map(&p.out_lo, space.lo[1 - from], 0);
       return rc != EP_OK ? rc : launch_newton<kApply>(p, stream);
     }
     if (out != nullptr) {
-      rc = x_map(&p.out, out, 128);
+      rc = x_map(&p.out, out, 0);
       return rc != EP_OK ? rc : launch_newton<kApplyOut>(p, stream);
     }
-    p.w = w;
-    p.w16 = w16;
+    p.w16 = w16 != nullptr;
     p.keep = keep;
     p.step = step;
+    rc = newton_map(&p.weights, w, 2 * (int64_t)N, M, count, 2 * (int64_t)N, 32);
+    if (rc == EP_OK && p.w16) rc = x_map(&p.out, w16, 0);
+    if (rc != EP_OK) return rc;
     return launch_newton<kApplyWeights>(p, stream);
   }
 };
