@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
 // ---------------------------------------------------------------- products
 
 constexpr int kNewtonThreads = 384;
-constexpr int kNewtonStages = 5;
+constexpr int kNewtonStages = 4;
 constexpr int kBlock = 256;                           // output rows of a pair's tile, and its columns at most
 constexpr int kInner = 64;                            // fp16 elements of one 128-byte row
 constexpr int kNewtonOperand = 128 * kInner * 2;      // 16 KB: one CTA's part of an operand
@@ -173,7 +173,7 @@ constexpr int kNewtonStage = 2 * kNewtonOperand;
 constexpr int kNewtonWarps = 8;                       // of the epilogue: four for the rows, two sides of column chunks
 constexpr int kChunkCols = 32;                        // columns that a warp takes at a time, of its 32 rows
 constexpr int kPiece = 32 * kChunkCols * 2;           // 2 KB: such a block of 16-bit numbers
-constexpr int kWarpBytes = 4 * kPiece;                // a warp's buffers
+constexpr int kWarpBytes = 6 * kPiece;                // a warp's buffers: three of hi and lo, or one and two of w
 
 enum NewtonForm { kGram, kSquare, kApply, kApplyOut, kApplyWeights };
 __host__ __device__ constexpr bool reads_tile(int form) { return form != kGram; }
@@ -181,28 +181,29 @@ __host__ __device__ constexpr bool symmetric(int form) { return form == kGram ||
 
 struct NewtonParams {
   CUtensorMap a, b;             // operands
-  CUtensorMap in, in_lo;        // what the epilogue adds: A, or X
-  CUtensorMap out, out_lo;
-  CUtensorMap weights;          // kApplyWeights: w as 16-bit halves, 64 at a time
+  const __half *in, *in_lo;     // what the epilogue adds: A, or X (in_lo may be nullptr)
+  int in_stride;
+  CUtensorMap out, out_lo;      // kApplyWeights: w as 16-bit halves
   int count, rows, cols, inner; // of a product
   int wide;                     // columns of a tile: 256 or 128
-  int tiles_m, tiles_n;         // kSquare, kGram: tiles_m only
-  int64_t tiles;
-  bool rows_fast, has_lo;
+  uint32_t tiles_m, tiles_n;    // kSquare, kGram: tiles_m only
+  uint32_t each, tiles;         // of a matrix, of all
+  bool rows_fast;
   bool a_mn, b_mn;
   float scale, add;             // epilogue: scale * sums + (add + diagonal_scale * diagonal) * in
   float diagonal_scale;
   const float* factor;          // [count] or nullptr
   float* diagonal;              // [count, S]: P's
   float keep, step;             // kApplyWeights
-  bool w16;                     // out is their bf16 copy
+  const float* w;
+  __nv_bfloat16* w16;
   int32_t* status;
 };
 
 struct NewtonShared {
   uint64_t full[kNewtonStages], empty[kNewtonStages];
   uint64_t sums_full[2], sums_empty[2];
-  uint64_t tile_full[kNewtonWarps][2];   // what a warp adds, by buffer
+  float columns[kNewtonWarps][kChunkCols];   // P's diagonal for the columns in hand
   uint32_t tmem;
 };
 
@@ -212,24 +213,23 @@ struct NewtonTile {
 };
 
 template <int kForm>
-__device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, int64_t t) {
+__device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, uint32_t t) {
   NewtonTile out;
-  const int each = (int)(p.tiles / p.count);
-  out.z = (int)(t / each);
-  const int u = (int)(t - (int64_t)out.z * each);
+  out.z = (int)(t / p.each);
+  const uint32_t u = t - (uint32_t)out.z * p.each;
   if (symmetric(kForm)) {
-    const int f = kBlock / p.wide, b = u / f;
-    int r = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
-    while ((int64_t)(r + 1) * (r + 2) / 2 <= b) ++r;
-    while ((int64_t)r * (r + 1) / 2 > b) --r;
-    const int c = b - (int)((int64_t)r * (r + 1) / 2);
-    out.i0 = r * kBlock;
-    out.j0 = c * kBlock + (u - b * f) * p.wide;
+    const uint32_t f = kBlock / p.wide, b = f == 1 ? u : u >> 1;
+    uint32_t r = (uint32_t)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
+    while ((r + 1) * (r + 2) / 2 <= b) ++r;   // each is below 2^25
+    while (r * (r + 1) / 2 > b) --r;
+    const uint32_t c = b - r * (r + 1) / 2;
+    out.i0 = (int)r * kBlock;
+    out.j0 = (int)(c * kBlock + (u - b * f) * p.wide);
     out.mirror = c < r;
   } else {
-    const int r = p.rows_fast ? u % p.tiles_m : u / p.tiles_n, c = p.rows_fast ? u / p.tiles_m : u % p.tiles_n;
-    out.i0 = r * kBlock;
-    out.j0 = c * p.wide;
+    const uint32_t fast = p.rows_fast ? p.tiles_m : p.tiles_n, slow = u / fast, rest = u - slow * fast;
+    out.i0 = (int)(p.rows_fast ? rest : slow) * kBlock;
+    out.j0 = (int)(p.rows_fast ? slow : rest) * p.wide;
     out.mirror = false;
   }
   return out;
@@ -255,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
   NewtonShared& sh = *reinterpret_cast<NewtonShared*>(pieces + kNewtonWarps * kWarpBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     prefetch_map(&p.a);
@@ -267,7 +267,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sums_full[i], 1);
       mbar_init(&sh.sums_empty[i], 2 * kNewtonWarps);
-      for (int w = 0; w < kNewtonWarps; ++w) mbar_init(&sh.tile_full[w][i], 1);
     }
     fence_barrier_init();
   }
@@ -277,20 +276,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
   cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = sh.tmem;
-  pdl_launch_dependents();
-  pdl_wait();
-
   bool ok = true;
   const int blocks = (p.inner + kInner - 1) / kInner;
   // a symmetric form's last column tile may lie past the matrix
-  auto next = [&](int64_t& t, NewtonTile& tile) {
+  auto next = [&](uint32_t& t, NewtonTile& tile) {
     for (; t < p.tiles; t += pairs) {
       tile = newton_tile<kForm>(p, t);
       if (tile.j0 < p.cols) return true;
     }
     return false;
   };
+  uint32_t t = pair;
   NewtonTile tile;
+  bool more = next(t, tile);
+  auto step = [&]() {
+    t += pairs;
+    more = next(t, tile);
+  };
+  pdl_launch_dependents();
+  pdl_wait();
   if (warp == 0 || warp == 3) {
     // ---------------------------------------------------------------- copies, a warp an operand
     const bool issue = elect_one(), first = warp == 0;
@@ -300,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     const CUtensorMap* map = first ? &p.a : &p.b;
     const uint32_t to0 = smem_addr(stages) + (first ? 0 : kNewtonOperand), full0 = map_to_rank(smem_addr(&sh.full[0]), 0);
     uint32_t s = 0, phase = 0;
-    for (int64_t t = pair; ok && next(t, tile); t += pairs) {
+    for (; ok && more; step()) {
       const int m0 = first ? tile.i0 + (int)rank * 128 : tile.j0 + (int)rank * half;
       for (int kb = 0; kb < blocks; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
@@ -333,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     const uint32_t step_a = (p.a_mn ? 2048 : 32) >> 4, step_b = (p.b_mn ? 2048 : 32) >> 4;
     const uint32_t idesc = umma_idesc_f16(kBlock, p.wide, p.a_mn, p.b_mn);
     uint32_t s = 0, phase = 0, n = 0;
-    for (int64_t t = pair; ok && next(t, tile); t += pairs, ++n) {
+    for (; ok && more; step(), ++n) {
       const uint32_t half = n & 1, d = tmem + half * kBlock;
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_empty[half], ((n >> 1) & 1) ^ 1, 4 * kWaitNs));
       if (!ok) break;
@@ -358,42 +362,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    // A warp takes its 32 rows, 32 columns at a time, on its own: what is added is copied into one of its buffers
-    // while the chunk before is worked on, replaced by the result in place and copied out.  (128 rows x 64 columns by
-    // four warps with barriers between them, one buffer: 25800 clocks a tile whose products take 16400.)
+    // A warp takes its 32 rows, 32 columns at a time, on its own.  What is added is loaded a chunk ahead into
+    // registers, whole 64-byte rows side by side, and turned to a row a thread by a buffer, in which the result takes its
+    // place and leaves by TMA.  (Loaded by TMA too, a chunk waited 2000 to 5000 clocks for copies that stand
+    // behind the operands' in the copy engine's queue, and a tile's epilogue took longer than its products.)
     const int q = warp & 3, side = (warp - 4) >> 2;
-    constexpr int kBuffers = kForm == kApplyWeights ? 1 : 2;   // those hold w too
+    constexpr int kBuffers = kForm == kApplyWeights ? 2 : 3;
     const uint32_t buffers = smem_addr(pieces) + (warp - 4) * kWarpBytes;
-    uint64_t* const tile_full = sh.tile_full[warp - 4];
+    const uint32_t columns = smem_addr(&sh.columns[warp - 4][0]);
     const int chunks = p.wide / kChunkCols, row0 = (int)rank * 128 + q * 32;
-    auto live = [&](const NewtonTile& x, int ch) { return x.j0 + ch * kChunkCols < p.cols && x.i0 + row0 < p.rows; };
-    int64_t t_ask = pair;
-    int ch_ask = side;
-    uint32_t n_ask = 0;
-    // copy in what the next chunk adds
-    auto ask = [&]() {
-      NewtonTile x;
-      for (; next(t_ask, x); t_ask += pairs, ch_ask = side)
-        if (ch_ask < chunks && live(x, ch_ask)) break;
-      if (t_ask >= p.tiles) return;
-      const int col = x.j0 + ch_ask * kChunkCols, i = n_ask % kBuffers;
-      const uint32_t to = buffers + i * (kWarpBytes / 2), bar = smem_addr(&tile_full[i]);
-      const bool lo = kForm != kSquare && p.has_lo;
-      mbar_arrive_expect_tx(&tile_full[i], (lo ? 2 : 1) * kPiece + (kForm == kApplyWeights ? 2 * kPiece : 0));
-      tma_load_3d<false>(to, &p.in, bar, col, x.i0 + row0, x.z);
-      if (lo) tma_load_3d<false>(to + kPiece, &p.in_lo, bar, col, x.i0 + row0, x.z);
-      if (kForm == kApplyWeights) tma_load_3d<false>(to + 2 * kPiece, &p.weights, bar, 2 * col, x.i0 + row0, x.z);
-      ch_ask += 2;
-      ++n_ask;
+    const bool lo = kForm != kSquare && p.in_lo != nullptr, by_column = kForm != kSquare && !p.rows_fast;
+    auto live = [&](const NewtonTile& x, int ch) { return ch < chunks && x.j0 + ch * kChunkCols < p.cols && x.i0 + row0 < p.rows; };
+    uint4 next_hi[4], next_lo[4], next_w[8];
+    float next_column = 0.0f;
+    uint32_t t_ahead = t;
+    int ch_ahead = side;
+    NewtonTile ahead = tile;
+    bool more_ahead = more;
+    auto fetch = [&]() {   // of the next chunk
+      while (more_ahead && !live(ahead, ch_ahead)) {
+        t_ahead += pairs;
+        ch_ahead = side;
+        more_ahead = next(t_ahead, ahead);
+      }
+      const int col0 = ahead.j0 + ch_ahead * kChunkCols;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = ahead.i0 + row0 + i * 8 + (lane >> 2), col = col0 + (lane & 3) * 8;
+        const bool in = more_ahead && row < p.rows && col < p.cols;
+        const int64_t at = ((int64_t)ahead.z * p.rows + row) * p.in_stride + col;
+        next_hi[i] = in ? ld_cg_v4(p.in + at) : make_uint4(0, 0, 0, 0);
+        if (kForm != kSquare) next_lo[i] = in && lo ? ld_cg_v4(p.in_lo + at) : make_uint4(0, 0, 0, 0);
+      }
+      if (kForm == kApplyWeights) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = ahead.i0 + row0 + i * 4 + (lane >> 3), col = col0 + (lane & 7) * 4;
+          const bool in = more_ahead && row < p.rows && col < p.cols;
+          next_w[i] = in ? ld_cg_v4(p.w + ((int64_t)ahead.z * p.rows + row) * p.cols + col) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (by_column) next_column = more_ahead && col0 + lane < p.cols ? __ldcg(p.diagonal + (int64_t)ahead.z * p.cols + col0 + lane) : 0.0f;
+      ch_ahead += 2;
     };
-    if (reads_tile(kForm) && lane == 0) ask();
+    if (reads_tile(kForm)) fetch();
     uint32_t n = 0, k = 0;   // tiles, chunks
-    for (int64_t t = pair; next(t, tile); t += pairs, ++n) {
+    for (; more; step(), ++n) {
       const uint32_t half = n & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_full[half], (n >> 1) & 1, kWaitNs + (uint64_t)blocks * 4000));
-      if (!ok) break;
-      tmem_fence_after();
-      const uint32_t d = tmem + half * kBlock + ((uint32_t)(q * 32) << 16);
       const float f = p.factor != nullptr ? __ldcg(p.factor + tile.z) : 1.0f;
       const float scale = kForm == kGram ? p.scale * f * f : p.scale;
       const int row = tile.i0 + row0 + lane;
@@ -401,22 +416,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
       const int64_t line = (int64_t)tile.z * p.rows + row;
       const float row_add =
           reads_tile(kForm) && kForm != kSquare && p.rows_fast && there ? fmaf(__ldcg(p.diagonal + line), p.diagonal_scale, p.add) : p.add;
-      int ch = side;
-      for (; ch < chunks && live(tile, ch); ch += 2, ++k) {
-        const int i = k % kBuffers;
-        const uint32_t at = buffers + i * (kWarpBytes / 2), at_lo = at + kPiece, at_w = at + 2 * kPiece;
-        if (reads_tile(kForm)) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tile_full[i], (k / kBuffers) & 1));
-          if (!ok) break;
-          if (kBuffers == 2 && lane == 0) {   // the other buffer's last copy has been read by now
-            tma_wait_read<0>();
-            ask();
-          }
-        } else {
-          if (lane == 0) tma_wait_read<1>();
-        }
-        __syncwarp();
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_full[half], (n >> 1) & 1, kWaitNs + (uint64_t)blocks * 4000));
+      if (!ok) break;
+      tmem_fence_after();
+      const uint32_t d = tmem + half * kBlock + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+      for (int ch = side; live(tile, ch); ch += 2, ++k) {
+        const uint32_t at = buffers + (kForm == kApplyWeights ? 0 : k % kBuffers * 2 * kPiece), at_lo = at + kPiece;
+        const uint32_t at_w = buffers + (1 + (k & 1)) * 2 * kPiece;
         const int col0 = tile.j0 + ch * kChunkCols;
+        if (lane == 0) tma_wait_read<kBuffers - 1>();   // this buffer's last copy
+        __syncwarp();
+        if (reads_tile(kForm)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            st_shared_v4_at(piece_address(at, i * 8 + (lane >> 2), lane & 3), next_hi[i]);
+            if (kForm != kSquare) st_shared_v4_at(piece_address(at_lo, i * 8 + (lane >> 2), lane & 3), next_lo[i]);
+          }
+          if (kForm == kApplyWeights) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + (lane >> 3);
+              st_shared_v4_at(at_w + r * 128 + (((lane & 7) ^ (r & 7)) << 4), next_w[i]);
+            }
+          }
+          if (by_column) sh.columns[warp - 4][lane] = next_column;
+          __syncwarp();
+          fetch();
+        }
         float v[32];
         tmem_ld32(d + ch * kChunkCols, v);
         tmem_wait_ld(v);
@@ -427,19 +454,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
           for (int e = 0; e < 8; ++e) x[e] = v[c * 8 + e] * scale;
           if (reads_tile(kForm)) {
             const uint4 hi = ld_shared_v4_at(piece_address(at, lane, c));
-            uint4 lo = make_uint4(0, 0, 0, 0);
-            if (kForm != kSquare && p.has_lo) lo = ld_shared_v4_at(piece_address(at_lo, lane, c));
-            const uint32_t wh[4] = {hi.x, hi.y, hi.z, hi.w}, wl[4] = {lo.x, lo.y, lo.z, lo.w};
+            uint4 low = make_uint4(0, 0, 0, 0);
+            if (kForm != kSquare) low = ld_shared_v4_at(piece_address(at_lo, lane, c));
+            const uint32_t wh[4] = {hi.x, hi.y, hi.z, hi.w}, wl[4] = {low.x, low.y, low.z, low.w};
             float add[8];   // a, and P's diagonal for the row, or for the column where P stands to the right
 #pragma unroll
             for (int e = 0; e < 8; ++e) add[e] = row_add;
-            if (kForm != kSquare && !p.rows_fast && col0 + c * 8 < p.cols) {
-              const float4* at_columns = reinterpret_cast<const float4*>(p.diagonal + (int64_t)tile.z * p.cols + col0 + c * 8);
-              const float4 c0 = __ldcg(at_columns), c1 = __ldcg(at_columns + 1);
-              add[0] = fmaf(c0.x, p.diagonal_scale, add[0]), add[1] = fmaf(c0.y, p.diagonal_scale, add[1]);
-              add[2] = fmaf(c0.z, p.diagonal_scale, add[2]), add[3] = fmaf(c0.w, p.diagonal_scale, add[3]);
-              add[4] = fmaf(c1.x, p.diagonal_scale, add[4]), add[5] = fmaf(c1.y, p.diagonal_scale, add[5]);
-              add[6] = fmaf(c1.z, p.diagonal_scale, add[6]), add[7] = fmaf(c1.w, p.diagonal_scale, add[7]);
+            if (by_column) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint4 y = ld_shared_v4_at(columns + (c * 2 + e) * 16);
+                add[4 * e] = fmaf(__uint_as_float(y.x), p.diagonal_scale, row_add), add[4 * e + 1] = fmaf(__uint_as_float(y.y), p.diagonal_scale, row_add);
+                add[4 * e + 2] = fmaf(__uint_as_float(y.z), p.diagonal_scale, row_add), add[4 * e + 3] = fmaf(__uint_as_float(y.w), p.diagonal_scale, row_add);
+              }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -510,30 +537,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (kForm != kApplyWeights || p.w16) tma_store_3d(&p.out, at, col0, tile.i0 + row0, tile.z);
-          if (kForm == kApplyWeights) tma_store_3d(&p.weights, at_w, 2 * col0, tile.i0 + row0, tile.z);
+          if (kForm == kApplyWeights)
+            tma_store_3d(&p.out, at_w, 2 * col0, tile.i0 + row0, tile.z);
+          else
+            tma_store_3d(&p.out, at, col0, tile.i0 + row0, tile.z);
           if (kForm == kApply) tma_store_3d(&p.out_lo, at_lo, col0, tile.i0 + row0, tile.z);
           if (symmetric(kForm) && tile.mirror) tma_store_3d(&p.out, at_lo, tile.i0 + row0, col0, tile.z);
           tma_commit();
-          if (kBuffers == 1) {
-            tma_wait_read<0>();
-            ask();
+        }
+        if (kForm == kApplyWeights && p.w16 != nullptr) {   // its block is free again after this
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), c = lane & 3;
+            if (tile.i0 + row0 + r < p.rows && col0 + c * 8 < p.cols)
+              st_v4(p.w16 + ((int64_t)tile.z * p.rows + tile.i0 + row0 + r) * p.cols + col0 + c * 8, ld_shared_v4_at(piece_address(at, r, c)));
           }
         }
       }
-      if (!ok) break;
       tmem_fence_before();   // the next tile's products may have this half
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
     }
-    if (lane == 0) {
-      tma_wait_all();
-      if (!ok) {   // what was asked for may be on its way
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 2000000ull) {
-        }
-      }
-    }
+    if (lane == 0) tma_wait_all();
   }
   if (!ok) set_status(p.status, EP_ERR_TIMEOUT);
   __syncwarp();
@@ -551,7 +576,9 @@ struct NewtonSpace {
   size_t bytes;
 };
 
-static int64_t padded(int n) { return (int64_t)(n + 7) / 8 * 8; }
+// Row stride of A and P: whole 128-byte lines, which a copied row of 64 elements then is one of (S = 1416 without: 870
+// clocks a stage instead of 610).
+static int64_t padded(int n) { return (int64_t)(n + 63) / 64 * 64; }
 
 static NewtonSpace newton_space(int count, int M, int N, void* base) {
   NewtonSpace s;
@@ -576,7 +603,10 @@ static NewtonSpace newton_space(int count, int M, int N, void* base) {
 }
 
 static bool newton_sizes(int count, int M, int N) {
-  return count >= 0 && count <= 65535 && M > 0 && N > 0 && N % 8 == 0 && M <= (1 << 20) && N <= (1 << 20) && (int64_t)count * M < ((int64_t)1 << 31);
+  if (count < 0 || count > 65535 || M <= 0 || N <= 0 || N % 8 != 0 || M > (1 << 20) || N > (1 << 20)) return false;
+  const int64_t lim = (int64_t)1 << 31, square = (std::min(M, N) + kBlock - 1) / kBlock;
+  const int64_t tiles = (int64_t)((M + kBlock - 1) / kBlock) * ((N + kBlock / 2 - 1) / (kBlock / 2));
+  return (int64_t)count * M < lim && count * tiles < lim && count * square * (square + 1) < lim;   // tiles are numbered in 32 bits
 }
 
 // Rows of `cols` 16-bit elements at `stride` elements; boxes of 64 columns, or an epilogue's of 32 x 32 (box_rows 0).
@@ -610,10 +640,11 @@ struct Newton {
       p.tiles_m = (p.rows + kBlock - 1) / kBlock;
       p.tiles_n = (p.cols + wide - 1) / wide;
       const int64_t each = sym ? (int64_t)p.tiles_m * (p.tiles_m + 1) / 2 * (kBlock / wide) : (int64_t)p.tiles_m * p.tiles_n;
-      p.tiles = each * count;
+      p.each = (uint32_t)each;
+      p.tiles = (uint32_t)(each * count);
     };
     of(kBlock);
-    if (p.tiles < std::max(1, ep_host::grid_cap(1) / 2)) of(kBlock / 2);
+    if ((int)p.tiles < ep_host::num_sms() / 2) of(kBlock / 2);   // whatever the SM budget: results go by the sizes alone
   }
   NewtonParams start(int rows, int cols, int inner, bool sym) const {
     NewtonParams p{};
@@ -647,7 +678,8 @@ struct Newton {
     p.diagonal = space.diagonal;
     int rc = square_map(&p.a, space.A, 128);
     if (rc == EP_OK) rc = square_map(&p.b, space.A, p.wide / 2);
-    if (rc == EP_OK) rc = square_map(&p.in, space.A, 0);
+    p.in = space.A;
+    p.in_stride = (int)padded(S);
     if (rc == EP_OK) rc = square_map(&p.out, space.P, 0);
     return rc != EP_OK ? rc : launch_newton<kSquare>(p, stream);
   }
@@ -658,7 +690,9 @@ struct Newton {
     const bool tall = M > N;
     p.rows_fast = !tall;
     p.b_mn = !tall;
-    p.has_lo = has_lo;
+    p.in = space.x[from];
+    p.in_lo = has_lo ? space.lo[from] : nullptr;
+    p.in_stride = N;
     p.factor = factor;
     p.scale = (last ? 1.0f / kHeld : 1.0f) / kHeld;
     p.diagonal_scale = last ? 1.0f / kHeld : 1.0f;
@@ -666,8 +700,6 @@ struct Newton {
     p.diagonal = space.diagonal;
     int rc = tall ? x_map(&p.a, space.x[from], 128) : square_map(&p.a, space.P, 128);
     if (rc == EP_OK) rc = tall ? square_map(&p.b, space.P, p.wide / 2) : x_map(&p.b, space.x[from], 64);
-    if (rc == EP_OK) rc = x_map(&p.in, space.x[from], 0);
-    if (rc == EP_OK) rc = x_map(&p.in_lo, has_lo ? space.lo[from] : space.x[from], 0);
     if (rc != EP_OK) return rc;
     if (!last) {
       rc = x_map(&p.out, space.x[1 - from], 0);
@@ -678,11 +710,11 @@ struct Newton {
       rc = x_map(&p.out, out, 0);
       return rc != EP_OK ? rc : launch_newton<kApplyOut>(p, stream);
     }
-    p.w16 = w16 != nullptr;
+    p.w = w;
+    p.w16 = w16;
     p.keep = keep;
     p.step = step;
-    rc = newton_map(&p.weights, w, 2 * (int64_t)N, M, count, 2 * (int64_t)N, 32);
-    if (rc == EP_OK && p.w16) rc = x_map(&p.out, w16, 0);
+    rc = newton_map(&p.out, w, 2 * (int64_t)N, M, count, 2 * (int64_t)N, 32);
     if (rc != EP_OK) return rc;
     return launch_newton<kApplyWeights>(p, stream);
   }
