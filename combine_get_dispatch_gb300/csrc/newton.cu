@@ -173,7 +173,7 @@ constexpr int kNewtonStage = 2 * kNewtonOperand;
 constexpr int kNewtonWarps = 8;                       // of the epilogue: four for the rows, two sides of column chunks
 constexpr int kChunkCols = 32;                        // columns that a warp takes at a time, of its 32 rows
 constexpr int kPiece = 32 * kChunkCols * 2;           // 2 KB: such a block of 16-bit numbers
-constexpr int kWarpBytes = 6 * kPiece;                // a warp's buffers: three of hi and lo, or one and two of w
+constexpr int kWarpBytes = 6 * kPiece;                // a warp's buffers: three of hi and lo, or two and one of w
 
 enum NewtonForm { kGram, kSquare, kApply, kApplyOut, kApplyWeights };
 __host__ __device__ constexpr bool reads_tile(int form) { return form != kGram; }
@@ -183,7 +183,7 @@ struct NewtonParams {
   CUtensorMap a, b;             // operands
   const __half *in, *in_lo;     // what the epilogue adds: A, or X (in_lo may be nullptr)
   int in_stride;
-  CUtensorMap out, out_lo;      // kApplyWeights: w as 16-bit halves
+  CUtensorMap out, out_lo;      // (not kApplyWeights)
   int count, rows, cols, inner; // of a product
   int wide;                     // columns of a tile: 256 or 128
   uint32_t tiles_m, tiles_n;    // kSquare, kGram: tiles_m only
@@ -195,7 +195,7 @@ struct NewtonParams {
   const float* factor;          // [count] or nullptr
   float* diagonal;              // [count, S]: P's
   float keep, step;             // kApplyWeights
-  const float* w;
+  float* w;
   __nv_bfloat16* w16;
   int32_t* status;
 };
@@ -203,7 +203,7 @@ struct NewtonParams {
 struct NewtonShared {
   uint64_t full[kNewtonStages], empty[kNewtonStages];
   uint64_t sums_full[2], sums_empty[2];
-  float columns[kNewtonWarps][kChunkCols];   // P's diagonal for the columns in hand
+  float columns[kNewtonWarps][2][kChunkCols];   // P's diagonal for the columns of a buffer
   uint32_t tmem;
 };
 
@@ -242,6 +242,17 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&v)[4])
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
+// 16 (4) bytes to shared memory when they come; zeros where there is nothing to read.
+__device__ __forceinline__ void copy_async16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Instruction descriptor, fp16 operands and fp32 sums.
 __device__ __forceinline__ uint32_t umma_idesc_f16(int m, int n, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
@@ -249,8 +260,7 @@ __device__ __forceinline__ uint32_t umma_idesc_f16(int m, int n, bool a_mn, bool
 
 template <int kForm>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k_newton(const __grid_constant__ NewtonParams p) {
-  extern __shared__ uint8_t raw[];
-  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t stages[];
   uint8_t* pieces = stages + kNewtonStages * kNewtonStage;
   NewtonShared& sh = *reinterpret_cast<NewtonShared*>(pieces + kNewtonWarps * kWarpBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -362,50 +372,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    // A warp takes its 32 rows, 32 columns at a time, on its own.  What is added is loaded a chunk ahead into
-    // registers, whole 64-byte rows side by side, and turned to a row a thread by a buffer, in which the result takes its
-    // place and leaves by TMA.  (Loaded by TMA too, a chunk waited 2000 to 5000 clocks for copies that stand
-    // behind the operands' in the copy engine's queue, and a tile's epilogue took longer than its products.)
+    // A warp takes its 32 rows, 32 columns at a time, on its own.  What is added is copied into a buffer a chunk
+    // ahead (cp.async: whole 64-byte rows side by side), read from it a row a thread, replaced there by the result,
+    // which leaves by TMA.  (Copied in by TMA, it stood behind the operands in the copy engine's queue, 2000 to 5000
+    // clocks; loaded a chunk ahead into registers, a chunk's arithmetic took 2500 clocks instead of 900, waiting
+    // for those loads with its own.)
     const int q = warp & 3, side = (warp - 4) >> 2;
     constexpr int kBuffers = kForm == kApplyWeights ? 2 : 3;
-    const uint32_t buffers = smem_addr(pieces) + (warp - 4) * kWarpBytes;
-    const uint32_t columns = smem_addr(&sh.columns[warp - 4][0]);
+    const uint32_t buffers = smem_addr(pieces) + (warp - 4) * kWarpBytes, at_w = buffers + 4 * kPiece;
+    const uint32_t columns = smem_addr(&sh.columns[warp - 4][0][0]);
     const int chunks = p.wide / kChunkCols, row0 = (int)rank * 128 + q * 32;
     const bool lo = kForm != kSquare && p.in_lo != nullptr, by_column = kForm != kSquare && !p.rows_fast;
     auto live = [&](const NewtonTile& x, int ch) { return ch < chunks && x.j0 + ch * kChunkCols < p.cols && x.i0 + row0 < p.rows; };
-    uint4 next_hi[4], next_lo[4], next_w[8];
-    float next_column = 0.0f;
-    uint32_t t_ahead = t;
+    // the chunk that is copied next: (t_ahead, ch_ahead), number k_ahead
+    uint32_t t_ahead = t, k_ahead = 0;
     int ch_ahead = side;
     NewtonTile ahead = tile;
     bool more_ahead = more;
-    auto fetch = [&]() {   // of the next chunk
+    auto seek = [&]() {
       while (more_ahead && !live(ahead, ch_ahead)) {
         t_ahead += pairs;
         ch_ahead = side;
         more_ahead = next(t_ahead, ahead);
       }
-      const int col0 = ahead.j0 + ch_ahead * kChunkCols;
+    };
+    auto fetch = [&]() {
+      seek();
+      if (more_ahead) {
+        const uint32_t to = buffers + k_ahead % kBuffers * 2 * kPiece;
+        const int col0 = ahead.j0 + ch_ahead * kChunkCols, c = lane & 3;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = ahead.i0 + row0 + i * 8 + (lane >> 2), col = col0 + (lane & 3) * 8;
-        const bool in = more_ahead && row < p.rows && col < p.cols;
-        const int64_t at = ((int64_t)ahead.z * p.rows + row) * p.in_stride + col;
-        next_hi[i] = in ? ld_cg_v4(p.in + at) : make_uint4(0, 0, 0, 0);
-        if (kForm != kSquare) next_lo[i] = in && lo ? ld_cg_v4(p.in_lo + at) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + (lane >> 2);
+          const bool in = ahead.i0 + row0 + r < p.rows && col0 + c * 8 < p.cols;
+          const int64_t at = in ? ((int64_t)ahead.z * p.rows + ahead.i0 + row0 + r) * p.in_stride + col0 + c * 8 : 0;
+          copy_async16(piece_address(to, r, c), p.in + at, in);
+          if (kForm != kSquare) copy_async16(piece_address(to + kPiece, r, c), lo ? p.in_lo + at : p.in, in && lo);
+        }
+        if (by_column) {
+          const bool in = col0 + lane < p.cols;
+          copy_async4(columns + k_ahead % 2 * (kChunkCols * 4) + lane * 4, p.diagonal + (in ? (int64_t)ahead.z * p.cols + col0 + lane : 0), in);
+        }
+        if (kForm != kApplyWeights) ch_ahead += 2;
+        ++k_ahead;
       }
-      if (kForm == kApplyWeights) {
+      copy_async_commit();
+    };
+    auto fetch_weights = [&]() {   // of the same chunk as the fetch before; 8 pieces of 4 a row, 128-byte swizzle
+      if (more_ahead) {
+        const int col0 = ahead.j0 + ch_ahead * kChunkCols, c = lane & 7;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int row = ahead.i0 + row0 + i * 4 + (lane >> 3), col = col0 + (lane & 7) * 4;
-          const bool in = more_ahead && row < p.rows && col < p.cols;
-          next_w[i] = in ? ld_cg_v4(p.w + ((int64_t)ahead.z * p.rows + row) * p.cols + col) : make_uint4(0, 0, 0, 0);
+          const int r = i * 4 + (lane >> 3);
+          const bool in = ahead.i0 + row0 + r < p.rows && col0 + c * 4 < p.cols;
+          copy_async16(at_w + r * 128 + ((c ^ (r & 7)) << 4), p.w + (in ? ((int64_t)ahead.z * p.rows + ahead.i0 + row0 + r) * p.cols + col0 + c * 4 : 0), in);
         }
+        ch_ahead += 2;
       }
-      if (by_column) next_column = more_ahead && col0 + lane < p.cols ? __ldcg(p.diagonal + (int64_t)ahead.z * p.cols + col0 + lane) : 0.0f;
-      ch_ahead += 2;
+      copy_async_commit();
     };
     if (reads_tile(kForm)) fetch();
+    if (kForm == kApplyWeights) fetch_weights();
     uint32_t n = 0, k = 0;   // tiles, chunks
     for (; more; step(), ++n) {
       const uint32_t half = n & 1;
@@ -422,27 +449,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
       const uint32_t d = tmem + half * kBlock + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
       for (int ch = side; live(tile, ch); ch += 2, ++k) {
-        const uint32_t at = buffers + (kForm == kApplyWeights ? 0 : k % kBuffers * 2 * kPiece), at_lo = at + kPiece;
-        const uint32_t at_w = buffers + (1 + (k & 1)) * 2 * kPiece;
+        const uint32_t at = buffers + k % kBuffers * 2 * kPiece, at_lo = at + kPiece;
         const int col0 = tile.j0 + ch * kChunkCols;
-        if (lane == 0) tma_wait_read<kBuffers - 1>();   // this buffer's last copy
+        // the next buffer's last copy, or (nothing is read ahead) this one's
+        if (kForm != kApplyWeights && lane == 0) tma_wait_read<(reads_tile(kForm) ? 1 : 2)>();
         __syncwarp();
         if (reads_tile(kForm)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            st_shared_v4_at(piece_address(at, i * 8 + (lane >> 2), lane & 3), next_hi[i]);
-            if (kForm != kSquare) st_shared_v4_at(piece_address(at_lo, i * 8 + (lane >> 2), lane & 3), next_lo[i]);
-          }
-          if (kForm == kApplyWeights) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = i * 4 + (lane >> 3);
-              st_shared_v4_at(at_w + r * 128 + (((lane & 7) ^ (r & 7)) << 4), next_w[i]);
-            }
-          }
-          if (by_column) sh.columns[warp - 4][lane] = next_column;
-          __syncwarp();
           fetch();
+          copy_async_wait<1>();
+          __syncwarp();
         }
         float v[32];
         tmem_ld32(d + ch * kChunkCols, v);
@@ -463,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
             if (by_column) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint4 y = ld_shared_v4_at(columns + (c * 2 + e) * 16);
+                const uint4 y = ld_shared_v4_at(columns + k % 2 * (kChunkCols * 4) + (c * 2 + e) * 16);
                 add[4 * e] = fmaf(__uint_as_float(y.x), p.diagonal_scale, row_add), add[4 * e + 1] = fmaf(__uint_as_float(y.y), p.diagonal_scale, row_add);
                 add[4 * e + 2] = fmaf(__uint_as_float(y.z), p.diagonal_scale, row_add), add[4 * e + 3] = fmaf(__uint_as_float(y.w), p.diagonal_scale, row_add);
               }
@@ -534,23 +549,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
             stmatrix4(piece_address(at_lo, j * 8 + (lane & 7), lane >> 3), x);
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (kForm == kApplyWeights)
-            tma_store_3d(&p.out, at_w, 2 * col0, tile.i0 + row0, tile.z);
-          else
-            tma_store_3d(&p.out, at, col0, tile.i0 + row0, tile.z);
-          if (kForm == kApply) tma_store_3d(&p.out_lo, at_lo, col0, tile.i0 + row0, tile.z);
-          if (symmetric(kForm) && tile.mirror) tma_store_3d(&p.out, at_lo, tile.i0 + row0, col0, tile.z);
-          tma_commit();
-        }
-        if (kForm == kApplyWeights && p.w16 != nullptr) {   // its block is free again after this
+        if (kForm == kApplyWeights) {   // by whole rows, so that the buffers are free at once
+          __syncwarp();
+          const int64_t base = ((int64_t)tile.z * p.rows + tile.i0 + row0) * p.cols + col0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2), c = lane & 3;
-            if (tile.i0 + row0 + r < p.rows && col0 + c * 8 < p.cols)
-              st_v4(p.w16 + ((int64_t)tile.z * p.rows + tile.i0 + row0 + r) * p.cols + col0 + c * 8, ld_shared_v4_at(piece_address(at, r, c)));
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), c = lane & 7;
+            if (tile.i0 + row0 + r < p.rows && col0 + c * 4 < p.cols)
+              st_v4(p.w + base + (int64_t)r * p.cols + c * 4, ld_shared_v4_at(at_w + r * 128 + ((c ^ (r & 7)) << 4)));
+          }
+          if (p.w16 != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + (lane >> 2), c = lane & 3;
+              if (tile.i0 + row0 + r < p.rows && col0 + c * 8 < p.cols)
+                st_v4(p.w16 + base + (int64_t)r * p.cols + c * 8, ld_shared_v4_at(piece_address(at, r, c)));
+            }
+          }
+          __syncwarp();
+          fetch_weights();
+        } else {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&p.out, at, col0, tile.i0 + row0, tile.z);
+            if (kForm == kApply) tma_store_3d(&p.out_lo, at_lo, col0, tile.i0 + row0, tile.z);
+            if (symmetric(kForm) && tile.mirror) tma_store_3d(&p.out, at_lo, tile.i0 + row0, col0, tile.z);
+            tma_commit();
           }
         }
       }
@@ -558,6 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&sh.sums_empty[half]), 0));
     }
+    copy_async_wait<0>();
     if (lane == 0) tma_wait_all();
   }
   if (!ok) set_status(p.status, EP_ERR_TIMEOUT);
@@ -618,7 +644,7 @@ static int newton_map(CUtensorMap* m, const void* base, int64_t cols, int64_t ro
 
 template <int kForm>
 static int launch_newton(NewtonParams& p, cudaStream_t s) {
-  constexpr int kSmem = kNewtonStages * kNewtonStage + kNewtonWarps * kWarpBytes + (int)sizeof(NewtonShared) + 1024;
+  constexpr int kSmem = kNewtonStages * kNewtonStage + kNewtonWarps * kWarpBytes + (int)sizeof(NewtonShared);
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(p.tiles, ep_host::grid_cap(1) / 2));
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(k_newton<kForm>), kSmem) != EP_OK) return EP_ERR_CUDA;
   if (ep_host::launch_dependent(k_newton<kForm>, (int)pairs * 2, kNewtonThreads, kSmem, s, p) != EP_OK) return EP_ERR_CUDA;
@@ -714,8 +740,6 @@ struct Newton {
     p.w16 = w16;
     p.keep = keep;
     p.step = step;
-    rc = newton_map(&p.out, w, 2 * (int64_t)N, M, count, 2 * (int64_t)N, 32);
-    if (rc != EP_OK) return rc;
     return launch_newton<kApplyWeights>(p, stream);
   }
 };
