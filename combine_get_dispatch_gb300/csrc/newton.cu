@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
 // ---------------------------------------------------------------- products
 
 constexpr int kNewtonThreads = 384;
-constexpr int kNewtonStages = 4;
+constexpr int kNewtonStages = 5;                      // of a whole tile's operands; more of a narrow one's
+constexpr int kMostNewtonStages = 6;
 constexpr int kBlock = 256;                           // output rows of a pair's tile, and its columns at most
 constexpr int kInner = 64;                            // fp16 elements of one 128-byte row
 constexpr int kNewtonOperand = 128 * kInner * 2;      // 16 KB: one CTA's part of an operand
@@ -173,7 +174,7 @@ constexpr int kNewtonStage = 2 * kNewtonOperand;
 constexpr int kNewtonWarps = 8;                       // of the epilogue: four for the rows, two sides of column chunks
 constexpr int kChunkCols = 32;                        // columns that a warp takes at a time, of its 32 rows
 constexpr int kPiece = 32 * kChunkCols * 2;           // 2 KB: such a block of 16-bit numbers
-constexpr int kWarpBytes = 6 * kPiece;                // a warp's buffers: three of hi and lo, or two and one of w
+constexpr int kWarpBytes = 4 * kPiece;                // a warp's buffers: two of hi and lo, or one and one of w
 
 enum NewtonForm { kGram, kSquare, kApply, kApplyOut, kApplyWeights };
 __host__ __device__ constexpr bool reads_tile(int form) { return form != kGram; }
@@ -186,6 +187,7 @@ struct NewtonParams {
   CUtensorMap out, out_lo;      // (not kApplyWeights)
   int count, rows, cols, inner; // of a product
   int wide;                     // columns of a tile: 256 or 128
+  uint32_t stages, stage_bytes;
   uint32_t tiles_m, tiles_n;    // kSquare, kGram: tiles_m only
   uint32_t each, tiles;         // of a matrix, of all
   bool rows_fast;
@@ -201,7 +203,7 @@ struct NewtonParams {
 };
 
 struct NewtonShared {
-  uint64_t full[kNewtonStages], empty[kNewtonStages];
+  uint64_t full[kMostNewtonStages], empty[kMostNewtonStages];
   uint64_t sums_full[2], sums_empty[2];
   float columns[kNewtonWarps][2][kChunkCols];   // P's diagonal for the columns of a buffer
   uint32_t tmem;
@@ -261,7 +263,7 @@ __device__ __forceinline__ uint32_t umma_idesc_f16(int m, int n, bool a_mn, bool
 template <int kForm>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k_newton(const __grid_constant__ NewtonParams p) {
   extern __shared__ __align__(1024) uint8_t stages[];
-  uint8_t* pieces = stages + kNewtonStages * kNewtonStage;
+  uint8_t* pieces = stages + kNewtonStages * kNewtonStage;   // narrow tiles' stages take no more
   NewtonShared& sh = *reinterpret_cast<NewtonShared*>(pieces + kNewtonWarps * kWarpBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -270,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
   if (threadIdx.x == 0) {
     prefetch_map(&p.a);
     prefetch_map(&p.b);
-    for (int s = 0; s < kNewtonStages; ++s) {
+    for (int s = 0; s < kMostNewtonStages; ++s) {
       mbar_init(&sh.full[s], 1);      // the first CTA's, with the bytes of both
       mbar_init(&sh.empty[s], 1);     // the products' commit
     }
@@ -320,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
         if (!ok) break;
         if (issue) {
-          const uint32_t to = to0 + s * kNewtonStage, bar = full0 + s * (uint32_t)sizeof(uint64_t);
+          const uint32_t to = to0 + s * p.stage_bytes, bar = full0 + s * (uint32_t)sizeof(uint64_t);
           if (first && rank == 0) mbar_arrive_expect_tx(&sh.full[s], both);
           if (!mn) {
             tma_load_3d<true>(to, map, bar, kb * kInner, m0, tile.z);
@@ -328,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
             for (int i = 0; i < (first ? 2 : half / 64); ++i) tma_load_3d<true>(to + i * (kNewtonOperand / 2), map, bar, m0 + i * 64, kb * kInner, tile.z);
           }
         }
-        if (++s == kNewtonStages) {
+        if (++s == p.stages) {
           s = 0;
           phase ^= 1;
         }
@@ -347,7 +349,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     const uint32_t step_a = (p.a_mn ? 2048 : 32) >> 4, step_b = (p.b_mn ? 2048 : 32) >> 4;
     const uint32_t idesc = umma_idesc_f16(kBlock, p.wide, p.a_mn, p.b_mn);
     uint32_t s = 0, phase = 0, n = 0;
-    for (; ok && more; step(), ++n) {
+    while (ok && more) {
+      step();   // looked up while this tile's products run
       const uint32_t half = n & 1, d = tmem + half * kBlock;
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_empty[half], ((n >> 1) & 1) ^ 1, 4 * kWaitNs));
       if (!ok) break;
@@ -357,29 +360,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
         if (!ok) break;
         tmem_fence_after();
         if (issue) {
-          const uint32_t a = a0 + s * (kNewtonStage >> 4), b = b0 + s * (kNewtonStage >> 4);
+          const uint32_t a = a0 + s * (p.stage_bytes >> 4), b = b0 + s * (p.stage_bytes >> 4);
 #pragma unroll
           for (uint32_t i = 0; i < kInner / 16; ++i) umma_bf16_pair(d, a + i * step_a, b + i * step_b, idesc, kb > 0 || i > 0);
           umma_commit_pair(&sh.empty[s]);
         }
-        if (++s == kNewtonStages) {
+        if (++s == p.stages) {
           s = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
       if (issue) umma_commit_pair(&sh.sums_full[half]);
+      ++n;
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    // A warp takes its 32 rows, 32 columns at a time, on its own.  What is added is copied into a buffer a chunk
-    // ahead (cp.async: whole 64-byte rows side by side), read from it a row a thread, replaced there by the result,
-    // which leaves by TMA.  (Copied in by TMA, it stood behind the operands in the copy engine's queue, 2000 to 5000
-    // clocks; loaded a chunk ahead into registers, a chunk's arithmetic took 2500 clocks instead of 900, waiting
-    // for those loads with its own.)
+    // A warp takes its 32 rows, 32 columns at a time, on its own.  What is added is copied into a buffer (cp.async:
+    // whole 64-byte rows side by side) while the last chunk leaves the other, read from it a row a thread, replaced
+    // there by the result, which leaves by TMA.  (Copied in by TMA, it stood behind the operands in the copy engine's
+    // queue, 2000 to 5000 clocks; loaded a chunk ahead into registers, a chunk's arithmetic took 2500 clocks instead
+    // of 900, waiting for those loads with its own.)
     const int q = warp & 3, side = (warp - 4) >> 2;
-    constexpr int kBuffers = kForm == kApplyWeights ? 2 : 3;
-    const uint32_t buffers = smem_addr(pieces) + (warp - 4) * kWarpBytes, at_w = buffers + 4 * kPiece;
+    constexpr int kBuffers = kForm == kApplyWeights ? 1 : 2;
+    const uint32_t buffers = smem_addr(pieces) + (warp - 4) * kWarpBytes, at_w = buffers + 2 * kPiece;
     const uint32_t columns = smem_addr(&sh.columns[warp - 4][0][0]);
     const int chunks = p.wide / kChunkCols, row0 = (int)rank * 128 + q * 32;
     const bool lo = kForm != kSquare && p.in_lo != nullptr, by_column = kForm != kSquare && !p.rows_fast;
@@ -413,26 +417,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
           const bool in = col0 + lane < p.cols;
           copy_async4(columns + k_ahead % 2 * (kChunkCols * 4) + lane * 4, p.diagonal + (in ? (int64_t)ahead.z * p.cols + col0 + lane : 0), in);
         }
-        if (kForm != kApplyWeights) ch_ahead += 2;
+        if (kForm == kApplyWeights) {   // 8 pieces of 4 a row, 128-byte swizzle
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), e = lane & 7;
+            const bool in = ahead.i0 + row0 + r < p.rows && col0 + e * 4 < p.cols;
+            copy_async16(at_w + r * 128 + ((e ^ (r & 7)) << 4), p.w + (in ? ((int64_t)ahead.z * p.rows + ahead.i0 + row0 + r) * p.cols + col0 + e * 4 : 0), in);
+          }
+        }
+        ch_ahead += 2;
         ++k_ahead;
       }
       copy_async_commit();
     };
-    auto fetch_weights = [&]() {   // of the same chunk as the fetch before; 8 pieces of 4 a row, 128-byte swizzle
-      if (more_ahead) {
-        const int col0 = ahead.j0 + ch_ahead * kChunkCols, c = lane & 7;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3);
-          const bool in = ahead.i0 + row0 + r < p.rows && col0 + c * 4 < p.cols;
-          copy_async16(at_w + r * 128 + ((c ^ (r & 7)) << 4), p.w + (in ? ((int64_t)ahead.z * p.rows + ahead.i0 + row0 + r) * p.cols + col0 + c * 4 : 0), in);
-        }
-        ch_ahead += 2;
-      }
-      copy_async_commit();
-    };
     if (reads_tile(kForm)) fetch();
-    if (kForm == kApplyWeights) fetch_weights();
     uint32_t n = 0, k = 0;   // tiles, chunks
     for (; more; step(), ++n) {
       const uint32_t half = n & 1;
@@ -451,14 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
       for (int ch = side; live(tile, ch); ch += 2, ++k) {
         const uint32_t at = buffers + k % kBuffers * 2 * kPiece, at_lo = at + kPiece;
         const int col0 = tile.j0 + ch * kChunkCols;
-        // the next buffer's last copy, or (nothing is read ahead) this one's
-        if (kForm != kApplyWeights && lane == 0) tma_wait_read<(reads_tile(kForm) ? 1 : 2)>();
+        if (reads_tile(kForm)) copy_async_wait<0>();
         __syncwarp();
-        if (reads_tile(kForm)) {
-          fetch();
-          copy_async_wait<1>();
-          __syncwarp();
-        }
         float v[32];
         tmem_ld32(d + ch * kChunkCols, v);
         tmem_wait_ld(v);
@@ -567,17 +559,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
             }
           }
           __syncwarp();
-          fetch_weights();
         } else {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
+            tma_wait_read<0>();   // the last chunk's copy, out of the other buffer
             tma_store_3d(&p.out, at, col0, tile.i0 + row0, tile.z);
             if (kForm == kApply) tma_store_3d(&p.out_lo, at_lo, col0, tile.i0 + row0, tile.z);
             if (symmetric(kForm) && tile.mirror) tma_store_3d(&p.out, at_lo, tile.i0 + row0, col0, tile.z);
             tma_commit();
           }
+          __syncwarp();
         }
+        if (reads_tile(kForm)) fetch();
       }
       tmem_fence_before();   // the next tile's products may have this half
       __syncwarp();
@@ -665,6 +659,8 @@ struct Newton {
       p.wide = wide;
       p.tiles_m = (p.rows + kBlock - 1) / kBlock;
       p.tiles_n = (p.cols + wide - 1) / wide;
+      p.stage_bytes = kNewtonOperand + wide / 2 * kInner * 2;
+      p.stages = std::min<uint32_t>(kMostNewtonStages, kNewtonStages * kNewtonStage / p.stage_bytes);
       const int64_t each = sym ? (int64_t)p.tiles_m * (p.tiles_m + 1) / 2 * (kBlock / wide) : (int64_t)p.tiles_m * p.tiles_n;
       p.each = (uint32_t)each;
       p.tiles = (uint32_t)(each * count);
