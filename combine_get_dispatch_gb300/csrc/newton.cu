@@ -27,8 +27,7 @@
 
 #include <cmath>
 
-#include "ep_common.cuh"
-#include "umma.cuh"
+#include "newton.cuh"
 
 namespace ep {
 
@@ -36,36 +35,6 @@ namespace ep {
 
 constexpr int kSourceThreads = 256;
 constexpr int kMostParts = 64;            // of a matrix's norm
-constexpr float kHeld = 256.0f;           // X, A and P are held this many times as large
-
-struct Source {
-  const void* g;
-  bool f32;
-  float* m;               // or nullptr: u is the gradient
-  float momentum;
-  bool nesterov;
-  int64_t each;           // elements of a matrix, a multiple of 8
-  int64_t part;           // elements of a part, a multiple of 8 kSourceThreads
-  int parts, count;
-  float eps;
-  float* sums;            // [count, parts]
-  float* factor;          // [count]
-  __half *hi, *lo;        // [count, each]; lo may be nullptr
-};
-
-__device__ __forceinline__ void load8(const Source& s, int64_t i, float (&v)[8]) {
-  if (s.f32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(s.g) + i);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(s.g) + i);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
-  }
-}
-
 // m <- momentum m + g and the squares' sums of u, a part of a matrix a CTA, in an
 // order that only the sizes give.  Memory bounds it.
 __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
@@ -131,11 +100,9 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
     const int64_t z = item / s.parts, begin = (item - z * s.parts) * s.part, end = min(begin + s.part, s.each), base = z * s.each;
     float square = 0.0f;
     for (int k = 0; k < s.parts; ++k) square += __ldcg(s.sums + z * s.parts + k);
-    const float norm = sqrtf(square) + s.eps;   // at least 1e-12
-    // 2^q the least power of two that is not below 2^8 / norm
-    const int q = 8 - ilogbf(norm);
-    const float up = norm <= 1.152921505e18f ? __uint_as_float((uint32_t)(127 + q) << 23) : __uint_as_float(0x7fc00000u);   // 2^60; NaN beyond and for NaN
-    if (begin == 0 && threadIdx.x == 0) s.factor[z] = norm <= 1.152921505e18f ? kHeld / (norm * up) : __uint_as_float(0x7fc00000u);
+    float up, factor;
+    source_scale(square, s.eps, up, factor);
+    if (begin == 0 && threadIdx.x == 0) s.factor[z] = factor;
     for (int64_t i = begin + threadIdx.x * 8; i < end; i += kSourceThreads * 8) {
       float u[8];
       load8(s, base + i, u);
@@ -148,14 +115,7 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
       }
       uint32_t h[4], l[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = u[2 * k] * up, y = u[2 * k + 1] * up;
-        const __half2 v = __floats2half2_rn(x, y);
-        const float2 b = __half22float2(v);
-        const __half2 r = __floats2half2_rn(x - b.x, y - b.y);
-        h[k] = *reinterpret_cast<const uint32_t*>(&v);
-        l[k] = *reinterpret_cast<const uint32_t*>(&r);
-      }
+      for (int k = 0; k < 4; ++k) split_f16(u[2 * k] * up, u[2 * k + 1] * up, h[k], l[k]);
       st_v4(s.hi + base + i, make_uint4(h[0], h[1], h[2], h[3]));
       if (s.lo != nullptr) st_v4(s.lo + base + i, make_uint4(l[0], l[1], l[2], l[3]));
     }
@@ -254,11 +214,6 @@ __device__ __forceinline__ void copy_async4(uint32_t to, const void* from, bool 
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Instruction descriptor, fp16 operands and fp32 sums.
-__device__ __forceinline__ uint32_t umma_idesc_f16(int m, int n, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
 
 template <int kForm>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k_newton(const __grid_constant__ NewtonParams p) {
@@ -477,9 +432,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float2 y = __half22float2(*reinterpret_cast<const __half2*>(&wh[e]));
+              float2 y = floats_of(wh[e]);
               if (kForm != kSquare) {
-                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&wl[e]));
+                const float2 l = floats_of(wl[e]);
                 y.x += l.x;
                 y.y += l.y;
               }
@@ -519,13 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
               if (kForm == kApplyOut) {
                 h[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
               } else {
-                const __half2 r = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
-                h[e] = *reinterpret_cast<const uint32_t*>(&r);
-                if (kForm == kApply) {
-                  const float2 y = __half22float2(r);
-                  const __half2 rest = __floats2half2_rn(x[2 * e] - y.x, x[2 * e + 1] - y.y);
-                  l[e] = *reinterpret_cast<const uint32_t*>(&rest);
-                }
+                split_f16(x[2 * e], x[2 * e + 1], h[e], l[e]);   // l: kApply
               }
             }
           }
@@ -742,13 +691,29 @@ struct Newton {
 
 static int newton(Source src, int count, int M, int N, int steps, const float* abc, float eps, __nv_bfloat16* out, float* w,
                   __nv_bfloat16* w16, float keep, float step, void* workspace, int32_t* status, cudaStream_t s) {
+  src.eps = eps;
+  if (std::min(M, N) <= kSmallSide && std::max(M, N) <= kSmallLength) {
+    SmallNewton p{};
+    p.src = src;
+    p.src.count = count;
+    p.M = M;
+    p.N = N;
+    p.steps = steps;
+    std::copy(abc, abc + 3 * steps, p.abc);
+    p.out = out;
+    p.w = w;
+    p.w16 = w16;
+    p.keep = keep;
+    p.step = step;
+    p.status = status;
+    return launch_newton_small(p, s);
+  }
   Newton n = {count, M, N, std::min(M, N), newton_space(count, M, N, workspace), status, s};
   src.each = (int64_t)M * N;
   const int64_t unit = 8 * kSourceThreads;
   src.part = std::max<int64_t>(2 * unit, ((src.each + kMostParts - 1) / kMostParts + unit - 1) / unit * unit);
   src.parts = (int)((src.each + src.part - 1) / src.part);
   src.count = count;
-  src.eps = eps;
   src.sums = n.space.sums;
   src.factor = n.space.factor;
   src.hi = n.space.x[0];

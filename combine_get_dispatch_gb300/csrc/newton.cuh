@@ -1,0 +1,78 @@
+// newton.cuh -- what the kernels of the orthogonalised update share: their source,
+// and how X is held.
+#pragma once
+
+#include "umma.cuh"
+
+namespace ep {
+
+constexpr float kHeld = 256.0f;           // X, A and P are held this many times as large
+
+struct Source {
+  const void* g;
+  bool f32;
+  float* m;               // or nullptr: u is the gradient
+  float momentum;
+  bool nesterov;
+  int64_t each;           // elements of a matrix, a multiple of 8
+  int64_t part;           // elements of a part, a multiple of 8 kSourceThreads
+  int parts, count;
+  float eps;
+  float* sums;            // [count, parts]
+  float* factor;          // [count]
+  __half *hi, *lo;        // [count, each]; lo may be nullptr
+};
+
+__device__ __forceinline__ void load8(const Source& s, int64_t i, float (&v)[8]) {
+  if (s.f32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(s.g) + i);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(s.g) + i);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+  }
+}
+
+// norm + eps -> the power of two that brings u near 2^8, and the factor that is
+// left; NaN for both where the norm is not finite or passes 2^60.
+__device__ __forceinline__ void source_scale(float square, float eps, float& up, float& factor) {
+  const float norm = sqrtf(square) + eps;   // at least 1e-12
+  const bool fits = norm <= 1.152921505e18f;
+  // the least power of two that is not below 2^8 / norm
+  up = fits ? __uint_as_float((uint32_t)(127 + 8 - ilogbf(norm)) << 23) : __uint_as_float(0x7fc00000u);
+  factor = fits ? kHeld / (norm * up) : __uint_as_float(0x7fc00000u);
+}
+
+// Two numbers as hi and lo words.
+__device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 b = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x - b.x, y - b.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ float2 floats_of(uint32_t half2) { return __half22float2(*reinterpret_cast<const __half2*>(&half2)); }
+
+// Instruction descriptor, fp16 operands and fp32 sums.
+__device__ __forceinline__ uint32_t umma_idesc_f16(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Matrices whose X fits one SM's registers, and with the polynomial its shared memory.
+constexpr int kSmallSide = 128, kSmallLength = 256;
+struct SmallNewton {
+  Source src;
+  int M, N, steps;
+  float abc[3 * 32];
+  __nv_bfloat16* out;       // or nullptr and
+  float* w;
+  __nv_bfloat16* w16;
+  float keep, step;
+  int32_t* status;
+};
+int launch_newton_small(const SmallNewton& p, cudaStream_t stream);
+
+}  // namespace ep
