@@ -104,6 +104,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
     tma_load_1d(to, static_cast<const uint8_t*>(a) + (int64_t)k * kPart * a_bytes, n * a_bytes, &sh.part[slot]);
     if (b != nullptr) tma_load_1d(to + kPartBytes / 2, static_cast<const uint8_t*>(b) + (int64_t)k * kPart * 32, n * 32, &sh.part[slot]);
   };
+  // part k's momentum or weights, replaced in place, go out by one copy (16 bytes a thread are half sectors, and
+  // took three times as long), and the part after next comes in where the last one went out
+  auto send = [&](int k, float* to, int offset, const void* a, int a_bytes, const void* b) {
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    const int n = min(kPart, vectors - k * kPart);
+    if (to != nullptr) {
+      tma_store_1d(to + (int64_t)k * kPart * 8, raw + (hi - wide) + (parts_seen + k) % kParts * kPartBytes + offset, n * 32);
+      tma_commit();
+      tma_wait_read<1>();
+    }
+    if (k > 0) bring(k - 1 + kParts, a, a_bytes, b);
+  };
   // wait for part k; where it is
   auto part = [&](int k) {
     const uint32_t at = parts_seen + k;
@@ -118,6 +132,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
     const uint8_t* const g = static_cast<const uint8_t*>(p.src.g) + base / 8 * g_bytes;
     const float* const momentum = p.src.m != nullptr ? p.src.m + base : nullptr;
     fence_proxy_async_smem();
+    if (threadIdx.x == 0) tma_wait_read<0>();
     __syncthreads();   // nobody uses X and the polynomial of the matrix before
     for (int k = 0; k < kParts; ++k) bring(k, g, g_bytes, momentum);
     // everything is zero where the matrix is not: rows past S, columns past L
@@ -143,20 +158,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
         u[0] = bf16_lo(v.x), u[1] = bf16_hi(v.x), u[2] = bf16_lo(v.y), u[3] = bf16_hi(v.y);
         u[4] = bf16_lo(v.z), u[5] = bf16_hi(v.z), u[6] = bf16_lo(v.w), u[7] = bf16_hi(v.w);
       }
-      if (momentum != nullptr) read8(at + kPartBytes / 2 + threadIdx.x * 32, m);
-      __syncthreads();
-      bring(k + kParts, g, g_bytes, momentum);
-      if (i >= vectors) continue;
       if (momentum != nullptr) {
+        const uint32_t at_m = at + kPartBytes / 2 + threadIdx.x * 32;
+        read8(at_m, m);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           m[e] = fmaf(p.src.momentum, m[e], u[e]);
           u[e] = p.src.nesterov ? fmaf(p.src.momentum, m[e], u[e]) : m[e];
         }
-        float4* to = reinterpret_cast<float4*>(p.src.m + base + (int64_t)i * 8);
-        to[0] = make_float4(m[0], m[1], m[2], m[3]);
-        to[1] = make_float4(m[4], m[5], m[6], m[7]);
+        st_shared_v4_at(at_m, make_uint4(__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3])));
+        st_shared_v4_at(at_m + 16, make_uint4(__float_as_uint(m[4]), __float_as_uint(m[5]), __float_as_uint(m[6]), __float_as_uint(m[7])));
       }
+      send(k, p.src.m != nullptr ? p.src.m + base : nullptr, kPartBytes / 2, g, g_bytes, momentum);
+      if (i >= vectors) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) square = fmaf(u[e], u[e], square);
       const int r = i / per_row, c = (i - r * per_row) * 8;
@@ -171,6 +185,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
       }
     }
     parts_seen += parts;
+    if (threadIdx.x == 0) tma_wait_read<0>();   // X goes where the momentum comes from
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) square += __shfl_xor_sync(0xffffffffu, square, o);
     if (lane == 0) sh.sums[warp] = square;
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
     }
     if (!ok) break;
     // ---------------------------------------------------------------- out
-    const float* const w = p.out == nullptr ? p.w + base : nullptr;
+    float* const w = p.out == nullptr ? p.w + base : nullptr;
     if (w != nullptr) {
       fence_proxy_async_smem();
       __syncthreads();
@@ -329,45 +344,39 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
 #pragma unroll 1
     for (int k = 0; k < parts; ++k) {
       const int i = k * kPart + threadIdx.x;
-      float4 a = {}, b = {};
-      if (w != nullptr) {
-        const uint32_t at = part(k) + threadIdx.x * 32;
-        const uint4 v0 = ld_shared_v4_at(at), v1 = ld_shared_v4_at(at + 16);
-        a = make_float4(__uint_as_float(v0.x), __uint_as_float(v0.y), __uint_as_float(v0.z), __uint_as_float(v0.w));
-        b = make_float4(__uint_as_float(v1.x), __uint_as_float(v1.y), __uint_as_float(v1.z), __uint_as_float(v1.w));
-        __syncthreads();
-        bring(k + kParts, w, 32, nullptr);
-      }
-      if (i >= vectors) continue;
       const int r = i / per_row, c = (i - r * per_row) * 8;
-      float y[8];
-      if (!tall) {
+      const bool in = i < vectors;
+      float y[8] = {};
+      if (in && !tall) {
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
           const uint4 v = ld_shared_v4_at(wide_address(wide, r, c + e));
           y[e] = __uint_as_float(v.x), y[e + 1] = __uint_as_float(v.y), y[e + 2] = __uint_as_float(v.z), y[e + 3] = __uint_as_float(v.w);
         }
-      } else {
+      } else if (in) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y[e]) : "r"(wide_address(wide, c + e, r)) : "memory");
       }
-      const int64_t at = base + (int64_t)i * 8;
-      if (w == nullptr) {
-        st_v4(p.out + at, make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])));
-      } else {
-        a.x = fmaf(-p.step, y[0], p.keep * a.x), a.y = fmaf(-p.step, y[1], p.keep * a.y);
-        a.z = fmaf(-p.step, y[2], p.keep * a.z), a.w = fmaf(-p.step, y[3], p.keep * a.w);
-        b.x = fmaf(-p.step, y[4], p.keep * b.x), b.y = fmaf(-p.step, y[5], p.keep * b.y);
-        b.z = fmaf(-p.step, y[6], p.keep * b.z), b.w = fmaf(-p.step, y[7], p.keep * b.w);
-        float4* to = reinterpret_cast<float4*>(p.w + at);
-        to[0] = a;
-        to[1] = b;
-        if (p.w16 != nullptr) st_v4(p.w16 + at, make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w)));
+      __nv_bfloat16* to = p.out;
+      if (w != nullptr) {
+        const uint32_t at = part(k) + threadIdx.x * 32;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const uint4 v = ld_shared_v4_at(at + e * 4);
+          y[e] = fmaf(-p.step, y[e], p.keep * __uint_as_float(v.x)), y[e + 1] = fmaf(-p.step, y[e + 1], p.keep * __uint_as_float(v.y));
+          y[e + 2] = fmaf(-p.step, y[e + 2], p.keep * __uint_as_float(v.z)), y[e + 3] = fmaf(-p.step, y[e + 3], p.keep * __uint_as_float(v.w));
+          st_shared_v4_at(at + e * 4, make_uint4(__float_as_uint(y[e]), __float_as_uint(y[e + 1]), __float_as_uint(y[e + 2]), __float_as_uint(y[e + 3])));
+        }
+        send(k, w, 0, w, 32, nullptr);
+        to = p.w16;
       }
+      if (in && to != nullptr)
+        st_v4(to + base + (int64_t)i * 8, make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])));
     }
     if (w != nullptr) parts_seen += parts;
     ok = __syncthreads_and(ok) != 0;   // the next matrix comes in
   }
+  if (threadIdx.x == 0) tma_wait_all();
   if (!ok) set_status(p.status, EP_ERR_TIMEOUT);
   tmem_fence_before();
   __syncthreads();
