@@ -6,15 +6,18 @@
 // Both are bound by reading each used expert's weights once.  The first deals
 // out (expert, h column) pairs evenly over the CTAs, the second output columns, so
 // that every CTA sums its own columns over all experts in a fixed order and
-// nothing is added up between CTAs.  A CTA walks its columns in units: 16 columns'
-// rows of gate and up, or 32 rows of W_down, whole in the inner index, for the
-// tokens of one expert.  Its warps:
-//   8 multiply: each its eighth of a stage's inner index, 32 weight rows as the
-//     first operand and 8 tokens as the second (m16n8k16: at a few tokens an expert
-//     the widest form that is not mostly padding; tcgen05 wants 64 rows or more in
-//     tiles of their own, and an SM gets 13 to 110 columns)
-//   4 add the eight sums of a unit up and finish it while the next one's products run
-//   1 copies the weights (TMA, 1 KB of each row a stage), the rest tokens' rows
+// nothing is added up between CTAs.  A CTA walks its columns in units: 32 columns'
+// rows of gate and up, or 64 rows of W_down, whole in the inner index, for the
+// tokens of one expert.  The weights' rows are the first operand of tcgen05.mma (of
+// 128 rows, those past the unit's being whatever lies there), the tokens
+// the second: 16 or 32 of them for 4 KB of weights read from shared memory, so the
+// products cost a fifth of the time in which the weights arrive, and no thread
+// touches a weight.  (By mma.sync E4M3 weights had to be turned into fp16 first, which bounded the
+// kernels at 3.5 to 4.5 TB/s.)  Warps:
+//   2 bring the sums out of tensor memory and finish a unit
+//   1 issues the products
+//   2 copy weights (TMA, 8 rows x 512 bytes a copy), 1 tokens' rows
+//   6 put the tokens where the products read them
 // The second kernel comes up as the first one's CTAs leave and fills its ring with
 // weights before it waits for h.
 
@@ -23,20 +26,21 @@
 
 namespace ep {
 
-constexpr int kParts = 8;             // warps that multiply
-constexpr int kAdders = 4;            // warps that add up
-constexpr int kPiece = 1024;          // bytes of a weight row in a stage
-constexpr int kUnitRows = 32;
-constexpr int kRedPitch = 36;         // floats: a warp's sums fall into distinct banks
-constexpr int kMaxSlots = EP_MOE_FEW_TOKENS * kMaxK;
-constexpr int kMaxFewStages = 8;
+constexpr int kEpilogues = 2, kWeightWarps = 2, kTurners = 6;
+constexpr int kFewThreads = (kEpilogues + 2 + kWeightWarps + kTurners) * kWarp;
+constexpr int kUnitRows = 64;         // of weights
+constexpr int kBlocks = 4;            // 128-byte blocks of a row in a stage
+constexpr int kGroupBytes = kBlocks * 1024;   // 8 rows of a stage
+constexpr int kWeightBytes = kUnitRows / 8 * kGroupBytes;
+constexpr int kProductBytes = 2 * kWeightBytes;   // what a product of 128 rows reads, from a stage's start on
+constexpr int kSums = 4;              // sums on their way out of tensor memory
+constexpr int kScaleRing = 16;        // stages whose tokens' scales are kept: more than are between the copies and the epilogue
+constexpr int kMaxFewStages = 6;
 constexpr int kFewSmem = 226 * 1024;
-__host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 24; }        // tokens of an expert taken at a time: two stages at least
-__host__ __device__ constexpr int token_warps_of(bool fp8) { return fp8 ? 3 : 2; }   // fp8: they also turn numbers into fp16
-__host__ __device__ constexpr int few_threads(bool fp8) { return (kParts + kAdders + 1 + token_warps_of(fp8)) * kWarp; }
+__host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 32; }   // tokens of an expert taken at a time
 
 struct FewParams {
-  CUtensorMap whole, four, one;   // weights [2 E or E][N][K]: boxes of 1 KB of a unit's rows (kIn: of gate or up), 4 and 1
+  CUtensorMap whole, tail;     // weights [2 E or E][N][K]: 8 rows of 4 blocks of 128 bytes; of one block, which K may cut
   const uint8_t* scales;
   const __nv_bfloat16* v;      // kIn: x [T, H]; kOut: h [T k, I]
   const int64_t* idx;          // [T, k]
@@ -46,36 +50,46 @@ struct FewParams {
   int T, k, E, K, N;           // K: inner extent; N: columns of h or out
 };
 
+struct FewShared {
+  uint64_t full[kMaxFewStages], turned[kMaxFewStages], empty[kMaxFewStages];
+  uint64_t sums_full[kSums], sums_empty[kSums];
+  int group_slots[kMaxE / kWarp], group_used[kMaxE / kWarp], group_most[kMaxE / kWarp];   // of 32 experts
+  int n_used, most;                    // used experts; slots of the largest
+  uint32_t tmem;
+  float scales[kScaleRing][kBlocks][pass_of(true)];   // E4M3: what a token's block was divided by
+  float up[2][pass_of(false)][kUnitRows / 2];         // kIn: on its way to its gate
+};
+
 // What every CTA works out first: the used experts in rising order, and their
 // slots in rising order.
 struct FewUsed {
   int16_t expert, first, count, pad;   // slots first .. first + count of the lists
 };
 struct FewLists {
-  FewUsed used[kMaxE];
-  int16_t slot[kMaxSlots], token[kMaxSlots];
-  float weight[kMaxSlots];
-  int16_t id[kMaxSlots];               // expert of a slot, -1: unused
-  int16_t start[kMaxE];
-  int group_slots[kMaxE / kWarp], group_used[kMaxE / kWarp], group_most[kMaxE / kWarp];   // of 32 experts
-  int n_used, most;                    // used experts; slots of the largest
-};
-
-struct FewShared {
-  uint64_t full[kMaxFewStages], empty[kMaxFewStages];
-  uint64_t red_full[2], red_empty[2];
-  FewLists lists;
-  float sums[EP_MOE_FEW_TOKENS * kUnitRows];   // kOut: the columns in hand, [token][column]
+  FewUsed* used;             // [E]
+  float* weight;             // [n], as the next three
+  int16_t *slot, *token, *id;   // id: expert of a slot, -1: unused
+  int16_t* start;            // [E]
+  float* sums;               // kOut: [T][kUnitRows], the columns in hand
+  static __host__ __device__ int bytes(int E, int T, int k) { return (E * 10 + T * k * 10 + T * kUnitRows * 4 + 127) / 128 * 128; }
+  __device__ __forceinline__ FewLists(uint8_t* at, int E, int T, int k) {
+    used = reinterpret_cast<FewUsed*>(at);
+    sums = reinterpret_cast<float*>(used + E);
+    weight = sums + T * kUnitRows;
+    slot = reinterpret_cast<int16_t*>(weight + T * k);
+    token = slot + T * k;
+    id = token + T * k;
+    start = id + T * k;
+  }
 };
 
 // masks: a bit a slot for every expert; memory that nothing else uses yet.
-template <int kThreads>
-__device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, uint32_t* masks, bool report) {
+__device__ __forceinline__ void few_lists(const FewParams& p, FewShared& sh, const FewLists& l, uint32_t* masks, bool report) {
   const int n = p.T * p.k, words = (n + 31) / 32, groups = (p.E + 31) / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < p.E * words; i += kThreads) masks[i] = 0;
+  for (int i = threadIdx.x; i < p.E * words; i += kFewThreads) masks[i] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += kFewThreads) {
     const int64_t e = p.idx[i];
     const bool fits = e >= 0 && e < p.E;
     if (report && !fits && e != -1) set_status(p.status, EP_ERR_INVALID_ARG);
@@ -89,21 +103,21 @@ __device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, uint3
       for (int w = 0; w < words; ++w) c += __popc(masks[e * words + w]);
     return c;
   };
-  for (int q = warp; q < groups; q += kThreads / kWarp) {
+  for (int q = warp; q < groups; q += kFewThreads / kWarp) {
     const int c = count_of(q * 32 + lane);
     const int all = __reduce_add_sync(0xffffffffu, c), most = __reduce_max_sync(0xffffffffu, c);
     const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
     if (lane == 0) {
-      l.group_slots[q] = all;
-      l.group_used[q] = __popc(some);
-      l.group_most[q] = most;
+      sh.group_slots[q] = all;
+      sh.group_used[q] = __popc(some);
+      sh.group_most[q] = most;
     }
   }
   __syncthreads();
-  for (int q = warp; q < groups; q += kThreads / kWarp) {
+  for (int q = warp; q < groups; q += kFewThreads / kWarp) {
     const bool before = lane < q;
-    const int slots = __reduce_add_sync(0xffffffffu, before ? l.group_slots[lane] : 0);
-    const int used = __reduce_add_sync(0xffffffffu, before ? l.group_used[lane] : 0);
+    const int slots = __reduce_add_sync(0xffffffffu, before ? sh.group_slots[lane] : 0);
+    const int used = __reduce_add_sync(0xffffffffu, before ? sh.group_used[lane] : 0);
     const int c = count_of(q * 32 + lane);
     int upto = c;
 #pragma unroll
@@ -118,16 +132,16 @@ __device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, uint3
       l.start[q * 32 + lane] = (int16_t)first;
     }
     if (q == 0) {
-      const int all = __reduce_add_sync(0xffffffffu, lane < groups ? l.group_used[lane] : 0);
-      const int most = __reduce_max_sync(0xffffffffu, lane < groups ? l.group_most[lane] : 0);
+      const int all = __reduce_add_sync(0xffffffffu, lane < groups ? sh.group_used[lane] : 0);
+      const int most = __reduce_max_sync(0xffffffffu, lane < groups ? sh.group_most[lane] : 0);
       if (lane == 0) {
-        l.n_used = all;
-        l.most = most;
+        sh.n_used = all;
+        sh.most = most;
       }
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += kFewThreads) {
     const int e = l.id[i];
     if (e < 0) continue;
     int at = l.start[e] + __popc(masks[e * words + (i >> 5)] & ((1u << (i & 31)) - 1));
@@ -140,22 +154,24 @@ __device__ __forceinline__ void few_lists(const FewParams& p, FewLists& l, uint3
   __syncthreads();
 }
 
-// A CTA's units, one after another: `cols` columns from `col` on of an expert, for
+// A CTA's units, one after another: `cols` columns from `col` on of expert e, for
 // the tokens s0 .. s0 + m of the lists.
 template <bool kIn, int kPass>
 struct FewWalk {
-  const FewLists* l;
+  const FewUsed* used;
+  int n_used;
   int N, left;           // kIn: (expert, column) pairs to come, from `col` of expert d on; kOut: columns from `col` on
   int d, e, col, cols, s0, m, behind;   // behind: the expert's tokens after these
   bool last;             // kOut: unit of these columns
 
-  __device__ __forceinline__ FewWalk(const FewLists& lists, int n) {
-    l = &lists;
+  __device__ __forceinline__ FewWalk(const FewUsed* list, int count, int n) {
+    used = list;
+    n_used = count;
     N = n;
-    const int64_t all = kIn ? (int64_t)lists.n_used * n : lists.n_used > 0 ? n : 0;
+    const int64_t all = kIn ? (int64_t)n_used * n : n_used > 0 ? n : 0;
     const int at = (int)(all * blockIdx.x / gridDim.x);
     left = (int)(all * (blockIdx.x + 1) / gridDim.x) - at;
-    d = kIn ? at / n : lists.n_used - 1;
+    d = kIn ? at / n : n_used - 1;
     col = kIn ? at - d * n : at;
     cols = s0 = m = behind = 0;
   }
@@ -173,7 +189,7 @@ struct FewWalk {
         if (left <= 0) return false;
         cols = min(min(kUnitRows / 2, N - col), left);
       } else {
-        if (++d >= l->n_used) {
+        if (++d >= n_used) {
           left -= cols;
           col += cols;
           if (left <= 0) return false;
@@ -181,69 +197,75 @@ struct FewWalk {
           d = 0;
         }
       }
-      const FewUsed u = l->used[d];
+      const FewUsed u = used[d];
       e = u.expert;
       s0 = u.first;
       behind = u.count;
     }
     m = min(kPass, behind);
     behind -= m;
-    last = !kIn && behind == 0 && d + 1 == l->n_used;
+    last = !kIn && behind == 0 && d + 1 == n_used;
     return true;
   }
 };
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// ---------------------------------------------------------------- products
+
+__device__ __forceinline__ void umma_few(bool fp8, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool add) {
+  constexpr uint32_t kWeightsHi = ((uint32_t)kGroupBytes >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 4 KB apart
+  if (fp8)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "r"(kWeightsHi), "r"(kDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "r"(kWeightsHi), "r"(kDescHi)
+        : "memory");
+}
+// Instruction descriptor: 128 rows, n tokens; E4M3 or bf16 operands, fp32 sums.
+__device__ __forceinline__ uint32_t umma_few_idesc(bool fp8, int n) {
+  return (1u << 4) | (fp8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four E4M3 numbers as fp16, exactly (one instruction a pair; a bf16 form of them
-// took 12 for the four and bounded the kernels at 3.5-4.0 TB/s of weights).
-__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
-}
-
-// So tokens' bf16 numbers are multiplied as fp16: a block of 128 inner elements
-// whose largest is in [2^e, 2^(e+1)) as x 2^(14-e), which is x itself down to
-// 2^-31 of the largest and 2^-39 of the largest off below: far less than sums in 32
-// bits lose.  A block with an infinity or NaN gets the scale NaN.
-// 32 elements a lane, 128 over four lanes; the scale 2^(e-14) by the first of them.
-__device__ __forceinline__ void scaled_f16(const uint4 (&v)[4], uint8_t* to, float* scale, bool first) {
-  const uint32_t w[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
-                          v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
-  uint32_t tops[4];
+// A token's bf16 numbers as two E4M3 ones, for E4M3 weights: in a block of 128
+// inner elements whose largest is in [2^e, 2^(e+1)), x = 2^(e-7) (hi + lo / 16) with
+// hi = E4M3(x 2^(7-e)) and lo = E4M3 of what that leaves, times 16: columns 2 j and
+// 2 j + 1 of the products.  bf16 has 8 significant bits and each part 4, so this is x
+// itself down to 2^-13 of the largest, and 2^-21 of the largest off below: no more
+// than sums in 32 bits lose.  A block with an infinity or NaN gets the scale NaN.
+// 8 elements a lane, a block sixteen lanes.
+__device__ __forceinline__ void split_e4m3(uint4 v, uint32_t (&hi)[2], uint32_t (&lo)[2], float& scale) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t a = w[0] & 0x7fff7fffu, b = w[1] & 0x7fff7fffu;
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(w[2] & 0x7fff7fffu));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(w[3] & 0x7fff7fffu));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  uint32_t top = max(a >> 16, a & 0xffffu);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    tops[i] = w[i] & 0x7fff7fffu;
+  for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const uint32_t e = top >> 7;   // biased; up = 2^(134 - e), no more than 2^127
+  const float up = __uint_as_float((e <= 7 ? 254u : 261u - min(e, 254u)) << 23);
+  scale = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(e <= 7 ? 0x00400000u : (e - 7) << 23);
 #pragma unroll
-    for (int q = 4; q < 16; q += 4) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(tops[i]) : "r"(w[i + q] & 0x7fff7fffu));
-  }
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(tops[0]) : "r"(tops[1]));
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(tops[2]) : "r"(tops[3]));
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(tops[0]) : "r"(tops[2]));
-  uint32_t top = max(tops[0] >> 16, tops[0] & 0xffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const uint32_t e = top >> 7;   // biased; up = 2^(141 - e), no more than 2^127
-  const float up = __uint_as_float((e <= 14 ? 254u : 268u - min(e, 254u)) << 23);
-  if (first) *scale = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(e <= 14 ? 0x00400000u : (e - 14) << 23);
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[2], r[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t f[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const __half2 h = __floats2half2_rn(bf16_lo(w[4 * i + q]) * up, bf16_hi(w[4 * i + q]) * up);
-      f[q] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int q = 0; q < 2; ++q) {
+      const float x = bf16_lo(w[2 * i + q]) * up, y = bf16_hi(w[2 * i + q]) * up;
+      h[q] = cvt_e4m3x2(x, y);
+      uint32_t back;
+      asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}" : "=r"(back) : "r"(h[q]));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+      r[q] = cvt_e4m3x2((x - f.x) * 16.0f, (y - f.y) * 16.0f);
     }
-    st_shared_v4(to + 16 * i, make_uint4(f[0], f[1], f[2], f[3]));
+    hi[i] = __byte_perm(h[0], h[1], 0x5410);
+    lo[i] = __byte_perm(r[0], r[1], 0x5410);
   }
 }
 
@@ -251,346 +273,298 @@ __device__ __forceinline__ float ue8m0_value(uint32_t b) {
   return b == 255 ? __uint_as_float(0x7fc00000u) : b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
 }
 
-// Where a role is in the ring of stages.
-struct RingPosition {
-  int s;
-  uint32_t phase;
-  int stages, stage_bytes;
+// A bounded wait that looks at the clock (a slow read) only after some tries.
+__device__ __forceinline__ bool wait_few(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitNs) {
+  bool ok = false;
+  for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok || mbar_wait_bounded(bar, parity, limit_ns));
+}
 
+// Where a role is in a ring.
+struct RingPosition {
+  int s, size;
+  uint32_t phase;
+
+  __device__ __forceinline__ RingPosition(int n) : s(0), size(n), phase(0) {}
   __device__ __forceinline__ void advance() {
-    if (++s == stages) {
+    if (++s == size) {
       s = 0;
       phase ^= 1;
     }
   }
-  __device__ __forceinline__ int offset() const { return s * stage_bytes; }
 };
 
-// A token's part of a stage: 8 lanes' 16 bytes (fp8: every second 16) fall into
-// distinct banks; fp8: the scales of its 8 blocks lie behind.
-__host__ __device__ constexpr int token_bytes(bool fp8) { return fp8 ? 2 * kPiece : kPiece; }
-__host__ __device__ constexpr int token_pitch(bool fp8) { return token_bytes(fp8) + (fp8 ? 48 : 64); }
-
-// A warp's eighth of a unit: 32 rows from column col of expert e on, 8 G tokens.
-// Nothing in here branches on what the unit holds (what lies where no row or token
-// does is multiplied and not used): with branches around its loads a stage took
-// 1500 clocks, most of them waiting for one load after the other.
-template <bool kFp8, bool kIn, int G>
-__device__ __forceinline__ void few_products(const FewParams& p, FewShared& sh, int e, int col, const uint8_t* ring, float* red, int chunks,
-                                             uint32_t unit, RingPosition& position, bool& ok) {
-  constexpr int kOne = kFp8 ? 1 : 2, kChunk = kPiece / kOne, kTokenPitch = token_pitch(kFp8);
-  constexpr int kStep = kFp8 ? 64 : 32;   // inner elements a warp multiplies at a time: 16 bytes of weights a lane
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, odd = g & 1;
-  const int k0 = warp * 2 * kStep;        // this warp's first inner element of a stage
-  // this lane's rows of a stage: kIn gate and up of column g, then of g + 8; kOut g, g + 8, g + 16, g + 24
-  auto row_of = [&](int q) { return kIn ? (q & 1) * 16 + (q >> 1) * 8 + g : q * 8 + g; };
-  float acc[2][G][4] = {};
-  const uint8_t* scale[4] = {};
-  uint32_t sc[4] = {};
+// The sums of a unit's rows for 8 G (E4M3) or 16 G tokens: y[j] of token j, a row a
+// thread; ok: no wait has run out.
+template <bool kFp8, int G>
+__device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int chunks, int K, const uint8_t* scale, RingPosition& sums, uint32_t& stage,
+                                         float (&y)[pass_of(false)], bool& ok) {
+  constexpr int kTokens = (kFp8 ? 8 : 16) * G;
+  const int lane = threadIdx.x & 31;
   if (kFp8) {
-    const int blocks_n = p.N / kFp8Block, blocks_k = p.K / kFp8Block;
+    const int blocks = K / kFp8Block;
+    uint32_t next[kBlocks];
+    auto fetch = [&](int c) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = min(col + (kIn ? (q >> 1) * 8 + g : q * 8 + g), p.N - 1);
-      scale[q] = p.scales + ((int64_t)(kIn ? e * 2 + (q & 1) : e) * blocks_n + n / kFp8Block) * blocks_k;
-      if (warp < blocks_k) sc[q] = __ldg(scale[q] + warp);
-    }
-  }
-  for (int c = 0; c < chunks; ++c) {
-    const int left = p.K - c * kChunk;   // inner elements from this stage on
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[position.s], position.phase));
-    if (k0 < left) {
-      const uint32_t at = smem_addr(ring + position.offset()), tokens = at + kUnitRows * kPiece;
-      const uint32_t wa = at + k0 * kOne + t * 16, va = tokens + g * kTokenPitch + k0 * 2 + t * (kFp8 ? 32 : 16);
-      // Rows lie 1 KB apart, in the same banks: lanes of odd rows read the two steps in the other order, so that
-      // a quarter-warp's two rows fall into different halves of the banks, and swap.
-      uint4 r[4][2];
+      for (int b = 0; b < kBlocks; ++b) next[b] = c * kBlocks + b < blocks ? __ldg(scale + c * kBlocks + b) : 0u;
+    };
+    fetch(0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+    for (int j = 0; j < kTokens; ++j) y[j] = 0.0f;
+    for (int c = 0; c < chunks; ++c) {
+      float f[kBlocks];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) r[q][i] = ld_shared_v4_at(wa + row_of(q) * kPiece + (odd ^ i) * 64);
-      if constexpr (kFp8) {   // a block of 128 inner elements, whose scale is one a row and one a token
-        uint4 lo[2][G], hi[2][G];
-        float token[G][2];   // scales of tokens 2 t and 2 t + 1
-        auto tokens_of = [&](int i) {
+      for (int b = 0; b < kBlocks; ++b) f[b] = ue8m0_value(next[b]);
+      fetch(c + 1);
+      if (ok) ok = wait_few(&sh.sums_full[sums.s], sums.phase, 4 * kWaitNs);
+      tmem_fence_after();
+      const uint32_t at = tmem + sums.s * (kBlocks * 16 * G);
 #pragma unroll
-          for (int j = 0; j < G; ++j) {
-            lo[i][j] = ld_shared_v4_at(va + j * 8 * kTokenPitch + i * kStep * 2);
-            hi[i][j] = ld_shared_v4_at(va + j * 8 * kTokenPitch + i * kStep * 2 + 16);
-          }
-        };
-        tokens_of(0);
-        if (G == 1) tokens_of(1);
+      for (int b = 0; b < kBlocks; ++b) {
+        if (c * kBlocks + b < blocks) {
+          const float* const token = sh.scales[stage % kScaleRing][b];
 #pragma unroll
-        for (int j = 0; j < G; ++j)
+          for (int i = 0; i < G; ++i) {
+            float v[16];
+            tmem_ld16(at + b * 16 * G + i * 16, v);
+            tmem_wait_ld(v);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            asm volatile("ld.shared.f32 %0, [%1];"
-                         : "=f"(token[j][i])
-                         : "r"(tokens + (j * 8 + 2 * t + i) * kTokenPitch + token_bytes(true) + warp * 4));
-        float sum[2][G][4] = {};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (G > 1 && i == 1) tokens_of(1);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w0[4], w1[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              w0[f] = odd ? (&r[2 * h][i ^ 1].x)[f] : (&r[2 * h][i].x)[f];
-              w1[f] = odd ? (&r[2 * h + 1][i ^ 1].x)[f] : (&r[2 * h + 1][i].x)[f];
-            }
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              uint32_t a0, a1, a2, a3;
-              e4m3_to_f16(w0[f], a0, a2);
-              e4m3_to_f16(w1[f], a1, a3);
-#pragma unroll
-              for (int j = 0; j < G; ++j)
-                mma_f16(sum[h][j], a0, a1, a2, a3, f == 0 ? lo[i][j].x : f == 1 ? lo[i][j].z : f == 2 ? hi[i][j].x : hi[i][j].z,
-                        f == 0 ? lo[i][j].y : f == 1 ? lo[i][j].w : f == 2 ? hi[i][j].y : hi[i][j].w);
-            }
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float f0 = ue8m0_value(sc[2 * h]), f1 = ue8m0_value(sc[2 * h + 1]);
-#pragma unroll
-          for (int j = 0; j < G; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[h][j][i] = fmaf(sum[h][j][i] * token[j][i & 1], i < 2 ? f0 : f1, acc[h][j][i]);
-        }
-      } else {
-        uint4 b[2][G];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < G; ++j) b[i][j] = ld_shared_v4_at(va + j * 8 * kTokenPitch + i * kStep * 2);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool in = k0 + i * kStep + t * 8 < left;   // what lies behind a token's row is not multiplied (weights are zeros there)
-#pragma unroll
-          for (int j = 0; j < G; ++j)
-            if (!in) b[i][j] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 r0 = odd ? r[2 * h][i ^ 1] : r[2 * h][i], r1 = odd ? r[2 * h + 1][i ^ 1] : r[2 * h + 1][i];
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-              mma_bf16(acc[h][j], r0.x, r1.x, r0.y, r1.y, b[i][j].x, b[i][j].y);
-              mma_bf16(acc[h][j], r0.z, r1.z, r0.w, r1.w, b[i][j].z, b[i][j].w);
-            }
+            for (int j = 0; j < 8; ++j) y[8 * i + j] = fmaf(fmaf(v[2 * j + 1], 0.0625f, v[2 * j]) * token[8 * i + j], f[b], y[8 * i + j]);
           }
         }
       }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.sums_empty[sums.s]);
+      sums.advance();
+      ++stage;
     }
+  } else {
+    if (ok) ok = wait_few(&sh.sums_full[sums.s], sums.phase, 4 * kWaitNs);
+    tmem_fence_after();
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      float v[16];
+      tmem_ld16(tmem + sums.s * (16 * G) + i * 16, v);
+      tmem_wait_ld(v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[16 * i + j] = v[j];
+    }
+    tmem_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.empty[position.s]);
-    position.advance();
-    if (kFp8) {   // the next stage's scales
-      const int next = (c + 1) * kParts + warp;
-      if (next * kFp8Block < p.K) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sc[q] = __ldg(scale[q] + next);
-      }
-    }
+    if (lane == 0) mbar_arrive(&sh.sums_empty[sums.s]);
+    sums.advance();
   }
-  if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.red_empty[unit & 1], ((unit >> 1) & 1) ^ 1));
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < G; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[(j * 8 + 2 * t + (i & 1)) * kRedPitch + h * 16 + (i >> 1) * 8 + g] = acc[h][j][i];
-  __syncwarp();
-  if (lane == 0) mbar_arrive(&sh.red_full[unit & 1]);
 }
 
 template <bool kFp8, bool kIn, int kAct>
-__global__ void __launch_bounds__(few_threads(kFp8), 1) k_few(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ FewParams p) {
   constexpr int kOne = kFp8 ? 1 : 2;                 // bytes of a weight
-  constexpr int kChunk = kPiece / kOne;              // inner elements of a stage
-  constexpr int kPass = pass_of(kFp8), kTokenWarps = token_warps_of(kFp8), kTokenBytes = token_bytes(kFp8), kTokenPitch = token_pitch(kFp8);
+  constexpr int kBlock = 128 / kOne, kChunk = kBlocks * kBlock;   // inner elements of a block, of a stage
+  constexpr int kPass = pass_of(kFp8), kColumns = kFp8 ? 2 : 1;   // of the products for a token
+  constexpr int kRawBytes = kChunk * 2;              // a token's row in a stage, as it comes
   extern __shared__ __align__(1024) uint8_t raw[];
   FewShared& sh = *reinterpret_cast<FewShared*>(raw);
+  uint8_t* const ring = raw + (sizeof(FewShared) + 1023) / 1024 * 1024;
+  uint8_t* const lists_at = raw + kFewSmem - FewLists::bytes(p.E, p.T, p.k);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxFewStages; ++s) {
-      mbar_init(&sh.full[s], kFp8 ? 1 + kTokenWarps : 1);
-      mbar_init(&sh.empty[s], kParts);
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.turned[s], kTurners);
+      mbar_init(&sh.empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&sh.red_full[b], kParts);
-      mbar_init(&sh.red_empty[b], kAdders);
+    for (int b = 0; b < kSums; ++b) {
+      mbar_init(&sh.sums_full[b], 1);
+      mbar_init(&sh.sums_empty[b], kEpilogues);
     }
     fence_barrier_init();
   }
+  if (warp == 2) tmem_alloc<1>(&sh.tmem, 512);
   if (kIn) {
     pdl_wait();   // ids and tokens may come from the kernel before
     pdl_launch_dependents();
   }
-  uint8_t* const red_base = raw + (sizeof(FewShared) + 127) / 128 * 128;
-  few_lists<few_threads(kFp8)>(p, sh.lists, reinterpret_cast<uint32_t*>(red_base), kIn && blockIdx.x == 0);
-  const FewLists& l = sh.lists;
-  const int tokens_most = min(l.most, kPass);
-  const int red_part = (tokens_most + 7) / 8 * 8 * kRedPitch;         // floats of one part's sums
-  const int red_bytes = kParts * red_part * 4;                        // of one unit; the next one's go to a second part
-  const int stage_bytes = kUnitRows * kPiece + (tokens_most * kTokenPitch + 127) / 128 * 128;
-  uint8_t* const ring = red_base + 2 * red_bytes;
-  // products read 8 tokens' rows, there or not: seven may lie behind the last stage
-  const int stages = min(kMaxFewStages, (int)((kFewSmem - (int)(ring - raw) - 7 * kTokenPitch) / stage_bytes));
+  const FewLists l(lists_at, p.E, p.T, p.k);
+  tmem_fence_before();
+  few_lists(p, sh, l, reinterpret_cast<uint32_t*>(ring), kIn && blockIdx.x == 0);
+  tmem_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int tokens_most = min(sh.most, kPass);
+  const bool two = tokens_most * kColumns > 16;      // 32 columns of products instead of 16
+  const int columns = two ? 32 : 16;
+  // a stage: weights, tokens for the products, tokens as they came
+  const int token_block = columns * 128, stage_bytes = (kWeightBytes + kBlocks * token_block + tokens_most * kRawBytes + 1023) / 1024 * 1024;
+  const int room = (int)(lists_at - ring), stages = min(min(kMaxFewStages, room / stage_bytes), ((int)(raw + kFewSmem - ring) - kProductBytes) / stage_bytes + 1);
   const int chunks = (p.K + kChunk - 1) / kChunk;
-  FewWalk<kIn, kPass> w(l, p.N);
+  FewWalk<kIn, kPass> w(l.used, sh.n_used, p.N);
+  RingPosition at(stages);
   bool ok = true;
-  RingPosition position = {0, 0, stages, stage_bytes};
 
-  if (warp < kParts) {
-    // ---------------------------------------------------------------- products
-    uint32_t unit = 0;
-    while (w.next()) {
-      float* const red = reinterpret_cast<float*>(red_base + (unit & 1) * red_bytes) + warp * red_part;
-      if (w.m <= 8)
-        few_products<kFp8, kIn, 1>(p, sh, w.e, w.col, ring, red, chunks, unit, position, ok);
-      else if (w.m <= 16)
-        few_products<kFp8, kIn, 2>(p, sh, w.e, w.col, ring, red, chunks, unit, position, ok);
-      else
-        few_products<kFp8, kIn, kPass / 8>(p, sh, w.e, w.col, ring, red, chunks, unit, position, ok);
-      ++unit;
-    }
-  } else if (warp < kParts + kAdders) {
-    // ---------------------------------------------------------------- sums
-    const int q = warp - kParts;
-    uint32_t unit = 0;
+  if (warp < kEpilogues) {
+    // ---------------------------------------------------------------- sums: a row a thread
+    RingPosition sums(kSums);
+    uint32_t stage = 0, unit = 0;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
     if (!kIn)
-      for (int n = q; n < p.T; n += kAdders) sh.sums[n * kUnitRows + lane] = 0.0f;
+      for (int n = 0; n < p.T; ++n) l.sums[n * kUnitRows + threadIdx.x] = 0.0f;
     while (w.next()) {
-      const int b = unit & 1;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.red_full[b], (unit >> 1) & 1, 2 * kWaitNs));
-      const float* const red = reinterpret_cast<const float*>(red_base + b * red_bytes);
-      auto total = [&](int n, int row) {
-        float v[kParts];
+      const uint8_t* scale = nullptr;
+      if (kFp8) {
+        const int n = min(w.col + (kIn ? lane : (int)threadIdx.x), p.N - 1);
+        scale = p.scales + ((int64_t)(kIn ? w.e * 2 + warp : w.e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
+      }
+      float y[pass_of(false)];
+      if (two)
+        few_sums<kFp8, 2>(sh, lanes, chunks, p.K, scale, sums, stage, y, ok);
+      else
+        few_sums<kFp8, 1>(sh, lanes, chunks, p.K, scale, sums, stage, y, ok);
+      if (kIn) {   // gate in one warp, up in the other
+        float(&up)[pass_of(false)][kUnitRows / 2] = sh.up[unit & 1];
+        if (warp == 1) {
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) v[i] = red[i * red_part + n * kRedPitch + row];
-        return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-      };
-      if (kIn) {
-        const int c = lane & 15, row = (c >> 3) * 16 + (c & 7);
-        for (int n = q * 2 + (lane >> 4); n < w.m; n += 2 * kAdders)
-          if (c < w.cols)   // rounded to bf16: the second kernel's operand
-            p.out[(int64_t)l.slot[w.s0 + n] * p.N + w.col + c] = __float2bfloat16_rn(act_value<kAct>(total(n, row)) * total(n, row + 8));
+          for (int j = 0; j < kPass; ++j)
+            if (j < w.m) up[j][lane] = y[j];
+        }
+        named_barrier_sync(1, kEpilogues * kWarp);
+        if (warp == 0 && lane < w.cols) {
+#pragma unroll
+          for (int j = 0; j < kPass; ++j)   // rounded to bf16: the second kernel's operand
+            if (j < w.m) p.out[(int64_t)l.slot[w.s0 + j] * p.N + w.col + lane] = __float2bfloat16_rn(act_value<kAct>(y[j]) * up[j][lane]);
+        }
       } else {
-        // a token is one warp's, so its slots are added in the lists' order
-        for (int n = 0; n < w.m; ++n) {
-          const int token = l.token[w.s0 + n];
-          if (token % kAdders == q) {
-            float* const sum = sh.sums + token * kUnitRows + lane;
-            *sum = fmaf(l.weight[w.s0 + n], total(n, lane), *sum);
+#pragma unroll
+        for (int j = 0; j < kPass; ++j)
+          if (j < w.m) {
+            float* const sum = l.sums + l.token[w.s0 + j] * kUnitRows + threadIdx.x;
+            *sum = fmaf(l.weight[w.s0 + j], y[j], *sum);
+          }
+        if (w.last) {
+          for (int n = 0; n < p.T; ++n) {
+            if ((int)threadIdx.x < w.cols) p.out[(int64_t)n * p.N + w.col + threadIdx.x] = __float2bfloat16_rn(l.sums[n * kUnitRows + threadIdx.x]);
+            l.sums[n * kUnitRows + threadIdx.x] = 0.0f;
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.red_empty[b]);
       ++unit;
-      if (!kIn && w.last) {
-        for (int n = q; n < p.T; n += kAdders) {
-          if (lane < w.cols) p.out[(int64_t)n * p.N + w.col + lane] = __float2bfloat16_rn(sh.sums[n * kUnitRows + lane]);
-          sh.sums[n * kUnitRows + lane] = 0.0f;
-        }
-      }
     }
-    if (!kIn && l.n_used == 0) {
+    if (!kIn && sh.n_used == 0) {
       pdl_wait();   // out may be x
-      for (int64_t i = (int64_t)blockIdx.x * (kAdders * kWarp) + q * kWarp + lane; i < (int64_t)p.T * p.N; i += (int64_t)gridDim.x * (kAdders * kWarp))
+      for (int64_t i = (int64_t)blockIdx.x * (kEpilogues * kWarp) + threadIdx.x; i < (int64_t)p.T * p.N; i += (int64_t)gridDim.x * (kEpilogues * kWarp))
         p.out[i] = __float2bfloat16_rn(0.0f);
     }
-  } else if (warp == kParts + kAdders) {
-    // ---------------------------------------------------------------- weights
-    // a unit's rows in two copies (kIn) or one: by rows of 1 KB, a copy each, a warp got through 2.4 TB/s.  kOut: those of
-    // the first stages before h is there.
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- products
     const bool issue = elect_one();
+    const uint32_t idesc = umma_few_idesc(kFp8, columns);
+    RingPosition sums(kSums);
     while (ok && w.next()) {
       for (int c = 0; c < chunks; ++c) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[position.s], position.phase ^ 1));
+        if (kFp8 || c == 0) ok = wait_few(&sh.sums_empty[sums.s], sums.phase ^ 1, 4 * kWaitNs);
+        if (ok) ok = wait_few(&sh.full[at.s], at.phase);
+        if (ok) ok = wait_few(&sh.turned[at.s], at.phase);
+        if (!ok) break;
+        tmem_fence_after();
+        if (issue) {
+          const int blocks = min(kBlocks, (p.K - c * kChunk + kBlock - 1) / kBlock);
+          const uint32_t from = smem_addr(ring + at.s * stage_bytes);
+          const uint32_t a = umma_desc_lo(from, 16), b = umma_desc_lo(from + kWeightBytes, 16);
+          const uint32_t d = tmem + sums.s * (columns * (kFp8 ? kBlocks : 1));
+          for (int i = 0; i < blocks; ++i) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              umma_few(kFp8, kFp8 ? d + i * columns : d, a + (i * 64 + q * 2), b + ((i * token_block) >> 4) + q * 2, idesc, q > 0 || (!kFp8 && (i > 0 || c > 0)));
+          }
+          umma_commit(&sh.empty[at.s]);
+          if (kFp8 || c + 1 == chunks) umma_commit(&sh.sums_full[sums.s]);
+        }
+        __syncwarp();
+        at.advance();
+        if (kFp8 || c + 1 == chunks) sums.advance();
+      }
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- tokens, a row a lane
+    if (!kIn) pdl_wait();
+    while (ok && w.next()) {
+      const int from = lane < w.m ? (kIn ? l.token[w.s0 + lane] : l.slot[w.s0 + lane]) : -1;
+      const __nv_bfloat16* row = p.v + (int64_t)from * p.K;
+      for (int c = 0; c < chunks; ++c) {
+        ok = wait_few(&sh.empty[at.s], at.phase ^ 1);
+        if (!ok) break;
+        if (from >= 0)
+          tma_load_1d(ring + at.s * stage_bytes + kWeightBytes + kBlocks * token_block + lane * kRawBytes, row + c * kChunk,
+                      min(kChunk, p.K - c * kChunk) * 2, &sh.full[at.s]);
+        __syncwarp();
+        at.advance();
+      }
+    }
+  } else if (warp < 4 + kWeightWarps) {
+    // ---------------------------------------------------------------- weights: groups of 8 rows in turn
+    // kOut: those of the first stages before h is there
+    const int turn = warp - 4;
+    const bool issue = elect_one();
+    while (ok && w.next()) {
+      const int groups = (w.cols + 7) / 8;   // of W_down, or of gate and of up each
+      for (int c = 0; c < chunks; ++c) {
+        ok = wait_few(&sh.empty[at.s], at.phase ^ 1);
         if (!ok) break;
         if (issue) {
           const int k = min(kChunk, p.K - c * kChunk);
-          mbar_arrive_expect_tx(&sh.full[position.s], (kIn ? 2 : 1) * w.cols * kPiece + (kFp8 ? 0 : w.m * k * 2));
-          const uint32_t bar = smem_addr(&sh.full[position.s]);
-          constexpr int kWhole = kIn ? kUnitRows / 2 : kUnitRows;
+          const bool cut = k % kBlock != 0;   // K ends inside a block: block by block
+          const int blocks = cut ? (k + kBlock - 1) / kBlock : kBlocks;
+          if (turn == 0) mbar_arrive_expect_tx(&sh.full[at.s], (kIn ? 2 : 1) * groups * blocks * 1024 + w.m * k * 2);
+          const uint32_t to = smem_addr(ring + at.s * stage_bytes), bar = smem_addr(&sh.full[at.s]);
           for (int half = 0; half < (kIn ? 2 : 1); ++half) {
-            const uint32_t to = smem_addr(ring + position.offset()) + half * kWhole * kPiece;
             const int z = kIn ? 2 * w.e + half : w.e;
-            if (w.cols == kWhole) {
-              tma_load_3d<false>(to, &p.whole, bar, c * (kPiece / 4), w.col, z);
-            } else {
-              int n = 0;
-              for (; n + 4 <= w.cols; n += 4) tma_load_3d<false>(to + n * kPiece, &p.four, bar, c * (kPiece / 4), w.col + n, z);
-              for (; n < w.cols; ++n) tma_load_3d<false>(to + n * kPiece, &p.one, bar, c * (kPiece / 4), w.col + n, z);
+            for (int g = turn; g < groups; g += kWeightWarps) {
+              const uint32_t group = to + (half * (kUnitRows / 16) + g) * kGroupBytes;
+              if (!cut)
+                tma_load_4d(group, &p.whole, bar, 0, w.col + g * 8, c * kBlocks, z);
+              else
+                for (int i = 0; i < blocks; ++i) tma_load_3d<false>(group + i * 1024, &p.tail, bar, c * kChunk + i * kBlock, w.col + g * 8, z);
             }
           }
         }
         __syncwarp();
-        position.advance();
+        at.advance();
       }
     }
   } else {
-    // ---------------------------------------------------------------- tokens
-    const int turn = warp - (kParts + kAdders + 1);
-    if (!kIn) pdl_wait();
-    if constexpr (kFp8) {
-      // a token a warp at a time, the next one's loads before this one is turned into fp16
-      FewWalk<kIn, kPass> ahead = w;
-      int ahead_c = 0, ahead_i = turn;
-      bool go = ahead.next();
-      uint4 next[4];
-      auto load = [&]() {   // the first token from here on that is this warp's
-        while (go && ahead_i >= ahead.m) {
-          ahead_i = turn;
-          if (++ahead_c == chunks) {
-            ahead_c = 0;
-            go = ahead.next();
+    // ---------------------------------------------------------------- tokens to where the products read them
+    const int turn = warp - (4 + kWeightWarps);
+    uint32_t stage = 0;
+    while (w.next()) {
+      for (int c = 0; c < chunks; ++c) {
+        if (ok) ok = wait_few(&sh.full[at.s], at.phase);
+        const uint32_t to = smem_addr(ring + at.s * stage_bytes + kWeightBytes), from = to + kBlocks * token_block;
+        const int left = p.K - c * kChunk;
+        if constexpr (kFp8) {
+          for (int i = turn; i < 2 * w.m; i += kTurners) {   // two blocks of a token
+            const int j = i >> 1, b = (i & 1) * 2 + (lane >> 4), piece = lane & 15;
+            const bool in = b * kBlock < left;
+            uint32_t hi[2], lo[2];
+            float scale;
+            split_e4m3(in ? ld_shared_v4_at(from + j * kRawBytes + (b * kBlock + piece * 8) * 2) : make_uint4(0, 0, 0, 0), hi, lo, scale);
+            if (in) {
+              const uint32_t row = to + b * token_block + 2 * j * 128, at_hi = row + ((((piece >> 1) ^ (2 * j & 7)) << 4) | ((piece & 1) << 3));
+              const uint32_t at_lo = row + 128 + ((((piece >> 1) ^ ((2 * j + 1) & 7)) << 4) | ((piece & 1) << 3));
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_hi), "r"(hi[0]), "r"(hi[1]) : "memory");
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_lo), "r"(lo[0]), "r"(lo[1]) : "memory");
+              if (piece == 0) sh.scales[stage % kScaleRing][b][j] = scale;
+            }
+          }
+        } else {
+          for (int j = turn; j < w.m; j += kTurners) {   // zeros behind the row's end, as the weights have them
+            const uint4 v = lane * 8 < left ? ld_shared_v4_at(from + j * kRawBytes + lane * 16) : make_uint4(0, 0, 0, 0);
+            st_shared_v4_at(to + (lane >> 3) * token_block + j * 128 + (((lane & 7) ^ (j & 7)) << 4), v);
           }
         }
-        if (!go || ahead_c * kChunk + lane * 32 >= p.K) return;
-        const int from = kIn ? l.token[ahead.s0 + ahead_i] : l.slot[ahead.s0 + ahead_i];
-        const __nv_bfloat16* row = p.v + (int64_t)from * p.K + ahead_c * kChunk + lane * 32;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) next[q] = ld_v4(row + 8 * q);
-      };
-      load();
-      while (ok && w.next()) {
-        for (int c = 0; c < chunks; ++c) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[position.s], position.phase ^ 1));
-          if (!ok) break;
-          uint8_t* const tokens = ring + position.offset() + kUnitRows * kPiece;
-          for (int i = turn; i < w.m; i += kTokenWarps) {
-            const bool in = c * kChunk + lane * 32 < p.K;
-            uint4 v[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = in ? next[q] : make_uint4(0, 0, 0, 0);
-            ahead_i += kTokenWarps;
-            load();
-            uint8_t* const to = tokens + i * kTokenPitch;
-            scaled_f16(v, to + lane * 64, reinterpret_cast<float*>(to + kTokenBytes) + (lane >> 2), (lane & 3) == 0);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.full[position.s]);
-          position.advance();
-        }
-      }
-    } else {
-      while (ok && w.next()) {   // a row a lane
-        const int mine = lane * kTokenWarps + turn;
-        const int from = mine < w.m ? (kIn ? l.token[w.s0 + mine] : l.slot[w.s0 + mine]) : -1;
-        const __nv_bfloat16* row = p.v + (int64_t)from * p.K;
-        for (int c = 0; c < chunks; ++c) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[position.s], position.phase ^ 1));
-          if (!ok) break;
-          if (from >= 0)
-            tma_load_1d(ring + position.offset() + kUnitRows * kPiece + mine * kTokenPitch, row + c * kChunk, min(kChunk, p.K - c * kChunk) * 2, &sh.full[position.s]);
-          __syncwarp();
-          position.advance();
-        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.turned[at.s]);
+        at.advance();
+        ++stage;
       }
     }
   }
@@ -600,6 +574,10 @@ __global__ void __launch_bounds__(few_threads(kFp8), 1) k_few(const __grid_const
     while (globaltimer_ns() - t0 < 2000000ull) {
     }
   }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == 2) tmem_free<1>(tmem, 512);
 }
 
 template <bool kFp8, bool kIn, int kAct>
@@ -608,8 +586,8 @@ static int launch_few_half(const FewParams& p, cudaStream_t s) {
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(fn), kFewSmem) != EP_OK) return EP_ERR_CUDA;
   const int grid = ep_host::grid_cap(1);
   if (!kIn && ep_host::sm_budget_set()) {   // the second kernel's CTAs do not come up beside the first's
-    fn<<<grid, few_threads(kFp8), kFewSmem, s>>>(p);
-  } else if (ep_host::launch_dependent<FewParams>(fn, grid, few_threads(kFp8), kFewSmem, s, p) != EP_OK) {
+    fn<<<grid, kFewThreads, kFewSmem, s>>>(p);
+  } else if (ep_host::launch_dependent<FewParams>(fn, grid, kFewThreads, kFewSmem, s, p) != EP_OK) {
     return EP_ERR_CUDA;
   }
   ep_host::count_launch();
@@ -672,14 +650,18 @@ extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* t
   q.out = static_cast<__nv_bfloat16*>(out);
   q.K = I;
   q.N = H;
-  const int one = fp8 ? 1 : 2;
-  auto maps = [&](FewParams& f, const void* w, int count, int whole) {
-    const uint64_t words = (uint64_t)f.K * one / 4;
-    int rc = ep_host::make_row_map(&f.whole, w, words, f.N, count, whole);
-    if (rc == EP_OK) rc = ep_host::make_row_map(&f.four, w, words, f.N, count, 4);
-    return rc == EP_OK ? ep_host::make_row_map(&f.one, w, words, f.N, count, 1) : rc;
+  auto maps = [&](FewParams& f, const void* w, uint64_t count) {
+    const uint64_t one = fp8 ? 1 : 2, block = 128 / one, row = f.K * one, N = f.N, K = f.K;
+    const uint64_t dims[4] = {block, N, std::max<uint64_t>(1, K / block), count}, strides[3] = {row, 128, N * row};
+    const uint32_t box[4] = {(uint32_t)block, 8, kBlocks, 1};
+    // (rows shorter than a block have none that is whole: that map is not used)
+    int rc = K >= block ? ep_host::make_map(&f.whole, fp8, 4, w, dims, strides, box) : EP_OK;
+    const uint64_t dims3[3] = {K, N, count}, strides3[2] = {row, N * row};
+    const uint32_t box3[3] = {(uint32_t)block, 8, 1};
+    if (rc == EP_OK) rc = ep_host::make_map(&f.tail, fp8, 3, w, dims3, strides3, box3);
+    return rc;
   };
-  if (maps(p, w_gu, 2 * E, kUnitRows / 2) != EP_OK || maps(q, w_down, E, kUnitRows) != EP_OK) return EP_ERR_CUDA;
+  if (maps(p, w_gu, 2 * E) != EP_OK || maps(q, w_down, E) != EP_OK) return EP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return fp8 ? launch_few<true>(p, q, act, s) : launch_few<false>(p, q, act, s);
 }
