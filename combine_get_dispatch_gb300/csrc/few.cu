@@ -8,16 +8,16 @@
 // that every CTA sums its own columns over all experts in a fixed order and
 // nothing is added up between CTAs.  A CTA walks its columns in units: 32 columns'
 // rows of gate and up, or 64 rows of W_down, whole in the inner index, for the
-// tokens of one expert.  The weights' rows are the first operand of tcgen05.mma (of
-// 128 rows, those past the unit's being whatever lies there), the tokens
-// the second: 16 or 32 of them for 4 KB of weights read from shared memory, so the
-// products cost a fifth of the time in which the weights arrive, and no thread
+// tokens of one expert.  The weights' rows are the first operand of tcgen05.mma (64
+// of them, those past the unit's being whatever lies there), the tokens
+// the second, 16 or 32 of them, so that a product costs what reading its 2 KB of
+// weights from shared memory does, a fifth of the time in which they arrive, and no thread
 // touches a weight.  (By mma.sync E4M3 weights had to be turned into fp16 first, which bounded the
 // kernels at 3.5 to 4.5 TB/s.)  Warps:
-//   2 bring the sums out of tensor memory and finish a unit
+//   4 bring the sums out of tensor memory and finish a unit
 //   1 issues the products
 //   2 copy weights (TMA, 8 rows x 512 bytes a copy), 1 tokens' rows
-//   6 put the tokens where the products read them
+//   6 put the tokens where the products read them, in three teams, a stage each
 // The second kernel comes up as the first one's CTAs leave and fills its ring with
 // weights before it waits for h.
 
@@ -26,13 +26,13 @@
 
 namespace ep {
 
-constexpr int kEpilogues = 2, kWeightWarps = 2, kTurners = 6;
+constexpr int kEpilogues = 4, kWeightWarps = 2;
+constexpr int kTeams = 3, kTeam = 2, kTurners = kTeams * kTeam;   // a stage is one team's: its latency is 500 clocks and more
 constexpr int kFewThreads = (kEpilogues + 2 + kWeightWarps + kTurners) * kWarp;
 constexpr int kUnitRows = 64;         // of weights
 constexpr int kBlocks = 4;            // 128-byte blocks of a row in a stage
 constexpr int kGroupBytes = kBlocks * 1024;   // 8 rows of a stage
 constexpr int kWeightBytes = kUnitRows / 8 * kGroupBytes;
-constexpr int kProductBytes = 2 * kWeightBytes;   // what a product of 128 rows reads, from a stage's start on
 constexpr int kSums = 4;              // sums on their way out of tensor memory
 constexpr int kScaleRing = 16;        // stages whose tokens' scales are kept: more than are between the copies and the epilogue
 constexpr int kMaxFewStages = 6;
@@ -168,9 +168,10 @@ struct FewWalk {
     used = list;
     n_used = count;
     N = n;
-    const int64_t all = kIn ? (int64_t)n_used * n : n_used > 0 ? n : 0;
-    const int at = (int)(all * blockIdx.x / gridDim.x);
-    left = (int)(all * (blockIdx.x + 1) / gridDim.x) - at;
+    const uint32_t all = kIn ? (uint32_t)n_used * n : n_used > 0 ? n : 0;   // below 2^31
+    const uint32_t each = all / gridDim.x, more = all - each * gridDim.x;
+    const int at = (int)(blockIdx.x * each + min(blockIdx.x, more));
+    left = (int)(each + (blockIdx.x < more ? 1 : 0));
     d = kIn ? at / n : n_used - 1;
     col = kIn ? at - d * n : at;
     cols = s0 = m = behind = 0;
@@ -228,9 +229,10 @@ __device__ __forceinline__ void umma_few(bool fp8, uint32_t d, uint32_t a_lo, ui
         "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "r"(kWeightsHi), "r"(kDescHi)
         : "memory");
 }
-// Instruction descriptor: 128 rows, n tokens; E4M3 or bf16 operands, fp32 sums.
+// Instruction descriptor: 64 rows, n tokens; E4M3 or bf16 operands, fp32 sums.  Rows
+// 16 w .. 16 w + 15 come out in the first 16 lanes of quarter w of the tensor memory.
 __device__ __forceinline__ uint32_t umma_few_idesc(bool fp8, int n) {
-  return (1u << 4) | (fp8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+  return (1u << 4) | (fp8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(n >> 3) << 17) | (4u << 24);
 }
 
 // A token's bf16 numbers as two E4M3 ones, for E4M3 weights: in a block of 128
@@ -278,6 +280,13 @@ __device__ __forceinline__ bool wait_few(uint64_t* bar, uint32_t parity, uint64_
   bool ok = false;
   for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
   return __all_sync(0xffffffffu, ok || mbar_wait_bounded(bar, parity, limit_ns));
+}
+
+// The same for a thread by itself.
+__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitNs) {
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity, limit_ns);
 }
 
 // Where a role is in a ring.
@@ -371,7 +380,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxFewStages; ++s) {
       mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.turned[s], kTurners);
+      mbar_init(&sh.turned[s], kTeam);
       mbar_init(&sh.empty[s], 1);
     }
     for (int b = 0; b < kSums; ++b) {
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     }
     fence_barrier_init();
   }
-  if (warp == 2) tmem_alloc<1>(&sh.tmem, 512);
+  if (warp == kEpilogues) tmem_alloc<1>(&sh.tmem, 512);
   if (kIn) {
     pdl_wait();   // ids and tokens may come from the kernel before
     pdl_launch_dependents();
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
   const int columns = two ? 32 : 16;
   // a stage: weights, tokens for the products, tokens as they came
   const int token_block = columns * 128, stage_bytes = (kWeightBytes + kBlocks * token_block + tokens_most * kRawBytes + 1023) / 1024 * 1024;
-  const int room = (int)(lists_at - ring), stages = min(min(kMaxFewStages, room / stage_bytes), ((int)(raw + kFewSmem - ring) - kProductBytes) / stage_bytes + 1);
+  const int room = (int)(lists_at - ring), stages = min(kMaxFewStages, room / stage_bytes);
   const int chunks = (p.K + kChunk - 1) / kChunk;
   FewWalk<kIn, kPass> w(l.used, sh.n_used, p.N);
   RingPosition at(stages);
@@ -406,43 +415,49 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     RingPosition sums(kSums);
     uint32_t stage = 0, unit = 0;
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    if (!kIn)
-      for (int n = 0; n < p.T; ++n) l.sums[n * kUnitRows + threadIdx.x] = 0.0f;
+    const int row = warp * 16 + (lane & 15), column = kIn ? row % (kUnitRows / 2) : row;   // kIn: gate in two warps, up in the others
+    const bool there = lane < 16;
+    if (!kIn && there)
+      for (int n = 0; n < p.T; ++n) l.sums[n * kUnitRows + row] = 0.0f;
     while (w.next()) {
       const uint8_t* scale = nullptr;
       if (kFp8) {
-        const int n = min(w.col + (kIn ? lane : (int)threadIdx.x), p.N - 1);
-        scale = p.scales + ((int64_t)(kIn ? w.e * 2 + warp : w.e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
+        const int n = min(w.col + column, p.N - 1);
+        scale = p.scales + ((int64_t)(kIn ? w.e * 2 + (warp >> 1) : w.e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
       }
       float y[pass_of(false)];
       if (two)
         few_sums<kFp8, 2>(sh, lanes, chunks, p.K, scale, sums, stage, y, ok);
       else
         few_sums<kFp8, 1>(sh, lanes, chunks, p.K, scale, sums, stage, y, ok);
-      if (kIn) {   // gate in one warp, up in the other
+      if (kIn) {
         float(&up)[pass_of(false)][kUnitRows / 2] = sh.up[unit & 1];
-        if (warp == 1) {
+        if (warp >= kEpilogues / 2 && there) {
 #pragma unroll
-          for (int j = 0; j < kPass; ++j)
-            if (j < w.m) up[j][lane] = y[j];
+          for (int j = 0; j < kPass; ++j) {
+            if (j >= w.m) break;
+            up[j][column] = y[j];
+          }
         }
         named_barrier_sync(1, kEpilogues * kWarp);
-        if (warp == 0 && lane < w.cols) {
+        if (warp < kEpilogues / 2 && there && column < w.cols) {
 #pragma unroll
-          for (int j = 0; j < kPass; ++j)   // rounded to bf16: the second kernel's operand
-            if (j < w.m) p.out[(int64_t)l.slot[w.s0 + j] * p.N + w.col + lane] = __float2bfloat16_rn(act_value<kAct>(y[j]) * up[j][lane]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPass; ++j)
-          if (j < w.m) {
-            float* const sum = l.sums + l.token[w.s0 + j] * kUnitRows + threadIdx.x;
-            *sum = fmaf(l.weight[w.s0 + j], y[j], *sum);
+          for (int j = 0; j < kPass; ++j) {   // rounded to bf16: the second kernel's operand
+            if (j >= w.m) break;
+            p.out[(int64_t)l.slot[w.s0 + j] * p.N + w.col + column] = __float2bfloat16_rn(act_value<kAct>(y[j]) * up[j][column]);
           }
+        }
+      } else if (there) {
+#pragma unroll
+        for (int j = 0; j < kPass; ++j) {
+          if (j >= w.m) break;
+          float* const sum = l.sums + l.token[w.s0 + j] * kUnitRows + row;
+          *sum = fmaf(l.weight[w.s0 + j], y[j], *sum);
+        }
         if (w.last) {
           for (int n = 0; n < p.T; ++n) {
-            if ((int)threadIdx.x < w.cols) p.out[(int64_t)n * p.N + w.col + threadIdx.x] = __float2bfloat16_rn(l.sums[n * kUnitRows + threadIdx.x]);
-            l.sums[n * kUnitRows + threadIdx.x] = 0.0f;
+            if (row < w.cols) p.out[(int64_t)n * p.N + w.col + row] = __float2bfloat16_rn(l.sums[n * kUnitRows + row]);
+            l.sums[n * kUnitRows + row] = 0.0f;
           }
         }
       }
@@ -453,37 +468,40 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
       for (int64_t i = (int64_t)blockIdx.x * (kEpilogues * kWarp) + threadIdx.x; i < (int64_t)p.T * p.N; i += (int64_t)gridDim.x * (kEpilogues * kWarp))
         p.out[i] = __float2bfloat16_rn(0.0f);
     }
-  } else if (warp == 2) {
+  } else if (warp == kEpilogues) {
     // ---------------------------------------------------------------- products
-    const bool issue = elect_one();
-    const uint32_t idesc = umma_few_idesc(kFp8, columns);
-    RingPosition sums(kSums);
-    while (ok && w.next()) {
-      for (int c = 0; c < chunks; ++c) {
-        if (kFp8 || c == 0) ok = wait_few(&sh.sums_empty[sums.s], sums.phase ^ 1, 4 * kWaitNs);
-        if (ok) ok = wait_few(&sh.full[at.s], at.phase);
-        if (ok) ok = wait_few(&sh.turned[at.s], at.phase);
-        if (!ok) break;
-        tmem_fence_after();
-        if (issue) {
-          const int blocks = min(kBlocks, (p.K - c * kChunk + kBlock - 1) / kBlock);
-          const uint32_t from = smem_addr(ring + at.s * stage_bytes);
-          const uint32_t a = umma_desc_lo(from, 16), b = umma_desc_lo(from + kWeightBytes, 16);
+    // one thread by itself: votes and the warp's steps cost as much as the products they stand between
+    if (elect_one()) {
+      const uint32_t idesc = umma_few_idesc(kFp8, columns), weights0 = umma_desc_lo(smem_addr(ring), 16), tokens0 = umma_desc_lo(smem_addr(ring) + kWeightBytes, 16);
+      RingPosition sums(kSums);
+      while (ok && w.next()) {
+        for (int c = 0; c < chunks; ++c) {
+          if (kFp8 || c == 0) ok = wait_alone(&sh.sums_empty[sums.s], sums.phase ^ 1, 4 * kWaitNs);
+          ok = ok && wait_alone(&sh.turned[at.s], at.phase);   // by who has seen the weights' copies
+          if (!ok) break;
+          tmem_fence_after();
+          const int blocks = (p.K - c * kChunk + kBlock - 1) / kBlock;
+          const uint32_t a = weights0 + (uint32_t)at.s * (stage_bytes >> 4), b = tokens0 + (uint32_t)at.s * (stage_bytes >> 4);
           const uint32_t d = tmem + sums.s * (columns * (kFp8 ? kBlocks : 1));
-          for (int i = 0; i < blocks; ++i) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              umma_few(kFp8, kFp8 ? d + i * columns : d, a + (i * 64 + q * 2), b + ((i * token_block) >> 4) + q * 2, idesc, q > 0 || (!kFp8 && (i > 0 || c > 0)));
+          for (int i = 0; i < kBlocks; ++i) {
+            if (i < blocks) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                umma_few(kFp8, kFp8 ? d + i * columns : d, a + (i * 64 + q * 2), b + i * (token_block >> 4) + q * 2, idesc, q > 0 || (!kFp8 && (i > 0 || c > 0)));
+            }
           }
           umma_commit(&sh.empty[at.s]);
-          if (kFp8 || c + 1 == chunks) umma_commit(&sh.sums_full[sums.s]);
+          at.advance();
+          if (kFp8 || c + 1 == chunks) {
+            umma_commit(&sh.sums_full[sums.s]);
+            sums.advance();
+          }
         }
-        __syncwarp();
-        at.advance();
-        if (kFp8 || c + 1 == chunks) sums.advance();
       }
     }
-  } else if (warp == 3) {
+    ok = __all_sync(0xffffffffu, ok);
+  } else if (warp == kEpilogues + 1) {
     // ---------------------------------------------------------------- tokens, a row a lane
     if (!kIn) pdl_wait();
     while (ok && w.next()) {
@@ -499,10 +517,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         at.advance();
       }
     }
-  } else if (warp < 4 + kWeightWarps) {
+  } else if (warp < kEpilogues + 2 + kWeightWarps) {
     // ---------------------------------------------------------------- weights: groups of 8 rows in turn
     // kOut: those of the first stages before h is there
-    const int turn = warp - 4;
+    const int turn = warp - (kEpilogues + 2);
     const bool issue = elect_one();
     while (ok && w.next()) {
       const int groups = (w.cols + 7) / 8;   // of W_down, or of gate and of up each
@@ -532,15 +550,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     }
   } else {
     // ---------------------------------------------------------------- tokens to where the products read them
-    const int turn = warp - (4 + kWeightWarps);
+    const int turn = warp - (kEpilogues + 2 + kWeightWarps), team = turn / kTeam, member = turn % kTeam;
     uint32_t stage = 0;
     while (w.next()) {
-      for (int c = 0; c < chunks; ++c) {
+      for (int c = 0; c < chunks; ++c, ++stage, at.advance()) {
+        // every stage is waited for, another team's too: they may land out of order, and a wait two phases ahead passes
         if (ok) ok = wait_few(&sh.full[at.s], at.phase);
+        if (stage % kTeams != (uint32_t)team) continue;
         const uint32_t to = smem_addr(ring + at.s * stage_bytes + kWeightBytes), from = to + kBlocks * token_block;
         const int left = p.K - c * kChunk;
         if constexpr (kFp8) {
-          for (int i = turn; i < 2 * w.m; i += kTurners) {   // two blocks of a token
+          for (int i = member; i < 2 * w.m; i += kTeam) {   // two blocks of a token
             const int j = i >> 1, b = (i & 1) * 2 + (lane >> 4), piece = lane & 15;
             const bool in = b * kBlock < left;
             uint32_t hi[2], lo[2];
@@ -555,7 +575,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
             }
           }
         } else {
-          for (int j = turn; j < w.m; j += kTurners) {   // zeros behind the row's end, as the weights have them
+          for (int j = member; j < w.m; j += kTeam) {   // zeros behind the row's end, as the weights have them
             const uint4 v = lane * 8 < left ? ld_shared_v4_at(from + j * kRawBytes + lane * 16) : make_uint4(0, 0, 0, 0);
             st_shared_v4_at(to + (lane >> 3) * token_block + j * 128 + (((lane & 7) ^ (j & 7)) << 4), v);
           }
@@ -563,8 +583,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.turned[at.s]);
-        at.advance();
-        ++stage;
       }
     }
   }
@@ -577,7 +595,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == 2) tmem_free<1>(tmem, 512);
+  if (warp == kEpilogues) tmem_free<1>(tmem, 512);
 }
 
 template <bool kFp8, bool kIn, int kAct>
