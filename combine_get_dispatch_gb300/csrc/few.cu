@@ -16,7 +16,7 @@
 // kernels at 3.5 to 4.5 TB/s.)  Warps:
 //   4 bring the sums out of tensor memory and finish a unit
 //   1 issues the products
-//   2 copy weights (TMA, 8 rows x 512 bytes a copy), 1 tokens' rows
+//   2 copy weights (TMA, 8 rows x 512 bytes a copy), 3 tokens' rows
 //   6 put the tokens where the products read them, in three teams, a stage each
 // The second kernel comes up as the first one's CTAs leave and fills its ring with
 // weights before it waits for h.
@@ -26,9 +26,9 @@
 
 namespace ep {
 
-constexpr int kEpilogues = 4, kWeightWarps = 2;
+constexpr int kEpilogues = 4, kWeightWarps = 2, kRowWarps = 3;   // a warp issues a copy in some 80 clocks
 constexpr int kTeams = 3, kTeam = 2, kTurners = kTeams * kTeam;   // a stage is one team's: its latency is 500 clocks and more
-constexpr int kFewThreads = (kEpilogues + 2 + kWeightWarps + kTurners) * kWarp;
+constexpr int kFewThreads = (kEpilogues + 1 + kRowWarps + kWeightWarps + kTurners) * kWarp;
 constexpr int kUnitRows = 64;         // of weights
 constexpr int kBlocks = 4;            // 128-byte blocks of a row in a stage
 constexpr int kGroupBytes = kBlocks * 1024;   // 8 rows of a stage
@@ -87,6 +87,38 @@ struct FewLists {
 __device__ __forceinline__ void few_lists(const FewParams& p, FewShared& sh, const FewLists& l, uint32_t* masks, bool report) {
   const int n = p.T * p.k, words = (n + 31) / 32, groups = (p.E + 31) / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (n <= kWarp) {   // one warp by itself, a slot a lane: places by counting the slots before (2.3 us the other way)
+    if (warp == 0) {
+      const int64_t id = lane < n ? p.idx[lane] : -1;
+      const bool fits = id >= 0 && id < p.E;
+      if (report && !fits && id != -1) set_status(p.status, EP_ERR_INVALID_ARG);
+      const int e = fits ? (int)id : kMaxE;
+      const float weight = fits ? p.weights[lane] : 0.0f;
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      const bool leads = fits && (same & lanemask_lt()) == 0;
+      int at = __popc(same & lanemask_lt()), d = 0;
+      for (int i = 0; i < n; ++i) {
+        const int other = __shfl_sync(0xffffffffu, e, i);
+        const bool other_leads = __shfl_sync(0xffffffffu, leads, i);
+        at += other < e;
+        d += other < e && other_leads;
+      }
+      const int c = __popc(same);
+      if (fits) {
+        l.slot[at] = (int16_t)lane;
+        l.token[at] = (int16_t)(lane / p.k);
+        l.weight[at] = weight;
+        if (leads) l.used[d] = {(int16_t)e, (int16_t)at, (int16_t)c, 0};
+      }
+      const int used = __popc(__ballot_sync(0xffffffffu, leads)), most = __reduce_max_sync(0xffffffffu, fits ? c : 0);
+      if (lane == 0) {
+        sh.n_used = used;
+        sh.most = most;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   for (int i = threadIdx.x; i < p.E * words; i += kFewThreads) masks[i] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kFewThreads) {
@@ -501,26 +533,27 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
       }
     }
     ok = __all_sync(0xffffffffu, ok);
-  } else if (warp == kEpilogues + 1) {
+  } else if (warp < kEpilogues + 1 + kRowWarps) {
     // ---------------------------------------------------------------- tokens, a row a lane
+    const int mine = lane * kRowWarps + warp - (kEpilogues + 1);
     if (!kIn) pdl_wait();
     while (ok && w.next()) {
-      const int from = lane < w.m ? (kIn ? l.token[w.s0 + lane] : l.slot[w.s0 + lane]) : -1;
+      const int from = mine < w.m ? (kIn ? l.token[w.s0 + mine] : l.slot[w.s0 + mine]) : -1;
       const __nv_bfloat16* row = p.v + (int64_t)from * p.K;
       for (int c = 0; c < chunks; ++c) {
         ok = wait_few(&sh.empty[at.s], at.phase ^ 1);
         if (!ok) break;
         if (from >= 0)
-          tma_load_1d(ring + at.s * stage_bytes + kWeightBytes + kBlocks * token_block + lane * kRawBytes, row + c * kChunk,
+          tma_load_1d(ring + at.s * stage_bytes + kWeightBytes + kBlocks * token_block + mine * kRawBytes, row + c * kChunk,
                       min(kChunk, p.K - c * kChunk) * 2, &sh.full[at.s]);
         __syncwarp();
         at.advance();
       }
     }
-  } else if (warp < kEpilogues + 2 + kWeightWarps) {
+  } else if (warp < kEpilogues + 1 + kRowWarps + kWeightWarps) {
     // ---------------------------------------------------------------- weights: groups of 8 rows in turn
     // kOut: those of the first stages before h is there
-    const int turn = warp - (kEpilogues + 2);
+    const int turn = warp - (kEpilogues + 1 + kRowWarps);
     const bool issue = elect_one();
     while (ok && w.next()) {
       const int groups = (w.cols + 7) / 8;   // of W_down, or of gate and of up each
@@ -550,7 +583,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     }
   } else {
     // ---------------------------------------------------------------- tokens to where the products read them
-    const int turn = warp - (kEpilogues + 2 + kWeightWarps), team = turn / kTeam, member = turn % kTeam;
+    const int turn = warp - (kEpilogues + 1 + kRowWarps + kWeightWarps), team = turn / kTeam, member = turn % kTeam;
     uint32_t stage = 0;
     while (w.next()) {
       for (int c = 0; c < chunks; ++c, ++stage, at.advance()) {
