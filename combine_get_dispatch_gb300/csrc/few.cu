@@ -35,7 +35,7 @@ constexpr int kGroupBytes = kBlocks * 1024;   // 8 rows of a stage
 constexpr int kWeightBytes = kUnitRows / 8 * kGroupBytes;
 constexpr int kSums = 4;              // sums on their way out of tensor memory
 constexpr int kScaleRing = 16;        // stages whose tokens' scales are kept: more than are between the copies and the epilogue
-constexpr int kMaxFewStages = 6;
+constexpr int kMaxFewStages = 8;
 constexpr int kFewSmem = 226 * 1024;
 __host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 32; }   // tokens of an expert taken at a time
 
@@ -195,6 +195,7 @@ struct FewWalk {
   int N, left;           // kIn: (expert, column) pairs to come, from `col` of expert d on; kOut: columns from `col` on
   int d, e, col, cols, s0, m, behind;   // behind: the expert's tokens after these
   bool last;             // kOut: unit of these columns
+  int most;              // columns of the widest unit
 
   __device__ __forceinline__ FewWalk(const FewUsed* list, int count, int n) {
     used = list;
@@ -204,6 +205,7 @@ struct FewWalk {
     const uint32_t each = all / gridDim.x, more = all - each * gridDim.x;
     const int at = (int)(blockIdx.x * each + min(blockIdx.x, more));
     left = (int)(each + (blockIdx.x < more ? 1 : 0));
+    most = min(kIn ? kUnitRows / 2 : kUnitRows, left);
     d = kIn ? at / n : n_used - 1;
     col = kIn ? at - d * n : at;
     cols = s0 = m = behind = 0;
@@ -335,10 +337,10 @@ struct RingPosition {
   }
 };
 
-// The sums of a unit's rows for 8 G (E4M3) or 16 G tokens: y[j] of token j, a row a
+// The sums of a unit's rows for up to 8 G (E4M3) or 16 G tokens: y[j] of token j, a row a
 // thread; ok: no wait has run out.
 template <bool kFp8, int G>
-__device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int chunks, int K, const uint8_t* scale, RingPosition& sums, uint32_t& stage,
+__device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int columns, int chunks, int K, const uint8_t* scale, RingPosition& sums, uint32_t& stage,
                                          float (&y)[pass_of(false)], bool& ok) {
   constexpr int kTokens = (kFp8 ? 8 : 16) * G;
   const int lane = threadIdx.x & 31;
@@ -359,7 +361,7 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int chunk
       fetch(c + 1);
       if (ok) ok = wait_few(&sh.sums_full[sums.s], sums.phase, 4 * kWaitNs);
       tmem_fence_after();
-      const uint32_t at = tmem + sums.s * (kBlocks * 16 * G);
+      const uint32_t at = tmem + sums.s * kBlocks * columns;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
         if (c * kBlocks + b < blocks) {
@@ -367,7 +369,7 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int chunk
 #pragma unroll
           for (int i = 0; i < G; ++i) {
             float v[16];
-            tmem_ld16(at + b * 16 * G + i * 16, v);
+            tmem_ld16(at + b * columns + i * 16, v);
             tmem_wait_ld(v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[8 * i + j] = fmaf(fmaf(v[2 * j + 1], 0.0625f, v[2 * j]) * token[8 * i + j], f[b], y[8 * i + j]);
@@ -386,7 +388,7 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int chunk
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       float v[16];
-      tmem_ld16(tmem + sums.s * (16 * G) + i * 16, v);
+      tmem_ld16(tmem + sums.s * columns + i * 16, v);
       tmem_wait_ld(v);
 #pragma unroll
       for (int j = 0; j < 16; ++j) y[16 * i + j] = v[j];
@@ -432,13 +434,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
   tmem_fence_after();
   const uint32_t tmem = sh.tmem;
   const int tokens_most = min(sh.most, kPass);
-  const bool two = tokens_most * kColumns > 16;      // 32 columns of products instead of 16
-  const int columns = two ? 32 : 16;
-  // a stage: weights, tokens for the products, tokens as they came
-  const int token_block = columns * 128, stage_bytes = (kWeightBytes + kBlocks * token_block + tokens_most * kRawBytes + 1023) / 1024 * 1024;
-  const int room = (int)(lists_at - ring), stages = min(kMaxFewStages, room / stage_bytes);
+  const bool two = tokens_most * kColumns > 16;
+  const int columns = two ? 32 : tokens_most * kColumns > 8 ? 16 : 8;   // of products
   const int chunks = (p.K + kChunk - 1) / kChunk;
   FewWalk<kIn, kPass> w(l.used, sh.n_used, p.N);
+  // a stage: weights, tokens for the products, tokens as they came.  Products read 64
+  // rows; what W_down's units have no rows for is other stages' memory, or the lists'.
+  const int weight_bytes = kIn ? kWeightBytes : (w.most + 7) / 8 * kGroupBytes;
+  const int token_block = columns * 128, stage_bytes = (weight_bytes + kBlocks * token_block + tokens_most * kRawBytes + 1023) / 1024 * 1024;
+  const int stages = max(1, min(kMaxFewStages, min((int)(lists_at - ring) / stage_bytes, ((int)(raw + kFewSmem - ring) - kWeightBytes) / stage_bytes + 1)));
   RingPosition at(stages);
   bool ok = true;
 
@@ -459,9 +463,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
       }
       float y[pass_of(false)];
       if (two)
-        few_sums<kFp8, 2>(sh, lanes, chunks, p.K, scale, sums, stage, y, ok);
+        few_sums<kFp8, 2>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
       else
-        few_sums<kFp8, 1>(sh, lanes, chunks, p.K, scale, sums, stage, y, ok);
+        few_sums<kFp8, 1>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
       if (kIn) {
         float(&up)[pass_of(false)][kUnitRows / 2] = sh.up[unit & 1];
         if (warp >= kEpilogues / 2 && there) {
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     // ---------------------------------------------------------------- products
     // one thread by itself: votes and the warp's steps cost as much as the products they stand between
     if (elect_one()) {
-      const uint32_t idesc = umma_few_idesc(kFp8, columns), weights0 = umma_desc_lo(smem_addr(ring), 16), tokens0 = umma_desc_lo(smem_addr(ring) + kWeightBytes, 16);
+      const uint32_t idesc = umma_few_idesc(kFp8, columns), weights0 = umma_desc_lo(smem_addr(ring), 16), tokens0 = umma_desc_lo(smem_addr(ring) + weight_bytes, 16);
       RingPosition sums(kSums);
       while (ok && w.next()) {
         for (int c = 0; c < chunks; ++c) {
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         ok = wait_few(&sh.empty[at.s], at.phase ^ 1);
         if (!ok) break;
         if (from >= 0)
-          tma_load_1d(ring + at.s * stage_bytes + kWeightBytes + kBlocks * token_block + mine * kRawBytes, row + c * kChunk,
+          tma_load_1d(ring + at.s * stage_bytes + weight_bytes + kBlocks * token_block + mine * kRawBytes, row + c * kChunk,
                       min(kChunk, p.K - c * kChunk) * 2, &sh.full[at.s]);
         __syncwarp();
         at.advance();
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         // every stage is waited for, another team's too: they may land out of order, and a wait two phases ahead passes
         if (ok) ok = wait_few(&sh.full[at.s], at.phase);
         if (stage % kTeams != (uint32_t)team) continue;
-        const uint32_t to = smem_addr(ring + at.s * stage_bytes + kWeightBytes), from = to + kBlocks * token_block;
+        const uint32_t to = smem_addr(ring + at.s * stage_bytes + weight_bytes), from = to + kBlocks * token_block;
         const int left = p.K - c * kChunk;
         if constexpr (kFp8) {
           for (int i = member; i < 2 * w.m; i += kTeam) {   // two blocks of a token
