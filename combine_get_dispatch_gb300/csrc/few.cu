@@ -35,6 +35,7 @@ constexpr int kGroupBytes = kBlocks * 1024;   // 8 rows of a stage
 constexpr int kWeightBytes = kUnitRows / 8 * kGroupBytes;
 constexpr int kSums = 4;              // sums on their way out of tensor memory
 constexpr int kScaleRing = 16;        // stages whose tokens' scales are kept: more than are between the copies and the epilogue
+constexpr int kCrossing = 16;         // columns: what a narrow unit at an expert's end costs by its products (evenly: 49 us instead of KX)
 constexpr int kMaxFewStages = 8;
 constexpr int kFewSmem = 226 * 1024;
 __host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 32; }   // tokens of an expert taken at a time
@@ -194,20 +195,20 @@ struct FewWalk {
   int n_used;
   int N, left;           // kIn: (expert, column) pairs to come, from `col` of expert d on; kOut: columns from `col` on
   int d, e, col, cols, s0, m, behind;   // behind: the expert's tokens after these
-  bool last;             // kOut: unit of these columns
+  bool last;             // kOut: last unit of these columns
   int most;              // columns of the widest unit
 
   __device__ __forceinline__ FewWalk(const FewUsed* list, int count, int n) {
     used = list;
     n_used = count;
     N = n;
-    const uint32_t all = kIn ? (uint32_t)n_used * n : n_used > 0 ? n : 0;   // below 2^31
+    const uint32_t all = kIn ? (uint32_t)n_used * (n + kCrossing) : n_used > 0 ? n : 0;   // below 2^32
     const uint32_t each = all / gridDim.x, more = all - each * gridDim.x;
-    const int at = (int)(blockIdx.x * each + min(blockIdx.x, more));
+    const uint32_t at = blockIdx.x * each + min(blockIdx.x, more);
     left = (int)(each + (blockIdx.x < more ? 1 : 0));
     most = min(kIn ? kUnitRows / 2 : kUnitRows, left);
-    d = kIn ? at / n : n_used - 1;
-    col = kIn ? at - d * n : at;
+    d = kIn ? (int)(at / (uint32_t)(n + kCrossing)) : n_used - 1;
+    col = (int)(kIn ? at - (uint32_t)d * (n + kCrossing) : at);
     cols = s0 = m = behind = 0;
   }
   __device__ __forceinline__ bool next() {
@@ -217,7 +218,8 @@ struct FewWalk {
       if (kIn) {
         left -= cols;
         col += cols;
-        if (col == N) {
+        if (col >= N) {
+          left -= N + kCrossing - col;
           col = 0;
           ++d;
         }
@@ -434,8 +436,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
   tmem_fence_after();
   const uint32_t tmem = sh.tmem;
   const int tokens_most = min(sh.most, kPass);
-  const bool two = tokens_most * kColumns > 16;
-  const int columns = two ? 32 : tokens_most * kColumns > 8 ? 16 : 8;   // of products
+  const int columns = (tokens_most * kColumns + 7) / 8 * 8;   // of products, most
   const int chunks = (p.K + kChunk - 1) / kChunk;
   FewWalk<kIn, kPass> w(l.used, sh.n_used, p.N);
   // a stage: weights, tokens for the products, tokens as they came.  Products read 64
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         scale = p.scales + ((int64_t)(kIn ? w.e * 2 + (warp >> 1) : w.e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
       }
       float y[pass_of(false)];
-      if (two)
+      if (w.m * kColumns > 16)
         few_sums<kFp8, 2>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
       else
         few_sums<kFp8, 1>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
@@ -508,9 +509,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     // ---------------------------------------------------------------- products
     // one thread by itself: votes and the warp's steps cost as much as the products they stand between
     if (elect_one()) {
-      const uint32_t idesc = umma_few_idesc(kFp8, columns), weights0 = umma_desc_lo(smem_addr(ring), 16), tokens0 = umma_desc_lo(smem_addr(ring) + weight_bytes, 16);
+      const uint32_t weights0 = umma_desc_lo(smem_addr(ring), 16), tokens0 = umma_desc_lo(smem_addr(ring) + weight_bytes, 16);
       RingPosition sums(kSums);
       while (ok && w.next()) {
+        const uint32_t idesc = umma_few_idesc(kFp8, (w.m * kColumns + 7) / 8 * 8);
         for (int c = 0; c < chunks; ++c) {
           if (kFp8 || c == 0) ok = wait_alone(&sh.sums_empty[sums.s], sums.phase ^ 1, 4 * kWaitNs);
           ok = ok && wait_alone(&sh.turned[at.s], at.phase);   // by who has seen the weights' copies
