@@ -36,6 +36,7 @@ constexpr int kWeightBytes = kUnitRows / 8 * kGroupBytes;
 constexpr int kSums = 4;              // sums on their way out of tensor memory
 constexpr int kScaleRing = 16;        // stages whose tokens' scales are kept: more than are between the copies and the epilogue
 constexpr int kCrossing = 16;         // columns: what a narrow unit at an expert's end costs by its products (evenly: 49 us instead of KX)
+constexpr int64_t kWaveWork = 1 << 23;
 constexpr int kMaxFewStages = 8;
 constexpr int kFewSmem = 226 * 1024;
 __host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 32; }   // tokens of an expert taken at a time
@@ -49,6 +50,7 @@ struct FewParams {
   __nv_bfloat16* out;          // kIn: h; kOut: out [T, H]
   int32_t* status;
   int T, k, E, K, N;           // K: inner extent; N: columns of h or out
+  uint32_t wave;               // CTAs that run at once
 };
 
 struct FewShared {
@@ -57,7 +59,7 @@ struct FewShared {
   int group_slots[kMaxE / kWarp], group_used[kMaxE / kWarp], group_most[kMaxE / kWarp];   // of 32 experts
   int n_used, most;                    // used experts; slots of the largest
   uint32_t tmem;
-  float scales[kScaleRing][kBlocks][pass_of(true)];   // E4M3: what a token's block was divided by
+  alignas(16) float scales[kScaleRing][kBlocks][pass_of(true)];   // E4M3: what a token's block was divided by
   float up[2][pass_of(false)][kUnitRows / 2];         // kIn: on its way to its gate
 };
 
@@ -198,14 +200,16 @@ struct FewWalk {
   bool last;             // kOut: last unit of these columns
   int most;              // columns of the widest unit
 
-  __device__ __forceinline__ FewWalk(const FewUsed* list, int count, int n) {
+  __device__ __forceinline__ FewWalk(const FewUsed* list, int count, int n, uint32_t wave) {
     used = list;
     n_used = count;
     N = n;
     const uint32_t all = kIn ? (uint32_t)n_used * (n + kCrossing) : n_used > 0 ? n : 0;   // below 2^32
-    const uint32_t each = all / gridDim.x, more = all - each * gridDim.x;
-    const uint32_t at = blockIdx.x * each + min(blockIdx.x, more);
-    left = (int)(each + (blockIdx.x < more ? 1 : 0));
+    // of kIn's CTAs that come after the first wave, each takes an eighth of a first one's columns
+    const uint32_t first = min(gridDim.x, wave), parts = 8 * first + (gridDim.x - first);
+    const uint32_t b = blockIdx.x < first ? 8 * blockIdx.x : 7 * first + blockIdx.x, size = blockIdx.x < first ? 8 : 1;
+    const uint32_t at = (uint32_t)((uint64_t)all * b / parts);
+    left = (int)((uint32_t)((uint64_t)all * (b + size) / parts) - at);
     most = min(kIn ? kUnitRows / 2 : kUnitRows, left);
     d = kIn ? (int)(at / (uint32_t)(n + kCrossing)) : n_used - 1;
     col = (int)(kIn ? at - (uint32_t)d * (n + kCrossing) : at);
@@ -339,14 +343,24 @@ struct RingPosition {
   }
 };
 
-// The sums of a unit's rows for up to 8 G (E4M3) or 16 G tokens: y[j] of token j, a row a
-// thread; ok: no wait has run out.
-template <bool kFp8, int G>
-__device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int columns, int chunks, int K, const uint8_t* scale, RingPosition& sums, uint32_t& stage,
-                                         float (&y)[pass_of(false)], bool& ok) {
-  constexpr int kTokens = (kFp8 ? 8 : 16) * G;
-  const int lane = threadIdx.x & 31;
-  if (kFp8) {
+// kColumns columns of kCount blocks' sums, all on their way before the first is waited for.
+template <int kColumns, int kCount>
+__device__ __forceinline__ void few_columns(uint32_t at, int columns, float (&v)[kCount][kColumns]) {
+#pragma unroll
+  for (int b = 0; b < kCount; ++b)
+#pragma unroll
+    for (int i = 0; i < kColumns; i += 8) tmem_ld8(at + b * columns + i, &v[b][i]);
+#pragma unroll
+  for (int b = 0; b < kCount; ++b) tmem_wait_ld(v[b]);
+}
+
+// The sums of a unit's rows for the tokens of kColumns columns: y[j] of token j, a
+// row a thread; ok: no wait has run out.
+template <bool kFp8, int kColumns>
+__device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int columns, int chunks, int K, const uint8_t* scale, RingPosition& sums,
+                                         uint32_t& stage, float (&y)[pass_of(false)], bool& ok) {
+  if constexpr (kFp8) {
+    constexpr int kTokens = kColumns / 2, kCount = kColumns == 32 ? 2 : kBlocks;
     const int blocks = K / kFp8Block;
     uint32_t next[kBlocks];
     auto fetch = [&](int c) {
@@ -365,39 +379,42 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int colum
       tmem_fence_after();
       const uint32_t at = tmem + sums.s * kBlocks * columns;
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        if (c * kBlocks + b < blocks) {
-          const float* const token = sh.scales[stage % kScaleRing][b];
+      for (int b0 = 0; b0 < kBlocks; b0 += kCount) {
+        float v[kCount][kColumns];
+        few_columns(at + b0 * columns, columns, v);
 #pragma unroll
-          for (int i = 0; i < G; ++i) {
-            float v[16];
-            tmem_ld16(at + b * columns + i * 16, v);
-            tmem_wait_ld(v);
+        for (int b = 0; b < kCount; ++b) {
+          if (c * kBlocks + b0 + b < blocks) {
+            const float4* const token = reinterpret_cast<const float4*>(sh.scales[stage % kScaleRing][b0 + b]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[8 * i + j] = fmaf(fmaf(v[2 * j + 1], 0.0625f, v[2 * j]) * token[8 * i + j], f[b], y[8 * i + j]);
+            for (int i = 0; i < kTokens / 4; ++i) {
+              const float4 t = token[i];
+              const float of[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int j = 4 * i + q;
+                y[j] = fmaf(fmaf(v[b][2 * j + 1], 0.0625f, v[b][2 * j]) * of[q], f[b0 + b], y[j]);
+              }
+            }
           }
         }
       }
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.sums_empty[sums.s]);
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.sums_empty[sums.s]);
       sums.advance();
       ++stage;
     }
   } else {
     if (ok) ok = wait_few(&sh.sums_full[sums.s], sums.phase, 4 * kWaitNs);
     tmem_fence_after();
+    float v[1][kColumns];
+    few_columns(tmem + sums.s * columns, columns, v);
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      float v[16];
-      tmem_ld16(tmem + sums.s * columns + i * 16, v);
-      tmem_wait_ld(v);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) y[16 * i + j] = v[j];
-    }
+    for (int j = 0; j < kColumns; ++j) y[j] = v[0][j];
     tmem_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.sums_empty[sums.s]);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.sums_empty[sums.s]);
     sums.advance();
   }
 }
@@ -438,7 +455,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
   const int tokens_most = min(sh.most, kPass);
   const int columns = (tokens_most * kColumns + 7) / 8 * 8;   // of products, most
   const int chunks = (p.K + kChunk - 1) / kChunk;
-  FewWalk<kIn, kPass> w(l.used, sh.n_used, p.N);
+  FewWalk<kIn, kPass> w(l.used, sh.n_used, p.N, p.wave);
   // a stage: weights, tokens for the products, tokens as they came.  Products read 64
   // rows; what W_down's units have no rows for is other stages' memory, or the lists'.
   const int weight_bytes = kIn ? kWeightBytes : (w.most + 7) / 8 * kGroupBytes;
@@ -464,9 +481,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
       }
       float y[pass_of(false)];
       if (w.m * kColumns > 16)
-        few_sums<kFp8, 2>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+        few_sums<kFp8, 32>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+      else if (w.m * kColumns > 8)
+        few_sums<kFp8, 16>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
       else
-        few_sums<kFp8, 1>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+        few_sums<kFp8, 8>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
       if (kIn) {
         float(&up)[pass_of(false)][kUnitRows / 2] = sh.up[unit & 1];
         if (warp >= kEpilogues / 2 && there) {
@@ -638,10 +657,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
 }
 
 template <bool kFp8, bool kIn, int kAct>
-static int launch_few_half(const FewParams& p, cudaStream_t s) {
+static int launch_few_half(const FewParams& in, cudaStream_t s) {
   auto* fn = k_few<kFp8, kIn, kAct>;
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(fn), kFewSmem) != EP_OK) return EP_ERR_CUDA;
-  const int grid = ep_host::grid_cap(1);
+  int grid = ep_host::grid_cap(1);
+  FewParams p = in;
+  p.wave = grid;
+  if (kIn && !ep_host::sm_budget_set() && (int64_t)p.T * p.k * p.N * p.K >= kWaveWork * grid) grid *= 1 + 2;
   if (!kIn && ep_host::sm_budget_set()) {   // the second kernel's CTAs do not come up beside the first's
     fn<<<grid, kFewThreads, kFewSmem, s>>>(p);
   } else if (ep_host::launch_dependent<FewParams>(fn, grid, kFewThreads, kFewSmem, s, p) != EP_OK) {
