@@ -103,7 +103,18 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
     float up, factor;
     source_scale(square, s.eps, up, factor);
     if (begin == 0 && threadIdx.x == 0) s.factor[z] = factor;
+    const int rows_on = kSourceThreads * 8 / s.cols, cols_on = kSourceThreads * 8 % s.cols;
+    int64_t row = (begin + threadIdx.x * 8) / s.cols;
+    int col = (int)(begin + threadIdx.x * 8 - row * s.cols);
+    row += z * s.rows;
     for (int64_t i = begin + threadIdx.x * 8; i < end; i += kSourceThreads * 8) {
+      const int64_t to = row * s.stride + col;
+      row += rows_on;
+      col += cols_on;
+      if (col >= s.cols) {
+        col -= s.cols;
+        ++row;
+      }
       float u[8];
       load8(s, base + i, u);
       if (s.m != nullptr) {
@@ -116,8 +127,8 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
       uint32_t h[4], l[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) split_f16(u[2 * k] * up, u[2 * k + 1] * up, h[k], l[k]);
-      st_v4(s.hi + base + i, make_uint4(h[0], h[1], h[2], h[3]));
-      if (s.lo != nullptr) st_v4(s.lo + base + i, make_uint4(l[0], l[1], l[2], l[3]));
+      st_v4(s.hi + to, make_uint4(h[0], h[1], h[2], h[3]));
+      if (s.lo != nullptr) st_v4(s.lo + to, make_uint4(l[0], l[1], l[2], l[3]));
     }
   }
 }
@@ -151,6 +162,7 @@ struct NewtonParams {
   uint32_t tiles_m, tiles_n;    // kSquare, kGram: tiles_m only
   uint32_t each, tiles;         // of a matrix, of all
   bool rows_fast;
+  bool backward;                // the last matrix first
   bool a_mn, b_mn;
   float scale, add;             // epilogue: scale * sums + (add + diagonal_scale * diagonal) * in
   float diagonal_scale;
@@ -177,8 +189,8 @@ struct NewtonTile {
 template <int kForm>
 __device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, uint32_t t) {
   NewtonTile out;
-  out.z = (int)(t / p.each);
-  const uint32_t u = t - (uint32_t)out.z * p.each;
+  const uint32_t z = t / p.each, u = t - z * p.each;
+  out.z = p.backward ? p.count - 1 - (int)z : (int)z;
   if (symmetric(kForm)) {
     const uint32_t f = kBlock / p.wide, b = f == 1 ? u : u >> 1;
     uint32_t r = (uint32_t)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
@@ -545,9 +557,10 @@ struct NewtonSpace {
   size_t bytes;
 };
 
-// Row stride of A and P: whole 128-byte lines, which a copied row of 64 elements then is one of (S = 1416 without: 870
-// clocks a stage instead of 610).
+// Row stride of A and P, and of X where it adds no more than an eighth: whole 128-byte lines, which a copied row of 64
+// elements then is one of (A and P, S = 1416, without: 870 clocks a stage instead of 610; X: PADX).
 static int64_t padded(int n) { return (int64_t)(n + 63) / 64 * 64; }
+static int64_t padded_x(int N) { return N >= 512 ? padded(N) : N; }
 
 static NewtonSpace newton_space(int count, int M, int N, void* base) {
   NewtonSpace s;
@@ -557,7 +570,7 @@ static NewtonSpace newton_space(int count, int M, int N, void* base) {
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  const size_t each = (size_t)M * N, S = std::min(M, N);
+  const size_t each = (size_t)M * padded_x(N), S = std::min(M, N);
   s.sums = reinterpret_cast<float*>(take((size_t)count * kMostParts * 4));
   s.factor = reinterpret_cast<float*>(take((size_t)count * 4));
   s.diagonal = reinterpret_cast<float*>(take((size_t)count * S * 4));
@@ -628,7 +641,7 @@ struct Newton {
     return p;
   }
   int square_map(CUtensorMap* m, const __half* base, int box_rows) const { return newton_map(m, base, S, S, count, padded(S), box_rows); }
-  int x_map(CUtensorMap* m, const void* base, int box_rows) const { return newton_map(m, base, N, M, count, N, box_rows); }
+  int x_map(CUtensorMap* m, const __half* base, int box_rows) const { return newton_map(m, base, N, M, count, padded_x(N), box_rows); }
 
   // A = X X^T (or b A where that is the whole polynomial) from x.
   int gram(const __half* x, __half* to, float b, const float* factor) const {
@@ -660,10 +673,11 @@ struct Newton {
     NewtonParams p = start(M, N, S, false);
     const bool tall = M > N;
     p.rows_fast = !tall;
+    p.backward = true;   // what the product before read last is still in L2, and what this one writes last for the next
     p.b_mn = !tall;
     p.in = space.x[from];
     p.in_lo = has_lo ? space.lo[from] : nullptr;
-    p.in_stride = N;
+    p.in_stride = (int)padded_x(N);
     p.factor = factor;
     p.scale = (last ? 1.0f / kHeld : 1.0f) / kHeld;
     p.diagonal_scale = last ? 1.0f / kHeld : 1.0f;
@@ -678,7 +692,7 @@ struct Newton {
       return rc != EP_OK ? rc : launch_newton<kApply>(p, stream);
     }
     if (out != nullptr) {
-      rc = x_map(&p.out, out, 0);
+      rc = newton_map(&p.out, out, N, M, count, N, 0);
       return rc != EP_OK ? rc : launch_newton<kApplyOut>(p, stream);
     }
     p.w = w;
@@ -716,6 +730,9 @@ static int newton(Source src, int count, int M, int N, int steps, const float* a
   src.count = count;
   src.sums = n.space.sums;
   src.factor = n.space.factor;
+  src.rows = M;
+  src.cols = N;
+  src.stride = (int)padded_x(N);
   src.hi = n.space.x[0];
   const bool exact = !src.f32 && src.m == nullptr;   // bf16 times a power of two is fp16, but for what is 2^-24 of the norm and smaller
   src.lo = exact ? nullptr : n.space.lo[0];

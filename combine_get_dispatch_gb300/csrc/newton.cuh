@@ -20,7 +20,8 @@ struct Source {
   float eps;
   float* sums;            // [count, parts]
   float* factor;          // [count]
-  __half *hi, *lo;        // [count, each]; lo may be nullptr
+  int rows, cols, stride; // of X: rows of `cols` elements, `stride` apart
+  __half *hi, *lo;        // lo may be nullptr
 };
 
 __device__ __forceinline__ void load8(const Source& s, int64_t i, float (&v)[8]) {
