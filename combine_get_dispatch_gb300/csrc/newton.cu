@@ -5,7 +5,7 @@
 // with A = X X^T (S x S, S the smaller side; X^T X and a product from the right
 // where M > N, so that nothing is transposed: an operand that lies the other way
 // is read MN-major).  A step is three launches over all matrices:
-//   kGram    A = X X^T                 symmetric: tiles on and below the diagonal,
+//   kGram    A = X X^T                 symmetric: tiles on and above the diagonal,
 //   kSquare  P = b A + c A^2           the others mirrored (none where c = 0)
 //   kApply   X' = a X + P X
 // all bound by the tensor cores.  Pairs of SMs compute 256 x 256 tiles as the
@@ -183,6 +183,7 @@ struct NewtonShared {
 
 struct NewtonTile {
   int z, i0, j0;
+  int wide;                     // columns of its products: fewer at the matrix's edge
   bool mirror;
 };
 
@@ -197,8 +198,8 @@ __device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, uint32_
     while ((r + 1) * (r + 2) / 2 <= b) ++r;   // each is below 2^25
     while (r * (r + 1) / 2 > b) --r;
     const uint32_t c = b - r * (r + 1) / 2;
-    out.i0 = (int)r * kBlock;
-    out.j0 = (int)(c * kBlock + (u - b * f) * p.wide);
+    out.i0 = (int)c * kBlock;
+    out.j0 = (int)(r * kBlock + (u - b * f) * p.wide);
     out.mirror = c < r;
   } else {
     const uint32_t fast = p.rows_fast ? p.tiles_m : p.tiles_n, slow = u / fast, rest = u - slow * fast;
@@ -206,6 +207,8 @@ __device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, uint32_
     out.j0 = (int)(p.rows_fast ? slow : rest) * p.wide;
     out.mirror = false;
   }
+  // (an MN-major operand comes 64 columns at a time)
+  out.wide = p.b_mn ? p.wide : min(p.wide, (p.cols - out.j0 + 31) / 32 * 32);
   return out;
 }
 
@@ -284,7 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     const uint32_t to0 = smem_addr(stages) + (first ? 0 : kNewtonOperand), full0 = map_to_rank(smem_addr(&sh.full[0]), 0);
     uint32_t s = 0, phase = 0;
     for (; ok && more; step()) {
-      const int m0 = first ? tile.i0 + (int)rank * 128 : tile.j0 + (int)rank * half;
+      const int m0 = first ? tile.i0 + (int)rank * 128 : tile.j0 + (int)rank * (tile.wide / 2);
       for (int kb = 0; kb < blocks; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[s], phase ^ 1));
         if (!ok) break;
@@ -314,9 +317,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     const uint32_t a0 = umma_desc_lo(smem_addr(stages), p.a_mn ? kNewtonOperand / 2 : 16);
     const uint32_t b0 = umma_desc_lo(smem_addr(stages) + kNewtonOperand, p.b_mn ? kNewtonOperand / 2 : 16);
     const uint32_t step_a = (p.a_mn ? 2048 : 32) >> 4, step_b = (p.b_mn ? 2048 : 32) >> 4;
-    const uint32_t idesc = umma_idesc_f16(kBlock, p.wide, p.a_mn, p.b_mn);
     uint32_t s = 0, phase = 0, n = 0;
     while (ok && more) {
+      const uint32_t idesc = umma_idesc_f16(kBlock, tile.wide, p.a_mn, p.b_mn);
       step();   // looked up while this tile's products run
       const uint32_t half = n & 1, d = tmem + half * kBlock;
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.sums_empty[half], ((n >> 1) & 1) ^ 1, 4 * kWaitNs));
