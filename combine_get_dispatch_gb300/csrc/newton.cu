@@ -34,6 +34,7 @@ namespace ep {
 // ---------------------------------------------------------------- momentum and norm
 
 constexpr int kSourceThreads = 256;
+constexpr int kAhead = 4;                 // loads on their way, of 8 elements a thread (two: 3.4 TB/s instead of KN)
 constexpr int kMostParts = 64;            // of a matrix's norm
 // m <- momentum m + g and the squares' sums of u, a part of a matrix a CTA, in an
 // order that only the sizes give.  Memory bounds it.
@@ -43,39 +44,40 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
   pdl_launch_dependents();
   for (int64_t item = blockIdx.x; item < (int64_t)s.count * s.parts; item += gridDim.x) {
     const int64_t z = item / s.parts, begin = (item - z * s.parts) * s.part, end = min(begin + s.part, s.each), base = z * s.each;
-    float sum[2] = {};
-    for (int64_t i0 = begin + threadIdx.x * 8; i0 < end; i0 += 2 * kSourceThreads * 8) {
-      float g[2][8] = {}, m[2][8];
+    float sum[kAhead] = {};
+    for (int64_t i0 = begin + threadIdx.x * 8; i0 < end; i0 += kAhead * kSourceThreads * 8) {
+      SourceWords g[kAhead] = {}, m[kAhead] = {};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kAhead; ++k) {
         const int64_t i = i0 + k * kSourceThreads * 8;
         if (i >= end) continue;
-        load8(s, base + i, g[k]);
-        if (s.m != nullptr) {
-          const float4* p = reinterpret_cast<const float4*>(s.m + base + i);
-          const float4 a = p[0], b = p[1];
-          m[k][0] = a.x, m[k][1] = a.y, m[k][2] = a.z, m[k][3] = a.w, m[k][4] = b.x, m[k][5] = b.y, m[k][6] = b.z, m[k][7] = b.w;
-        }
+        g[k] = load_words(s.g, s.f32, base + i);
+        if (s.m != nullptr) m[k] = load_words(s.m, true, base + i);
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kAhead; ++k) {
         const int64_t i = i0 + k * kSourceThreads * 8;
-        if (i >= end) continue;
+        float u[8];
+        words_to_floats(g[k], s.f32, u);
         if (s.m != nullptr) {
+          float v[8];
+          words_to_floats(m[k], true, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            m[k][e] = fmaf(s.momentum, m[k][e], g[k][e]);
-            g[k][e] = s.nesterov ? fmaf(s.momentum, m[k][e], g[k][e]) : m[k][e];
+            v[e] = fmaf(s.momentum, v[e], u[e]);
+            u[e] = s.nesterov ? fmaf(s.momentum, v[e], u[e]) : v[e];
           }
-          float4* p = reinterpret_cast<float4*>(s.m + base + i);
-          p[0] = make_float4(m[k][0], m[k][1], m[k][2], m[k][3]);
-          p[1] = make_float4(m[k][4], m[k][5], m[k][6], m[k][7]);
+          if (i < end) {
+            float4* p = reinterpret_cast<float4*>(s.m + base + i);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[k] = fmaf(g[k][e], g[k][e], sum[k]);
+        for (int e = 0; e < 8; ++e) sum[k] = fmaf(u[e], u[e], sum[k]);
       }
     }
-    float all = sum[0] + sum[1];
+    float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = all;
@@ -90,7 +92,8 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
 }
 
 // X = u 2^q, in hi and lo, and the factor that makes it 2^8 u / (|u| + eps).  The
-// parts in the other order, as the last ones of the kernel before are still in L2.
+// parts in the other order, as the last ones of the kernel before are still in L2.  m is read past the first-level
+// cache, which may hold what it was.
 __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
   pdl_launch_dependents();
   pdl_wait();
@@ -107,28 +110,40 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
     int64_t row = (begin + threadIdx.x * 8) / s.cols;
     int col = (int)(begin + threadIdx.x * 8 - row * s.cols);
     row += z * s.rows;
-    for (int64_t i = begin + threadIdx.x * 8; i < end; i += kSourceThreads * 8) {
-      const int64_t to = row * s.stride + col;
-      row += rows_on;
-      col += cols_on;
-      if (col >= s.cols) {
-        col -= s.cols;
-        ++row;
-      }
-      float u[8];
-      load8(s, base + i, u);
-      if (s.m != nullptr) {
-        const float4* p = reinterpret_cast<const float4*>(s.m + base + i);
-        const float4 a = __ldcg(p), b = __ldcg(p + 1);   // from L2: an SM may hold what m was
-        const float m[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const bool reads_g = s.m == nullptr || s.nesterov;
+    for (int64_t i0 = begin + threadIdx.x * 8; i0 < end; i0 += kAhead * kSourceThreads * 8) {
+      SourceWords g[kAhead] = {}, m[kAhead] = {};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = s.nesterov ? fmaf(s.momentum, m[e], u[e]) : m[e];
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t i = i0 + k * kSourceThreads * 8;
+        if (i >= end) continue;
+        if (reads_g) g[k] = load_words(s.g, s.f32, base + i);
+        if (s.m != nullptr) m[k] = load_words(s.m, true, base + i);
       }
-      uint32_t h[4], l[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) split_f16(u[2 * k] * up, u[2 * k + 1] * up, h[k], l[k]);
-      st_v4(s.hi + to, make_uint4(h[0], h[1], h[2], h[3]));
-      if (s.lo != nullptr) st_v4(s.lo + to, make_uint4(l[0], l[1], l[2], l[3]));
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t to = row * s.stride + col;
+        row += rows_on;
+        col += cols_on;
+        if (col >= s.cols) {
+          col -= s.cols;
+          ++row;
+        }
+        if (i0 + k * kSourceThreads * 8 >= end) continue;
+        float u[8];
+        words_to_floats(g[k], s.f32, u);
+        if (s.m != nullptr) {
+          float v[8];
+          words_to_floats(m[k], true, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = s.nesterov ? fmaf(s.momentum, v[e], u[e]) : v[e];
+        }
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_f16(u[2 * e] * up, u[2 * e + 1] * up, h[e], l[e]);
+        st_v4(s.hi + to, make_uint4(h[0], h[1], h[2], h[3]));
+        if (s.lo != nullptr) st_v4(s.lo + to, make_uint4(l[0], l[1], l[2], l[3]));
+      }
     }
   }
 }

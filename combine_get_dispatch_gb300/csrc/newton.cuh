@@ -24,19 +24,29 @@ struct Source {
   __half *hi, *lo;        // lo may be nullptr
 };
 
-__device__ __forceinline__ void load8(const Source& s, int64_t i, float (&v)[8]) {
-  if (s.f32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(s.g) + i);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// 8 elements as they lie in memory, read past the first-level cache.
+struct SourceWords {
+  uint4 a, b;   // b: of fp32
+};
+__device__ __forceinline__ SourceWords load_words(const void* from, bool f32, int64_t i) {
+  SourceWords w{};
+  if (f32) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(from) + i);
+    w.a = __ldcg(p);
+    w.b = __ldcg(p + 1);
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(s.g) + i);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    w.a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(from) + i));
+  }
+  return w;
+}
+__device__ __forceinline__ void words_to_floats(const SourceWords& s, bool f32, float (&v)[8]) {
+  const uint32_t w[8] = {s.a.x, s.a.y, s.a.z, s.a.w, s.b.x, s.b.y, s.b.z, s.b.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = f32 ? __uint_as_float(w[2 * k]) : bf16_lo(w[k]);
+    v[2 * k + 1] = f32 ? __uint_as_float(w[2 * k + 1]) : bf16_hi(w[k]);
   }
 }
-
 // norm + eps -> the power of two that brings u near 2^8, and the factor that is
 // left; NaN for both where the norm is not finite or passes 2^60.
 __device__ __forceinline__ void source_scale(float square, float eps, float& up, float& factor) {
