@@ -608,4 +608,15 @@ int make_map(CUtensorMap* m, bool bytes, int rank, const void* base, const uint6
   return r == CUDA_SUCCESS ? EP_OK : EP_ERR_CUDA;
 }
 
+int make_row_map(CUtensorMap* m, const void* base, uint64_t words, uint64_t rows, uint64_t count, uint32_t box_rows) {
+  const Encode encode = encoder();
+  if (encode == nullptr) return EP_ERR_CUDA;
+  const cuuint64_t dims[3] = {words, rows, count}, strides[2] = {words * 4, words * rows * 4};
+  const cuuint32_t box[3] = {256, box_rows, 1}, steps[3] = {1, 1, 1};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, steps,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? EP_OK : EP_ERR_CUDA;
+}
+
 }  // namespace ep_host

@@ -1,28 +1,28 @@
 // few.cu -- a whole mixture-of-experts layer for a few tokens, in two kernels.
 //
-//   k_few<.., kIn>    h = act(Wg x) * (Wu x)   for every slot (a token and one of its experts)
-//   k_few<.., kOut>   out = sum over a token's slots of weight * (W_down h)
+//   kIn    h = act(Wg x) * (Wu x)   for every slot (a token and one of its experts)
+//   kOut   out = sum over a token's slots of weight * (W_down h)
 //
 // Both are bound by reading each used expert's weights once.  The first deals
-// out (expert, h column) pairs evenly over the CTAs, the second output columns, so
+// out (expert, h column) pairs over the CTAs, the second output columns, so
 // that every CTA sums its own columns over all experts in a fixed order and
-// nothing is added up between CTAs.  A CTA walks its columns in units: 32 columns'
-// rows of gate and up, or 64 rows of W_down, whole in the inner index, for the
-// tokens of one expert.  The weights' rows are the first operand of tcgen05.mma (64
-// of them, those past the unit's being whatever lies there), the tokens
-// the second, 16 or 32 of them, so that a product costs what reading its 2 KB of
-// weights from shared memory does, a fifth of the time in which they arrive, and no thread
-// touches a weight.  (By mma.sync E4M3 weights had to be turned into fp16 first, which bounded the
-// kernels at 3.5 to 4.5 TB/s.)  Warps:
+// nothing is added up between CTAs.  A CTA walks its columns in units, whole in the
+// inner index, for the tokens of one expert.  The second kernel comes up as the first
+// one's CTAs leave and fills its ring with weights before it waits for h.
+//
+// Here for E4M3 weights, by tcgen05: a unit is 32 columns' rows of gate and up, or 64
+// rows of W_down.  The weights' rows are the first operand (64
+// of them, those past the unit's being whatever lies there), the tokens, split into two E4M3 numbers each,
+// the second, 8 to 32 columns, and no thread touches a weight: by mma.sync they had to be turned into fp16 first,
+// which took a batch of 32 (128 experts, 7168 x 2048, top-8) 1129 us instead of 814.  bf16 weights need no turning, and
+// their rows, of any multiple of 16 bytes, come in 1 KB pieces where this form wants 128-byte ones: few_bf16.cu.
+// Warps:
 //   4 bring the sums out of tensor memory and finish a unit
 //   1 issues the products
 //   2 copy weights (TMA, 8 rows x 512 bytes a copy), 3 tokens' rows
 //   6 put the tokens where the products read them, in three teams, a stage each
-// The second kernel comes up as the first one's CTAs leave and fills its ring with
-// weights before it waits for h.
 
-#include "expert.cuh"
-#include "umma.cuh"
+#include "few.cuh"
 
 namespace ep {
 
@@ -35,245 +35,36 @@ constexpr int kGroupBytes = kBlocks * 1024;   // 8 rows of a stage
 constexpr int kWeightBytes = kUnitRows / 8 * kGroupBytes;
 constexpr int kSums = 4;              // sums on their way out of tensor memory
 constexpr int kScaleRing = 16;        // stages whose tokens' scales are kept: more than are between the copies and the epilogue
-constexpr int kCrossing = 16;         // columns: what a narrow unit at an expert's end costs by its products (evenly: 49 us instead of KX)
-constexpr int64_t kWaveWork = 1 << 23;
 constexpr int kMaxFewStages = 8;
-constexpr int kFewSmem = 226 * 1024;
-__host__ __device__ constexpr int pass_of(bool fp8) { return fp8 ? 16 : 32; }   // tokens of an expert taken at a time
+constexpr int kPass = 16;             // tokens of an expert taken at a time, two columns of products each
 
-struct FewParams {
-  CUtensorMap whole, tail;     // weights [2 E or E][N][K]: 8 rows of 4 blocks of 128 bytes; of one block, which K may cut
-  const uint8_t* scales;
-  const __nv_bfloat16* v;      // kIn: x [T, H]; kOut: h [T k, I]
-  const int64_t* idx;          // [T, k]
-  const float* weights;
-  __nv_bfloat16* out;          // kIn: h; kOut: out [T, H]
-  int32_t* status;
-  int T, k, E, K, N;           // K: inner extent; N: columns of h or out
-  uint32_t wave;               // CTAs that run at once
+struct FewParams : FewCall {
+  CUtensorMap w;               // weights [2 E or E][N][K]: 8 rows of 4 blocks of 128 bytes
 };
 
 struct FewShared {
   uint64_t full[kMaxFewStages], turned[kMaxFewStages], empty[kMaxFewStages];
   uint64_t sums_full[kSums], sums_empty[kSums];
-  int group_slots[kMaxE / kWarp], group_used[kMaxE / kWarp], group_most[kMaxE / kWarp];   // of 32 experts
-  int n_used, most;                    // used experts; slots of the largest
+  FewCounts counts;
   uint32_t tmem;
-  alignas(16) float scales[kScaleRing][kBlocks][pass_of(true)];   // E4M3: what a token's block was divided by
-  float up[2][pass_of(false)][kUnitRows / 2];         // kIn: on its way to its gate
-};
-
-// What every CTA works out first: the used experts in rising order, and their
-// slots in rising order.
-struct FewUsed {
-  int16_t expert, first, count, pad;   // slots first .. first + count of the lists
-};
-struct FewLists {
-  FewUsed* used;             // [E]
-  float* weight;             // [n], as the next three
-  int16_t *slot, *token, *id;   // id: expert of a slot, -1: unused
-  int16_t* start;            // [E]
-  float* sums;               // kOut: [T][kUnitRows], the columns in hand
-  static __host__ __device__ int bytes(int E, int T, int k) { return (E * 10 + T * k * 10 + T * kUnitRows * 4 + 127) / 128 * 128; }
-  __device__ __forceinline__ FewLists(uint8_t* at, int E, int T, int k) {
-    used = reinterpret_cast<FewUsed*>(at);
-    sums = reinterpret_cast<float*>(used + E);
-    weight = sums + T * kUnitRows;
-    slot = reinterpret_cast<int16_t*>(weight + T * k);
-    token = slot + T * k;
-    id = token + T * k;
-    start = id + T * k;
-  }
-};
-
-// masks: a bit a slot for every expert; memory that nothing else uses yet.
-__device__ __forceinline__ void few_lists(const FewParams& p, FewShared& sh, const FewLists& l, uint32_t* masks, bool report) {
-  const int n = p.T * p.k, words = (n + 31) / 32, groups = (p.E + 31) / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (n <= kWarp) {   // one warp by itself, a slot a lane: places by counting the slots before (2.3 us the other way)
-    if (warp == 0) {
-      const int64_t id = lane < n ? p.idx[lane] : -1;
-      const bool fits = id >= 0 && id < p.E;
-      if (report && !fits && id != -1) set_status(p.status, EP_ERR_INVALID_ARG);
-      const int e = fits ? (int)id : kMaxE;
-      const float weight = fits ? p.weights[lane] : 0.0f;
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      const bool leads = fits && (same & lanemask_lt()) == 0;
-      int at = __popc(same & lanemask_lt()), d = 0;
-      for (int i = 0; i < n; ++i) {
-        const int other = __shfl_sync(0xffffffffu, e, i);
-        const bool other_leads = __shfl_sync(0xffffffffu, leads, i);
-        at += other < e;
-        d += other < e && other_leads;
-      }
-      const int c = __popc(same);
-      if (fits) {
-        l.slot[at] = (int16_t)lane;
-        l.token[at] = (int16_t)(lane / p.k);
-        l.weight[at] = weight;
-        if (leads) l.used[d] = {(int16_t)e, (int16_t)at, (int16_t)c, 0};
-      }
-      const int used = __popc(__ballot_sync(0xffffffffu, leads)), most = __reduce_max_sync(0xffffffffu, fits ? c : 0);
-      if (lane == 0) {
-        sh.n_used = used;
-        sh.most = most;
-      }
-    }
-    __syncthreads();
-    return;
-  }
-  for (int i = threadIdx.x; i < p.E * words; i += kFewThreads) masks[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kFewThreads) {
-    const int64_t e = p.idx[i];
-    const bool fits = e >= 0 && e < p.E;
-    if (report && !fits && e != -1) set_status(p.status, EP_ERR_INVALID_ARG);
-    if (fits) atomicOr(masks + (int)e * words + (i >> 5), 1u << (i & 31));
-    l.id[i] = fits ? (int16_t)e : (int16_t)-1;
-  }
-  __syncthreads();
-  auto count_of = [&](int e) {
-    int c = 0;
-    if (e < p.E)
-      for (int w = 0; w < words; ++w) c += __popc(masks[e * words + w]);
-    return c;
-  };
-  for (int q = warp; q < groups; q += kFewThreads / kWarp) {
-    const int c = count_of(q * 32 + lane);
-    const int all = __reduce_add_sync(0xffffffffu, c), most = __reduce_max_sync(0xffffffffu, c);
-    const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
-    if (lane == 0) {
-      sh.group_slots[q] = all;
-      sh.group_used[q] = __popc(some);
-      sh.group_most[q] = most;
-    }
-  }
-  __syncthreads();
-  for (int q = warp; q < groups; q += kFewThreads / kWarp) {
-    const bool before = lane < q;
-    const int slots = __reduce_add_sync(0xffffffffu, before ? sh.group_slots[lane] : 0);
-    const int used = __reduce_add_sync(0xffffffffu, before ? sh.group_used[lane] : 0);
-    const int c = count_of(q * 32 + lane);
-    int upto = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
-    if (c > 0) {
-      const int first = slots + upto - c;
-      l.used[used + __popc(some & lanemask_lt())] = {(int16_t)(q * 32 + lane), (int16_t)first, (int16_t)c, 0};
-      l.start[q * 32 + lane] = (int16_t)first;
-    }
-    if (q == 0) {
-      const int all = __reduce_add_sync(0xffffffffu, lane < groups ? sh.group_used[lane] : 0);
-      const int most = __reduce_max_sync(0xffffffffu, lane < groups ? sh.group_most[lane] : 0);
-      if (lane == 0) {
-        sh.n_used = all;
-        sh.most = most;
-      }
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kFewThreads) {
-    const int e = l.id[i];
-    if (e < 0) continue;
-    int at = l.start[e] + __popc(masks[e * words + (i >> 5)] & ((1u << (i & 31)) - 1));
-    for (int w = 0; w < (i >> 5); ++w) at += __popc(masks[e * words + w]);
-    l.slot[at] = (int16_t)i;
-    l.token[at] = (int16_t)(i / p.k);
-    l.weight[at] = p.weights[i];
-  }
-  fence_proxy_async_smem();   // copies will land where the masks are
-  __syncthreads();
-}
-
-// A CTA's units, one after another: `cols` columns from `col` on of expert e, for
-// the tokens s0 .. s0 + m of the lists.
-template <bool kIn, int kPass>
-struct FewWalk {
-  const FewUsed* used;
-  int n_used;
-  int N, left;           // kIn: (expert, column) pairs to come, from `col` of expert d on; kOut: columns from `col` on
-  int d, e, col, cols, s0, m, behind;   // behind: the expert's tokens after these
-  bool last;             // kOut: last unit of these columns
-  int most;              // columns of the widest unit
-
-  __device__ __forceinline__ FewWalk(const FewUsed* list, int count, int n, uint32_t wave) {
-    used = list;
-    n_used = count;
-    N = n;
-    const uint32_t all = kIn ? (uint32_t)n_used * (n + kCrossing) : n_used > 0 ? n : 0;   // below 2^32
-    // of kIn's CTAs that come after the first wave, each takes an eighth of a first one's columns
-    const uint32_t first = min(gridDim.x, wave), parts = 8 * first + (gridDim.x - first);
-    const uint32_t b = blockIdx.x < first ? 8 * blockIdx.x : 7 * first + blockIdx.x, size = blockIdx.x < first ? 8 : 1;
-    const uint32_t at = (uint32_t)((uint64_t)all * b / parts);
-    left = (int)((uint32_t)((uint64_t)all * (b + size) / parts) - at);
-    most = min(kIn ? kUnitRows / 2 : kUnitRows, left);
-    d = kIn ? (int)(at / (uint32_t)(n + kCrossing)) : n_used - 1;
-    col = (int)(kIn ? at - (uint32_t)d * (n + kCrossing) : at);
-    cols = s0 = m = behind = 0;
-  }
-  __device__ __forceinline__ bool next() {
-    if (behind > 0) {
-      s0 += m;
-    } else {
-      if (kIn) {
-        left -= cols;
-        col += cols;
-        if (col >= N) {
-          left -= N + kCrossing - col;
-          col = 0;
-          ++d;
-        }
-        if (left <= 0) return false;
-        cols = min(min(kUnitRows / 2, N - col), left);
-      } else {
-        if (++d >= n_used) {
-          left -= cols;
-          col += cols;
-          if (left <= 0) return false;
-          cols = min(kUnitRows, left);
-          d = 0;
-        }
-      }
-      const FewUsed u = used[d];
-      e = u.expert;
-      s0 = u.first;
-      behind = u.count;
-    }
-    m = min(kPass, behind);
-    behind -= m;
-    last = !kIn && behind == 0 && d + 1 == n_used;
-    return true;
-  }
+  alignas(16) float scales[kScaleRing][kBlocks][kPass];   // what a token's block was divided by
+  float up[2][kPass][kUnitRows / 2];         // kIn: on its way to its gate
 };
 
 // ---------------------------------------------------------------- products
 
-__device__ __forceinline__ void umma_few(bool fp8, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_few(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool add) {
   constexpr uint32_t kWeightsHi = ((uint32_t)kGroupBytes >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 4 KB apart
-  if (fp8)
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
-        " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %6};\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "r"(kWeightsHi), "r"(kDescHi)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
-        " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %6};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "r"(kWeightsHi), "r"(kDescHi)
-        : "memory");
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %6};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "r"(kWeightsHi), "r"(kDescHi)
+      : "memory");
 }
-// Instruction descriptor: 64 rows, n tokens; E4M3 or bf16 operands, fp32 sums.  Rows
+// Instruction descriptor: 64 rows, n columns; E4M3 operands, fp32 sums.  Rows
 // 16 w .. 16 w + 15 come out in the first 16 lanes of quarter w of the tensor memory.
-__device__ __forceinline__ uint32_t umma_few_idesc(bool fp8, int n) {
-  return (1u << 4) | (fp8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(n >> 3) << 17) | (4u << 24);
-}
+__device__ __forceinline__ uint32_t umma_few_idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (4u << 24); }
 
 // A token's bf16 numbers as two E4M3 ones, for E4M3 weights: in a block of 128
 // inner elements whose largest is in [2^e, 2^(e+1)), x = 2^(e-7) (hi + lo / 16) with
@@ -315,34 +106,6 @@ __device__ __forceinline__ float ue8m0_value(uint32_t b) {
   return b == 255 ? __uint_as_float(0x7fc00000u) : b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
 }
 
-// A bounded wait that looks at the clock (a slow read) only after some tries.
-__device__ __forceinline__ bool wait_few(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitNs) {
-  bool ok = false;
-  for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-  return __all_sync(0xffffffffu, ok || mbar_wait_bounded(bar, parity, limit_ns));
-}
-
-// The same for a thread by itself.
-__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitNs) {
-  for (int i = 0; i < 32; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_bounded(bar, parity, limit_ns);
-}
-
-// Where a role is in a ring.
-struct RingPosition {
-  int s, size;
-  uint32_t phase;
-
-  __device__ __forceinline__ RingPosition(int n) : s(0), size(n), phase(0) {}
-  __device__ __forceinline__ void advance() {
-    if (++s == size) {
-      s = 0;
-      phase ^= 1;
-    }
-  }
-};
-
 // kColumns columns of kCount blocks' sums, all on their way before the first is waited for.
 template <int kColumns, int kCount>
 __device__ __forceinline__ void few_columns(uint32_t at, int columns, float (&v)[kCount][kColumns]) {
@@ -356,79 +119,66 @@ __device__ __forceinline__ void few_columns(uint32_t at, int columns, float (&v)
 
 // The sums of a unit's rows for the tokens of kColumns columns: y[j] of token j, a
 // row a thread; ok: no wait has run out.
-template <bool kFp8, int kColumns>
+template <int kColumns>
 __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int columns, int chunks, int K, const uint8_t* scale, RingPosition& sums,
-                                         uint32_t& stage, float (&y)[pass_of(false)], bool& ok) {
-  if constexpr (kFp8) {
-    constexpr int kTokens = kColumns / 2, kCount = kColumns == 32 ? 2 : kBlocks;
-    const int blocks = K / kFp8Block;
-    uint32_t next[kBlocks];
-    auto fetch = [&](int c) {
+                                         uint32_t& stage, float (&y)[kPass], bool& ok) {
+  constexpr int kTokens = kColumns / 2, kCount = kColumns == 32 ? 2 : kBlocks;
+  const int blocks = K / kFp8Block;
+  uint32_t next[kBlocks];
+  auto fetch = [&](int c) {
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) next[b] = c * kBlocks + b < blocks ? __ldg(scale + c * kBlocks + b) : 0u;
-    };
-    fetch(0);
+    for (int b = 0; b < kBlocks; ++b) next[b] = c * kBlocks + b < blocks ? __ldg(scale + c * kBlocks + b) : 0u;
+  };
+  fetch(0);
 #pragma unroll
-    for (int j = 0; j < kTokens; ++j) y[j] = 0.0f;
-    for (int c = 0; c < chunks; ++c) {
-      float f[kBlocks];
+  for (int j = 0; j < kTokens; ++j) y[j] = 0.0f;
+  for (int c = 0; c < chunks; ++c) {
+    float f[kBlocks];
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) f[b] = ue8m0_value(next[b]);
-      fetch(c + 1);
-      if (ok) ok = wait_few(&sh.sums_full[sums.s], sums.phase, 4 * kWaitNs);
-      tmem_fence_after();
-      const uint32_t at = tmem + sums.s * kBlocks * columns;
+    for (int b = 0; b < kBlocks; ++b) f[b] = ue8m0_value(next[b]);
+    fetch(c + 1);
+    if (ok) ok = wait_few(&sh.sums_full[sums.s], sums.phase, 4 * kWaitNs);
+    tmem_fence_after();
+    const uint32_t at = tmem + sums.s * kBlocks * columns;
 #pragma unroll
-      for (int b0 = 0; b0 < kBlocks; b0 += kCount) {
-        float v[kCount][kColumns];
-        few_columns(at + b0 * columns, columns, v);
+    for (int b0 = 0; b0 < kBlocks; b0 += kCount) {
+      float v[kCount][kColumns];
+      few_columns(at + b0 * columns, columns, v);
 #pragma unroll
-        for (int b = 0; b < kCount; ++b) {
-          if (c * kBlocks + b0 + b < blocks) {
-            const float4* const token = reinterpret_cast<const float4*>(sh.scales[stage % kScaleRing][b0 + b]);
+      for (int b = 0; b < kCount; ++b) {
+        if (c * kBlocks + b0 + b < blocks) {
+          const float4* const token = reinterpret_cast<const float4*>(sh.scales[stage % kScaleRing][b0 + b]);
 #pragma unroll
-            for (int i = 0; i < kTokens / 4; ++i) {
-              const float4 t = token[i];
-              const float of[4] = {t.x, t.y, t.z, t.w};
+          for (int i = 0; i < kTokens / 4; ++i) {
+            const float4 t = token[i];
+            const float of[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int j = 4 * i + q;
-                y[j] = fmaf(fmaf(v[b][2 * j + 1], 0.0625f, v[b][2 * j]) * of[q], f[b0 + b], y[j]);
-              }
+            for (int q = 0; q < 4; ++q) {
+              const int j = 4 * i + q;
+              y[j] = fmaf(fmaf(v[b][2 * j + 1], 0.0625f, v[b][2 * j]) * of[q], f[b0 + b], y[j]);
             }
           }
         }
       }
-      tmem_fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.sums_empty[sums.s]);
-      sums.advance();
-      ++stage;
     }
-  } else {
-    if (ok) ok = wait_few(&sh.sums_full[sums.s], sums.phase, 4 * kWaitNs);
-    tmem_fence_after();
-    float v[1][kColumns];
-    few_columns(tmem + sums.s * columns, columns, v);
-#pragma unroll
-    for (int j = 0; j < kColumns; ++j) y[j] = v[0][j];
     tmem_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.sums_empty[sums.s]);
     sums.advance();
+    ++stage;
   }
 }
 
-template <bool kFp8, bool kIn, int kAct>
-__global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ FewParams p) {
-  constexpr int kOne = kFp8 ? 1 : 2;                 // bytes of a weight
-  constexpr int kBlock = 128 / kOne, kChunk = kBlocks * kBlock;   // inner elements of a block, of a stage
-  constexpr int kPass = pass_of(kFp8), kColumns = kFp8 ? 2 : 1;   // of the products for a token
+template <bool kIn, int kAct>
+__global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_constant__ FewParams p) {
+  constexpr int kBlock = 128, kChunk = kBlocks * kBlock;   // inner elements of a block, of a stage
   constexpr int kRawBytes = kChunk * 2;              // a token's row in a stage, as it comes
+  using Lists = FewLists<kUnitRows>;
+  using Walk = FewWalk<kIn, kPass, kUnitRows>;
   extern __shared__ __align__(1024) uint8_t raw[];
   FewShared& sh = *reinterpret_cast<FewShared*>(raw);
   uint8_t* const ring = raw + (sizeof(FewShared) + 1023) / 1024 * 1024;
-  uint8_t* const lists_at = raw + kFewSmem - FewLists::bytes(p.E, p.T, p.k);
+  uint8_t* const lists_at = raw + kFewSmem - Lists::bytes(p.E, p.T, p.k);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxFewStages; ++s) {
@@ -447,15 +197,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     pdl_wait();   // ids and tokens may come from the kernel before
     pdl_launch_dependents();
   }
-  const FewLists l(lists_at, p.E, p.T, p.k);
+  const Lists l(lists_at, p.E, p.T, p.k);
   tmem_fence_before();
-  few_lists(p, sh, l, reinterpret_cast<uint32_t*>(ring), kIn && blockIdx.x == 0);
+  few_lists<kFewThreads>(p, sh.counts, l, reinterpret_cast<uint32_t*>(ring), kIn && blockIdx.x == 0);
   tmem_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int tokens_most = min(sh.most, kPass);
-  const int columns = (tokens_most * kColumns + 7) / 8 * 8;   // of products, most
+  const int tokens_most = min(sh.counts.most, kPass);
+  const int columns = (tokens_most * 2 + 7) / 8 * 8;   // of products, most
   const int chunks = (p.K + kChunk - 1) / kChunk;
-  FewWalk<kIn, kPass> w(l.used, sh.n_used, p.N, p.wave);
+  Walk w(l.used, sh.counts.n_used, p.N, p.wave);
   // a stage: weights, tokens for the products, tokens as they came.  Products read 64
   // rows; what W_down's units have no rows for is other stages' memory, or the lists'.
   const int weight_bytes = kIn ? kWeightBytes : (w.most + 7) / 8 * kGroupBytes;
@@ -474,20 +224,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     if (!kIn && there)
       for (int n = 0; n < p.T; ++n) l.sums[n * kUnitRows + row] = 0.0f;
     while (w.next()) {
-      const uint8_t* scale = nullptr;
-      if (kFp8) {
-        const int n = min(w.col + column, p.N - 1);
-        scale = p.scales + ((int64_t)(kIn ? w.e * 2 + (warp >> 1) : w.e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
-      }
-      float y[pass_of(false)];
-      if (w.m * kColumns > 16)
-        few_sums<kFp8, 32>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
-      else if (w.m * kColumns > 8)
-        few_sums<kFp8, 16>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+      const int n = min(w.col + column, p.N - 1);
+      const uint8_t* const scale = p.scales + ((int64_t)(kIn ? w.e * 2 + (warp >> 1) : w.e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
+      float y[kPass];
+      if (w.m * 2 > 16)
+        few_sums<32>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+      else if (w.m * 2 > 8)
+        few_sums<16>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
       else
-        few_sums<kFp8, 8>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+        few_sums<8>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
       if (kIn) {
-        float(&up)[pass_of(false)][kUnitRows / 2] = sh.up[unit & 1];
+        float(&up)[kPass][kUnitRows / 2] = sh.up[unit & 1];
         if (warp >= kEpilogues / 2 && there) {
 #pragma unroll
           for (int j = 0; j < kPass; ++j) {
@@ -519,7 +266,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
       }
       ++unit;
     }
-    if (!kIn && sh.n_used == 0) {
+    if (!kIn && sh.counts.n_used == 0) {
       pdl_wait();   // out may be x
       for (int64_t i = (int64_t)blockIdx.x * (kEpilogues * kWarp) + threadIdx.x; i < (int64_t)p.T * p.N; i += (int64_t)gridDim.x * (kEpilogues * kWarp))
         p.out[i] = __float2bfloat16_rn(0.0f);
@@ -531,29 +278,27 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
       const uint32_t weights0 = umma_desc_lo(smem_addr(ring), 16), tokens0 = umma_desc_lo(smem_addr(ring) + weight_bytes, 16);
       RingPosition sums(kSums);
       while (ok && w.next()) {
-        const uint32_t idesc = umma_few_idesc(kFp8, (w.m * kColumns + 7) / 8 * 8);
+        const uint32_t idesc = umma_few_idesc((w.m * 2 + 7) / 8 * 8);
         for (int c = 0; c < chunks; ++c) {
-          if (kFp8 || c == 0) ok = wait_alone(&sh.sums_empty[sums.s], sums.phase ^ 1, 4 * kWaitNs);
+          ok = wait_alone(&sh.sums_empty[sums.s], sums.phase ^ 1, 4 * kWaitNs);
           ok = ok && wait_alone(&sh.turned[at.s], at.phase);   // by who has seen the weights' copies
           if (!ok) break;
           tmem_fence_after();
           const int blocks = (p.K - c * kChunk + kBlock - 1) / kBlock;
           const uint32_t a = weights0 + (uint32_t)at.s * (stage_bytes >> 4), b = tokens0 + (uint32_t)at.s * (stage_bytes >> 4);
-          const uint32_t d = tmem + sums.s * (columns * (kFp8 ? kBlocks : 1));
+          const uint32_t d = tmem + sums.s * (columns * kBlocks);
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i) {
             if (i < blocks) {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                umma_few(kFp8, kFp8 ? d + i * columns : d, a + (i * 64 + q * 2), b + i * (token_block >> 4) + q * 2, idesc, q > 0 || (!kFp8 && (i > 0 || c > 0)));
+                umma_few(d + i * columns, a + (i * 64 + q * 2), b + i * (token_block >> 4) + q * 2, idesc, q > 0);
             }
           }
           umma_commit(&sh.empty[at.s]);
           at.advance();
-          if (kFp8 || c + 1 == chunks) {
-            umma_commit(&sh.sums_full[sums.s]);
-            sums.advance();
-          }
+          umma_commit(&sh.sums_full[sums.s]);
+          sums.advance();
         }
       }
     }
@@ -587,18 +332,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         if (!ok) break;
         if (issue) {
           const int k = min(kChunk, p.K - c * kChunk);
-          const bool cut = k % kBlock != 0;   // K ends inside a block: block by block
-          const int blocks = cut ? (k + kBlock - 1) / kBlock : kBlocks;
-          if (turn == 0) mbar_arrive_expect_tx(&sh.full[at.s], (kIn ? 2 : 1) * groups * blocks * 1024 + w.m * k * 2);
+          if (turn == 0) mbar_arrive_expect_tx(&sh.full[at.s], (kIn ? 2 : 1) * groups * kGroupBytes + w.m * k * 2);
           const uint32_t to = smem_addr(ring + at.s * stage_bytes), bar = smem_addr(&sh.full[at.s]);
           for (int half = 0; half < (kIn ? 2 : 1); ++half) {
             const int z = kIn ? 2 * w.e + half : w.e;
             for (int g = turn; g < groups; g += kWeightWarps) {
               const uint32_t group = to + (half * (kUnitRows / 16) + g) * kGroupBytes;
-              if (!cut)
-                tma_load_4d(group, &p.whole, bar, 0, w.col + g * 8, c * kBlocks, z);
-              else
-                for (int i = 0; i < blocks; ++i) tma_load_3d<false>(group + i * 1024, &p.tail, bar, c * kChunk + i * kBlock, w.col + g * 8, z);
+              tma_load_4d(group, &p.w, bar, 0, w.col + g * 8, c * kBlocks, z);   // blocks behind the row's end are zeros
             }
           }
         }
@@ -617,25 +357,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
         if (stage % kTeams != (uint32_t)team) continue;
         const uint32_t to = smem_addr(ring + at.s * stage_bytes + weight_bytes), from = to + kBlocks * token_block;
         const int left = p.K - c * kChunk;
-        if constexpr (kFp8) {
-          for (int i = member; i < 2 * w.m; i += kTeam) {   // two blocks of a token
-            const int j = i >> 1, b = (i & 1) * 2 + (lane >> 4), piece = lane & 15;
-            const bool in = b * kBlock < left;
-            uint32_t hi[2], lo[2];
-            float scale;
-            split_e4m3(in ? ld_shared_v4_at(from + j * kRawBytes + (b * kBlock + piece * 8) * 2) : make_uint4(0, 0, 0, 0), hi, lo, scale);
-            if (in) {
-              const uint32_t row = to + b * token_block + 2 * j * 128, at_hi = row + ((((piece >> 1) ^ (2 * j & 7)) << 4) | ((piece & 1) << 3));
-              const uint32_t at_lo = row + 128 + ((((piece >> 1) ^ ((2 * j + 1) & 7)) << 4) | ((piece & 1) << 3));
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_hi), "r"(hi[0]), "r"(hi[1]) : "memory");
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_lo), "r"(lo[0]), "r"(lo[1]) : "memory");
-              if (piece == 0) sh.scales[stage % kScaleRing][b][j] = scale;
-            }
-          }
-        } else {
-          for (int j = member; j < w.m; j += kTeam) {   // zeros behind the row's end, as the weights have them
-            const uint4 v = lane * 8 < left ? ld_shared_v4_at(from + j * kRawBytes + lane * 16) : make_uint4(0, 0, 0, 0);
-            st_shared_v4_at(to + (lane >> 3) * token_block + j * 128 + (((lane & 7) ^ (j & 7)) << 4), v);
+        for (int i = member; i < 2 * w.m; i += kTeam) {   // two blocks of a token
+          const int j = i >> 1, b = (i & 1) * 2 + (lane >> 4), piece = lane & 15;
+          const bool in = b * kBlock < left;
+          uint32_t hi[2], lo[2];
+          float scale;
+          split_e4m3(in ? ld_shared_v4_at(from + j * kRawBytes + (b * kBlock + piece * 8) * 2) : make_uint4(0, 0, 0, 0), hi, lo, scale);
+          if (in) {
+            const uint32_t row = to + b * token_block + 2 * j * 128, at_hi = row + ((((piece >> 1) ^ (2 * j & 7)) << 4) | ((piece & 1) << 3));
+            const uint32_t at_lo = row + 128 + ((((piece >> 1) ^ ((2 * j + 1) & 7)) << 4) | ((piece & 1) << 3));
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_hi), "r"(hi[0]), "r"(hi[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_lo), "r"(lo[0]), "r"(lo[1]) : "memory");
+            if (piece == 0) sh.scales[stage % kScaleRing][b][j] = scale;
           }
         }
         fence_proxy_async_smem();
@@ -656,29 +389,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
   if (warp == kEpilogues) tmem_free<1>(tmem, 512);
 }
 
-template <bool kFp8, bool kIn, int kAct>
-static int launch_few_half(const FewParams& in, cudaStream_t s) {
-  auto* fn = k_few<kFp8, kIn, kAct>;
-  if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(fn), kFewSmem) != EP_OK) return EP_ERR_CUDA;
-  int grid = ep_host::grid_cap(1);
-  FewParams p = in;
-  p.wave = grid;
-  if (kIn && !ep_host::sm_budget_set() && (int64_t)p.T * p.k * p.N * p.K >= kWaveWork * grid) grid *= 1 + 2;
-  if (!kIn && ep_host::sm_budget_set()) {   // the second kernel's CTAs do not come up beside the first's
-    fn<<<grid, kFewThreads, kFewSmem, s>>>(p);
-  } else if (ep_host::launch_dependent<FewParams>(fn, grid, kFewThreads, kFewSmem, s, p) != EP_OK) {
-    return EP_ERR_CUDA;
-  }
-  ep_host::count_launch();
-  return ep_host::check_launch();
-}
-
-template <bool kFp8>
-static int launch_few(const FewParams& in, const FewParams& out, int act, cudaStream_t s) {
-  const int rc = act == EP_ACT_RELU   ? launch_few_half<kFp8, true, EP_ACT_RELU>(in, s)
-                 : act == EP_ACT_SILU ? launch_few_half<kFp8, true, EP_ACT_SILU>(in, s)
-                                      : launch_few_half<kFp8, true, EP_ACT_GELU>(in, s);
-  return rc != EP_OK ? rc : launch_few_half<kFp8, false, EP_ACT_NONE>(out, s);
+static int launch_few_e4m3(const FewCall& in, const FewCall& out, const void* w_gu, const void* w_down, int act, cudaStream_t s) {
+  FewParams p{in}, q{out};
+  auto map = [&](FewParams& f, const void* w, uint64_t count) {
+    const uint64_t N = f.N, K = f.K;
+    const uint64_t dims[4] = {kFp8Block, N, K / kFp8Block, count}, strides[3] = {K, kFp8Block, N * K};
+    const uint32_t box[4] = {kFp8Block, 8, kBlocks, 1};
+    return ep_host::make_map(&f.w, true, 4, w, dims, strides, box);
+  };
+  if (map(p, w_gu, 2 * (uint64_t)in.E) != EP_OK || map(q, w_down, in.E) != EP_OK) return EP_ERR_CUDA;
+  auto* fn = act == EP_ACT_RELU ? k_few_e4m3<true, EP_ACT_RELU> : act == EP_ACT_SILU ? k_few_e4m3<true, EP_ACT_SILU> : k_few_e4m3<true, EP_ACT_GELU>;
+  const int rc = launch_few_half<true>(fn, kFewThreads, p, s);
+  return rc != EP_OK ? rc : launch_few_half<false>(k_few_e4m3<false, EP_ACT_NONE>, kFewThreads, q, s);
 }
 
 static bool few_sizes(int R, int T_r, int k, int E, int I) {
@@ -711,7 +433,7 @@ extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* t
     if (p == nullptr || !ep_host::aligned16(p)) return EP_ERR_INVALID_ARG;
   if (topk_idx == nullptr || topk_weights == nullptr || workspace_bytes < ep_moe_few_workspace_size(R, T_r, k, E, I))
     return EP_ERR_INVALID_ARG;
-  FewParams p{};
+  FewCall p{};
   p.scales = w_gu_scales;
   p.v = static_cast<const __nv_bfloat16*>(x);
   p.idx = topk_idx;
@@ -723,24 +445,12 @@ extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* t
   p.E = E;
   p.K = H;
   p.N = I;
-  FewParams q = p;
+  FewCall q = p;
   q.scales = w_down_scales;
   q.v = p.out;
   q.out = static_cast<__nv_bfloat16*>(out);
   q.K = I;
   q.N = H;
-  auto maps = [&](FewParams& f, const void* w, uint64_t count) {
-    const uint64_t one = fp8 ? 1 : 2, block = 128 / one, row = f.K * one, N = f.N, K = f.K;
-    const uint64_t dims[4] = {block, N, std::max<uint64_t>(1, K / block), count}, strides[3] = {row, 128, N * row};
-    const uint32_t box[4] = {(uint32_t)block, 8, kBlocks, 1};
-    // (rows shorter than a block have none that is whole: that map is not used)
-    int rc = K >= block ? ep_host::make_map(&f.whole, fp8, 4, w, dims, strides, box) : EP_OK;
-    const uint64_t dims3[3] = {K, N, count}, strides3[2] = {row, N * row};
-    const uint32_t box3[3] = {(uint32_t)block, 8, 1};
-    if (rc == EP_OK) rc = ep_host::make_map(&f.tail, fp8, 3, w, dims3, strides3, box3);
-    return rc;
-  };
-  if (maps(p, w_gu, 2 * E) != EP_OK || maps(q, w_down, E) != EP_OK) return EP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return fp8 ? launch_few<true>(p, q, act, s) : launch_few<false>(p, q, act, s);
+  return fp8 ? launch_few_e4m3(p, q, w_gu, w_down, act, s) : launch_few_bf16(p, q, w_gu, w_down, act, s);
 }

@@ -324,4 +324,7 @@ namespace ep_host {
 // others), 128-byte swizzle, elements outside read as zero.
 int make_map(CUtensorMap* m, bool bytes, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
              const uint32_t* box, bool half_swizzle = false);   // half_swizzle: 64 bytes instead
+// Rows of `words` 32-bit words (count times `rows` of them), in boxes of 1 KB of
+// box_rows rows, one row behind the other; words outside read as zero.
+int make_row_map(CUtensorMap* m, const void* base, uint64_t words, uint64_t rows, uint64_t count, uint32_t box_rows);
 }  // namespace ep_host
