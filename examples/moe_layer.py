@@ -4,9 +4,11 @@ combine.
 `serve` is the low-latency form: tokens travel as E4M3 with ue8m0 scales and
 the experts' weights are E4M3 with one scale per 128 x 128 block.  `forward` /
 `backward` are a training step in bf16 over the contiguous layout, with the
-gradients of the tokens, the router's logits and all expert weights.
+gradients of the tokens, the router's logits and all expert weights; `update` is
+the optimiser's step on those weights.  `serve_few` is the layer for at most
+EP_MOE_FEW_TOKENS tokens, on bf16 weights as training leaves them or on E4M3 ones.
 
-    python examples/moe_layer.py        # runs both on small random data (needs a GB300)
+    python examples/moe_layer.py        # runs all of them on small random data (needs a GB300)
 """
 from __future__ import annotations
 
@@ -114,6 +116,40 @@ def backward(d_out, s, status):
     return d_x, d_logits, d_w_in, d_w_out
 
 
+# Newton-Schulz coefficients of Muon, five steps
+QUINTIC = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def masters(w):
+    """What the optimiser holds of the bf16 weights w: fp32 weights, momentum and a workspace."""
+    return {"w": w.float(), "m": torch.zeros_like(w, dtype=torch.float32),
+            "ws": ep.alloc_orthogonalize_workspace(w.shape, device=w.device)}
+
+
+def update(w, grad, state, lr, status, momentum=0.95, weight_decay=0.0):
+    """One Muon step on the experts' weights w [..., M, N] (bf16) and their masters,
+    every matrix by itself."""
+    M, N = w.shape[-2:]
+    ep.ep_muon_update(grad, state["m"], state["w"], w, QUINTIC, state["ws"], lr, scale=max(1.0, M / N) ** 0.5, momentum=momentum,
+                      weight_decay=weight_decay, status=status)
+
+
+def serve_few(x, logits, k, w_in, w_out, status):
+    """x [R, T_r, H] bf16 with few tokens, logits [R, T_r, E]; w_in, w_out as for
+    `forward` or as for `serve`.  Returns [R, T_r, H] bf16."""
+    R, T_r, _ = x.shape
+    w_in, in_scales = w_in if isinstance(w_in, tuple) else (w_in, None)
+    w_out, out_scales = w_out if isinstance(w_out, tuple) else (w_out, None)
+    E, _, I, _ = w_in.shape
+    idx = torch.empty((R, T_r, k), dtype=torch.int64, device=x.device)
+    weights = torch.empty((R, T_r, k), dtype=torch.float32, device=x.device)
+    ep.ep_gate_topk(logits, ep.EP_GATE_SOFTMAX, idx, weights)
+    out = torch.empty_like(x)
+    ep.ep_moe_few(x, idx, weights, w_in, in_scales, w_out, out_scales, ep.EP_ACT_SILU, out,
+                  ep.alloc_moe_few_workspace(R, T_r, k, E, I, device=x.device), status)
+    return out
+
+
 def main():
     torch.manual_seed(0)
     R, T_r, E, k, H, I = 4, 64, 32, 4, 1024, 512
@@ -126,10 +162,13 @@ def main():
     out, saved = forward(x, logits, k, w_in, w_out, R * T_r * min(k, E // R), status)
     grads = backward(torch.randn_like(x), saved, status)
     fast = serve(x, logits, k, quantise_weights(w_in), quantise_weights(w_out), T_r, status)
+    for w, g in ((w_in, grads[2]), (w_out, grads[3])):
+        update(w, g, masters(w), 0.02, status)
+    few = serve_few(x[:, :8].contiguous(), logits[:, :8].contiguous(), k, w_in, w_out, status)
     torch.cuda.synchronize()
     if ep.ep_read_status(status) != ep.EP_OK:
         raise SystemExit("a kernel reported " + ep.error_string(ep.ep_read_status(status)))
-    print("forward", tuple(out.shape), "gradients", [tuple(g.shape) for g in grads], "serve", tuple(fast.shape))
+    print("forward", tuple(out.shape), "gradients", [tuple(g.shape) for g in grads], "serve", tuple(fast.shape), "few", tuple(few.shape))
 
 
 if __name__ == "__main__":
