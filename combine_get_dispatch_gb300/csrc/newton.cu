@@ -34,7 +34,7 @@ namespace ep {
 // ---------------------------------------------------------------- momentum and norm
 
 constexpr int kSourceThreads = 256;
-constexpr int kAhead = 4;                 // loads on their way, of 8 elements a thread (two: 3.4 TB/s instead of KN)
+constexpr int kAhead = 4;                 // loads on their way, of 8 elements a thread (8 of 4096 x 1416: momentum and norm at 6.7 TB/s)
 constexpr int kMostParts = 64;            // of a matrix's norm
 // m <- momentum m + g and the squares' sums of u, a part of a matrix a CTA, in an
 // order that only the sizes give.  Memory bounds it.
@@ -176,6 +176,7 @@ struct NewtonParams {
   uint32_t stages, stage_bytes;
   uint32_t tiles_m, tiles_n;    // kSquare, kGram: tiles_m only
   uint32_t each, tiles;         // of a matrix, of all
+  uint32_t whole;               // tiles before those that are halved
   bool rows_fast;
   bool backward;                // the last matrix first
   bool a_mn, b_mn;
@@ -205,6 +206,9 @@ struct NewtonTile {
 template <int kForm>
 __device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, uint32_t t) {
   NewtonTile out;
+  const bool halved = t >= p.whole;
+  const uint32_t side = halved ? (t - p.whole) & 1 : 0;
+  if (halved) t = p.whole + ((t - p.whole) >> 1);
   const uint32_t z = t / p.each, u = t - z * p.each;
   out.z = p.backward ? p.count - 1 - (int)z : (int)z;
   if (symmetric(kForm)) {
@@ -222,8 +226,10 @@ __device__ __forceinline__ NewtonTile newton_tile(const NewtonParams& p, uint32_
     out.j0 = (int)(p.rows_fast ? slow : rest) * p.wide;
     out.mirror = false;
   }
+  const int wide = halved ? p.wide / 2 : p.wide;
+  out.j0 += (int)side * wide;
   // (an MN-major operand comes 64 columns at a time)
-  out.wide = p.b_mn ? p.wide : min(p.wide, (p.cols - out.j0 + 31) / 32 * 32);
+  out.wide = p.b_mn ? wide : min(wide, (p.cols - out.j0 + 31) / 32 * 32);
   return out;
 }
 
@@ -370,9 +376,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     constexpr int kBuffers = kForm == kApplyWeights ? 1 : 2;
     const uint32_t buffers = smem_addr(pieces) + (warp - 4) * kWarpBytes, at_w = buffers + 2 * kPiece;
     const uint32_t columns = smem_addr(&sh.columns[warp - 4][0][0]);
-    const int chunks = p.wide / kChunkCols, row0 = (int)rank * 128 + q * 32;
+    const int row0 = (int)rank * 128 + q * 32;
     const bool lo = kForm != kSquare && p.in_lo != nullptr, by_column = kForm != kSquare && !p.rows_fast;
-    auto live = [&](const NewtonTile& x, int ch) { return ch < chunks && x.j0 + ch * kChunkCols < p.cols && x.i0 + row0 < p.rows; };
+    auto live = [&](const NewtonTile& x, int ch) { return ch < x.wide / kChunkCols && x.j0 + ch * kChunkCols < p.cols && x.i0 + row0 < p.rows; };
     // the chunk that is copied next: (t_ahead, ch_ahead), number k_ahead
     uint32_t t_ahead = t, k_ahead = 0;
     int ch_ahead = side;
@@ -576,7 +582,7 @@ struct NewtonSpace {
 };
 
 // Row stride of A and P, and of X where it adds no more than an eighth: whole 128-byte lines, which a copied row of 64
-// elements then is one of (A and P, S = 1416, without: 870 clocks a stage instead of 610; X: PADX).
+// elements then is one of (A and P, S = 1416, without: 870 clocks a stage instead of 610; with X too, 8 of 4096 x 1416 took 1386 us instead of 1543).
 static int64_t padded(int n) { return (int64_t)(n + 63) / 64 * 64; }
 static int64_t padded_x(int N) { return N >= 512 ? padded(N) : N; }
 
@@ -646,7 +652,16 @@ struct Newton {
       p.tiles = (uint32_t)(each * count);
     };
     of(kBlock);
-    if ((int)p.tiles < ep_host::num_sms() / 2) of(kBlock / 2);   // whatever the SM budget: results go by the sizes alone
+    // whatever the SM budget: results go by the sizes alone
+    const uint32_t pairs = std::max(1, ep_host::num_sms() / 2), left = p.tiles % pairs;
+    p.whole = p.tiles;
+    if (p.tiles < pairs) {
+      of(kBlock / 2);
+      p.whole = p.tiles;
+    } else if (2 * left <= pairs) {   // a last wave of halves (16 of 1416 x 4096: X X^T in 94 us instead of 99, its square in 47 instead of 49)
+      p.whole -= left;
+      p.tiles += left;
+    }
   }
   NewtonParams start(int rows, int cols, int inner, bool sym) const {
     NewtonParams p{};

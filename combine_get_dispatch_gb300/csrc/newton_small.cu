@@ -8,7 +8,7 @@
 // as an MN-major one (P X).  A step is three
 // products, tcgen05.mma of one SM, with the epilogue of each by sixteen warps, a row
 // a thread.  Bound by latency: a launch a product took 7 us each, 125 us for 32
-// matrices of 128 x 256 and five steps; so it is N_SMALL us.
+// matrices of 128 x 256 and five steps; so it is 37 us.
 
 #include "newton.cuh"
 
