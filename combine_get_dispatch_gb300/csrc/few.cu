@@ -425,7 +425,7 @@ extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* t
   if (!few_sizes(R, T_r, k, E, I) || H <= 0 || H > (1 << 24)) return EP_ERR_INVALID_ARG;
   const int unit = fp8 ? kFp8Block : 8;
   const int64_t lim = (int64_t)1 << 31;
-  if (H % unit != 0 || I % unit != 0 || (int64_t)E * H >= lim || (int64_t)E * I >= lim) return EP_ERR_INVALID_ARG;
+  if (H % unit != 0 || I % unit != 0 || (int64_t)E * H >= lim || (int64_t)E * (I + kCrossing) >= lim) return EP_ERR_INVALID_ARG;
   if (act <= EP_ACT_NONE || act > EP_ACT_GELU) return EP_ERR_INVALID_ARG;
   if (fp8 != (w_gu_scales != nullptr) || fp8 != (w_down_scales != nullptr)) return EP_ERR_INVALID_ARG;
   if (T_r == 0) return EP_OK;

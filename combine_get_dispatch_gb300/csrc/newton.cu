@@ -34,10 +34,15 @@ namespace ep {
 // ---------------------------------------------------------------- momentum and norm
 
 constexpr int kSourceThreads = 256;
-constexpr int kAhead = 4;                 // loads on their way, of 8 elements a thread (8 of 4096 x 1416: momentum and norm at 6.7 TB/s)
-constexpr int kMostParts = 64;            // of a matrix's norm
+constexpr int kAhead = 4;                 // loads on their way, of 8 elements a thread
+// Parts of a matrix's norm, whatever the stack: a matrix comes out as it does alone.
+constexpr int kMostParts = 256;
+
 // m <- momentum m + g and the squares' sums of u, a part of a matrix a CTA, in an
-// order that only the sizes give.  Memory bounds it.
+// order that only the sizes give.  Memory bounds it: 8 of 4096 x 1416 with momentum at 6.7
+// TB/s; 186 MB of bf16 without at 5.2, where one kernel for all types, with the registers of the largest,
+// got through 3.4 (k_newton_scale below: 371 MB in 56 us instead of 108).
+template <bool kF32, bool kMomentum>
 __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
   __shared__ float warps[kSourceThreads / kWarp];
   pdl_wait();
@@ -51,15 +56,15 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
       for (int k = 0; k < kAhead; ++k) {
         const int64_t i = i0 + k * kSourceThreads * 8;
         if (i >= end) continue;
-        g[k] = load_words(s.g, s.f32, base + i);
-        if (s.m != nullptr) m[k] = load_words(s.m, true, base + i);
+        g[k] = load_words(s.g, kF32, base + i);
+        if (kMomentum) m[k] = load_words(s.m, true, base + i);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int64_t i = i0 + k * kSourceThreads * 8;
         float u[8];
-        words_to_floats(g[k], s.f32, u);
-        if (s.m != nullptr) {
+        words_to_floats(g[k], kF32, u);
+        if (kMomentum) {
           float v[8];
           words_to_floats(m[k], true, v);
 #pragma unroll
@@ -94,6 +99,7 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
 // X = u 2^q, in hi and lo, and the factor that makes it 2^8 u / (|u| + eps).  The
 // parts in the other order, as the last ones of the kernel before are still in L2.  m is read past the first-level
 // cache, which may hold what it was.
+template <bool kF32, bool kMomentum>
 __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
   pdl_launch_dependents();
   pdl_wait();
@@ -101,8 +107,11 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
   for (int64_t at = blockIdx.x; at < items; at += gridDim.x) {
     const int64_t item = items - 1 - at;
     const int64_t z = item / s.parts, begin = (item - z * s.parts) * s.part, end = min(begin + s.part, s.each), base = z * s.each;
-    float square = 0.0f;
-    for (int k = 0; k < s.parts; ++k) square += __ldcg(s.sums + z * s.parts + k);
+    float square = 0.0f;   // a warp for itself
+#pragma unroll 4
+    for (int k = threadIdx.x & 31; k < s.parts; k += kWarp) square += __ldcg(s.sums + z * s.parts + k);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) square += __shfl_xor_sync(0xffffffffu, square, o);
     float up, factor;
     source_scale(square, s.eps, up, factor);
     if (begin == 0 && threadIdx.x == 0) s.factor[z] = factor;
@@ -110,15 +119,15 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
     int64_t row = (begin + threadIdx.x * 8) / s.cols;
     int col = (int)(begin + threadIdx.x * 8 - row * s.cols);
     row += z * s.rows;
-    const bool reads_g = s.m == nullptr || s.nesterov;
+    const bool reads_g = !kMomentum || s.nesterov;
     for (int64_t i0 = begin + threadIdx.x * 8; i0 < end; i0 += kAhead * kSourceThreads * 8) {
       SourceWords g[kAhead] = {}, m[kAhead] = {};
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int64_t i = i0 + k * kSourceThreads * 8;
         if (i >= end) continue;
-        if (reads_g) g[k] = load_words(s.g, s.f32, base + i);
-        if (s.m != nullptr) m[k] = load_words(s.m, true, base + i);
+        if (reads_g) g[k] = load_words(s.g, kF32, base + i);
+        if (kMomentum) m[k] = load_words(s.m, true, base + i);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -131,8 +140,8 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
         }
         if (i0 + k * kSourceThreads * 8 >= end) continue;
         float u[8];
-        words_to_floats(g[k], s.f32, u);
-        if (s.m != nullptr) {
+        words_to_floats(g[k], kF32, u);
+        if (kMomentum) {
           float v[8];
           words_to_floats(m[k], true, v);
 #pragma unroll
@@ -769,8 +778,10 @@ static int newton(Source src, int count, int M, int N, int steps, const float* a
   src.hi = n.space.x[0];
   const bool exact = !src.f32 && src.m == nullptr;   // bf16 times a power of two is fp16, but for what is 2^-24 of the norm and smaller
   src.lo = exact ? nullptr : n.space.lo[0];
-  const int grid = (int)std::min<int64_t>((int64_t)count * src.parts, ep_host::grid_cap(4));
-  for (auto* kernel : {k_newton_norm, k_newton_scale}) {
+  const int grid = (int)std::min<int64_t>((int64_t)count * src.parts, ep_host::grid_cap(16));
+  auto* norm = src.m != nullptr ? (src.f32 ? k_newton_norm<true, true> : k_newton_norm<false, true>) : src.f32 ? k_newton_norm<true, false> : k_newton_norm<false, false>;
+  auto* scale = src.m != nullptr ? (src.f32 ? k_newton_scale<true, true> : k_newton_scale<false, true>) : src.f32 ? k_newton_scale<true, false> : k_newton_scale<false, false>;
+  for (auto* kernel : {norm, scale}) {
     if (ep_host::launch_dependent(kernel, grid, kSourceThreads, 0, s, src) != EP_OK) return EP_ERR_CUDA;
     ep_host::count_launch();
   }

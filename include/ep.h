@@ -457,7 +457,11 @@ int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, co
  *                (EP_FP8_NONE, scales NULL), or E4M3 with one ue8m0 byte per
  *                128 x 128 block (EP_FP8_E4M3_UE8M0; scales [E, 2, I/128, H/128]
  *                and [E, H/128, I/128]; scale byte 255 is NaN).  x and h stay
- *                bf16 either way: nothing is quantised here.
+ *                bf16 either way.  With E4M3 weights a token's 128 numbers under
+ *                one scale are multiplied as the sum of two E4M3 parts each:
+ *                exact down to 2^-13 of the largest of them, at most 2^-21 of the
+ *                largest off below; with an infinity or NaN among them the token's
+ *                outputs are NaN.
  *   out          [R, T_r, H] bf16; may be x itself
  *   workspace    ep_moe_few_workspace_size bytes, 16-byte aligned, no
  *                initialisation; calls that share one must be ordered
@@ -465,8 +469,9 @@ int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, co
  * other tokens change (over the slots: by expert, then by slot); h and out are
  * rounded to bf16 once each.  Ids outside [-1, E) set EP_ERR_INVALID_ARG in
  * *status and count as unused; a wait that runs out sets EP_ERR_TIMEOUT and
- * leaves outputs incomplete.  Limits: H, I multiples of 8 (128 with E4M3),
- * E * H and E * I below 2^31, act as for ep_expert_glu. */
+ * leaves outputs incomplete.  Limits: H, I multiples of 8 (128 with E4M3), at most
+ * 2^24, E * H and E * (I + 16) below 2^31, act as for ep_expert_glu.  All pointers
+ * but the ids, weights and scales 16-byte aligned. */
 #define EP_MOE_FEW_TOKENS 64
 size_t ep_moe_few_workspace_size(int R, int T_r, int k, int E, int I);
 int ep_moe_few(const void* x, const int64_t* topk_idx, const float* topk_weights, const void* w_gu,
@@ -495,9 +500,11 @@ int ep_moe_few(const void* x, const int64_t* topk_idx, const float* topk_weights
  *   workspace    ep_orthogonalize_workspace_size bytes, 16-byte aligned, no
  *                initialisation; calls that share one must be ordered
  * Limits: M >= 1, N a multiple of 8, M and N at most 2^20, count at most 65535,
- * count * M below 2^31, 1 <= steps <= 32, eps >= 1e-12, finite coefficients;
- * pointers 16-byte aligned.  Results do not depend on the SM budget.  A wait that runs
- * out sets EP_ERR_TIMEOUT in *status and leaves outputs incomplete. */
+ * count * M and the tiles of all matrices (256 x 128, each begun one whole) below
+ * 2^31, 1 <= steps <= 32, eps >= 1e-12, finite coefficients;
+ * pointers 16-byte aligned.  A matrix comes out as it would alone, and results do
+ * not depend on the SM budget.  A wait that runs out sets EP_ERR_TIMEOUT in
+ * *status and leaves outputs incomplete. */
 size_t ep_orthogonalize_workspace_size(int count, int M, int N);
 int ep_orthogonalize(const void* g, int dtype, int count, int M, int N, int steps,
                      const float* coefficients, float eps, void* out, void* workspace,

@@ -173,3 +173,13 @@ def test_edges_of_tiles(shape):
         g = gradient(sum(shape), *shape, dtype=dtype)
         steps = [QUINTIC] * 5
         assert rel(call(g, steps), exact(g, steps)) < off(steps) + 2.0 ** -8 / math.sqrt(3)
+
+
+@pytest.mark.parametrize("shape,count", [((300, 296), 40), ((1000, 520), 12), ((264, 1416), 90), ((40, 136), 700)])
+def test_a_matrix_comes_out_as_it_does_alone(shape, count):
+    """Stacks of few and of many matrices are cut into tiles of different widths."""
+    from test_gpu_newton import QUINTIC, call, gradient
+    g = gradient(count, count, *shape)
+    out = call(g, [QUINTIC] * 4)
+    for z in (0, count // 2, count - 1):
+        assert torch.equal(call(g[z:z + 1].contiguous(), [QUINTIC] * 4)[0], out[z])
