@@ -383,6 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     // of 900, waiting for those loads with its own.)
     const int q = warp & 3, side = (warp - 4) >> 2;
     constexpr int kBuffers = kForm == kApplyWeights ? 1 : 2;
+    constexpr bool kAheadOfChunk = reads_tile(kForm) && kBuffers == 2;
     const uint32_t buffers = smem_addr(pieces) + (warp - 4) * kWarpBytes, at_w = buffers + 2 * kPiece;
     const uint32_t columns = smem_addr(&sh.columns[warp - 4][0][0]);
     const int row0 = (int)rank * 128 + q * 32;
@@ -431,6 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
       copy_async_commit();
     };
     if (reads_tile(kForm)) fetch();
+    if (kAheadOfChunk) fetch();
     uint32_t n = 0, k = 0;   // tiles, chunks
     for (; more; step(), ++n) {
       const uint32_t half = n & 1;
@@ -453,6 +455,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
         __syncwarp();
         float v[32];
         tmem_ld32(d + ch * kChunkCols, v);
+        if (kAheadOfChunk && k > 0) {   // the next chunk's, into the other buffer, once the last one's copy has left it
+          if (lane == 0) tma_wait_read<0>();
+          __syncwarp();
+          fetch();
+        }
         tmem_wait_ld(v);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {   // 8 columns
@@ -557,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_wait_read<0>();   // the last chunk's copy, out of the other buffer
+            if (!kAheadOfChunk) tma_wait_read<0>();   // the last chunk's copy, out of the other buffer
             tma_store_3d(&p.out, at, col0, tile.i0 + row0, tile.z);
             if (kForm == kApply) tma_store_3d(&p.out_lo, at_lo, col0, tile.i0 + row0, tile.z);
             if (symmetric(kForm) && tile.mirror) tma_store_3d(&p.out, at_lo, tile.i0 + row0, col0, tile.z);
@@ -565,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
           }
           __syncwarp();
         }
-        if (reads_tile(kForm)) fetch();
+        if (kForm == kApplyWeights) fetch();
       }
       tmem_fence_before();   // the next tile's products may have this half
       __syncwarp();
