@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
     fence_barrier_init();
   }
   if (warp == kEpilogues) tmem_alloc<1>(&sh.tmem, 512);
+  if (threadIdx.x == kFewThreads - 1) prefetch_map(&p.w);
   if (kIn) {
     pdl_wait();   // ids and tokens may come from the kernel before
     pdl_launch_dependents();

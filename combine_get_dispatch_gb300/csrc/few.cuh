@@ -172,8 +172,9 @@ struct FewWalk {
     // of kIn's CTAs that come after the first wave, each takes an eighth of a first one's columns
     const uint32_t first = min(gridDim.x, wave), parts = 8 * first + (gridDim.x - first);
     const uint32_t b = blockIdx.x < first ? 8 * blockIdx.x : 7 * first + blockIdx.x, size = blockIdx.x < first ? 8 : 1;
-    const uint32_t at = (uint32_t)((uint64_t)all * b / parts);
-    left = (int)((uint32_t)((uint64_t)all * (b + size) / parts) - at);
+    const uint32_t each = all / parts, more = all - each * parts;   // the first `more` parts have one more
+    const uint32_t at = each * b + min(b, more);
+    left = (int)(each * size + min(b + size, more) - min(b, more));
     most = min(kIn ? kUnitRows / 2 : kUnitRows, left);
     d = kIn ? (int)(at / (uint32_t)(n + kCrossing)) : n_used - 1;
     col = (int)(kIn ? at - (uint32_t)d * (n + kCrossing) : at);

@@ -126,6 +126,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
     }
     fence_barrier_init();
   }
+  if (threadIdx.x == kRowThreads - 1) {
+    prefetch_map(&p.whole);
+    prefetch_map(&p.four);
+    prefetch_map(&p.one);
+  }
   if (kIn) {
     pdl_wait();   // ids and tokens may come from the kernel before
     pdl_launch_dependents();
