@@ -14,20 +14,21 @@
 // rows of W_down.  The weights' rows are the first operand (64
 // of them, those past the unit's being whatever lies there), the tokens, split into two E4M3 numbers each,
 // the second, 8 to 32 columns, and no thread touches a weight: by mma.sync they had to be turned into fp16 first,
-// which took a batch of 32 (128 experts, 7168 x 2048, top-8) 1129 us instead of 814.  bf16 weights need no turning, and
+// which took a batch of 32 (128 experts, 7168 x 2048, top-8) 1129 us instead of 776.  bf16 weights need no turning, and
 // their rows, of any multiple of 16 bytes, come in 1 KB pieces where this form wants 128-byte ones: few_bf16.cu.
 // Warps:
-//   4 bring the sums out of tensor memory and finish a unit
+//   8 bring the sums out of tensor memory, in two teams, a stage each; the first finishes a unit
 //   1 issues the products
-//   2 copy weights (TMA, 8 rows x 512 bytes a copy), 3 tokens' rows
-//   6 put the tokens where the products read them, in three teams, a stage each
+//   2 copy weights (TMA, 8 rows x 512 bytes a copy), 1 tokens' rows
+//   4 put the tokens where the products read them, in two teams, a stage each
 
 #include "few.cuh"
 
 namespace ep {
 
-constexpr int kEpilogues = 4, kWeightWarps = 2, kRowWarps = 3;   // a warp issues a copy in some 80 clocks
-constexpr int kTeams = 3, kTeam = 2, kTurners = kTeams * kTeam;   // a stage is one team's: its latency is 500 clocks and more
+constexpr int kQuarters = 4, kSumTeams = 2, kEpilogues = kQuarters * kSumTeams;   // a unit's stages in turn: one takes a team 1050 clocks
+constexpr int kWeightWarps = 2, kRowWarps = 1;   // a warp issues a copy in some 80 clocks; sixteen warps: with one more, 96 registers
+constexpr int kTeams = 2, kTeam = 2, kTurners = kTeams * kTeam;   // a stage is one team's: its latency is 500 clocks and more
 constexpr int kFewThreads = (kEpilogues + 1 + kRowWarps + kWeightWarps + kTurners) * kWarp;
 constexpr int kUnitRows = 64;         // of weights
 constexpr int kBlocks = 4;            // 128-byte blocks of a row in a stage
@@ -45,9 +46,11 @@ struct FewParams : FewCall {
 struct FewShared {
   uint64_t full[kMaxFewStages], turned[kMaxFewStages], empty[kMaxFewStages];
   uint64_t sums_full[kSums], sums_empty[kSums];
+  uint64_t part_full[2], part_empty[2];
   FewCounts counts;
   uint32_t tmem;
   alignas(16) float scales[kScaleRing][kBlocks][kPass];   // what a token's block was divided by
+  float part[2][kPass][kUnitRows];           // the second team's sums of a unit
   float up[2][kPass][kUnitRows / 2];         // kIn: on its way to its gate
 };
 
@@ -117,10 +120,10 @@ __device__ __forceinline__ void few_columns(uint32_t at, int columns, float (&v)
   for (int b = 0; b < kCount; ++b) tmem_wait_ld(v[b]);
 }
 
-// The sums of a unit's rows for the tokens of kColumns columns: y[j] of token j, a
-// row a thread; ok: no wait has run out.
+// A team's sums of a unit's rows, over its stages, for the tokens of kColumns columns:
+// y[j] of token j, a row a thread; ok: no wait has run out.
 template <int kColumns>
-__device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int columns, int chunks, int K, const uint8_t* scale, RingPosition& sums,
+__device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int team, int columns, int chunks, int K, const uint8_t* scale, RingPosition& sums,
                                          uint32_t& stage, float (&y)[kPass], bool& ok) {
   constexpr int kTokens = kColumns / 2, kCount = kColumns == 32 ? 2 : kBlocks;
   const int blocks = K / kFp8Block;
@@ -129,14 +132,17 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int colum
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) next[b] = c * kBlocks + b < blocks ? __ldg(scale + c * kBlocks + b) : 0u;
   };
-  fetch(0);
+  fetch(team);
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) y[j] = 0.0f;
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = 0; c < chunks; ++c, ++stage, sums.advance()) {
+    // (the other team's are skipped: a wait for a phase two ahead cannot pass, as the last stage that was this team's
+    // lies after the one that had these sums before)
+    if (c % kSumTeams != team) continue;
     float f[kBlocks];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) f[b] = ue8m0_value(next[b]);
-    fetch(c + 1);
+    fetch(c + kSumTeams);
     if (ok) ok = wait_few(&sh.sums_full[sums.s], sums.phase, 4 * kWaitNs);
     tmem_fence_after();
     const uint32_t at = tmem + sums.s * kBlocks * columns;
@@ -164,8 +170,6 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int colum
     tmem_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.sums_empty[sums.s]);
-    sums.advance();
-    ++stage;
   }
 }
 
@@ -188,7 +192,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
     }
     for (int b = 0; b < kSums; ++b) {
       mbar_init(&sh.sums_full[b], 1);
-      mbar_init(&sh.sums_empty[b], kEpilogues);
+      mbar_init(&sh.sums_empty[b], kQuarters);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.part_full[b], kQuarters);
+      mbar_init(&sh.part_empty[b], kQuarters);
     }
     fence_barrier_init();
   }
@@ -219,32 +227,52 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
     // ---------------------------------------------------------------- sums: a row a thread
     RingPosition sums(kSums);
     uint32_t stage = 0, unit = 0;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    const int row = warp * 16 + (lane & 15), column = kIn ? row % (kUnitRows / 2) : row;   // kIn: gate in two warps, up in the others
+    const int quarter = warp % kQuarters, team = warp / kQuarters;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int row = quarter * 16 + (lane & 15), column = kIn ? row % (kUnitRows / 2) : row;   // kIn: gate in two warps, up in the others
     const bool there = lane < 16;
-    if (!kIn && there)
+    if (!kIn && there && team == 0)
       for (int n = 0; n < p.T; ++n) l.sums[n * kUnitRows + row] = 0.0f;
     while (w.next()) {
       const int n = min(w.col + column, p.N - 1);
-      const uint8_t* const scale = p.scales + ((int64_t)(kIn ? w.e * 2 + (warp >> 1) : w.e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
+      const uint8_t* const scale = p.scales + ((int64_t)(kIn ? w.e * 2 + (quarter >> 1) : w.e) * (p.N / kFp8Block) + n / kFp8Block) * (p.K / kFp8Block);
       float y[kPass];
       if (w.m * 2 > 16)
-        few_sums<32>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+        few_sums<32>(sh, lanes, team, columns, chunks, p.K, scale, sums, stage, y, ok);
       else if (w.m * 2 > 8)
-        few_sums<16>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+        few_sums<16>(sh, lanes, team, columns, chunks, p.K, scale, sums, stage, y, ok);
       else
-        few_sums<8>(sh, lanes, columns, chunks, p.K, scale, sums, stage, y, ok);
+        few_sums<8>(sh, lanes, team, columns, chunks, p.K, scale, sums, stage, y, ok);
+      if (chunks > 1) {   // the teams' sums together
+        const int b = unit & 1;
+        const uint32_t phase = (unit >> 1) & 1;
+        if (ok) ok = team == 0 ? wait_few(&sh.part_full[b], phase, 4 * kWaitNs) : wait_few(&sh.part_empty[b], phase ^ 1, 4 * kWaitNs);
+        if (there) {
+#pragma unroll
+          for (int j = 0; j < kPass; ++j) {
+            if (j >= w.m) break;
+            if (team == 0)
+              y[j] += sh.part[b][j][row];
+            else
+              sh.part[b][j][row] = y[j];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(team == 0 ? &sh.part_empty[b] : &sh.part_full[b]);
+      }
+      ++unit;
+      if (team != 0) continue;
       if (kIn) {
         float(&up)[kPass][kUnitRows / 2] = sh.up[unit & 1];
-        if (warp >= kEpilogues / 2 && there) {
+        if (quarter >= kQuarters / 2 && there) {
 #pragma unroll
           for (int j = 0; j < kPass; ++j) {
             if (j >= w.m) break;
             up[j][column] = y[j];
           }
         }
-        named_barrier_sync(1, kEpilogues * kWarp);
-        if (warp < kEpilogues / 2 && there && column < w.cols) {
+        named_barrier_sync(1, kQuarters * kWarp);
+        if (quarter < kQuarters / 2 && there && column < w.cols) {
 #pragma unroll
           for (int j = 0; j < kPass; ++j) {   // rounded to bf16: the second kernel's operand
             if (j >= w.m) break;
@@ -265,7 +293,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
           }
         }
       }
-      ++unit;
     }
     if (!kIn && sh.counts.n_used == 0) {
       pdl_wait();   // out may be x
