@@ -50,7 +50,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // 1500 clocks, most of them waiting for one load after the other.
 template <bool kIn, int G>
 __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t* ring, int stage_bytes, float* red, int chunks,
-                                             uint32_t unit, RingPosition& at_stage, bool& ok) {
+                                             RingPosition& at_red, RingPosition& at_stage, bool& ok) {
   constexpr int kStep = 32;   // inner elements a warp multiplies at a time: 16 bytes of weights a lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, odd = g & 1;
   const int k0 = warp * 2 * kStep;        // this warp's first inner element of a stage
@@ -96,7 +96,7 @@ __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t
     if (lane == 0) mbar_arrive(&sh.empty[at_stage.s]);
     at_stage.advance();
   }
-  if (ok) ok = wait_few(&sh.red_empty[unit & 1], ((unit >> 1) & 1) ^ 1);
+  if (ok) ok = wait_few(&sh.red_empty[at_red.s], at_red.phase ^ 1);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -104,12 +104,13 @@ __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[(j * 8 + 2 * t + (i & 1)) * kRedPitch + h * 16 + (i >> 1) * 8 + g] = acc[h][j][i];
   __syncwarp();
-  if (lane == 0) mbar_arrive(&sh.red_full[unit & 1]);
+  if (lane == 0) mbar_arrive(&sh.red_full[at_red.s]);
+  at_red.advance();
 }
 
 template <bool kIn, int kAct>
 __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_constant__ RowParams p) {
-  using Lists = FewLists<kRowUnit>;
+  using Lists = FewLists<kIn ? 0 : kRowUnit>;
   extern __shared__ __align__(1024) uint8_t raw[];
   RowShared& sh = *reinterpret_cast<RowShared*>(raw);
   uint8_t* const lists_at = raw + kFewSmem - Lists::bytes(p.E, p.T, p.k);
@@ -139,38 +140,37 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
   few_lists<kRowThreads>(p, sh.counts, l, reinterpret_cast<uint32_t*>(red_base), kIn && blockIdx.x == 0);
   const int tokens_most = min(sh.counts.most, kRowPass);
   const int red_part = (tokens_most + 7) / 8 * 8 * kRedPitch;         // floats of one part's sums
-  const int red_bytes = kParts * red_part * 4;                        // of one unit; the next one's go to a second part
+  const int red_bytes = kParts * red_part * 4;                        // of one unit
   const int stage_bytes = kRowUnit * kPiece + (tokens_most * kTokenPitch + 127) / 128 * 128;
-  uint8_t* const ring = red_base + 2 * red_bytes;
   // products read 8 tokens' rows, there or not: seven may lie behind the last stage
-  const int stages = min(kRowStages, ((int)(lists_at - ring) - 7 * kTokenPitch) / stage_bytes);
+  auto stages_with = [&](int reds) { return min(kRowStages, ((int)(lists_at - red_base) - reds * red_bytes - 7 * kTokenPitch) / stage_bytes); };
+  // two units' sums, or one's where that makes room for a stage (64 tokens over eight experts: RED)
+  const int reds = stages_with(1) > stages_with(2) && stages_with(1) <= 4 ? 1 : 2, stages = stages_with(reds);
+  uint8_t* const ring = red_base + reds * red_bytes;
   const int chunks = (p.K + kChunk - 1) / kChunk;
   FewWalk<kIn, kRowPass, kRowUnit> w(l.used, sh.counts.n_used, p.N, p.wave);
   bool ok = true;
-  RingPosition position(stages);
+  RingPosition position(stages), at_red(reds);
 
   if (warp < kParts) {
     // ---------------------------------------------------------------- products
-    uint32_t unit = 0;
     while (w.next()) {
-      float* const red = reinterpret_cast<float*>(red_base + (unit & 1) * red_bytes) + warp * red_part;
+      float* const red = reinterpret_cast<float*>(red_base + at_red.s * red_bytes) + warp * red_part;
       if (w.m <= 8)
-        few_products<kIn, 1>(p.K, sh, ring, stage_bytes, red, chunks, unit, position, ok);
+        few_products<kIn, 1>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok);
       else if (w.m <= 16)
-        few_products<kIn, 2>(p.K, sh, ring, stage_bytes, red, chunks, unit, position, ok);
+        few_products<kIn, 2>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok);
       else
-        few_products<kIn, kRowPass / 8>(p.K, sh, ring, stage_bytes, red, chunks, unit, position, ok);
-      ++unit;
+        few_products<kIn, kRowPass / 8>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok);
     }
   } else if (warp < kParts + kAdders) {
     // ---------------------------------------------------------------- sums
     const int q = warp - kParts;
-    uint32_t unit = 0;
     if (!kIn)
       for (int n = q; n < p.T; n += kAdders) l.sums[n * kRowUnit + lane] = 0.0f;
     while (w.next()) {
-      const int b = unit & 1;
-      if (ok) ok = wait_few(&sh.red_full[b], (unit >> 1) & 1, 2 * kWaitNs);
+      const int b = at_red.s;
+      if (ok) ok = wait_few(&sh.red_full[b], at_red.phase, 2 * kWaitNs);
       const float* const red = reinterpret_cast<const float*>(red_base + b * red_bytes);
       auto total = [&](int n, int row) {
         float v[kParts];
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.red_empty[b]);
-      ++unit;
+      at_red.advance();
       if (!kIn && w.last) {
         for (int n = q; n < p.T; n += kAdders) {
           if (lane < w.cols) p.out[(int64_t)n * p.N + w.col + lane] = __float2bfloat16_rn(l.sums[n * kRowUnit + lane]);
