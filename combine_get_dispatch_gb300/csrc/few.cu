@@ -22,6 +22,8 @@
 //   2 copy weights (TMA, 8 rows x 512 bytes a copy), 1 tokens' rows
 //   4 put the tokens where the products read them, in two teams, a stage each
 
+#include <type_traits>
+
 #include "few.cuh"
 
 namespace ep {
@@ -75,16 +77,16 @@ __device__ __forceinline__ uint32_t umma_few_idesc(int n) { return (1u << 4) | (
 // 2 j + 1 of the products.  bf16 has 8 significant bits and each part 4, so this is x
 // itself down to 2^-13 of the largest, and 2^-21 of the largest off below: no more
 // than sums in 32 bits lose.  A block with an infinity or NaN gets the scale NaN.
-// 8 elements a lane, a block sixteen lanes.
-__device__ __forceinline__ void split_e4m3(uint4 v, uint32_t (&hi)[2], uint32_t (&lo)[2], float& scale) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t a = w[0] & 0x7fff7fffu, b = w[1] & 0x7fff7fffu;
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(w[2] & 0x7fff7fffu));
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(w[3] & 0x7fff7fffu));
+// 8 elements a lane, a block sixteen lanes.  top: the largest as a bf16 number's bits, of a lane's elements, then of the block.
+__device__ __forceinline__ uint32_t top_bf16(uint4 v) {
+  uint32_t a = v.x & 0x7fff7fffu, b = v.y & 0x7fff7fffu;
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(v.z & 0x7fff7fffu));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(v.w & 0x7fff7fffu));
   asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
-  uint32_t top = max(a >> 16, a & 0xffffu);
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return max(a >> 16, a & 0xffffu);
+}
+__device__ __forceinline__ void split_e4m3(uint4 v, uint32_t top, uint32_t (&hi)[2], uint32_t (&lo)[2], float& scale) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   const uint32_t e = top >> 7;   // biased; up = 2^(134 - e), no more than 2^127
   const float up = __uint_as_float((e <= 7 ? 254u : 261u - min(e, 254u)) << 23);
   scale = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(e <= 7 ? 0x00400000u : (e - 7) << 23);
@@ -385,20 +387,48 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
         if (stage % kTeams != (uint32_t)team) continue;
         const uint32_t to = smem_addr(ring + at.s * stage_bytes + weight_bytes), from = to + kBlocks * token_block;
         const int left = p.K - c * kChunk;
-        for (int i = member; i < 2 * w.m; i += kTeam) {   // two blocks of a token
-          const int j = i >> 1, b = (i & 1) * 2 + (lane >> 4), piece = lane & 15;
-          const bool in = b * kBlock < left;
-          uint32_t hi[2], lo[2];
-          float scale;
-          split_e4m3(in ? ld_shared_v4_at(from + j * kRawBytes + (b * kBlock + piece * 8) * 2) : make_uint4(0, 0, 0, 0), hi, lo, scale);
-          if (in) {
-            const uint32_t row = to + b * token_block + 2 * j * 128, at_hi = row + ((((piece >> 1) ^ (2 * j & 7)) << 4) | ((piece & 1) << 3));
-            const uint32_t at_lo = row + 128 + ((((piece >> 1) ^ ((2 * j + 1) & 7)) << 4) | ((piece & 1) << 3));
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_hi), "r"(hi[0]), "r"(hi[1]) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_lo), "r"(lo[0]), "r"(lo[1]) : "memory");
-            if (piece == 0) sh.scales[stage % kScaleRing][b][j] = scale;
+        // an item is two blocks of a token, a lane's 8 elements of one: several at a time, each step of all before the next
+        // (one after the other they took 440 clocks each: 32 tokens through 32 experts, top-8:
+        // 372 us instead of 458)
+        auto turn_items = [&](auto items) {
+          constexpr int kItems = decltype(items)::value;
+          for (int i0 = member; i0 < 2 * w.m; i0 += kTeam * kItems) {
+            const int piece = lane & 15;
+            uint4 v[kItems];
+            uint32_t top[kItems];
+            bool in[kItems];
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) {
+              const int i = i0 + u * kTeam, b = (i & 1) * 2 + (lane >> 4);
+              in[u] = i < 2 * w.m && b * kBlock < left;
+              v[u] = in[u] ? ld_shared_v4_at(from + (i >> 1) * kRawBytes + (b * kBlock + piece * 8) * 2) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) top[u] = top_bf16(v[u]);
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+              for (int u = 0; u < kItems; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) {
+              const int i = i0 + u * kTeam, j = i >> 1, b = (i & 1) * 2 + (lane >> 4);
+              uint32_t hi[2], lo[2];
+              float scale;
+              split_e4m3(v[u], top[u], hi, lo, scale);
+              if (in[u]) {
+                const uint32_t row = to + b * token_block + 2 * j * 128, at_hi = row + ((((piece >> 1) ^ (2 * j & 7)) << 4) | ((piece & 1) << 3));
+                const uint32_t at_lo = row + 128 + ((((piece >> 1) ^ ((2 * j + 1) & 7)) << 4) | ((piece & 1) << 3));
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_hi), "r"(hi[0]), "r"(hi[1]) : "memory");
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_lo), "r"(lo[0]), "r"(lo[1]) : "memory");
+                if (piece == 0) sh.scales[stage % kScaleRing][b][j] = scale;
+              }
+            }
           }
-        }
+        };
+        if (w.m == 1)
+          turn_items(std::integral_constant<int, 2 / kTeam>());
+        else
+          turn_items(std::integral_constant<int, 4>());
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.turned[at.s]);
@@ -427,8 +457,15 @@ static int launch_few_e4m3(const FewCall& in, const FewCall& out, const void* w_
   };
   if (map(p, w_gu, 2 * (uint64_t)in.E) != EP_OK || map(q, w_down, in.E) != EP_OK) return EP_ERR_CUDA;
   auto* fn = act == EP_ACT_RELU ? k_few_e4m3<true, EP_ACT_RELU> : act == EP_ACT_SILU ? k_few_e4m3<true, EP_ACT_SILU> : k_few_e4m3<true, EP_ACT_GELU>;
-  const int rc = launch_few_half<true>(fn, kFewThreads, p, s);
-  return rc != EP_OK ? rc : launch_few_half<false>(k_few_e4m3<false, EP_ACT_NONE>, kFewThreads, q, s);
+  // SMs get through the same work up to a sixth faster or slower than the mean, which a large call
+  // pays for at its end: more CTAs with a few columns, which come up where others have left.  0.47 GB of gate and
+  // up take 88 us in one wave and 98 so, 0.70 GB 255 and 232, 3.8 GB 842 and 763 (with W_down).  bf16: 0.7 GB 3 % slower
+  // so, 2.8 GB 0.3 % faster, so that its kernel keeps to one wave.
+  constexpr int64_t kWaveBytes = (int64_t)1 << 29;   // of gate and up, if every slot has its own expert
+  const int64_t bytes = 2 * (int64_t)std::min(p.T * p.k, p.E) * p.N * p.K;
+  const int waves = bytes >= kWaveBytes && !ep_host::sm_budget_set() ? 3 : 1;
+  const int rc = launch_few_half<true>(fn, kFewThreads, p, waves, s);
+  return rc != EP_OK ? rc : launch_few_half<false>(k_few_e4m3<false, EP_ACT_NONE>, kFewThreads, q, 1, s);
 }
 
 static bool few_sizes(int R, int T_r, int k, int E, int I) {

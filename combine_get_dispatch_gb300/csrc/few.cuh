@@ -243,21 +243,16 @@ struct RingPosition {
   }
 };
 
-// A half of the layer: kIn or kOut.
+// A half of the layer: kIn or kOut; waves: how many times the CTAs that run at once.
 template <bool kIn, typename Params>
-int launch_few_half(void (*fn)(Params), int threads, const Params& in, cudaStream_t s) {
-  constexpr int64_t kWaveWork = 1 << 23;
+int launch_few_half(void (*fn)(Params), int threads, const Params& in, int waves, cudaStream_t s) {
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(fn), kFewSmem) != EP_OK) return EP_ERR_CUDA;
-  int grid = ep_host::grid_cap(1);
+  const int grid = ep_host::grid_cap(1);
   Params p = in;
   p.wave = grid;
-  // SMs get through the same bytes up to a sixth faster or slower than the mean, which a call of some hundred
-  // microseconds pays for at its end: more CTAs with a few columns, which come up where others have left (a batch
-  // of 32 on E4M3 weights: 896 us in one wave, 824 so, where calls of 180 us and less gained nothing).
-  if (kIn && !ep_host::sm_budget_set() && (int64_t)p.T * p.k * p.N * p.K >= kWaveWork * grid) grid *= 3;
   if (!kIn && ep_host::sm_budget_set()) {   // the second kernel's CTAs do not come up beside the first's
     fn<<<grid, threads, kFewSmem, s>>>(p);
-  } else if (ep_host::launch_dependent<Params>(fn, grid, threads, kFewSmem, s, p) != EP_OK) {
+  } else if (ep_host::launch_dependent<Params>(fn, grid * waves, threads, kFewSmem, s, p) != EP_OK) {
     return EP_ERR_CUDA;
   }
   ep_host::count_launch();

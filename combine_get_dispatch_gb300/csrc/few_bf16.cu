@@ -275,8 +275,8 @@ int launch_few_bf16(const FewCall& in, const FewCall& out, const void* w_gu, con
   };
   if (maps(p, w_gu, 2 * in.E, kRowUnit / 2) != EP_OK || maps(q, w_down, in.E, kRowUnit) != EP_OK) return EP_ERR_CUDA;
   auto* fn = act == EP_ACT_RELU ? k_few_bf16<true, EP_ACT_RELU> : act == EP_ACT_SILU ? k_few_bf16<true, EP_ACT_SILU> : k_few_bf16<true, EP_ACT_GELU>;
-  const int rc = launch_few_half<true>(fn, kRowThreads, p, s);
-  return rc != EP_OK ? rc : launch_few_half<false>(k_few_bf16<false, EP_ACT_NONE>, kRowThreads, q, s);
+  const int rc = launch_few_half<true>(fn, kRowThreads, p, 1, s);
+  return rc != EP_OK ? rc : launch_few_half<false>(k_few_bf16<false, EP_ACT_NONE>, kRowThreads, q, 1, s);
 }
 
 }  // namespace ep

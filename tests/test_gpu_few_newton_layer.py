@@ -136,11 +136,11 @@ def test_two_graphs_share_workspaces():
         assert torch.equal(w, w2) and torch.equal(s["w"], s2["w"]) and torch.equal(s["m"], s2["m"])
 
 
-@pytest.mark.parametrize("kind,H,I", [("bf16", 2568, 2056), ("e4m3", 2560, 2176)])
-def test_large_calls(kind, H, I):
-    """Calls large enough for more CTAs than run at once; with an SM budget they are not, and give the same."""
+@pytest.mark.parametrize("kind,E,H,I", [("bf16", 20, 2568, 2056), ("e4m3", 52, 2560, 2176)])
+def test_large_calls(kind, E, H, I):
+    """E4M3: large enough for more CTAs than run at once; with an SM budget they are not, and give the same."""
     from test_gpu_few import call, check, make
-    s = make(11, 1, 32, 8, 20, H, I, kind)
+    s = make(11, 1, 32, 8, E, H, I, kind)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     out = call(s, "silu", status=status)
     check(s, "silu", out)
