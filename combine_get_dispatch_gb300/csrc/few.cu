@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
   Walk w(l.used, sh.counts.n_used, p.N, p.wave);
   // a stage: weights, tokens for the products, tokens as they came.  Products read 64
   // rows; what W_down's units have no rows for is other stages' memory, or the lists'.
-  const int weight_bytes = kIn ? kWeightBytes : (w.most + 7) / 8 * kGroupBytes;
+  const int weight_bytes = kIn ? kWeightBytes : (max(w.most, 1) + 7) / 8 * kGroupBytes;
   const int token_block = columns * 128, stage_bytes = (weight_bytes + kBlocks * token_block + tokens_most * kRawBytes + 1023) / 1024 * 1024;
   const int stages = max(1, min(kMaxFewStages, min((int)(lists_at - ring) / stage_bytes, ((int)(raw + kFewSmem - ring) - kWeightBytes) / stage_bytes + 1)));
   RingPosition at(stages);

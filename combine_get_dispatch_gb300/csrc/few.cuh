@@ -169,10 +169,11 @@ struct FewWalk {
     n_used = count;
     N = n;
     const uint32_t all = kIn ? (uint32_t)n_used * (n + kCrossing) : n_used > 0 ? n : 0;   // below 2^32
-    // of kIn's CTAs that come after the first wave, each takes an eighth of a first one's columns
+    // eight parts a CTA; one for each of kIn's CTAs that come after the first wave
     const uint32_t first = min(gridDim.x, wave), parts = 8 * first + (gridDim.x - first);
     const uint32_t b = blockIdx.x < first ? 8 * blockIdx.x : 7 * first + blockIdx.x, size = blockIdx.x < first ? 8 : 1;
-    const uint32_t each = all / parts, more = all - each * parts;   // the first `more` parts have one more
+    // the first `more` parts have one more: in one wave all shares are multiples of 8 columns, as copies of E4M3 weights are
+    const uint32_t each = all / parts, more = all - each * parts;
     const uint32_t at = each * b + min(b, more);
     left = (int)(each * size + min(b + size, more) - min(b, more));
     most = min(kIn ? kUnitRows / 2 : kUnitRows, left);
