@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
   constexpr int kBlock = 128, kChunk = kBlocks * kBlock;   // inner elements of a block, of a stage
   constexpr int kRawBytes = kChunk * 2;              // a token's row in a stage, as it comes
   using Lists = FewLists<kIn ? 0 : kUnitRows>;
-  using Walk = FewWalk<kIn, kPass, kUnitRows, 8>;
+  using Walk = FewWalk<kIn, kPass, kUnitRows>;
   extern __shared__ __align__(1024) uint8_t raw[];
   FewShared& sh = *reinterpret_cast<FewShared*>(raw);
   uint8_t* const ring = raw + (sizeof(FewShared) + 1023) / 1024 * 1024;

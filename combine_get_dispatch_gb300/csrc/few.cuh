@@ -155,7 +155,7 @@ __device__ __forceinline__ void few_lists(const FewCall& p, FewCounts& sh, const
 
 // A CTA's units, one after another: `cols` columns from `col` on of expert e, for
 // the tokens s0 .. s0 + m of the lists.
-template <bool kIn, int kPass, int kUnitRows, int kShare>
+template <bool kIn, int kPass, int kUnitRows>
 struct FewWalk {
   const FewUsed* used;
   int n_used;
@@ -169,11 +169,12 @@ struct FewWalk {
     n_used = count;
     N = n;
     const uint32_t all = kIn ? (uint32_t)n_used * (n + kCrossing) : n_used > 0 ? n : 0;   // below 2^32
-    // kShare parts a CTA; one for each of kIn's CTAs that come after the first wave
-    const uint32_t first = min(gridDim.x, wave), parts = kShare * first + (gridDim.x - first);
-    const uint32_t b = blockIdx.x < first ? kShare * blockIdx.x : (kShare - 1) * first + blockIdx.x, size = blockIdx.x < first ? kShare : 1;
-    // the first `more` parts have one more, so that in one wave shares are multiples of kShare columns, as copies are, but
-    // where widths are not (four tokens of 256 x 128, bf16: 10.8 us by single columns, 9.5 by 8, 9.1 by 16)
+    // 16 parts a CTA; two for each of kIn's CTAs that come after the first wave
+    const uint32_t first = min(gridDim.x, wave), parts = 16 * first + 2 * (gridDim.x - first);
+    const uint32_t b = blockIdx.x < first ? 16 * blockIdx.x : 14 * first + 2 * blockIdx.x, size = blockIdx.x < first ? 16 : 2;
+    // the first `more` parts have one more, so that in one wave shares are multiples of 16 columns, as copies are, but where
+    // widths are not (four tokens, 256 x 128, bf16: 10.8 us by single columns, 9.5 by 8, 9.2 by 16; 16 tokens, 2560 x 1536,
+    // E4M3: 81, 79, 79)
     const uint32_t each = all / parts, more = all - each * parts;
     const uint32_t at = each * b + min(b, more);
     left = (int)(each * size + min(b + size, more) - min(b, more));

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
   const int reds = stages_with(1) > stages_with(2) && stages_with(1) <= 4 ? 1 : 2, stages = stages_with(reds);
   uint8_t* const ring = red_base + reds * red_bytes;
   const int chunks = (p.K + kChunk - 1) / kChunk;
-  FewWalk<kIn, kRowPass, kRowUnit, 16> w(l.used, sh.counts.n_used, p.N, p.wave);
+  FewWalk<kIn, kRowPass, kRowUnit> w(l.used, sh.counts.n_used, p.N, p.wave);
   bool ok = true;
   RingPosition position(stages), at_red(reds);
 
