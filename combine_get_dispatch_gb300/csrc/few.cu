@@ -77,35 +77,56 @@ __device__ __forceinline__ uint32_t umma_few_idesc(int n) { return (1u << 4) | (
 // 2 j + 1 of the products.  bf16 has 8 significant bits and each part 4, so this is x
 // itself down to 2^-13 of the largest, and 2^-21 of the largest off below: no more
 // than sums in 32 bits lose.  A block with an infinity or NaN gets the scale NaN.
-// 8 elements a lane, a block sixteen lanes.  top: the largest as a bf16 number's bits, of a lane's elements, then of the block.
-__device__ __forceinline__ uint32_t top_bf16(uint4 v) {
-  uint32_t a = v.x & 0x7fff7fffu, b = v.y & 0x7fff7fffu;
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(v.z & 0x7fff7fffu));
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(v.w & 0x7fff7fffu));
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
-  return max(a >> 16, a & 0xffffu);
-}
-__device__ __forceinline__ void split_e4m3(uint4 v, uint32_t top, uint32_t (&hi)[2], uint32_t (&lo)[2], float& scale) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  const uint32_t e = top >> 7;   // biased; up = 2^(134 - e), no more than 2^127
-  const float up = __uint_as_float((e <= 7 ? 254u : 261u - min(e, 254u)) << 23);
-  scale = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(e <= 7 ? 0x00400000u : (e - 7) << 23);
+// An fp32 number (few_fine's h) is rounded so to about 2^-9 of itself.  8 elements a lane, a block sixteen lanes.
+template <bool kWide>
+struct TokenPiece {   // as it lies in memory: bf16 or fp32
+  uint4 v[kWide ? 2 : 1];
+
+  // the largest exponent, biased, or 255 with an infinity or NaN among them
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (kWide) {
+      uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t h[2], r[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float x = bf16_lo(w[2 * i + q]) * up, y = bf16_hi(w[2 * i + q]) * up;
-      h[q] = cvt_e4m3x2(x, y);
-      uint32_t back;
-      asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}" : "=r"(back) : "r"(h[q]));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-      r[q] = cvt_e4m3x2((x - f.x) * 16.0f, (y - f.y) * 16.0f);
+      for (int i = 0; i < 2; ++i) m = max(max(m, max(v[i].x & 0x7fffffffu, v[i].y & 0x7fffffffu)), max(v[i].z & 0x7fffffffu, v[i].w & 0x7fffffffu));
+      return m >> 23;
+    } else {
+      uint32_t a = v[0].x & 0x7fff7fffu, b = v[0].y & 0x7fff7fffu;
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(v[0].z & 0x7fff7fffu));
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(v[0].w & 0x7fff7fffu));
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      return max(a >> 16, a & 0xffffu) >> 7;
     }
-    hi[i] = __byte_perm(h[0], h[1], 0x5410);
-    lo[i] = __byte_perm(r[0], r[1], 0x5410);
   }
-}
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (kWide) {
+      const uint4 q = v[i >> 1];
+      return i & 1 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w)) : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    } else {
+      const uint32_t w = i == 0 ? v[0].x : i == 1 ? v[0].y : i == 2 ? v[0].z : v[0].w;
+      return make_float2(bf16_lo(w), bf16_hi(w));
+    }
+  }
+  __device__ __forceinline__ void split(uint32_t e, uint32_t (&hi)[2], uint32_t (&lo)[2], float& scale) const {
+    const float up = __uint_as_float((e <= 7 ? 254u : 261u - min(e, 254u)) << 23);   // 2^(134 - e), no more than 2^127
+    scale = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(e <= 7 ? 0x00400000u : (e - 7) << 23);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h[2], r[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float2 p = pair(2 * i + q);
+        const float x = p.x * up, y = p.y * up;
+        h[q] = cvt_e4m3x2(x, y);
+        uint32_t back;
+        asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}" : "=r"(back) : "r"(h[q]));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        r[q] = cvt_e4m3x2((x - f.x) * 16.0f, (y - f.y) * 16.0f);
+      }
+      hi[i] = __byte_perm(h[0], h[1], 0x5410);
+      lo[i] = __byte_perm(r[0], r[1], 0x5410);
+    }
+  }
+};
 
 __device__ __forceinline__ float ue8m0_value(uint32_t b) {
   return b == 255 ? __uint_as_float(0x7fc00000u) : b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
@@ -175,10 +196,11 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int team,
   }
 }
 
-template <bool kIn, int kAct>
+template <bool kIn, int kAct, bool kFine>
 __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_constant__ FewParams p) {
   constexpr int kBlock = 128, kChunk = kBlocks * kBlock;   // inner elements of a block, of a stage
-  constexpr int kRawBytes = kChunk * 2;              // a token's row in a stage, as it comes
+  constexpr bool kWide = !kIn && kFine;              // tokens' rows are fp32
+  constexpr int kRawBytes = kChunk * (kWide ? 4 : 2);   // a token's row in a stage, as it comes
   using Lists = FewLists<kIn ? 0 : kUnitRows>;
   using Walk = FewWalk<kIn, kPass, kUnitRows>;
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -276,9 +298,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
         named_barrier_sync(1, kQuarters * kWarp);
         if (quarter < kQuarters / 2 && there && column < w.cols) {
 #pragma unroll
-          for (int j = 0; j < kPass; ++j) {   // rounded to bf16: the second kernel's operand
+          for (int j = 0; j < kPass; ++j) {   // the second kernel's operand
             if (j >= w.m) break;
-            p.out[(int64_t)l.slot[w.s0 + j] * p.N + w.col + column] = __float2bfloat16_rn(act_value<kAct>(y[j]) * up[j][column]);
+            const float h = act_value<kAct>(y[j]) * up[j][column];
+            const int64_t to = (int64_t)l.slot[w.s0 + j] * p.N + w.col + column;
+            if (kFine)
+              reinterpret_cast<float*>(p.out)[to] = h;
+            else
+              p.out[to] = __float2bfloat16_rn(h);
           }
         }
       } else if (there) {
@@ -339,13 +366,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
     if (!kIn) pdl_wait();
     while (ok && w.next()) {
       const int from = mine < w.m ? (kIn ? l.token[w.s0 + mine] : l.slot[w.s0 + mine]) : -1;
-      const __nv_bfloat16* row = p.v + (int64_t)from * p.K;
+      const uint8_t* row = reinterpret_cast<const uint8_t*>(p.v) + (int64_t)from * p.K * (kRawBytes / kChunk);
       for (int c = 0; c < chunks; ++c) {
         ok = wait_few(&sh.empty[at.s], at.phase ^ 1);
         if (!ok) break;
         if (from >= 0)
-          tma_load_1d(ring + at.s * stage_bytes + weight_bytes + kBlocks * token_block + mine * kRawBytes, row + c * kChunk,
-                      min(kChunk, p.K - c * kChunk) * 2, &sh.full[at.s]);
+          tma_load_1d(ring + at.s * stage_bytes + weight_bytes + kBlocks * token_block + mine * kRawBytes, row + (int64_t)c * kRawBytes,
+                      min(kChunk, p.K - c * kChunk) * (kRawBytes / kChunk), &sh.full[at.s]);
         __syncwarp();
         at.advance();
       }
@@ -362,7 +389,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
         if (!ok) break;
         if (issue) {
           const int k = min(kChunk, p.K - c * kChunk);
-          if (turn == 0) mbar_arrive_expect_tx(&sh.full[at.s], (kIn ? 2 : 1) * groups * kGroupBytes + w.m * k * 2);
+          if (turn == 0) mbar_arrive_expect_tx(&sh.full[at.s], (kIn ? 2 : 1) * groups * kGroupBytes + w.m * k * (kRawBytes / kChunk));
           const uint32_t to = smem_addr(ring + at.s * stage_bytes), bar = smem_addr(&sh.full[at.s]);
           for (int half = 0; half < (kIn ? 2 : 1); ++half) {
             const int z = kIn ? 2 * w.e + half : w.e;
@@ -394,17 +421,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
           constexpr int kItems = decltype(items)::value;
           for (int i0 = member; i0 < 2 * w.m; i0 += kTeam * kItems) {
             const int piece = lane & 15;
-            uint4 v[kItems];
+            TokenPiece<kWide> v[kItems];
             uint32_t top[kItems];
             bool in[kItems];
 #pragma unroll
             for (int u = 0; u < kItems; ++u) {
               const int i = i0 + u * kTeam, b = (i & 1) * 2 + (lane >> 4);
               in[u] = i < 2 * w.m && b * kBlock < left;
-              v[u] = in[u] ? ld_shared_v4_at(from + (i >> 1) * kRawBytes + (b * kBlock + piece * 8) * 2) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int h = 0; h < (kWide ? 2 : 1); ++h)
+                v[u].v[h] = in[u] ? ld_shared_v4_at(from + (i >> 1) * kRawBytes + (b * kBlock + piece * 8) * (kRawBytes / kChunk) + h * 16) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int u = 0; u < kItems; ++u) top[u] = top_bf16(v[u]);
+            for (int u = 0; u < kItems; ++u) top[u] = v[u].top();
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1)
 #pragma unroll
@@ -414,7 +443,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
               const int i = i0 + u * kTeam, j = i >> 1, b = (i & 1) * 2 + (lane >> 4);
               uint32_t hi[2], lo[2];
               float scale;
-              split_e4m3(v[u], top[u], hi, lo, scale);
+              v[u].split(top[u], hi, lo, scale);
               if (in[u]) {
                 const uint32_t row = to + b * token_block + 2 * j * 128, at_hi = row + ((((piece >> 1) ^ (2 * j & 7)) << 4) | ((piece & 1) << 3));
                 const uint32_t at_lo = row + 128 + ((((piece >> 1) ^ ((2 * j + 1) & 7)) << 4) | ((piece & 1) << 3));
@@ -456,7 +485,6 @@ static int launch_few_e4m3(const FewCall& in, const FewCall& out, const void* w_
     return ep_host::make_map(&f.w, true, 4, w, dims, strides, box);
   };
   if (map(p, w_gu, 2 * (uint64_t)in.E) != EP_OK || map(q, w_down, in.E) != EP_OK) return EP_ERR_CUDA;
-  auto* fn = act == EP_ACT_RELU ? k_few_e4m3<true, EP_ACT_RELU> : act == EP_ACT_SILU ? k_few_e4m3<true, EP_ACT_SILU> : k_few_e4m3<true, EP_ACT_GELU>;
   // SMs get through the same work up to a sixth faster or slower than the mean, which a large call
   // pays for at its end: more CTAs with a few columns, which come up where others have left.  0.47 GB of gate and
   // up take 88 us in one wave and 98 so, 0.70 GB 255 and 232, 3.8 GB 842 and 763 (with W_down).  bf16: 0.7 GB 3 % slower
@@ -464,8 +492,15 @@ static int launch_few_e4m3(const FewCall& in, const FewCall& out, const void* w_
   constexpr int64_t kWaveBytes = (int64_t)1 << 29;   // of gate and up, if every slot has its own expert
   const int64_t bytes = 2 * (int64_t)std::min(p.T * p.k, p.E) * p.N * p.K;
   const int waves = bytes >= kWaveBytes && !ep_host::sm_budget_set() ? 3 : 1;
-  const int rc = launch_few_half<true>(fn, kFewThreads, p, waves, s);
-  return rc != EP_OK ? rc : launch_few_half<false>(k_few_e4m3<false, EP_ACT_NONE>, kFewThreads, q, 1, s);
+  auto go = [&](auto fine) {
+    constexpr bool kFine = decltype(fine)::value;
+    auto* fn = act == EP_ACT_RELU   ? k_few_e4m3<true, EP_ACT_RELU, kFine>
+               : act == EP_ACT_SILU ? k_few_e4m3<true, EP_ACT_SILU, kFine>
+                                    : k_few_e4m3<true, EP_ACT_GELU, kFine>;
+    const int rc = launch_few_half<true>(fn, kFewThreads, p, waves, s);
+    return rc != EP_OK ? rc : launch_few_half<false>(k_few_e4m3<false, EP_ACT_NONE, kFine>, kFewThreads, q, 1, s);
+  };
+  return few_fine(in.T) ? go(std::true_type()) : go(std::false_type());
 }
 
 static bool few_sizes(int R, int T_r, int k, int E, int I) {
@@ -477,7 +512,8 @@ static bool few_sizes(int R, int T_r, int k, int E, int I) {
 
 extern "C" size_t ep_moe_few_workspace_size(int R, int T_r, int k, int E, int I) {
   if (!ep::few_sizes(R, T_r, k, E, I)) return 0;
-  return std::max<size_t>(16, ((size_t)R * T_r * k * I * 2 + 15) / 16 * 16);
+  static_assert(2 * ep::kFineTokens >= EP_MOE_FEW_TOKENS);   // enough for more tokens too, and for fewer than asked for
+  return std::max<size_t>(16, ((size_t)std::min(R * T_r, ep::kFineTokens) * k * I * 4 + 15) / 16 * 16);
 }
 
 extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* topk_weights, const void* w_gu,

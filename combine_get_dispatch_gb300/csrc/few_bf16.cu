@@ -12,6 +12,8 @@
 // product: one token through six experts of 4096 x 1416
 // 49 us instead of 40, 18 tokens through 32 of them 176 instead of 150, 64 through eight of 4096 x 2048 92 instead of 88.
 
+#include <type_traits>
+
 #include "few.cuh"
 
 namespace ep {
@@ -24,7 +26,7 @@ constexpr int kPiece = 1024;          // bytes of a weight row in a stage
 constexpr int kChunk = kPiece / 2;    // inner elements of a stage
 constexpr int kRowUnit = 32;          // rows of a unit
 constexpr int kRedPitch = 36;         // floats: a warp's sums fall into distinct banks
-constexpr int kRowPass = 24;          // tokens of an expert taken at a time: two stages at least
+__host__ __device__ constexpr int row_pass(bool two) { return two ? 16 : 24; }   // tokens of an expert taken at a time: two stages at least
 constexpr int kRowStages = 8;
 constexpr int kTokenPitch = kPiece + 64;   // 8 lanes' 16 bytes fall into distinct banks
 
@@ -44,11 +46,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A warp's eighth of a unit: 32 rows, 8 G tokens.
+// A warp's eighth of a unit: 32 rows, 8 G columns: of tokens, or (kFine) of the two words of each, whose
+// sums come together at the end: the second words lie 4 columns on where all fit 8 (G = 1), else G / 2 times 8.
 // Nothing in here branches on what the unit holds (what lies where no row or token
 // does is multiplied and not used): with branches around its loads a stage took
 // 1500 clocks, most of them waiting for one load after the other.
-template <bool kIn, int G>
+template <bool kIn, bool kFine, int G>
 __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t* ring, int stage_bytes, float* red, int chunks,
                                              RingPosition& at_red, RingPosition& at_stage, bool& ok) {
   constexpr int kStep = 32;   // inner elements a warp multiplies at a time: 16 bytes of weights a lane
@@ -96,11 +99,20 @@ __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t
     if (lane == 0) mbar_arrive(&sh.empty[at_stage.s]);
     at_stage.advance();
   }
+  constexpr int kSums = kFine && G > 1 ? G / 2 : G;
+  if constexpr (kFine) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < kSums; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[h][j][i] += G == 1 ? __shfl_xor_sync(0xffffffffu, acc[h][j][i], 2) : acc[h][j + G / 2][i];
+  }
   if (ok) ok = wait_few(&sh.red_empty[at_red.s], at_red.phase ^ 1);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int j = 0; j < G; ++j)
+    for (int j = 0; j < kSums; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[(j * 8 + 2 * t + (i & 1)) * kRedPitch + h * 16 + (i >> 1) * 8 + g] = acc[h][j][i];
   __syncwarp();
@@ -108,7 +120,7 @@ __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t
   at_red.advance();
 }
 
-template <bool kIn, int kAct>
+template <bool kIn, int kAct, bool kFine>
 __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_constant__ RowParams p) {
   using Lists = FewLists<kIn ? 0 : kRowUnit>;
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -138,18 +150,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
   }
   const Lists l(lists_at, p.E, p.T, p.k);
   few_lists<kRowThreads>(p, sh.counts, l, reinterpret_cast<uint32_t*>(red_base), kIn && blockIdx.x == 0);
-  const int tokens_most = min(sh.counts.most, kRowPass);
+  constexpr bool kTwo = !kIn && kFine;   // token rows of a stage: two for each, as few_products wants them
+  constexpr int kPass = row_pass(kTwo);
+  const int tokens_most = min(sh.counts.most, kPass);
+  const int rows_most = !kTwo ? tokens_most : tokens_most <= 4 ? 8 : (tokens_most + 7) / 8 * 16;
   const int red_part = (tokens_most + 7) / 8 * 8 * kRedPitch;         // floats of one part's sums
   const int red_bytes = kParts * red_part * 4;                        // of one unit
-  const int stage_bytes = kRowUnit * kPiece + (tokens_most * kTokenPitch + 127) / 128 * 128;
+  const int stage_bytes = kRowUnit * kPiece + (rows_most * kTokenPitch + 127) / 128 * 128;
   // products read 8 tokens' rows, there or not: some may lie behind the last stage
-  const int behind = ((tokens_most + 7) / 8 * 8 - tokens_most) * kTokenPitch;
+  const int behind = kTwo ? 0 : ((tokens_most + 7) / 8 * 8 - tokens_most) * kTokenPitch;
   auto stages_with = [&](int reds) { return min(kRowStages, ((int)(lists_at - red_base) - reds * red_bytes - behind) / stage_bytes); };
   // two units' sums, or one's where that makes a third or fourth stage (64 tokens over eight experts: 87 us with three, 76 so)
   const int reds = stages_with(1) > stages_with(2) && stages_with(1) <= 4 ? 1 : 2, stages = stages_with(reds);
   uint8_t* const ring = red_base + reds * red_bytes;
   const int chunks = (p.K + kChunk - 1) / kChunk;
-  FewWalk<kIn, kRowPass, kRowUnit> w(l.used, sh.counts.n_used, p.N, p.wave);
+  FewWalk<kIn, kPass, kRowUnit> w(l.used, sh.counts.n_used, p.N, p.wave);
   bool ok = true;
   RingPosition position(stages), at_red(reds);
 
@@ -157,12 +172,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
     // ---------------------------------------------------------------- products
     while (w.next()) {
       float* const red = reinterpret_cast<float*>(red_base + at_red.s * red_bytes) + warp * red_part;
-      if (w.m <= 8)
-        few_products<kIn, 1>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok);
+      auto products = [&](auto g) { few_products<kIn, kTwo, decltype(g)::value>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok); };
+      using std::integral_constant;
+      if (kTwo && w.m <= 4)
+        products(integral_constant<int, 1>());
+      else if (w.m <= 8)
+        products(integral_constant<int, kTwo ? 2 : 1>());
       else if (w.m <= 16)
-        few_products<kIn, 2>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok);
-      else
-        few_products<kIn, kRowPass / 8>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok);
+        products(integral_constant<int, kTwo ? 4 : 2>());
+      else if constexpr (!kTwo)
+        products(integral_constant<int, kPass / 8>());
     }
   } else if (warp < kParts + kAdders) {
     // ---------------------------------------------------------------- sums
@@ -182,8 +201,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
       if (kIn) {
         const int c = lane & 15, row = (c >> 3) * 16 + (c & 7);
         for (int n = q * 2 + (lane >> 4); n < w.m; n += 2 * kAdders)
-          if (c < w.cols)   // rounded to bf16: the second kernel's operand
-            p.out[(int64_t)l.slot[w.s0 + n] * p.N + w.col + c] = __float2bfloat16_rn(act_value<kAct>(total(n, row)) * total(n, row + 8));
+          if (c < w.cols) {
+            const float h = act_value<kAct>(total(n, row)) * total(n, row + 8);
+            const __nv_bfloat16 hi = __float2bfloat16_rn(h);   // the second kernel's operand
+            __nv_bfloat16* const to = p.out + (int64_t)l.slot[w.s0 + n] * (kFine ? 2 : 1) * p.N + w.col + c;
+            to[0] = hi;
+            if (kFine) to[p.N] = __float2bfloat16_rn(isfinite(__bfloat162float(hi)) ? h - __bfloat162float(hi) : 0.0f);
+          }
       } else {
         // a token is one warp's, so its slots are added in the lists' order
         for (int n = 0; n < w.m; ++n) {
@@ -220,7 +244,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
         if (!ok) break;
         if (issue) {
           const int k = min(kChunk, p.K - c * kChunk);
-          mbar_arrive_expect_tx(&sh.full[position.s], (kIn ? 2 : 1) * w.cols * kPiece + w.m * k * 2);
+          mbar_arrive_expect_tx(&sh.full[position.s], (kIn ? 2 : 1) * w.cols * kPiece + (kTwo ? 2 : 1) * w.m * k * 2);
           const uint32_t bar = smem_addr(&sh.full[position.s]);
           constexpr int kWhole = kIn ? kRowUnit / 2 : kRowUnit;
           for (int half = 0; half < (kIn ? 2 : 1); ++half) {
@@ -244,14 +268,15 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
     const int turn = warp - (kParts + kAdders + 1);
     if (!kIn) pdl_wait();
     while (ok && w.next()) {   // a row a lane
-      const int mine = lane * kTokenWarps + turn;
-      const int from = mine < w.m ? (kIn ? l.token[w.s0 + mine] : l.slot[w.s0 + mine]) : -1;
+      const int mine = lane * kTokenWarps + turn, word = kTwo && mine >= w.m ? 1 : 0, n = mine - word * w.m;
+      const int from = n < w.m ? (kIn ? l.token[w.s0 + n] : l.slot[w.s0 + n] * (kTwo ? 2 : 1) + word) : -1;
+      const int place = n + word * (w.m <= 4 ? 4 : (w.m + 7) / 8 * 8);
       const __nv_bfloat16* row = p.v + (int64_t)from * p.K;
       for (int c = 0; c < chunks; ++c) {
         ok = wait_few(&sh.empty[position.s], position.phase ^ 1);
         if (!ok) break;
         if (from >= 0)
-          tma_load_1d(ring + position.s * stage_bytes + kRowUnit * kPiece + mine * kTokenPitch, row + c * kChunk, min(kChunk, p.K - c * kChunk) * 2, &sh.full[position.s]);
+          tma_load_1d(ring + position.s * stage_bytes + kRowUnit * kPiece + place * kTokenPitch, row + c * kChunk, min(kChunk, p.K - c * kChunk) * 2, &sh.full[position.s]);
         __syncwarp();
         position.advance();
       }
@@ -274,9 +299,15 @@ int launch_few_bf16(const FewCall& in, const FewCall& out, const void* w_gu, con
     return rc == EP_OK ? ep_host::make_row_map(&f.one, w, words, f.N, count, 1) : rc;
   };
   if (maps(p, w_gu, 2 * in.E, kRowUnit / 2) != EP_OK || maps(q, w_down, in.E, kRowUnit) != EP_OK) return EP_ERR_CUDA;
-  auto* fn = act == EP_ACT_RELU ? k_few_bf16<true, EP_ACT_RELU> : act == EP_ACT_SILU ? k_few_bf16<true, EP_ACT_SILU> : k_few_bf16<true, EP_ACT_GELU>;
-  const int rc = launch_few_half<true>(fn, kRowThreads, p, 1, s);
-  return rc != EP_OK ? rc : launch_few_half<false>(k_few_bf16<false, EP_ACT_NONE>, kRowThreads, q, 1, s);
+  auto go = [&](auto fine) {
+    constexpr bool kFine = decltype(fine)::value;
+    auto* fn = act == EP_ACT_RELU   ? k_few_bf16<true, EP_ACT_RELU, kFine>
+               : act == EP_ACT_SILU ? k_few_bf16<true, EP_ACT_SILU, kFine>
+                                    : k_few_bf16<true, EP_ACT_GELU, kFine>;
+    const int rc = launch_few_half<true>(fn, kRowThreads, p, 1, s);
+    return rc != EP_OK ? rc : launch_few_half<false>(k_few_bf16<false, EP_ACT_NONE, kFine>, kRowThreads, q, 1, s);
+  };
+  return few_fine(in.T) ? go(std::true_type()) : go(std::false_type());
 }
 
 }  // namespace ep

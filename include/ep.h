@@ -456,20 +456,22 @@ int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, co
  *   w_gu         [E, 2, I, H] (gate, then up), w_down [E, H, I]: bf16
  *                (EP_FP8_NONE, scales NULL), or E4M3 with one ue8m0 byte per
  *                128 x 128 block (EP_FP8_E4M3_UE8M0; scales [E, 2, I/128, H/128]
- *                and [E, H/128, I/128]; scale byte 255 is NaN).  x and h stay
- *                bf16 either way.  With E4M3 weights a token's 128 numbers under
- *                one scale are multiplied as the sum of two E4M3 parts each:
- *                exact down to 2^-13 of the largest of them, at most 2^-21 of the
- *                largest off below; with an infinity or NaN among them the token's
- *                outputs are NaN.
+ *                and [E, H/128, I/128]; scale byte 255 is NaN).  With E4M3
+ *                weights a token's 128 bf16 numbers under one scale are
+ *                multiplied as the sum of two E4M3 parts each: exact down to
+ *                2^-13 of the largest of them, at most 2^-21 of the largest off
+ *                below; with an infinity or NaN among them the token's outputs
+ *                are NaN.
  *   out          [R, T_r, H] bf16; may be x itself
  *   workspace    ep_moe_few_workspace_size bytes, 16-byte aligned, no
  *                initialisation; calls that share one must be ordered
  * Sums run in 32 bits in an order that neither the SM budget nor the batch's
- * other tokens change (over the slots: by expert, then by slot); h and out are
- * rounded to bf16 once each.  Ids outside [-1, E) set EP_ERR_INVALID_ARG in
- * *status and count as unused; a wait that runs out sets EP_ERR_TIMEOUT and
- * leaves outputs incomplete.  Limits: H, I multiples of 8 (128 with E4M3), at most
+ * other tokens change (over the slots: by expert, then by slot); out is rounded to
+ * bf16.  Up to 32 tokens (R * T_r) h keeps 16 significant bits (bf16 weights; an
+ * infinity among W_down's may then come out as NaN) or 9 (E4M3), so that out is as
+ * exact as its rounding; with more tokens h is rounded to bf16.  Ids outside [-1, E)
+ * set EP_ERR_INVALID_ARG in *status and count as unused; a wait that runs out sets
+ * EP_ERR_TIMEOUT and leaves outputs incomplete.  Limits: H, I multiples of 8 (128 with E4M3), at most
  * 2^24, E * H and E * (I + 16) below 2^31, act as for ep_expert_glu.  All pointers
  * but the ids, weights and scales 16-byte aligned. */
 #define EP_MOE_FEW_TOKENS 64

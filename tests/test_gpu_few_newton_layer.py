@@ -183,3 +183,51 @@ def test_a_matrix_comes_out_as_it_does_alone(shape, count):
     out = call(g, [QUINTIC] * 4)
     for z in (0, count // 2, count - 1):
         assert torch.equal(call(g[z:z + 1].contiguous(), [QUINTIC] * 4)[0], out[z])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("R,T_r,k,E,H,I", [(1, 1, 8, 16, 1024, 512), (1, 4, 2, 16, 256, 128), (2, 16, 2, 4, 384, 256), (1, 32, 1, 1, 512, 640), (1, 9, 4, 6, 128, 2176)])
+def test_h_is_kept_for_few_tokens(kind, R, T_r, k, E, H, I):
+    """Up to 32 tokens the output is off by its own rounding (2^-8 of itself), by sums in 32 bits (2^-23 a product of the
+    magnitudes) and by h's: two bf16 words are off by 2^-16 of it, two E4M3 parts by 2^-9 and, where they run out of
+    exponents, 2^-21 of the largest; the same 2^-21 holds for x; the activation is off by 2^-16."""
+    from test_gpu_few import act64, call, make, wide
+    s = make(R + T_r + H, R, T_r, k, E, H, I, kind)
+    x, idx, weights = s["x"].double().reshape(-1, H), s["idx"].reshape(R * T_r, -1), s["weights"].double().reshape(R * T_r, -1)
+    out, off = torch.zeros_like(x), torch.zeros_like(x)
+    part, low = (2.0 ** -16, 0.0) if kind == "bf16" else (2.0 ** -9, 2.0 ** -21)
+    for e in range(E):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        gu, down = wide(s["w_gu"], s["gu_scales"], e), wide(s["w_down"], s["down_scales"], e)
+        gate, up = x[t] @ gu[0].t(), x[t] @ gu[1].t()
+        a = act64(gate, "silu")
+        h = a * up
+        dx = low * x[t].abs().amax(-1, keepdim=True) + H * 2.0 ** -23 * x[t].abs()
+        dg, du = dx @ gu[0].abs().t(), dx @ gu[1].abs().t()
+        dh = (part + 2.0 ** -16) * h.abs() + 1.13 * dg * up.abs() + a.abs() * du + 1.13 * dg * du
+        if h.numel():
+            dh = dh + low * h.abs().amax(-1, keepdim=True)
+        w = weights[t, j].unsqueeze(1)
+        out.index_add_(0, t, w * (h @ down.t()))
+        off.index_add_(0, t, w.abs() * (dh @ down.abs().t() + (I + 16) * 2.0 ** -23 * (h.abs() @ down.abs().t())))
+    d = (call(s, "silu").double().reshape(-1, H) - out).abs()
+    bound = 1.004 * off + 2.0 ** -8 * out.abs() + 1e-30
+    assert bool((d <= bound).all()), f"{float((d / bound).max())} of the bound"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_one_expert_takes_every_token(kind):
+    """More tokens an expert than are taken at a time, on either side of 32 tokens."""
+    from test_gpu_few import call, check, make
+    for T in (16, 17, 24, 31, 32, 33, 48, 64):
+        s = make(T, 1, T, 2, 2, 256, 384, kind)
+        check(s, "gelu", call(s, "gelu"))
+
+
+def test_a_workspace_for_more_tokens_serves_fewer():
+    from test_gpu_few import call, make
+    sizes = [ep.ep_moe_few_workspace_size(1, T, 2, 8, 72) for T in range(65)]
+    assert sizes == sorted(sizes)
+    ws = ep.alloc_moe_few_workspace(1, 40, 2, 8, 72)
+    s = make(3, 1, 32, 2, 8, 64, 72, "bf16")
+    assert torch.equal(call(s, "silu", workspace=ws), call(s, "silu"))
