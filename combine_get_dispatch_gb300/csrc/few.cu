@@ -14,7 +14,7 @@
 // rows of W_down.  The weights' rows are the first operand (64
 // of them, those past the unit's being whatever lies there), the tokens, split into two E4M3 numbers each,
 // the second, 8 to 32 columns, and no thread touches a weight: by mma.sync they had to be turned into fp16 first,
-// which took a batch of 32 (128 experts, 7168 x 2048, top-8) 1129 us instead of 776.  bf16 weights need no turning, and
+// which took a batch of 32 (128 experts, 7168 x 2048, top-8) 1129 us instead of 767.  bf16 weights need no turning, and
 // their rows, of any multiple of 16 bytes, come in 1 KB pieces where this form wants 128-byte ones: few_bf16.cu.
 // Warps:
 //   8 bring the sums out of tensor memory, in two teams, a stage each; the first finishes a unit
