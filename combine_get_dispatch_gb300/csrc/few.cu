@@ -209,9 +209,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
   uint8_t* const lists_at = raw + kFewSmem - Lists::bytes(p.E, p.T, p.k);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    // Everybody who waits for a phase of a barrier takes part in the slot's next one, so that nobody can be left a whole
+    // turn of the ring behind: weights' warps without a copy of the stage, and the team of the other stages, arrive too.
     for (int s = 0; s < kMaxFewStages; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.turned[s], kTeam);
+      mbar_init(&sh.full[s], kWeightWarps);
+      mbar_init(&sh.turned[s], kTurners);
       mbar_init(&sh.empty[s], 1);
     }
     for (int b = 0; b < kSums; ++b) {
@@ -389,7 +391,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
         if (!ok) break;
         if (issue) {
           const int k = min(kChunk, p.K - c * kChunk);
-          if (turn == 0) mbar_arrive_expect_tx(&sh.full[at.s], (kIn ? 2 : 1) * groups * kGroupBytes + w.m * k * (kRawBytes / kChunk));
+          if (turn == 0)
+            mbar_arrive_expect_tx(&sh.full[at.s], (kIn ? 2 : 1) * groups * kGroupBytes + w.m * k * (kRawBytes / kChunk));
+          else
+            mbar_arrive(&sh.full[at.s]);
           const uint32_t to = smem_addr(ring + at.s * stage_bytes), bar = smem_addr(&sh.full[at.s]);
           for (int half = 0; half < (kIn ? 2 : 1); ++half) {
             const int z = kIn ? 2 * w.e + half : w.e;
@@ -409,9 +414,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
     uint32_t stage = 0;
     while (w.next()) {
       for (int c = 0; c < chunks; ++c, ++stage, at.advance()) {
-        // every stage is waited for, another team's too: they may land out of order, and a wait two phases ahead passes
+        // every stage is waited for, another team's too: they may land out of order, and a wait two phases ahead passes;
+        // and the products wait until both teams have seen it, or the slot could be filled anew before this team looks
         if (ok) ok = wait_few(&sh.full[at.s], at.phase);
-        if (stage % kTeams != (uint32_t)team) continue;
+        if (stage % kTeams != (uint32_t)team) {
+          if (lane == 0) mbar_arrive(&sh.turned[at.s]);
+          continue;
+        }
         const uint32_t to = smem_addr(ring + at.s * stage_bytes + weight_bytes), from = to + kBlocks * token_block;
         const int left = p.K - c * kChunk;
         // an item is two blocks of a token, a lane's 8 elements of one: several at a time, each step of all before the next

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRowStages; ++s) {
-      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.full[s], 1 + kTokenWarps);   // a token warp without a row of the stage arrives too, or could be left a turn of the ring behind
       mbar_init(&sh.empty[s], kParts);
     }
     for (int b = 0; b < 2; ++b) {
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
         if (from >= 0)
           tma_load_1d(ring + position.s * stage_bytes + kRowUnit * kPiece + place * kTokenPitch, row + c * kChunk, min(kChunk, p.K - c * kChunk) * 2, &sh.full[position.s]);
         __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[position.s]);
         position.advance();
       }
     }
