@@ -357,5 +357,13 @@ inline int launch_dependent(void (*kernel)(P), dim3 grid, int threads, int smem,
   }
   return EP_OK;
 }
+// The same, but under an SM budget only once that kernel has left: a grid that comes up
+// while the one before it still runs does so on other SMs.
+template <typename P>
+inline int launch_in_budget(void (*kernel)(P), int grid, int threads, int smem, cudaStream_t stream, const P& params) {
+  if (!sm_budget_set()) return launch_dependent<P>(kernel, grid, threads, smem, stream, params);
+  kernel<<<grid, threads, smem, stream>>>(params);
+  return check_launch();
+}
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 }  // namespace ep_host

@@ -260,11 +260,7 @@ int launch_few_half(void (*fn)(Params), int threads, const Params& in, int waves
   const int grid = ep_host::grid_cap(1);
   Params p = in;
   p.wave = grid;
-  if (!kIn && ep_host::sm_budget_set()) {   // the second kernel's CTAs do not come up beside the first's
-    fn<<<grid, threads, kFewSmem, s>>>(p);
-  } else if (ep_host::launch_dependent<Params>(fn, grid * waves, threads, kFewSmem, s, p) != EP_OK) {
-    return EP_ERR_CUDA;
-  }
+  if (ep_host::launch_in_budget<Params>(fn, grid * waves, threads, kFewSmem, s, p) != EP_OK) return EP_ERR_CUDA;
   ep_host::count_launch();
   return ep_host::check_launch();
 }

@@ -46,7 +46,7 @@ template <bool kF32, bool kMomentum>
 __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
   __shared__ float warps[kSourceThreads / kWarp];
   pdl_wait();
-  pdl_launch_dependents();
+  if (s.early) pdl_launch_dependents();
   for (int64_t item = blockIdx.x; item < (int64_t)s.count * s.parts; item += gridDim.x) {
     const int64_t z = item / s.parts, begin = (item - z * s.parts) * s.part, end = min(begin + s.part, s.each), base = z * s.each;
     float sum[kAhead] = {};
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
 // cache, which may hold what it was.
 template <bool kF32, bool kMomentum>
 __global__ void __launch_bounds__(kSourceThreads) k_newton_scale(Source s) {
-  pdl_launch_dependents();
+  if (s.early) pdl_launch_dependents();
   pdl_wait();
   const int64_t items = (int64_t)s.count * s.parts;
   for (int64_t at = blockIdx.x; at < items; at += gridDim.x) {
@@ -189,6 +189,7 @@ struct NewtonParams {
   bool rows_fast;
   bool backward;                // the last matrix first
   bool a_mn, b_mn;
+  bool early;                   // as Source's
   float scale, add;             // epilogue: scale * sums + (add + diagonal_scale * diagonal) * in
   float diagonal_scale;
   const float* factor;          // [count] or nullptr
@@ -305,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     t += pairs;
     more = next(t, tile);
   };
-  pdl_launch_dependents();
+  if (p.early) pdl_launch_dependents();
   pdl_wait();
   if (warp == 0 || warp == 3) {
     // ---------------------------------------------------------------- copies, a warp an operand
@@ -643,7 +644,7 @@ static int launch_newton(NewtonParams& p, cudaStream_t s) {
   constexpr int kSmem = kNewtonStages * kNewtonStage + kNewtonWarps * kWarpBytes + (int)sizeof(NewtonShared);
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(p.tiles, ep_host::grid_cap(1) / 2));
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(k_newton<kForm>), kSmem) != EP_OK) return EP_ERR_CUDA;
-  if (ep_host::launch_dependent(k_newton<kForm>, (int)pairs * 2, kNewtonThreads, kSmem, s, p) != EP_OK) return EP_ERR_CUDA;
+  if (ep_host::launch_in_budget(k_newton<kForm>, (int)pairs * 2, kNewtonThreads, kSmem, s, p) != EP_OK) return EP_ERR_CUDA;
   ep_host::count_launch();
   return ep_host::check_launch();
 }
@@ -686,6 +687,7 @@ struct Newton {
     p.cols = cols;
     p.inner = inner;
     p.status = status;
+    p.early = !ep_host::sm_budget_set();
     tiles(p, sym);
     return p;
   }
@@ -755,6 +757,7 @@ struct Newton {
 static int newton(Source src, int count, int M, int N, int steps, const float* abc, float eps, __nv_bfloat16* out, float* w,
                   __nv_bfloat16* w16, float keep, float step, void* workspace, int32_t* status, cudaStream_t s) {
   src.eps = eps;
+  src.early = !ep_host::sm_budget_set();
   if (std::min(M, N) <= kSmallSide && std::max(M, N) <= kSmallLength) {
     SmallNewton p{};
     p.src = src;
@@ -789,7 +792,7 @@ static int newton(Source src, int count, int M, int N, int steps, const float* a
   auto* norm = src.m != nullptr ? (src.f32 ? k_newton_norm<true, true> : k_newton_norm<false, true>) : src.f32 ? k_newton_norm<true, false> : k_newton_norm<false, false>;
   auto* scale = src.m != nullptr ? (src.f32 ? k_newton_scale<true, true> : k_newton_scale<false, true>) : src.f32 ? k_newton_scale<true, false> : k_newton_scale<false, false>;
   for (auto* kernel : {norm, scale}) {
-    if (ep_host::launch_dependent(kernel, grid, kSourceThreads, 0, s, src) != EP_OK) return EP_ERR_CUDA;
+    if (ep_host::launch_in_budget(kernel, grid, kSourceThreads, 0, s, src) != EP_OK) return EP_ERR_CUDA;
     ep_host::count_launch();
   }
   for (int t = 0; t < steps; ++t) {

@@ -17,6 +17,7 @@ struct Source {
   int64_t each;           // elements of a matrix, a multiple of 8
   int64_t part;           // elements of a part, a multiple of 8 kSourceThreads
   int parts, count;
+  bool early;             // the next kernel may come up while one runs: without an SM budget
   float eps;
   float* sums;            // [count, parts]
   float* factor;          // [count]

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
   tmem_fence_after();
   const uint32_t tmem = sh.tmem, t_square = tmem, t_apply = tmem + 128;
   const uint32_t lanes = (uint32_t)(q * 32) << 16;
-  pdl_launch_dependents();
+  if (p.src.early) pdl_launch_dependents();
   pdl_wait();
   bool ok = true;
   uint32_t phase = 0;
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
 int launch_newton_small(const SmallNewton& p, cudaStream_t stream) {
   constexpr int kSmem = kSmallBytes + (int)sizeof(SmallShared);
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(k_newton_small), kSmem) != EP_OK) return EP_ERR_CUDA;
-  if (ep_host::launch_dependent(k_newton_small, std::min(p.src.count, ep_host::grid_cap(1)), kSmallThreads, kSmem, stream, p) != EP_OK) return EP_ERR_CUDA;
+  if (ep_host::launch_in_budget(k_newton_small, std::min(p.src.count, ep_host::grid_cap(1)), kSmallThreads, kSmem, stream, p) != EP_OK) return EP_ERR_CUDA;
   ep_host::count_launch();
   return ep_host::check_launch();
 }
