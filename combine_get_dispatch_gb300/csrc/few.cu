@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t umma_few_idesc(int n) { return (1u << 4) | (
 // 2 j + 1 of the products.  bf16 has 8 significant bits and each part 4, so this is x
 // itself down to 2^-13 of the largest, and 2^-21 of the largest off below: no more
 // than sums in 32 bits lose.  A block with an infinity or NaN gets the scale NaN.
-// An fp32 number (few_fine's h) is rounded so to about 2^-9 of itself.  8 elements a lane, a block sixteen lanes.
+// An fp32 number (h) is rounded so to about 2^-9 of itself.  8 elements a lane, a block sixteen lanes.
 template <bool kWide>
 struct TokenPiece {   // as it lies in memory: bf16 or fp32
   uint4 v[kWide ? 2 : 1];
@@ -196,10 +196,10 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int team,
   }
 }
 
-template <bool kIn, int kAct, bool kFine>
+template <bool kIn, int kAct>
 __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_constant__ FewParams p) {
   constexpr int kBlock = 128, kChunk = kBlocks * kBlock;   // inner elements of a block, of a stage
-  constexpr bool kWide = !kIn && kFine;              // tokens' rows are fp32
+  constexpr bool kWide = !kIn;                       // tokens' rows are fp32
   constexpr int kRawBytes = kChunk * (kWide ? 4 : 2);   // a token's row in a stage, as it comes
   using Lists = FewLists<kIn ? 0 : kUnitRows>;
   using Walk = FewWalk<kIn, kPass, kUnitRows>;
@@ -302,12 +302,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_e4m3(const __grid_consta
 #pragma unroll
           for (int j = 0; j < kPass; ++j) {   // the second kernel's operand
             if (j >= w.m) break;
-            const float h = act_value<kAct>(y[j]) * up[j][column];
-            const int64_t to = (int64_t)l.slot[w.s0 + j] * p.N + w.col + column;
-            if (kFine)
-              reinterpret_cast<float*>(p.out)[to] = h;
-            else
-              p.out[to] = __float2bfloat16_rn(h);
+            reinterpret_cast<float*>(p.out)[(int64_t)l.slot[w.s0 + j] * p.N + w.col + column] = act_value<kAct>(y[j]) * up[j][column];
           }
         }
       } else if (there) {
@@ -501,15 +496,9 @@ static int launch_few_e4m3(const FewCall& in, const FewCall& out, const void* w_
   constexpr int64_t kWaveBytes = (int64_t)1 << 29;   // of gate and up, if every slot has its own expert
   const int64_t bytes = 2 * (int64_t)std::min(p.T * p.k, p.E) * p.N * p.K;
   const int waves = bytes >= kWaveBytes && !ep_host::sm_budget_set() ? 3 : 1;
-  auto go = [&](auto fine) {
-    constexpr bool kFine = decltype(fine)::value;
-    auto* fn = act == EP_ACT_RELU   ? k_few_e4m3<true, EP_ACT_RELU, kFine>
-               : act == EP_ACT_SILU ? k_few_e4m3<true, EP_ACT_SILU, kFine>
-                                    : k_few_e4m3<true, EP_ACT_GELU, kFine>;
-    const int rc = launch_few_half<true>(fn, kFewThreads, p, waves, s);
-    return rc != EP_OK ? rc : launch_few_half<false>(k_few_e4m3<false, EP_ACT_NONE, kFine>, kFewThreads, q, 1, s);
-  };
-  return few_fine(in.T) ? go(std::true_type()) : go(std::false_type());
+  auto* fn = act == EP_ACT_RELU ? k_few_e4m3<true, EP_ACT_RELU> : act == EP_ACT_SILU ? k_few_e4m3<true, EP_ACT_SILU> : k_few_e4m3<true, EP_ACT_GELU>;
+  const int rc = launch_few_half(fn, kFewThreads, p, waves, s);
+  return rc != EP_OK ? rc : launch_few_half(k_few_e4m3<false, EP_ACT_NONE>, kFewThreads, q, 1, s);
 }
 
 static bool few_sizes(int R, int T_r, int k, int E, int I) {
@@ -521,8 +510,7 @@ static bool few_sizes(int R, int T_r, int k, int E, int I) {
 
 extern "C" size_t ep_moe_few_workspace_size(int R, int T_r, int k, int E, int I) {
   if (!ep::few_sizes(R, T_r, k, E, I)) return 0;
-  static_assert(2 * ep::kFineTokens >= EP_MOE_FEW_TOKENS);   // enough for more tokens too, and for fewer than asked for
-  return std::max<size_t>(16, ((size_t)std::min(R * T_r, ep::kFineTokens) * k * I * 4 + 15) / 16 * 16);
+  return std::max<size_t>(16, (size_t)R * T_r * k * I * ep::kHiddenBytes);   // (I is a multiple of 8)
 }
 
 extern "C" int ep_moe_few(const void* x, const int64_t* topk_idx, const float* topk_weights, const void* w_gu,

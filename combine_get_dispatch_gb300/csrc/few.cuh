@@ -10,16 +10,15 @@ namespace ep {
 constexpr int kFewSmem = 226 * 1024;
 constexpr int kCrossing = 16;   // columns: what a narrow unit at an expert's end costs by its products (one token: bf16 43 us without, 41 so; E4M3 76, 69)
 
-// h between the kernels: for few tokens in more than bf16's 8 bits (with bf16 weights two words, with E4M3 fp32), so
-// that the output is as near as its own rounding lets it be; with h rounded to bf16 it is 1.4 times as far off, which
-// is left so where tokens' bytes count: 64 tokens through eight experts of 4096 x 2048 take 75 us so and 87 with two
-// words, 21 through 32 of 4096 x 1416 146 and 151, one token 38.5 and 38.7, 32 on E4M3 weights 763 and 767.
-constexpr int kFineTokens = 32;
-inline bool few_fine(int tokens) { return tokens <= kFineTokens; }
+// h between the kernels has more than bf16's 8 bits (with bf16 weights two words, with E4M3 fp32), so that the output
+// is as near as its own rounding lets it be: with h rounded to bf16 it is 1.4 times as far off.  In every call, so that a
+// token comes out the same whatever the batch, though 64 bf16 tokens through eight experts of 4096 x 2048 take 86 us
+// and 74 with h in bf16, as tokens' bytes count there (one token 39 either way; 32 on E4M3 weights 763, 767).
+constexpr int kHiddenBytes = 4;
 
 struct FewCall {
   const uint8_t* scales;       // of E4M3 weights
-  const __nv_bfloat16* v;      // kIn: x [T, H]; kOut: h [T k, I] (few_fine: [T k, 2, I], or fp32)
+  const __nv_bfloat16* v;      // kIn: x [T, H]; kOut: h [T k, 2, I], or fp32 [T k, I]
   const int64_t* idx;          // [T, k]
   const float* weights;
   __nv_bfloat16* out;          // kIn: h; kOut: out [T, H]
@@ -254,7 +253,7 @@ struct RingPosition {
 };
 
 // A half of the layer: kIn or kOut; waves: how many times the CTAs that run at once.
-template <bool kIn, typename Params>
+template <typename Params>
 int launch_few_half(void (*fn)(Params), int threads, const Params& in, int waves, cudaStream_t s) {
   if (ep_host::ensure_max_smem(reinterpret_cast<const void*>(fn), kFewSmem) != EP_OK) return EP_ERR_CUDA;
   const int grid = ep_host::grid_cap(1);

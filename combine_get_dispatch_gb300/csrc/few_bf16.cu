@@ -26,7 +26,9 @@ constexpr int kPiece = 1024;          // bytes of a weight row in a stage
 constexpr int kChunk = kPiece / 2;    // inner elements of a stage
 constexpr int kRowUnit = 32;          // rows of a unit
 constexpr int kRedPitch = 36;         // floats: a warp's sums fall into distinct banks
-__host__ __device__ constexpr int row_pass(bool two) { return two ? 16 : 24; }   // tokens of an expert taken at a time: two stages at least
+// Tokens of an expert taken at a time: two stages at least.  24 of two words each do not fit the registers (64 tokens
+// through eight experts of 4096 x 2048 86 us with 16, 88 with 24, one token 39.2 and 41.0).
+__host__ __device__ constexpr int row_pass(bool two) { return two ? 16 : 24; }
 constexpr int kRowStages = 8;
 constexpr int kTokenPitch = kPiece + 64;   // 8 lanes' 16 bytes fall into distinct banks
 
@@ -46,12 +48,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A warp's eighth of a unit: 32 rows, 8 G columns: of tokens, or (kFine) of the two words of each, whose
+// A warp's eighth of a unit: 32 rows, 8 G columns: of tokens, or (kOut) of the two words of each, whose
 // sums come together at the end: the second words lie 4 columns on where all fit 8 (G = 1), else G / 2 times 8.
 // Nothing in here branches on what the unit holds (what lies where no row or token
 // does is multiplied and not used): with branches around its loads a stage took
 // 1500 clocks, most of them waiting for one load after the other.
-template <bool kIn, bool kFine, int G>
+template <bool kIn, int G>
 __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t* ring, int stage_bytes, float* red, int chunks,
                                              RingPosition& at_red, RingPosition& at_stage, bool& ok) {
   constexpr int kStep = 32;   // inner elements a warp multiplies at a time: 16 bytes of weights a lane
@@ -99,8 +101,8 @@ __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t
     if (lane == 0) mbar_arrive(&sh.empty[at_stage.s]);
     at_stage.advance();
   }
-  constexpr int kSums = kFine && G > 1 ? G / 2 : G;
-  if constexpr (kFine) {
+  constexpr int kSums = !kIn && G > 1 ? G / 2 : G;
+  if constexpr (!kIn) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -120,7 +122,7 @@ __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t
   at_red.advance();
 }
 
-template <bool kIn, int kAct, bool kFine>
+template <bool kIn, int kAct>
 __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_constant__ RowParams p) {
   using Lists = FewLists<kIn ? 0 : kRowUnit>;
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
   }
   const Lists l(lists_at, p.E, p.T, p.k);
   few_lists<kRowThreads>(p, sh.counts, l, reinterpret_cast<uint32_t*>(red_base), kIn && blockIdx.x == 0);
-  constexpr bool kTwo = !kIn && kFine;   // token rows of a stage: two for each, as few_products wants them
+  constexpr bool kTwo = !kIn;   // token rows of a stage: two for each, as few_products wants them
   constexpr int kPass = row_pass(kTwo);
   const int tokens_most = min(sh.counts.most, kPass);
   const int rows_most = !kTwo ? tokens_most : tokens_most <= 4 ? 8 : (tokens_most + 7) / 8 * 16;
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
   // products read 8 tokens' rows, there or not: some may lie behind the last stage
   const int behind = kTwo ? 0 : ((tokens_most + 7) / 8 * 8 - tokens_most) * kTokenPitch;
   auto stages_with = [&](int reds) { return min(kRowStages, ((int)(lists_at - red_base) - reds * red_bytes - behind) / stage_bytes); };
-  // two units' sums, or one's where that makes a third or fourth stage (64 tokens over eight experts: 87 us with three, 76 so)
+  // two units' sums, or one's where that makes a third or fourth stage
   const int reds = stages_with(1) > stages_with(2) && stages_with(1) <= 4 ? 1 : 2, stages = stages_with(reds);
   uint8_t* const ring = red_base + reds * red_bytes;
   const int chunks = (p.K + kChunk - 1) / kChunk;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
     // ---------------------------------------------------------------- products
     while (w.next()) {
       float* const red = reinterpret_cast<float*>(red_base + at_red.s * red_bytes) + warp * red_part;
-      auto products = [&](auto g) { few_products<kIn, kTwo, decltype(g)::value>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok); };
+      auto products = [&](auto g) { few_products<kIn, decltype(g)::value>(p.K, sh, ring, stage_bytes, red, chunks, at_red, position, ok); };
       using std::integral_constant;
       if (kTwo && w.m <= 4)
         products(integral_constant<int, 1>());
@@ -204,9 +206,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
           if (c < w.cols) {
             const float h = act_value<kAct>(total(n, row)) * total(n, row + 8);
             const __nv_bfloat16 hi = __float2bfloat16_rn(h);   // the second kernel's operand
-            __nv_bfloat16* const to = p.out + (int64_t)l.slot[w.s0 + n] * (kFine ? 2 : 1) * p.N + w.col + c;
+            __nv_bfloat16* const to = p.out + (int64_t)l.slot[w.s0 + n] * 2 * p.N + w.col + c;
             to[0] = hi;
-            if (kFine) to[p.N] = __float2bfloat16_rn(isfinite(__bfloat162float(hi)) ? h - __bfloat162float(hi) : 0.0f);
+            to[p.N] = __float2bfloat16_rn(isfinite(__bfloat162float(hi)) ? h - __bfloat162float(hi) : 0.0f);
           }
       } else {
         // a token is one warp's, so its slots are added in the lists' order
@@ -300,15 +302,9 @@ int launch_few_bf16(const FewCall& in, const FewCall& out, const void* w_gu, con
     return rc == EP_OK ? ep_host::make_row_map(&f.one, w, words, f.N, count, 1) : rc;
   };
   if (maps(p, w_gu, 2 * in.E, kRowUnit / 2) != EP_OK || maps(q, w_down, in.E, kRowUnit) != EP_OK) return EP_ERR_CUDA;
-  auto go = [&](auto fine) {
-    constexpr bool kFine = decltype(fine)::value;
-    auto* fn = act == EP_ACT_RELU   ? k_few_bf16<true, EP_ACT_RELU, kFine>
-               : act == EP_ACT_SILU ? k_few_bf16<true, EP_ACT_SILU, kFine>
-                                    : k_few_bf16<true, EP_ACT_GELU, kFine>;
-    const int rc = launch_few_half<true>(fn, kRowThreads, p, 1, s);
-    return rc != EP_OK ? rc : launch_few_half<false>(k_few_bf16<false, EP_ACT_NONE, kFine>, kRowThreads, q, 1, s);
-  };
-  return few_fine(in.T) ? go(std::true_type()) : go(std::false_type());
+  auto* fn = act == EP_ACT_RELU ? k_few_bf16<true, EP_ACT_RELU> : act == EP_ACT_SILU ? k_few_bf16<true, EP_ACT_SILU> : k_few_bf16<true, EP_ACT_GELU>;
+  const int rc = launch_few_half(fn, kRowThreads, p, 1, s);
+  return rc != EP_OK ? rc : launch_few_half(k_few_bf16<false, EP_ACT_NONE>, kRowThreads, q, 1, s);
 }
 
 }  // namespace ep
