@@ -122,6 +122,15 @@ __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t
   at_red.advance();
 }
 
+// What cutting h to bf16 leaves, off by 2^-16 of h at most.  It has h's sign and is no zero where h is none, so that
+// an infinity among the weights comes out as it does from h: of two products with it neither is a NaN, or the other infinity.
+__device__ __forceinline__ __nv_bfloat16 second_word(float h) {
+  const float hi = __bfloat162float(__float2bfloat16_rz(h));
+  float lo = isfinite(hi) ? h - hi : hi;
+  if (lo == 0.0f && hi != 0.0f) lo = copysignf(fmaxf(fabsf(hi) * 9.3132257e-10f, 1.1754944e-38f), hi);   // 2^-30 of it, or the least normal number
+  return __float2bfloat16_rn(lo);
+}
+
 template <bool kIn, int kAct>
 __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_constant__ RowParams p) {
   using Lists = FewLists<kIn ? 0 : kRowUnit>;
@@ -205,10 +214,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_few_bf16(const __grid_consta
         for (int n = q * 2 + (lane >> 4); n < w.m; n += 2 * kAdders)
           if (c < w.cols) {
             const float h = act_value<kAct>(total(n, row)) * total(n, row + 8);
-            const __nv_bfloat16 hi = __float2bfloat16_rn(h);   // the second kernel's operand
-            __nv_bfloat16* const to = p.out + (int64_t)l.slot[w.s0 + n] * 2 * p.N + w.col + c;
-            to[0] = hi;
-            to[p.N] = __float2bfloat16_rn(isfinite(__bfloat162float(hi)) ? h - __bfloat162float(hi) : 0.0f);
+            __nv_bfloat16* const to = p.out + (int64_t)l.slot[w.s0 + n] * 2 * p.N + w.col + c;   // the second kernel's operand
+            to[0] = __float2bfloat16_rz(h);
+            to[p.N] = second_word(h);
           }
       } else {
         // a token is one warp's, so its slots are added in the lists' order

@@ -467,9 +467,8 @@ int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, co
  *                initialisation; calls that share one must be ordered
  * Sums run in 32 bits in an order that neither the SM budget nor the batch's
  * other tokens change (over the slots: by expert, then by slot); out is rounded to
- * bf16.  h keeps 16 significant bits (bf16 weights; an infinity among W_down's may
- * then come out as NaN) or 9 (E4M3), so that out is about as exact as its rounding, and
- * a token comes out the same in a batch of any size.  Ids outside [-1, E)
+ * bf16.  h keeps 16 significant bits (bf16 weights) or 9 (E4M3), so that out is about as
+ * exact as its rounding, and a token comes out the same in a batch of any size.  Ids outside [-1, E)
  * set EP_ERR_INVALID_ARG in *status and count as unused; a wait that runs out sets
  * EP_ERR_TIMEOUT and leaves outputs incomplete.  Limits: H, I multiples of 8 (128 with E4M3), at most
  * 2^24, E * H and E * (I + 16) below 2^31, act as for ep_expert_glu.  All pointers
