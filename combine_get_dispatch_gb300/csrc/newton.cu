@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(kSourceThreads) k_newton_norm(Source s) {
   __shared__ float warps[kSourceThreads / kWarp];
   pdl_wait();
   if (s.early) pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *s.failed = 0;
   for (int64_t item = blockIdx.x; item < (int64_t)s.count * s.parts; item += gridDim.x) {
     const int64_t z = item / s.parts, begin = (item - z * s.parts) * s.part, end = min(begin + s.part, s.each), base = z * s.each;
     float sum[kAhead] = {};
@@ -198,6 +199,7 @@ struct NewtonParams {
   float* w;
   __nv_bfloat16* w16;
   int32_t* status;
+  int32_t* failed;              // as Source's
 };
 
 struct NewtonShared {
@@ -308,6 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
   };
   if (p.early) pdl_launch_dependents();
   pdl_wait();
+  if (kForm == kApplyWeights && __ldcg(p.failed) != 0) more = false;   // (no launch of this form sets it)
   if (warp == 0 || warp == 3) {
     // ---------------------------------------------------------------- copies, a warp an operand
     const bool issue = elect_one(), first = warp == 0;
@@ -582,7 +585,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
     copy_async_wait<0>();
     if (lane == 0) tma_wait_all();
   }
-  if (!ok) set_status(p.status, EP_ERR_TIMEOUT);
+  if (!ok) {
+    set_status(p.status, EP_ERR_TIMEOUT);
+    if (kForm != kApplyWeights) *p.failed = 1;
+  }
   __syncwarp();
   tmem_fence_before();
   cluster_sync();
@@ -595,6 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNewtonThreads, 1) k
 struct NewtonSpace {
   float *sums, *factor, *diagonal;
   __half *x[2], *lo[2], *A, *P;
+  int32_t* failed;
   size_t bytes;
 };
 
@@ -621,7 +628,8 @@ static NewtonSpace newton_space(int count, int M, int N, void* base) {
   }
   s.A = reinterpret_cast<__half*>(take(count * S * padded((int)S) * 2));
   s.P = reinterpret_cast<__half*>(take(count * S * padded((int)S) * 2));
-  s.bytes = std::max<size_t>(16, at);
+  s.failed = reinterpret_cast<int32_t*>(take(4));
+  s.bytes = at;
   return s;
 }
 
@@ -687,6 +695,7 @@ struct Newton {
     p.cols = cols;
     p.inner = inner;
     p.status = status;
+    p.failed = space.failed;
     p.early = !ep_host::sm_budget_set();
     tiles(p, sym);
     return p;
@@ -782,6 +791,7 @@ static int newton(Source src, int count, int M, int N, int steps, const float* a
   src.count = count;
   src.sums = n.space.sums;
   src.factor = n.space.factor;
+  src.failed = n.space.failed;
   src.rows = M;
   src.cols = N;
   src.stride = (int)padded_x(N);

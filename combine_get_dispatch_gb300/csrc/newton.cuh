@@ -21,6 +21,7 @@ struct Source {
   float eps;
   float* sums;            // [count, parts]
   float* factor;          // [count]
+  int32_t* failed;        // set by products whose waits ran out, so that weights are not updated from what they left
   int rows, cols, stride; // of X: rows of `cols` elements, `stride` apart
   __half *hi, *lo;        // lo may be nullptr
 };

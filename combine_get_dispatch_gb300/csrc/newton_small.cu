@@ -104,12 +104,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
     tma_load_1d(to, static_cast<const uint8_t*>(a) + (int64_t)k * kPart * a_bytes, n * a_bytes, &sh.part[slot]);
     if (b != nullptr) tma_load_1d(to + kPartBytes / 2, static_cast<const uint8_t*>(b) + (int64_t)k * kPart * 32, n * 32, &sh.part[slot]);
   };
+  // false: a wait has run out, and nothing more goes out;
   // part k's momentum or weights, replaced in place, go out by one copy (16 bytes a thread are half sectors, and
   // took three times as long), and the part after next comes in where the last one went out
   auto send = [&](int k, float* to, int offset, const void* a, int a_bytes, const void* b) {
     fence_proxy_async_smem();
-    __syncthreads();
-    if (threadIdx.x != 0) return;
+    ok = __syncthreads_and(ok) != 0;
+    if (!ok) return false;
+    if (threadIdx.x != 0) return true;
     const int n = min(kPart, vectors - k * kPart);
     if (to != nullptr) {
       tma_store_1d(to + (int64_t)k * kPart * 8, raw + (hi - wide) + (parts_seen + k) % kParts * kPartBytes + offset, n * 32);
@@ -117,6 +119,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
       tma_wait_read<1>();
     }
     if (k > 0) bring(k - 1 + kParts, a, a_bytes, b);
+    return true;
   };
   // wait for part k; where it is
   auto part = [&](int k) {
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
         st_shared_v4_at(at_m, make_uint4(__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3])));
         st_shared_v4_at(at_m + 16, make_uint4(__float_as_uint(m[4]), __float_as_uint(m[5]), __float_as_uint(m[6]), __float_as_uint(m[7])));
       }
-      send(k, p.src.m != nullptr ? p.src.m + base : nullptr, kPartBytes / 2, g, g_bytes, momentum);
+      if (!send(k, p.src.m != nullptr ? p.src.m + base : nullptr, kPartBytes / 2, g, g_bytes, momentum)) break;
       if (i >= vectors) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) square = fmaf(u[e], u[e], square);
@@ -184,6 +187,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
         for (int e = 0; e < 8; ++e) asm volatile("st.shared.f32 [%0], %1;" ::"r"(wide_address(wide, c + e, r)), "f"(u[e]) : "memory");
       }
     }
+    if (!ok) break;
     parts_seen += parts;
     if (threadIdx.x == 0) tma_wait_read<0>();   // X goes where the momentum comes from
 #pragma unroll
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
           y[e + 2] = fmaf(-p.step, y[e + 2], p.keep * __uint_as_float(v.z)), y[e + 3] = fmaf(-p.step, y[e + 3], p.keep * __uint_as_float(v.w));
           st_shared_v4_at(at + e * 4, make_uint4(__float_as_uint(y[e]), __float_as_uint(y[e + 1]), __float_as_uint(y[e + 2]), __float_as_uint(y[e + 3])));
         }
-        send(k, w, 0, w, 32, nullptr);
+        if (!send(k, w, 0, w, 32, nullptr)) break;
         to = p.w16;
       }
       if (in && to != nullptr)
@@ -377,7 +381,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
     ok = __syncthreads_and(ok) != 0;   // the next matrix comes in
   }
   if (threadIdx.x == 0) tma_wait_all();
-  if (!ok) set_status(p.status, EP_ERR_TIMEOUT);
+  if (!ok) {
+    set_status(p.status, EP_ERR_TIMEOUT);
+    const uint64_t t0 = globaltimer_ns();   // give the copies in flight time to land before the memory goes
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();

@@ -728,7 +728,8 @@ def ep_muon_update(g, m, w, w16, steps, workspace, lr, scale=1.0, momentum=0.95,
                    weight_decay=0.0, eps=1e-7, status=None, stream=None):
     """One Muon step on a stack of weights [..., M, N], in place: momentum m and
     weights w (fp32), their bf16 copy w16 (may be None), from the gradient g (bf16
-    or fp32).  steps and workspace as for ep_orthogonalize."""
+    or fp32).  steps and workspace as for ep_orthogonalize.  A wait that ran out is told
+    by status alone; m, w and w16 then hold updated numbers and numbers as they were."""
     count, M, N, dtype, abc = _stack(g, steps)
     _need(m, torch.float32, g.shape, "m")
     _need(w, torch.float32, g.shape, "w")

@@ -518,8 +518,11 @@ int ep_orthogonalize(const void* g, int dtype, int count, int M, int N, int step
  *   w16 = w rounded to bf16
  * g [count, M, N] EP_DTYPE_BF16 or EP_DTYPE_F32 (read only), m and w [count, M, N]
  * fp32, w16 [count, M, N] bf16 or NULL; m, w and w16 are updated in place.  The host's
- * numbers are read before the call returns (a captured call keeps them).  The
- * workspace, limits and errors are ep_orthogonalize's; momentum in [0, 1), lr, scale
+ * numbers are read before the call returns (a captured call keeps them).  A wait
+ * that runs out sets EP_ERR_TIMEOUT in *status (without one the call gives no sign):
+ * every number of m, w and w16 is then either updated or as it was, w and w16 in
+ * whole blocks of a matrix, and none comes from what the wait left undone.  The
+ * workspace, limits and other errors are ep_orthogonalize's; momentum in [0, 1), lr, scale
  * and weight_decay finite. */
 int ep_muon_update(const void* g, int dtype, float* m, float* w, void* w16, int count, int M, int N,
                    float lr, float scale, float momentum, int nesterov, float weight_decay, int steps,
