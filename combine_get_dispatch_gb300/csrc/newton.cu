@@ -606,7 +606,9 @@ struct NewtonSpace {
 };
 
 // Row stride of A and P, and of X where it adds no more than an eighth: whole 128-byte lines, which a copied row of 64
-// elements then is one of (A and P, S = 1416, without: 870 clocks a stage instead of 610; with X too, 8 of 4096 x 1416 took 1386 us instead of 1543).
+// elements then is one of (A and P, S = 1416, without: 870 clocks a stage instead of 610).  X without and with it, five quintic
+// steps: 8 of 4096 x 1416 1247 us, 1057; 8 of 2048 x 2056 1214, 1070; 16 of 2048 x 520 500, 470; 16 of 520 x 584 266.5, 266.
+// Narrower ones gain too (16 of 1024 x 504 273, 258; 32 of 1024 x 264 313, 290) but would need up to 8 times the room.
 static int64_t padded(int n) { return (int64_t)(n + 63) / 64 * 64; }
 static int64_t padded_x(int N) { return N >= 512 ? padded(N) : N; }
 
@@ -664,7 +666,9 @@ struct Newton {
   int32_t* status;
   cudaStream_t stream;
 
-  // Tiles of 256 columns, of 128 where those would leave pairs of SMs without one.
+  // Tiles of 256 columns, or of 128 where twice as many still come at once (five quintic steps, us with 256 and with 128:
+  // 2048 x 1000 187.5, 181; two of them 219.6, 212.4; 1024 x 1024 147.5, 145.3; eight of 512 x 512 132.7, 130; where they come in
+  // two waves 20 of 512 x 512 195.7, 204.5; two of 1416 x 1416 244.6, 261.5).
   void tiles(NewtonParams& p, bool sym) const {
     auto of = [&](int wide) {
       p.wide = wide;
@@ -680,7 +684,7 @@ struct Newton {
     // whatever the SM budget: results go by the sizes alone
     const uint32_t pairs = std::max(1, ep_host::num_sms() / 2), left = p.tiles % pairs;
     p.whole = p.tiles;
-    if (p.tiles < pairs) {
+    if (2 * p.tiles <= pairs) {
       of(kBlock / 2);
       p.whole = p.tiles;
     } else if (2 * left <= pairs) {   // a last wave of halves (16 of 1416 x 4096: X X^T in 94 us instead of 99, its square in 47 instead of 49)
