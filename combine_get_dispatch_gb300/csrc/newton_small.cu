@@ -104,14 +104,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
     tma_load_1d(to, static_cast<const uint8_t*>(a) + (int64_t)k * kPart * a_bytes, n * a_bytes, &sh.part[slot]);
     if (b != nullptr) tma_load_1d(to + kPartBytes / 2, static_cast<const uint8_t*>(b) + (int64_t)k * kPart * 32, n * 32, &sh.part[slot]);
   };
-  // false: a wait has run out, and nothing more goes out;
   // part k's momentum or weights, replaced in place, go out by one copy (16 bytes a thread are half sectors, and
   // took three times as long), and the part after next comes in where the last one went out
   auto send = [&](int k, float* to, int offset, const void* a, int a_bytes, const void* b) {
     fence_proxy_async_smem();
-    ok = __syncthreads_and(ok) != 0;
-    if (!ok) return false;
-    if (threadIdx.x != 0) return true;
+    __syncthreads();
+    if (threadIdx.x != 0 || !ok) return;
     const int n = min(kPart, vectors - k * kPart);
     if (to != nullptr) {
       tma_store_1d(to + (int64_t)k * kPart * 8, raw + (hi - wide) + (parts_seen + k) % kParts * kPartBytes + offset, n * 32);
@@ -119,12 +117,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
       tma_wait_read<1>();
     }
     if (k > 0) bring(k - 1 + kParts, a, a_bytes, b);
-    return true;
   };
-  // wait for part k; where it is
+  // wait for part k; where it is.  A warp whose wait ran out leaves its share there as it comes, so that it goes out as it was
   auto part = [&](int k) {
     const uint32_t at = parts_seen + k;
-    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.part[at % kParts], (at / kParts) & 1)) && ok;
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.part[at % kParts], (at / kParts) & 1, ok ? kWaitNs : 0)) && ok;
     return hi + at % kParts * kPartBytes;
   };
 
@@ -169,10 +166,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
           m[e] = fmaf(p.src.momentum, m[e], u[e]);
           u[e] = p.src.nesterov ? fmaf(p.src.momentum, m[e], u[e]) : m[e];
         }
-        st_shared_v4_at(at_m, make_uint4(__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3])));
-        st_shared_v4_at(at_m + 16, make_uint4(__float_as_uint(m[4]), __float_as_uint(m[5]), __float_as_uint(m[6]), __float_as_uint(m[7])));
+        if (ok) st_shared_v4_at(at_m, make_uint4(__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3])));
+        if (ok) st_shared_v4_at(at_m + 16, make_uint4(__float_as_uint(m[4]), __float_as_uint(m[5]), __float_as_uint(m[6]), __float_as_uint(m[7])));
       }
-      if (!send(k, p.src.m != nullptr ? p.src.m + base : nullptr, kPartBytes / 2, g, g_bytes, momentum)) break;
+      send(k, p.src.m != nullptr ? p.src.m + base : nullptr, kPartBytes / 2, g, g_bytes, momentum);
       if (i >= vectors) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) square = fmaf(u[e], u[e], square);
@@ -187,7 +184,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
         for (int e = 0; e < 8; ++e) asm volatile("st.shared.f32 [%0], %1;" ::"r"(wide_address(wide, c + e, r)), "f"(u[e]) : "memory");
       }
     }
-    if (!ok) break;
     parts_seen += parts;
     if (threadIdx.x == 0) tma_wait_read<0>();   // X goes where the momentum comes from
 #pragma unroll
@@ -369,12 +365,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_newton_small(const __grid_
           const uint4 v = ld_shared_v4_at(at + e * 4);
           y[e] = fmaf(-p.step, y[e], p.keep * __uint_as_float(v.x)), y[e + 1] = fmaf(-p.step, y[e + 1], p.keep * __uint_as_float(v.y));
           y[e + 2] = fmaf(-p.step, y[e + 2], p.keep * __uint_as_float(v.z)), y[e + 3] = fmaf(-p.step, y[e + 3], p.keep * __uint_as_float(v.w));
-          st_shared_v4_at(at + e * 4, make_uint4(__float_as_uint(y[e]), __float_as_uint(y[e + 1]), __float_as_uint(y[e + 2]), __float_as_uint(y[e + 3])));
+          if (ok) st_shared_v4_at(at + e * 4, make_uint4(__float_as_uint(y[e]), __float_as_uint(y[e + 1]), __float_as_uint(y[e + 2]), __float_as_uint(y[e + 3])));
         }
-        if (!send(k, w, 0, w, 32, nullptr)) break;
+        send(k, w, 0, w, 32, nullptr);
         to = p.w16;
       }
-      if (in && to != nullptr)
+      if (in && ok && to != nullptr)
         st_v4(to + base + (int64_t)i * 8, make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])));
     }
     if (w != nullptr) parts_seen += parts;
