@@ -46,8 +46,8 @@ def others_are_free(lib, n, call):
 
 @pytest.mark.parametrize("n", [2, 8])
 def test_update_leaves_the_other_sms(budget, hold_lib, n):  # noqa: F811
-    """Five steps of three products, of some 7 ms each."""
-    count = 16 * n
+    """Five steps of three products, of some 10 ms each."""
+    count = 24 * n
     g = torch.randn((count, 1416, 2048), device="cuda").bfloat16()
     m, w, ws = torch.zeros_like(g, dtype=torch.float32), g.float(), ep.alloc_orthogonalize_workspace(g.shape)
     budget(n)
