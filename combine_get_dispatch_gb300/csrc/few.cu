@@ -184,7 +184,7 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int team,
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int j = 4 * i + q;
-              y[j] = fmaf(fmaf(v[b][2 * j + 1], 0.0625f, v[b][2 * j]), of[q] * f[b0 + b], y[j]);   // (the sums times one scale alone may overflow)
+              y[j] = fmaf(fmaf(v[b][2 * j + 1], 0.0625f, v[b][2 * j]) * of[q], f[b0 + b], y[j]);
             }
           }
         }
