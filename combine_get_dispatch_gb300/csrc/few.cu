@@ -184,6 +184,8 @@ __device__ __forceinline__ void few_sums(FewShared& sh, uint32_t tmem, int team,
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int j = 4 * i + q;
+              // (the token's scale first: zeros stay zeros under any weights' scale.  The other way round they would not, and with
+              // an order by size, which lifts the limit of 2^111 for tokens, 32 tokens take 783 us instead of 770)
               y[j] = fmaf(fmaf(v[b][2 * j + 1], 0.0625f, v[b][2 * j]) * of[q], f[b0 + b], y[j]);
             }
           }

@@ -123,7 +123,7 @@ __device__ __forceinline__ void few_products(int K, RowShared& sh, const uint8_t
   at_red.advance();
 }
 
-// What cutting h to bf16 leaves, off by 2^-16 of h at most.  It has h's sign and is no zero where h is none, so that
+// What cutting h to bf16 leaves, off by 2^-16 of h at most (where that is a normal number: above 2^-110).  It has h's sign and is no zero where h is none, so that
 // an infinity among the weights comes out as it does from h: of two products with it neither is a NaN, or the other infinity.
 __device__ __forceinline__ __nv_bfloat16 second_word(float h) {
   const float hi = __bfloat162float(__float2bfloat16_rz(h));

@@ -462,7 +462,9 @@ int ep_expert_linear_backward(const void* dy, const void* pre, const void* x, co
  *                multiplied as the sum of two E4M3 parts each: exact down to
  *                2^-13 of the largest of them, at most 2^-21 of the largest off
  *                below; with an infinity or NaN among them the token's outputs
- *                are NaN.
+ *                are NaN.  Numbers of x and h from 2^111 on may come out as
+ *                infinities or NaN too (a block's sum, up to 2^24 times its
+ *                scale, is held in 32 bits before the weights' scale).
  *   out          [R, T_r, H] bf16; may be x itself
  *   workspace    ep_moe_few_workspace_size bytes, 16-byte aligned, no
  *                initialisation; calls that share one must be ordered

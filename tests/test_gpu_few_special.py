@@ -72,3 +72,36 @@ def test_hidden_numbers_that_bf16_holds(T):
     want = torch.tensor([INF, float("nan"), float("nan"), INF, float("nan"), INF, INF, float("nan"), INF, -INF, float("nan")] + [INF] * 5, device="cuda").bfloat16()
     assert torch.equal(torch.nan_to_num(out[0], nan=77.0), torch.nan_to_num(want, nan=77.0).expand(T, 16))
     assert ep.ACTS["relu"] == ep.EP_ACT_RELU
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+@pytest.mark.parametrize("size", [-126, -110, -60, 0, 60, 100, 106])
+def test_e4m3_scales_against_tokens(T, size):
+    """Tokens of 2^size against gate and up scales of about 2^-size: what the layer computes with is of ordinary size."""
+    from test_gpu_few import reference
+    s = make(T, 1, T, 2, 4, 256, 128, "e4m3")
+    s["x"] = (s["x"].clamp(-3.9, 3.9).double() * 2.0 ** size).bfloat16()
+    s["gu_scales"] = (s["gu_scales"].int() - size).clamp(0, 254).to(torch.uint8)
+    out = call(s, "silu")
+    want, off = reference(s, "silu")
+    # (a token's two parts lie 2^-140 apart at the least, closer than bf16 numbers anywhere)
+    d = (out.double() - want).abs()
+    assert bool((d <= off).all()), float((d / off).max())
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+@pytest.mark.parametrize("byte", [0, 20, 127, 240, 254])
+def test_e4m3_zeros_under_any_scale(T, byte):
+    """Blocks of zero weights, whatever their scale, add nothing to tokens of any size."""
+    from test_gpu_few import reference
+    s = make(T, 1, T, 2, 4, 384, 256, "e4m3")
+    s["x"] *= 2.0 ** 12
+    s["gu_scales"] -= 12
+    for w, sc, at in ((s["w_gu"], s["gu_scales"], (slice(None), 1, 0, 1)), (s["w_gu"], s["gu_scales"], (2, 0, 1, 2)), (s["w_down"], s["down_scales"], (1, 2, 0))):
+        *lead, n, k = at
+        w[(*lead, slice(128 * n, 128 * n + 128), slice(128 * k, 128 * k + 128))] = 0
+        sc[at] = byte
+    out = call(s, "silu")
+    want, off = reference(s, "silu")
+    d = (out.double() - want).abs()
+    assert bool((d <= off).all()), float((d / off).max())
